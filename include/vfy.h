@@ -15,6 +15,15 @@
  *   vfy_attend_swa       sliding-window layer over a position ring
  *   vfy_accept           fused argmax + greedy acceptance
  *
+ * The drafted tokens may also form a tree instead of a chain:
+ *
+ *   vfy_tree_plan              parents of the block's nodes -> depths and row masks
+ *   vfy_attend_full_tree/_swa_tree   the two attention layers for a tree block
+ *   vfy_process_logits         repetition penalties, biases and grammar masks, per block row
+ *   vfy_count_tokens           the token counts behind the penalties
+ *   vfy_accept_tree            fused argmax + walk along the accepted path
+ *   vfy_compact_full/_swa      the accepted path's K/V rows next to the committed prefix
+ *
  * Conventions shared by every call
  * --------------------------------
  *  - Pointers named host_* are host pointers; every other pointer is DEVICE memory on the
@@ -346,6 +355,183 @@ VFY_API vfy_status vfy_accept_static(const float* logits, int vocab, const int32
                                      const int32_t* cu_rows, int num_seqs, int max_rows,
                                      int32_t* accepted_len, int32_t* bonus, int32_t* committed,
                                      int32_t* device_error, vfy_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------------------------
+ * Tree speculation
+ * ---------------------------------------------------------------------------------------------
+ * A drafter may propose several continuations of a token: the block of sequence b is then a tree of
+ * q_b nodes (rows cu_q[b] .. cu_q[b+1]). Node 0 is the last committed token; node j > 0 is the
+ * drafted token drafts[cu_q[b] - b + j - 1] (the packing of vfy_accept; it wants a row of every
+ * sequence, so the calls that read drafts report an empty one). parents[cu_q[b] + j] is
+ * the block-local index of node j's parent, below j, or -1 for a node whose parent is the last
+ * position before the block (node 0 always). Node j's K/V row is stored at position
+ * p0 + j, p0 = seq_len[b] - q_b, where vfy_append_full / vfy_append_swa put it; the token it stands
+ * for sits at position p0 + depth_j of its sequence (the position for a rotary embedding and for
+ * the window). A chain (parent of j = j - 1) gives the results of the calls without _tree, up to rounding.
+ */
+#define VFY_MAX_TREE_NODES 256 /* nodes of one sequence's tree */
+#define VFY_TREE_WORDS 8       /* 32-bit words of a node's row mask */
+
+/*
+ * vfy_tree_plan -- depths and row masks of the block's nodes, once per step for all layers.
+ *  parents    int32 [cu_q[B]] (device), cu_q int32 [B+1] (device)
+ *  depth      int32 [cu_q[B]]                    OUT: edges from a node without a parent (0 there)
+ *  tree_mask  uint32 [cu_q[B]][VFY_TREE_WORDS]   OUT: bit j of node i's mask (word j / 32, bit j mod
+ *             32) is set if node j is i or an ancestor of i. 16-byte aligned.
+ * A tree whose shape never changes needs one call; its masks can be kept.
+ * Device errors: a parent outside [-1, j) counts as -1; a sequence with more than
+ * VFY_MAX_TREE_NODES nodes (or than the context's capacity) is skipped: VFY_EDEVICE_INPUT.
+ */
+VFY_API vfy_status vfy_tree_plan(vfy_ctx* ctx, const int32_t* parents, const int32_t* cu_q, int32_t* depth,
+                                 uint32_t* tree_mask, int num_seqs, vfy_stream_t stream);
+
+/*
+ * vfy_attend_full_tree -- vfy_attend_full for a tree block: node i attends every resident position
+ * before the block (p < p0) and, inside the block, the resident rows j whose bit its mask holds.
+ * The mask may be any set of block rows (not only a plan's): bits at or past q_b are ignored, and a
+ * row that attends nothing gets out = 0, lse = -inf.
+ *  tree_mask  uint32 [cu_q[B]][VFY_TREE_WORDS], 16-byte aligned; read after the kernel's
+ *             dependency wait even where vfy_set_stable_metadata is on, so a plan made earlier
+ *             on the same stream is seen
+ *  The other arguments are those of vfy_attend_full; block rows must be finite.
+ * Device errors: as vfy_attend_full; also a sequence with more than VFY_MAX_TREE_NODES nodes.
+ */
+VFY_API vfy_status vfy_attend_full_tree(vfy_ctx* ctx, const uint16_t* q, const int32_t* cu_q,
+                                        const uint32_t* tree_mask, const uint16_t* k_pool, const uint16_t* v_pool,
+                                        int num_slots, const int32_t* resident_ids, const int32_t* resident_slots,
+                                        const int32_t* cu_resident, int max_resident_per_seq,
+                                        const int32_t* seq_len, uint16_t* out, float* lse, int num_seqs,
+                                        vfy_stream_t stream);
+
+/*
+ * vfy_attend_swa_tree -- vfy_attend_swa for a tree block: node i attends positions
+ * [p0 + depth_i - window + 1, p0) and, inside the block, the rows of its mask.
+ *  depth  int32 [cu_q[B]] (device), as written by vfy_tree_plan, in [0, q_b)
+ * The window has to hold the block: a context whose window is smaller than its tree capacity
+ * min(max_queries_per_seq, VFY_MAX_TREE_NODES) gets VFY_EINVAL (then no ancestor falls out of it).
+ * Device errors: as vfy_attend_full_tree; a depth outside [0, q_b) is clamped into it.
+ */
+VFY_API vfy_status vfy_attend_swa_tree(vfy_ctx* ctx, const uint16_t* q, const int32_t* cu_q,
+                                       const uint32_t* tree_mask, const int32_t* depth, const uint16_t* k_ring,
+                                       const uint16_t* v_ring, const int32_t* ring_offset, const int32_t* seq_len,
+                                       uint16_t* out, float* lse, int num_seqs, vfy_stream_t stream);
+
+/* What vfy_process_logits does to the logits. Every pointer is device memory; NULL turns a rule
+ * off. */
+typedef struct vfy_logit_rules {
+  const int32_t* counts;      /* [B][vocab] as kept by vfy_count_tokens: bit 31 = the prompt holds the
+                                 token, bits 0-30 = how often it was generated. NULL: no penalties */
+  const float* repetition;    /* [B] with counts: > 0, 1 = none */
+  const float* frequency;     /* [B] with counts: 0 = none */
+  const float* presence;      /* [B] with counts: 0 = none */
+  const int32_t* drafts;      /* with counts: the block's drafted tokens, packed as in vfy_accept; NULL
+                                 where every sequence has one row */
+  const uint32_t* tree_mask;  /* [rows][VFY_TREE_WORDS], 16-byte aligned: a row's own path. NULL: a chain
+                                 (row i's path is rows 0 .. i) */
+  const int32_t* cu_bias;     /* [B+1]: the bias entries of each sequence */
+  const int32_t* bias_token;  /* [cu_bias[B]], with cu_bias */
+  const float* bias_value;    /* [cu_bias[B]], with cu_bias */
+  const uint32_t* grammar;    /* [num_masks][ceil(vocab / 32)]: bit v mod 32 of word v / 32 set = token v
+                                 may follow */
+  const int32_t* mask_index;  /* [rows] with grammar: a row's mask, -1 = everything may follow. NULL:
+                                 row r takes mask r */
+  int num_masks;              /* with grammar */
+} vfy_logit_rules;
+
+#define VFY_LOGITS_F32 0
+#define VFY_LOGITS_BF16 1
+
+/*
+ * vfy_process_logits -- the rules of vfy_logit_rules over every row of a block, before the
+ * acceptance. For row i of sequence b (i < q_b = cu_rows[b+1] - cu_rows[b], at most
+ * VFY_MAX_TREE_NODES) and token v, in fp32:
+ *     c = generated count of v + how often v is drafted on row i's path (node 0 not counted: the
+ *         counts hold it already); seen = the counts' word is not 0, or c > 0
+ *     x = seen ? (x > 0 ? x / repetition : x * repetition) : x
+ *     x = x - frequency * c - (c > 0 ? presence : 0)
+ *     x = x + the sum of v's bias entries, added up in list order (a token may be listed twice)
+ *     x = -inf if the row's grammar mask does not hold v (whatever x was, NaN included)
+ * With no rule for an entry, x is copied (bf16 widens exactly).
+ *  logits      [cu_rows[B]] rows of `vocab` entries, row stride row_stride >= vocab entries
+ *  logits_type VFY_LOGITS_F32 or VFY_LOGITS_BF16
+ *  cu_rows     int32 [B+1] (device); max_rows host bound on cu_rows[B] (<= max_seqs * max_queries_per_seq)
+ *  out         fp32 [cu_rows[B]][vocab], what vfy_accept and vfy_accept_tree read. It may be the logits
+ *              themselves (fp32, row_stride == vocab); any other overlap of the two gives VFY_EINVAL
+ * A row whose mask lets nothing follow holds -inf everywhere (its argmax is then token 0).
+ * Device errors: a drafted or bias token outside [0, vocab) (skipped), a mask_index outside [-1,
+ * num_masks) (no mask), a sequence's rows out of range (left unwritten): VFY_EDEVICE_INPUT.
+ */
+VFY_API vfy_status vfy_process_logits(vfy_ctx* ctx, const void* logits, int logits_type, int64_t row_stride,
+                                      int vocab, const int32_t* cu_rows, int max_rows,
+                                      const vfy_logit_rules* rules, float* out, int num_seqs,
+                                      vfy_stream_t stream);
+
+/*
+ * vfy_count_tokens -- bring the counts of vfy_logit_rules up to date.
+ *  tokens      int32 [cu_tokens[B]]; a token of -1 is skipped (so `committed` of vfy_accept and
+ *              vfy_accept_tree, with cu_rows, can be passed as it is)
+ *  cu_tokens   int32 [B+1] (device); max_tokens host bound on cu_tokens[B]
+ *  as_prompt   1: mark the tokens as held by the prompt (bit 31); 0: count each as generated once more
+ *  reset       1: zero the counts of all num_seqs sequences first
+ *  counts      int32 [B][vocab], updated
+ * Device errors: a token outside [-1, vocab), or offsets out of order (skipped): VFY_EDEVICE_INPUT.
+ */
+VFY_API vfy_status vfy_count_tokens(vfy_ctx* ctx, const int32_t* tokens, const int32_t* cu_tokens,
+                                    int64_t max_tokens, int as_prompt, int reset, int32_t* counts, int vocab,
+                                    int num_seqs, vfy_stream_t stream);
+
+/*
+ * vfy_accept_tree -- vfy_accept for a tree block. a_r = argmax of row r (ties and NaN as in
+ * vfy_accept). Starting at node 0, the walk moves from node i to its child whose drafted token is
+ * a_i (the lowest index, if several), until there is none.
+ *  drafts, parents  as above;  cu_rows int32 [B+1] (device), the tree's cu_q
+ *  max_rows      host bound on cu_rows[B], <= max_seqs * max_queries_per_seq
+ *  accepted_len  int32 [B]              OUT n_b: drafted nodes on the path
+ *  path          int32 [cu_rows[B]]     OUT the path's node indices: path[cu_rows[b]] = 0, ..., n_b + 1
+ *                                       entries, the rest of the sequence's rows -1
+ *  bonus         int32 [B]              OUT the token of the path's last row
+ *  committed     int32 [cu_rows[B]]     OUT the n_b drafted tokens, the bonus token, then -1
+ * Device errors: a parent outside [-1, j) (the node is never reached), a sequence without rows, with
+ * more than VFY_MAX_TREE_NODES or past max_rows (its outputs are not written): VFY_EDEVICE_INPUT.
+ */
+VFY_API vfy_status vfy_accept_tree(vfy_ctx* ctx, const float* logits, int vocab, const int32_t* drafts,
+                                   const int32_t* parents, const int32_t* cu_rows, int max_rows,
+                                   int32_t* accepted_len, int32_t* path, int32_t* bonus, int32_t* committed,
+                                   int num_seqs, vfy_stream_t stream);
+
+#define VFY_MAX_COMPACT_LAYERS 64 /* layers of one vfy_compact_* call */
+
+/*
+ * vfy_compact_full -- after an acceptance, move the accepted path's K/V rows of full layers next to
+ * the committed prefix: the row at position p0 + path[j] goes to p0 + j, j = 1 .. accepted_len[b],
+ * bit for bit, in every layer of the call. The sequence then holds p0 + accepted_len[b] + 1 valid
+ * positions; the block's other rows may hold anything (the next block is written over them).
+ *  path, accepted_len, cu_q   as written by / passed to vfy_accept_tree; path ascending
+ *  seq_len       int32 [B]  as in the step's attention calls (counting the whole block)
+ *  cu_chunks, slot_of_chunk, num_host_chunks, num_slots   as in vfy_append_full, shared by the layers
+ *  host_k, host_v, k_pool, v_pool   HOST arrays of num_layers pointers: each layer's chunk store
+ *                (pinned host or device memory) and pool
+ * A row is read from its chunk's pool slot if it has one, else from the store, and written to the
+ * store and to the pool slot of the chunk it moves to, if that has one.
+ * Device errors: a path entry outside [j, q_b), a length outside [0, q_b), a chunk outside the store:
+ * skipped, VFY_EDEVICE_INPUT.
+ */
+VFY_API vfy_status vfy_compact_full(vfy_ctx* ctx, const int32_t* path, const int32_t* accepted_len,
+                                    const int32_t* cu_q, const int32_t* seq_len, const int32_t* cu_chunks,
+                                    const int32_t* slot_of_chunk, int num_layers, uint16_t* const* host_k,
+                                    uint16_t* const* host_v, int64_t num_host_chunks, uint16_t* const* k_pool,
+                                    uint16_t* const* v_pool, int num_slots, int num_seqs, vfy_stream_t stream);
+
+/*
+ * vfy_compact_swa -- the same for window layers: ring slot (p0 + path[j] + ring_offset[b]) mod ring_len
+ * to slot (p0 + j + ring_offset[b]) mod ring_len. k_ring, v_ring: HOST arrays of num_layers pointers
+ * to bf16 [B][Hkv][ring_len][d].
+ */
+VFY_API vfy_status vfy_compact_swa(vfy_ctx* ctx, const int32_t* path, const int32_t* accepted_len,
+                                   const int32_t* cu_q, const int32_t* seq_len, const int32_t* ring_offset,
+                                   int num_layers, uint16_t* const* k_ring, uint16_t* const* v_ring,
+                                   int num_seqs, vfy_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -6,13 +6,12 @@
 //
 // Phase 1 (every CTA): a vocabulary segment of one logit row is scanned with 16-byte loads and
 // reduced to one 64-bit key per row, combined across CTAs with atomicMax. The key orders a row's
-// entries exactly like the greedy rule: high 32 bits = the fp32 value mapped to an unsigned
-// integer that sorts like the value (every NaN maps to the top, -0 to +0), low 32 bits = the
-// complement of the index (so equal values prefer the lower index).
+// entries exactly like the greedy rule (argmax.cuh).
 // Phase 2 (the last CTA to finish, by an atomic ticket; no CTA ever waits for another): decode
 // the argmax of every row, find each sequence's first draft mismatch with a warp ballot, write
 // the accepted length, the bonus token and the committed tokens, then zero the keys and the
 // ticket for the next call.
+#include "argmax.cuh"
 #include "ptx.cuh"
 #include "vfy_internal.cuh"
 
@@ -21,33 +20,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnroll = 8;     // float4 loads in flight per thread
-
-__device__ __forceinline__ uint32_t order_key(float x) {
-  uint32_t u = __float_as_uint(x);
-  if ((u & 0x7fffffffu) > 0x7f800000u) return 0xffffffffu;  // NaN: above everything
-  if (u == 0x80000000u) u = 0u;                              // -0 ties +0
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-
-__device__ __forceinline__ unsigned long long pack(float x, int idx) {
-  return (static_cast<unsigned long long>(order_key(x)) << 32) |
-         static_cast<unsigned long long>(0xffffffffu - static_cast<uint32_t>(idx));
-}
-
-__device__ __forceinline__ int unpack_index(unsigned long long key) {
-  return static_cast<int>(0xffffffffu - static_cast<uint32_t>(key & 0xffffffffull));
-}
-
-// max that returns NaN when either operand is NaN (fmaxf returns the other operand)
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
-
-__device__ __forceinline__ unsigned long long umax64(unsigned long long a, unsigned long long b) {
-  return a > b ? a : b;
-}
 
 template <bool VEC4>
 __global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptParams p) {
@@ -84,43 +56,7 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptParams p) 
       // round are issued before any is used, so the segment costs about one memory round trip.
       const float4* s4 = reinterpret_cast<const float4*>(src + v0);
       const int n4 = v1 > v0 ? (v1 - v0) >> 2 : 0;
-      for (int i0 = threadIdx.x; i0 < n4; i0 += kThreads * kUnroll) {
-        float4 v[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-          if (i0 + u * kThreads < n4) v[u] = __ldcs(s4 + i0 + u * kThreads);
-          else v[u] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        // The round's best key without packing every entry: the largest value by a NaN-propagating
-        // max (NaN iff the round holds one), then the lowest index holding that value (a float
-        // compare: -0 == +0, the two keys' tie) or, with a NaN, the lowest NaN's index. Padding
-        // entries hold -inf at indices past the segment, so they never win a tie.
-        float m = -INFINITY;
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-          m = max_nan(m, max_nan(max_nan(v[u].x, v[u].y), max_nan(v[u].z, v[u].w)));
-        int at = 0x7fffffff;
-        if (m == m) {
-#pragma unroll
-          for (int u = kUnroll - 1; u >= 0; --u) {
-            const int base = v0 + 4 * (i0 + u * kThreads);
-            at = v[u].w == m ? base + 3 : at;
-            at = v[u].z == m ? base + 2 : at;
-            at = v[u].y == m ? base + 1 : at;
-            at = v[u].x == m ? base : at;
-          }
-        } else {
-          m = __uint_as_float(0x7fffffffu);
-#pragma unroll
-          for (int u = kUnroll - 1; u >= 0; --u) {
-            const int base = v0 + 4 * (i0 + u * kThreads);
-            at = v[u].w != v[u].w ? base + 3 : at;
-            at = v[u].z != v[u].z ? base + 2 : at;
-            at = v[u].y != v[u].y ? base + 1 : at;
-            at = v[u].x != v[u].x ? base : at;
-          }
-        }
-        if (at != 0x7fffffff) best = umax64(best, pack(m, at));
-      }
+      best = scan_words<kThreads, kUnroll>(s4, n4, v0);
       for (int i = v0 + 4 * n4 + threadIdx.x; i < v1; i += kThreads) best = umax64(best, pack(src[i], i));
     } else {
       for (int i = v0 + threadIdx.x; i < v1; i += kThreads) best = umax64(best, pack(src[i], i));

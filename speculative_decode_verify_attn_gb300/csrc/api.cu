@@ -21,6 +21,7 @@ struct vfy_ctx {
   unsigned long long* accept_keys;
   int accept_rows_cap;
   unsigned int* accept_counter;
+  unsigned int* tree_counters;   // one per sequence (tree acceptance)
   // sticky device error word
   int* err;
   int full_splits;   // 0 = automatic
@@ -86,6 +87,9 @@ struct DeviceGuard {
     if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
   }
 };
+
+// Largest vocabulary of the calls that step over it in whole segments (32-bit indices do not wrap).
+constexpr int kMaxVocab = 1 << 30;
 
 int ceil_div(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
 
@@ -167,10 +171,12 @@ vfy_status vfy_create(const vfy_config* cfg_in, int device, vfy_ctx** out) {
             cudaMalloc(&ctx->part_ml, parts * 2 * sizeof(float)) == cudaSuccess &&
             cudaMalloc(&ctx->accept_keys, ctx->accept_rows_cap * sizeof(unsigned long long)) == cudaSuccess &&
             cudaMalloc(&ctx->accept_counter, sizeof(unsigned int)) == cudaSuccess &&
+            cudaMalloc(&ctx->tree_counters, cfg.max_seqs * sizeof(unsigned int)) == cudaSuccess &&
             cudaMalloc(&ctx->err, sizeof(int)) == cudaSuccess;
   if (ok)
     ok = cudaMemset(ctx->accept_keys, 0, ctx->accept_rows_cap * sizeof(unsigned long long)) == cudaSuccess &&
          cudaMemset(ctx->accept_counter, 0, sizeof(unsigned int)) == cudaSuccess &&
+         cudaMemset(ctx->tree_counters, 0, cfg.max_seqs * sizeof(unsigned int)) == cudaSuccess &&
          cudaMemset(ctx->err, 0, sizeof(int)) == cudaSuccess &&
          cudaMemset(ctx->part_ml, 0, parts * 2 * sizeof(float)) == cudaSuccess &&
          cudaDeviceSynchronize() == cudaSuccess;
@@ -192,6 +198,7 @@ void vfy_destroy(vfy_ctx* ctx) {
     cudaFree(ctx->part_ml);
     cudaFree(ctx->accept_keys);
     cudaFree(ctx->accept_counter);
+    cudaFree(ctx->tree_counters);
     cudaFree(ctx->err);
     (void)cudaGetLastError();
   }
@@ -393,12 +400,20 @@ vfy_status vfy_append_swa(vfy_ctx* ctx, const uint16_t* k_new, const uint16_t* v
   return VFY_OK;
 }
 
+// Nodes of one sequence's tree that a context takes.
+static int tree_capacity(const vfy_config& c) { return std::min(c.max_queries_per_seq, VFY_MAX_TREE_NODES); }
+
 static vfy_status attend_common(vfy_ctx* ctx, bool ring, const uint16_t* q, const int32_t* cu_q,
                                 const uint16_t* k_src, const uint16_t* v_src, uint64_t src_rows,
                                 const int32_t* ids, const int32_t* slots, const int32_t* cu_res, int num_slots,
                                 int max_res, const int32_t* ring_offset, const int32_t* seq_len, uint16_t* out,
-                                float* lse, int num_seqs, vfy_stream_t stream) {
+                                float* lse, int num_seqs, vfy_stream_t stream,
+                                const uint32_t* tree_mask = nullptr, const int32_t* tree_depth = nullptr) {
   const vfy_config& c = ctx->cfg;
+  const bool tree = tree_mask != nullptr;
+  const int max_q = tree ? tree_capacity(c) : c.max_queries_per_seq;
+  const int row_tiles =
+      tree ? ceil_div(static_cast<long long>(max_q) * (c.num_q_heads / c.num_kv_heads), kMaxRows) : ctx->row_tiles;
   DeviceGuard guard(ctx->device);
   if (!guard.ok) return VFY_ECUDA;
   CUtensorMap tk, tv;
@@ -409,12 +424,12 @@ static vfy_status attend_common(vfy_ctx* ctx, bool ring, const uint16_t* q, cons
   if (!ring) {
     splits = ctx->full_splits;
     if (splits == 0) {
-      if (ctx->row_tiles > 1) {
+      if (row_tiles > 1) {
         // Blocks of several row tiles (prefill-shaped) have (KV head, row tile) items enough to
         // fill the SMs with few splits, and a long split keeps the tensor pipe busier: at most one
         // wave. Measured with 1024 queries over 128 chunks (128 items): 1 split 121 us, 2 splits
         // 130, 3 138, 4 146, 5 (four waves) 155.
-        splits = ctx->num_sms / (hkv * num_seqs * ctx->row_tiles);
+        splits = ctx->num_sms / (hkv * num_seqs * row_tiles);
       } else {
         // One wave of CTAs for one sequence; several waves for a batch, so that the hardware
         // scheduler can balance sequences of different lengths.
@@ -427,9 +442,10 @@ static vfy_status attend_common(vfy_ctx* ctx, bool ring, const uint16_t* q, cons
     splits = ctx->swa_splits;
     if (splits == 0) {
       // a row tile's queries: at most 128 / G of them
-      const int tile_q = std::min(c.max_queries_per_seq, ceil_div(kMaxRows, c.num_q_heads / hkv));
+      // (a tree's row tiles all take the whole block's span)
+      const int tile_q = tree ? max_q : std::min(max_q, ceil_div(kMaxRows, c.num_q_heads / hkv));
       const int max_tiles = ceil_div(static_cast<long long>(kChunk - 1) + c.window + tile_q - 1, kChunk);
-      const int by_sms = ceil_div(ctx->num_sms, static_cast<long long>(hkv) * num_seqs * ctx->row_tiles);
+      const int by_sms = ceil_div(ctx->num_sms, static_cast<long long>(hkv) * num_seqs * row_tiles);
       splits = clampi(by_sms, 1, max_tiles);
       // With SMs to spare (one tile per split), two more splits than tiles: the splits without a
       // tile only take their share of the cluster merge. Measured on the 40-layer pass (10
@@ -455,14 +471,16 @@ static vfy_status attend_common(vfy_ctx* ctx, bool ring, const uint16_t* q, cons
   p.hkv = hkv;
   p.group = c.num_q_heads / hkv;
   p.num_splits = splits;
-  p.max_q = c.max_queries_per_seq;
-  p.row_tiles = ctx->row_tiles;
+  p.max_q = max_q;
+  p.row_tiles = row_tiles;
   p.scale_log2 = ctx->scale * 1.4426950408889634f;
   p.part_o = ctx->part_o;
   p.part_ml = ctx->part_ml;
   p.timeout_test_ns = ctx->timeout_test_ns;
   p.stable_metadata = ctx->stable_metadata;
   p.err = ctx->err;
+  p.tree_mask = tree_mask;
+  p.tree_depth = tree_depth;
   // Full-layer splits over many resident chunks take wide tiles (their combine is a small part
   // of a long split). Otherwise up to kMaxClusterSplits splits (and no more than one GPC holds)
   // merge inside the attention kernel, as one thread-block cluster per (sequence, KV head, row
@@ -471,14 +489,14 @@ static vfy_status attend_common(vfy_ctx* ctx, bool ring, const uint16_t* q, cons
   // A single split of a long block writes O itself (no combine launch).
   const bool direct = wide && splits == 1;
   const bool merge = !direct && !wide && splits <= vfy::kMaxClusterSplits &&
-                     splits <= vfy::attend_merge_limit(ring, c.head_dim);
+                     splits <= vfy::attend_merge_limit(ring, c.head_dim, tree);
   const vfy::AttnTiles tiles = merge    ? vfy::AttnTiles::kMerge
                               : direct ? vfy::AttnTiles::kWideDirect
                               : wide   ? vfy::AttnTiles::kWide
                                        : vfy::AttnTiles::kNarrow;
   p.out = merge || direct ? out : nullptr;
   p.lse = merge || direct ? lse : nullptr;
-  p.token_cap = num_seqs * c.max_queries_per_seq;
+  p.token_cap = num_seqs * max_q;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   VFY_CUDA(vfy::launch_attend(ring, c.head_dim, tiles, p, tk, tv, num_seqs, s));
   ++ctx->launches;
@@ -492,9 +510,9 @@ static vfy_status attend_common(vfy_ctx* ctx, bool ring, const uint16_t* q, cons
   cp.hkv = hkv;
   cp.group = p.group;
   cp.num_splits = splits;
-  cp.max_q = c.max_queries_per_seq;
-  cp.row_tiles = ctx->row_tiles;
-  cp.token_cap = num_seqs * c.max_queries_per_seq;
+  cp.max_q = max_q;
+  cp.row_tiles = row_tiles;
+  cp.token_cap = num_seqs * max_q;
   cp.stable_metadata = ctx->stable_metadata;
   cp.part_o = ctx->part_o;
   cp.part_ml = ctx->part_ml;
@@ -571,6 +589,245 @@ vfy_status vfy_accept(vfy_ctx* ctx, const float* logits, int vocab, const int32_
   p.err = ctx->err;
   const bool vec4 = (vocab % 4 == 0) && aligned16(logits);
   VFY_CUDA(vfy::launch_accept(p, vec4, reinterpret_cast<cudaStream_t>(stream)));
+  ++ctx->launches;
+  return VFY_OK;
+}
+
+vfy_status vfy_tree_plan(vfy_ctx* ctx, const int32_t* parents, const int32_t* cu_q, int32_t* depth,
+                         uint32_t* tree_mask, int num_seqs, vfy_stream_t stream) {
+  VFY_REQUIRE(ctx != nullptr && parents != nullptr && cu_q != nullptr && depth != nullptr && tree_mask != nullptr);
+  VFY_REQUIRE(aligned16(tree_mask));
+  VFY_REQUIRE(num_seqs >= 1 && num_seqs <= ctx->cfg.max_seqs);
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return VFY_ECUDA;
+  vfy::TreePlanParams p;
+  p.parents = parents;
+  p.cu_q = cu_q;
+  p.num_seqs = num_seqs;
+  p.max_q = tree_capacity(ctx->cfg);
+  p.token_cap = num_seqs * p.max_q;
+  p.depth = depth;
+  p.mask = tree_mask;
+  p.err = ctx->err;
+  VFY_CUDA(vfy::launch_tree_plan(p, reinterpret_cast<cudaStream_t>(stream)));
+  ++ctx->launches;
+  return VFY_OK;
+}
+
+vfy_status vfy_attend_full_tree(vfy_ctx* ctx, const uint16_t* q, const int32_t* cu_q, const uint32_t* tree_mask,
+                                const uint16_t* k_pool, const uint16_t* v_pool, int num_slots,
+                                const int32_t* resident_ids, const int32_t* resident_slots,
+                                const int32_t* cu_resident, int max_resident_per_seq, const int32_t* seq_len,
+                                uint16_t* out, float* lse, int num_seqs, vfy_stream_t stream) {
+  VFY_REQUIRE(ctx != nullptr && q != nullptr && cu_q != nullptr && tree_mask != nullptr);
+  VFY_REQUIRE(k_pool != nullptr && v_pool != nullptr);
+  VFY_REQUIRE(resident_ids != nullptr && resident_slots != nullptr && cu_resident != nullptr);
+  VFY_REQUIRE(seq_len != nullptr && out != nullptr);
+  VFY_REQUIRE(aligned16(q) && aligned16(tree_mask) && aligned16(k_pool) && aligned16(v_pool) && aligned16(out));
+  VFY_REQUIRE(lse == nullptr || (reinterpret_cast<uintptr_t>(lse) & 3u) == 0);
+  VFY_REQUIRE(num_seqs >= 1 && num_seqs <= ctx->cfg.max_seqs);
+  VFY_REQUIRE(num_slots >= 1 && max_resident_per_seq >= 0);
+  const uint64_t rows = static_cast<uint64_t>(num_slots) * ctx->cfg.num_kv_heads * kChunk;
+  VFY_REQUIRE(rows <= static_cast<uint64_t>(INT_MAX));
+  return attend_common(ctx, false, q, cu_q, k_pool, v_pool, rows, resident_ids, resident_slots, cu_resident,
+                       num_slots, max_resident_per_seq, nullptr, seq_len, out, lse, num_seqs, stream, tree_mask);
+}
+
+vfy_status vfy_attend_swa_tree(vfy_ctx* ctx, const uint16_t* q, const int32_t* cu_q, const uint32_t* tree_mask,
+                               const int32_t* depth, const uint16_t* k_ring, const uint16_t* v_ring,
+                               const int32_t* ring_offset, const int32_t* seq_len, uint16_t* out, float* lse,
+                               int num_seqs, vfy_stream_t stream) {
+  VFY_REQUIRE(ctx != nullptr && q != nullptr && cu_q != nullptr && tree_mask != nullptr && depth != nullptr);
+  VFY_REQUIRE(k_ring != nullptr && v_ring != nullptr && ring_offset != nullptr && seq_len != nullptr);
+  VFY_REQUIRE(out != nullptr);
+  VFY_REQUIRE(aligned16(q) && aligned16(tree_mask) && aligned16(k_ring) && aligned16(v_ring) && aligned16(out));
+  VFY_REQUIRE(lse == nullptr || (reinterpret_cast<uintptr_t>(lse) & 3u) == 0);
+  VFY_REQUIRE(num_seqs >= 1 && num_seqs <= ctx->cfg.max_seqs);
+  VFY_REQUIRE(ctx->cfg.window >= tree_capacity(ctx->cfg));
+  const uint64_t rows = static_cast<uint64_t>(num_seqs) * ctx->cfg.num_kv_heads * ctx->cfg.ring_len;
+  VFY_REQUIRE(rows <= static_cast<uint64_t>(INT_MAX));
+  return attend_common(ctx, true, q, cu_q, k_ring, v_ring, rows, nullptr, nullptr, nullptr, 0, 0, ring_offset,
+                       seq_len, out, lse, num_seqs, stream, tree_mask, depth);
+}
+
+vfy_status vfy_process_logits(vfy_ctx* ctx, const void* logits, int logits_type, int64_t row_stride, int vocab,
+                              const int32_t* cu_rows, int max_rows, const vfy_logit_rules* rules, float* out,
+                              int num_seqs, vfy_stream_t stream) {
+  VFY_REQUIRE(ctx != nullptr && logits != nullptr && cu_rows != nullptr && rules != nullptr && out != nullptr);
+  VFY_REQUIRE(logits_type == VFY_LOGITS_F32 || logits_type == VFY_LOGITS_BF16);
+  const bool bf16 = logits_type == VFY_LOGITS_BF16;
+  VFY_REQUIRE(vocab >= 1 && vocab <= kMaxVocab && row_stride >= vocab);
+  VFY_REQUIRE((reinterpret_cast<uintptr_t>(logits) & (bf16 ? 1u : 3u)) == 0);
+  VFY_REQUIRE((reinterpret_cast<uintptr_t>(out) & 3u) == 0);
+  VFY_REQUIRE(num_seqs >= 1 && num_seqs <= ctx->cfg.max_seqs && num_seqs <= 65535);
+  VFY_REQUIRE(max_rows >= 1 && max_rows <= ctx->accept_rows_cap);
+  VFY_REQUIRE(row_stride <= (INT64_MAX / 8) / max_rows);
+  const vfy_logit_rules& r = *rules;
+  VFY_REQUIRE(r.cu_bias == nullptr || (r.bias_token != nullptr && r.bias_value != nullptr));
+  VFY_REQUIRE(r.grammar == nullptr || r.num_masks >= 1);
+  VFY_REQUIRE(r.tree_mask == nullptr || aligned16(r.tree_mask));
+  // In place (the same rows) or apart: the kernel reads other rows' logits after it wrote some.
+  const bool same = !bf16 && static_cast<const void*>(out) == logits && row_stride == vocab;
+  const uintptr_t l0 = reinterpret_cast<uintptr_t>(logits), o0 = reinterpret_cast<uintptr_t>(out);
+  const uintptr_t l1 = l0 + (static_cast<uintptr_t>(max_rows - 1) * row_stride + vocab) * (bf16 ? 2u : 4u);
+  const uintptr_t o1 = o0 + static_cast<uintptr_t>(max_rows) * vocab * 4u;
+  VFY_REQUIRE(same || l1 <= o0 || o1 <= l0);
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return VFY_ECUDA;
+  vfy::LogitParams p;
+  p.logits = logits;
+  p.stride = row_stride;
+  p.vocab = vocab;
+  p.cu_rows = cu_rows;
+  p.num_seqs = num_seqs;
+  p.max_rows = max_rows;
+  p.row_parts = 1;
+  p.rules = r;
+  p.out = out;
+  p.err = ctx->err;
+  VFY_CUDA(vfy::launch_process_logits(p, bf16, reinterpret_cast<cudaStream_t>(stream)));
+  ++ctx->launches;
+  return VFY_OK;
+}
+
+vfy_status vfy_count_tokens(vfy_ctx* ctx, const int32_t* tokens, const int32_t* cu_tokens, int64_t max_tokens,
+                            int as_prompt, int reset, int32_t* counts, int vocab, int num_seqs,
+                            vfy_stream_t stream) {
+  VFY_REQUIRE(ctx != nullptr && tokens != nullptr && cu_tokens != nullptr && counts != nullptr);
+  VFY_REQUIRE(max_tokens >= 1 && max_tokens <= INT_MAX && vocab >= 1 && vocab <= kMaxVocab);
+  VFY_REQUIRE((as_prompt == 0 || as_prompt == 1) && (reset == 0 || reset == 1));
+  VFY_REQUIRE(num_seqs >= 1 && num_seqs <= ctx->cfg.max_seqs);
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return VFY_ECUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (reset) VFY_CUDA(cudaMemsetAsync(counts, 0, static_cast<size_t>(num_seqs) * vocab * sizeof(int32_t), s));
+  vfy::CountParams p;
+  p.tokens = tokens;
+  p.cu_tokens = cu_tokens;
+  p.max_tokens = max_tokens;
+  p.num_seqs = num_seqs;
+  p.vocab = vocab;
+  p.as_prompt = as_prompt;
+  p.counts = counts;
+  p.err = ctx->err;
+  VFY_CUDA(vfy::launch_count_tokens(p, s));
+  ++ctx->launches;
+  return VFY_OK;
+}
+
+vfy_status vfy_accept_tree(vfy_ctx* ctx, const float* logits, int vocab, const int32_t* drafts,
+                           const int32_t* parents, const int32_t* cu_rows, int max_rows, int32_t* accepted_len,
+                           int32_t* path, int32_t* bonus, int32_t* committed, int num_seqs, vfy_stream_t stream) {
+  VFY_REQUIRE(ctx != nullptr && logits != nullptr && drafts != nullptr && parents != nullptr && cu_rows != nullptr);
+  VFY_REQUIRE(accepted_len != nullptr && path != nullptr && bonus != nullptr && committed != nullptr);
+  VFY_REQUIRE(vocab >= 1 && vocab <= kMaxVocab && num_seqs >= 1 && num_seqs <= ctx->cfg.max_seqs);
+  VFY_REQUIRE(max_rows >= 1 && max_rows <= ctx->accept_rows_cap && max_rows <= 65535);
+  VFY_REQUIRE((reinterpret_cast<uintptr_t>(logits) & 3u) == 0);
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return VFY_ECUDA;
+  vfy::AcceptTreeParams p;
+  p.logits = logits;
+  p.vocab = vocab;
+  p.drafts = drafts;
+  p.parents = parents;
+  p.cu_rows = cu_rows;
+  p.num_seqs = num_seqs;
+  p.max_rows = max_rows;
+  // As in vfy_accept: about two CTAs per SM over all rows, segments of at least 1024 entries.
+  int parts = ceil_div(2LL * ctx->num_sms, max_rows);
+  parts = clampi(parts, 1, ceil_div(vocab, 1024));
+  int seg = ceil_div(vocab, parts);
+  seg = (seg + 3) & ~3;
+  p.parts = ceil_div(vocab, seg);
+  p.seg = seg;
+  p.accepted_len = accepted_len;
+  p.path = path;
+  p.bonus = bonus;
+  p.committed = committed;
+  p.keys = ctx->accept_keys;
+  p.counters = ctx->tree_counters;
+  p.err = ctx->err;
+  VFY_CUDA(vfy::launch_accept_tree(p, reinterpret_cast<cudaStream_t>(stream)));
+  ++ctx->launches;
+  return VFY_OK;
+}
+
+// The arguments that both compactions share.
+static void compact_params(const vfy_ctx* ctx, const int32_t* path, const int32_t* accepted_len,
+                           const int32_t* cu_q, const int32_t* seq_len, int num_layers, int num_seqs,
+                           vfy::CompactParams* p) {
+  p->path = path;
+  p->accepted = accepted_len;
+  p->cu_q = cu_q;
+  p->seq_len = seq_len;
+  p->num_seqs = num_seqs;
+  p->max_q = tree_capacity(ctx->cfg);
+  p->token_cap = num_seqs * p->max_q;
+  p->hkv = ctx->cfg.num_kv_heads;
+  p->head_dim = ctx->cfg.head_dim;
+  p->num_layers = num_layers;
+  p->err = ctx->err;
+}
+
+vfy_status vfy_compact_full(vfy_ctx* ctx, const int32_t* path, const int32_t* accepted_len, const int32_t* cu_q,
+                            const int32_t* seq_len, const int32_t* cu_chunks, const int32_t* slot_of_chunk,
+                            int num_layers, uint16_t* const* host_k, uint16_t* const* host_v,
+                            int64_t num_host_chunks, uint16_t* const* k_pool, uint16_t* const* v_pool,
+                            int num_slots, int num_seqs, vfy_stream_t stream) {
+  VFY_REQUIRE(ctx != nullptr && path != nullptr && accepted_len != nullptr && cu_q != nullptr && seq_len != nullptr);
+  VFY_REQUIRE(cu_chunks != nullptr && slot_of_chunk != nullptr);
+  VFY_REQUIRE(host_k != nullptr && host_v != nullptr && k_pool != nullptr && v_pool != nullptr);
+  VFY_REQUIRE(num_layers >= 1 && num_layers <= VFY_MAX_COMPACT_LAYERS);
+  VFY_REQUIRE(num_host_chunks >= 1 && num_host_chunks <= INT_MAX && num_slots >= 1);
+  VFY_REQUIRE(num_seqs >= 1 && num_seqs <= ctx->cfg.max_seqs);
+  for (int l = 0; l < num_layers; ++l) {
+    VFY_REQUIRE(host_k[l] != nullptr && host_v[l] != nullptr && k_pool[l] != nullptr && v_pool[l] != nullptr);
+    VFY_REQUIRE(aligned16(host_k[l]) && aligned16(host_v[l]) && aligned16(k_pool[l]) && aligned16(v_pool[l]));
+  }
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return VFY_ECUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  vfy::CompactParams p = {};
+  compact_params(ctx, path, accepted_len, cu_q, seq_len, num_layers, num_seqs, &p);
+  p.cu_chunks = cu_chunks;
+  p.slot_of_chunk = slot_of_chunk;
+  p.num_host_chunks = num_host_chunks;
+  p.num_slots = num_slots;
+  for (int l = 0; l < num_layers; ++l) {
+    void* store[2] = {host_k[l], host_v[l]};
+    const vfy_status st = device_view(s, store, 2);
+    if (st != VFY_OK) return st;
+    p.store[l][0] = static_cast<uint16_t*>(store[0]);
+    p.store[l][1] = static_cast<uint16_t*>(store[1]);
+    p.dst[l][0] = k_pool[l];
+    p.dst[l][1] = v_pool[l];
+  }
+  VFY_CUDA(vfy::launch_compact(false, p, s));
+  ++ctx->launches;
+  return VFY_OK;
+}
+
+vfy_status vfy_compact_swa(vfy_ctx* ctx, const int32_t* path, const int32_t* accepted_len, const int32_t* cu_q,
+                           const int32_t* seq_len, const int32_t* ring_offset, int num_layers,
+                           uint16_t* const* k_ring, uint16_t* const* v_ring, int num_seqs, vfy_stream_t stream) {
+  VFY_REQUIRE(ctx != nullptr && path != nullptr && accepted_len != nullptr && cu_q != nullptr && seq_len != nullptr);
+  VFY_REQUIRE(ring_offset != nullptr && k_ring != nullptr && v_ring != nullptr);
+  VFY_REQUIRE(num_layers >= 1 && num_layers <= VFY_MAX_COMPACT_LAYERS);
+  VFY_REQUIRE(num_seqs >= 1 && num_seqs <= ctx->cfg.max_seqs);
+  for (int l = 0; l < num_layers; ++l) {
+    VFY_REQUIRE(k_ring[l] != nullptr && v_ring[l] != nullptr && aligned16(k_ring[l]) && aligned16(v_ring[l]));
+  }
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return VFY_ECUDA;
+  vfy::CompactParams p = {};
+  compact_params(ctx, path, accepted_len, cu_q, seq_len, num_layers, num_seqs, &p);
+  p.ring_off = ring_offset;
+  p.ring_len = ctx->cfg.ring_len;
+  for (int l = 0; l < num_layers; ++l) {
+    p.dst[l][0] = k_ring[l];
+    p.dst[l][1] = v_ring[l];
+  }
+  VFY_CUDA(vfy::launch_compact(true, p, reinterpret_cast<cudaStream_t>(stream)));
   ++ctx->launches;
   return VFY_OK;
 }

@@ -66,8 +66,10 @@ constexpr int kBarsBytes = 4096;  // shared memory reserved for the barrier bloc
 // tiles, so it takes fewer K/V stages. Sending the rows as bf16 halved what the merge moves
 // (window layers 7.50 -> 7.30 us in their chain; the rounding, about 2^-9 of a partial, stays far
 // inside the attention tolerance), and sending them straight from the softmax threads' registers,
-// with no staging in shared memory and no barrier before the sends, 7.09 -> 6.68 us.
-template <int HD, bool RING, bool MERGE, bool WIDE>
+// with no staging in shared memory and no barrier before the sends, 7.09 -> 6.68 us. Tree blocks send
+// fp32 rows: the third bf16 rounding (after P's, before O's) took a window layer's error against
+// fp64 from 1.4 to 1.6 times that of rounding O alone.
+template <int HD, bool RING, bool MERGE, bool WIDE, bool TREE>
 struct Cfg {
   static_assert(!WIDE || (!RING && !MERGE), "wide tiles are for full layers without the cluster merge");
   static constexpr int kCPT = WIDE ? 2 : 1;             // 64-token chunks per tile
@@ -89,7 +91,8 @@ struct Cfg {
   static_assert(kColS + kSBufs * kKT <= kTmemCols, "tensor memory");
   static constexpr int kRecvEntries = kMaxRows + kMaxClusterSplits;
   static constexpr int kRecvOffset = kQBytes + (kKStages + kVStages) * kTileBytes;
-  static constexpr int kRecvMlOffset = kRecvOffset + (MERGE ? kRecvEntries * HD * 2 : 0);
+  static constexpr int kRecvRowBytes = HD * (TREE ? 4 : 2);
+  static constexpr int kRecvMlOffset = kRecvOffset + (MERGE ? kRecvEntries * kRecvRowBytes : 0);
   static constexpr int kBarOffset = kRecvMlOffset + (MERGE ? kRecvEntries * 8 : 0);
   static constexpr int kSmemBytes = kBarOffset + kBarsBytes + 1024;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
@@ -136,7 +139,7 @@ struct Work {
   bool bad;        // the sequence's q or L is out of range: it is skipped
 };
 
-template <bool RING, int CPT>
+template <bool RING, int CPT, bool TREE>
 __device__ __forceinline__ Work make_work(const AttnParams& p) {
   Work w;
   // A verify block is one row tile: no integer division on the path to the first load.
@@ -161,7 +164,7 @@ __device__ __forceinline__ Work make_work(const AttnParams& p) {
   w.lo = 0;
   w.span = 0;
   w.s_lo = 0;
-  w.bad = w.nq < 0 || w.nq > p.max_q || w.L < w.nq || w.q0 < 0;
+  w.bad = w.nq < 0 || w.nq > p.max_q || w.L < w.nq || w.q0 < 0;   // (a tree's max_q is its own limit)
   if (w.bad) {
     w.nq = 0;
     w.rows = 0;
@@ -179,8 +182,10 @@ __device__ __forceinline__ Work make_work(const AttnParams& p) {
     // lo + phi fits.
     const int R = p.ring_len;
     const unsigned phi = static_cast<unsigned>(roff % R + R) % static_cast<unsigned>(R);
-    // The tile's queries are i in [row0 / G, (row0 + rows - 1) / G], at positions L - nq + i.
-    const bool whole = p.row_tiles == 1;               // then the tile is the whole block
+    // The tile's queries are i in [row0 / G, (row0 + rows - 1) / G], at positions L - nq + i. A
+    // tree's row may attend any block row and its window starts at its depth: every row tile
+    // takes the span of the whole block.
+    const bool whole = TREE || p.row_tiles == 1;       // then the tile is the whole block
     const int i_first = whole ? 0 : w.row0 / p.group;
     const int i_last = whole ? w.nq - 1 : (w.row0 + w.rows - 1) / p.group;
     w.lo = max(0, w.L - w.nq + i_first - p.window + 1);
@@ -276,12 +281,42 @@ __device__ __forceinline__ void key_interval(const AttnParams& p, const Work& w,
   }
 }
 
-template <int HD, bool RING, bool MERGE, bool WIDE, bool DIRECT = false>
+// Tree blocks: which of the 32 keys from tile index k0 on this row attends, as bits. With p0 the
+// block's first position and pos the first of the 32 positions (the tile's wrap as in key_interval):
+//   prefix  positions in [first, p0) -- first = p0 + depth - W + 1 in a window layer, 0 in a full one
+//   block   position p0 + j iff bit j of the row's mask is set, j < q
+// `words` is the row's mask. The 32 block bits that start at j = pos - p0 straddle two words.
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
+}
+template <bool RING>
+__device__ __forceinline__ uint32_t tree_keep32(const AttnParams& p, const Work& w, const Tile& t, int first,
+                                                const uint32_t* words, int k0) {
+  int pos;
+  if (RING) {
+    pos = w.lo + k0 + (t.base + kChunk - 1 < p.ring_len ? t.base : t.base - p.ring_len);
+  } else {
+    if (!t.valid) return 0u;
+    pos = t.base + k0;
+  }
+  const int p0 = w.L - w.nq;
+  uint32_t keep = low_bits(p0 - pos) & ~low_bits(first - pos);
+  const int j = pos - p0;
+  if (j > -32 && j < w.nq) {
+    const int at = j >> 5;                             // -1: the block starts inside these 32 keys
+    const uint32_t w0 = at >= 0 ? __ldg(words + at) : 0u;
+    const uint32_t w1 = at + 1 < VFY_TREE_WORDS ? __ldg(words + at + 1) : 0u;
+    keep |= __funnelshift_r(w0, w1, j & 31) & low_bits(w.L - pos);
+  }
+  return keep;
+}
+
+template <int HD, bool RING, bool MERGE, bool WIDE, bool DIRECT = false, bool TREE = false>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tmap_k,
                   const __grid_constant__ CUtensorMap tmap_v) {
   static_assert(!DIRECT || !MERGE, "a single split writes its output without a merge");
-  using C = Cfg<HD, RING, MERGE, WIDE>;
+  using C = Cfg<HD, RING, MERGE, WIDE, TREE>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
@@ -335,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // stable (written only by work that completed before this kernel started), it is read before
   // waiting for the previous kernel, off the critical path.
   if (!p.stable_metadata) pdl_wait();
-  const Work w = make_work<RING, C::kCPT>(p);
+  const Work w = make_work<RING, C::kCPT, TREE>(p);
   if (p.stable_metadata) pdl_wait();
   if (w.bad && threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(p.err, kErrDeviceInput);
 
@@ -543,6 +578,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(&bars->q_ready);
     }
     const int p_i = w.L - w.nq + qi;                   // this row's query position
+    // Tree blocks: the row's mask, and the first position its window holds.
+    const uint32_t* words = nullptr;
+    int first = 0;
+    if constexpr (TREE) {
+      words = p.tree_mask + static_cast<size_t>(w.q0 + qi) * VFY_TREE_WORDS;
+      if constexpr (RING) {
+        const int depth = rv ? __ldg(p.tree_depth + w.q0 + qi) : 0;
+        if (depth < 0 || depth >= w.nq) {
+          if (rv) atomicOr(p.err, kErrDeviceInput);
+        }
+        first = max(0, w.L - w.nq + max(0, min(depth, w.nq - 1)) - p.window + 1);
+      }
+    }
     const uint32_t lane_base = tbase + (static_cast<uint32_t>(quarter * 32) << 16);
     constexpr int KH = C::kKH;                         // keys of a tile this warpgroup takes
     const int cw = C::kCPT == 2 ? wg : 0;              // the chunk that holds them
@@ -566,12 +614,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       Tile t;
       t.base = bars->tile_base[gs][cw];
       t.valid = bars->tile_valid[gs][cw] != 0;
-      int klo = 0, khi = kChunk - 1;
-      if (rv) key_interval<RING>(p, w, t, p_i, &klo, &khi);
-      klo -= kofs;
-      khi -= kofs;
       // Rows past the block (padding lanes) see Q = 0; their P and O rows are never read.
-      const bool whole = __all_sync(0xffffffffu, klo <= 0 && khi >= KH - 1);
+      int klo = 0, khi = kChunk - 1;
+      uint32_t keep[KH / 32];
+      bool whole;
+      if constexpr (TREE) {
+        bool all = true;
+#pragma unroll
+        for (int u = 0; u < KH / 32; ++u) {
+          keep[u] = rv ? tree_keep32<RING>(p, w, t, first, words, kofs + 32 * u) : 0xffffffffu;
+          all = all && keep[u] == 0xffffffffu;
+        }
+        whole = __all_sync(0xffffffffu, all);
+      } else {
+        if (rv) key_interval<RING>(p, w, t, p_i, &klo, &khi);
+        klo -= kofs;
+        khi -= kofs;
+        whole = __all_sync(0xffffffffu, klo <= 0 && khi >= KH - 1);
+      }
       ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[sb], (j / C::kSBufs) & 1, abort, p.err));
       if (!ok) break;
       tc_fence_after();
@@ -590,7 +650,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!whole) {
 #pragma unroll
-          for (int k = 0; k < KH; ++k) sv[k] = (k >= klo && k <= khi) ? sv[k] : -INFINITY;
+          for (int k = 0; k < KH; ++k) {
+            if constexpr (TREE)
+              sv[k] = (keep[k >> 5] >> (k & 31)) & 1u ? sv[k] : -INFINITY;
+            else
+              sv[k] = (k >= klo && k <= khi) ? sv[k] : -INFINITY;
+          }
         }
         float mx[8];
 #pragma unroll
@@ -722,13 +787,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         st_dsmem_f2(dsmem_addr(recv_ml + e * 8, owner), make_float2(l_sum > 0.f ? m_row : -INFINITY, l_sum));
       if (ok && w.nt > 0) {
         const float inv = l_sum > 0.f ? 1.f / l_sum : 0.f;
-        const uint32_t row_at = recv + e * HD * 2 + wg * HD;   // this half's bytes of the entry
+        const uint32_t row_at = recv + e * C::kRecvRowBytes + wg * (C::kRecvRowBytes / 2);   // this half's bytes
 #pragma unroll
         for (int c = 0; c < HD / 64; ++c) {
           uint32_t o0[32], o1[32];
           tmem_ld32x2(lane_base + kColO + wg * (HD / 2) + c * 32, lane_base + kColO + 128 + wg * (HD / 2) + c * 32,
                       o0, o1);
-          if (rv && l_sum > 0.f) {
+          if constexpr (TREE) {
+            if (rv && l_sum > 0.f) {
+#pragma unroll
+              for (int x = 0; x < 32; x += 4) {
+                uint32_t pk[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                  pk[q] = __float_as_uint((w0 * __uint_as_float(o0[x + q]) + w1 * __uint_as_float(o1[x + q])) * inv);
+                st_dsmem_u4(dsmem_addr(row_at + (c * 32 + x) * 4, owner), make_uint4(pk[0], pk[1], pk[2], pk[3]));
+              }
+            }
+          } else if (rv && l_sum > 0.f) {
 #pragma unroll
             for (int x = 0; x < 32; x += 8) {
               uint32_t pk[4];
@@ -821,7 +897,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n = static_cast<int>(cluster_nctarank());
     const int rank = static_cast<int>(cluster_ctarank());
     constexpr int kPer = HD / 32;                      // columns per lane
-    const uint16_t* recv = reinterpret_cast<const uint16_t*>(smem + C::kRecvOffset);
+    const uint8_t* recv = smem + C::kRecvOffset;
     const float2* recv_ml = reinterpret_cast<const float2*>(smem + C::kRecvMlOffset);
     for (int k = warp;; k += kThreads / 32) {
       const int r = rank + n * k;
@@ -831,24 +907,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       // split without data for the row sent no O row: its entry holds anything, and its zero weight
       // selects it out.
       const float2* mlk = recv_ml + k * n;
-      const uint16_t* rowk = recv + static_cast<size_t>(k * n) * HD + lane * kPer;
+      constexpr int kVals = TREE ? kPer : kPer / 2;    // 32-bit words of a lane's columns
+      const uint8_t* rowk = recv + k * n * C::kRecvRowBytes + lane * kVals * 4;
       float2 mls[kMaxClusterSplits];
-      uint32_t u[kMaxClusterSplits][kPer / 2];
+      uint32_t u[kMaxClusterSplits][kVals];
 #pragma unroll
       for (int s = 0; s < kMaxClusterSplits; ++s) {
         if (s < n) {
           mls[s] = mlk[s];
-          if constexpr (kPer == 4) {
-            const uint2 v = *reinterpret_cast<const uint2*>(rowk + s * HD);
+          const uint8_t* at = rowk + s * C::kRecvRowBytes;
+          if constexpr (kVals == 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(at);
+            u[s][0] = v.x;
+            u[s][1] = v.y;
+            u[s][2] = v.z;
+            u[s][3] = v.w;
+          } else if constexpr (kVals == 2) {
+            const uint2 v = *reinterpret_cast<const uint2*>(at);
             u[s][0] = v.x;
             u[s][1] = v.y;
           } else {
-            u[s][0] = *reinterpret_cast<const uint32_t*>(rowk + s * HD);
+            u[s][0] = *reinterpret_cast<const uint32_t*>(at);
           }
         } else {
           mls[s] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-          for (int x = 0; x < kPer / 2; ++x) u[s][x] = 0u;
+          for (int x = 0; x < kVals; ++x) u[s][x] = 0u;
         }
       }
       float mm = -INFINITY;
@@ -866,7 +950,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         lsum += ws;
 #pragma unroll
         for (int x = 0; x < kPer / 2; ++x) {
-          const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u[s][x]));
+          float2 a;
+          if constexpr (TREE)
+            a = make_float2(__uint_as_float(u[s][2 * x]), __uint_as_float(u[s][2 * x + 1]));
+          else
+            a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u[s][x]));
           acc[2 * x] = use ? fmaf(ws, a.x, acc[2 * x]) : acc[2 * x];
           acc[2 * x + 1] = use ? fmaf(ws, a.y, acc[2 * x + 1]) : acc[2 * x + 1];
         }
@@ -1035,14 +1123,14 @@ __global__ void __launch_bounds__(128) combine_kernel(const CombineParams p) {
 
 // Largest cluster of merging attend_kernel CTAs that can be resident on the current device (one
 // CTA per SM: the cluster must fit in one GPC), cached per device.
-template <int HD, bool RING>
+template <int HD, bool RING, bool TREE>
 static int merge_cluster_limit() {
   static int limit[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   if (limit[dev] != 0) return limit[dev];
-  auto kern = attend_kernel<HD, RING, true, false>;
-  constexpr int kSmem = Cfg<HD, RING, true, false>::kSmemBytes;
+  auto kern = attend_kernel<HD, RING, true, false, false, TREE>;
+  constexpr int kSmem = Cfg<HD, RING, true, false, TREE>::kSmemBytes;
   static size_t done[64] = {};
   if (ensure_smem_limit(kern, kSmem, done) != cudaSuccess) return 0;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return 0;
@@ -1059,47 +1147,60 @@ static int merge_cluster_limit() {
   return limit[dev];
 }
 
-template <int HD, bool RING, bool MERGE, bool WIDE, bool DIRECT = false>
+template <int HD, bool RING, bool MERGE, bool WIDE, bool DIRECT, bool TREE>
 static cudaError_t launch_attend_t(const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                                    int num_seqs, cudaStream_t stream) {
   static size_t done[64] = {};
-  auto kern = attend_kernel<HD, RING, MERGE, WIDE, DIRECT>;
-  constexpr int kSmem = Cfg<HD, RING, MERGE, WIDE>::kSmemBytes;
+  auto kern = attend_kernel<HD, RING, MERGE, WIDE, DIRECT, TREE>;
+  constexpr int kSmem = Cfg<HD, RING, MERGE, WIDE, TREE>::kSmemBytes;
   cudaError_t e = ensure_smem_limit(kern, kSmem, done);
   if (e != cudaSuccess) return e;
   dim3 grid(p.num_splits, p.hkv, num_seqs * p.row_tiles);
   if constexpr (!MERGE) {
     return launch_pdl(kern, grid, dim3(kThreads), kSmem, stream, p, tk, tv);
   } else {
-    if (p.num_splits > merge_cluster_limit<HD, RING>()) return cudaErrorNotSupported;
+    if (p.num_splits > merge_cluster_limit<HD, RING, TREE>()) return cudaErrorNotSupported;
     return launch_pdl_cluster(kern, grid, dim3(kThreads), kSmem, p.num_splits, stream, p, tk, tv);
   }
 }
 
-int attend_merge_limit(bool ring, int head_dim) {
-  if (head_dim == 128) return ring ? merge_cluster_limit<128, true>() : merge_cluster_limit<128, false>();
-  return ring ? merge_cluster_limit<64, true>() : merge_cluster_limit<64, false>();
+template <bool TREE>
+static int merge_limit(bool ring, int head_dim) {
+  if (head_dim == 128) return ring ? merge_cluster_limit<128, true, TREE>() : merge_cluster_limit<128, false, TREE>();
+  return ring ? merge_cluster_limit<64, true, TREE>() : merge_cluster_limit<64, false, TREE>();
 }
 
-template <int HD>
+int attend_merge_limit(bool ring, int head_dim, bool tree) {
+  return tree ? merge_limit<true>(ring, head_dim) : merge_limit<false>(ring, head_dim);
+}
+
+template <int HD, bool TREE>
 static cudaError_t launch_attend_hd(bool ring, AttnTiles tiles, const AttnParams& p, const CUtensorMap& tk,
                                     const CUtensorMap& tv, int num_seqs, cudaStream_t stream) {
   if (ring)
-    return tiles == AttnTiles::kMerge ? launch_attend_t<HD, true, true, false>(p, tk, tv, num_seqs, stream)
-                                      : launch_attend_t<HD, true, false, false>(p, tk, tv, num_seqs, stream);
+    return tiles == AttnTiles::kMerge
+               ? launch_attend_t<HD, true, true, false, false, TREE>(p, tk, tv, num_seqs, stream)
+               : launch_attend_t<HD, true, false, false, false, TREE>(p, tk, tv, num_seqs, stream);
   switch (tiles) {
-    case AttnTiles::kMerge: return launch_attend_t<HD, false, true, false>(p, tk, tv, num_seqs, stream);
-    case AttnTiles::kWide: return launch_attend_t<HD, false, false, true>(p, tk, tv, num_seqs, stream);
-    case AttnTiles::kWideDirect: return launch_attend_t<HD, false, false, true, true>(p, tk, tv, num_seqs, stream);
-    default: return launch_attend_t<HD, false, false, false>(p, tk, tv, num_seqs, stream);
+    case AttnTiles::kMerge:
+      return launch_attend_t<HD, false, true, false, false, TREE>(p, tk, tv, num_seqs, stream);
+    case AttnTiles::kWide:
+      return launch_attend_t<HD, false, false, true, false, TREE>(p, tk, tv, num_seqs, stream);
+    case AttnTiles::kWideDirect:
+      return launch_attend_t<HD, false, false, true, true, TREE>(p, tk, tv, num_seqs, stream);
+    default: return launch_attend_t<HD, false, false, false, false, TREE>(p, tk, tv, num_seqs, stream);
   }
 }
 
 cudaError_t launch_attend(bool ring, int head_dim, AttnTiles tiles, const AttnParams& p, const CUtensorMap& tk,
                           const CUtensorMap& tv, int num_seqs, cudaStream_t stream) {
   if (ring && (tiles == AttnTiles::kWide || tiles == AttnTiles::kWideDirect)) return cudaErrorInvalidValue;
-  if (head_dim == 128) return launch_attend_hd<128>(ring, tiles, p, tk, tv, num_seqs, stream);
-  return launch_attend_hd<64>(ring, tiles, p, tk, tv, num_seqs, stream);
+  const bool tree = p.tree_mask != nullptr;
+  if (head_dim == 128)
+    return tree ? launch_attend_hd<128, true>(ring, tiles, p, tk, tv, num_seqs, stream)
+                : launch_attend_hd<128, false>(ring, tiles, p, tk, tv, num_seqs, stream);
+  return tree ? launch_attend_hd<64, true>(ring, tiles, p, tk, tv, num_seqs, stream)
+              : launch_attend_hd<64, false>(ring, tiles, p, tk, tv, num_seqs, stream);
 }
 
 cudaError_t launch_combine(int head_dim, const CombineParams& p, cudaStream_t stream) {

@@ -47,6 +47,9 @@ struct AttnParams {
                                        // nothing completes (the timeout path's test)
   int stable_metadata;        // read the work item before the dependency wait
   int* err;
+  // tree blocks only (null for chains): the row mask and depth of every node
+  const uint32_t* tree_mask;  // [T][VFY_TREE_WORDS]
+  const int32_t* tree_depth;  // [T], window layers
 };
 
 // Splits of one (sequence, KV head) that one cluster can merge in the attention kernel (the
@@ -88,7 +91,92 @@ cudaError_t launch_attend(bool ring, int head_dim, AttnTiles tiles, const AttnPa
                           const CUtensorMap& tv, int num_seqs, cudaStream_t stream);
 cudaError_t launch_combine(int head_dim, const CombineParams& p, cudaStream_t stream);
 // The most splits one merging launch can take on the current device (0 on error).
-int attend_merge_limit(bool ring, int head_dim);
+int attend_merge_limit(bool ring, int head_dim, bool tree);
+
+// ------------------------------ trees -------------------------------------------------------
+struct TreePlanParams {
+  const int32_t* parents;     // [T]
+  const int32_t* cu_q;        // [B+1]
+  int num_seqs;
+  int max_q;                  // nodes per sequence, <= VFY_MAX_TREE_NODES
+  int token_cap;              // host bound on cu_q[B]
+  int32_t* depth;             // [T]
+  uint32_t* mask;             // [T][VFY_TREE_WORDS]
+  int* err;
+};
+cudaError_t launch_tree_plan(const TreePlanParams& p, cudaStream_t stream);
+
+struct CompactParams {
+  const int32_t* path;        // [T]
+  const int32_t* accepted;    // [B]
+  const int32_t* cu_q;        // [B+1]
+  const int32_t* seq_len;     // [B]
+  int num_seqs;
+  int max_q;
+  int token_cap;
+  int hkv, head_dim;
+  int num_layers;
+  // full layers: chunk store (write-through) and pool
+  const int32_t* cu_chunks;
+  const int32_t* slot_of_chunk;
+  long long num_host_chunks;
+  int num_slots;
+  // window layers: ring
+  const int32_t* ring_off;
+  int ring_len;
+  int* err;
+  uint16_t* dst[VFY_MAX_COMPACT_LAYERS][2];    // [layer][K, V]: pool or ring
+  uint16_t* store[VFY_MAX_COMPACT_LAYERS][2];  // full layers
+};
+cudaError_t launch_compact(bool ring, const CompactParams& p, cudaStream_t stream);
+
+// ------------------------------ logit rules -------------------------------------------------
+struct LogitParams {
+  const void* logits;
+  long long stride;           // row stride of logits, in entries
+  int vocab;
+  const int32_t* cu_rows;     // [B+1]
+  int num_seqs;
+  int max_rows;
+  int row_parts;              // CTAs that share a vocabulary segment's rows
+  vfy_logit_rules rules;
+  float* out;
+  int* err;
+};
+cudaError_t launch_process_logits(const LogitParams& p, bool bf16, cudaStream_t stream);
+
+struct CountParams {
+  const int32_t* tokens;
+  const int32_t* cu_tokens;   // [B+1]
+  long long max_tokens;
+  int num_seqs;
+  int vocab;
+  int as_prompt;
+  int32_t* counts;
+  int* err;
+};
+cudaError_t launch_count_tokens(const CountParams& p, cudaStream_t stream);
+
+// ------------------------------ tree acceptance ---------------------------------------------
+struct AcceptTreeParams {
+  const float* logits;
+  int vocab;
+  const int32_t* drafts;
+  const int32_t* parents;
+  const int32_t* cu_rows;
+  int num_seqs;
+  int max_rows;
+  int parts;                  // CTAs per row
+  int seg;                    // vocab entries per CTA
+  int32_t* accepted_len;
+  int32_t* path;
+  int32_t* bonus;
+  int32_t* committed;
+  unsigned long long* keys;   // [max_rows] workspace, zero between calls
+  unsigned int* counters;     // [max_seqs] workspace, zero between calls
+  int* err;
+};
+cudaError_t launch_accept_tree(const AcceptTreeParams& p, cudaStream_t stream);
 
 // ------------------------------ acceptance --------------------------------------------------
 struct AcceptParams {

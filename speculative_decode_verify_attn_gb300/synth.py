@@ -230,3 +230,23 @@ def workload_ragged(seed: int = 0) -> Workload:
     depths = [int(x) for x in rng.choice([2, 4, 8, 11, 16], 8)]
     return Workload("ragged batch of 8, contexts 4K-200K, depths {2,4,8,11,16}, 12 full + 36 window",
                     LAGUNA, lens, depths, n_full=12, n_swa=36, resident_chunks=0)
+
+
+# --------------------------------------------------------------------------------------------
+# Trees of drafted tokens
+# --------------------------------------------------------------------------------------------
+
+def random_tree(rng, n: int, width: int = 6) -> np.ndarray:
+    """Parents of a random tree of n nodes in breadth-first order; node 0 is the root (-1)."""
+    p = np.array([int(rng.integers(max(0, i - width), i)) for i in range(1, n)], dtype=np.int64)
+    return np.concatenate([[-1], np.sort(p)]).astype(np.int32)
+
+
+def tree_drafts_matching(rng, targets, parents, match_prob: float, vocab: int) -> np.ndarray:
+    """Drafted tokens of nodes 1 .. n-1: the target's token of the parent's row with probability
+    match_prob, else a uniform different one."""
+    out = np.empty(len(parents) - 1, dtype=np.int32)
+    for c in range(1, len(parents)):
+        t = int(targets[parents[c]])
+        out[c - 1] = t if rng.random() < match_prob else other_token(rng, t, vocab)
+    return out

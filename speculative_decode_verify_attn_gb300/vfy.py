@@ -16,7 +16,13 @@ VFY_OK, VFY_EINVAL, VFY_ECUDA, VFY_ENOMEM, VFY_EUNSUPPORTED, VFY_EDEVICE_INPUT, 
 EXPORTS = ("vfy_create", "vfy_destroy", "vfy_get_status", "vfy_strerror", "vfy_set_splits",
            "vfy_select_resident", "vfy_page_in", "vfy_attend_full", "vfy_attend_swa", "vfy_accept",
            "vfy_accept_static", "vfy_launch_count", "vfy_append_full", "vfy_append_swa",
-           "vfy_gate_depths", "vfy_test_wait_timeout", "vfy_set_stable_metadata", "vfy_set_pagein_ctas")
+           "vfy_gate_depths", "vfy_test_wait_timeout", "vfy_set_stable_metadata", "vfy_set_pagein_ctas",
+           "vfy_tree_plan", "vfy_attend_full_tree", "vfy_attend_swa_tree", "vfy_process_logits",
+           "vfy_count_tokens", "vfy_accept_tree", "vfy_compact_full", "vfy_compact_swa")
+
+MAX_TREE_NODES = 256      # VFY_MAX_TREE_NODES
+TREE_WORDS = 8            # VFY_TREE_WORDS
+MAX_COMPACT_LAYERS = 64   # VFY_MAX_COMPACT_LAYERS
 
 
 class VfyError(RuntimeError):
@@ -69,6 +75,14 @@ def lib() -> ctypes.CDLL:
         L.vfy_append_full.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_int64, _P, _P, _I, _I, _P]
         L.vfy_append_swa.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _I, _P]
         L.vfy_gate_depths.argtypes = [_P, _I, _I, _I, _P]
+        L.vfy_tree_plan.argtypes = [_P, _P, _P, _P, _P, _I, _P]
+        L.vfy_attend_full_tree.argtypes = [_P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _P, _P, _P, _I, _P]
+        L.vfy_attend_swa_tree.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P]
+        L.vfy_process_logits.argtypes = [_P, _P, _I, ctypes.c_int64, _I, _P, _I, _P, _P, _I, _P]
+        L.vfy_count_tokens.argtypes = [_P, _P, _P, ctypes.c_int64, _I, _I, _P, _I, _I, _P]
+        L.vfy_accept_tree.argtypes = [_P, _P, _I, _P, _P, _P, _I, _P, _P, _P, _P, _I, _P]
+        L.vfy_compact_full.argtypes = [_P, _P, _P, _P, _P, _P, _P, _I, _P, _P, ctypes.c_int64, _P, _P, _I, _I, _P]
+        L.vfy_compact_swa.argtypes = [_P, _P, _P, _P, _P, _P, _I, _P, _P, _I, _P]
         L.vfy_launch_count.argtypes = [_P]
         L.vfy_launch_count.restype = ctypes.c_ulonglong
         for name in EXPORTS:
@@ -279,3 +293,120 @@ def vfy_accept_static(logits, vocab: int, drafts, cu_rows, num_seqs: int, max_ro
         num_seqs, max_rows, _dev(accepted_len, I32, "accepted_len"), _dev(bonus, I32, "bonus"),
         _dev(committed, I32, "committed"), _dev(device_error, I32, "device_error"), _stream(stream)),
         "vfy_accept_static")
+
+
+# ---------------------------------------------------------------------------------------------
+# Tree speculation
+# ---------------------------------------------------------------------------------------------
+
+U32 = (torch.int32, torch.uint32)       # row and grammar masks: 32-bit words
+
+
+class LogitRules:
+    """What vfy_process_logits does to the logits (vfy_logit_rules; every tensor may be None). Keeps
+    the tensors alive: build it once for buffers that stay where they are."""
+
+    class _Struct(ctypes.Structure):
+        _fields_ = [("counts", _P), ("repetition", _P), ("frequency", _P), ("presence", _P), ("drafts", _P),
+                    ("tree_mask", _P), ("cu_bias", _P), ("bias_token", _P), ("bias_value", _P), ("grammar", _P),
+                    ("mask_index", _P), ("num_masks", _I)]
+
+    def __init__(self, counts=None, repetition=None, frequency=None, presence=None, drafts=None, tree_mask=None,
+                 cu_bias=None, bias_token=None, bias_value=None, grammar=None, mask_index=None):
+        self.tensors = (counts, repetition, frequency, presence, drafts, tree_mask, cu_bias, bias_token, bias_value,
+                        grammar, mask_index)
+        self.struct = LogitRules._Struct(
+            _dev(counts, I32, "counts"), _dev(repetition, F32, "repetition"), _dev(frequency, F32, "frequency"),
+            _dev(presence, F32, "presence"), _dev(drafts, I32, "drafts"), _dev(tree_mask, U32, "tree_mask"),
+            _dev(cu_bias, I32, "cu_bias"), _dev(bias_token, I32, "bias_token"), _dev(bias_value, F32, "bias_value"),
+            _dev(grammar, U32, "grammar"), _dev(mask_index, I32, "mask_index"),
+            0 if grammar is None else grammar.shape[0])
+        self.vocab = None if counts is None else counts.shape[-1]
+        self.mask_words = None if grammar is None else grammar.shape[-1]
+
+
+def vfy_tree_plan(ctx: Context, parents, cu_q, depth, tree_mask, num_seqs: int, stream=None):
+    _check(lib().vfy_tree_plan(
+        ctx.handle, _dev(parents, I32, "parents"), _dev(cu_q, I32, "cu_q"), _dev(depth, I32, "depth"),
+        _dev(tree_mask, U32, "tree_mask"), num_seqs, _stream(stream)), "vfy_tree_plan")
+
+
+def vfy_attend_full_tree(ctx: Context, q, cu_q, tree_mask, k_pool, v_pool, num_slots: int, resident_ids,
+                         resident_slots, cu_resident, max_resident_per_seq: int, seq_len, out, lse, num_seqs: int,
+                         stream=None):
+    _check(lib().vfy_attend_full_tree(
+        ctx.handle, _dev(q, BF16, "q"), _dev(cu_q, I32, "cu_q"), _dev(tree_mask, U32, "tree_mask"),
+        _dev(k_pool, BF16, "k_pool"), _dev(v_pool, BF16, "v_pool"), num_slots, _dev(resident_ids, I32, "resident_ids"),
+        _dev(resident_slots, I32, "resident_slots"), _dev(cu_resident, I32, "cu_resident"), max_resident_per_seq,
+        _dev(seq_len, I32, "seq_len"), _dev(out, BF16, "out"), _dev(lse, F32, "lse"), num_seqs, _stream(stream)),
+        "vfy_attend_full_tree")
+
+
+def vfy_attend_swa_tree(ctx: Context, q, cu_q, tree_mask, depth, k_ring, v_ring, ring_offset, seq_len, out, lse,
+                        num_seqs: int, stream=None):
+    _check(lib().vfy_attend_swa_tree(
+        ctx.handle, _dev(q, BF16, "q"), _dev(cu_q, I32, "cu_q"), _dev(tree_mask, U32, "tree_mask"),
+        _dev(depth, I32, "depth"), _dev(k_ring, BF16, "k_ring"), _dev(v_ring, BF16, "v_ring"),
+        _dev(ring_offset, I32, "ring_offset"), _dev(seq_len, I32, "seq_len"), _dev(out, BF16, "out"),
+        _dev(lse, F32, "lse"), num_seqs, _stream(stream)), "vfy_attend_swa_tree")
+
+
+def vfy_process_logits(ctx: Context, logits, vocab: int, cu_rows, max_rows: int, rules: LogitRules, out,
+                       num_seqs: int, stream=None):
+    """`logits`: fp32 or bf16 [rows][vocab]; its rows may be further apart than `vocab` entries (a view
+    of a wider matrix). `out`: fp32 [rows][vocab], or the logits themselves."""
+    if not logits.is_cuda or logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"logits must be a float32 or bfloat16 CUDA tensor, got {logits.dtype} on {logits.device}")
+    if logits.dim() != 2 or logits.stride(1) != 1 or logits.shape[1] < vocab:
+        raise ValueError("logits must be [rows][vocab] with contiguous rows")
+    if rules.vocab not in (None, vocab) or rules.mask_words not in (None, (vocab + 31) // 32):
+        raise ValueError("the rules' counts or grammar masks are for another vocabulary")
+    _check(lib().vfy_process_logits(
+        ctx.handle, _P(logits.data_ptr()), 1 if logits.dtype == torch.bfloat16 else 0,
+        logits.stride(0) if logits.shape[0] > 1 else logits.shape[1], vocab, _dev(cu_rows, I32, "cu_rows"), max_rows,
+        ctypes.byref(rules.struct), _dev(out, F32, "out"), num_seqs, _stream(stream)), "vfy_process_logits")
+
+
+def vfy_count_tokens(ctx: Context, tokens, cu_tokens, max_tokens: int, counts, vocab: int, num_seqs: int, *,
+                     as_prompt: bool = False, reset: bool = False, stream=None):
+    _check(lib().vfy_count_tokens(
+        ctx.handle, _dev(tokens, I32, "tokens"), _dev(cu_tokens, I32, "cu_tokens"), max_tokens, 1 if as_prompt else 0,
+        1 if reset else 0, _dev(counts, I32, "counts"), vocab, num_seqs, _stream(stream)), "vfy_count_tokens")
+
+
+def vfy_accept_tree(ctx: Context, logits, vocab: int, drafts, parents, cu_rows, max_rows: int, accepted_len, path,
+                    bonus, committed, num_seqs: int, stream=None):
+    _check(lib().vfy_accept_tree(
+        ctx.handle, _dev(logits, F32, "logits"), vocab, _dev(drafts, I32, "drafts"), _dev(parents, I32, "parents"),
+        _dev(cu_rows, I32, "cu_rows"), max_rows, _dev(accepted_len, I32, "accepted_len"), _dev(path, I32, "path"),
+        _dev(bonus, I32, "bonus"), _dev(committed, I32, "committed"), num_seqs, _stream(stream)), "vfy_accept_tree")
+
+
+def _layers(tensors, name: str, host_allowed: bool = False):
+    """A host array of the layers' pointers."""
+    return (_P * len(tensors))(*[
+        _host(t, BF16, name) if host_allowed and not t.is_cuda else _dev(t, BF16, name) for t in tensors])
+
+
+def vfy_compact_full(ctx: Context, path, accepted_len, cu_q, seq_len, cu_chunks, slot_of_chunk, host_k, host_v,
+                     num_host_chunks: int, k_pool, v_pool, num_slots: int, num_seqs: int, stream=None):
+    """host_k, host_v, k_pool, v_pool: one tensor per layer, in lists of one length."""
+    if not len(host_k) == len(host_v) == len(k_pool) == len(v_pool):
+        raise ValueError("host_k, host_v, k_pool and v_pool must have one tensor per layer")
+    _check(lib().vfy_compact_full(
+        ctx.handle, _dev(path, I32, "path"), _dev(accepted_len, I32, "accepted_len"), _dev(cu_q, I32, "cu_q"),
+        _dev(seq_len, I32, "seq_len"), _dev(cu_chunks, I32, "cu_chunks"), _dev(slot_of_chunk, I32, "slot_of_chunk"),
+        len(k_pool), _layers(host_k, "host_k", True), _layers(host_v, "host_v", True), num_host_chunks,
+        _layers(k_pool, "k_pool"), _layers(v_pool, "v_pool"), num_slots, num_seqs, _stream(stream)),
+        "vfy_compact_full")
+
+
+def vfy_compact_swa(ctx: Context, path, accepted_len, cu_q, seq_len, ring_offset, k_ring, v_ring, num_seqs: int,
+                    stream=None):
+    """k_ring, v_ring: one tensor per layer, in lists of one length."""
+    if len(k_ring) != len(v_ring):
+        raise ValueError("k_ring and v_ring must have one tensor per layer")
+    _check(lib().vfy_compact_swa(
+        ctx.handle, _dev(path, I32, "path"), _dev(accepted_len, I32, "accepted_len"), _dev(cu_q, I32, "cu_q"),
+        _dev(seq_len, I32, "seq_len"), _dev(ring_offset, I32, "ring_offset"), len(k_ring),
+        _layers(k_ring, "k_ring"), _layers(v_ring, "v_ring"), num_seqs, _stream(stream)), "vfy_compact_swa")
