@@ -659,7 +659,7 @@ vfy_status vfy_process_logits(vfy_ctx* ctx, const void* logits, int logits_type,
   VFY_REQUIRE(vocab >= 1 && vocab <= kMaxVocab && row_stride >= vocab);
   VFY_REQUIRE((reinterpret_cast<uintptr_t>(logits) & (bf16 ? 1u : 3u)) == 0);
   VFY_REQUIRE((reinterpret_cast<uintptr_t>(out) & 3u) == 0);
-  VFY_REQUIRE(num_seqs >= 1 && num_seqs <= ctx->cfg.max_seqs && num_seqs <= 65535);
+  VFY_REQUIRE(num_seqs >= 1 && num_seqs <= ctx->cfg.max_seqs);
   VFY_REQUIRE(max_rows >= 1 && max_rows <= ctx->accept_rows_cap);
   VFY_REQUIRE(row_stride <= (INT64_MAX / 8) / max_rows);
   const vfy_logit_rules& r = *rules;
@@ -681,7 +681,15 @@ vfy_status vfy_process_logits(vfy_ctx* ctx, const void* logits, int logits_type,
   p.cu_rows = cu_rows;
   p.num_seqs = num_seqs;
   p.max_rows = max_rows;
-  p.row_parts = 1;
+  // About four CTAs per SM where the rows allow it, else one for all rows of a segment: each reads the
+  // segment's counts and biases. (Where rows start at different places of a 16-byte word, parts that are
+  // a multiple of 4 hold rows that start alike.)
+  const bool even = vocab % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & 15u) == 0 && row_stride % 4 == 0;
+  p.segs = vfy::logit_segments(vocab, even);
+  const long long ctas = static_cast<long long>(p.segs) * num_seqs;
+  const int rows_per_seq = std::min(ceil_div(max_rows, num_seqs), VFY_MAX_TREE_NODES);
+  p.row_parts = clampi(ceil_div(4LL * ctx->num_sms, ctas), 1, rows_per_seq);
+  if (!even && p.row_parts > 1) p.row_parts = (p.row_parts + 3) & ~3;
   p.rules = r;
   p.out = out;
   p.err = ctx->err;
@@ -700,7 +708,6 @@ vfy_status vfy_count_tokens(vfy_ctx* ctx, const int32_t* tokens, const int32_t* 
   DeviceGuard guard(ctx->device);
   if (!guard.ok) return VFY_ECUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (reset) VFY_CUDA(cudaMemsetAsync(counts, 0, static_cast<size_t>(num_seqs) * vocab * sizeof(int32_t), s));
   vfy::CountParams p;
   p.tokens = tokens;
   p.cu_tokens = cu_tokens;
@@ -708,6 +715,9 @@ vfy_status vfy_count_tokens(vfy_ctx* ctx, const int32_t* tokens, const int32_t* 
   p.num_seqs = num_seqs;
   p.vocab = vocab;
   p.as_prompt = as_prompt;
+  p.reset = reset;
+  // A reset takes segments for about one wave of CTAs, of 1K to 8K counts (32 KB of shared memory).
+  p.seg = clampi(ceil_div(static_cast<long long>(vocab) * num_seqs, ctx->num_sms), 1024, 8192);
   p.counts = counts;
   p.err = ctx->err;
   VFY_CUDA(vfy::launch_count_tokens(p, s));

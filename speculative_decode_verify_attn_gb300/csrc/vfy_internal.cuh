@@ -138,12 +138,15 @@ struct LogitParams {
   const int32_t* cu_rows;     // [B+1]
   int num_seqs;
   int max_rows;
-  int row_parts;              // CTAs that share a vocabulary segment's rows
+  int segs;                   // vocabulary segments
+  int row_parts;              // CTAs that share a vocabulary segment's rows: row r goes to r mod row_parts
   vfy_logit_rules rules;
   float* out;
   int* err;
 };
 cudaError_t launch_process_logits(const LogitParams& p, bool bf16, cudaStream_t stream);
+// vocabulary segments (CTAs) of one row; even: every row starts on a 16-byte boundary of out
+int logit_segments(int vocab, bool even);
 
 struct CountParams {
   const int32_t* tokens;
@@ -152,6 +155,8 @@ struct CountParams {
   int num_seqs;
   int vocab;
   int as_prompt;
+  int reset;
+  int seg;                    // reset: counts per CTA
   int32_t* counts;
   int* err;
 };
