@@ -54,19 +54,16 @@ def _attend(q, group, keys, values, see, scale):
     n, hq, d = q.shape
     out, mag = np.zeros((n, hq, d)), np.zeros((n, hq, d))
     lse = np.full((n, hq), -math.inf)
+    some = see.any(axis=1)
     for g in range(hq):
         h = g // group
-        for i in range(n):
-            at = np.flatnonzero(see[i])
-            if not at.size:
-                continue
-            s = scale * (keys[h][at] @ q[i, g])
-            m = s.max()
-            w = np.exp(s - m)
-            z = w.sum()
-            out[i, g] = (w / z) @ values[h][at]
-            mag[i, g] = (w / z) @ np.abs(values[h][at])
-            lse[i, g] = m + math.log(z)
+        s = np.where(see, scale * (q[:, g] @ keys[h].T), -math.inf)
+        m = np.where(some, s.max(axis=1, initial=-math.inf), 0.0)
+        w = np.exp(s - m[:, None])
+        z = np.where(some, w.sum(axis=1), 1.0)
+        w /= z[:, None]
+        out[:, g], mag[:, g] = w @ values[h], w @ np.abs(values[h])
+        lse[some, g] = (m + np.log(z))[some]
     return out, lse, mag
 
 

@@ -164,8 +164,9 @@ vfy_status vfy_create(const vfy_config* cfg_in, int device, vfy_ctx** out) {
   ctx->scale = cfg.softmax_scale > 0.f ? cfg.softmax_scale : 1.0f / std::sqrt(static_cast<float>(cfg.head_dim));
 
   ctx->row_tiles = ceil_div(static_cast<long long>(cfg.max_queries_per_seq) * group, kMaxRows);
-  const size_t parts =
-      static_cast<size_t>(cfg.max_seqs) * ctx->row_tiles * cfg.num_kv_heads * cfg.max_splits * kMaxRows;
+  size_t parts = static_cast<size_t>(cfg.max_seqs) * ctx->row_tiles * cfg.num_kv_heads * cfg.max_splits * kMaxRows;
+  // tree attention in pairs of row tiles: two partial segments per SM
+  parts = std::max(parts, static_cast<size_t>(ctx->num_sms) * 2 * 2 * kMaxRows);
   ctx->accept_rows_cap = cfg.max_seqs * cfg.max_queries_per_seq;
   bool ok = cudaMalloc(&ctx->part_o, parts * cfg.head_dim * sizeof(float)) == cudaSuccess &&
             cudaMalloc(&ctx->part_ml, parts * 2 * sizeof(float)) == cudaSuccess &&
@@ -403,6 +404,10 @@ vfy_status vfy_append_swa(vfy_ctx* ctx, const uint16_t* k_new, const uint16_t* v
 // Nodes of one sequence's tree that a context takes.
 static int tree_capacity(const vfy_config& c) { return std::min(c.max_queries_per_seq, VFY_MAX_TREE_NODES); }
 
+static bool tree_pairs(const vfy_ctx* ctx, int row_tiles, int num_seqs) {
+  return ctx->full_splits == 0 && (row_tiles > 1 || num_seqs > 1);
+}
+
 static vfy_status attend_common(vfy_ctx* ctx, bool ring, const uint16_t* q, const int32_t* cu_q,
                                 const uint16_t* k_src, const uint16_t* v_src, uint64_t src_rows,
                                 const int32_t* ids, const int32_t* slots, const int32_t* cu_res, int num_slots,
@@ -481,6 +486,16 @@ static vfy_status attend_common(vfy_ctx* ctx, bool ring, const uint16_t* q, cons
   p.err = ctx->err;
   p.tree_mask = tree_mask;
   p.tree_depth = tree_depth;
+  p.num_seqs = num_seqs;
+  p.token_cap = num_seqs * max_q;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (tree && !ring && tree_pairs(ctx, row_tiles, num_seqs)) {
+    p.out = out;
+    p.lse = lse;
+    VFY_CUDA(vfy::launch_attend_tree(c.head_dim, p, tk, tv, ctx->num_sms, s));
+    ctx->launches += 2;
+    return VFY_OK;
+  }
   // Full-layer splits over many resident chunks take wide tiles (their combine is a small part
   // of a long split). Otherwise up to kMaxClusterSplits splits (and no more than one GPC holds)
   // merge inside the attention kernel, as one thread-block cluster per (sequence, KV head, row
@@ -496,8 +511,6 @@ static vfy_status attend_common(vfy_ctx* ctx, bool ring, const uint16_t* q, cons
                                        : vfy::AttnTiles::kNarrow;
   p.out = merge || direct ? out : nullptr;
   p.lse = merge || direct ? lse : nullptr;
-  p.token_cap = num_seqs * max_q;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   VFY_CUDA(vfy::launch_attend(ring, c.head_dim, tiles, p, tk, tv, num_seqs, s));
   ++ctx->launches;
   if (merge || direct) return VFY_OK;

@@ -50,6 +50,7 @@ struct AttnParams {
   // tree blocks only (null for chains): the row mask and depth of every node
   const uint32_t* tree_mask;  // [T][VFY_TREE_WORDS]
   const int32_t* tree_depth;  // [T], window layers
+  int num_seqs;               // attend_tree_kernel: the grid is no function of it
 };
 
 // Splits of one (sequence, KV head) that one cluster can merge in the attention kernel (the
@@ -94,6 +95,11 @@ cudaError_t launch_combine(int head_dim, const CombineParams& p, cudaStream_t st
 int attend_merge_limit(bool ring, int head_dim, bool tree);
 
 // ------------------------------ trees -------------------------------------------------------
+// Tree attention of a full layer in 256-row pairs by `ctas` persistent CTAs, and the merge (two
+// launches). p.part_o / p.part_ml hold 2 * ctas partial segments of 256 rows.
+cudaError_t launch_attend_tree(int head_dim, const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                               int ctas, cudaStream_t stream);
+
 struct TreePlanParams {
   const int32_t* parents;     // [T]
   const int32_t* cu_q;        // [B+1]

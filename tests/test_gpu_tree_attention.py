@@ -229,6 +229,34 @@ def test_ragged_batch(env, splits):
         ctx.close()
 
 
+@pytest.mark.parametrize("ns,Ls", [([9, 47, 20, 64, 3], [60000, 50000, 70000, 3000, 130]), ([64, 10], [40000, 190000]),
+                                   ([10, 64], [190000, 40000]), ([130, 200, 64], [30000, 64000, 90000])])
+def test_long_ragged_batch(env, ns, Ls):
+    """One KV head, so that a CTA's run holds many tiles and passes from sequences of one row tile to such
+    of two and back."""
+    H, vfy = env
+    rng = np.random.default_rng(sum(Ls))
+    hq, d = 4, 64
+    cu = np.concatenate([[0], np.cumsum(ns)])
+    counts = [-(-L // C) for L in Ls]
+    cu_res = np.concatenate([[0], np.cumsum(counts)])
+    total = int(cu_res[-1])
+    slots = rng.permutation(total)
+    kp, vp = synth.normal_bf16(rng, (total, 1, C, d)), synth.normal_bf16(rng, (total, 1, C, d))
+    q = synth.normal_bf16(rng, (int(cu[-1]), hq, d))
+    sets = [T.ancestors(synth.random_tree(rng, n).tolist()) for n in ns]
+    ids = np.concatenate([np.arange(c) for c in counts])
+    ctx = vfy.vfy_create(hq, 1, d, max_seqs=len(ns), max_queries_per_seq=256, device=0)
+    try:
+        got, lse = attend_full(H, vfy, ctx, q, cu, T.mask_words(sum(sets, [])), kp, vp, ids, slots, cu_res, Ls)
+        assert vfy.vfy_get_status(ctx) == vfy.VFY_OK
+        for b in range(len(ns)):
+            rows, at = slice(cu[b], cu[b + 1]), slice(cu_res[b], cu_res[b + 1])
+            check(got[rows], lse[rows], *T.attend_tree_full_seq(q[rows], sets[b], kp, vp, ids[at], slots[at], Ls[b]), f"{b}")
+    finally:
+        ctx.close()
+
+
 @pytest.mark.parametrize("n", [1, 17, 32])
 def test_a_chain_gives_the_bits_of_the_linear_block(env, n):
     """A chain's masks and depths: in a full layer whose splits go through the combine, a block of one
