@@ -14,11 +14,13 @@
 // A run has at most two partial segments, its first and its last: 2 slots per CTA.
 //
 // Warps: 0-3 softmax and epilogue of row tile 0, 4-7 of row tile 1 (TMEM lane = row, one thread per row),
-// 8 K producer and tile geometry, 9 V producer, 10 MMA issuer. Tensor memory: two S buffers of 128 columns
-// (P, bf16, over the first half of its S), two O accumulators. In a pair buffer h belongs to row tile h,
-// and the issuer alternates PV_0(j), S_0(j+1), PV_1(j), S_1(j+1): one tile's MMAs run during the other's
-// softmax. A segment of at most 128 rows has no second tile; its S alternates between the two buffers,
-// S(j+1) before PV(j).
+// 8 K producer and tile geometry, 9 V producer, 10 and 11 MMA issuers, one per row tile. A tile's two chunks
+// are two steps. Tensor memory per row tile: two S buffers of 64 columns (P, bf16, over the first half of its
+// S) and O. S of step s+1 is issued before PV of step s, so the tensor core works on one step while the
+// softmax works on the other, and the two row tiles run free of each other. An MMA costs its issuer 50 to 110
+// cycles beside busy softmax warps, more than its 32 or 64 cycles in the tensor pipe: hence two issuers. In a
+// segment of at most 128 rows the second row tile's warps only keep the barrier protocol, so that every role
+// sees every phase of every barrier it waits on.
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -29,16 +31,17 @@
 namespace vfy {
 namespace {
 
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;
 constexpr int kKWarp = 8;
 constexpr int kVWarp = 9;
-constexpr int kMmaWarp = 10;
+constexpr int kMmaWarp = 10;              // and 11
+constexpr int kVRelayWarp = 3;            // softmax warp of a row tile whose P arrival waits for V
 constexpr int kPairRows = 2 * kMaxRows;
 constexpr int kKeys = 2 * kChunk;         // keys per tile
 constexpr int kGeo = 8;                   // tile-geometry ring
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0;             // two S buffers of kKeys columns
-constexpr uint32_t kColO = 256;           // two O accumulators of d columns, 128 apart
+constexpr uint32_t kColS = 0;             // [row tile][chunk]: S buffers of kChunk columns
+constexpr uint32_t kColO = 256;           // [row tile]: O accumulators of d columns, 128 apart
 constexpr int kPrefetch = 3;              // tiles prefetched into L2 beyond the shared-memory stages
 // A row keeps a stale reference maximum until a tile's maximum exceeds it by this much (log2 units).
 constexpr float kRescaleLog2 = 8.0f;
@@ -52,23 +55,24 @@ struct Cfg {
   static constexpr int kTileBytes = kKeys * HD * 2;
   static constexpr int kQBoxBytes = kMaxRows * 128;
   static constexpr int kQTileBytes = kMaxRows * HD * 2;
-  static constexpr int kStages = HD == 128 ? 2 : 4;     // of K and of V
-  static constexpr int kBarOffset = 2 * kQTileBytes + 2 * kStages * kTileBytes;
+  // A K stage frees as soon as both row tiles' S have read it, a V stage only after their last PV.
+  static constexpr int kKStages = HD == 128 ? 2 : 4;
+  static constexpr int kVStages = HD == 128 ? 3 : 4;
+  static constexpr int kBarOffset = 2 * kQTileBytes + (kKStages + kVStages) * kTileBytes;
   static constexpr int kSmemBytes = kBarOffset + 2048 + 1024;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
-  static_assert(kStages + 3 <= kGeo, "geometry ring");
+  static_assert(kKStages + 3 <= kGeo && kKStages <= 4 && kVStages <= 4, "rings");
 };
 
 struct Bars {
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
   uint64_t geo_full[kGeo];
-  uint64_t s_full[2];      // [S buffer]
-  uint64_t p_full[2];      // [S buffer]: the tile's P is written (and V's outside rows are zero)
-  uint64_t o_full[2];      // [row tile]: one phase per PV (before rescaling O)
-  uint64_t o_done[2];      // [row tile]: one phase per segment, after its last PV (before the epilogue)
+  uint64_t s_full[2][2];   // [row tile][chunk], one phase per tile
+  uint64_t p_full[2][2];   // [row tile][chunk]: P is written (and V has landed, its outside rows zeroed)
+  uint64_t o_full[2];      // [row tile]: one phase per step, after its PV
+  uint64_t o_done[2];      // [row tile]: one phase per segment with rows in it, after its last PV
   uint64_t q_ready[2];     // [row tile]: one phase per segment
-  uint64_t single_done;    // one phase per segment of one row tile
-  uint64_t drain, never;
+  uint64_t drain[2], never;
   uint32_t tmem_base;
   int abort;
   int base[kGeo][2];       // position of each chunk's first key
@@ -243,28 +247,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
   uint8_t* sK = smem + 2 * C::kQTileBytes;
-  uint8_t* sV = sK + C::kStages * C::kTileBytes;
+  uint8_t* sV = sK + C::kKStages * C::kTileBytes;
   Bars* bars = reinterpret_cast<Bars*>(smem + C::kBarOffset);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == kKWarp * 32) {
-    for (int i = 0; i < C::kStages; ++i) {
+    for (int i = 0; i < C::kKStages; ++i) {
       mbar_init(&bars->k_full[i], 1);
-      mbar_init(&bars->k_empty[i], 1);
+      mbar_init(&bars->k_empty[i], 2);       // both issuers
+    }
+    for (int i = 0; i < C::kVStages; ++i) {
       mbar_init(&bars->v_full[i], 1);
-      mbar_init(&bars->v_empty[i], 1);
+      mbar_init(&bars->v_empty[i], 2);
     }
     for (int i = 0; i < kGeo; ++i) mbar_init(&bars->geo_full[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars->s_full[i], 1);
-      mbar_init(&bars->p_full[i], 128);
+      for (int k = 0; k < 2; ++k) {
+        mbar_init(&bars->s_full[i][k], 1);
+        mbar_init(&bars->p_full[i][k], 128);
+      }
+      mbar_init(&bars->drain[i], 1);
       mbar_init(&bars->o_full[i], 1);
       mbar_init(&bars->o_done[i], 1);
       mbar_init(&bars->q_ready[i], 128);
     }
-    mbar_init(&bars->single_done, 1);
-    mbar_init(&bars->drain, 1);
     mbar_init(&bars->never, 1);
     bars->abort = 0;
     fence_mbar_init();
@@ -299,8 +306,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true, reported = false;
       for (; ok && w.more(); w.next(p)) {
         for (int j = 0; j < w.nt; ++j, ++n) {
-          const int st = n % C::kStages;
-          if (n >= C::kStages) ok = mbar_wait(&bars->k_empty[st], (n / C::kStages - 1) & 1, abort, p.err);
+          const int st = n % C::kKStages;
+          if (n >= C::kKStages) ok = mbar_wait(&bars->k_empty[st], (n / C::kKStages - 1) & 1, abort, p.err);
           if (!ok) break;
           const int g = n % kGeo;
           const int p0 = w.s.L - w.s.nq;
@@ -334,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                           &bars->k_full[st], bx * 64, c[i].y, pol);
           }
           // more of the stream in flight from HBM than the stages hold
-          const int f = j + kPrefetch + C::kStages - 1;
+          const int f = j + kPrefetch + C::kKStages - 1;
           if (f < w.nt) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -350,8 +357,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // every copy lands before the CTA can exit, also when the pipeline was aborted
-      for (uint32_t i = n > C::kStages ? n - C::kStages : 0; i < n; ++i)
-        mbar_drain(&bars->k_full[i % C::kStages], (i / C::kStages) & 1, p.err);
+      for (uint32_t i = n > C::kKStages ? n - C::kKStages : 0; i < n; ++i)
+        mbar_drain(&bars->k_full[i % C::kKStages], (i / C::kKStages) & 1, p.err);
     }
   } else if (warp == kVWarp) {
     // ------------------------------ V producer --------------------------------------------------
@@ -361,8 +368,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (; ok && w.more(); w.next(p)) {
         for (int j = 0; j < w.nt; ++j, ++n) {
-          const int st = n % C::kStages;
-          if (n >= C::kStages) ok = mbar_wait(&bars->v_empty[st], (n / C::kStages - 1) & 1, abort, p.err);
+          const int st = n % C::kVStages;
+          if (n >= C::kVStages) ok = mbar_wait(&bars->v_empty[st], (n / C::kVStages - 1) & 1, abort, p.err);
           if (!ok) break;
           Chunk c[2];
           int present = 0;
@@ -382,100 +389,85 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      for (uint32_t i = n > C::kStages ? n - C::kStages : 0; i < n; ++i)
-        mbar_drain(&bars->v_full[i % C::kStages], (i / C::kStages) & 1, p.err);
+      for (uint32_t i = n > C::kVStages ? n - C::kVStages : 0; i < n; ++i)
+        mbar_drain(&bars->v_full[i % C::kVStages], (i / C::kVStages) & 1, p.err);
     }
-  } else if (warp == kMmaWarp) {
-    // ------------------------------ MMA issuer (one lane) ---------------------------------------
+  } else if (warp >= kMmaWarp) {
+    // ------------------------------ MMA issuers (one lane each) ---------------------------------
     if (lane == 0) {
-      if (p.timeout_test_ns != 0) mbar_wait_limit(&bars->never, 0, p.timeout_test_ns, abort, p.err);
+      const int h = warp - kMmaWarp;         // row tile
+      if (h == 0 && p.timeout_test_ns != 0) mbar_wait_limit(&bars->never, 0, p.timeout_test_ns, abort, p.err);
       bool ok = !*abort;
-      const uint32_t idesc_s = idesc_bf16_f32(128, kKeys, 0, 0);
+      const uint32_t idesc_s = idesc_bf16_f32(128, kChunk, 0, 0);
       const uint32_t idesc_pv = idesc_bf16_f32(128, HD, 0, 1);
-      const uint64_t qdesc = sw128_desc(smem_u32(sQ), 16, 1024);
-      const uint64_t kdesc = sw128_desc(smem_u32(sK), 16, 1024);
-      const uint64_t vdesc = sw128_desc(smem_u32(sV), C::kBoxBytes, 1024);
-      uint32_t n = 0;                        // tiles before this segment
-      uint32_t used[2] = {0, 0};             // P's consumed per S buffer
+      const uint64_t qd = sw128_desc(smem_u32(sQ + h * C::kQTileBytes), 16, 1024);
+      const uint64_t kd = sw128_desc(smem_u32(sK), 16, 1024);
+      const uint64_t vd = sw128_desc(smem_u32(sV), C::kBoxBytes, 1024);
+      const uint32_t q_lo = static_cast<uint32_t>(qd), q_hi = static_cast<uint32_t>(qd >> 32);
+      const uint32_t k_lo = static_cast<uint32_t>(kd), k_hi = static_cast<uint32_t>(kd >> 32);
+      const uint32_t v_lo = static_cast<uint32_t>(vd), v_hi = static_cast<uint32_t>(vd >> 32);
+      const uint32_t col_s = tbase + kColS + h * 128, col_o = tbase + kColO + h * 128;
+      uint32_t n = 0;                        // tiles of the run before the segment's
       uint32_t segs = 0;                     // segments so far
-      // S of row tile h, tile i of the run, into buffer `buf`
-      auto issue_s = [&](int h, int buf, uint32_t i) {
-        const uint64_t q = qdesc + static_cast<uint64_t>((h * C::kQTileBytes) >> 4);
-        const uint64_t kd = kdesc + static_cast<uint64_t>(((i % C::kStages) * C::kTileBytes) >> 4);
-#pragma unroll
-        for (int kk = 0; kk < HD / 16; ++kk)
-          mma_ss(tbase + kColS + buf * kKeys,
-                 q + static_cast<uint64_t>(((kk >> 2) * C::kQBoxBytes + (kk & 3) * 32) >> 4),
-                 kd + static_cast<uint64_t>(((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4), idesc_s, kk > 0 ? 1u : 0u);
-        mma_commit(&bars->s_full[buf]);
-      };
-      auto issue_pv = [&](int h, int buf, uint32_t i, bool first, bool last) {
-        const uint64_t vd = vdesc + static_cast<uint64_t>(((i % C::kStages) * C::kTileBytes) >> 4);
-#pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-          mma_ts(tbase + kColO + h * 128, tbase + kColS + buf * kKeys + kk * 8,
-                 vd + static_cast<uint64_t>((16 * kk * 128) >> 4), idesc_pv, (!first || kk > 0) ? 1u : 0u);
-        mma_commit(&bars->o_full[h]);
-        if (last) mma_commit(&bars->o_done[h]);
-      };
-      auto wait_k = [&](uint32_t i) {
-        return mbar_wait(&bars->k_full[i % C::kStages], (i / C::kStages) & 1, abort, p.err);
-      };
-      auto wait_v = [&](uint32_t i) {
-        return mbar_wait(&bars->v_full[i % C::kStages], (i / C::kStages) & 1, abort, p.err);
-      };
-      auto wait_p = [&](int buf) { return mbar_wait(&bars->p_full[buf], used[buf]++ & 1, abort, p.err); };
       for (; ok && w.more(); w.next(p)) {
-        const bool single = w.single();
-        for (int h = 0; ok && h < 2; ++h) ok = mbar_wait(&bars->q_ready[h], segs & 1, abort, p.err);
-        ++segs;
-        ok = ok && wait_k(n);
-        if (!ok) break;
-        tc_fence_after();
-        issue_s(0, 0, n);
-        if (!single) issue_s(1, 1, n);
-        mma_commit(&bars->k_empty[n % C::kStages]);
-        for (int j = 0; ok && j < w.nt; ++j, ++n) {
-          const bool more = j + 1 < w.nt;
-          if (single) {
-            if (more) {
-              ok = wait_k(n + 1);
-              if (!ok) break;
-              tc_fence_after();
-              issue_s(0, (j + 1) & 1, n + 1);
-              mma_commit(&bars->k_empty[(n + 1) % C::kStages]);
-            }
-            ok = wait_v(n) && wait_p(j & 1);
-            if (!ok) break;
-            tc_fence_after();
-            issue_pv(0, j & 1, n, j == 0, !more);
-          } else {
-            ok = wait_v(n) && wait_p(0);
-            if (!ok) break;
-            tc_fence_after();
-            issue_pv(0, 0, n, j == 0, !more);
-            if (more) {
-              ok = wait_k(n + 1);
-              if (!ok) break;
-              tc_fence_after();
-              issue_s(0, 0, n + 1);
-            }
-            ok = wait_p(1);
-            if (!ok) break;
-            tc_fence_after();
-            issue_pv(1, 1, n, j == 0, !more);
-            if (more) {
-              issue_s(1, 1, n + 1);
-              mma_commit(&bars->k_empty[(n + 1) % C::kStages]);
-            }
+        const bool idle = h == 1 && w.single();      // no rows here: the barriers only
+        // S of step s: chunk s & 1 of tile n + s / 2; with a tile's second chunk its K stage is read
+        auto issue_s = [&](int s) {
+          const uint32_t st = (n + (s >> 1)) % C::kKStages;
+          if (idle) {
+            mbar_arrive(&bars->s_full[h][s & 1]);
+            if (s & 1) mbar_arrive(&bars->k_empty[st]);
+            return;
           }
-          mma_commit(&bars->v_empty[n % C::kStages]);
+          const uint32_t k0 = k_lo + ((st * C::kTileBytes + (s & 1) * C::kChunkRowsBytes) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk)
+            mma_ss_lo(col_s + (s & 1) * kChunk, q_lo + (((kk >> 2) * C::kQBoxBytes + (kk & 3) * 32) >> 4), q_hi,
+                      k0 + (((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4), k_hi, idesc_s, kk > 0 ? 1u : 0u);
+          mma_commit(&bars->s_full[h][s & 1]);
+          if (s & 1) mma_commit(&bars->k_empty[st]);
+        };
+        auto wait_k = [&](uint32_t i) {
+          const bool got = mbar_wait(&bars->k_full[i % C::kKStages], (i / C::kKStages) & 1, abort, p.err);
+          tc_fence_after();
+          return got;
+        };
+        const int ns = 2 * w.nt;
+        ok = mbar_wait(&bars->q_ready[h], segs++ & 1, abort, p.err) && wait_k(n);
+        if (!ok) break;
+        issue_s(0);
+        for (int s = 0; s < ns; ++s) {
+          if (s + 1 < ns) {
+            if (s & 1) ok = wait_k(n + ((s + 1) >> 1));
+            if (!ok) break;
+            issue_s(s + 1);
+          }
+          const int c = s & 1;
+          const uint32_t i = n + (s >> 1), st = i % C::kVStages;
+          ok = mbar_wait(&bars->p_full[h][c], i & 1, abort, p.err);
+          // (an idle row tile gives a V stage back once per load too, as its PV would)
+          if (idle && c == 1) ok = ok && mbar_wait(&bars->v_full[st], (i / C::kVStages) & 1, abort, p.err);
+          if (!ok) break;
+          if (idle) {
+            mbar_arrive(&bars->o_full[h]);
+            if (c == 1) mbar_arrive(&bars->v_empty[st]);
+            continue;
+          }
+          tc_fence_after();
+          const uint32_t v0 = v_lo + ((st * C::kTileBytes + c * C::kChunkRowsBytes) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kChunk / 16; ++kk)
+            mma_ts_lo(col_o, col_s + c * kChunk + kk * 8, v0 + ((16 * kk * 128) >> 4), v_hi, idesc_pv,
+                      (s > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&bars->o_full[h]);
+          if (c == 1) mma_commit(&bars->v_empty[st]);
+          if (s + 1 == ns) mma_commit(&bars->o_done[h]);
         }
-        if (single) mma_commit(&bars->single_done);
+        n += w.nt;
       }
       // every MMA completes before TMEM is freed
-      mma_commit(&bars->drain);
-      mbar_drain(&bars->drain, 0, p.err);
+      mma_commit(&bars->drain[h]);
+      mbar_drain(&bars->drain[h], 0, p.err);
     }
     __syncwarp();
   } else {
@@ -487,12 +479,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* sq = sQ + h * C::kQTileBytes;
     bool ok = true;
     uint32_t n = 0;                                    // tiles before this segment
-    // Phases: an S buffer is used once per tile in a pair, by every second tile in a single row tile.
-    uint32_t s_used[2] = {0, 0}, o_used = 0;
-    auto count_s = [&](const Walk& v) {
-      s_used[0] += v.single() ? (v.nt + 1) >> 1 : v.nt;
-      s_used[1] += v.single() ? v.nt >> 1 : v.nt;
-    };
     // Q of a segment's row tile -> shared memory, in the 128-byte swizzle
     auto stage_q = [&](const Walk& v) {
       const int r = h * kMaxRows + lr;
@@ -512,28 +498,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_proxy_async_smem();
     };
-    uint32_t segs = 0, singles = 0;                    // segments that this row tile takes part in, and the others
+    uint32_t segs = 0;                                 // segments with rows in this tile
     if (w.more()) {
       if (h == 0 || !w.single()) stage_q(w);
       mbar_arrive(&bars->q_ready[h]);
     }
     while (ok && w.more()) {
-      const bool single = w.single();
-      if (h == 1 && single) {
-        Walk nx = w;
-        nx.next(p);
-        // Nothing to do here but to keep in step: a parity wait tells phases apart only one at a time, so
-        // this warpgroup sees the segment's end before the issuer can begin the next (which waits for both
-        // row tiles' Q).
-        if (nx.more() && !nx.single()) stage_q(nx);
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars->single_done, singles++ & 1, abort, p.err));
-        if (!ok) break;
-        if (nx.more()) mbar_arrive(&bars->q_ready[h]);
-        n += w.nt;
-        count_s(w);
-        w = nx;
-        continue;
-      }
+      const bool idle = h == 1 && w.single();
       const int r = h * kMaxRows + lr;
       const bool rv = r < w.rows();
       const bool active = __any_sync(0xffffffffu, rv);
@@ -542,43 +513,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int p0 = w.s.L - w.s.nq;
       const uint32_t* words = p.tree_mask + static_cast<size_t>(w.s.q0 + qi) * VFY_TREE_WORDS;
       float m_ref = -INFINITY, l = 0.f;
-      for (int j = 0; j < w.nt; ++j) {
+      const int ns = 2 * w.nt;
+      bool plain = true, zero = false;                 // of the tile
+      for (int s = 0; s < ns; ++s) {
+        const int j = s >> 1, c = s & 1;
         const uint32_t i = n + j;
         const int gs = i % kGeo;
-        const int buf = single ? j & 1 : h;
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars->geo_full[gs], (i / kGeo) & 1, abort, p.err));
-        if (!ok) break;
-        const bool plain = bars->plain[gs] != 0;
-        uint32_t keep[4];
-        if (!plain) {
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int c = u >> 1;
-            keep[u] = bars->valid[gs][c] && rv ? keep32(words, bars->base[gs][c] + (u & 1) * 32, p0, w.s.L) : 0u;
-          }
+        if (c == 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->geo_full[gs], (i / kGeo) & 1, abort, p.err));
+          if (!ok) break;
+          plain = bars->plain[gs] != 0;
+          zero = bars->zero[gs] != 0;
         }
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[buf], (s_used[buf] + (single ? j >> 1 : j)) & 1, abort, p.err));
+        uint32_t keep[2] = {0u, 0u};
+        if (!plain && bars->valid[gs][c] != 0 && rv) {
+          keep[0] = keep32(words, bars->base[gs][c], p0, w.s.L);
+          keep[1] = keep32(words, bars->base[gs][c] + 32, p0, w.s.L);
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[h][c], i & 1, abort, p.err));
         if (!ok) break;
         tc_fence_after();
         if (active) {
-          const uint32_t ts = lane_base + kColS + buf * kKeys;
-          auto masked = [&](float x, int k) { return plain || ((keep[k >> 5] >> (k & 31)) & 1u) ? x : -INFINITY; };
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          const uint32_t ts = lane_base + kColS + h * 128 + c * kChunk;
+          float sv[kChunk];
+          {
+            uint32_t sr[kChunk];
+            tmem_ld64(ts, sr);
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            uint32_t sr[64];
-            tmem_ld64(ts + u * 64, sr);
-            if (plain) {
-#pragma unroll
-              for (int e = 0; e < 64; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(sr[e]));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 64; ++e) mx[e & 3] = fmaxf(mx[e & 3], masked(__uint_as_float(sr[e]), u * 64 + e));
-            }
+            for (int e = 0; e < kChunk; ++e) sv[e] = __uint_as_float(sr[e]);
           }
-          const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+          if (!plain) {
+#pragma unroll
+            for (int e = 0; e < kChunk; ++e) sv[e] = (keep[e >> 5] >> (e & 31)) & 1u ? sv[e] : -INFINITY;
+          }
+          float mx[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) mx[e] = sv[e];
+#pragma unroll
+          for (int e = 8; e < kChunk; ++e) mx[e & 7] = fmaxf(mx[e & 7], sv[e]);
+          const float m_tile = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                     fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * p.scale_log2;
           const bool raise = m_tile > m_ref + kRescaleLog2;
-          const bool scale_o = raise && j > 0 && m_ref != -INFINITY;
+          const bool scale_o = raise && m_ref != -INFINITY;
           float alpha = 1.f;
           if (raise) {
             alpha = ex2_approx(m_ref - m_tile);        // 0 where m_ref = -inf
@@ -586,62 +562,58 @@ __global__ void __launch_bounds__(kThreads, 1)
             m_ref = m_tile;
           }
           if (__any_sync(0xffffffffu, scale_o)) {
-            // O holds the tiles before j. In a pair S_h(j) was issued after PV_h(j-1), so that is done; in a
-            // single row tile it is waited for (PV(j) needs this tile's P, PV(j-2) was issued before S(j): the
-            // barrier is in that phase or the one after).
-            if (single) ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_full[h], (o_used + j - 1) & 1, abort, p.err));
+            // O holds the steps before s. PV(s-2) was issued before S(s) and PV(s) needs this step's P: the
+            // barrier of PV(s-1) is in that phase or the one after.
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_full[h], (2 * n + s - 1) & 1, abort, p.err));
             if (!ok) break;
             tc_fence_after();
             const float a = scale_o ? alpha : 1.f;
 #pragma unroll 1
-            for (int c = 0; c < HD / 32; ++c) {
+            for (int x = 0; x < HD / 32; ++x) {
               uint32_t o[32];
-              tmem_ld32(lane_base + kColO + h * 128 + c * 32, o);
+              tmem_ld32(lane_base + kColO + h * 128 + x * 32, o);
 #pragma unroll
               for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-              tmem_st32(lane_base + kColO + h * 128 + c * 32, o);
+              tmem_st32(lane_base + kColO + h * 128 + x * 32, o);
             }
           }
-          // p = 2^(s * scale * log2e - m_ref), packed over the columns of S that are read already
+          // p = 2^(s * scale * log2e - m_ref), packed over the first half of this S
           const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
-          float ps[4] = {0.f, 0.f, 0.f, 0.f};
+          const float2 scale2 = make_float2(p.scale_log2, p.scale_log2), neg2 = make_float2(neg, neg);
+          float2 ps[4];
+          uint32_t pk[kChunk / 2];
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            uint32_t sr[64], pk[32];
-            tmem_ld64(ts + u * 64, sr);
-            if (!plain) {
-#pragma unroll
-              for (int e = 0; e < 64; ++e) sr[e] = __float_as_uint(masked(__uint_as_float(sr[e]), u * 64 + e));
-            }
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float a = ex2_approx(fmaf(__uint_as_float(sr[2 * e]), p.scale_log2, neg));
-              const float c = ex2_approx(fmaf(__uint_as_float(sr[2 * e + 1]), p.scale_log2, neg));
-              ps[e & 3] += a + c;
-              const __nv_bfloat162 h2 = __floats2bfloat162_rn(a, c);
-              pk[e] = *reinterpret_cast<const uint32_t*>(&h2);
-            }
-            tmem_st32(ts + u * 32, pk);
+          for (int e = 0; e < kChunk / 2; ++e) {
+            float2 x = fma_f32x2(make_float2(sv[2 * e], sv[2 * e + 1]), scale2, neg2);
+            x = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            ps[e & 3] = e < 4 ? x : add_f32x2(ps[e & 3], x);
+            const __nv_bfloat162 h2 = __floats2bfloat162_rn(x.x, x.y);
+            pk[e] = *reinterpret_cast<const uint32_t*>(&h2);
           }
-          l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+          const float2 sum = add_f32x2(add_f32x2(ps[0], ps[1]), add_f32x2(ps[2], ps[3]));
+          l += sum.x + sum.y;
+          tmem_st32(ts, pk);
         }
         tc_fence_before();
-        if (h == 0 && bars->zero[gs]) {
-          // V rows of keys outside the sequence may hold anything, and 0 * NaN is NaN on the tensor core.
-          // Row tile 0 zeroes them before its P; PV of row tile 1 is issued after PV of row tile 0.
-          const int sv = i % C::kStages;
-          ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_full[sv], (i / C::kStages) & 1, abort, p.err));
+        // One warp's arrival waits for the tile's V, so the issuer's wait for P covers V too.
+        if (!idle && (zero || ((warp & 3) == kVRelayWarp && c == 0))) {
+          const int sv = i % C::kVStages;
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_full[sv], (i / C::kVStages) & 1, abort, p.err));
           if (!ok) break;
-          const int c = lr >> 6;
-          if (!bars->valid[gs][c] || bars->base[gs][c] + (lr & 63) >= w.s.L) {
-            uint8_t* row = sV + sv * C::kTileBytes + lr * 128;
+          if (zero) {
+            // V rows of keys outside the sequence may hold anything, and 0 * NaN is NaN on the tensor core. Both
+            // row tiles zero them (the same zeros), each before its own P.
+            const int key = lr >> 1;                   // two threads per key
+            if (bars->valid[gs][c] == 0 || bars->base[gs][c] + key >= w.s.L) {
+              uint8_t* row = sV + sv * C::kTileBytes + c * C::kChunkRowsBytes + key * 128;
 #pragma unroll
-            for (int x = 0; x < C::kBoxes * 8; ++x)
-              *reinterpret_cast<uint4*>(row + (x >> 3) * C::kBoxBytes + (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+              for (int x = (lr & 1) * C::kBoxes * 4; x < ((lr & 1) + 1) * C::kBoxes * 4; ++x)
+                *reinterpret_cast<uint4*>(row + (x >> 3) * C::kBoxBytes + (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
           }
-          fence_proxy_async_smem();
         }
-        mbar_arrive(&bars->p_full[buf]);
+        mbar_arrive(&bars->p_full[h][c]);
       }
       if (!ok) break;
       // the next segment's first S may run during this one's epilogue: every S here has read Q
@@ -651,7 +623,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (h == 0 || !nx.single()) stage_q(nx);
         mbar_arrive(&bars->q_ready[h]);
       }
-      o_used += w.nt;
+      if (idle) {
+        n += w.nt;
+        w = nx;
+        continue;
+      }
       ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[h], segs++ & 1, abort, p.err));
       if (!ok) break;
       tc_fence_after();
@@ -699,7 +675,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       n += w.nt;
-      count_s(w);
       w = nx;
     }
   }
