@@ -4,7 +4,9 @@ stream becomes the stream handle. Every step of the verify path runs in the libr
 There is no fallback: if the library is not built, or its device is absent, calls raise."""
 from __future__ import annotations
 
+import array
 import ctypes
+import operator
 import os
 
 import torch
@@ -136,6 +138,25 @@ def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+# The tree calls run once or more per layer or step, and a call's checks in Python cost more than its
+# launch: these helpers take 0.3 us a tensor and 0.1 us for the stream (torch.cuda.current_stream()
+# builds a Stream object: 3 us).
+
+def _raw_stream(ctx, stream) -> int:
+    """The handle of `stream`, or of the current stream of the context's device."""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(ctx.device)
+
+
+def _ptr(ctx, t, dtypes, name: str):
+    """Address of a contiguous tensor on the context's device (None for None)."""
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.get_device() == ctx.device and t.dtype in dtypes and t.is_contiguous():
+        return t.data_ptr()
+    _dev(t, dtypes, name)              # says what is wrong with any other tensor
+    raise ValueError(f"{name} is on {t.device}, the context on cuda:{ctx.device}")
 
 
 # ---------------------------------------------------------------------------------------------
@@ -300,6 +321,7 @@ def vfy_accept_static(logits, vocab: int, drafts, cu_rows, num_seqs: int, max_ro
 # ---------------------------------------------------------------------------------------------
 
 U32 = (torch.int32, torch.uint32)       # row and grammar masks: 32-bit words
+_DTYPE = operator.attrgetter("dtype")
 
 
 class LogitRules:
@@ -327,65 +349,75 @@ class LogitRules:
 
 def vfy_tree_plan(ctx: Context, parents, cu_q, depth, tree_mask, num_seqs: int, stream=None):
     _check(lib().vfy_tree_plan(
-        ctx.handle, _dev(parents, I32, "parents"), _dev(cu_q, I32, "cu_q"), _dev(depth, I32, "depth"),
-        _dev(tree_mask, U32, "tree_mask"), num_seqs, _stream(stream)), "vfy_tree_plan")
+        ctx.handle, _ptr(ctx, parents, I32, "parents"), _ptr(ctx, cu_q, I32, "cu_q"), _ptr(ctx, depth, I32, "depth"),
+        _ptr(ctx, tree_mask, U32, "tree_mask"), num_seqs, _raw_stream(ctx, stream)), "vfy_tree_plan")
 
 
 def vfy_attend_full_tree(ctx: Context, q, cu_q, tree_mask, k_pool, v_pool, num_slots: int, resident_ids,
                          resident_slots, cu_resident, max_resident_per_seq: int, seq_len, out, lse, num_seqs: int,
                          stream=None):
     _check(lib().vfy_attend_full_tree(
-        ctx.handle, _dev(q, BF16, "q"), _dev(cu_q, I32, "cu_q"), _dev(tree_mask, U32, "tree_mask"),
-        _dev(k_pool, BF16, "k_pool"), _dev(v_pool, BF16, "v_pool"), num_slots, _dev(resident_ids, I32, "resident_ids"),
-        _dev(resident_slots, I32, "resident_slots"), _dev(cu_resident, I32, "cu_resident"), max_resident_per_seq,
-        _dev(seq_len, I32, "seq_len"), _dev(out, BF16, "out"), _dev(lse, F32, "lse"), num_seqs, _stream(stream)),
+        ctx.handle, _ptr(ctx, q, BF16, "q"), _ptr(ctx, cu_q, I32, "cu_q"), _ptr(ctx, tree_mask, U32, "tree_mask"),
+        _ptr(ctx, k_pool, BF16, "k_pool"), _ptr(ctx, v_pool, BF16, "v_pool"), num_slots, _ptr(ctx, resident_ids, I32, "resident_ids"),
+        _ptr(ctx, resident_slots, I32, "resident_slots"), _ptr(ctx, cu_resident, I32, "cu_resident"), max_resident_per_seq,
+        _ptr(ctx, seq_len, I32, "seq_len"), _ptr(ctx, out, BF16, "out"), _ptr(ctx, lse, F32, "lse"), num_seqs, _raw_stream(ctx, stream)),
         "vfy_attend_full_tree")
 
 
 def vfy_attend_swa_tree(ctx: Context, q, cu_q, tree_mask, depth, k_ring, v_ring, ring_offset, seq_len, out, lse,
                         num_seqs: int, stream=None):
     _check(lib().vfy_attend_swa_tree(
-        ctx.handle, _dev(q, BF16, "q"), _dev(cu_q, I32, "cu_q"), _dev(tree_mask, U32, "tree_mask"),
-        _dev(depth, I32, "depth"), _dev(k_ring, BF16, "k_ring"), _dev(v_ring, BF16, "v_ring"),
-        _dev(ring_offset, I32, "ring_offset"), _dev(seq_len, I32, "seq_len"), _dev(out, BF16, "out"),
-        _dev(lse, F32, "lse"), num_seqs, _stream(stream)), "vfy_attend_swa_tree")
+        ctx.handle, _ptr(ctx, q, BF16, "q"), _ptr(ctx, cu_q, I32, "cu_q"), _ptr(ctx, tree_mask, U32, "tree_mask"),
+        _ptr(ctx, depth, I32, "depth"), _ptr(ctx, k_ring, BF16, "k_ring"), _ptr(ctx, v_ring, BF16, "v_ring"),
+        _ptr(ctx, ring_offset, I32, "ring_offset"), _ptr(ctx, seq_len, I32, "seq_len"), _ptr(ctx, out, BF16, "out"),
+        _ptr(ctx, lse, F32, "lse"), num_seqs, _raw_stream(ctx, stream)), "vfy_attend_swa_tree")
 
 
 def vfy_process_logits(ctx: Context, logits, vocab: int, cu_rows, max_rows: int, rules: LogitRules, out,
                        num_seqs: int, stream=None):
     """`logits`: fp32 or bf16 [rows][vocab]; its rows may be further apart than `vocab` entries (a view
     of a wider matrix). `out`: fp32 [rows][vocab], or the logits themselves."""
-    if not logits.is_cuda or logits.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"logits must be a float32 or bfloat16 CUDA tensor, got {logits.dtype} on {logits.device}")
+    if logits.get_device() != ctx.device or logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"logits must be a float32 or bfloat16 tensor on the context's device, got {logits.dtype} on "
+                        f"{logits.device}")
     if logits.dim() != 2 or logits.stride(1) != 1 or logits.shape[1] < vocab:
         raise ValueError("logits must be [rows][vocab] with contiguous rows")
     if rules.vocab not in (None, vocab) or rules.mask_words not in (None, (vocab + 31) // 32):
         raise ValueError("the rules' counts or grammar masks are for another vocabulary")
     _check(lib().vfy_process_logits(
-        ctx.handle, _P(logits.data_ptr()), 1 if logits.dtype == torch.bfloat16 else 0,
-        logits.stride(0) if logits.shape[0] > 1 else logits.shape[1], vocab, _dev(cu_rows, I32, "cu_rows"), max_rows,
-        ctypes.byref(rules.struct), _dev(out, F32, "out"), num_seqs, _stream(stream)), "vfy_process_logits")
+        ctx.handle, logits.data_ptr(), 1 if logits.dtype == torch.bfloat16 else 0,
+        logits.stride(0) if logits.shape[0] > 1 else logits.shape[1], vocab, _ptr(ctx, cu_rows, I32, "cu_rows"), max_rows,
+        ctypes.byref(rules.struct), _ptr(ctx, out, F32, "out"), num_seqs, _raw_stream(ctx, stream)), "vfy_process_logits")
 
 
 def vfy_count_tokens(ctx: Context, tokens, cu_tokens, max_tokens: int, counts, vocab: int, num_seqs: int, *,
                      as_prompt: bool = False, reset: bool = False, stream=None):
     _check(lib().vfy_count_tokens(
-        ctx.handle, _dev(tokens, I32, "tokens"), _dev(cu_tokens, I32, "cu_tokens"), max_tokens, 1 if as_prompt else 0,
-        1 if reset else 0, _dev(counts, I32, "counts"), vocab, num_seqs, _stream(stream)), "vfy_count_tokens")
+        ctx.handle, _ptr(ctx, tokens, I32, "tokens"), _ptr(ctx, cu_tokens, I32, "cu_tokens"), max_tokens, 1 if as_prompt else 0,
+        1 if reset else 0, _ptr(ctx, counts, I32, "counts"), vocab, num_seqs, _raw_stream(ctx, stream)), "vfy_count_tokens")
 
 
 def vfy_accept_tree(ctx: Context, logits, vocab: int, drafts, parents, cu_rows, max_rows: int, accepted_len, path,
                     bonus, committed, num_seqs: int, stream=None):
     _check(lib().vfy_accept_tree(
-        ctx.handle, _dev(logits, F32, "logits"), vocab, _dev(drafts, I32, "drafts"), _dev(parents, I32, "parents"),
-        _dev(cu_rows, I32, "cu_rows"), max_rows, _dev(accepted_len, I32, "accepted_len"), _dev(path, I32, "path"),
-        _dev(bonus, I32, "bonus"), _dev(committed, I32, "committed"), num_seqs, _stream(stream)), "vfy_accept_tree")
+        ctx.handle, _ptr(ctx, logits, F32, "logits"), vocab, _ptr(ctx, drafts, I32, "drafts"), _ptr(ctx, parents, I32, "parents"),
+        _ptr(ctx, cu_rows, I32, "cu_rows"), max_rows, _ptr(ctx, accepted_len, I32, "accepted_len"), _ptr(ctx, path, I32, "path"),
+        _ptr(ctx, bonus, I32, "bonus"), _ptr(ctx, committed, I32, "committed"), num_seqs, _raw_stream(ctx, stream)), "vfy_accept_tree")
 
 
-def _layers(tensors, name: str, host_allowed: bool = False):
-    """A host array of the layers' pointers."""
-    return (_P * len(tensors))(*[
-        _host(t, BF16, name) if host_allowed and not t.is_cuda else _dev(t, BF16, name) for t in tensors])
+def _layers(ctx, tensors, name: str, host_allowed: bool = False):
+    """A host array of the layers' addresses (keep it while the call runs)."""
+    tensors = list(tensors)
+    # (in C where possible: a call names up to 256 tensors)
+    if (set(map(torch.Tensor.get_device, tensors)) <= {ctx.device} and all(map(torch.Tensor.is_contiguous, tensors))
+            and set(map(_DTYPE, tensors)) <= set(BF16)):
+        return array.array("Q", map(torch.Tensor.data_ptr, tensors))
+    return array.array("Q", [(_host(t, BF16, name) if host_allowed and not t.is_cuda
+                              else _c(_ptr(ctx, t, BF16, name))).value or 0 for t in tensors])
+
+
+def _c(address):
+    return ctypes.c_void_p(address)
 
 
 def vfy_compact_full(ctx: Context, path, accepted_len, cu_q, seq_len, cu_chunks, slot_of_chunk, host_k, host_v,
@@ -393,11 +425,13 @@ def vfy_compact_full(ctx: Context, path, accepted_len, cu_q, seq_len, cu_chunks,
     """host_k, host_v, k_pool, v_pool: one tensor per layer, in lists of one length."""
     if not len(host_k) == len(host_v) == len(k_pool) == len(v_pool):
         raise ValueError("host_k, host_v, k_pool and v_pool must have one tensor per layer")
+    hk, hv = _layers(ctx, host_k, "host_k", True), _layers(ctx, host_v, "host_v", True)
+    kp, vp = _layers(ctx, k_pool, "k_pool"), _layers(ctx, v_pool, "v_pool")
     _check(lib().vfy_compact_full(
-        ctx.handle, _dev(path, I32, "path"), _dev(accepted_len, I32, "accepted_len"), _dev(cu_q, I32, "cu_q"),
-        _dev(seq_len, I32, "seq_len"), _dev(cu_chunks, I32, "cu_chunks"), _dev(slot_of_chunk, I32, "slot_of_chunk"),
-        len(k_pool), _layers(host_k, "host_k", True), _layers(host_v, "host_v", True), num_host_chunks,
-        _layers(k_pool, "k_pool"), _layers(v_pool, "v_pool"), num_slots, num_seqs, _stream(stream)),
+        ctx.handle, _ptr(ctx, path, I32, "path"), _ptr(ctx, accepted_len, I32, "accepted_len"), _ptr(ctx, cu_q, I32, "cu_q"),
+        _ptr(ctx, seq_len, I32, "seq_len"), _ptr(ctx, cu_chunks, I32, "cu_chunks"), _ptr(ctx, slot_of_chunk, I32, "slot_of_chunk"),
+        len(k_pool), hk.buffer_info()[0], hv.buffer_info()[0], num_host_chunks, kp.buffer_info()[0],
+        vp.buffer_info()[0], num_slots, num_seqs, _raw_stream(ctx, stream)),
         "vfy_compact_full")
 
 
@@ -406,7 +440,8 @@ def vfy_compact_swa(ctx: Context, path, accepted_len, cu_q, seq_len, ring_offset
     """k_ring, v_ring: one tensor per layer, in lists of one length."""
     if len(k_ring) != len(v_ring):
         raise ValueError("k_ring and v_ring must have one tensor per layer")
+    kr, vr = _layers(ctx, k_ring, "k_ring"), _layers(ctx, v_ring, "v_ring")
     _check(lib().vfy_compact_swa(
-        ctx.handle, _dev(path, I32, "path"), _dev(accepted_len, I32, "accepted_len"), _dev(cu_q, I32, "cu_q"),
-        _dev(seq_len, I32, "seq_len"), _dev(ring_offset, I32, "ring_offset"), len(k_ring),
-        _layers(k_ring, "k_ring"), _layers(v_ring, "v_ring"), num_seqs, _stream(stream)), "vfy_compact_swa")
+        ctx.handle, _ptr(ctx, path, I32, "path"), _ptr(ctx, accepted_len, I32, "accepted_len"), _ptr(ctx, cu_q, I32, "cu_q"),
+        _ptr(ctx, seq_len, I32, "seq_len"), _ptr(ctx, ring_offset, I32, "ring_offset"), len(k_ring),
+        kr.buffer_info()[0], vr.buffer_info()[0], num_seqs, _raw_stream(ctx, stream)), "vfy_compact_swa")
