@@ -404,8 +404,10 @@ vfy_status vfy_append_swa(vfy_ctx* ctx, const uint16_t* k_new, const uint16_t* v
 // Nodes of one sequence's tree that a context takes.
 static int tree_capacity(const vfy_config& c) { return std::min(c.max_queries_per_seq, VFY_MAX_TREE_NODES); }
 
-static bool tree_pairs(const vfy_ctx* ctx, int row_tiles, int num_seqs) {
-  return ctx->full_splits == 0 && (row_tiles > 1 || num_seqs > 1);
+// Does a tree's full layer go to CTA pairs of 256 rows (and how many), or to the linear block's kernel (0)?
+static int tree_pairs(const vfy_ctx* ctx, int row_tiles, int num_seqs) {
+  if (ctx->full_splits != 0 || ctx->cfg.head_dim != 128 || (row_tiles == 1 && num_seqs == 1)) return 0;
+  return std::min(vfy::attend_tree_pairs(), ctx->num_sms / 2);
 }
 
 static vfy_status attend_common(vfy_ctx* ctx, bool ring, const uint16_t* q, const int32_t* cu_q,
@@ -492,10 +494,11 @@ static vfy_status attend_common(vfy_ctx* ctx, bool ring, const uint16_t* q, cons
   p.num_seqs = num_seqs;
   p.token_cap = num_seqs * max_q;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (tree && !ring && tree_pairs(ctx, row_tiles, num_seqs)) {
+  const int pairs = tree && !ring ? tree_pairs(ctx, row_tiles, num_seqs) : 0;
+  if (pairs > 0) {
     p.out = out;
     p.lse = lse;
-    VFY_CUDA(vfy::launch_attend_tree(c.head_dim, p, tk, tv, ctx->num_sms, s));
+    VFY_CUDA(vfy::launch_attend_tree(p, tk, tv, pairs, s));
     ctx->launches += 2;
     return VFY_OK;
   }

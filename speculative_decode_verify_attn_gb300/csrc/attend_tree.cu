@@ -1,26 +1,25 @@
-// Tree attention of full layers for large blocks: split-KV flash-decode with 256 block rows per CTA.
+// Tree attention of full layers for large blocks (d = 128): split-KV flash-decode with 256 block rows per
+// CTA pair.
 //
-// A tree of more than 128 / G nodes has more rows per KV head than one M = 128 MMA holds. Here one CTA
-// takes two row tiles of 128 (a pair), so that every K/V byte that reaches shared memory serves 256 rows:
-// with d = 128 a 128-key tile is 64 KB for 4 * 128 * 128 * 128 multiply-adds, 1.4 us of one SM's HBM share
-// and 1.1 us of its tensor core -- the two bounds meet.
+// A tree of more than 128 / G nodes has more rows per KV head than one M = 128 MMA holds. Here two CTAs of a
+// cluster take two row tiles of 128, one each, as the halves of M = 256 MMAs (cta_group::2): every K/V byte is
+// fetched by one of the two SMs (K: a chunk each; V: half of the columns each) and serves 256 rows.
 //
-// The work is one list of tiles: item (sequence b, KV head h, pair t) has T_b tiles of two resident chunks
-// each, and the persistent CTAs cut the list of all items' tiles into equal runs. So a ragged batch is as
-// balanced as one sequence, whatever the lengths. A CTA's run is a sequence of segments, each inside one
-// item; a segment that covers its item writes O and the LSE itself, others write fp32 partials (m, l,
-// unnormalised O) that the combine kernel merges:
+// The work is one list of tiles: item (sequence b, KV head h, pair of row tiles t) has T_b tiles of two
+// resident chunks each, and the persistent CTA pairs cut the list of all items' tiles into equal runs. So a
+// ragged batch is as balanced as one sequence, whatever the lengths. A run is a sequence of segments, each
+// inside one item; a segment that covers its item writes O and the LSE itself, others write fp32 partials
+// (m, l, unnormalised O) that the combine kernel merges:
 //     O = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s,  LSE = ln2 * (M + log2 sum_s 2^(m_s - M) l_s)
-// A run has at most two partial segments, its first and its last: 2 slots per CTA.
+// A run has at most two partial segments, its first and its last: 2 slots per pair.
 //
-// Warps: 0-3 softmax and epilogue of row tile 0, 4-7 of row tile 1 (TMEM lane = row, one thread per row),
-// 8 K producer and tile geometry, 9 V producer, 10 and 11 MMA issuers, one per row tile. A tile's two chunks
-// are two steps. Tensor memory per row tile: two S buffers of 64 columns (P, bf16, over the first half of its
-// S) and O. S of step s+1 is issued before PV of step s, so the tensor core works on one step while the
-// softmax works on the other, and the two row tiles run free of each other. An MMA costs its issuer 50 to 110
-// cycles beside busy softmax warps, more than its 32 or 64 cycles in the tensor pipe: hence two issuers. In a
-// segment of at most 128 rows the second row tile's warps only keep the barrier protocol, so that every role
-// sees every phase of every barrier it waits on.
+// Warps of each CTA: 0-3 and 4-7 two softmax warpgroups (TMEM lane = row of the CTA's row tile, one thread
+// per row and warpgroup), 8 K producer and tile geometry, 9 V producer; in the leading CTA 10 issues the S
+// MMAs and 11 the PV MMAs. Warpgroup g takes chunk g of every tile, with a running maximum, a row sum and an
+// O of its own (O_g += P_g V_g); the halves merge once, at the segment's end. S of a tile (128 columns, P as
+// bf16 over the first half of each chunk's) has two buffers, so S of the next tile runs during the softmax of
+// this one. An MMA costs its issuer 50 to 110 cycles beside busy softmax warps, more than the pair's 64 in the
+// tensor pipes: hence two issuers (one for everything: 2360 cycles a tile, in the linear block's kernel).
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -31,56 +30,55 @@
 namespace vfy {
 namespace {
 
+constexpr int HD = 128;
 constexpr int kThreads = 384;
 constexpr int kKWarp = 8;
 constexpr int kVWarp = 9;
 constexpr int kMmaWarp = 10;              // and 11
-constexpr int kVRelayWarp = 3;            // softmax warp of a row tile whose P arrival waits for V
+constexpr int kVRelayWarp = 3;            // softmax warp of a warpgroup whose P arrival waits for V
 constexpr int kPairRows = 2 * kMaxRows;
 constexpr int kKeys = 2 * kChunk;         // keys per tile
-constexpr int kGeo = 8;                   // tile-geometry ring
+constexpr int kGeo = 16;                  // tile-geometry ring
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0;             // [row tile][chunk]: S buffers of kChunk columns
-constexpr uint32_t kColO = 256;           // [row tile]: O accumulators of d columns, 128 apart
-constexpr int kPrefetch = 3;              // tiles prefetched into L2 beyond the shared-memory stages
+constexpr uint32_t kColS = 0;             // [tile parity]: S of kKeys columns
+constexpr uint32_t kColO = 256;           // [chunk]: O of 128 columns
 // A row keeps a stale reference maximum until a tile's maximum exceeds it by this much (log2 units).
 constexpr float kRescaleLog2 = 8.0f;
 
-template <int HD>
-struct Cfg {
-  static constexpr int kBoxes = HD / 64;                // 128-byte (64-column) boxes per row
-  static constexpr int kBoxBytes = kKeys * 128;
-  static constexpr int kChunkRowsBytes = kChunk * 128;  // one chunk's rows within a box
-  static constexpr int kChunkBytes = kChunk * HD * 2;
-  static constexpr int kTileBytes = kKeys * HD * 2;
-  static constexpr int kQBoxBytes = kMaxRows * 128;
-  static constexpr int kQTileBytes = kMaxRows * HD * 2;
-  // A K stage frees as soon as both row tiles' S have read it, a V stage only after their last PV.
-  static constexpr int kKStages = HD == 128 ? 2 : 4;
-  static constexpr int kVStages = HD == 128 ? 3 : 4;
-  static constexpr int kBarOffset = 2 * kQTileBytes + (kKStages + kVStages) * kTileBytes;
-  static constexpr int kSmemBytes = kBarOffset + 2048 + 1024;
-  static_assert(kSmemBytes <= 227 * 1024, "shared memory");
-  static_assert(kKStages + 3 <= kGeo && kKStages <= 4 && kVStages <= 4, "rings");
-};
+// Shared memory of one CTA: its row tile of Q; K stages of its chunk (64 keys x 128); V stages of its 64
+// columns (128 keys x 64). Each is made of 128-byte rows in the 128-byte swizzle.
+constexpr int kBoxBytes = kChunk * 128;               // 64 rows of 128 bytes
+constexpr int kQBoxBytes = kMaxRows * 128;
+constexpr int kQBytes = 2 * kQBoxBytes;
+constexpr int kStageBytes = 2 * kBoxBytes;            // of K (two column boxes) and of V (two chunks)
+constexpr int kKStages = 6, kVStages = 4;
+constexpr int kBarOffset = kQBytes + (kKStages + kVStages) * kStageBytes;
+constexpr int kBarBytes = 3072;
+constexpr int kSmemBytes = kBarOffset + kBarBytes + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+static_assert(kKStages + 4 <= kGeo, "geometry ring");
 
 struct Bars {
-  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t k_full[kKStages];   // in the leading CTA: both CTAs' chunks
+  uint64_t k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
   uint64_t geo_full[kGeo];
-  uint64_t s_full[2][2];   // [row tile][chunk], one phase per tile
-  uint64_t p_full[2][2];   // [row tile][chunk]: P is written (and V has landed, its outside rows zeroed)
-  uint64_t o_full[2];      // [row tile]: one phase per step, after its PV
-  uint64_t o_done[2];      // [row tile]: one phase per segment with rows in it, after its last PV
-  uint64_t q_ready[2];     // [row tile]: one phase per segment
+  uint64_t s_full[2], s_free[2];   // [tile parity]: S is there; its P has been read (leading CTA)
+  uint64_t p_full[2];          // in the leading CTA, [tile parity]: P is written in both CTAs (and V has landed)
+  uint64_t o_full;             // one phase per tile, after its PV
+  uint64_t o_done;             // one phase per segment, after its last PV
+  uint64_t q_ready;            // in the leading CTA, one phase per segment: Q is staged in both CTAs
+  uint64_t half_ready[4];      // [lane quarter], one phase per segment: both warpgroups' (m, l)
+  uint64_t o_read;             // one phase per segment: both warpgroups have read both O
   uint64_t drain[2], never;
   uint32_t tmem_base;
   int abort;
-  int base[kGeo][2];       // position of each chunk's first key
+  int base[kGeo][2];           // position of each chunk's first key
   int valid[kGeo][2];
-  int plain[kGeo];         // every key lies before the block: all rows attend all of them
-  int zero[kGeo];          // some key lies outside the sequence: its V row is to be zeroed
+  int plain[kGeo];             // every key lies before the block: all rows attend all of them
+  int zero[kGeo];              // some key lies outside the sequence: its V row is to be zeroed
+  float xm[2][128], xl[2][128];
 };
-static_assert(sizeof(Bars) <= 2048, "barrier block");
+static_assert(sizeof(Bars) <= kBarBytes, "barrier block");
 
 // One sequence's share of the list.
 struct Seq {
@@ -201,7 +199,6 @@ struct Walk {
     set();
   }
   __device__ __forceinline__ int rows() const { return min(kPairRows, s.rows - t * kPairRows); }
-  __device__ __forceinline__ bool single() const { return rows() <= kMaxRows; }
   __device__ __forceinline__ bool whole() const { return k == 0 && nt == s.tiles; }
 };
 
@@ -238,52 +235,63 @@ __device__ __forceinline__ uint32_t keep32(const uint32_t* words, int pos, int p
   return keep;
 }
 
-template <int HD>
-__global__ void __launch_bounds__(kThreads, 1)
+// A copy lands within microseconds; after an abort the producers keep their CTA for a thousand times that.
+__device__ __forceinline__ void let_copies_land() {
+  const unsigned long long t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     attend_tree_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tmap_k,
                        const __grid_constant__ CUtensorMap tmap_v) {
-  using C = Cfg<HD>;
   extern __shared__ uint8_t smem_raw[];
+  // (the pair's descriptors need the same offsets in both CTAs: the dynamic block starts at one address in all)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
-  uint8_t* sK = smem + 2 * C::kQTileBytes;
-  uint8_t* sV = sK + C::kKStages * C::kTileBytes;
-  Bars* bars = reinterpret_cast<Bars*>(smem + C::kBarOffset);
+  uint8_t* sK = smem + kQBytes;
+  uint8_t* sV = sK + kKStages * kStageBytes;
+  Bars* bars = reinterpret_cast<Bars*>(smem + kBarOffset);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int pair = static_cast<int>(blockIdx.x) >> 1, pairs = static_cast<int>(gridDim.x) >> 1;
+  auto leader = [&](const uint64_t* bar) { return dsmem_addr(smem_u32(bar), 0); };
 
   if (threadIdx.x == kKWarp * 32) {
-    for (int i = 0; i < C::kKStages; ++i) {
+    for (int i = 0; i < kKStages; ++i) {
       mbar_init(&bars->k_full[i], 1);
-      mbar_init(&bars->k_empty[i], 2);       // both issuers
+      mbar_init(&bars->k_empty[i], 1);
     }
-    for (int i = 0; i < C::kVStages; ++i) {
+    for (int i = 0; i < kVStages; ++i) {
       mbar_init(&bars->v_full[i], 1);
-      mbar_init(&bars->v_empty[i], 2);
+      mbar_init(&bars->v_empty[i], 1);
     }
     for (int i = 0; i < kGeo; ++i) mbar_init(&bars->geo_full[i], 1);
     for (int i = 0; i < 2; ++i) {
-      for (int k = 0; k < 2; ++k) {
-        mbar_init(&bars->s_full[i][k], 1);
-        mbar_init(&bars->p_full[i][k], 128);
-      }
+      mbar_init(&bars->s_full[i], 1);
+      mbar_init(&bars->s_free[i], 1);
+      mbar_init(&bars->p_full[i], 16);                                   // all softmax warps, both CTAs
       mbar_init(&bars->drain[i], 1);
-      mbar_init(&bars->o_full[i], 1);
-      mbar_init(&bars->o_done[i], 1);
-      mbar_init(&bars->q_ready[i], 128);
     }
+    mbar_init(&bars->o_full, 1);
+    mbar_init(&bars->o_done, 1);
+    mbar_init(&bars->q_ready, 16);                                       // all softmax warps, both CTAs
+    for (int i = 0; i < 4; ++i) mbar_init(&bars->half_ready[i], 64);
+    mbar_init(&bars->o_read, 256);
     mbar_init(&bars->never, 1);
     bars->abort = 0;
     fence_mbar_init();
     prefetch_tmap(&tmap_k);
     prefetch_tmap(&tmap_v);
   }
+  __syncwarp();
   if (warp == kMmaWarp) {
-    tmem_alloc(&bars->tmem_base, kTmemCols);
-    tmem_relinquish();
+    tmem_alloc_pair(&bars->tmem_base, kTmemCols);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();                          // both CTAs' barriers are ready
   tc_fence_after();
   const uint32_t tbase = bars->tmem_base;
   volatile int* abort = &bars->abort;
@@ -291,23 +299,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
   if (!p.stable_metadata) pdl_wait();
   Walk w;
-  w.begin(p, lane, blockIdx.x, gridDim.x);
+  w.begin(p, lane, pair, pairs);
   if (p.stable_metadata) pdl_wait();
   if (blockIdx.x == 0) {
     for (int b = threadIdx.x; b < p.num_seqs; b += kThreads)
       if (seq_is_bad(p, b)) atomicOr(p.err, kErrDeviceInput);
   }
+  bool ok = true;
 
   if (warp == kKWarp) {
     // ------------------------------ K producer and tile geometry --------------------------------
     if (lane == 0) {
       const uint64_t pol = l2_policy_evict_first();
       uint32_t n = 0;                        // tiles so far
-      bool ok = true, reported = false;
+      bool reported = rank != 0;
       for (; ok && w.more(); w.next(p)) {
         for (int j = 0; j < w.nt; ++j, ++n) {
-          const int st = n % C::kKStages;
-          if (n >= C::kKStages) ok = mbar_wait(&bars->k_empty[st], (n / C::kKStages - 1) & 1, abort, p.err);
+          const int st = n % kKStages;
+          if (n >= kKStages) ok = mbar_wait(&bars->k_empty[st], (n / kKStages - 1) & 1, abort, p.err);
           if (!ok) break;
           const int g = n % kGeo;
           const int p0 = w.s.L - w.s.nq;
@@ -331,45 +340,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           bars->zero[g] = zero ? 1 : 0;
           mbar_arrive(&bars->geo_full[g]);
           // a chunk the sequence lacks is not loaded: the mask and the zeroed V rows cover its stale rows
-          mbar_arrive_expect_tx(&bars->k_full[st], present * C::kChunkBytes);
+          if (rank == 0) mbar_arrive_expect_tx(&bars->k_full[st], present * kStageBytes);
+          const Chunk mine = rank == 0 ? c[0] : c[1];
+          if (mine.present) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (!c[i].present) continue;
-#pragma unroll
-            for (int bx = 0; bx < C::kBoxes; ++bx)
-              tma_load_2d(sK + st * C::kTileBytes + bx * C::kBoxBytes + i * C::kChunkRowsBytes, &tmap_k,
-                          &bars->k_full[st], bx * 64, c[i].y, pol);
-          }
-          // more of the stream in flight from HBM than the stages hold
-          const int f = j + kPrefetch + C::kKStages - 1;
-          if (f < w.nt) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const Chunk a = chunk_at(p, w, f, i);
-              if (!a.present) continue;
-#pragma unroll
-              for (int bx = 0; bx < C::kBoxes; ++bx) {
-                tma_prefetch_2d(&tmap_k, bx * 64, a.y);
-                tma_prefetch_2d(&tmap_v, bx * 64, a.y);
-              }
-            }
+            for (int bx = 0; bx < 2; ++bx)
+              tma_load_2d_pair(sK + st * kStageBytes + bx * kBoxBytes, &tmap_k, leader(&bars->k_full[st]), bx * 64,
+                               mine.y, pol);
           }
         }
       }
-      // every copy lands before the CTA can exit, also when the pipeline was aborted
-      for (uint32_t i = n > C::kKStages ? n - C::kKStages : 0; i < n; ++i)
-        mbar_drain(&bars->k_full[i % C::kKStages], (i / C::kKStages) & 1, p.err);
+      // Every copy has been read when the run ends as it should. After a wait that ran out, copies of either CTA
+      // may be in flight, and the leading CTA's barriers count both CTAs': they get time to land.
+      if (!ok) let_copies_land();
     }
   } else if (warp == kVWarp) {
     // ------------------------------ V producer --------------------------------------------------
     if (lane == 0) {
       const uint64_t pol = l2_policy_evict_first();
       uint32_t n = 0;
-      bool ok = true;
       for (; ok && w.more(); w.next(p)) {
         for (int j = 0; j < w.nt; ++j, ++n) {
-          const int st = n % C::kVStages;
-          if (n >= C::kVStages) ok = mbar_wait(&bars->v_empty[st], (n / C::kVStages - 1) & 1, abort, p.err);
+          const int st = n % kVStages;
+          if (n >= kVStages) ok = mbar_wait(&bars->v_empty[st], (n / kVStages - 1) & 1, abort, p.err);
           if (!ok) break;
           Chunk c[2];
           int present = 0;
@@ -378,134 +371,100 @@ __global__ void __launch_bounds__(kThreads, 1)
             c[i] = chunk_at(p, w, j, i);
             present += c[i].present ? 1 : 0;
           }
-          mbar_arrive_expect_tx(&bars->v_full[st], present * C::kChunkBytes);
+          mbar_arrive_expect_tx(&bars->v_full[st], present * kBoxBytes);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (!c[i].present) continue;
-#pragma unroll
-            for (int bx = 0; bx < C::kBoxes; ++bx)
-              tma_load_2d(sV + st * C::kTileBytes + bx * C::kBoxBytes + i * C::kChunkRowsBytes, &tmap_v,
-                          &bars->v_full[st], bx * 64, c[i].y, pol);
-          }
+          for (int i = 0; i < 2; ++i)
+            if (c[i].present)
+              tma_load_2d(sV + st * kStageBytes + i * kBoxBytes, &tmap_v, &bars->v_full[st], rank * 64, c[i].y, pol);
         }
       }
-      for (uint32_t i = n > C::kVStages ? n - C::kVStages : 0; i < n; ++i)
-        mbar_drain(&bars->v_full[i % C::kVStages], (i / C::kVStages) & 1, p.err);
+      if (!ok) let_copies_land();
     }
   } else if (warp >= kMmaWarp) {
-    // ------------------------------ MMA issuers (one lane each) ---------------------------------
-    if (lane == 0) {
-      const int h = warp - kMmaWarp;         // row tile
-      if (h == 0 && p.timeout_test_ns != 0) mbar_wait_limit(&bars->never, 0, p.timeout_test_ns, abort, p.err);
-      bool ok = !*abort;
-      const uint32_t idesc_s = idesc_bf16_f32(128, kChunk, 0, 0);
-      const uint32_t idesc_pv = idesc_bf16_f32(128, HD, 0, 1);
-      const uint64_t qd = sw128_desc(smem_u32(sQ + h * C::kQTileBytes), 16, 1024);
-      const uint64_t kd = sw128_desc(smem_u32(sK), 16, 1024);
-      const uint64_t vd = sw128_desc(smem_u32(sV), C::kBoxBytes, 1024);
-      const uint32_t q_lo = static_cast<uint32_t>(qd), q_hi = static_cast<uint32_t>(qd >> 32);
-      const uint32_t k_lo = static_cast<uint32_t>(kd), k_hi = static_cast<uint32_t>(kd >> 32);
-      const uint32_t v_lo = static_cast<uint32_t>(vd), v_hi = static_cast<uint32_t>(vd >> 32);
-      const uint32_t col_s = tbase + kColS + h * 128, col_o = tbase + kColO + h * 128;
-      uint32_t n = 0;                        // tiles of the run before the segment's
-      uint32_t segs = 0;                     // segments so far
-      for (; ok && w.more(); w.next(p)) {
-        const bool idle = h == 1 && w.single();      // no rows here: the barriers only
-        // S of step s: chunk s & 1 of tile n + s / 2; with a tile's second chunk its K stage is read
-        auto issue_s = [&](int s) {
-          const uint32_t st = (n + (s >> 1)) % C::kKStages;
-          if (idle) {
-            mbar_arrive(&bars->s_full[h][s & 1]);
-            if (s & 1) mbar_arrive(&bars->k_empty[st]);
-            return;
-          }
-          const uint32_t k0 = k_lo + ((st * C::kTileBytes + (s & 1) * C::kChunkRowsBytes) >> 4);
-#pragma unroll
-          for (int kk = 0; kk < HD / 16; ++kk)
-            mma_ss_lo(col_s + (s & 1) * kChunk, q_lo + (((kk >> 2) * C::kQBoxBytes + (kk & 3) * 32) >> 4), q_hi,
-                      k0 + (((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4), k_hi, idesc_s, kk > 0 ? 1u : 0u);
-          mma_commit(&bars->s_full[h][s & 1]);
-          if (s & 1) mma_commit(&bars->k_empty[st]);
-        };
-        auto wait_k = [&](uint32_t i) {
-          const bool got = mbar_wait(&bars->k_full[i % C::kKStages], (i / C::kKStages) & 1, abort, p.err);
-          tc_fence_after();
-          return got;
-        };
-        const int ns = 2 * w.nt;
-        ok = mbar_wait(&bars->q_ready[h], segs++ & 1, abort, p.err) && wait_k(n);
-        if (!ok) break;
-        issue_s(0);
-        for (int s = 0; s < ns; ++s) {
-          if (s + 1 < ns) {
-            if (s & 1) ok = wait_k(n + ((s + 1) >> 1));
+    // ------------------------------ MMA issuers (one lane each, leading CTA) --------------------
+    if (lane == 0 && rank == 0) {
+      const bool s_issuer = warp == kMmaWarp;
+      if (p.timeout_test_ns != 0) mbar_wait_limit(&bars->never, 0, p.timeout_test_ns, abort, p.err);
+      ok = !*abort;
+      uint32_t n = 0, segs = 0;              // tiles and segments so far
+      if (s_issuer) {
+        const uint32_t idesc = idesc_bf16_f32(256, kKeys, 0, 0);
+        const uint64_t qdesc = sw128_desc(smem_u32(sQ), 16, 1024);
+        const uint64_t kdesc = sw128_desc(smem_u32(sK), 16, 1024);
+        for (; ok && w.more(); w.next(p)) {
+          ok = mbar_wait(&bars->q_ready, segs++ & 1, abort, p.err);
+          for (int j = 0; ok && j < w.nt; ++j, ++n) {
+            const uint32_t ks = n % kKStages, sb = n & 1;
+            if (n >= 2) ok = mbar_wait(&bars->s_free[sb], ((n >> 1) - 1) & 1, abort, p.err);
+            ok = ok && mbar_wait(&bars->k_full[ks], (n / kKStages) & 1, abort, p.err);
             if (!ok) break;
-            issue_s(s + 1);
-          }
-          const int c = s & 1;
-          const uint32_t i = n + (s >> 1), st = i % C::kVStages;
-          ok = mbar_wait(&bars->p_full[h][c], i & 1, abort, p.err);
-          // (an idle row tile gives a V stage back once per load too, as its PV would)
-          if (idle && c == 1) ok = ok && mbar_wait(&bars->v_full[st], (i / C::kVStages) & 1, abort, p.err);
-          if (!ok) break;
-          if (idle) {
-            mbar_arrive(&bars->o_full[h]);
-            if (c == 1) mbar_arrive(&bars->v_empty[st]);
-            continue;
-          }
-          tc_fence_after();
-          const uint32_t v0 = v_lo + ((st * C::kTileBytes + c * C::kChunkRowsBytes) >> 4);
+            tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < kChunk / 16; ++kk)
-            mma_ts_lo(col_o, col_s + c * kChunk + kk * 8, v0 + ((16 * kk * 128) >> 4), v_hi, idesc_pv,
-                      (s > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(&bars->o_full[h]);
-          if (c == 1) mma_commit(&bars->v_empty[st]);
-          if (s + 1 == ns) mma_commit(&bars->o_done[h]);
+            for (int kk = 0; kk < HD / 16; ++kk)
+              mma_ss_pair(tbase + kColS + sb * kKeys,
+                          qdesc + static_cast<uint64_t>(((kk >> 2) * kQBoxBytes + (kk & 3) * 32) >> 4),
+                          kdesc + static_cast<uint64_t>((ks * kStageBytes + (kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4),
+                          idesc, kk > 0 ? 1u : 0u);
+            mma_commit_pair(&bars->s_full[sb]);
+            mma_commit_pair(&bars->k_empty[ks]);
+          }
         }
-        n += w.nt;
+      } else {
+        const uint32_t idesc = idesc_bf16_f32(256, HD, 0, 1);
+        const uint64_t vdesc = sw128_desc(smem_u32(sV), kStageBytes, 1024);
+        for (; ok && w.more(); w.next(p)) {
+          for (int j = 0; j < w.nt; ++j, ++n) {
+            const uint32_t vs = n % kVStages, sb = n & 1;
+            ok = mbar_wait(&bars->p_full[sb], (n >> 1) & 1, abort, p.err);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int kk = 0; kk < kChunk / 16; ++kk)
+                mma_ts_pair(tbase + kColO + c * 128, tbase + kColS + sb * kKeys + c * kChunk + kk * 8,
+                            vdesc + static_cast<uint64_t>((vs * kStageBytes + c * kBoxBytes + 16 * kk * 128) >> 4), idesc,
+                            (j > 0 || kk > 0) ? 1u : 0u);
+            mma_commit_pair(&bars->s_free[sb]);
+            mma_commit_pair(&bars->v_empty[vs]);
+            mma_commit_pair(&bars->o_full);
+            if (j == w.nt - 1) mma_commit_pair(&bars->o_done);
+          }
+        }
       }
       // every MMA completes before TMEM is freed
-      mma_commit(&bars->drain[h]);
-      mbar_drain(&bars->drain[h], 0, p.err);
+      mma_commit_pair(&bars->drain[warp - kMmaWarp]);
+      mbar_drain(&bars->drain[warp - kMmaWarp], 0, p.err);
     }
     __syncwarp();
   } else {
     // ------------------------------ softmax / epilogue ------------------------------------------
-    const int h = warp >> 2;                           // row tile
-    const int lr = (warp & 3) * 32 + lane;             // row of the tile and TMEM lane
-    const uint32_t lane_base = tbase + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const int g = warp >> 2;                           // warpgroup: its chunk of every tile
+    const int quarter = warp & 3;
+    const int lr = quarter * 32 + lane;                // row of the CTA's row tile and TMEM lane
+    const int r = rank * kMaxRows + lr;                // row of the pair
+    const uint32_t lane_base = tbase + (static_cast<uint32_t>(quarter * 32) << 16);
     const unsigned ug = static_cast<unsigned>(p.group);
-    uint8_t* sq = sQ + h * C::kQTileBytes;
-    bool ok = true;
-    uint32_t n = 0;                                    // tiles before this segment
-    // Q of a segment's row tile -> shared memory, in the 128-byte swizzle
+    uint32_t n = 0, segs = 0;                          // tiles and segments so far
+    // Q of a segment's rows -> shared memory, in the 128-byte swizzle: warpgroup g takes columns [64 g, 64 g + 64)
     auto stage_q = [&](const Walk& v) {
-      const int r = h * kMaxRows + lr;
       const bool rv = r < v.rows();
       const unsigned br = static_cast<unsigned>(v.t * kPairRows + (rv ? r : 0));
-      const unsigned qi = br / ug, g = br - qi * ug;
+      const unsigned qi = br / ug, gq = br - qi * ug;
       const uint4* src = reinterpret_cast<const uint4*>(
-          p.q + (static_cast<size_t>(v.s.q0 + qi) * p.hq + static_cast<size_t>(v.h) * p.group + g) * HD);
+          p.q + (static_cast<size_t>(v.s.q0 + qi) * p.hq + static_cast<size_t>(v.h) * p.group + gq) * HD) + g * 8;
+      uint4 x[8];
 #pragma unroll
-      for (int half = 0; half < HD / 64; ++half) {
-        uint4 x[8];
+      for (int c = 0; c < 8; ++c) x[c] = rv ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) x[c] = rv ? __ldg(src + half * 8 + c) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4*>(sq + half * C::kQBoxBytes + lr * 128 + ((c ^ (lr & 7)) << 4)) = x[c];
-      }
+      for (int c = 0; c < 8; ++c)
+        *reinterpret_cast<uint4*>(sQ + g * kQBoxBytes + lr * 128 + ((c ^ (lr & 7)) << 4)) = x[c];
       fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(leader(&bars->q_ready));
     };
-    uint32_t segs = 0;                                 // segments with rows in this tile
-    if (w.more()) {
-      if (h == 0 || !w.single()) stage_q(w);
-      mbar_arrive(&bars->q_ready[h]);
-    }
-    while (ok && w.more()) {
-      const bool idle = h == 1 && w.single();
-      const int r = h * kMaxRows + lr;
+    if (w.more()) stage_q(w);
+    while (w.more()) {
       const bool rv = r < w.rows();
       const bool active = __any_sync(0xffffffffu, rv);
       const unsigned br = static_cast<unsigned>(w.t * kPairRows + (rv ? r : 0));
@@ -513,28 +472,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int p0 = w.s.L - w.s.nq;
       const uint32_t* words = p.tree_mask + static_cast<size_t>(w.s.q0 + qi) * VFY_TREE_WORDS;
       float m_ref = -INFINITY, l = 0.f;
-      const int ns = 2 * w.nt;
-      bool plain = true, zero = false;                 // of the tile
-      for (int s = 0; s < ns; ++s) {
-        const int j = s >> 1, c = s & 1;
-        const uint32_t i = n + j;
-        const int gs = i % kGeo;
-        if (c == 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&bars->geo_full[gs], (i / kGeo) & 1, abort, p.err));
-          if (!ok) break;
-          plain = bars->plain[gs] != 0;
-          zero = bars->zero[gs] != 0;
-        }
+      for (int j = 0; j < w.nt; ++j, ++n) {
+        const int gs = n % kGeo;
+        const uint32_t sb = n & 1;
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->geo_full[gs], (n / kGeo) & 1, abort, p.err));
+        if (!ok) break;
+        const bool plain = bars->plain[gs] != 0, zero = bars->zero[gs] != 0;
         uint32_t keep[2] = {0u, 0u};
-        if (!plain && bars->valid[gs][c] != 0 && rv) {
-          keep[0] = keep32(words, bars->base[gs][c], p0, w.s.L);
-          keep[1] = keep32(words, bars->base[gs][c] + 32, p0, w.s.L);
+        if (!plain && bars->valid[gs][g] != 0 && rv) {
+          keep[0] = keep32(words, bars->base[gs][g], p0, w.s.L);
+          keep[1] = keep32(words, bars->base[gs][g] + 32, p0, w.s.L);
         }
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[h][c], i & 1, abort, p.err));
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[sb], (n >> 1) & 1, abort, p.err));
         if (!ok) break;
         tc_fence_after();
         if (active) {
-          const uint32_t ts = lane_base + kColS + h * 128 + c * kChunk;
+          const uint32_t ts = lane_base + kColS + sb * kKeys + g * kChunk;
           float sv[kChunk];
           {
             uint32_t sr[kChunk];
@@ -557,27 +510,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool scale_o = raise && m_ref != -INFINITY;
           float alpha = 1.f;
           if (raise) {
-            alpha = ex2_approx(m_ref - m_tile);        // 0 where m_ref = -inf
+            alpha = ex2_approx(m_ref - m_tile);      // 0 where m_ref = -inf
             l *= alpha;
             m_ref = m_tile;
           }
           if (__any_sync(0xffffffffu, scale_o)) {
-            // O holds the steps before s. PV(s-2) was issued before S(s) and PV(s) needs this step's P: the
-            // barrier of PV(s-1) is in that phase or the one after.
-            ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_full[h], (2 * n + s - 1) & 1, abort, p.err));
+            // O holds the tiles before this one: PV of the last one is waited for. (S of this tile was issued after
+            // PV of the tile before that, and PV of this tile needs its P: the barrier is in that phase or the one
+            // after.)
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_full, (n - 1) & 1, abort, p.err));
             if (!ok) break;
             tc_fence_after();
             const float a = scale_o ? alpha : 1.f;
 #pragma unroll 1
             for (int x = 0; x < HD / 32; ++x) {
               uint32_t o[32];
-              tmem_ld32(lane_base + kColO + h * 128 + x * 32, o);
+              tmem_ld32(lane_base + kColO + g * 128 + x * 32, o);
 #pragma unroll
               for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-              tmem_st32(lane_base + kColO + h * 128 + x * 32, o);
+              tmem_st32(lane_base + kColO + g * 128 + x * 32, o);
             }
           }
-          // p = 2^(s * scale * log2e - m_ref), packed over the first half of this S
+          // p = 2^(s * scale * log2e - m_ref), packed over the first half of this chunk's S
           const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
           const float2 scale2 = make_float2(p.scale_log2, p.scale_log2), neg2 = make_float2(neg, neg);
           float2 ps[4];
@@ -595,94 +549,108 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st32(ts, pk);
         }
         tc_fence_before();
-        // One warp's arrival waits for the tile's V, so the issuer's wait for P covers V too.
-        if (!idle && (zero || ((warp & 3) == kVRelayWarp && c == 0))) {
-          const int sv = i % C::kVStages;
-          ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_full[sv], (i / C::kVStages) & 1, abort, p.err));
+        // One warp's arrival waits for the tile's V in this CTA, so the issuer's wait for P covers V too.
+        if (zero || warp == kVRelayWarp) {
+          const int sv = n % kVStages;
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_full[sv], (n / kVStages) & 1, abort, p.err));
           if (!ok) break;
           if (zero) {
-            // V rows of keys outside the sequence may hold anything, and 0 * NaN is NaN on the tensor core. Both
-            // row tiles zero them (the same zeros), each before its own P.
-            const int key = lr >> 1;                   // two threads per key
-            if (bars->valid[gs][c] == 0 || bars->base[gs][c] + key >= w.s.L) {
-              uint8_t* row = sV + sv * C::kTileBytes + c * C::kChunkRowsBytes + key * 128;
+            // V rows of keys outside the sequence may hold anything, and 0 * NaN is NaN on the tensor core: two
+            // threads zero a key's row (its CTA's columns) before P.
+            const int key = lr >> 1;
+            if (bars->valid[gs][g] == 0 || bars->base[gs][g] + key >= w.s.L) {
+              uint8_t* row = sV + sv * kStageBytes + g * kBoxBytes + key * 128 + (lr & 1) * 64;
 #pragma unroll
-              for (int x = (lr & 1) * C::kBoxes * 4; x < ((lr & 1) + 1) * C::kBoxes * 4; ++x)
-                *reinterpret_cast<uint4*>(row + (x >> 3) * C::kBoxBytes + (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+              for (int x = 0; x < 4; ++x) *reinterpret_cast<uint4*>(row + x * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
             fence_proxy_async_smem();
           }
         }
-        mbar_arrive(&bars->p_full[h][c]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(leader(&bars->p_full[sb]));
       }
       if (!ok) break;
-      // the next segment's first S may run during this one's epilogue: every S here has read Q
-      Walk nx = w;
-      nx.next(p);
-      if (nx.more()) {
-        if (h == 0 || !nx.single()) stage_q(nx);
-        mbar_arrive(&bars->q_ready[h]);
-      }
-      if (idle) {
-        n += w.nt;
-        w = nx;
-        continue;
-      }
-      ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[h], segs++ & 1, abort, p.err));
+      // ---- the segment's end: merge the two warpgroups' halves ----
+      bars->xm[g][lr] = l > 0.f ? m_ref : -INFINITY;
+      bars->xl[g][lr] = l;
+      mbar_arrive(&bars->half_ready[quarter]);
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars->half_ready[quarter], segs & 1, abort, p.err));
+      if (!ok) break;
+      const float m0 = bars->xm[0][lr], m1 = bars->xm[1][lr], l0 = bars->xl[0][lr], l1 = bars->xl[1][lr];
+      const float m_row = fmaxf(m0, m1);
+      const float w0 = l0 > 0.f ? ex2_approx(m0 - m_row) : 0.f, w1 = l1 > 0.f ? ex2_approx(m1 - m_row) : 0.f;
+      const float l_row = w0 * l0 + w1 * l1;
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done, segs & 1, abort, p.err));
       if (!ok) break;
       tc_fence_after();
+      // every S of the segment has read Q: the next one's first S may run during this one's epilogue
+      Walk nx = w;
+      nx.next(p);
+      if (nx.more()) stage_q(nx);
       if (active) {
-        const uint32_t to = lane_base + kColO + h * 128;
-        if (w.whole()) {
-          const float inv = l > 0.f ? 1.f / l : 0.f;
-          const int t = w.s.q0 + static_cast<int>(qi);
-          const int hq = w.h * p.group + static_cast<int>(br - qi * ug);
-          const bool wr = rv && t < p.token_cap;
-          uint16_t* dst = p.out + (static_cast<size_t>(wr ? t : 0) * p.hq + hq) * HD;
-#pragma unroll 1
-          for (int c = 0; c < HD / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(to + c * 32, o);
-            if (!wr) continue;
-            uint32_t out[16];
+        // warpgroup g writes columns [64 g, 64 g + 64); a half without a key has no weight, and its O may be anything
+        const bool whole = w.whole();
+        const float inv = whole ? (l_row > 0.f ? 1.f / l_row : 0.f) : 1.f;
+        const float a0 = w0 * inv, a1 = w1 * inv;
+        const int t = w.s.q0 + static_cast<int>(qi);
+        const int hq = w.h * p.group + static_cast<int>(br - qi * ug);
+        const bool wr = rv && (!whole || t < p.token_cap);
+        const size_t at = (2 * static_cast<size_t>(pair) + (w.index > 0 ? 1 : 0)) * kPairRows + r;
+        uint16_t* out = p.out + (static_cast<size_t>(wr ? t : 0) * p.hq + hq) * HD + g * 64;
+        float* part = p.part_o + at * HD + g * 64;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          uint32_t o0[32], o1[32];
+          tmem_ld32x2(lane_base + kColO + g * 64 + x * 32, lane_base + kColO + 128 + g * 64 + x * 32, o0, o1);
+          if (!wr) continue;
+          float v[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            v[e] = l0 > 0.f ? a0 * __uint_as_float(o0[e]) : 0.f;
+            v[e] = l1 > 0.f ? fmaf(a1, __uint_as_float(o1[e]), v[e]) : v[e];
+          }
+          if (whole) {
+            uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float a = l > 0.f ? __uint_as_float(o[2 * e]) * inv : 0.f;
-              const float b = l > 0.f ? __uint_as_float(o[2 * e + 1]) * inv : 0.f;
-              const __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b);
-              out[e] = *reinterpret_cast<const uint32_t*>(&h2);
+              const __nv_bfloat162 h2 = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+              pk[e] = *reinterpret_cast<const uint32_t*>(&h2);
             }
 #pragma unroll
             for (int e = 0; e < 16; e += 4)
-              *reinterpret_cast<uint4*>(dst + c * 32 + 2 * e) = make_uint4(out[e], out[e + 1], out[e + 2], out[e + 3]);
-          }
-          if (wr && p.lse != nullptr)
-            p.lse[static_cast<size_t>(t) * p.hq + hq] = l > 0.f ? (m_ref + __log2f(l)) * 0.6931471805599453f : -INFINITY;
-        } else {
-          const size_t at = (2 * static_cast<size_t>(blockIdx.x) + (w.index > 0 ? 1 : 0)) * kPairRows + r;
-          float* dst = p.part_o + at * HD;
-#pragma unroll 1
-          for (int c = 0; c < HD / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(to + c * 32, o);
-            if (!rv || !(l > 0.f)) continue;
+              *reinterpret_cast<uint4*>(out + x * 32 + 2 * e) = make_uint4(pk[e], pk[e + 1], pk[e + 2], pk[e + 3]);
+          } else if (l_row > 0.f) {
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(dst + c * 32 + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              *reinterpret_cast<float4*>(part + x * 32 + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
           }
-          if (rv) reinterpret_cast<float2*>(p.part_ml)[at] = make_float2(l > 0.f ? m_ref : -INFINITY, l);
+        }
+        if (wr && g == 0) {
+          if (!whole)
+            reinterpret_cast<float2*>(p.part_ml)[at] = make_float2(l_row > 0.f ? m_row : -INFINITY, l_row);
+          else if (p.lse != nullptr)
+            p.lse[static_cast<size_t>(t) * p.hq + hq] =
+                l_row > 0.f ? (m_row + __log2f(l_row)) * 0.6931471805599453f : -INFINITY;
         }
       }
+      // the next segment's PV writes O, and its end (m, l): both warpgroups are done with both
       tc_fence_before();
-      n += w.nt;
+      mbar_arrive(&bars->o_read);
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_read, segs & 1, abort, p.err));
+      if (!ok) break;
+      ++segs;
       w = nx;
     }
   }
+  // A wait that ran out ends the other CTA's waits too; both leave together (remote arrivals, pair MMAs).
+  if (!ok && lane == 0) st_dsmem_u32(dsmem_addr(smem_u32(&bars->abort), rank ^ 1), 1u);
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();
   if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tbase, kTmemCols);
+    tmem_dealloc_pair(tbase, kTmemCols);
   }
 }
 
@@ -692,7 +660,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 // four warps' sums meet in shared memory.
 constexpr int kAhead = 8;
 
-template <int HD>
 __global__ void __launch_bounds__(128) combine_tree_kernel(const AttnParams p, int ctas) {
   constexpr int kPer = HD / 32;
   using Vec = typename std::conditional<kPer == 4, float4, float2>::type;
@@ -801,24 +768,45 @@ __global__ void __launch_bounds__(128) combine_tree_kernel(const AttnParams p, i
     p.lse[static_cast<size_t>(t) * p.hq + hq] = lsum > 0.f ? (mmax + __log2f(lsum)) * 0.6931471805599453f : -INFINITY;
 }
 
-template <int HD>
-cudaError_t launch_hd(const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int ctas,
-                      cudaStream_t stream) {
-  static size_t done[64] = {};
-  auto kern = attend_tree_kernel<HD>;
-  cudaError_t e = ensure_smem_limit(kern, Cfg<HD>::kSmemBytes, done);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(kern, dim3(ctas), dim3(kThreads), Cfg<HD>::kSmemBytes, stream, p, tk, tv);
-  if (e != cudaSuccess) return e;
-  const long long rows = static_cast<long long>(p.token_cap) * p.hq;
-  return launch_pdl(combine_tree_kernel<HD>, dim3(static_cast<unsigned>(rows)), dim3(128), 0, stream, p, ctas);
-}
-
 }  // namespace
 
-cudaError_t launch_attend_tree(int head_dim, const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
-                               int ctas, cudaStream_t stream) {
-  return head_dim == 128 ? launch_hd<128>(p, tk, tv, ctas, stream) : launch_hd<64>(p, tk, tv, ctas, stream);
+// CTA pairs that can be resident at once on the current device (one CTA per SM), cached per device.
+int attend_tree_pairs() {
+  static int count[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if (count[dev] != 0) return count[dev];
+  static size_t done[64] = {};
+  if (ensure_smem_limit(attend_tree_kernel, kSmemBytes, done) != cudaSuccess) return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, attend_tree_kernel, &cfg) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  count[dev] = n;
+  return n;
+}
+
+cudaError_t launch_attend_tree(const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int pairs,
+                               cudaStream_t stream) {
+  static size_t done[64] = {};
+  cudaError_t e = ensure_smem_limit(attend_tree_kernel, kSmemBytes, done);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(attend_tree_kernel, dim3(2 * pairs), dim3(kThreads), kSmemBytes, stream, p, tk, tv);
+  if (e != cudaSuccess) return e;
+  const long long rows = static_cast<long long>(p.token_cap) * p.hq;
+  return launch_pdl(combine_tree_kernel, dim3(static_cast<unsigned>(rows)), dim3(128), 0, stream, p, pairs);
 }
 
 }  // namespace vfy

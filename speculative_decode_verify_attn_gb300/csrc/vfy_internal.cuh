@@ -95,10 +95,12 @@ cudaError_t launch_combine(int head_dim, const CombineParams& p, cudaStream_t st
 int attend_merge_limit(bool ring, int head_dim, bool tree);
 
 // ------------------------------ trees -------------------------------------------------------
-// Tree attention of a full layer in 256-row pairs by `ctas` persistent CTAs, and the merge (two
-// launches). p.part_o / p.part_ml hold 2 * ctas partial segments of 256 rows.
-cudaError_t launch_attend_tree(int head_dim, const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
-                               int ctas, cudaStream_t stream);
+// Tree attention of a full layer (d = 128) by `pairs` persistent CTA pairs of 256 rows, and the merge (two
+// launches). p.part_o / p.part_ml hold 2 * pairs partial segments of 256 rows.
+cudaError_t launch_attend_tree(const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int pairs,
+                               cudaStream_t stream);
+// The most pairs that are resident at once on the current device (0 on error).
+int attend_tree_pairs();
 
 struct TreePlanParams {
   const int32_t* parents;     // [T]

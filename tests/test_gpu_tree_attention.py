@@ -229,14 +229,15 @@ def test_ragged_batch(env, splits):
         ctx.close()
 
 
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("ns,Ls", [([9, 47, 20, 64, 3], [60000, 50000, 70000, 3000, 130]), ([64, 10], [40000, 190000]),
                                    ([10, 64], [190000, 40000]), ([130, 200, 64], [30000, 64000, 90000])])
-def test_long_ragged_batch(env, ns, Ls):
+def test_long_ragged_batch(env, ns, Ls, d):
     """One KV head, so that a CTA's run holds many tiles and passes from sequences of one row tile to such
     of two and back."""
     H, vfy = env
     rng = np.random.default_rng(sum(Ls))
-    hq, d = 4, 64
+    hq = 4
     cu = np.concatenate([[0], np.cumsum(ns)])
     counts = [-(-L // C) for L in Ls]
     cu_res = np.concatenate([[0], np.cumsum(counts)])
