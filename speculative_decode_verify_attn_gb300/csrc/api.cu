@@ -22,6 +22,7 @@ struct vfy_ctx {
   int accept_rows_cap;
   unsigned int* accept_counter;
   unsigned int* tree_counters;   // one per sequence (tree acceptance)
+  vfy::TreePiece* tree_pieces;   // items cut between CTA pairs (tree attention)
   // sticky device error word
   int* err;
   int full_splits;   // 0 = automatic
@@ -165,14 +166,15 @@ vfy_status vfy_create(const vfy_config* cfg_in, int device, vfy_ctx** out) {
 
   ctx->row_tiles = ceil_div(static_cast<long long>(cfg.max_queries_per_seq) * group, kMaxRows);
   size_t parts = static_cast<size_t>(cfg.max_seqs) * ctx->row_tiles * cfg.num_kv_heads * cfg.max_splits * kMaxRows;
-  // tree attention in pairs of row tiles: two partial segments per SM
-  parts = std::max(parts, static_cast<size_t>(ctx->num_sms) * 2 * 2 * kMaxRows);
+  // tree attention by CTA pairs: two partial segments of two row tiles for every two SMs
+  parts = std::max(parts, static_cast<size_t>(ctx->num_sms) * 2 * kMaxRows);
   ctx->accept_rows_cap = cfg.max_seqs * cfg.max_queries_per_seq;
   bool ok = cudaMalloc(&ctx->part_o, parts * cfg.head_dim * sizeof(float)) == cudaSuccess &&
             cudaMalloc(&ctx->part_ml, parts * 2 * sizeof(float)) == cudaSuccess &&
             cudaMalloc(&ctx->accept_keys, ctx->accept_rows_cap * sizeof(unsigned long long)) == cudaSuccess &&
             cudaMalloc(&ctx->accept_counter, sizeof(unsigned int)) == cudaSuccess &&
             cudaMalloc(&ctx->tree_counters, cfg.max_seqs * sizeof(unsigned int)) == cudaSuccess &&
+            cudaMalloc(&ctx->tree_pieces, ctx->num_sms * sizeof(vfy::TreePiece)) == cudaSuccess &&
             cudaMalloc(&ctx->err, sizeof(int)) == cudaSuccess;
   if (ok)
     ok = cudaMemset(ctx->accept_keys, 0, ctx->accept_rows_cap * sizeof(unsigned long long)) == cudaSuccess &&
@@ -200,6 +202,7 @@ void vfy_destroy(vfy_ctx* ctx) {
     cudaFree(ctx->accept_keys);
     cudaFree(ctx->accept_counter);
     cudaFree(ctx->tree_counters);
+    cudaFree(ctx->tree_pieces);
     cudaFree(ctx->err);
     (void)cudaGetLastError();
   }
@@ -492,6 +495,7 @@ static vfy_status attend_common(vfy_ctx* ctx, bool ring, const uint16_t* q, cons
   p.tree_mask = tree_mask;
   p.tree_depth = tree_depth;
   p.num_seqs = num_seqs;
+  p.tree_pieces = ctx->tree_pieces;
   p.token_cap = num_seqs * max_q;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int pairs = tree && !ring ? tree_pairs(ctx, row_tiles, num_seqs) : 0;

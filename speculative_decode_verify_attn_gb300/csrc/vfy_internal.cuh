@@ -17,6 +17,15 @@ constexpr int kMaxSelectChunks = 32768;
 constexpr int kMaxSelectK = 4096;
 
 // ------------------------------ attention ---------------------------------------------------
+// What a CTA pair of attend_tree_kernel tells the combine: the item that starts in its run and ends in a later one.
+struct alignas(16) TreePiece {
+  int rows;                   // of the item (at most 256); 0: no such item
+  int row0, q0, head0;        // its first row in the sequence's block, the block's first token, its first query head
+  int slot;                   // partial slot of the item's first piece (2 per pair)
+  int last;                   // last pair with a piece of it
+  int pad[2];
+};
+
 struct AttnParams {
   const uint16_t* q;          // [T][Hq][d]
   const int32_t* cu_q;        // [B+1]
@@ -51,6 +60,7 @@ struct AttnParams {
   const uint32_t* tree_mask;  // [T][VFY_TREE_WORDS]
   const int32_t* tree_depth;  // [T], window layers
   int num_seqs;               // attend_tree_kernel: the grid is no function of it
+  TreePiece* tree_pieces;     // [CTA pairs] workspace of attend_tree_kernel and its combine
 };
 
 // Splits of one (sequence, KV head) that one cluster can merge in the attention kernel (the
