@@ -408,9 +408,17 @@ vfy_status vfy_append_swa(vfy_ctx* ctx, const uint16_t* k_new, const uint16_t* v
 static int tree_capacity(const vfy_config& c) { return std::min(c.max_queries_per_seq, VFY_MAX_TREE_NODES); }
 
 // Does a tree's full layer go to CTA pairs of 256 rows (and how many), or to the linear block's kernel (0)?
-static int tree_pairs(const vfy_ctx* ctx, int row_tiles, int num_seqs) {
-  if (ctx->full_splits != 0 || ctx->cfg.head_dim != 128 || (row_tiles == 1 && num_seqs == 1)) return 0;
-  return std::min(vfy::attend_tree_pairs(), ctx->num_sms / 2);
+// Pairs balance whatever the lengths, and halve the K/V traffic of two row tiles; each run pays about 8 us for its
+// start and the merge. us of one layer, 4 KV heads, the linear kernel with its best splits against pairs:
+//   two row tiles (64 nodes, G = 4), 64 chunks: 1 sequence 15.0 / 18.7, 4: 26.9 / 27.8, 8: 43.9 / 34.8, 16: 46.5 / 52.2;
+//   256 chunks: 1: 22.5 / 23.8, 4: 55 / 44, 16: 159 / 106; 1024 chunks: 1: 47 / 43, 8: 263 / 173;
+//   one row tile (17 nodes), 256 chunks: 2 sequences 19.6 / 25.9, 4: 31.5 / 36.9, 8: 54 / 57, 16: 97 / 87;
+//   1024 chunks: 2: 57 / 64, 4: 97 / 97, 8: 168 / 167, 8 ragged (750 chunks at most): 105 / 104, and 130 with one
+//   wave of splits, which is the best for equal lengths.
+static int tree_pairs(const vfy_ctx* ctx, int row_tiles, int num_seqs, int max_res) {
+  if (ctx->full_splits != 0 || ctx->cfg.head_dim != 128) return 0;
+  const bool take = row_tiles > 1 ? max_res >= 128 : num_seqs >= 4 && max_res >= 256;
+  return take ? std::min(vfy::attend_tree_pairs(), ctx->num_sms / 2) : 0;
 }
 
 static vfy_status attend_common(vfy_ctx* ctx, bool ring, const uint16_t* q, const int32_t* cu_q,
@@ -434,7 +442,16 @@ static vfy_status attend_common(vfy_ctx* ctx, bool ring, const uint16_t* q, cons
   if (!ring) {
     splits = ctx->full_splits;
     if (splits == 0) {
-      if (row_tiles > 1) {
+      if (tree && (row_tiles > 1 || num_seqs > 1)) {   // (else as the linear block: a chain has its bits)
+        // One wave of CTAs: us with one wave against four of 17 nodes over 64 chunks, 4 sequences 15.3 / 31.9, 8
+        // 22.3 / 36.4, 16 35.3 / 47.1. Long contexts of a batch (here with d = 64; with d = 128 CTA pairs take them)
+        // get two waves, for sequences of different lengths: 8 of equal lengths over 256 chunks 25.0 / 27.3.
+        const int items = hkv * num_seqs * row_tiles;
+        splits = ctx->num_sms * (num_seqs >= 4 && max_res >= 256 ? 2 : 1) / items;
+        // Short contexts: as many as one cluster merges in the attention kernel, which with 16 splits finds too few
+        // GPCs (64 chunks, 8 items: 12 splits 11.9 us, 16 20.6, 19 and the combine 13.5).
+        if (max_res <= 64) splits = std::min(splits, 12);
+      } else if (row_tiles > 1) {
         // Blocks of several row tiles (prefill-shaped) have (KV head, row tile) items enough to
         // fill the SMs with few splits, and a long split keeps the tensor pipe busier: at most one
         // wave. Measured with 1024 queries over 128 chunks (128 items): 1 split 121 us, 2 splits
@@ -498,7 +515,7 @@ static vfy_status attend_common(vfy_ctx* ctx, bool ring, const uint16_t* q, cons
   p.tree_pieces = ctx->tree_pieces;
   p.token_cap = num_seqs * max_q;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int pairs = tree && !ring ? tree_pairs(ctx, row_tiles, num_seqs) : 0;
+  const int pairs = tree && !ring ? tree_pairs(ctx, row_tiles, num_seqs, max_res) : 0;
   if (pairs > 0) {
     p.out = out;
     p.lse = lse;
