@@ -11,10 +11,12 @@
 // Every entry is read and written by one thread, so the call may work in place.
 // Bound by bytes in flight: the first rows' logits are loaded before the rules, the mask words of 32 rows
 // at a time go through shared memory (one wait instead of one per batch), four rows of eight columns are
-// in flight per thread. GB300: 17 x 131072 fp32 9.7 us (5.3 with no rule; the bytes alone 2.7); 339 rows x
-// 100003 bf16 of 16 sequences 73.5 us (2.9 TB/s), fp32 rows of 131072 without rules 6.4 TB/s. Loading
-// eight neighbouring columns per thread (half-sector stores), per-thread mask loads, and columns past a
-// row's end in a loop of their own each cost 15 to 40 us of the batch.
+// in flight per thread. GB300: 17 x 131072 fp32 8.5 us (5.3 with no rule; the bytes alone 2.7); 339 rows x
+// 100003 bf16 of 16 sequences 66.8 us (3.2 TB/s; 56 us with a vocabulary of 100000, whose rows all start alike,
+// and 41 without rules). Loading eight neighbouring columns per thread (half-sector stores), per-thread mask
+// loads, and columns past a row's end in a loop of their own each cost 15 to 40 us of the batch; registers for
+// six CTAs per SM instead of five 10 us, and refilling each row's registers as soon as it is done, instead of
+// four rows at a time, 20.
 #include "ptx.cuh"
 #include "vfy_internal.cuh"
 
@@ -25,13 +27,12 @@ constexpr int kThreads = 128;
 constexpr int kCols = 8;                       // columns per thread: two groups of four neighbours, so that a
 constexpr int kGroup = kThreads * 4;           // warp's 16-byte stores cover whole sectors
 constexpr int kSeg = kThreads * kCols;         // columns per CTA
-constexpr int kNodes = VFY_MAX_TREE_NODES;
 constexpr int kWords = VFY_TREE_WORDS;
 constexpr int kNone = 0x7fffffff;
 constexpr int kSpan = kSeg + 3;                // columns a CTA keeps
 constexpr int kBiasAhead = 4;                  // bias entries in flight per thread
-constexpr int kMaskRows = 32;                  // rows whose mask words are staged at a time
 constexpr int kSpanWords = kSeg / 32 + 2;      // words that kSpan columns touch
+constexpr int kSpanIters = (kSpan + kThreads - 1) / kThreads;
 
 // A thread's eight columns of one row, as they were loaded: rows in flight cost registers. Bit e of `valid`:
 // column e lies in the row (the others read 0). `vec`: the groups are aligned to their four-entry words.
@@ -78,12 +79,18 @@ __device__ __forceinline__ float entry_of(const Raw<BF16>& d, int e) {
 // column e of a thread's eight, from its first
 __device__ __forceinline__ constexpr int col_of(int e) { return (e >> 2) * kGroup + (e & 3); }
 
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads, BF16 ? 6 : 5) process_logits_kernel(const LogitParams p) {
+// ONE: every sequence has one row, as when a request starts or decodes without drafts: node 0 is in the counts, so
+// no token is drafted. Seven CTAs per SM then hold 8 rows of 131072 columns in one wave (8 requests' first rows with
+// their prompt counts 9.8 us, 14.3 with the general kernel).
+template <bool BF16, bool ONE>
+__global__ void __launch_bounds__(kThreads, ONE ? 7 : 5) process_logits_kernel(const LogitParams p) {
+  constexpr int kNodes = ONE ? 1 : VFY_MAX_TREE_NODES;
+  constexpr int kMaskRows = ONE ? 1 : 32;      // rows whose mask words are staged at a time
+  constexpr int kMaskIters = (kMaskRows * kSpanWords + kThreads - 1) / kThreads;
   // Columns seg0 - 3 .. seg0 + kSeg - 1 of the sequence (a row uses kSeg of them, see below).
   __shared__ int32_t s_count[kSpan];
   __shared__ float s_bias[kSpan];
-  __shared__ int s_entry[kSpan];               // lowest node (less one) that drafts the column
+  __shared__ int s_entry[ONE ? 1 : kSpan];     // lowest node (less one) that drafts the column
   __shared__ int s_turn[kSpan];                // lowest bias entry of the column still to be added
   __shared__ uint32_t s_set[kNodes][kWords];   // per entry: the nodes that draft its token
   __shared__ int s_mask[kNodes];               // per row: its grammar mask, -1 = none
@@ -110,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 6 : 5) process_logits_kernel(
   const int step = gridDim.z;
   const int i0 = (static_cast<int>(blockIdx.z) - r0 % step + step) % step;
   if (i0 >= n && !report) return;
-  const int passes = ((p.vocab & 3) == 0 && (p.stride & 3) == 0) || (step & 3) == 0 ? 1 : 4;
+  const int passes = ONE || ((p.vocab & 3) == 0 && (p.stride & 3) == 0) || (step & 3) == 0 ? 1 : 4;
   const int stride = passes * step;            // rows of one pass
   const int seg0 = static_cast<int>(blockIdx.x) * kSeg;
   const long long out_base = static_cast<long long>(reinterpret_cast<uintptr_t>(p.out) >> 2);
@@ -118,9 +125,9 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 6 : 5) process_logits_kernel(
   auto shift_of = [&](int i) { return static_cast<int>(((r0 + static_cast<long long>(i)) * p.vocab + out_base) & 3); };
 
   // A batch: kRows rows of a pass at the columns v0 + {0 .. 3} and v0 + kGroup + {0 .. 3} of this thread:
-  // 64 or 128 bytes of logits in flight per thread, 20 to 24 warps per SM. Columns past the row's ends are
+  // 64 or 128 bytes of logits in flight per thread, 20 warps per SM. Columns past the row's ends are
   // left out one by one, within the same batches.
-  constexpr int kRows = 4;
+  constexpr int kRows = ONE ? 1 : 4;
   constexpr int kSize = BF16 ? 2 : 4;
   const uint32_t words_per_mask = (static_cast<uint32_t>(p.vocab) + 31u) / 32u;
   const long long in_pitch = static_cast<long long>(stride) * p.stride * kSize;
@@ -155,14 +162,15 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 6 : 5) process_logits_kernel(
     e0 = r.cu_bias[b];
     e1 = r.cu_bias[b + 1];
   }
-  int draft_col[kNodes / kThreads];            // this thread's nodes tid + 1, ... (node 0 is in the counts)
+  constexpr int kNodeIters = (kNodes + kThreads - 1) / kThreads;
+  int draft_col[kNodeIters];                   // this thread's nodes tid + 1, ... (node 0 is in the counts)
   if (penalties) {
     if (r.repetition != nullptr) rep = r.repetition[b];
     if (r.frequency != nullptr) freq = r.frequency[b];
     if (r.presence != nullptr) pres = r.presence[b];
   }
 #pragma unroll
-  for (int k = 0; k < kNodes / kThreads; ++k) {
+  for (int k = 0; k < kNodeIters; ++k) {
     draft_col[k] = -1;
     const int at = k * kThreads + tid;
     if (penalties && r.drafts != nullptr && at + 1 < n) {
@@ -201,18 +209,56 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 6 : 5) process_logits_kernel(
     }
   };
   load_bias(e0);
-  for (int c = tid; c < kSpan; c += kThreads) {
-    const int v = seg0 - 3 + c;
-    s_count[c] = penalties && v >= 0 && v < p.vocab ? __ldg(r.counts + static_cast<size_t>(b) * p.vocab + v) : 0;
+  // (all of a thread's counts and mask words at once: a wait for memory less each)
+  int32_t count[kSpanIters];
+#pragma unroll
+  for (int u = 0; u < kSpanIters; ++u) {
+    const int v = seg0 - 3 + tid + u * kThreads;
+    count[u] = penalties && v >= 0 && v < p.vocab && tid + u * kThreads < kSpan
+                   ? __ldg(r.counts + static_cast<size_t>(b) * p.vocab + v)
+                   : 0;
+  }
+  const int my_rows = i0 < n ? (n - i0 + step - 1) / step : 0;
+  const int word0 = max(seg0 - 3, 0) >> 5;     // first staged word of a mask
+  // the mask words of rows j0 .. j1 - 1 of this CTA, into s_lets; mask_of(i) = the mask of row i, -1 = none
+  auto stage_masks = [&](int j0, int j1, auto mask_of) {
+    const int have = min(kSpanWords, static_cast<int>(words_per_mask) - word0);
+    uint32_t word[kMaskIters];
+#pragma unroll
+    for (int u = 0; u < kMaskIters; ++u) {
+      const int x = tid + u * kThreads, j = x / kSpanWords, w = x - j * kSpanWords;
+      word[u] = 0xffffffffu;
+      if (j < j1 - j0 && w < have) {
+        const int mask = mask_of(i0 + (j0 + j) * step);
+        if (mask >= 0)
+          word[u] = __ldg(r.grammar + static_cast<uint64_t>(static_cast<uint32_t>(mask)) * words_per_mask + word0 + w);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kMaskIters; ++u) {
+      const int x = tid + u * kThreads;
+      if (x < (j1 - j0) * kSpanWords) (&s_lets[0][0])[x] = word[u];
+    }
+  };
+  if (grammar)
+    stage_masks(0, min(my_rows, kMaskRows), [&](int i) {
+      const int mask = r.mask_index != nullptr ? __ldg(r.mask_index + r0 + i) : r0 + i;
+      return mask < r.num_masks ? mask : -1;
+    });
+#pragma unroll
+  for (int u = 0; u < kSpanIters; ++u) {
+    const int c = tid + u * kThreads;
+    if (c >= kSpan) break;
+    s_count[c] = count[u];
     s_bias[c] = -0.f;
-    s_entry[c] = kNone;
+    if constexpr (!ONE) s_entry[c] = kNone;
     s_turn[c] = kNone;
   }
   if (tid == 0) s_num_drafted = 0;
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < kNodes / kThreads; ++k) {
-    if (draft_col[k] < 0) continue;
+  for (int k = 0; k < kNodeIters; ++k) {
+    if (ONE || draft_col[k] < 0) continue;
     if (atomicMin(&s_entry[draft_col[k]], k * kThreads + tid) == kNone)
       s_drafted[atomicAdd(&s_num_drafted, 1)] = draft_col[k];
   }
@@ -254,12 +300,12 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 6 : 5) process_logits_kernel(
     if (base >= e1) break;
     load_bias(base);
   }
-  const int num_drafted = s_num_drafted;       // (the bias rounds passed at least one barrier)
+  const int num_drafted = ONE ? 0 : s_num_drafted;       // (the bias rounds passed at least one barrier)
   if (num_drafted > 0) {
     for (int w = tid; w < kNodes * kWords; w += kThreads) s_set[0][w] = 0u;
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kNodes / kThreads; ++k) {
+    for (int k = 0; k < kNodeIters; ++k) {
       const int node = k * kThreads + tid + 1;
       if (draft_col[k] >= 0) atomicOr(&s_set[s_entry[draft_col[k]]][node >> 5], 1u << (node & 31));
     }
@@ -277,20 +323,11 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 6 : 5) process_logits_kernel(
   };
   auto rule = [&](float v, bool seen, float add) { return rules ? fmaf(v, seen ? (v > 0.f ? inv : rep) : 1.f, add) : v; };
   // ---- the rows, kMaskRows of this CTA's at a time (row j: i = i0 + j step) ----
-  const int my_rows = i0 < n ? (n - i0 + step - 1) / step : 0;
-  const int word0 = max(seg0 - 3, 0) >> 5;     // first staged word of a mask
   for (int j0 = 0; j0 < my_rows; j0 += kMaskRows) {
     const int j1 = min(my_rows, j0 + kMaskRows);
-    if (grammar) {
-      if (j0 > 0) __syncthreads();
-      const int have = min(kSpanWords, static_cast<int>(words_per_mask) - word0);
-      for (int x = tid; x < (j1 - j0) * kSpanWords; x += kThreads) {
-        const int j = x / kSpanWords, w = x - j * kSpanWords;
-        const int mask = s_mask[i0 + (j0 + j) * step];
-        s_lets[j][w] = mask >= 0 && w < have
-                           ? __ldg(r.grammar + static_cast<uint64_t>(static_cast<uint32_t>(mask)) * words_per_mask + word0 + w)
-                           : 0xffffffffu;
-      }
+    if (grammar && j0 > 0) {
+      __syncthreads();
+      stage_masks(j0, j1, [&](int i) { return s_mask[i]; });
       __syncthreads();
     }
     for (int pass = 0; pass < passes; ++pass) {
@@ -310,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 6 : 5) process_logits_kernel(
         const int32_t word = s_count[c];
         if (word != 0) seen |= 1u << e;
         add[e] = addend(word, s_bias[c]);
-        if (num_drafted > 0 && s_entry[c] != kNone) mine &= ~(1u << e);
+        if (!ONE && num_drafted > 0 && s_entry[c] != kNone) mine &= ~(1u << e);
       }
       const int bit0 = v0 - 32 * word0;          // of a staged mask; -3 .. -1 only where word0 = 0
       float* dst = p.out + ((r0 + static_cast<long long>(i0 + first * step)) * p.vocab + v0);
@@ -457,8 +494,13 @@ __global__ void __launch_bounds__(kHistThreads) rebuild_counts_kernel(const Coun
 
 cudaError_t launch_process_logits(const LogitParams& p, bool bf16, cudaStream_t stream) {
   dim3 grid(p.segs, p.num_seqs, p.row_parts);
-  if (bf16) return launch_pdl(process_logits_kernel<true>, grid, dim3(kThreads), 0, stream, p);
-  return launch_pdl(process_logits_kernel<false>, grid, dim3(kThreads), 0, stream, p);
+  // (each sequence has a row at least)
+  const bool one = p.max_rows == p.num_seqs;
+  if (bf16)
+    return one ? launch_pdl(process_logits_kernel<true, true>, grid, dim3(kThreads), 0, stream, p)
+               : launch_pdl(process_logits_kernel<true, false>, grid, dim3(kThreads), 0, stream, p);
+  return one ? launch_pdl(process_logits_kernel<false, true>, grid, dim3(kThreads), 0, stream, p)
+             : launch_pdl(process_logits_kernel<false, false>, grid, dim3(kThreads), 0, stream, p);
 }
 
 // (where rows are not aligned, up to 3 columns of the first CTA lie before the row)

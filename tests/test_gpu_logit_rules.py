@@ -132,6 +132,11 @@ CASES = {
     "biases only": dict(ns=[6], vocab=5000, penalties=False, bias=600, grammar=False),
     "grammar only": dict(ns=[6], vocab=2048, penalties=False, indexed=False),
     "no rule": dict(ns=[6], vocab=2048, penalties=False, grammar=False),
+    "a row each": dict(ns=[1] * 5, vocab=2049, bf16=True, bias=30),
+    "a row each, fp32": dict(ns=[1, 1, 1], vocab=4096, bias=3, indexed=False),
+    # enough segments of enough sequences for one CTA to run over all rows of a sequence, more than it stages masks for
+    "whole sequences": dict(ns=[40, 1, 2, 33, 70] + [5] * 15, vocab=32001, bf16=True, bias=5),
+    "whole sequences, aligned rows": dict(ns=[70, 36, 1, 2] + [5] * 16, vocab=32000, bias=5),
 }
 
 
@@ -225,6 +230,21 @@ def test_bad_input_is_reported_and_skipped(env):
                 del c.bias[1][2]
                 r, m = c.want()
                 check(got, r, m, c.repeats)
+    finally:
+        ctx.close()
+
+
+def test_a_row_each_needs_a_row_each(env):
+    """As many rows as sequences, but another sequence has both: reported, and no other row written."""
+    H, vfy = env
+    case = Case(5, ns=[1, 1], vocab=512)
+    ctx = vfy.vfy_create(4, 1, 64, max_seqs=2, max_queries_per_seq=4, device=0)
+    try:
+        for cu in ([0, 0, 2], [0, 2, 2], [0, 2, 3], [1, 2, 3]):
+            out = torch.full((4, 512), 77.0, device="cuda")
+            vfy.vfy_process_logits(ctx, case.logits(), 512, H.dev_i32(cu), 2, case.rules(vfy, H), out, 2)
+            assert vfy.vfy_get_status(ctx) == vfy.VFY_EDEVICE_INPUT
+            assert (out[2:] == 77).all()
     finally:
         ctx.close()
 
