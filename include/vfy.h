@@ -115,7 +115,8 @@ VFY_API unsigned long long vfy_launch_count(const vfy_ctx* ctx);
  * 8 resident chunks stream two chunks per pipeline step and finish in a second, combine kernel.
  * Otherwise a layer whose splits per (sequence, KV head) fit one thread-block cluster (at most
  * 16, and what one GPC holds) merges them inside its attention kernel; more splits also go
- * through the combine kernel. */
+ * through the combine kernel. With full_splits = 0 a tree block's full layer may go to a kernel of CTA
+ * pairs instead, which cuts the batch's work evenly and has no splits. */
 VFY_API vfy_status vfy_set_splits(vfy_ctx* ctx, int full_splits, int swa_splits);
 
 /* CTAs that copy each chunk in the vfy_page_in calls enqueued afterwards: 1 to 4, or 0 (the
@@ -422,7 +423,7 @@ VFY_API vfy_status vfy_attend_swa_tree(vfy_ctx* ctx, const uint16_t* q, const in
 typedef struct vfy_logit_rules {
   const int32_t* counts;      /* [B][vocab] as kept by vfy_count_tokens: bit 31 = the prompt holds the
                                  token, bits 0-30 = how often it was generated. NULL: no penalties */
-  const float* repetition;    /* [B] with counts: > 0, 1 = none */
+  const float* repetition;    /* [B] with counts: 1 = none; in [2^-100, 2^100] (its reciprocal is used) */
   const float* frequency;     /* [B] with counts: 0 = none */
   const float* presence;      /* [B] with counts: 0 = none */
   const int32_t* drafts;      /* with counts: the block's drafted tokens, packed as in vfy_accept; NULL
@@ -513,7 +514,8 @@ VFY_API vfy_status vfy_accept_tree(vfy_ctx* ctx, const float* logits, int vocab,
  *  host_k, host_v, k_pool, v_pool   HOST arrays of num_layers pointers: each layer's chunk store
  *                (pinned host or device memory) and pool
  * A row is read from its chunk's pool slot if it has one, else from the store, and written to the
- * store and to the pool slot of the chunk it moves to, if that has one.
+ * store and to the pool slot of the chunk it moves to, if that has one. The layers move at the same time:
+ * pools that overlap one another, or stores that do, give VFY_EINVAL.
  * Device errors: a path entry outside [j, q_b), a length outside [0, q_b), a chunk outside the store:
  * skipped, VFY_EDEVICE_INPUT.
  */
@@ -526,7 +528,7 @@ VFY_API vfy_status vfy_compact_full(vfy_ctx* ctx, const int32_t* path, const int
 /*
  * vfy_compact_swa -- the same for window layers: ring slot (p0 + path[j] + ring_offset[b]) mod ring_len
  * to slot (p0 + j + ring_offset[b]) mod ring_len. k_ring, v_ring: HOST arrays of num_layers pointers
- * to bf16 [B][Hkv][ring_len][d].
+ * to bf16 [B][Hkv][ring_len][d], which lie apart (else VFY_EINVAL).
  */
 VFY_API vfy_status vfy_compact_swa(vfy_ctx* ctx, const int32_t* path, const int32_t* accepted_len,
                                    const int32_t* cu_q, const int32_t* seq_len, const int32_t* ring_offset,

@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kThreads) accept_tree_kernel(const AcceptTreeP
   const int n4 = (v1 - a0) >> 2;
   unsigned long long best = scan_words<kThreads, kUnroll>(reinterpret_cast<const float4*>(src + a0), n4, a0);
   if (threadIdx.x < 8) {                           // at most 3 entries before and 3 after the words
-    const int i = threadIdx.x < 4 ? v0 + static_cast<int>(threadIdx.x) : a0 + 4 * n4 + static_cast<int>(threadIdx.x) - 4;
+    const int x = static_cast<int>(threadIdx.x), i = x < 4 ? v0 + x : a0 + 4 * n4 + x - 4;
     if (threadIdx.x < 4 ? i < a0 : i < v1) best = umax64(best, pack(src[i], i));
   }
 #pragma unroll

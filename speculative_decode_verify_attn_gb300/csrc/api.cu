@@ -410,7 +410,7 @@ static int tree_capacity(const vfy_config& c) { return std::min(c.max_queries_pe
 // Does a tree's full layer go to CTA pairs of 256 rows (and how many), or to the linear block's kernel (0)?
 // Pairs balance whatever the lengths, and halve the K/V traffic of two row tiles; each run pays about 8 us for its
 // start and the merge. us of one layer, 4 KV heads, the linear kernel with its best splits against pairs:
-//   two row tiles (64 nodes, G = 4), 64 chunks: 1 sequence 15.0 / 18.7, 4: 26.9 / 27.8, 8: 43.9 / 34.8, 16: 46.5 / 52.2;
+//   two row tiles (64 nodes, G = 4), 64 chunks: 1 sequence 15.0 / 18.7, 4: 26.9 / 27.8, 8: 43.9 / 34.8, 16: 46.5 / 52;
 //   256 chunks: 1: 22.5 / 23.8, 4: 55 / 44, 16: 159 / 106; 1024 chunks: 1: 47 / 43, 8: 263 / 173;
 //   one row tile (17 nodes), 256 chunks: 2 sequences 19.6 / 25.9, 4: 31.5 / 36.9, 8: 54 / 57, 16: 97 / 87;
 //   1024 chunks: 2: 57 / 64, 4: 97 / 97, 8: 168 / 167, 8 ragged (750 chunks at most): 105 / 104, and 130 with one
@@ -446,8 +446,8 @@ static vfy_status attend_common(vfy_ctx* ctx, bool ring, const uint16_t* q, cons
         // One wave of CTAs: us with one wave against four of 17 nodes over 64 chunks, 4 sequences 15.3 / 31.9, 8
         // 22.3 / 36.4, 16 35.3 / 47.1. Long contexts of a batch (here with d = 64; with d = 128 CTA pairs take them)
         // get two waves, for sequences of different lengths: 8 of equal lengths over 256 chunks 25.0 / 27.3.
-        const int items = hkv * num_seqs * row_tiles;
-        splits = ctx->num_sms * (num_seqs >= 4 && max_res >= 256 ? 2 : 1) / items;
+        const long long items = static_cast<long long>(hkv) * num_seqs * row_tiles;
+        splits = static_cast<int>(ctx->num_sms * (num_seqs >= 4 && max_res >= 256 ? 2 : 1) / items);
         // Short contexts: as many as one cluster merges in the attention kernel, which with 16 splits finds too few
         // GPCs (64 chunks, 8 items: 12 splits 11.9 us, 16 20.6, 19 and the combine 13.5).
         if (max_res <= 64) splits = std::min(splits, 12);
@@ -802,6 +802,14 @@ vfy_status vfy_accept_tree(vfy_ctx* ctx, const float* logits, int vocab, const i
   return VFY_OK;
 }
 
+// Do buffers of `bytes` bytes from these addresses on lie apart? (The layers of a call move their rows at the same time.)
+static bool apart(uintptr_t* at, int n, uint64_t bytes) {
+  std::sort(at, at + n);
+  for (int i = 1; i < n; ++i)
+    if (at[i] - at[i - 1] < bytes) return false;
+  return true;
+}
+
 // The arguments that both compactions share.
 static void compact_params(const vfy_ctx* ctx, const int32_t* path, const int32_t* accepted_len,
                            const int32_t* cu_q, const int32_t* seq_len, int num_layers, int num_seqs,
@@ -830,10 +838,18 @@ vfy_status vfy_compact_full(vfy_ctx* ctx, const int32_t* path, const int32_t* ac
   VFY_REQUIRE(num_layers >= 1 && num_layers <= VFY_MAX_COMPACT_LAYERS);
   VFY_REQUIRE(num_host_chunks >= 1 && num_host_chunks <= INT_MAX && num_slots >= 1);
   VFY_REQUIRE(num_seqs >= 1 && num_seqs <= ctx->cfg.max_seqs);
+  uintptr_t pools[2 * VFY_MAX_COMPACT_LAYERS], stores[2 * VFY_MAX_COMPACT_LAYERS];
   for (int l = 0; l < num_layers; ++l) {
     VFY_REQUIRE(host_k[l] != nullptr && host_v[l] != nullptr && k_pool[l] != nullptr && v_pool[l] != nullptr);
     VFY_REQUIRE(aligned16(host_k[l]) && aligned16(host_v[l]) && aligned16(k_pool[l]) && aligned16(v_pool[l]));
+    pools[2 * l] = reinterpret_cast<uintptr_t>(k_pool[l]);
+    pools[2 * l + 1] = reinterpret_cast<uintptr_t>(v_pool[l]);
+    stores[2 * l] = reinterpret_cast<uintptr_t>(host_k[l]);
+    stores[2 * l + 1] = reinterpret_cast<uintptr_t>(host_v[l]);
   }
+  const uint64_t chunk_bytes = 2ull * ctx->cfg.num_kv_heads * kChunk * ctx->cfg.head_dim;
+  VFY_REQUIRE(apart(pools, 2 * num_layers, chunk_bytes * num_slots));
+  VFY_REQUIRE(apart(stores, 2 * num_layers, chunk_bytes * static_cast<uint64_t>(num_host_chunks)));
   DeviceGuard guard(ctx->device);
   if (!guard.ok) return VFY_ECUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -864,9 +880,14 @@ vfy_status vfy_compact_swa(vfy_ctx* ctx, const int32_t* path, const int32_t* acc
   VFY_REQUIRE(ring_offset != nullptr && k_ring != nullptr && v_ring != nullptr);
   VFY_REQUIRE(num_layers >= 1 && num_layers <= VFY_MAX_COMPACT_LAYERS);
   VFY_REQUIRE(num_seqs >= 1 && num_seqs <= ctx->cfg.max_seqs);
+  uintptr_t rings[2 * VFY_MAX_COMPACT_LAYERS];
   for (int l = 0; l < num_layers; ++l) {
     VFY_REQUIRE(k_ring[l] != nullptr && v_ring[l] != nullptr && aligned16(k_ring[l]) && aligned16(v_ring[l]));
+    rings[2 * l] = reinterpret_cast<uintptr_t>(k_ring[l]);
+    rings[2 * l + 1] = reinterpret_cast<uintptr_t>(v_ring[l]);
   }
+  const uint64_t ring_bytes = 2ull * ctx->cfg.num_kv_heads * ctx->cfg.ring_len * ctx->cfg.head_dim;
+  VFY_REQUIRE(apart(rings, 2 * num_layers, ring_bytes * num_seqs));
   DeviceGuard guard(ctx->device);
   if (!guard.ok) return VFY_ECUDA;
   vfy::CompactParams p = {};

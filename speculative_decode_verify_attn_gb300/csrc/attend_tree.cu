@@ -91,7 +91,7 @@ __device__ __forceinline__ Seq load_seq(const AttnParams& p, int b) {
   s.r0 = p.cu_res[b];
   s.nres = max(0, p.cu_res[b + 1] - s.r0);
   s.nq = q1 - s.q0;
-  const bool bad = s.nq < 0 || s.nq > p.max_q || s.L < s.nq || s.q0 < 0;
+  const bool bad = s.nq < 0 || s.nq > p.max_q || s.L < s.nq || s.q0 < 0 || s.q0 > p.token_cap - s.nq;
   if (bad) s.nq = 0;
   s.rows = s.nq * p.group;
   s.pairs = (s.rows + kPairRows - 1) / kPairRows;
@@ -101,7 +101,7 @@ __device__ __forceinline__ Seq load_seq(const AttnParams& p, int b) {
 }
 __device__ __forceinline__ bool seq_is_bad(const AttnParams& p, int b) {
   const int q0 = p.cu_q[b], nq = p.cu_q[b + 1] - q0;
-  return nq < 0 || nq > p.max_q || p.seq_len[b] < nq || q0 < 0;
+  return nq < 0 || nq > p.max_q || p.seq_len[b] < nq || q0 < 0 || q0 > p.token_cap - nq;
 }
 
 // Tiles of all sequences, and where tile x lies: its sequence and the tiles before that sequence. Every
@@ -419,7 +419,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int kk = 0; kk < HD / 16; ++kk)
               mma_ss_pair(tbase + kColS + sb * kKeys,
                           qdesc + static_cast<uint64_t>(((kk >> 2) * kQBoxBytes + (kk & 3) * 32) >> 4),
-                          kdesc + static_cast<uint64_t>((ks * kStageBytes + (kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4),
+                          kdesc + ((ks * kStageBytes + (kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4),
                           idesc, kk > 0 ? 1u : 0u);
             mma_commit_pair(&bars->s_full[sb]);
             mma_commit_pair(&bars->k_empty[ks]);
@@ -439,7 +439,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int kk = 0; kk < kChunk / 16; ++kk)
                 mma_ts_pair(tbase + kColO + c * 128, tbase + kColS + sb * kKeys + c * kChunk + kk * 8,
-                            vdesc + static_cast<uint64_t>((vs * kStageBytes + c * kBoxBytes + 16 * kk * 128) >> 4), idesc,
+                            vdesc + ((vs * kStageBytes + c * kBoxBytes + 16 * kk * 128) >> 4), idesc,
                             (j > 0 || kk > 0) ? 1u : 0u);
             mma_commit_pair(&bars->s_free[sb]);
             mma_commit_pair(&bars->v_empty[vs]);

@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, ONE ? 7 : 5) process_logits_kernel(c
   const bool grammar = r.grammar != nullptr;
   int v0 = seg0 - shift_of(i0) + 4 * tid;
   uint32_t valid = valid_of(v0);
-  if (i0 < n) load_rows(i0, min((n - i0 + step - 1) / step, kMaskRows), v0, valid);     // on their way while the rules are read
+  if (i0 < n) load_rows(i0, min((n - i0 + step - 1) / step, kMaskRows), v0, valid);     // while the rules are read
 
   // ---- the sequence's rules for these columns ----
   const bool penalties = r.counts != nullptr;
@@ -321,7 +321,9 @@ __global__ void __launch_bounds__(kThreads, ONE ? 7 : 5) process_logits_kernel(c
     const float c = static_cast<float>(word & 0x7fffffff);
     return bias - (word != 0 ? fmaf(freq, c, c > 0.f ? pres : 0.f) : 0.f);
   };
-  auto rule = [&](float v, bool seen, float add) { return rules ? fmaf(v, seen ? (v > 0.f ? inv : rep) : 1.f, add) : v; };
+  auto rule = [&](float v, bool seen, float add) {
+    return rules ? fmaf(v, seen ? (v > 0.f ? inv : rep) : 1.f, add) : v;
+  };
   // ---- the rows, kMaskRows of this CTA's at a time (row j: i = i0 + j step) ----
   for (int j0 = 0; j0 < my_rows; j0 += kMaskRows) {
     const int j1 = min(my_rows, j0 + kMaskRows);
@@ -388,32 +390,35 @@ __global__ void __launch_bounds__(kThreads, ONE ? 7 : 5) process_logits_kernel(c
   }
 
   // ---- the drafted columns, a thread per (row, column): the row's own path counts too ----
-  for (int x = tid; x < my_rows * num_drafted; x += kThreads) {
-    const int i = i0 + (x / num_drafted) * step, c = s_drafted[x % num_drafted];
-    const long long row = r0 + static_cast<long long>(i);
-    const int v = seg0 - 3 + c;
-    const int shift = shift_of(i);
-    if (v < seg0 - shift || v >= seg0 - shift + kSeg) continue;      // another CTA's column in this row
-    const uint32_t* set = s_set[s_entry[c]];
-    int extra = 0;
-#pragma unroll
-    for (int w = 0; w < kWords; ++w) {
-      const uint32_t path = r.tree_mask != nullptr ? __ldg(r.tree_mask + row * kWords + w)
-                            : i >= 32 * w + 31     ? 0xffffffffu     // a chain's path: nodes 0 .. i
-                            : i < 32 * w           ? 0u
-                                                   : (2u << (i - 32 * w)) - 1u;
-      extra += __popc(path & set[w]);
+  if constexpr (!ONE) {
+    for (int x = tid; x < my_rows * num_drafted; x += kThreads) {
+      const int i = i0 + (x / num_drafted) * step, c = s_drafted[x % num_drafted];
+      const long long row = r0 + static_cast<long long>(i);
+      const int v = seg0 - 3 + c;
+      const int shift = shift_of(i);
+      if (v < seg0 - shift || v >= seg0 - shift + kSeg) continue;      // another CTA's column in this row
+      const uint32_t* set = s_set[s_entry[c]];
+      int extra = 0;
+  #pragma unroll
+      for (int w = 0; w < kWords; ++w) {
+        const uint32_t path = r.tree_mask != nullptr ? __ldg(r.tree_mask + row * kWords + w)
+                              : i >= 32 * w + 31     ? 0xffffffffu     // a chain's path: nodes 0 .. i
+                              : i < 32 * w           ? 0u
+                                                     : (2u << (i - 32 * w)) - 1u;
+        extra += __popc(path & set[w]);
+      }
+      const int32_t word = s_count[c] + extra;                         // bit 31 stays: counts stay below 2^31
+      const long long at = row * p.stride + v;
+      const float in = BF16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p.logits)[at]) << 16)
+                            : static_cast<const float*>(p.logits)[at];
+      float y = rule(in, word != 0, addend(word, s_bias[c]));
+      if (s_mask[i] >= 0) {
+        const uint64_t word0 = static_cast<uint64_t>(static_cast<uint32_t>(s_mask[i])) * words_per_mask;
+        const uint32_t bits = __ldg(r.grammar + word0 + (v >> 5));
+        if (!((bits >> (v & 31)) & 1u)) y = -INFINITY;
+      }
+      p.out[row * p.vocab + v] = y;
     }
-    const int32_t word = s_count[c] + extra;                         // bit 31 stays: counts stay below 2^31
-    const long long at = row * p.stride + v;
-    const float in = BF16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p.logits)[at]) << 16)
-                          : static_cast<const float*>(p.logits)[at];
-    float y = rule(in, word != 0, addend(word, s_bias[c]));
-    if (s_mask[i] >= 0) {
-      const uint32_t bits = __ldg(r.grammar + static_cast<uint64_t>(static_cast<uint32_t>(s_mask[i])) * words_per_mask + (v >> 5));
-      if (!((bits >> (v & 31)) & 1u)) y = -INFINITY;
-    }
-    p.out[row * p.vocab + v] = y;
   }
 }
 
@@ -459,19 +464,20 @@ __global__ void __launch_bounds__(kHistThreads) rebuild_counts_kernel(const Coun
   pdl_wait();
   const int b = blockIdx.y;
   const int t0 = p.cu_tokens[b];
-  int t1 = p.cu_tokens[b + 1];
+  int t1 = p.cu_tokens[b + 1];                           // (up to 2^31 - 1: places past it are unsigned)
   bool bad = false;
   if (t0 < 0 || t1 < t0 || t1 > p.max_tokens) {        // its counts become zero
     bad = true;
-    t1 = t0;
+    t1 = t0 < 0 ? 0 : t0;
   }
   __syncthreads();
-  for (int base = t0; base < t1; base += kHistThreads * kHistAhead) {
+  const unsigned end = static_cast<unsigned>(t1);
+  for (unsigned base = static_cast<unsigned>(t0); base < end; base += kHistThreads * kHistAhead) {
     int tok[kHistAhead];
 #pragma unroll
     for (int u = 0; u < kHistAhead; ++u) {
-      const int at = base + u * kHistThreads + static_cast<int>(threadIdx.x);
-      tok[u] = at < t1 ? __ldg(p.tokens + at) : -1;
+      const unsigned at = base + u * kHistThreads + threadIdx.x;
+      tok[u] = at < end ? __ldg(p.tokens + at) : -1;
     }
 #pragma unroll
     for (int u = 0; u < kHistAhead; ++u) {

@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(kNodes) tree_plan_kernel(const TreePlanParams 
   const int r0 = p.cu_q[b];
   const int nq = p.cu_q[b + 1] - r0;
   const int i = threadIdx.x;
-  if (nq < 0 || nq > p.max_q || r0 < 0 || r0 + nq > p.token_cap) {
+  if (nq < 0 || nq > p.max_q || r0 < 0 || r0 > p.token_cap - nq) {
     if (i == 0) atomicOr(p.err, kErrDeviceInput);
     return;
   }
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactP
   const int L = p.seq_len[b];
   int n = p.accepted[b];
   const bool report = blockIdx.x == 0 && layer == 0;
-  if (nq < 1 || nq > p.max_q || q0 < 0 || q0 + nq > p.token_cap || L < nq || n < 0 || n >= nq) {
+  if (nq < 1 || nq > p.max_q || q0 < 0 || q0 > p.token_cap - nq || L < nq || n < 0 || n >= nq) {
     if (report && threadIdx.x == 0) atomicOr(p.err, kErrDeviceInput);
     return;
   }

@@ -345,6 +345,7 @@ class LogitRules:
             0 if grammar is None else grammar.shape[0])
         self.vocab = None if counts is None else counts.shape[-1]
         self.mask_words = None if grammar is None else grammar.shape[-1]
+        self.devices = {t.get_device() for t in self.tensors if t is not None}
 
 
 def vfy_tree_plan(ctx: Context, parents, cu_q, depth, tree_mask, num_seqs: int, stream=None):
@@ -358,9 +359,10 @@ def vfy_attend_full_tree(ctx: Context, q, cu_q, tree_mask, k_pool, v_pool, num_s
                          stream=None):
     _check(lib().vfy_attend_full_tree(
         ctx.handle, _ptr(ctx, q, BF16, "q"), _ptr(ctx, cu_q, I32, "cu_q"), _ptr(ctx, tree_mask, U32, "tree_mask"),
-        _ptr(ctx, k_pool, BF16, "k_pool"), _ptr(ctx, v_pool, BF16, "v_pool"), num_slots, _ptr(ctx, resident_ids, I32, "resident_ids"),
-        _ptr(ctx, resident_slots, I32, "resident_slots"), _ptr(ctx, cu_resident, I32, "cu_resident"), max_resident_per_seq,
-        _ptr(ctx, seq_len, I32, "seq_len"), _ptr(ctx, out, BF16, "out"), _ptr(ctx, lse, F32, "lse"), num_seqs, _raw_stream(ctx, stream)),
+        _ptr(ctx, k_pool, BF16, "k_pool"), _ptr(ctx, v_pool, BF16, "v_pool"), num_slots,
+        _ptr(ctx, resident_ids, I32, "resident_ids"), _ptr(ctx, resident_slots, I32, "resident_slots"),
+        _ptr(ctx, cu_resident, I32, "cu_resident"), max_resident_per_seq, _ptr(ctx, seq_len, I32, "seq_len"),
+        _ptr(ctx, out, BF16, "out"), _ptr(ctx, lse, F32, "lse"), num_seqs, _raw_stream(ctx, stream)),
         "vfy_attend_full_tree")
 
 
@@ -384,25 +386,30 @@ def vfy_process_logits(ctx: Context, logits, vocab: int, cu_rows, max_rows: int,
         raise ValueError("logits must be [rows][vocab] with contiguous rows")
     if rules.vocab not in (None, vocab) or rules.mask_words not in (None, (vocab + 31) // 32):
         raise ValueError("the rules' counts or grammar masks are for another vocabulary")
+    if not rules.devices <= {ctx.device}:
+        raise ValueError(f"the rules are on cuda:{sorted(rules.devices)}, the context on cuda:{ctx.device}")
     _check(lib().vfy_process_logits(
         ctx.handle, logits.data_ptr(), 1 if logits.dtype == torch.bfloat16 else 0,
-        logits.stride(0) if logits.shape[0] > 1 else logits.shape[1], vocab, _ptr(ctx, cu_rows, I32, "cu_rows"), max_rows,
-        ctypes.byref(rules.struct), _ptr(ctx, out, F32, "out"), num_seqs, _raw_stream(ctx, stream)), "vfy_process_logits")
+        logits.stride(0) if logits.shape[0] > 1 else logits.shape[1], vocab, _ptr(ctx, cu_rows, I32, "cu_rows"),
+        max_rows, ctypes.byref(rules.struct), _ptr(ctx, out, F32, "out"), num_seqs, _raw_stream(ctx, stream)),
+        "vfy_process_logits")
 
 
 def vfy_count_tokens(ctx: Context, tokens, cu_tokens, max_tokens: int, counts, vocab: int, num_seqs: int, *,
                      as_prompt: bool = False, reset: bool = False, stream=None):
     _check(lib().vfy_count_tokens(
-        ctx.handle, _ptr(ctx, tokens, I32, "tokens"), _ptr(ctx, cu_tokens, I32, "cu_tokens"), max_tokens, 1 if as_prompt else 0,
-        1 if reset else 0, _ptr(ctx, counts, I32, "counts"), vocab, num_seqs, _raw_stream(ctx, stream)), "vfy_count_tokens")
+        ctx.handle, _ptr(ctx, tokens, I32, "tokens"), _ptr(ctx, cu_tokens, I32, "cu_tokens"), max_tokens,
+        1 if as_prompt else 0, 1 if reset else 0, _ptr(ctx, counts, I32, "counts"), vocab, num_seqs,
+        _raw_stream(ctx, stream)), "vfy_count_tokens")
 
 
 def vfy_accept_tree(ctx: Context, logits, vocab: int, drafts, parents, cu_rows, max_rows: int, accepted_len, path,
                     bonus, committed, num_seqs: int, stream=None):
     _check(lib().vfy_accept_tree(
-        ctx.handle, _ptr(ctx, logits, F32, "logits"), vocab, _ptr(ctx, drafts, I32, "drafts"), _ptr(ctx, parents, I32, "parents"),
-        _ptr(ctx, cu_rows, I32, "cu_rows"), max_rows, _ptr(ctx, accepted_len, I32, "accepted_len"), _ptr(ctx, path, I32, "path"),
-        _ptr(ctx, bonus, I32, "bonus"), _ptr(ctx, committed, I32, "committed"), num_seqs, _raw_stream(ctx, stream)), "vfy_accept_tree")
+        ctx.handle, _ptr(ctx, logits, F32, "logits"), vocab, _ptr(ctx, drafts, I32, "drafts"),
+        _ptr(ctx, parents, I32, "parents"), _ptr(ctx, cu_rows, I32, "cu_rows"), max_rows,
+        _ptr(ctx, accepted_len, I32, "accepted_len"), _ptr(ctx, path, I32, "path"), _ptr(ctx, bonus, I32, "bonus"),
+        _ptr(ctx, committed, I32, "committed"), num_seqs, _raw_stream(ctx, stream)), "vfy_accept_tree")
 
 
 def _layers(ctx, tensors, name: str, host_allowed: bool = False):
@@ -412,12 +419,8 @@ def _layers(ctx, tensors, name: str, host_allowed: bool = False):
     if (set(map(torch.Tensor.get_device, tensors)) <= {ctx.device} and all(map(torch.Tensor.is_contiguous, tensors))
             and set(map(_DTYPE, tensors)) <= set(BF16)):
         return array.array("Q", map(torch.Tensor.data_ptr, tensors))
-    return array.array("Q", [(_host(t, BF16, name) if host_allowed and not t.is_cuda
-                              else _c(_ptr(ctx, t, BF16, name))).value or 0 for t in tensors])
-
-
-def _c(address):
-    return ctypes.c_void_p(address)
+    return array.array("Q", [_host(t, BF16, name).value or 0 if host_allowed and not t.is_cuda
+                             else _ptr(ctx, t, BF16, name) for t in tensors])
 
 
 def vfy_compact_full(ctx: Context, path, accepted_len, cu_q, seq_len, cu_chunks, slot_of_chunk, host_k, host_v,
@@ -428,9 +431,10 @@ def vfy_compact_full(ctx: Context, path, accepted_len, cu_q, seq_len, cu_chunks,
     hk, hv = _layers(ctx, host_k, "host_k", True), _layers(ctx, host_v, "host_v", True)
     kp, vp = _layers(ctx, k_pool, "k_pool"), _layers(ctx, v_pool, "v_pool")
     _check(lib().vfy_compact_full(
-        ctx.handle, _ptr(ctx, path, I32, "path"), _ptr(ctx, accepted_len, I32, "accepted_len"), _ptr(ctx, cu_q, I32, "cu_q"),
-        _ptr(ctx, seq_len, I32, "seq_len"), _ptr(ctx, cu_chunks, I32, "cu_chunks"), _ptr(ctx, slot_of_chunk, I32, "slot_of_chunk"),
-        len(k_pool), hk.buffer_info()[0], hv.buffer_info()[0], num_host_chunks, kp.buffer_info()[0],
+        ctx.handle, _ptr(ctx, path, I32, "path"), _ptr(ctx, accepted_len, I32, "accepted_len"),
+        _ptr(ctx, cu_q, I32, "cu_q"), _ptr(ctx, seq_len, I32, "seq_len"), _ptr(ctx, cu_chunks, I32, "cu_chunks"),
+        _ptr(ctx, slot_of_chunk, I32, "slot_of_chunk"), len(k_pool), hk.buffer_info()[0], hv.buffer_info()[0],
+        num_host_chunks, kp.buffer_info()[0],
         vp.buffer_info()[0], num_slots, num_seqs, _raw_stream(ctx, stream)),
         "vfy_compact_full")
 
@@ -442,6 +446,7 @@ def vfy_compact_swa(ctx: Context, path, accepted_len, cu_q, seq_len, ring_offset
         raise ValueError("k_ring and v_ring must have one tensor per layer")
     kr, vr = _layers(ctx, k_ring, "k_ring"), _layers(ctx, v_ring, "v_ring")
     _check(lib().vfy_compact_swa(
-        ctx.handle, _ptr(ctx, path, I32, "path"), _ptr(ctx, accepted_len, I32, "accepted_len"), _ptr(ctx, cu_q, I32, "cu_q"),
-        _ptr(ctx, seq_len, I32, "seq_len"), _ptr(ctx, ring_offset, I32, "ring_offset"), len(k_ring),
+        ctx.handle, _ptr(ctx, path, I32, "path"), _ptr(ctx, accepted_len, I32, "accepted_len"),
+        _ptr(ctx, cu_q, I32, "cu_q"), _ptr(ctx, seq_len, I32, "seq_len"), _ptr(ctx, ring_offset, I32, "ring_offset"),
+        len(k_ring),
         kr.buffer_info()[0], vr.buffer_info()[0], num_seqs, _raw_stream(ctx, stream)), "vfy_compact_swa")

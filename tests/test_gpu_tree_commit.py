@@ -288,6 +288,64 @@ def test_refusals(env):
         ctx.close()
 
 
+def test_layers_that_overlap_are_refused(env):
+    """The layers of one call move their rows at the same time: a buffer in two places would be moved twice."""
+    H, vfy = env
+    ctx = vfy.vfy_create(4, 4, 128, max_seqs=2, max_queries_per_seq=8, device=0)
+    i = torch.zeros(64, dtype=torch.int32, device="cuda")
+    ring = torch.zeros((8, 1, 4, 2048, 128), dtype=torch.bfloat16, device="cuda")
+    pool = torch.zeros((8, 32, 4, C, 128), dtype=torch.bfloat16, device="cuda")
+    host = torch.zeros((8, 32, 4, C, 128), dtype=torch.bfloat16).pin_memory()
+    half = ring.view(-1)[ring[0].numel() // 2:][:ring[0].numel()]          # the end of ring 0, the start of ring 1
+    try:
+        def swa(ks, vs):
+            vfy.vfy_compact_swa(ctx, i, i, H.dev_i32([0, 1]), H.dev_i32([9]), i, ks, vs, 1)
+
+        def full(hk, hv, ks, vs):
+            vfy.vfy_compact_full(ctx, i, i, H.dev_i32([0, 1]), H.dev_i32([9]), i, i, hk, hv, 32, ks, vs, 32, 1)
+        bad = [lambda: swa([ring[0]], [ring[0]]), lambda: swa([ring[0], ring[0]], [ring[1], ring[2]]),
+               lambda: swa([ring[0]], [half]),
+               lambda: full([host[0]], [host[1]], [pool[0]], [pool[0]]),
+               lambda: full([host[0]], [host[0]], [pool[0]], [pool[1]]),
+               lambda: full([host[0], host[1]], [host[2], host[3]], [pool[0], pool[1]], [pool[2], pool[0]])]
+        for f in bad:
+            before = vfy.vfy_launch_count(ctx)
+            with pytest.raises(vfy.VfyError) as e:
+                f()
+            assert e.value.status == vfy.VFY_EINVAL and vfy.vfy_launch_count(ctx) == before
+        swa([ring[k] for k in range(0, 8, 2)], [ring[k] for k in range(1, 8, 2)])
+        full(list(host[:4]), list(host[4:]), list(pool[:4]), list(pool[4:]))
+        full(list(pool[:2]), list(pool[2:4]), list(pool[4:6]), list(pool[6:]))      # a store on the device
+        assert vfy.vfy_get_status(ctx) == vfy.VFY_OK
+    finally:
+        ctx.close()
+
+
+def test_offsets_past_the_capacity_are_reported(env):
+    """Row offsets that only a 32-bit sum would let pass, and ones past the host bound: reported, nothing written."""
+    H, vfy = env
+    ctx = vfy.vfy_create(4, 1, 128, max_seqs=1, max_queries_per_seq=64, device=0)
+    big = 2 ** 31 - 8
+    out = torch.full((64, 8), 77, dtype=torch.int32, device="cuda")
+    ring = torch.full((2, 1, 1, 2048, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    o = torch.full((64, 4, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    q, pool = torch.zeros_like(o), torch.zeros((256, 1, C, 128), dtype=torch.bfloat16, device="cuda")
+    ids = H.dev_i32(range(256))
+    try:
+        for cu in ([big, big + 15 - 2 ** 32], [60, 75]):
+            cu = H.dev_i32(cu)
+            vfy.vfy_tree_plan(ctx, out[:, 0].contiguous(), cu, out[:, 1].contiguous(), out, 1)
+            assert vfy.vfy_get_status(ctx) == vfy.VFY_EDEVICE_INPUT
+            vfy.vfy_compact_swa(ctx, ids, H.dev_i32([2]), cu, H.dev_i32([100]), H.dev_i32([0]), [ring[0]], [ring[1]], 1)
+            assert vfy.vfy_get_status(ctx) == vfy.VFY_EDEVICE_INPUT
+            vfy.vfy_attend_full_tree(ctx, q, cu, out, pool, pool, 256, ids, ids, H.dev_i32([0, 256]), 256,
+                                     H.dev_i32([256 * C]), o, None, 1)       # two row tiles: CTA pairs
+            assert vfy.vfy_get_status(ctx) == vfy.VFY_EDEVICE_INPUT
+        assert (out == 77).all() and (ring == 3).all() and (o == 3).all()
+    finally:
+        ctx.close()
+
+
 def test_a_whole_tree_step_in_one_graph(env):
     """Two sequences, one full and one window layer, three steps of one captured graph: every step's trees,
     drafts and K/V are new, the cache, the lengths and the counts are those the last step left. The
