@@ -48,14 +48,19 @@ def words_dev(sets_or_words):
     return torch.from_numpy(np.ascontiguousarray(w).view(np.int32)).cuda()
 
 
-def attend_full(H, vfy, ctx, q, cu, words, kp, vp, ids, slots, cu_res, lens, stream=None):
+# A host bound on the resident chunks above the longest list: what decides that a block of several row tiles
+# (or a batch) goes to the kernel of CTA pairs.
+LOOSE = pytest.mark.parametrize("bound", [0, 256])
+
+
+def attend_full(H, vfy, ctx, q, cu, words, kp, vp, ids, slots, cu_res, lens, stream=None, bound=0):
     qd = H.dev_bf16(q)
     out = torch.full_like(qd, 7.0)
     lse = torch.full(qd.shape[:2], 7.0, device="cuda")
     k, v = H.dev_bf16(kp), H.dev_bf16(vp)
     vfy.vfy_attend_full_tree(ctx, qd, H.dev_i32(cu), words_dev(words), k, v, k.shape[0], H.dev_i32(ids),
-                             H.dev_i32(slots), H.dev_i32(cu_res), int(np.diff(cu_res).max()), H.dev_i32(lens), out, lse,
-                             len(cu) - 1, stream)
+                             H.dev_i32(slots), H.dev_i32(cu_res), max(bound, int(np.diff(cu_res).max())), H.dev_i32(lens),
+                             out, lse, len(cu) - 1, stream)
     torch.cuda.synchronize()
     return H.bits_of(out), lse.cpu().numpy()
 
@@ -94,10 +99,11 @@ def pool_case(rng, hq, hkv, d, n, L, keep=None):
 LAYOUTS = [(16, 4, 128), (4, 1, 64), (8, 8, 128), (32, 4, 128), (16, 2, 64)]
 
 
+@LOOSE
 @pytest.mark.parametrize("heads", LAYOUTS)
 @pytest.mark.parametrize("n,L", [(1, 1), (1, 64), (2, 65), (17, 17), (17, 1000), (33, 97), (64, 128), (65, 700),
                                  (255, 300), (256, 513)])
-def test_full_layer(env, heads, n, L):
+def test_full_layer(env, heads, n, L, bound):
     H, vfy = env
     hq, hkv, d = heads
     rng = np.random.default_rng([n, L, hq])
@@ -106,16 +112,17 @@ def test_full_layer(env, heads, n, L):
     ref = T.attend_tree_full_seq(q, sets, kp, vp, ids, slots, L)
     ctx = vfy.vfy_create(hq, hkv, d, max_queries_per_seq=n, ring_len=4096, device=0)
     try:
-        got = attend_full(H, vfy, ctx, q, [0, n], sets, kp, vp, ids, slots, [0, len(ids)], [L])
+        got = attend_full(H, vfy, ctx, q, [0, n], sets, kp, vp, ids, slots, [0, len(ids)], [L], bound=bound)
         check(*got, *ref, f"{heads} {n} {L}")
         assert vfy.vfy_get_status(ctx) == vfy.VFY_OK
     finally:
         ctx.close()
 
 
+@LOOSE
 @pytest.mark.parametrize("splits", [0, 1, 2, 3, 7, 16, 40])
 @pytest.mark.parametrize("n", [9, 47, 64])
-def test_full_layer_split_settings(env, splits, n):
+def test_full_layer_split_settings(env, splits, n, bound):
     H, vfy = env
     rng = np.random.default_rng([splits, n])
     L, keep = 9000, 41
@@ -125,7 +132,8 @@ def test_full_layer_split_settings(env, splits, n):
     ctx = vfy.vfy_create(16, 4, 128, max_queries_per_seq=64, device=0)
     try:
         vfy.vfy_set_splits(ctx, splits, 0)
-        check(*attend_full(H, vfy, ctx, q, [0, n], sets, kp, vp, ids, slots, [0, len(ids)], [L]), *ref, f"{splits} {n}")
+        got = attend_full(H, vfy, ctx, q, [0, n], sets, kp, vp, ids, slots, [0, len(ids)], [L], bound=bound)
+        check(*got, *ref, f"{splits} {n}")
         assert vfy.vfy_get_status(ctx) == vfy.VFY_OK
     finally:
         ctx.close()
@@ -156,7 +164,8 @@ def test_window_layer(env, heads, splits, n, L, phi):
         ctx.close()
 
 
-def test_any_mask_is_taken(env):
+@LOOSE
+def test_any_mask_is_taken(env, bound):
     """Masks that no plan makes: later nodes, no node at all (with and without a prefix), bits past
     the block (ignored)."""
     H, vfy = env
@@ -172,7 +181,7 @@ def test_any_mask_is_taken(env):
         ref = T.attend_tree_full_seq(q, sets, kp, vp, ids, slots, L)
         ctx = vfy.vfy_create(16, 4, 128, max_queries_per_seq=n, device=0)
         try:
-            got, lse = attend_full(H, vfy, ctx, q, [0, n], sets, kp, vp, ids, slots, [0, len(ids)], [L])
+            got, lse = attend_full(H, vfy, ctx, q, [0, n], sets, kp, vp, ids, slots, [0, len(ids)], [L], bound=bound)
             check(got, lse, *ref, f"L {L}")
             if L == n:
                 assert not got[3].any() and np.isneginf(lse[3]).all() and np.isneginf(lse[7]).all()
@@ -180,8 +189,9 @@ def test_any_mask_is_taken(env):
             ctx.close()
 
 
+@LOOSE
 @pytest.mark.parametrize("splits", [0, 2, 5])
-def test_ragged_batch(env, splits):
+def test_ragged_batch(env, splits, bound):
     """Sequences of 1 to 200 nodes, one of them empty, in both layers; rows behind the last sequence
     are left as they were."""
     H, vfy = env
@@ -212,7 +222,7 @@ def test_ragged_batch(env, splits):
     ctx = vfy.vfy_create(hq, hkv, d, max_seqs=len(ns), max_queries_per_seq=200, device=0)
     try:
         vfy.vfy_set_splits(ctx, splits, splits)
-        got, lse = attend_full(H, vfy, ctx, q, cu, words, kp, vp, ids, slots, cu_res, Ls)
+        got, lse = attend_full(H, vfy, ctx, q, cu, words, kp, vp, ids, slots, cu_res, Ls, bound=bound)
         gotw, lsew = attend_swa(H, vfy, ctx, q, cu, words, depth, kr, vr, phi, Ls)
         assert vfy.vfy_get_status(ctx) == vfy.VFY_OK
         for b, (sets, i_b, s_b, parents) in enumerate(seqs):
@@ -350,6 +360,34 @@ def test_attention_reports_bad_input(env):
         ctx.close()
 
 
+def test_pairs_report_bad_input(env):
+    """The same in a context of two row tiles, in the kernel of CTA pairs; a bad sequence leaves the others alone."""
+    H, vfy = env
+    rng = np.random.default_rng(52)
+    n, L = 60, 2000
+    q, kp, vp, ids, slots = pool_case(rng, 16, 4, 128, n, L)
+    sets = T.ancestors(synth.random_tree(rng, n).tolist())
+    ctx = vfy.vfy_create(16, 4, 128, max_seqs=2, max_queries_per_seq=60, device=0)
+    both = [0, len(ids), 2 * len(ids)]
+    two = [np.concatenate([x, x]) for x in (q, T.mask_words(sets), ids, slots)]
+    try:
+        bad = slots.copy()
+        bad[3] = 99
+        got, lse = attend_full(H, vfy, ctx, q, [0, n], sets, kp, vp, ids, bad, [0, len(ids)], [L], bound=256)
+        assert vfy.vfy_get_status(ctx) == vfy.VFY_EDEVICE_INPUT
+        keep = np.arange(len(ids)) != 3
+        ref = T.attend_tree_full_seq(q, sets, kp, vp, ids[keep], slots[keep], L)
+        check(got, lse, *ref, "bad slot")
+        ref = T.attend_tree_full_seq(q, sets, kp, vp, ids, slots, L)
+        for cu, lens in (([0, n, 2 * n], [L, n - 1]), ([0, n, 2 * n + 1], [L, L])):    # too short; 61 nodes of 60
+            got, lse = attend_full(H, vfy, ctx, two[0], cu, two[1], kp, vp, two[2], two[3], both, lens, bound=256)
+            assert vfy.vfy_get_status(ctx) == vfy.VFY_EDEVICE_INPUT
+            check(got[:n], lse[:n], *ref, "the good sequence")
+            assert (lse[n:] == 7).all()
+    finally:
+        ctx.close()
+
+
 def test_refusals(env):
     """Host-side checks: nothing is launched."""
     H, vfy = env
@@ -377,7 +415,8 @@ def test_refusals(env):
         small.close()
 
 
-def test_plan_and_attention_in_one_graph(env):
+@LOOSE
+def test_plan_and_attention_in_one_graph(env, bound):
     """Captured on a side stream with stable metadata on: every replay attends by the tree that
     stands in `parents` then."""
     H, vfy = env
@@ -398,7 +437,8 @@ def test_plan_and_attention_in_one_graph(env):
 
         def step():
             vfy.vfy_tree_plan(ctx, parents, cu, depth, mask, 1)
-            vfy.vfy_attend_full_tree(ctx, qd, cu, mask, kd, vd, kd.shape[0], idd, sd, cr, len(ids), lens, out, lse, 1)
+            vfy.vfy_attend_full_tree(ctx, qd, cu, mask, kd, vd, kd.shape[0], idd, sd, cr, max(bound, len(ids)), lens, out,
+                                     lse, 1)
         with torch.cuda.stream(stream):
             parents.copy_(H.dev_i32(synth.random_tree(rng, n)))
             step()
@@ -419,8 +459,9 @@ def test_plan_and_attention_in_one_graph(env):
         ctx.close()
 
 
+@LOOSE
 @pytest.mark.parametrize("n", [9, 64])
-def test_wait_timeout_is_reported_and_recovered(env, n):
+def test_wait_timeout_is_reported_and_recovered(env, n, bound):
     H, vfy = env
     rng = np.random.default_rng(70)
     L = 9000
@@ -429,10 +470,10 @@ def test_wait_timeout_is_reported_and_recovered(env, n):
     ctx = vfy.vfy_create(16, 4, 128, max_queries_per_seq=n, device=0)
     try:
         vfy.vfy_test_wait_timeout(ctx, 2000)
-        attend_full(H, vfy, ctx, q, [0, n], sets, kp, vp, ids, slots, [0, len(ids)], [L])
+        attend_full(H, vfy, ctx, q, [0, n], sets, kp, vp, ids, slots, [0, len(ids)], [L], bound=bound)
         assert vfy.vfy_get_status(ctx) == vfy.VFY_EDEVICE_TIMEOUT
         vfy.vfy_test_wait_timeout(ctx, 0)
-        got = attend_full(H, vfy, ctx, q, [0, n], sets, kp, vp, ids, slots, [0, len(ids)], [L])
+        got = attend_full(H, vfy, ctx, q, [0, n], sets, kp, vp, ids, slots, [0, len(ids)], [L], bound=bound)
         assert vfy.vfy_get_status(ctx) == vfy.VFY_OK
         check(*got, *T.attend_tree_full_seq(q, sets, kp, vp, ids, slots, L), "after a timeout")
     finally:
