@@ -20,6 +20,17 @@
 // bf16 over the first half of each chunk's) has two buffers, so S of the next tile runs during the softmax of
 // this one. An MMA costs its issuer 50 to 110 cycles beside busy softmax warps, more than the pair's 64 in the
 // tensor pipes: hence two issuers (one for everything: 2360 cycles a tile, in the linear block's kernel).
+//
+// GB300, 4 KV heads, G = 4, one layer with its merge: 64 nodes over 4096 resident chunks (537 MB) 117 us, 4.6 TB/s
+// and 1.17 PFLOP/s of full row tiles (the linear block's kernel with its best splits 146); 8 ragged sequences of 48
+// nodes up to 48K 116 us (147). A tile of 128 keys takes a pair 2060 cycles, of which its MMAs fill 1024 and the
+// copies at the HBM rate would 1400: the bound is the loop P(n) -> PV(n) -> S(n + 2) -> P(n + 2), two tiles long, and
+// beside it the softmax warps' own time (1160 cycles of a tile are arithmetic, some 800 are barrier operations; a wait
+// for a barrier that is complete already takes 150 cycles on an idle SM, 300 here). Measured and not kept, the same
+// stream in us: P in columns of its own, so that S(n + 1) runs as soon as S(n) is loaded: 128 with one S buffer, 140
+// with two and one O for both warpgroups (which then have to agree on each row's maximum, tile by tile); one lane
+// waiting for its warp: 131; the issuing warp converged, with predicated MMAs: 119; the geometry read ahead or without
+// a barrier: 119.
 #include <cuda_bf16.h>
 
 #include "ptx.cuh"

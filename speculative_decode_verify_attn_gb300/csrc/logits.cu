@@ -12,11 +12,11 @@
 // Bound by bytes in flight: the first rows' logits are loaded before the rules, the mask words of 32 rows
 // at a time go through shared memory (one wait instead of one per batch), four rows of eight columns are
 // in flight per thread. GB300: 17 x 131072 fp32 8.5 us (5.3 with no rule; the bytes alone 2.7); 339 rows x
-// 100003 bf16 of 16 sequences 66.8 us (3.2 TB/s; 56 us with a vocabulary of 100000, whose rows all start alike,
-// and 41 without rules). Loading eight neighbouring columns per thread (half-sector stores), per-thread mask
+// 100003 bf16 of 16 sequences 60.8 us (3.5 TB/s; 52 us with a vocabulary of 100000, whose rows all start alike,
+// 39.5 of it without rules; half of the issue slots are taken). Loading eight neighbouring columns per thread (half-sector stores), per-thread mask
 // loads, and columns past a row's end in a loop of their own each cost 15 to 40 us of the batch; registers for
-// six CTAs per SM instead of five 10 us, and refilling each row's registers as soon as it is done, instead of
-// four rows at a time, 20.
+// six CTAs per SM instead of five 10 us, refilling each row's registers as soon as it is done, instead of four
+// rows at a time, 20, loading a batch ahead 5.
 #include "ptx.cuh"
 #include "vfy_internal.cuh"
 
@@ -100,8 +100,21 @@ __global__ void __launch_bounds__(kThreads, ONE ? 7 : 5) process_logits_kernel(c
   pdl_launch_dependents();
   pdl_wait();
   const vfy_logit_rules& r = p.rules;
-  const int b = blockIdx.y;
   const int tid = static_cast<int>(threadIdx.x);
+  int b = blockIdx.y;
+  if (!ONE && p.num_seqs > 1 && p.num_seqs <= 32) {
+    // The sequences with the most rows go first, so that the last CTAs are short ones (the ragged batch 67.4 -> 60.8 us,
+    // one of equal lengths 95.2 -> 96.1).
+    const int lane = tid & 31;
+    const bool have = lane < p.num_seqs;
+    const int rows = have ? p.cu_rows[lane + 1] - p.cu_rows[lane] : 0;
+    int rank = 0;
+    for (int i = 0; i < p.num_seqs; ++i) {
+      const int other = __shfl_sync(0xffffffffu, rows, i);
+      rank += other > rows || (other == rows && i < lane) ? 1 : 0;
+    }
+    b = __ffs(__ballot_sync(0xffffffffu, have && rank == b)) - 1;
+  }
   const int r0 = p.cu_rows[b];
   const int n = p.cu_rows[b + 1] - r0;
   const bool report = blockIdx.x == 0 && blockIdx.z == 0;

@@ -12,7 +12,8 @@
 // never reads a word that it has overwritten, and no two threads share a word. One CTA covers one
 // (sequence, layer, part of the words); the rows' places come from one pass over the path, kept in
 // shared memory. The call moves a few KB per layer and is latency-bound: path -> chunk -> slot ->
-// row, three dependent loads (two for rings), then the copy.
+// row, three dependent loads (two for rings), then the copy: 30 rings 2.7 us, 10 pools of 8 sequences 4.0 us (in a
+// graph; the host needs 21 and 23 us to name that many layers from Python).
 #include "ptx.cuh"
 #include "vfy_internal.cuh"
 

@@ -134,6 +134,7 @@ CASES = {
     "no rule": dict(ns=[6], vocab=2048, penalties=False, grammar=False),
     "a row each": dict(ns=[1] * 5, vocab=2049, bf16=True, bias=30),
     "a row each, fp32": dict(ns=[1, 1, 1], vocab=4096, bias=3, indexed=False),
+    "more sequences than a warp has lanes": dict(ns=[2, 1, 3] * 13, vocab=300, bias=2),
     # enough segments of enough sequences for one CTA to run over all rows of a sequence, more than it stages masks for
     "whole sequences": dict(ns=[40, 1, 2, 33, 70] + [5] * 15, vocab=32001, bf16=True, bias=5),
     "whole sequences, aligned rows": dict(ns=[70, 36, 1, 2] + [5] * 16, vocab=32000, bias=5),
