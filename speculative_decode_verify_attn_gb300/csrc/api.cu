@@ -411,10 +411,10 @@ static int tree_capacity(const vfy_config& c) { return std::min(c.max_queries_pe
 // Pairs balance whatever the lengths, and halve the K/V traffic of two row tiles; each run pays about 8 us for its
 // start and the merge. us of one layer, 4 KV heads, the linear kernel with its best splits against pairs:
 //   two row tiles (64 nodes, G = 4), 64 chunks: 1 sequence 15.0 / 18.7, 4: 26.9 / 27.8, 8: 43.9 / 34.8, 16: 46.5 / 52;
-//   256 chunks: 1: 22.5 / 23.8, 4: 55 / 44, 16: 159 / 106; 1024 chunks: 1: 47 / 43, 8: 263 / 173;
-//   one row tile (17 nodes), 256 chunks: 2 sequences 19.6 / 25.9, 4: 31.5 / 36.9, 8: 54 / 57, 16: 97 / 87;
-//   1024 chunks: 2: 57 / 64, 4: 97 / 97, 8: 168 / 167, 8 ragged (750 chunks at most): 105 / 104, and 130 with one
-//   wave of splits, which is the best for equal lengths.
+//   256 chunks: 1: 22.5 / 22.1, 4: 55 / 41, 16: 160 / 99; 1024 chunks: 8: 264 / 162;
+//   one row tile (17 nodes), 256 chunks: 2 sequences 19.6 / 25.9, 4: 31.6 / 35.5, 8: 54 / 54, 16: 97 / 83;
+//   1024 chunks: 2: 57 / 64, 8: 168 / 157, 8 ragged (750 chunks at most): 105 / 98, and 130 with one wave of splits,
+//   which is the best for equal lengths.
 static int tree_pairs(const vfy_ctx* ctx, int row_tiles, int num_seqs, int max_res) {
   if (ctx->full_splits != 0 || ctx->cfg.head_dim != 128) return 0;
   const bool take = row_tiles > 1 ? max_res >= 128 : num_seqs >= 4 && max_res >= 256;

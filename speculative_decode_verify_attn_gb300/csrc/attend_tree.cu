@@ -21,16 +21,18 @@
 // this one. An MMA costs its issuer 50 to 110 cycles beside busy softmax warps, more than the pair's 64 in the
 // tensor pipes: hence two issuers (one for everything: 2360 cycles a tile, in the linear block's kernel).
 //
-// GB300, 4 KV heads, G = 4, one layer with its merge: 64 nodes over 4096 resident chunks (537 MB) 117 us, 4.6 TB/s
-// and 1.17 PFLOP/s of full row tiles (the linear block's kernel with its best splits 146); 8 ragged sequences of 48
-// nodes up to 48K 116 us (147). A tile of 128 keys takes a pair 2060 cycles, of which its MMAs fill 1024 and the
+// GB300, 4 KV heads, G = 4, one layer with its merge: 64 nodes over 4096 resident chunks (537 MB) 109 us, 4.9 TB/s
+// and 1.26 PFLOP/s of full row tiles (the linear block's kernel with its best splits 146); 8 ragged sequences of 48
+// nodes up to 48K 110 us (147). A tile of 128 keys takes a pair some 1850 cycles, of which its MMAs fill 1024 and the
 // copies at the HBM rate would 1400: the bound is the loop P(n) -> PV(n) -> S(n + 2) -> P(n + 2), two tiles long, and
-// beside it the softmax warps' own time (1160 cycles of a tile are arithmetic, some 800 are barrier operations; a wait
-// for a barrier that is complete already takes 150 cycles on an idle SM, 300 here). Measured and not kept, the same
-// stream in us: P in columns of its own, so that S(n + 1) runs as soon as S(n) is loaded: 128 with one S buffer, 140
-// with two and one O for both warpgroups (which then have to agree on each row's maximum, tile by tile); one lane
-// waiting for its warp: 131; the issuing warp converged, with predicated MMAs: 119; the geometry read ahead or without
-// a barrier: 119.
+// beside it the softmax warps' own time (1160 cycles of a tile are arithmetic, the rest barrier operations; a wait for
+// a phase that is complete takes 145 cycles on an idle SM, 70 when it is tested first, both twice that here). So every
+// wait and index in that loop counts: rings of 4 stages (6 of K, or 5 of V, cost 4 to 6 us for the division), V's wait
+// before S's, where the warp waits anyway (3 us), tests first, no wait for the geometry of most tiles (1 us each).
+// Measured and not kept, against 117 then: P in columns of its own, so that S(n + 1) runs as soon as S(n) is loaded,
+// 128 with one S buffer, 140 with two and one O for both warpgroups (which then have to agree on each row's maximum);
+// one lane waiting for its warp 131; spinning without suspending 116; the issuing warp converged, with predicated
+// MMAs, 119.
 #include <cuda_bf16.h>
 
 #include "ptx.cuh"
@@ -60,9 +62,9 @@ constexpr int kBoxBytes = kChunk * 128;               // 64 rows of 128 bytes
 constexpr int kQBoxBytes = kMaxRows * 128;
 constexpr int kQBytes = 2 * kQBoxBytes;
 constexpr int kStageBytes = 2 * kBoxBytes;            // of K (two column boxes) and of V (two chunks)
-constexpr int kKStages = 6, kVStages = 4;
+constexpr int kKStages = 4, kVStages = 4;
 constexpr int kBarOffset = kQBytes + (kKStages + kVStages) * kStageBytes;
-constexpr int kBarBytes = 3072;
+constexpr int kBarBytes = 4096;
 constexpr int kSmemBytes = kBarOffset + kBarBytes + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 static_assert(kKStages + 4 <= kGeo, "geometry ring");
@@ -73,7 +75,6 @@ struct Bars {
   uint64_t geo_full[kGeo];
   uint64_t s_full[2], s_free[2];   // [tile parity]: S is there; its P has been read (leading CTA)
   uint64_t p_full[2];          // in the leading CTA, [tile parity]: P is written in both CTAs (and V has landed)
-  uint64_t o_full;             // one phase per tile, after its PV
   uint64_t o_done;             // one phase per segment, after its last PV
   uint64_t q_ready;            // in the leading CTA, one phase per segment: Q is staged in both CTAs
   uint64_t half_ready[4];      // [lane quarter], one phase per segment: both warpgroups' (m, l)
@@ -83,7 +84,7 @@ struct Bars {
   int abort;
   int base[kGeo][2];           // position of each chunk's first key
   int valid[kGeo][2];
-  int plain[kGeo];             // every key lies before the block: all rows attend all of them
+  uint32_t plain_tag[kGeo];    // tile + 1 if every key of the tile lies before the block: all rows attend them
   int zero[kGeo];              // some key lies outside the sequence: its V row is to be zeroed
   float xm[2][128], xl[2][128];
 };
@@ -289,12 +290,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&bars->p_full[i], 16);                                   // all softmax warps, both CTAs
       mbar_init(&bars->drain[i], 1);
     }
-    mbar_init(&bars->o_full, 1);
     mbar_init(&bars->o_done, 1);
     mbar_init(&bars->q_ready, 16);                                       // all softmax warps, both CTAs
-    for (int i = 0; i < 4; ++i) mbar_init(&bars->half_ready[i], 64);
-    mbar_init(&bars->o_read, 256);
+    for (int i = 0; i < 4; ++i) mbar_init(&bars->half_ready[i], 2);
+    mbar_init(&bars->o_read, 8);
     mbar_init(&bars->never, 1);
+    for (int i = 0; i < kGeo; ++i) bars->plain_tag[i] = 0;
     bars->abort = 0;
     fence_mbar_init();
     prefetch_tmap(&tmap_k);
@@ -363,8 +364,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             zero = zero || !c[i].valid || c[i].base + kChunk > w.s.L;
             present += c[i].present ? 1 : 0;
           }
-          bars->plain[g] = plain ? 1 : 0;
           bars->zero[g] = zero ? 1 : 0;
+          if (plain) *reinterpret_cast<volatile uint32_t*>(&bars->plain_tag[g]) = n + 1;
           mbar_arrive(&bars->geo_full[g]);
           // a chunk the sequence lacks is not loaded: the mask and the zeroed V rows cover its stale rows
           if (rank == 0) mbar_arrive_expect_tx(&bars->k_full[st], present * kStageBytes);
@@ -422,8 +423,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ok = mbar_wait(&bars->q_ready, segs++ & 1, abort, p.err);
           for (int j = 0; ok && j < w.nt; ++j, ++n) {
             const uint32_t ks = n % kKStages, sb = n & 1;
-            if (n >= 2) ok = mbar_wait(&bars->s_free[sb], ((n >> 1) - 1) & 1, abort, p.err);
-            ok = ok && mbar_wait(&bars->k_full[ks], (n / kKStages) & 1, abort, p.err);
+            ok = mbar_wait_tested(&bars->k_full[ks], (n / kKStages) & 1, abort, p.err);
+            if (n >= 2)
+              ok = ok && mbar_wait_tested(&bars->s_free[sb], ((n >> 1) - 1) & 1, abort, p.err);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
@@ -442,7 +444,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (; ok && w.more(); w.next(p)) {
           for (int j = 0; j < w.nt; ++j, ++n) {
             const uint32_t vs = n % kVStages, sb = n & 1;
-            ok = mbar_wait(&bars->p_full[sb], (n >> 1) & 1, abort, p.err);
+            ok = mbar_wait_tested(&bars->p_full[sb], (n >> 1) & 1, abort, p.err);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
@@ -454,7 +456,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             (j > 0 || kk > 0) ? 1u : 0u);
             mma_commit_pair(&bars->s_free[sb]);
             mma_commit_pair(&bars->v_empty[vs]);
-            mma_commit_pair(&bars->o_full);
             if (j == w.nt - 1) mma_commit_pair(&bars->o_done);
           }
         }
@@ -472,6 +473,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int r = rank * kMaxRows + lr;                // row of the pair
     const uint32_t lane_base = tbase + (static_cast<uint32_t>(quarter * 32) << 16);
     const unsigned ug = static_cast<unsigned>(p.group);
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait_tested(bar, parity, abort, p.err)) != 0;
+    };
     uint32_t n = 0, segs = 0;                          // tiles and segments so far
     // Q of a segment's rows -> shared memory, in the 128-byte swizzle: warpgroup g takes columns [64 g, 64 g + 64)
     auto stage_q = [&](const Walk& v) {
@@ -502,15 +506,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int j = 0; j < w.nt; ++j, ++n) {
         const int gs = n % kGeo;
         const uint32_t sb = n & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars->geo_full[gs], (n / kGeo) & 1, abort, p.err));
-        if (!ok) break;
-        const bool plain = bars->plain[gs] != 0, zero = bars->zero[gs] != 0;
-        uint32_t keep[2] = {0u, 0u};
-        if (!plain && bars->valid[gs][g] != 0 && rv) {
-          keep[0] = keep32(words, bars->base[gs][g], p0, w.s.L);
-          keep[1] = keep32(words, bars->base[gs][g] + 32, p0, w.s.L);
+        // One warp waits for the tile's V in this CTA before it arrives for P, so the issuer's wait for P covers V too.
+        if (warp == kVRelayWarp) {
+          ok = wait(&bars->v_full[n % kVStages], (n / kVStages) & 1);
+          if (!ok) break;
         }
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[sb], (n >> 1) & 1, abort, p.err));
+        // (a tag that names the tile says all there is to know: most tiles need no wait for their geometry)
+        const bool plain =
+            __all_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(&bars->plain_tag[gs]) == n + 1) != 0;
+        bool zero = false;
+        uint32_t keep[2] = {0u, 0u};
+        if (!plain) {
+          ok = wait(&bars->geo_full[gs], (n / kGeo) & 1);
+          if (!ok) break;
+          zero = bars->zero[gs] != 0;
+          if (bars->valid[gs][g] != 0 && rv) {
+            keep[0] = keep32(words, bars->base[gs][g], p0, w.s.L);
+            keep[1] = keep32(words, bars->base[gs][g] + 32, p0, w.s.L);
+          }
+        }
+        ok = wait(&bars->s_full[sb], (n >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
         if (active) {
@@ -542,10 +557,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             m_ref = m_tile;
           }
           if (__any_sync(0xffffffffu, scale_o)) {
-            // O holds the tiles before this one: PV of the last one is waited for. (S of this tile was issued after
-            // PV of the tile before that, and PV of this tile needs its P: the barrier is in that phase or the one
-            // after.)
-            ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_full, (n - 1) & 1, abort, p.err));
+            // O holds the tiles before this one: PV of the last one is waited for, which gives its V stage back. (PV of
+            // this tile needs its P, so the stage's barrier is in that phase or the one after.)
+            const uint32_t last = n - 1;
+            ok = wait(&bars->v_empty[last % kVStages], (last / kVStages) & 1);
             if (!ok) break;
             tc_fence_after();
             const float a = scale_o ? alpha : 1.f;
@@ -576,22 +591,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tmem_st32(ts, pk);
         }
         tc_fence_before();
-        // One warp's arrival waits for the tile's V in this CTA, so the issuer's wait for P covers V too.
-        if (zero || warp == kVRelayWarp) {
+        if (zero) {
+          // V rows of keys outside the sequence may hold anything, and 0 * NaN is NaN on the tensor core: two threads
+          // zero a key's row (its CTA's columns) before P.
           const int sv = n % kVStages;
-          ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_full[sv], (n / kVStages) & 1, abort, p.err));
+          ok = wait(&bars->v_full[sv], (n / kVStages) & 1);
           if (!ok) break;
-          if (zero) {
-            // V rows of keys outside the sequence may hold anything, and 0 * NaN is NaN on the tensor core: two
-            // threads zero a key's row (its CTA's columns) before P.
-            const int key = lr >> 1;
-            if (bars->valid[gs][g] == 0 || bars->base[gs][g] + key >= w.s.L) {
-              uint8_t* row = sV + sv * kStageBytes + g * kBoxBytes + key * 128 + (lr & 1) * 64;
+          const int key = lr >> 1;
+          if (bars->valid[gs][g] == 0 || bars->base[gs][g] + key >= w.s.L) {
+            uint8_t* row = sV + sv * kStageBytes + g * kBoxBytes + key * 128 + (lr & 1) * 64;
 #pragma unroll
-              for (int x = 0; x < 4; ++x) *reinterpret_cast<uint4*>(row + x * 16) = make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();
+            for (int x = 0; x < 4; ++x) *reinterpret_cast<uint4*>(row + x * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
+          fence_proxy_async_smem();
         }
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(leader(&bars->p_full[sb]));
@@ -600,14 +612,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // ---- the segment's end: merge the two warpgroups' halves ----
       bars->xm[g][lr] = l > 0.f ? m_ref : -INFINITY;
       bars->xl[g][lr] = l;
-      mbar_arrive(&bars->half_ready[quarter]);
-      ok = __all_sync(0xffffffffu, mbar_wait(&bars->half_ready[quarter], segs & 1, abort, p.err));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->half_ready[quarter]);
+      ok = wait(&bars->half_ready[quarter], segs & 1);
       if (!ok) break;
       const float m0 = bars->xm[0][lr], m1 = bars->xm[1][lr], l0 = bars->xl[0][lr], l1 = bars->xl[1][lr];
       const float m_row = fmaxf(m0, m1);
       const float w0 = l0 > 0.f ? ex2_approx(m0 - m_row) : 0.f, w1 = l1 > 0.f ? ex2_approx(m1 - m_row) : 0.f;
       const float l_row = w0 * l0 + w1 * l1;
-      ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done, segs & 1, abort, p.err));
+      ok = wait(&bars->o_done, segs & 1);
       if (!ok) break;
       tc_fence_after();
       // every S of the segment has read Q: the next one's first S may run during this one's epilogue
@@ -662,8 +675,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       // the next segment's PV writes O, and its end (m, l): both warpgroups are done with both
       tc_fence_before();
-      mbar_arrive(&bars->o_read);
-      ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_read, segs & 1, abort, p.err));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->o_read);
+      ok = wait(&bars->o_read, segs & 1);
       if (!ok) break;
       ++segs;
       w = nx;
