@@ -344,16 +344,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int j = 0; j < w.nt; ++j, ++n) {
           const int st = n % kKStages;
+          Chunk c[2] = {chunk_at(p, w, j, 0), chunk_at(p, w, j, 1)};       // (read while the stage empties)
           if (n >= kKStages) ok = mbar_wait(&bars->k_empty[st], (n / kKStages - 1) & 1, abort, p.err);
           if (!ok) break;
           const int g = n % kGeo;
           const int p0 = w.s.L - w.s.nq;
-          Chunk c[2];
           int present = 0;
           bool plain = true, zero = false;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            c[i] = chunk_at(p, w, j, i);
             if (c[i].present && !c[i].valid && !reported) {
               atomicOr(p.err, kErrDeviceInput);
               reported = true;
@@ -390,15 +389,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (; ok && w.more(); w.next(p)) {
         for (int j = 0; j < w.nt; ++j, ++n) {
           const int st = n % kVStages;
+          Chunk c[2] = {chunk_at(p, w, j, 0), chunk_at(p, w, j, 1)};
           if (n >= kVStages) ok = mbar_wait(&bars->v_empty[st], (n / kVStages - 1) & 1, abort, p.err);
           if (!ok) break;
-          Chunk c[2];
-          int present = 0;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            c[i] = chunk_at(p, w, j, i);
-            present += c[i].present ? 1 : 0;
-          }
+          const int present = (c[0].present ? 1 : 0) + (c[1].present ? 1 : 0);
           mbar_arrive_expect_tx(&bars->v_full[st], present * kBoxBytes);
 #pragma unroll
           for (int i = 0; i < 2; ++i)
@@ -586,9 +580,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const __nv_bfloat162 h2 = __floats2bfloat162_rn(x.x, x.y);
             pk[e] = *reinterpret_cast<const uint32_t*>(&h2);
           }
+          tmem_st32(ts, pk);
           const float2 sum = add_f32x2(add_f32x2(ps[0], ps[1]), add_f32x2(ps[2], ps[3]));
           l += sum.x + sum.y;
-          tmem_st32(ts, pk);
         }
         tc_fence_before();
         if (zero) {
