@@ -326,6 +326,7 @@ def vfy_accept_static(logits, vocab: int, drafts, cu_rows, num_seqs: int, max_ro
 
 U32 = (torch.int32, torch.uint32)       # row and grammar masks: 32-bit words
 _DTYPE = operator.attrgetter("dtype")
+_BF16_SET = frozenset(BF16)
 
 
 class LogitRules:
@@ -417,15 +418,19 @@ def vfy_accept_tree(ctx: Context, logits, vocab: int, drafts, parents, cu_rows, 
         _ptr(ctx, committed, I32, "committed"), num_seqs, _raw_stream(ctx, stream)), "vfy_accept_tree")
 
 
-def _layers(ctx, tensors, name: str, host_allowed: bool = False):
-    """A host array of the layers' addresses (keep it while the call runs)."""
-    tensors = list(tensors)
+def _layers(ctx, name: str, *lists, host_allowed: bool = False):
+    """One host array of the addresses of all layers of these lists (keep it while the call runs), and the address of
+    each list's part."""
+    tensors = [t for ts in lists for t in ts]
     # (in C where possible: a call names up to 256 tensors)
     if (set(map(_DEVICE_OF, tensors)) <= {ctx.device} and all(map(_CONTIGUOUS, tensors))
-            and set(map(_DTYPE, tensors)) <= set(BF16)):
-        return array.array("Q", map(_DATA_PTR, tensors))
-    return array.array("Q", [_host(t, BF16, name).value or 0 if host_allowed and not t.is_cuda
-                             else _ptr(ctx, t, BF16, name) for t in tensors])
+            and set(map(_DTYPE, tensors)) <= _BF16_SET):
+        found = array.array("Q", map(_DATA_PTR, tensors))
+    else:
+        found = array.array("Q", [_host(t, BF16, name).value or 0 if host_allowed and not t.is_cuda
+                                  else _ptr(ctx, t, BF16, name) for t in tensors])
+    at, step = found.buffer_info()[0], 8 * len(lists[0])
+    return found, *(at + step * i for i in range(len(lists)))
 
 
 def vfy_compact_full(ctx: Context, path, accepted_len, cu_q, seq_len, cu_chunks, slot_of_chunk, host_k, host_v,
@@ -433,15 +438,13 @@ def vfy_compact_full(ctx: Context, path, accepted_len, cu_q, seq_len, cu_chunks,
     """host_k, host_v, k_pool, v_pool: one tensor per layer, in lists of one length."""
     if not len(host_k) == len(host_v) == len(k_pool) == len(v_pool):
         raise ValueError("host_k, host_v, k_pool and v_pool must have one tensor per layer")
-    hk, hv = _layers(ctx, host_k, "host_k", True), _layers(ctx, host_v, "host_v", True)
-    kp, vp = _layers(ctx, k_pool, "k_pool"), _layers(ctx, v_pool, "v_pool")
+    stores, hk, hv = _layers(ctx, "host_k, host_v", host_k, host_v, host_allowed=True)
+    pools, kp, vp = _layers(ctx, "k_pool, v_pool", k_pool, v_pool)
     _check(lib().vfy_compact_full(
         ctx.handle, _ptr(ctx, path, I32, "path"), _ptr(ctx, accepted_len, I32, "accepted_len"),
         _ptr(ctx, cu_q, I32, "cu_q"), _ptr(ctx, seq_len, I32, "seq_len"), _ptr(ctx, cu_chunks, I32, "cu_chunks"),
-        _ptr(ctx, slot_of_chunk, I32, "slot_of_chunk"), len(k_pool), hk.buffer_info()[0], hv.buffer_info()[0],
-        num_host_chunks, kp.buffer_info()[0],
-        vp.buffer_info()[0], num_slots, num_seqs, _raw_stream(ctx, stream)),
-        "vfy_compact_full")
+        _ptr(ctx, slot_of_chunk, I32, "slot_of_chunk"), len(k_pool), hk, hv, num_host_chunks, kp, vp, num_slots,
+        num_seqs, _raw_stream(ctx, stream)), "vfy_compact_full")
 
 
 def vfy_compact_swa(ctx: Context, path, accepted_len, cu_q, seq_len, ring_offset, k_ring, v_ring, num_seqs: int,
@@ -449,9 +452,8 @@ def vfy_compact_swa(ctx: Context, path, accepted_len, cu_q, seq_len, ring_offset
     """k_ring, v_ring: one tensor per layer, in lists of one length."""
     if len(k_ring) != len(v_ring):
         raise ValueError("k_ring and v_ring must have one tensor per layer")
-    kr, vr = _layers(ctx, k_ring, "k_ring"), _layers(ctx, v_ring, "v_ring")
+    rings, kr, vr = _layers(ctx, "k_ring, v_ring", k_ring, v_ring)
     _check(lib().vfy_compact_swa(
         ctx.handle, _ptr(ctx, path, I32, "path"), _ptr(ctx, accepted_len, I32, "accepted_len"),
         _ptr(ctx, cu_q, I32, "cu_q"), _ptr(ctx, seq_len, I32, "seq_len"), _ptr(ctx, ring_offset, I32, "ring_offset"),
-        len(k_ring),
-        kr.buffer_info()[0], vr.buffer_info()[0], num_seqs, _raw_stream(ctx, stream)), "vfy_compact_swa")
+        len(k_ring), kr, vr, num_seqs, _raw_stream(ctx, stream)), "vfy_compact_swa")
