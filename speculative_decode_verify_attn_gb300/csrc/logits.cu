@@ -11,9 +11,10 @@
 // Every entry is read and written by one thread, so the call may work in place.
 // Bound by bytes in flight: the first rows' logits are loaded before the rules, the mask words of 32 rows
 // at a time go through shared memory (one wait instead of one per batch), four rows of eight columns are
-// in flight per thread. GB300: 17 x 131072 fp32 8.5 us (5.3 with no rule; the bytes alone 2.7); 339 rows x
-// 100003 bf16 of 16 sequences 60.8 us (3.5 TB/s; 52 us with a vocabulary of 100000, whose rows all start alike,
-// 39.5 of it without rules; half of the issue slots are taken). Loading eight neighbouring columns per thread (half-sector stores), per-thread mask
+// in flight per thread, and by issue slots, half of which a batch takes: masks are staged from each row's first
+// column on, so that a thread's bits are two shifts, and entries take the steps of the rules in use only. GB300: 17 x
+// 131072 fp32 8.2 us (the bytes alone 2.7); 339 rows x 100003 bf16 of 16 sequences 55.7 us (3.8 TB/s; 47.7 us with a
+// vocabulary of 100000, whose rows all start alike, 37.8 of it without rules). Loading eight neighbouring columns per thread (half-sector stores), per-thread mask
 // loads, and columns past a row's end in a loop of their own each cost 15 to 40 us of the batch; registers for
 // six CTAs per SM instead of five 10 us, refilling each row's registers as soon as it is done, instead of four
 // rows at a time, 20, loading a batch ahead 5.
@@ -31,7 +32,7 @@ constexpr int kWords = VFY_TREE_WORDS;
 constexpr int kNone = 0x7fffffff;
 constexpr int kSpan = kSeg + 3;                // columns a CTA keeps
 constexpr int kBiasAhead = 4;                  // bias entries in flight per thread
-constexpr int kSpanWords = kSeg / 32 + 2;      // words that kSpan columns touch
+constexpr int kSegWords = kSeg / 32;           // words of a row's staged mask
 constexpr int kSpanIters = (kSpan + kThreads - 1) / kThreads;
 
 // A thread's eight columns of one row, as they were loaded: rows in flight cost registers. Bit e of `valid`:
@@ -86,7 +87,7 @@ template <bool BF16, bool ONE>
 __global__ void __launch_bounds__(kThreads, ONE ? 7 : 5) process_logits_kernel(const LogitParams p) {
   constexpr int kNodes = ONE ? 1 : VFY_MAX_TREE_NODES;
   constexpr int kMaskRows = ONE ? 1 : 32;      // rows whose mask words are staged at a time
-  constexpr int kMaskIters = (kMaskRows * kSpanWords + kThreads - 1) / kThreads;
+  constexpr int kMaskIters = (kMaskRows * kSegWords + kThreads - 1) / kThreads;
   // Columns seg0 - 3 .. seg0 + kSeg - 1 of the sequence (a row uses kSeg of them, see below).
   __shared__ int32_t s_count[kSpan];
   __shared__ float s_bias[kSpan];
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(kThreads, ONE ? 7 : 5) process_logits_kernel(c
   __shared__ uint32_t s_set[kNodes][kWords];   // per entry: the nodes that draft its token
   __shared__ int s_mask[kNodes];               // per row: its grammar mask, -1 = none
   __shared__ int s_drafted[kNodes];            // the drafted columns, once each
-  __shared__ uint32_t s_lets[kMaskRows][kSpanWords];   // mask words of a chunk of this CTA's rows
+  __shared__ uint32_t s_lets[kMaskRows][kSegWords];   // masks of a chunk of this CTA's rows, from the row's first column on
   __shared__ int s_num_drafted;
   pdl_launch_dependents();
   pdl_wait();
@@ -232,25 +233,28 @@ __global__ void __launch_bounds__(kThreads, ONE ? 7 : 5) process_logits_kernel(c
                    : 0;
   }
   const int my_rows = i0 < n ? (n - i0 + step - 1) / step : 0;
-  const int word0 = max(seg0 - 3, 0) >> 5;     // first staged word of a mask
-  // the mask words of rows j0 .. j1 - 1 of this CTA, into s_lets; mask_of(i) = the mask of row i, -1 = none
+  // the masks of rows j0 .. j1 - 1 of this CTA, into s_lets; mask_of(i) = the mask of row i, -1 = none
   auto stage_masks = [&](int j0, int j1, auto mask_of) {
-    const int have = min(kSpanWords, static_cast<int>(words_per_mask) - word0);
-    uint32_t word[kMaskIters];
+    uint32_t lo[kMaskIters], hi[kMaskIters];
 #pragma unroll
     for (int u = 0; u < kMaskIters; ++u) {
-      const int x = tid + u * kThreads, j = x / kSpanWords, w = x - j * kSpanWords;
-      word[u] = 0xffffffffu;
-      if (j < j1 - j0 && w < have) {
-        const int mask = mask_of(i0 + (j0 + j) * step);
-        if (mask >= 0)
-          word[u] = __ldg(r.grammar + static_cast<uint64_t>(static_cast<uint32_t>(mask)) * words_per_mask + word0 + w);
+      const int x = tid + u * kThreads, j = x / kSegWords, w = x % kSegWords;
+      lo[u] = hi[u] = 0xffffffffu;
+      if (j < j1 - j0) {
+        const int i = i0 + (j0 + j) * step, mask = mask_of(i), shift = shift_of(i);
+        const int at = (seg0 >> 5) + w - (shift > 0 ? 1 : 0);        // the word of this one's first column
+        if (mask >= 0) {
+          const uint32_t* words = r.grammar + static_cast<uint64_t>(static_cast<uint32_t>(mask)) * words_per_mask;
+          if (at >= 0 && at < static_cast<int>(words_per_mask)) lo[u] = __ldg(words + at);
+          if (shift > 0 && at + 1 < static_cast<int>(words_per_mask)) hi[u] = __ldg(words + at + 1);
+        }
       }
     }
 #pragma unroll
     for (int u = 0; u < kMaskIters; ++u) {
-      const int x = tid + u * kThreads;
-      if (x < (j1 - j0) * kSpanWords) (&s_lets[0][0])[x] = word[u];
+      const int x = tid + u * kThreads, j = x / kSegWords;
+      const int shift = shift_of(i0 + (j0 + j) * step);
+      if (j < j1 - j0) (&s_lets[0][0])[x] = shift > 0 ? __funnelshift_r(lo[u], hi[u], 32 - shift) : lo[u];
     }
   };
   if (grammar)
@@ -335,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, ONE ? 7 : 5) process_logits_kernel(c
     return bias - (word != 0 ? fmaf(freq, c, c > 0.f ? pres : 0.f) : 0.f);
   };
   auto rule = [&](float v, bool seen, float add) {
-    return rules ? fmaf(v, seen ? (v > 0.f ? inv : rep) : 1.f, add) : v;
+    return fmaf(v, seen ? (v > 0.f ? inv : rep) : 1.f, add);
   };
   // ---- the rows, kMaskRows of this CTA's at a time (row j: i = i0 + j step) ----
   for (int j0 = 0; j0 < my_rows; j0 += kMaskRows) {
@@ -364,7 +368,6 @@ __global__ void __launch_bounds__(kThreads, ONE ? 7 : 5) process_logits_kernel(c
         add[e] = addend(word, s_bias[c]);
         if (!ONE && num_drafted > 0 && s_entry[c] != kNone) mine &= ~(1u << e);
       }
-      const int bit0 = v0 - 32 * word0;          // of a staged mask; -3 .. -1 only where word0 = 0
       float* dst = p.out + ((r0 + static_cast<long long>(i0 + first * step)) * p.vocab + v0);
       for (int jb = first; jb < j1; jb += kRows * passes) {
         if (jb > 0) load_rows(i0 + jb * step, j1 - jb, v0, valid);
@@ -372,19 +375,21 @@ __global__ void __launch_bounds__(kThreads, ONE ? 7 : 5) process_logits_kernel(c
         for (int u = 0; u < kRows; ++u) {
           const int j = jb + u * passes;
           if (j >= j1) break;
-          uint32_t lets = 0xffu;
-          if (grammar) {                         // a group's four bits may straddle two words
-            const uint32_t* words = s_lets[j - j0];
-            const int w = bit0 >> 5, w2 = (bit0 + kGroup) >> 5;
-            const uint32_t a = bit0 >= 0 ? __funnelshift_r(words[w], words[w + 1], bit0 & 31) : words[0] << -bit0;
-            const uint32_t c = __funnelshift_r(words[w2], words[w2 + 1], (bit0 + kGroup) & 31);
-            lets = (a & 15u) | (c << 4);
-          }
           float y[kCols];
 #pragma unroll
-          for (int e = 0; e < kCols; ++e) {
-            y[e] = rule(entry_of<BF16>(x[u], e), (seen >> e) & 1u, add[e]);
-            y[e] = (lets >> e) & 1u ? y[e] : -INFINITY;
+          for (int e = 0; e < kCols; ++e) y[e] = entry_of<BF16>(x[u], e);
+          if (rules) {
+#pragma unroll
+            for (int e = 0; e < kCols; ++e) y[e] = rule(y[e], (seen >> e) & 1u, add[e]);
+          }
+          if (grammar) {
+            const uint32_t* words = s_lets[j - j0] + (tid >> 3);
+            const uint32_t a = words[0] >> (4 * (tid & 7)), c = words[kGroup / 32] >> (4 * (tid & 7));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              y[e] = (a >> e) & 1u ? y[e] : -INFINITY;
+              y[e + 4] = (c >> e) & 1u ? y[e + 4] : -INFINITY;
+            }
           }
 #pragma unroll
           for (int e = 0; e < kCols; e += 4) {
@@ -424,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, ONE ? 7 : 5) process_logits_kernel(c
       const long long at = row * p.stride + v;
       const float in = BF16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p.logits)[at]) << 16)
                             : static_cast<const float*>(p.logits)[at];
-      float y = rule(in, word != 0, addend(word, s_bias[c]));
+      float y = rule(in, word != 0, addend(word, s_bias[c]));      // (drafts come with counts)
       if (s_mask[i] >= 0) {
         const uint64_t word0 = static_cast<uint64_t>(static_cast<uint32_t>(s_mask[i])) * words_per_mask;
         const uint32_t bits = __ldg(r.grammar + word0 + (v >> 5));
