@@ -9,15 +9,15 @@
 // drafted tokens on their paths: the main loop leaves out the few columns of the segment that any node
 // drafts, and at the end a thread per (row, such column) counts the drafting nodes in the row's mask.
 // Every entry is read and written by one thread, so the call may work in place.
-// Bound by bytes in flight: the first rows' logits are loaded before the rules, the mask words of 32 rows
-// at a time go through shared memory (one wait instead of one per batch), four rows of eight columns are
-// in flight per thread, and by issue slots, half of which a batch takes: masks are staged from each row's first
-// column on, so that a thread's bits are two shifts, and entries take the steps of the rules in use only. GB300: 17 x
-// 131072 fp32 8.2 us (the bytes alone 2.7); 339 rows x 100003 bf16 of 16 sequences 55.7 us (3.8 TB/s; 47.7 us with a
-// vocabulary of 100000, whose rows all start alike, 37.8 of it without rules). Loading eight neighbouring columns per thread (half-sector stores), per-thread mask
-// loads, and columns past a row's end in a loop of their own each cost 15 to 40 us of the batch; registers for
-// six CTAs per SM instead of five 10 us, refilling each row's registers as soon as it is done, instead of four
-// rows at a time, 20, loading a batch ahead 5.
+// Bound by bytes in flight and, in a batch, by issue slots, half of which are taken. So the first rows' logits are
+// loaded before the rules, the masks of 32 rows at a time go through shared memory (one wait instead of one per batch),
+// staged from each row's first column on, so that a thread's bits are two shifts; four rows of eight columns are in
+// flight per thread; and entries take the steps of the rules in use only. GB300: 17 x 131072 fp32 8.2 us (the bytes
+// alone 2.7); 339 rows x 100003 bf16 of 16 sequences 55.7 us (3.8 TB/s; 47.7 us with a vocabulary of 100000, whose rows
+// all start alike, 37.8 of it without rules). Loading eight neighbouring columns per thread (half-sector stores),
+// per-thread mask loads, and columns past a row's end in a loop of their own each cost 15 to 40 us of the batch;
+// refilling each row's registers as soon as it is done, instead of four rows at a time, 20, loading a batch ahead 5.
+// Five CTAs per SM or six made no difference to the batch; fp32 rows take five (four: 17 rows 10.4 us).
 #include "ptx.cuh"
 #include "vfy_internal.cuh"
 
