@@ -23,7 +23,7 @@
 //
 // GB300, 4 KV heads, G = 4, one layer with its merge: 64 nodes over 4096 resident chunks (537 MB) 109 us, 4.9 TB/s
 // and 1.26 PFLOP/s of full row tiles (the linear block's kernel with its best splits 146); 8 ragged sequences of 48
-// nodes up to 48K 110 us (147). A tile of 128 keys takes a pair some 1850 cycles, of which its MMAs fill 1024 and the
+// nodes up to 48K 110 us (147). A tile of 128 keys takes a pair some 1880 cycles, of which its MMAs fill 1024 and the
 // copies at the HBM rate would 1400: the bound is the loop P(n) -> PV(n) -> S(n + 2) -> P(n + 2), two tiles long, and
 // beside it the softmax warps' own time (1160 cycles of a tile are arithmetic, the rest barrier operations; a wait for
 // a phase that is complete takes 145 cycles on an idle SM, 70 when it is tested first, both twice that here). So every
