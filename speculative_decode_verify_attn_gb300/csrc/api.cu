@@ -410,14 +410,16 @@ static int tree_capacity(const vfy_config& c) { return std::min(c.max_queries_pe
 // Does a tree's full layer go to CTA pairs of 256 rows (and how many), or to the linear block's kernel (0)?
 // Pairs balance whatever the lengths, and halve the K/V traffic of two row tiles; each run pays about 8 us for its
 // start and the merge. us of one layer, 4 KV heads, the linear kernel with its best splits against pairs:
-//   two row tiles (64 nodes, G = 4), 64 chunks: 1 sequence 15.0 / 18.7, 4: 26.9 / 27.8, 8: 43.9 / 34.8, 16: 46.5 / 52;
+//   two row tiles (64 nodes, G = 4), 32 chunks: 8 sequences 28.0 / 27.9, 12: 28.2 / 32.4; 64 chunks: 1: 14.9 / 17.8,
+//   2: 19.5 / 23.4, 4: 26.9 / 26.3, 8: 43.8 / 32.4, 16: 46.8 / 48.5, 16 ragged: 46.3 / 41.3; 128 chunks: 1: 18.5 / 19.7;
 //   256 chunks: 1: 22.5 / 22.1, 4: 55 / 41, 16: 160 / 99; 1024 chunks: 8: 264 / 162;
 //   one row tile (17 nodes), 256 chunks: 2 sequences 19.6 / 25.9, 4: 31.6 / 35.5, 8: 54 / 54, 16: 97 / 83;
 //   1024 chunks: 2: 57 / 64, 8: 168 / 157, 8 ragged (750 chunks at most): 105 / 98, and 130 with one wave of splits,
 //   which is the best for equal lengths.
 static int tree_pairs(const vfy_ctx* ctx, int row_tiles, int num_seqs, int max_res) {
   if (ctx->full_splits != 0 || ctx->cfg.head_dim != 128) return 0;
-  const bool take = row_tiles > 1 ? max_res >= 128 : num_seqs >= 4 && max_res >= 256;
+  const long long items = static_cast<long long>(ctx->cfg.num_kv_heads) * num_seqs * row_tiles;
+  const bool take = row_tiles > 1 ? max_res >= 128 || (max_res >= 48 && items >= 32) : num_seqs >= 4 && max_res >= 256;
   return take ? std::min(vfy::attend_tree_pairs(), ctx->num_sms / 2) : 0;
 }
 
