@@ -224,8 +224,8 @@ VFY_API vfy_status vfy_page_in(vfy_ctx* ctx, const uint16_t* host_k, const uint1
  * Values at positions some block query attends must be finite (a masked entry contributes
  * P = 0, and 0 * inf is NaN on the tensor core). Rows past seq_len and chunks not in the list
  * may hold anything.
- * Device errors: a slot outside [0, num_slots) or q_b beyond capacity: element skipped,
- * VFY_EDEVICE_INPUT.
+ * Device errors: a slot outside [0, num_slots), q_b beyond capacity, or rows outside
+ * [0, num_seqs * max_queries_per_seq): element skipped, VFY_EDEVICE_INPUT.
  */
 VFY_API vfy_status vfy_attend_full(vfy_ctx* ctx, const uint16_t* q, const int32_t* cu_q,
                                    const uint16_t* k_pool, const uint16_t* v_pool, int num_slots,

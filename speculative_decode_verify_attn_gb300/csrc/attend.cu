@@ -136,7 +136,7 @@ struct Work {
   int nres;        // full: resident chunks of sequence b
   int lo, span;    // ring: first attended position of the tile's rows and the union span length
   int s_lo;        // ring: slot of position lo
-  bool bad;        // the sequence's q or L is out of range: it is skipped
+  bool bad;        // the sequence's rows or L are out of range: it is skipped
 };
 
 template <bool RING, int CPT, bool TREE>
@@ -164,7 +164,9 @@ __device__ __forceinline__ Work make_work(const AttnParams& p) {
   w.lo = 0;
   w.span = 0;
   w.s_lo = 0;
-  w.bad = w.nq < 0 || w.nq > p.max_q || w.L < w.nq || w.q0 < 0;   // (a tree's max_q is its own limit)
+  // (a tree's max_q is its own limit; Q, masks and depths are read at these rows, so the rows lie within the
+  // capacity or the sequence is left out)
+  w.bad = w.nq < 0 || w.nq > p.max_q || w.L < w.nq || w.q0 < 0 || w.q0 > p.token_cap - w.nq;
   if (w.bad) {
     w.nq = 0;
     w.rows = 0;
@@ -1028,7 +1030,8 @@ __global__ void __launch_bounds__(128) combine_kernel(const CombineParams p) {
   if (t >= p.token_cap || t >= total) return;
   const int i = t - c0;
   const int nq = c1 - c0;
-  if (i < 0 || nq < 0 || nq > p.max_q || len < nq) return;   // skipped by the attention kernel too
+  // skipped by the attention kernel too
+  if (i < 0 || nq < 0 || nq > p.max_q || len < nq || c0 < 0 || c0 > p.token_cap - nq) return;
   const int h = static_cast<int>(static_cast<unsigned>(hq) / static_cast<unsigned>(p.group));
   const int rg = i * p.group + (hq - h * p.group);        // block row
   const int rt = rg / kMaxRows;                           // its row tile

@@ -1,0 +1,80 @@
+"""The tree calls at the limits of their arguments: row offsets past a context's capacity, sequences behind one
+that is too long, the last chunk id, bias offsets out of order, and what a context's workspace holds.
+
+Attention is compared within 2^-8 (A + |o|) + 2^-16 A + 7e-4 A, A = sum_j p_j |v_j|: P is rounded to bf16 (half a
+step, 2^-8, of every weight), then O, of a value that the first rounding moved; the last term is that of fp32 scores
+of 128 products of N(0,1) values."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import tree_oracle as T
+from oracle import vfy_oracle as O
+from speculative_decode_verify_attn_gb300 import synth
+
+pytestmark = pytest.mark.gpu
+
+C = 64
+
+
+@pytest.fixture(scope="module")
+def env():
+    import __graft_entry__
+    __graft_entry__.build()
+    from speculative_decode_verify_attn_gb300 import harness, vfy
+    torch.cuda.set_device(0)
+    return harness, vfy
+
+
+def close(got, lse, ref, rlse, mag):
+    g = O.bf16_to_f64(got)
+    assert np.all(np.abs(g - ref) <= 2.0 ** -8 * (mag + np.abs(ref)) + (2.0 ** -16 + 7e-4) * mag + 1e-30)
+    fin = np.isfinite(rlse)
+    assert np.array_equal(np.isneginf(lse), np.isneginf(rlse))
+    assert np.all(np.abs(lse[fin] - rlse[fin]) <= 3.1e-4 + np.abs(rlse[fin]) * 2.0 ** -22)
+
+
+def masks(sets, rows):
+    """Row masks of `sets`, then rows of zeros."""
+    w = np.zeros((rows, 8), np.uint32)
+    w[:len(sets)] = T.mask_words(sets)
+    return torch.from_numpy(w.view(np.int32)).cuda()
+
+
+# ---------------------------------------------------------------------------------------------
+# Row offsets past the capacity
+# ---------------------------------------------------------------------------------------------
+
+# (nodes a sequence, splits of full layers, of window layers): one and two row tiles; the merge in a cluster, the
+# combine kernel, wide tiles and a single split
+FORMS = [(32, 0, 0), (32, 40, 20), (32, 3, 1), (32, 1, 1), (64, 12, 3), (64, 1, 20)]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap,full_splits,swa_splits", FORMS)
+def test_rows_past_the_capacity_are_neither_read_nor_written(env, d, cap, full_splits, swa_splits):
+    """Offsets that only a 32-bit sum would let pass, a sequence that begins inside the capacity and ends behind it,
+    one that begins before the first row: reported and left out whole, by the chain's layers too."""
+    H, vfy = env
+    ctx = vfy.vfy_create(4, 1, d, max_seqs=1, max_queries_per_seq=cap, device=0)
+    q = torch.zeros((cap, 4, d), dtype=torch.bfloat16, device="cuda")
+    pool = torch.zeros((64, 1, C, d), dtype=torch.bfloat16, device="cuda")
+    ring = torch.zeros((1, 1, 2048, d), dtype=torch.bfloat16, device="cuda")
+    words, depth = torch.zeros((cap, 8), dtype=torch.int32, device="cuda"), H.dev_i32(np.zeros(cap))
+    ids, cu_res, L, zero = H.dev_i32(np.arange(64)), H.dev_i32([0, 64]), H.dev_i32([64 * C]), H.dev_i32([0])
+    out, lse = torch.full_like(q, 3.0), torch.full((cap, 4), 3.0, device="cuda")
+    big = 2 ** 31 - 8
+    try:
+        vfy.vfy_set_splits(ctx, full_splits, swa_splits)
+        for offsets in ([big, big + 15 - 2 ** 32], [cap - 4, cap + 11], [cap, cap + 1], [-5, 10]):
+            cu = H.dev_i32(offsets)
+            calls = [lambda: vfy.vfy_attend_full_tree(ctx, q, cu, words, pool, pool, 64, ids, ids, cu_res, 64, L, out, lse, 1),
+                     lambda: vfy.vfy_attend_swa_tree(ctx, q, cu, words, depth, ring, ring, zero, L, out, lse, 1),
+                     lambda: vfy.vfy_attend_full(ctx, q, cu, pool, pool, 64, ids, ids, cu_res, 64, L, out, lse, 1),
+                     lambda: vfy.vfy_attend_swa(ctx, q, cu, ring, ring, zero, L, out, lse, 1)]
+            for i, call in enumerate(calls):
+                call()
+                assert vfy.vfy_get_status(ctx) == vfy.VFY_EDEVICE_INPUT, (offsets, i)
+                assert (out == 3).all() and (lse == 3).all(), (offsets, i)
+    finally:
+        ctx.close()
