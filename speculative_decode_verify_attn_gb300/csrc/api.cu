@@ -515,7 +515,7 @@ static vfy_status attend_common(vfy_ctx* ctx, bool ring, const uint16_t* q, cons
   p.tree_depth = tree_depth;
   p.num_seqs = num_seqs;
   p.tree_pieces = ctx->tree_pieces;
-  p.token_cap = num_seqs * max_q;
+  p.token_cap = num_seqs * c.max_queries_per_seq;      // (a tree may lie behind a longer sequence, which is left out)
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int pairs = tree && !ring ? tree_pairs(ctx, row_tiles, num_seqs, max_res) : 0;
   if (pairs > 0) {
@@ -554,7 +554,8 @@ static vfy_status attend_common(vfy_ctx* ctx, bool ring, const uint16_t* q, cons
   cp.num_splits = splits;
   cp.max_q = max_q;
   cp.row_tiles = row_tiles;
-  cp.token_cap = num_seqs * max_q;
+  cp.token_cap = p.token_cap;
+  cp.by_seq = max_q < c.max_queries_per_seq;
   cp.stable_metadata = ctx->stable_metadata;
   cp.part_o = ctx->part_o;
   cp.part_ml = ctx->part_ml;
@@ -647,7 +648,7 @@ vfy_status vfy_tree_plan(vfy_ctx* ctx, const int32_t* parents, const int32_t* cu
   p.cu_q = cu_q;
   p.num_seqs = num_seqs;
   p.max_q = tree_capacity(ctx->cfg);
-  p.token_cap = num_seqs * p.max_q;
+  p.token_cap = num_seqs * ctx->cfg.max_queries_per_seq;
   p.depth = depth;
   p.mask = tree_mask;
   p.err = ctx->err;
@@ -822,7 +823,7 @@ static void compact_params(const vfy_ctx* ctx, const int32_t* path, const int32_
   p->seq_len = seq_len;
   p->num_seqs = num_seqs;
   p->max_q = tree_capacity(ctx->cfg);
-  p->token_cap = num_seqs * p->max_q;
+  p->token_cap = num_seqs * ctx->cfg.max_queries_per_seq;
   p->hkv = ctx->cfg.num_kv_heads;
   p->head_dim = ctx->cfg.head_dim;
   p->num_layers = num_layers;

@@ -166,7 +166,8 @@ __device__ __forceinline__ Work make_work(const AttnParams& p) {
   w.s_lo = 0;
   // (a tree's max_q is its own limit; Q, masks and depths are read at these rows, so the rows lie within the
   // capacity or the sequence is left out)
-  w.bad = w.nq < 0 || w.nq > p.max_q || w.L < w.nq || w.q0 < 0 || w.q0 > p.token_cap - w.nq;
+  w.bad = w.nq < 0 || w.nq > p.max_q || w.L < w.nq ||
+          static_cast<unsigned>(w.q0) > static_cast<unsigned>(p.token_cap - w.nq);
   if (w.bad) {
     w.nq = 0;
     w.rows = 0;
@@ -1001,7 +1002,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 //   O = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s,  LSE = ln2 * (M + log2 sum_s 2^(m_s - M) l_s)
 constexpr int kCombineMaxPerWarp = 16;   // splits per warp (64 splits per row at most)
 
-template <int HD>
+template <int HD, bool BY_SEQ>
 __global__ void __launch_bounds__(128) combine_kernel(const CombineParams p) {
   constexpr int kPer = HD / 32;
   using Vec = typename std::conditional<kPer == 4, float4, float2>::type;
@@ -1013,25 +1014,27 @@ __global__ void __launch_bounds__(128) combine_kernel(const CombineParams p) {
   // caller has declared it stable, after it otherwise. The partials are read after it.
   if (!p.stable_metadata) pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = static_cast<int>(blockIdx.x / p.hq);
+  const int x = static_cast<int>(blockIdx.x / p.hq);
   const int hq = static_cast<int>(blockIdx.x % p.hq);
+  // x is row x of the batch or, BY_SEQ, row x mod max_q of sequence x / max_q (see CombineParams).
   // One round trip for a one-sequence batch: its values are loaded with the batch's token count
   // (all in bounds: cu_q has B + 1 entries, seq_len B). A batch searches for its sequence.
   const int total = p.cu_q[p.num_seqs];
-  int b = 0;
-  int c0 = p.cu_q[0], c1 = p.cu_q[1], len = p.seq_len[0];
-  if (p.num_seqs > 1 && t < p.token_cap && t < total) {
-    while (b + 1 < p.num_seqs && p.cu_q[b + 1] <= t) ++b;
+  int b = BY_SEQ ? static_cast<int>(static_cast<unsigned>(x) / static_cast<unsigned>(p.max_q)) : 0;
+  int c0 = p.cu_q[b], c1 = p.cu_q[b + 1], len = p.seq_len[b];
+  if (!BY_SEQ && p.num_seqs > 1 && x < p.token_cap && x < total) {
+    while (b + 1 < p.num_seqs && p.cu_q[b + 1] <= x) ++b;
     c0 = p.cu_q[b];
     c1 = p.cu_q[b + 1];
     len = p.seq_len[b];
   }
   if (p.stable_metadata) pdl_wait();
-  if (t >= p.token_cap || t >= total) return;
-  const int i = t - c0;
+  if (!BY_SEQ && (x >= p.token_cap || x >= total)) return;
+  const int i = BY_SEQ ? x - b * p.max_q : x - c0;
   const int nq = c1 - c0;
   // skipped by the attention kernel too
-  if (i < 0 || nq < 0 || nq > p.max_q || len < nq || c0 < 0 || c0 > p.token_cap - nq) return;
+  if (i < 0 || i >= nq || nq > p.max_q || len < nq || c0 < 0 || c0 > p.token_cap - nq) return;
+  const int t = c0 + i;
   const int h = static_cast<int>(static_cast<unsigned>(hq) / static_cast<unsigned>(p.group));
   const int rg = i * p.group + (hq - h * p.group);        // block row
   const int rt = rg / kMaxRows;                           // its row tile
@@ -1207,10 +1210,14 @@ cudaError_t launch_attend(bool ring, int head_dim, AttnTiles tiles, const AttnPa
 }
 
 cudaError_t launch_combine(int head_dim, const CombineParams& p, cudaStream_t stream) {
-  const long long rows = static_cast<long long>(p.token_cap) * p.hq;
+  const long long tokens = p.by_seq ? static_cast<long long>(p.num_seqs) * p.max_q : p.token_cap;
+  const long long rows = tokens * p.hq;
   dim3 grid(static_cast<unsigned>(rows));
-  if (head_dim == 128) return launch_pdl(combine_kernel<128>, grid, dim3(128), 0, stream, p);
-  return launch_pdl(combine_kernel<64>, grid, dim3(128), 0, stream, p);
+  if (head_dim == 128)
+    return p.by_seq ? launch_pdl(combine_kernel<128, true>, grid, dim3(128), 0, stream, p)
+                    : launch_pdl(combine_kernel<128, false>, grid, dim3(128), 0, stream, p);
+  return p.by_seq ? launch_pdl(combine_kernel<64, true>, grid, dim3(128), 0, stream, p)
+                  : launch_pdl(combine_kernel<64, false>, grid, dim3(128), 0, stream, p);
 }
 
 }  // namespace vfy

@@ -78,3 +78,56 @@ def test_rows_past_the_capacity_are_neither_read_nor_written(env, d, cap, full_s
                 assert (out == 3).all() and (lse == 3).all(), (offsets, i)
     finally:
         ctx.close()
+
+
+@pytest.mark.parametrize("heads", [(4, 1, 128), (4, 1, 64)])
+@pytest.mark.parametrize("splits,bound", [(0, 0), (0, 256), (40, 0), (3, 0)])
+def test_a_sequence_behind_one_that_is_too_long(env, heads, splits, bound):
+    """A context of 1024 queries: 400 rows are more than a tree may have and are left out, the tree of 200 behind them
+    (rows 400 to 599, past 256 a sequence) is planned, attended and compacted."""
+    H, vfy = env
+    hq, hkv, d = heads
+    W, R = 512, 2048
+    rng = np.random.default_rng([splits, bound, d])
+    n, L = 200, 1000
+    cu = [0, 400, 600]
+    parents = synth.random_tree(rng, n)
+    sets, depth = T.ancestors(parents.tolist()), T.depths(parents.tolist())
+    ctx = vfy.vfy_create(hq, hkv, d, max_seqs=2, max_queries_per_seq=1024, window=W, ring_len=R, device=0)
+    q = synth.normal_bf16(rng, (600, hq, d))
+    m = -(-L // C)
+    kp, vp = synth.normal_bf16(rng, (m, hkv, C, d)), synth.normal_bf16(rng, (m, hkv, C, d))
+    kr, vr = synth.normal_bf16(rng, (2, hkv, R, d)), synth.normal_bf16(rng, (2, hkv, R, d))
+    ids = np.arange(m)
+    cu_d, lens = H.dev_i32(cu), H.dev_i32([3000, L])
+    dep, words = H.dev_i32(np.full(600, -9)), torch.full((600, 8), -9, dtype=torch.int32, device="cuda")
+    try:
+        vfy.vfy_set_splits(ctx, splits, min(splits, 20))
+        vfy.vfy_tree_plan(ctx, H.dev_i32(np.concatenate([np.arange(-1, 399), parents])), cu_d, dep, words, 2)
+        assert vfy.vfy_get_status(ctx) == vfy.VFY_EDEVICE_INPUT
+        assert (dep[:400] == -9).all() and dep[400:].cpu().tolist() == depth
+        assert np.array_equal(words[400:].cpu().numpy().view(np.uint32), T.mask_words(sets))
+        dep[:400] = 0
+        qd = H.dev_bf16(q)
+        for window in (False, True):
+            out, lse = torch.full_like(qd, 7.0), torch.full((600, hq), 7.0, device="cuda")
+            if window:
+                vfy.vfy_attend_swa_tree(ctx, qd, cu_d, words, dep, H.dev_bf16(kr), H.dev_bf16(vr), H.dev_i32([0, 77]), lens,
+                                        out, lse, 2)
+                ref = T.attend_tree_ring_seq(q[400:], sets, depth, kr[1], vr[1], 77, L, W)
+            else:
+                vfy.vfy_attend_full_tree(ctx, qd, cu_d, words, H.dev_bf16(kp), H.dev_bf16(vp), m, H.dev_i32(ids),
+                                         H.dev_i32(ids), H.dev_i32([0, 0, m]), max(m, bound), lens, out, lse, 2)
+                ref = T.attend_tree_full_seq(q[400:], sets, kp, vp, ids, ids, L)
+            assert vfy.vfy_get_status(ctx) == vfy.VFY_EDEVICE_INPUT
+            assert (out[:400] == 7).all() and (lse[:400] == 7).all()
+            close(H.bits_of(out)[400:], lse[400:].cpu().numpy(), *ref)
+        path = np.full(600, -1)
+        path[[0, 400, 401, 402]] = [0, 0, 5, 9]
+        k, v = H.dev_bf16(kr), H.dev_bf16(vr)
+        vfy.vfy_compact_swa(ctx, H.dev_i32(path), H.dev_i32([0, 2]), cu_d, lens, H.dev_i32([0, 77]), [k], [v], 2)
+        assert vfy.vfy_get_status(ctx) == vfy.VFY_EDEVICE_INPUT
+        want = T.compact_ring(path, [0, 2], cu, [3000, L], [0, 77], kr)
+        assert np.array_equal(H.bits_of(k), want)
+    finally:
+        ctx.close()
