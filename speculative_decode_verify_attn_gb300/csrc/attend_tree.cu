@@ -359,8 +359,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             bars->base[g][i] = c[i].base;
             bars->valid[g][i] = c[i].valid ? 1 : 0;
-            plain = plain && c[i].valid && c[i].base + kChunk <= p0;
-            zero = zero || !c[i].valid || c[i].base + kChunk > w.s.L;
+            // (the last chunk ends at 2^31: no sums with its base)
+            plain = plain && c[i].valid && c[i].base <= p0 - kChunk;
+            zero = zero || !c[i].valid || c[i].base > w.s.L - kChunk;
             present += c[i].present ? 1 : 0;
           }
           bars->zero[g] = zero ? 1 : 0;

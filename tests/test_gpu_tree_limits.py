@@ -131,3 +131,30 @@ def test_a_sequence_behind_one_that_is_too_long(env, heads, splits, bound):
         assert np.array_equal(H.bits_of(k), want)
     finally:
         ctx.close()
+
+
+@pytest.mark.parametrize("bound", [0, 256])
+@pytest.mark.parametrize("at", [0, 1, 2])
+def test_the_last_chunk_id(env, at, bound):
+    """The last chunk that a list may name ends at position 2^31 - 1: behind every short sequence, so that no row
+    attends it, wherever it stands in the list, and whatever its slot holds."""
+    H, vfy = env
+    rng = np.random.default_rng(at)
+    n, L = 40, 100
+    sets = T.ancestors(synth.random_tree(rng, n).tolist())
+    q = synth.normal_bf16(rng, (n, 16, 128))
+    kp, vp = synth.normal_bf16(rng, (3, 4, C, 128)), synth.normal_bf16(rng, (3, 4, C, 128))
+    kp[2], vp[2] = 0x7FC0, 0x7FC0
+    ids, slots = [0, 1], [0, 1]
+    ids.insert(at, 2 ** 25 - 1)
+    slots.insert(at, 2)
+    ctx = vfy.vfy_create(16, 4, 128, max_queries_per_seq=n, device=0)
+    qd = H.dev_bf16(q)
+    out, lse = torch.full_like(qd, 7.0), torch.full((n, 16), 7.0, device="cuda")
+    try:
+        vfy.vfy_attend_full_tree(ctx, qd, H.dev_i32([0, n]), masks(sets, n), H.dev_bf16(kp), H.dev_bf16(vp), 3, H.dev_i32(ids),
+                                 H.dev_i32(slots), H.dev_i32([0, 3]), max(3, bound), H.dev_i32([L]), out, lse, 1)
+        assert vfy.vfy_get_status(ctx) == vfy.VFY_OK
+        close(H.bits_of(out), lse.cpu().numpy(), *T.attend_tree_full_seq(q, sets, kp, vp, [0, 1], [0, 1], L))
+    finally:
+        ctx.close()
