@@ -96,6 +96,17 @@ int ceil_div(long long a, long long b) { return static_cast<int>((a + b - 1) / b
 
 int clampi(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
 
+// Nodes of one sequence's tree that a context takes, and their row tiles.
+int tree_capacity(const vfy_config& c) { return std::min(c.max_queries_per_seq, VFY_MAX_TREE_NODES); }
+int tree_row_tiles(const vfy_config& c) {
+  return ceil_div(static_cast<long long>(tree_capacity(c)) * (c.num_q_heads / c.num_kv_heads), kMaxRows);
+}
+// Can a context's trees go to CTA pairs at all (see tree_pairs)? Only then does it hold their partials (20 MB).
+constexpr int kPairSeqs = 4;
+bool pairs_possible(const vfy_config& c) {
+  return c.head_dim == 128 && (tree_row_tiles(c) > 1 || c.max_seqs >= kPairSeqs);
+}
+
 }  // namespace
 
 #define VFY_REQUIRE(c)           \
@@ -167,7 +178,7 @@ vfy_status vfy_create(const vfy_config* cfg_in, int device, vfy_ctx** out) {
   ctx->row_tiles = ceil_div(static_cast<long long>(cfg.max_queries_per_seq) * group, kMaxRows);
   size_t parts = static_cast<size_t>(cfg.max_seqs) * ctx->row_tiles * cfg.num_kv_heads * cfg.max_splits * kMaxRows;
   // tree attention by CTA pairs: two partial segments of two row tiles for every two SMs
-  parts = std::max(parts, static_cast<size_t>(ctx->num_sms) * 2 * kMaxRows);
+  if (pairs_possible(cfg)) parts = std::max(parts, static_cast<size_t>(ctx->num_sms) * 2 * kMaxRows);
   ctx->accept_rows_cap = cfg.max_seqs * cfg.max_queries_per_seq;
   bool ok = cudaMalloc(&ctx->part_o, parts * cfg.head_dim * sizeof(float)) == cudaSuccess &&
             cudaMalloc(&ctx->part_ml, parts * 2 * sizeof(float)) == cudaSuccess &&
@@ -404,9 +415,6 @@ vfy_status vfy_append_swa(vfy_ctx* ctx, const uint16_t* k_new, const uint16_t* v
   return VFY_OK;
 }
 
-// Nodes of one sequence's tree that a context takes.
-static int tree_capacity(const vfy_config& c) { return std::min(c.max_queries_per_seq, VFY_MAX_TREE_NODES); }
-
 // Does a tree's full layer go to CTA pairs of 256 rows (and how many), or to the linear block's kernel (0)?
 // Pairs balance whatever the lengths, and halve the K/V traffic of two row tiles; each run pays about 8 us for its
 // start and the merge. us of one layer, 4 KV heads, the linear kernel with its best splits against pairs:
@@ -417,9 +425,10 @@ static int tree_capacity(const vfy_config& c) { return std::min(c.max_queries_pe
 //   1024 chunks: 2: 57 / 64, 8: 168 / 157, 8 ragged (750 chunks at most): 105 / 98, and 130 with one wave of splits,
 //   which is the best for equal lengths.
 static int tree_pairs(const vfy_ctx* ctx, int row_tiles, int num_seqs, int max_res) {
-  if (ctx->full_splits != 0 || ctx->cfg.head_dim != 128) return 0;
+  if (ctx->full_splits != 0 || !pairs_possible(ctx->cfg)) return 0;
   const long long items = static_cast<long long>(ctx->cfg.num_kv_heads) * num_seqs * row_tiles;
-  const bool take = row_tiles > 1 ? max_res >= 128 || (max_res >= 48 && items >= 32) : num_seqs >= 4 && max_res >= 256;
+  // (pairs_possible names what this rule asks of a context)
+  const bool take = row_tiles > 1 ? max_res >= 128 || (max_res >= 48 && items >= 32) : num_seqs >= kPairSeqs && max_res >= 256;
   return take ? std::min(vfy::attend_tree_pairs(), ctx->num_sms / 2) : 0;
 }
 
@@ -432,8 +441,7 @@ static vfy_status attend_common(vfy_ctx* ctx, bool ring, const uint16_t* q, cons
   const vfy_config& c = ctx->cfg;
   const bool tree = tree_mask != nullptr;
   const int max_q = tree ? tree_capacity(c) : c.max_queries_per_seq;
-  const int row_tiles =
-      tree ? ceil_div(static_cast<long long>(max_q) * (c.num_q_heads / c.num_kv_heads), kMaxRows) : ctx->row_tiles;
+  const int row_tiles = tree ? tree_row_tiles(c) : ctx->row_tiles;
   DeviceGuard guard(ctx->device);
   if (!guard.ok) return VFY_ECUDA;
   CUtensorMap tk, tv;

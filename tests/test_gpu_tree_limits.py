@@ -158,3 +158,37 @@ def test_the_last_chunk_id(env, at, bound):
         close(H.bits_of(out), lse.cpu().numpy(), *T.attend_tree_full_seq(q, sets, kp, vp, [0, 1], [0, 1], L))
     finally:
         ctx.close()
+
+
+# ---------------------------------------------------------------------------------------------
+# Workspace
+# ---------------------------------------------------------------------------------------------
+
+def test_a_context_holds_the_partials_that_its_calls_can_use(env):
+    """Only contexts whose trees can go to CTA pairs (d = 128, and two row tiles or four sequences) hold those
+    pairs' partials: 256 rows a SM. A chain's context of one sequence holds its splits."""
+    H, vfy = env
+    n = 16                                             # contexts, so that the allocator's granularity is small beside
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+
+    def each(*shape, **kw):
+        torch.cuda.synchronize()
+        before = torch.cuda.mem_get_info()[0]
+        held = [vfy.vfy_create(*shape, device=0, **kw) for _ in range(n)]
+        after = torch.cuda.mem_get_info()[0]
+        for c in held:
+            c.close()
+        return (before - after) / n
+
+    each(4, 1, 64, max_queries_per_seq=17)             # (the first context loads the kernels)
+    pairs = sms * 256 * (128 + 2) * 4
+    slack = 6 << 20                                    # seven allocations, the small ones of at most 2 MB together
+    for shape, kw in (((4, 1, 64), dict(max_queries_per_seq=256)), ((4, 1, 128), dict(max_queries_per_seq=17)),
+                      ((4, 4, 128), dict(max_queries_per_seq=128, max_seqs=3))):
+        hkv, d, seqs = shape[1], shape[2], kw.get("max_seqs", 1)
+        tiles = -(-kw["max_queries_per_seq"] * shape[0] // hkv // 128)
+        own = seqs * tiles * hkv * 4 * 128 * (d + 2) * 4
+        assert own + slack < pairs
+        assert each(*shape, max_splits=4, **kw) <= own + slack, (shape, kw)
+    assert each(4, 1, 128, max_queries_per_seq=64, max_splits=4) >= pairs
+    assert each(4, 1, 128, max_queries_per_seq=17, max_seqs=4, max_splits=4) >= pairs
