@@ -460,8 +460,9 @@ typedef struct vfy_logit_rules {
  *  out         fp32 [cu_rows[B]][vocab], what vfy_accept and vfy_accept_tree read. It may be the logits
  *              themselves (fp32, row_stride == vocab); any other overlap of the two gives VFY_EINVAL
  * A row whose mask lets nothing follow holds -inf everywhere (its argmax is then token 0).
- * Device errors: a drafted or bias token outside [0, vocab) (skipped), a mask_index outside [-1,
- * num_masks) (no mask), a sequence's rows out of range (left unwritten): VFY_EDEVICE_INPUT.
+ * Device errors: a drafted or bias token outside [0, vocab) (skipped), a sequence's cu_bias negative or out of
+ * order (no bias), a mask_index outside [-1, num_masks) (no mask), a sequence's rows out of range (left unwritten):
+ * VFY_EDEVICE_INPUT.
  */
 VFY_API vfy_status vfy_process_logits(vfy_ctx* ctx, const void* logits, int logits_type, int64_t row_stride,
                                       int vocab, const int32_t* cu_rows, int max_rows,

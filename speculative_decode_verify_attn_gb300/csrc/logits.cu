@@ -175,6 +175,10 @@ __global__ void __launch_bounds__(kThreads, ONE ? 7 : 5) process_logits_kernel(c
   if (r.cu_bias != nullptr) {
     e0 = r.cu_bias[b];
     e1 = r.cu_bias[b + 1];
+    if (e0 < 0 || e1 < e0) {
+      if (report && tid == 0) atomicOr(p.err, kErrDeviceInput);
+      e0 = e1 = 0;
+    }
   }
   constexpr int kNodeIters = (kNodes + kThreads - 1) / kThreads;
   int draft_col[kNodeIters];                   // this thread's nodes tid + 1, ... (node 0 is in the counts)
@@ -209,10 +213,10 @@ __global__ void __launch_bounds__(kThreads, ONE ? 7 : 5) process_logits_kernel(c
   auto load_bias = [&](int base) {
 #pragma unroll
     for (int u = 0; u < kBiasAhead; ++u) {
-      const int e = base + u * kThreads + tid;
+      const unsigned e = static_cast<unsigned>(base) + u * kThreads + tid;     // (past 2^31 behind the longest list)
       bias_col[u] = -1;
       bias_val[u] = 0.f;
-      if (e >= e1) continue;
+      if (e >= static_cast<unsigned>(e1)) continue;
       const int tok = r.bias_token[e];
       bias_val[u] = r.bias_value[e];
       if (tok < 0 || tok >= p.vocab) {
@@ -313,8 +317,8 @@ __global__ void __launch_bounds__(kThreads, ONE ? 7 : 5) process_logits_kernel(c
         if (bias_col[u] >= 0) atomicMin(&s_turn[bias_col[u]], base + u * kThreads + tid);
       __syncthreads();
     }
+    if (e1 - base <= kThreads * kBiasAhead) break;
     base += kThreads * kBiasAhead;
-    if (base >= e1) break;
     load_bias(base);
   }
   const int num_drafted = ONE ? 0 : s_num_drafted;       // (the bias rounds passed at least one barrier)

@@ -161,8 +161,30 @@ def test_the_last_chunk_id(env, at, bound):
 
 
 # ---------------------------------------------------------------------------------------------
-# Workspace
+# Bias offsets, workspace
 # ---------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("rows", [1, 3])
+@pytest.mark.parametrize("offsets", [[0, 2, 1], [0, -1, 2], [-3, 0, 2], [0, -2, -1]])
+def test_bias_offsets_out_of_order_are_reported(env, rows, offsets):
+    """The sequences whose offsets are negative or descend get no bias; the others get theirs."""
+    H, vfy = env
+    ctx = vfy.vfy_create(4, 1, 64, max_seqs=2, max_queries_per_seq=4, device=0)
+    x = torch.arange(2 * rows * 50, device="cuda", dtype=torch.float32).view(2 * rows, 50)
+    token, value = [7, 7], [1.0, 2.0]
+    try:
+        rules = vfy.LogitRules(cu_bias=H.dev_i32(offsets), bias_token=H.dev_i32(token), bias_value=H.dev_f32(value))
+        out = torch.full_like(x, 77.0)
+        vfy.vfy_process_logits(ctx, x, 50, H.dev_i32([0, rows, 2 * rows]), 2 * rows, rules, out, 2)
+        assert vfy.vfy_get_status(ctx) == vfy.VFY_EDEVICE_INPUT
+        want = x.clone()
+        for b in range(2):
+            if 0 <= offsets[b] <= offsets[b + 1]:
+                want[rows * b:rows * (b + 1), 7] += sum(value[offsets[b]:offsets[b + 1]])
+        assert torch.equal(out, want)
+    finally:
+        ctx.close()
+
 
 def test_a_context_holds_the_partials_that_its_calls_can_use(env):
     """Only contexts whose trees can go to CTA pairs (d = 128, and two row tiles or four sequences) hold those
