@@ -370,6 +370,8 @@ VFY_API vfy_status vfy_accept_static(const float* logits, int vocab, const int32
  * p0 + j, p0 = seq_len[b] - q_b, where vfy_append_full / vfy_append_swa put it; the token it stands
  * for sits at position p0 + depth_j of its sequence (the position for a rotary embedding and for
  * the window). A chain (parent of j = j - 1) gives the results of the calls without _tree, up to rounding.
+ * The attention's work is divided for the most nodes that the context takes, min(max_queries_per_seq,
+ * VFY_MAX_TREE_NODES), whatever the block holds: a context made for the trees that it verifies is the fastest.
  */
 #define VFY_MAX_TREE_NODES 256 /* nodes of one sequence's tree */
 #define VFY_TREE_WORDS 8       /* 32-bit words of a node's row mask */
@@ -458,7 +460,8 @@ typedef struct vfy_logit_rules {
  *  logits_type VFY_LOGITS_F32 or VFY_LOGITS_BF16
  *  cu_rows     int32 [B+1] (device); max_rows host bound on cu_rows[B] (<= max_seqs * max_queries_per_seq)
  *  out         fp32 [cu_rows[B]][vocab], what vfy_accept and vfy_accept_tree read. It may be the logits
- *              themselves (fp32, row_stride == vocab); any other overlap of the two gives VFY_EINVAL
+ *              themselves (fp32, row_stride == vocab); any other overlap of the two, as max_rows rows each,
+ *              gives VFY_EINVAL
  * A row whose mask lets nothing follow holds -inf everywhere (its argmax is then token 0).
  * Device errors: a drafted or bias token outside [0, vocab) (skipped), a sequence's cu_bias negative or out of
  * order (no bias), a mask_index outside [-1, num_masks) (no mask), a sequence's rows out of range (left unwritten):

@@ -424,11 +424,16 @@ vfy_status vfy_append_swa(vfy_ctx* ctx, const uint16_t* k_new, const uint16_t* v
 //   one row tile (17 nodes), 256 chunks: 2 sequences 19.6 / 25.9, 4: 31.6 / 35.5, 8: 54 / 54, 16: 97 / 83;
 //   1024 chunks: 2: 57 / 64, 8: 168 / 157, 8 ragged (750 chunks at most): 105 / 98, and 130 with one wave of splits,
 //   which is the best for equal lengths.
+// The rule is coarser than the table and takes pairs at three of its points where they are slower: one sequence, two
+// row tiles, 128 chunks (1.2 us); four sequences, one row tile, 256 chunks (3.9); 16 equal sequences, two row tiles,
+// 64 chunks (1.7, where ragged ones gain 5.0). Row tiles are those of the context's capacity, not of the block. The
+// table is for 4 KV heads; the pair kernel is written for d = 128.
 static int tree_pairs(const vfy_ctx* ctx, int row_tiles, int num_seqs, int max_res) {
   if (ctx->full_splits != 0 || !pairs_possible(ctx->cfg)) return 0;
   const long long items = static_cast<long long>(ctx->cfg.num_kv_heads) * num_seqs * row_tiles;
   // (pairs_possible names what this rule asks of a context)
-  const bool take = row_tiles > 1 ? max_res >= 128 || (max_res >= 48 && items >= 32) : num_seqs >= kPairSeqs && max_res >= 256;
+  const bool take = row_tiles > 1 ? max_res >= 128 || (max_res >= 48 && items >= 32)
+                                  : num_seqs >= kPairSeqs && max_res >= 256;
   return take ? std::min(vfy::attend_tree_pairs(), ctx->num_sms / 2) : 0;
 }
 

@@ -21,13 +21,17 @@
 // this one. An MMA costs its issuer 50 to 110 cycles beside busy softmax warps, more than the pair's 64 in the
 // tensor pipes: hence two issuers (one for everything: 2360 cycles a tile, in the linear block's kernel).
 //
-// GB300, 4 KV heads, G = 4, one layer with its merge: 64 nodes over 4096 resident chunks (537 MB) 109 us, 4.9 TB/s
-// and 1.26 PFLOP/s of full row tiles (the linear block's kernel with its best splits 146); 8 ragged sequences of 48
-// nodes up to 48K 110 us (147). A tile of 128 keys takes a pair some 1880 cycles, of which its MMAs fill 1024 and the
-// copies at the HBM rate would 1400: the bound is the loop P(n) -> PV(n) -> S(n + 2) -> P(n + 2), two tiles long, and
-// beside it the softmax warps' own time (1160 cycles of a tile are arithmetic, the rest barrier operations; a wait for
-// a phase that is complete takes 145 cycles on an idle SM, 70 when it is tested first, both twice that here). So every
-// wait and index in that loop counts: rings of 4 stages (6 of K, or 5 of V, cost 4 to 6 us for the division), V's wait
+// P is rounded to bf16 for the second MMA (half a step, 2^-8, of each weight, and O once more at the end; its sum l is
+// that of the unrounded weights), as V's type asks; P in two bf16 parts would double that MMA. Against fp64 the
+// outputs are off by 0.0023 of their norm, rounding O alone costs 0.0017.
+//
+// GB300, 4 KV heads, G = 4, one layer with its merge, replayed in a graph: 64 nodes over 4096 resident chunks (537 MB)
+// 109 us, 4.9 TB/s and 1.26 PFLOP/s of full row tiles (the linear block's kernel with its best splits 146); 8 ragged
+// sequences of 48 nodes up to 48K 110 us (147). Calls in a loop on the stream take 120 and 115. A tile of 128 keys
+// takes a pair 1880 to 1910 cycles, of which its MMAs fill 1024 and the copies at the HBM rate would 1400: the bound is
+// the loop P(n) -> PV(n) -> S(n + 2) -> P(n + 2), two tiles long, and beside it the softmax warps' own time (1160 cycles
+// of a tile are arithmetic, the rest barrier operations; a wait for a phase that is complete takes 145 cycles on an idle
+// SM, 70 when it is tested first, both twice that here). So every wait and index in that loop counts: rings of 4 stages (6 of K, or 5 of V, cost 4 to 6 us for the division), V's wait
 // before S's, where the warp waits anyway (3 us), tests first, no wait for the geometry of most tiles (1 us each).
 // Measured and not kept, against 117 then: P in columns of its own, so that S(n + 1) runs as soon as S(n) is loaded,
 // 128 with one S buffer, 140 with two and one O for both warpgroups (which then have to agree on each row's maximum);

@@ -12,8 +12,8 @@
 // Bound by bytes in flight and, in a batch, by issue slots, half of which are taken. So the first rows' logits are
 // loaded before the rules, the masks of 32 rows at a time go through shared memory (one wait instead of one per batch),
 // staged from each row's first column on, so that a thread's bits are two shifts; four rows of eight columns are in
-// flight per thread; and entries take the steps of the rules in use only. GB300: 17 x 131072 fp32 8.2 us (the bytes
-// alone 2.7); 339 rows x 100003 bf16 of 16 sequences 55.7 us (3.8 TB/s; 47.7 us with a vocabulary of 100000, whose rows
+// flight per thread; and entries take the steps of the rules in use only. GB300: 17 x 131072 fp32 8.4 us (the bytes
+// alone 2.7); 339 rows x 100003 bf16 of 16 sequences 56.0 us (3.8 TB/s; 47.7 us with a vocabulary of 100000, whose rows
 // all start alike, 37.8 of it without rules). Loading eight neighbouring columns per thread (half-sector stores),
 // per-thread mask loads, and columns past a row's end in a loop of their own each cost 15 to 40 us of the batch;
 // refilling each row's registers as soon as it is done, instead of four rows at a time, 20, loading a batch ahead 5.
