@@ -31,8 +31,9 @@
 // takes a pair 1880 to 1910 cycles, of which its MMAs fill 1024 and the copies at the HBM rate would 1400: the bound is
 // the loop P(n) -> PV(n) -> S(n + 2) -> P(n + 2), two tiles long, and beside it the softmax warps' own time (1160 cycles
 // of a tile are arithmetic, the rest barrier operations; a wait for a phase that is complete takes 145 cycles on an idle
-// SM, 70 when it is tested first, both twice that here). So every wait and index in that loop counts: rings of 4 stages (6 of K, or 5 of V, cost 4 to 6 us for the division), V's wait
-// before S's, where the warp waits anyway (3 us), tests first, no wait for the geometry of most tiles (1 us each).
+// SM, 70 when it is tested first, both twice that here). So every wait and index in that loop counts: rings of 4 stages
+// (6 of K, or 5 of V, cost 4 to 6 us for the division), V's wait before S's, where the warp waits anyway (3 us), tests
+// first, no wait for the geometry of most tiles (1 us each).
 // Measured and not kept, against 117 then: P in columns of its own, so that S(n + 1) runs as soon as S(n) is loaded,
 // 128 with one S buffer, 140 with two and one O for both warpgroups (which then have to agree on each row's maximum);
 // one lane waiting for its warp 131; spinning without suspending 116; the issuing warp converged, with predicated
