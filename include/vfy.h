@@ -24,6 +24,14 @@
  *   vfy_accept_tree            fused argmax + walk along the accepted path
  *   vfy_compact_full/_swa      the accepted path's K/V rows next to the committed prefix
  *
+ * Around the attention and behind the logits:
+ *
+ *   vfy_rope, vfy_rope_append_full/_swa   the block's queries and keys normalised per head and rotated,
+ *                              keys and values written where the layer's attention reads them
+ *   vfy_append_full_packed, vfy_page_in_packed, vfy_unpack_chunks, vfy_attend_full_packed
+ *                              a pool of 4-bit chunks: written, paged in, read back and attended
+ *   vfy_accept_sampled         drafted tokens accepted and the next token drawn by given random numbers
+ *
  * Conventions shared by every call
  * --------------------------------
  *  - Pointers named host_* are host pointers; every other pointer is DEVICE memory on the
@@ -538,6 +546,157 @@ VFY_API vfy_status vfy_compact_swa(vfy_ctx* ctx, const int32_t* path, const int3
                                    const int32_t* cu_q, const int32_t* seq_len, const int32_t* ring_offset,
                                    int num_layers, uint16_t* const* k_ring, uint16_t* const* v_ring,
                                    int num_seqs, vfy_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------------------------
+ * Position rotation and append
+ * ---------------------------------------------------------------------------------------------
+ * A layer's projection gives the block's queries, keys and values; before the attention the queries and
+ * keys are normalised per head (in some models) and rotated to their positions. These calls do both in one
+ * pass over the rows, in fp32 with one rounding to bf16, and the append calls write the keys and values
+ * straight to where vfy_append_full / vfy_append_swa would put them.
+ */
+typedef struct vfy_rotary {
+  const float* inv_freq;    /* [rot_dim / 2] device, radians per position; NULL: no rotation (rot_dim 0) */
+  int rot_dim;              /* channels 0 .. rot_dim - 1 of every head are rotated, the others pass: a multiple of
+                               8, at most d */
+  int interleaved;          /* 0: pairs (i, i + rot_dim / 2); 1: pairs (2 i, 2 i + 1), i < rot_dim / 2 */
+  float attention_factor;   /* multiplies cos and sin; 0 -> 1 */
+  const uint16_t* q_norm;   /* bf16 [d] device: x * w / sqrt(mean(x^2) + eps) of every query head; NULL: none */
+  const uint16_t* k_norm;   /* the same for key heads */
+  float eps;                /* >= 0 */
+} vfy_rotary;
+
+/*
+ * vfy_rope -- normalise and rotate the block's queries and keys.
+ * Row i of sequence b is at position p = seq_len[b] - q_b + i, or, with depths (a tree), at
+ * seq_len[b] - q_b + depth[cu_q[b] + i]. With t = p * inv_freq[j] every pair (x, y) becomes
+ * (x cos t - y sin t, x sin t + y cos t). Angles are reduced in 64 bits: far positions keep their precision.
+ *  q, q_stride    bf16 rows of Hq * d values, q_stride values apart (>= Hq * d, a multiple of 8): a view of a
+ *                 wider matrix. NULL with q_out NULL: no queries
+ *  k, k_stride    bf16 rows of Hkv * d values; NULL with k_out NULL: no keys
+ *  cu_q, seq_len  as in vfy_attend_full;  depth  int32 [cu_q[B]] or NULL
+ *  q_out, k_out   bf16 [cu_q[B]][Hq][d], [cu_q[B]][Hkv][d]. They may be q and k themselves (packed rows), else they
+ *                 must not overlap them
+ * Pointers must be 16-byte aligned. Device errors: q_b beyond capacity, rows outside [0, num_seqs *
+ * max_queries_per_seq) or a sequence shorter than its block: its rows are left unwritten, VFY_EDEVICE_INPUT.
+ */
+VFY_API vfy_status vfy_rope(vfy_ctx* ctx, const vfy_rotary* rotary, const uint16_t* q, int64_t q_stride,
+                            const uint16_t* k, int64_t k_stride, const int32_t* cu_q, const int32_t* seq_len,
+                            const int32_t* depth, uint16_t* q_out, uint16_t* k_out, int num_seqs,
+                            vfy_stream_t stream);
+
+/*
+ * vfy_rope_append_full -- vfy_rope and vfy_append_full in one pass: K rotated and V as it is go to the chunk store
+ * and the pool, rotated queries to q_out.
+ *  v, v_stride  bf16 rows of Hkv * d values;  k and v are required, q as in vfy_rope
+ *  The other arguments and device errors are those of vfy_append_full (rows go to seq_len[b] - q_b + i, whatever
+ *  the depth) and vfy_rope. A token whose chunk lies outside the store still gets its queries.
+ */
+VFY_API vfy_status vfy_rope_append_full(vfy_ctx* ctx, const vfy_rotary* rotary, const uint16_t* q, int64_t q_stride,
+                                        const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                                        const int32_t* cu_q, const int32_t* seq_len, const int32_t* depth,
+                                        const int32_t* cu_chunks, const int32_t* slot_of_chunk, uint16_t* host_k,
+                                        uint16_t* host_v, int64_t num_host_chunks, uint16_t* k_pool,
+                                        uint16_t* v_pool, int num_slots, uint16_t* q_out, int num_seqs,
+                                        vfy_stream_t stream);
+
+/* vfy_rope_append_swa -- the same with the rows going to the ring, as in vfy_append_swa. */
+VFY_API vfy_status vfy_rope_append_swa(vfy_ctx* ctx, const vfy_rotary* rotary, const uint16_t* q, int64_t q_stride,
+                                       const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                                       const int32_t* cu_q, const int32_t* seq_len, const int32_t* depth,
+                                       const int32_t* ring_offset, uint16_t* k_ring, uint16_t* v_ring,
+                                       uint16_t* q_out, int num_seqs, vfy_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------------------------
+ * The 4-bit pool
+ * ---------------------------------------------------------------------------------------------
+ * Chunks may be held in 4 bits: 3.6 times as many tokens in the same memory, and 3.6 times fewer bytes to page in
+ * and to attend. A value is g * s * e: e a 4-bit float (sign, 2 exponent bits, 1 mantissa bit: 0, 1/2, 1, 3/2, 2, 3, 4,
+ * 6), s an e4m3 scale that 16 neighbouring channels of one token share, g (k_scale, v_scale) an fp32 scale of the
+ * whole tensor. s * e has 6 significant bits: exact in fp16 and bf16, so the tensor cores multiply exact values.
+ * One (chunk, KV head) of K or of V is one record of VFY_PACKED_BYTES(d) bytes:
+ *     codes   [d / 32][64 tokens][16 bytes]   bytes of channels 32 j .. 32 j + 31; the even channel in the low 4 bits
+ *     scales  [64 tokens][d / 16]             e4m3, not negative
+ * and a pool or store is [chunks][Hkv] such records, 16-byte aligned.
+ */
+#define VFY_PACKED_BYTES(d) (36 * (d))
+
+/*
+ * vfy_append_full_packed -- vfy_append_full into 4-bit chunks. For each 16 channels x of a row:
+ *     s = e4m3(max|x / g| / 6) (to the nearest, at most 448), e = (x / g) / s to the nearest, ties to the even code, at most 6
+ * (s = 0 gives e = 0). Store and pool get the same bytes. A group that holds a NaN or an infinity gets finite, otherwise
+ * unspecified values.
+ *  host_k, host_v  [num_host_chunks][Hkv] records (pinned host or device memory); k_pool, v_pool [num_slots][Hkv] records
+ *  k_scale, v_scale  g of K and of V, > 0 and finite
+ *  The other arguments and device errors are those of vfy_append_full.
+ */
+VFY_API vfy_status vfy_append_full_packed(vfy_ctx* ctx, const uint16_t* k_new, const uint16_t* v_new,
+                                          const int32_t* cu_q, const int32_t* seq_len, const int32_t* cu_chunks,
+                                          const int32_t* slot_of_chunk, uint8_t* host_k, uint8_t* host_v,
+                                          int64_t num_host_chunks, uint8_t* k_pool, uint8_t* v_pool, int num_slots,
+                                          float k_scale, float v_scale, int num_seqs, vfy_stream_t stream);
+
+/* vfy_page_in_packed -- vfy_page_in of 4-bit chunks: [chunks][Hkv] records, copied bit for bit. */
+VFY_API vfy_status vfy_page_in_packed(vfy_ctx* ctx, const uint8_t* host_k, const uint8_t* host_v,
+                                      int64_t num_host_chunks, uint8_t* k_pool, uint8_t* v_pool, int num_slots,
+                                      const int32_t* pagein_list, const int32_t* pagein_count, int num_seqs, int k,
+                                      vfy_stream_t stream);
+
+/*
+ * vfy_unpack_chunks -- 4-bit chunks as bf16: entry i of `slots` gives k_out[i], v_out[i] (g * s * e, rounded once).
+ *  k_pool, v_pool  [num_slots][Hkv] records (a pool, or a store with chunk indices as slots)
+ *  slots           int32 [num_chunks] (device);  num_chunks  host int >= 0
+ *  k_out, v_out    bf16 [num_chunks][Hkv][64][d]: the layout of a bf16 pool's chunks
+ * Device errors: a slot outside [0, num_slots): its chunk is left unwritten, VFY_EDEVICE_INPUT.
+ */
+VFY_API vfy_status vfy_unpack_chunks(vfy_ctx* ctx, const uint8_t* k_pool, const uint8_t* v_pool, int num_slots,
+                                     const int32_t* slots, int num_chunks, float k_scale, float v_scale,
+                                     uint16_t* k_out, uint16_t* v_out, vfy_stream_t stream);
+
+/*
+ * vfy_attend_full_packed -- vfy_attend_full over a pool of 4-bit chunks (a chain block; one row per sequence is plain
+ * decoding).
+ *  k_pool, v_pool    [num_slots][Hkv] records;  k_scale, v_scale  g of K and of V, finite and > 0
+ *  The other arguments, results and device errors are those of vfy_attend_full. Queries must be finite; scales of tokens
+ *  that some block query attends must not be NaN (vfy_append_full_packed writes none).
+ */
+VFY_API vfy_status vfy_attend_full_packed(vfy_ctx* ctx, const uint16_t* q, const int32_t* cu_q, const uint8_t* k_pool,
+                                          const uint8_t* v_pool, int num_slots, const int32_t* resident_ids,
+                                          const int32_t* resident_slots, const int32_t* cu_resident,
+                                          int max_resident_per_seq, const int32_t* seq_len, float k_scale,
+                                          float v_scale, uint16_t* out, float* lse, int num_seqs,
+                                          vfy_stream_t stream);
+
+/*
+ * vfy_accept_sampled -- acceptance of sampled drafts, and the next token drawn, by random numbers that the caller gives.
+ * Row r of sequence b has p_r(v) = exp(x_v / T_b) / sum of the row (x its logits). Draft j of D_b (token d) was drawn from
+ * q_j and is kept iff
+ *     u_j q_j(d) < p_j(d)
+ * n_b is the first refused draft, or D_b. The next token is drawn from w = max(p_n - q_n, 0) (n < D_b) or w = p_n
+ * (n = D_b): the token with the largest w_v / E_v, ties to the lowest index. With E_v exponentially distributed that
+ * is a draw in proportion to w, and the committed tokens are distributed as the target's own.
+ *  logits, logits_type, row_stride, vocab, cu_rows, max_rows   as in vfy_process_logits. -inf is a token that cannot
+ *                follow; a NaN counts as -inf; +inf entries share the whole row. One row per sequence is plain sampling
+ *  temperature   fp32 [B]   T_b >= 0. T_b = 0: the row's argmax has all of p (vfy_accept's rules: ties, NaN), and is the
+ *                next token
+ *  drafts        int32 [cu_rows[B] - B], packed as in vfy_accept
+ *  draft_probs   fp32 [cu_rows[B] - B][vocab]   q_j; NULL: the drafts were certain (q_j = 1 at d, 0 elsewhere)
+ *  uniform       fp32 [cu_rows[B] - B]   u_j in [0, 1)
+ *  noise         fp32 [B][vocab]         E_v > 0; an entry that is not (or is NaN or infinite) is never drawn
+ *  accepted_len, bonus, committed   as in vfy_accept
+ * drafts, draft_probs and uniform may be NULL where every sequence has one row. If w leaves nothing to draw, p_n is drawn
+ * from; if that leaves nothing, the row's argmax is taken.
+ * Device errors: a drafted token outside [0, vocab) (refused; nothing is taken off p), a temperature that is negative,
+ * NaN or infinite (taken as 0), rows out of range or a sequence without rows (its outputs are not written):
+ * VFY_EDEVICE_INPUT.
+ */
+VFY_API vfy_status vfy_accept_sampled(vfy_ctx* ctx, const void* logits, int logits_type, int64_t row_stride, int vocab,
+                                      const float* temperature, const int32_t* drafts, const float* draft_probs,
+                                      const float* uniform, const float* noise, const int32_t* cu_rows, int max_rows,
+                                      int32_t* accepted_len, int32_t* bonus, int32_t* committed, int num_seqs,
+                                      vfy_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -23,6 +23,10 @@ struct vfy_ctx {
   unsigned int* accept_counter;
   unsigned int* tree_counters;   // one per sequence (tree acceptance)
   vfy::TreePiece* tree_pieces;   // items cut between CTA pairs (tree attention)
+  // sampled acceptance: row statistics, race keys, tickets
+  float4* sample_stats;
+  unsigned long long* sample_keys;
+  unsigned int* sample_counters;
   // sticky device error word
   int* err;
   int full_splits;   // 0 = automatic
@@ -186,11 +190,16 @@ vfy_status vfy_create(const vfy_config* cfg_in, int device, vfy_ctx** out) {
             cudaMalloc(&ctx->accept_counter, sizeof(unsigned int)) == cudaSuccess &&
             cudaMalloc(&ctx->tree_counters, cfg.max_seqs * sizeof(unsigned int)) == cudaSuccess &&
             cudaMalloc(&ctx->tree_pieces, ctx->num_sms * sizeof(vfy::TreePiece)) == cudaSuccess &&
+            cudaMalloc(&ctx->sample_stats, (ctx->accept_rows_cap + 2 * ctx->num_sms) * sizeof(float4)) == cudaSuccess &&
+            cudaMalloc(&ctx->sample_keys, 3 * cfg.max_seqs * sizeof(unsigned long long)) == cudaSuccess &&
+            cudaMalloc(&ctx->sample_counters, cfg.max_seqs * sizeof(unsigned int)) == cudaSuccess &&
             cudaMalloc(&ctx->err, sizeof(int)) == cudaSuccess;
   if (ok)
     ok = cudaMemset(ctx->accept_keys, 0, ctx->accept_rows_cap * sizeof(unsigned long long)) == cudaSuccess &&
          cudaMemset(ctx->accept_counter, 0, sizeof(unsigned int)) == cudaSuccess &&
          cudaMemset(ctx->tree_counters, 0, cfg.max_seqs * sizeof(unsigned int)) == cudaSuccess &&
+         cudaMemset(ctx->sample_keys, 0, 3 * cfg.max_seqs * sizeof(unsigned long long)) == cudaSuccess &&
+         cudaMemset(ctx->sample_counters, 0, cfg.max_seqs * sizeof(unsigned int)) == cudaSuccess &&
          cudaMemset(ctx->err, 0, sizeof(int)) == cudaSuccess &&
          cudaMemset(ctx->part_ml, 0, parts * 2 * sizeof(float)) == cudaSuccess &&
          cudaDeviceSynchronize() == cudaSuccess;
@@ -214,6 +223,9 @@ void vfy_destroy(vfy_ctx* ctx) {
     cudaFree(ctx->accept_counter);
     cudaFree(ctx->tree_counters);
     cudaFree(ctx->tree_pieces);
+    cudaFree(ctx->sample_stats);
+    cudaFree(ctx->sample_keys);
+    cudaFree(ctx->sample_counters);
     cudaFree(ctx->err);
     (void)cudaGetLastError();
   }
@@ -916,6 +928,359 @@ vfy_status vfy_compact_swa(vfy_ctx* ctx, const int32_t* path, const int32_t* acc
   }
   VFY_CUDA(vfy::launch_compact(true, p, reinterpret_cast<cudaStream_t>(stream)));
   ++ctx->launches;
+  return VFY_OK;
+}
+
+// ------------------------------ rotation and append ------------------------------------------
+// Rows of `width` values, `stride` apart: 16-byte words of every row are aligned.
+static bool row_stride_ok(int64_t stride, int64_t width) {
+  return stride >= width && stride % 8 == 0 && stride <= (int64_t{1} << 32);
+}
+// Arguments that the three calls share (q and k may be absent in vfy_rope; the output rows of a call may be its input rows).
+static bool rope_params(const vfy_ctx* ctx, const vfy_rotary* r, const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                        int64_t k_stride, const int32_t* cu_q, const int32_t* seq_len, const int32_t* depth,
+                        uint16_t* q_out, int num_seqs, vfy::RopeParams* p) {
+  if (ctx == nullptr || r == nullptr || cu_q == nullptr || seq_len == nullptr) return false;
+  if (num_seqs < 1 || num_seqs > ctx->cfg.max_seqs) return false;
+  const vfy_config& c = ctx->cfg;
+  if (r->rot_dim < 0 || r->rot_dim > c.head_dim || r->rot_dim % 8 != 0) return false;
+  if ((r->rot_dim > 0) != (r->inv_freq != nullptr)) return false;
+  if ((reinterpret_cast<uintptr_t>(r->inv_freq) & 3u) != 0) return false;
+  if (r->interleaved != 0 && r->interleaved != 1) return false;
+  if (!std::isfinite(r->attention_factor) || !(r->eps >= 0.f) || !std::isfinite(r->eps)) return false;
+  if (!aligned16(r->q_norm) || !aligned16(r->k_norm)) return false;
+  const int64_t q_width = static_cast<int64_t>(c.num_q_heads) * c.head_dim;
+  if ((q != nullptr) != (q_out != nullptr)) return false;
+  if (q != nullptr && (!aligned16(q) || !aligned16(q_out) || !row_stride_ok(q_stride, q_width))) return false;
+  if (q != nullptr && q == q_out && q_stride != q_width) return false;
+  if (k != nullptr && (!aligned16(k) || !row_stride_ok(k_stride, static_cast<int64_t>(c.num_kv_heads) * c.head_dim)))
+    return false;
+  *p = {};
+  p->q = q;
+  p->k = k;
+  p->q_stride = q_stride;
+  p->k_stride = k_stride;
+  p->inv_freq = r->inv_freq;
+  p->rot = r->rot_dim;
+  p->interleaved = r->interleaved;
+  p->factor = r->attention_factor == 0.f ? 1.f : r->attention_factor;
+  p->q_norm = r->q_norm;
+  p->k_norm = r->k_norm;
+  p->eps = r->eps;
+  p->cu_q = cu_q;
+  p->seq_len = seq_len;
+  p->depth = depth;
+  p->num_seqs = num_seqs;
+  p->max_q = c.max_queries_per_seq;
+  p->token_cap = num_seqs * c.max_queries_per_seq;
+  p->hq = c.num_q_heads;
+  p->hkv = c.num_kv_heads;
+  p->head_dim = c.head_dim;
+  p->q_out = q_out;
+  p->err = ctx->err;
+  return true;
+}
+
+vfy_status vfy_rope(vfy_ctx* ctx, const vfy_rotary* rotary, const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                    int64_t k_stride, const int32_t* cu_q, const int32_t* seq_len, const int32_t* depth, uint16_t* q_out,
+                    uint16_t* k_out, int num_seqs, vfy_stream_t stream) {
+  vfy::RopeParams p;
+  VFY_REQUIRE(rope_params(ctx, rotary, q, q_stride, k, k_stride, cu_q, seq_len, depth, q_out, num_seqs, &p));
+  VFY_REQUIRE((k != nullptr) == (k_out != nullptr) && (q != nullptr || k != nullptr));
+  VFY_REQUIRE(aligned16(k_out));
+  VFY_REQUIRE(k == nullptr || k != k_out || k_stride == static_cast<int64_t>(p.hkv) * p.head_dim);
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return VFY_ECUDA;
+  p.k_dst = k_out;
+  VFY_CUDA(vfy::launch_rope(p, reinterpret_cast<cudaStream_t>(stream)));
+  ++ctx->launches;
+  return VFY_OK;
+}
+
+vfy_status vfy_rope_append_full(vfy_ctx* ctx, const vfy_rotary* rotary, const uint16_t* q, int64_t q_stride,
+                                const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                                const int32_t* cu_q, const int32_t* seq_len, const int32_t* depth,
+                                const int32_t* cu_chunks, const int32_t* slot_of_chunk, uint16_t* host_k,
+                                uint16_t* host_v, int64_t num_host_chunks, uint16_t* k_pool, uint16_t* v_pool,
+                                int num_slots, uint16_t* q_out, int num_seqs, vfy_stream_t stream) {
+  vfy::RopeParams p;
+  VFY_REQUIRE(rope_params(ctx, rotary, q, q_stride, k, k_stride, cu_q, seq_len, depth, q_out, num_seqs, &p));
+  VFY_REQUIRE(k != nullptr && v != nullptr && cu_chunks != nullptr && slot_of_chunk != nullptr);
+  VFY_REQUIRE(host_k != nullptr && host_v != nullptr && k_pool != nullptr && v_pool != nullptr);
+  VFY_REQUIRE(aligned16(v) && aligned16(host_k) && aligned16(host_v) && aligned16(k_pool) && aligned16(v_pool));
+  VFY_REQUIRE(row_stride_ok(v_stride, static_cast<int64_t>(p.hkv) * p.head_dim));
+  VFY_REQUIRE(num_host_chunks >= 1 && num_host_chunks <= INT_MAX && num_slots >= 1);
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return VFY_ECUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  void* store[2] = {host_k, host_v};
+  const vfy_status st = device_view(s, store, 2);
+  if (st != VFY_OK) return st;
+  p.v = v;
+  p.v_stride = v_stride;
+  p.cu_chunks = cu_chunks;
+  p.slot_of_chunk = slot_of_chunk;
+  p.host_k = static_cast<uint16_t*>(store[0]);
+  p.host_v = static_cast<uint16_t*>(store[1]);
+  p.num_host_chunks = num_host_chunks;
+  p.num_slots = num_slots;
+  p.k_dst = k_pool;
+  p.v_dst = v_pool;
+  VFY_CUDA(vfy::launch_rope(p, s));
+  ++ctx->launches;
+  return VFY_OK;
+}
+
+vfy_status vfy_rope_append_swa(vfy_ctx* ctx, const vfy_rotary* rotary, const uint16_t* q, int64_t q_stride,
+                               const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                               const int32_t* cu_q, const int32_t* seq_len, const int32_t* depth,
+                               const int32_t* ring_offset, uint16_t* k_ring, uint16_t* v_ring, uint16_t* q_out,
+                               int num_seqs, vfy_stream_t stream) {
+  vfy::RopeParams p;
+  VFY_REQUIRE(rope_params(ctx, rotary, q, q_stride, k, k_stride, cu_q, seq_len, depth, q_out, num_seqs, &p));
+  VFY_REQUIRE(k != nullptr && v != nullptr && ring_offset != nullptr && k_ring != nullptr && v_ring != nullptr);
+  VFY_REQUIRE(aligned16(v) && aligned16(k_ring) && aligned16(v_ring));
+  VFY_REQUIRE(row_stride_ok(v_stride, static_cast<int64_t>(p.hkv) * p.head_dim));
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return VFY_ECUDA;
+  p.v = v;
+  p.v_stride = v_stride;
+  p.ring_off = ring_offset;
+  p.ring_len = ctx->cfg.ring_len;
+  p.k_dst = k_ring;
+  p.v_dst = v_ring;
+  VFY_CUDA(vfy::launch_rope(p, reinterpret_cast<cudaStream_t>(stream)));
+  ++ctx->launches;
+  return VFY_OK;
+}
+
+// ------------------------------ 4-bit chunks -------------------------------------------------
+static bool tensor_scale_ok(float g) { return g > 0.f && std::isfinite(g); }
+
+vfy_status vfy_append_full_packed(vfy_ctx* ctx, const uint16_t* k_new, const uint16_t* v_new, const int32_t* cu_q,
+                                  const int32_t* seq_len, const int32_t* cu_chunks, const int32_t* slot_of_chunk,
+                                  uint8_t* host_k, uint8_t* host_v, int64_t num_host_chunks, uint8_t* k_pool,
+                                  uint8_t* v_pool, int num_slots, float k_scale, float v_scale, int num_seqs,
+                                  vfy_stream_t stream) {
+  VFY_REQUIRE(ctx != nullptr && k_new != nullptr && v_new != nullptr && cu_q != nullptr && seq_len != nullptr);
+  VFY_REQUIRE(cu_chunks != nullptr && slot_of_chunk != nullptr && host_k != nullptr && host_v != nullptr);
+  VFY_REQUIRE(k_pool != nullptr && v_pool != nullptr);
+  VFY_REQUIRE(aligned16(k_new) && aligned16(v_new) && aligned16(host_k) && aligned16(host_v) && aligned16(k_pool) &&
+              aligned16(v_pool));
+  VFY_REQUIRE(num_host_chunks >= 1 && num_host_chunks <= INT_MAX && num_slots >= 1);
+  VFY_REQUIRE(tensor_scale_ok(k_scale) && tensor_scale_ok(v_scale));
+  VFY_REQUIRE(num_seqs >= 1 && num_seqs <= ctx->cfg.max_seqs);
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return VFY_ECUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  void* store[2] = {host_k, host_v};
+  const vfy_status st = device_view(s, store, 2);
+  if (st != VFY_OK) return st;
+  vfy::PackedAppendParams p = {};
+  p.k_new = k_new;
+  p.v_new = v_new;
+  p.cu_q = cu_q;
+  p.seq_len = seq_len;
+  p.num_seqs = num_seqs;
+  p.max_q = ctx->cfg.max_queries_per_seq;
+  p.token_cap = num_seqs * ctx->cfg.max_queries_per_seq;
+  p.hkv = ctx->cfg.num_kv_heads;
+  p.head_dim = ctx->cfg.head_dim;
+  p.cu_chunks = cu_chunks;
+  p.slot_of_chunk = slot_of_chunk;
+  p.host_k = static_cast<uint8_t*>(store[0]);
+  p.host_v = static_cast<uint8_t*>(store[1]);
+  p.num_host_chunks = num_host_chunks;
+  p.num_slots = num_slots;
+  p.k_pool = k_pool;
+  p.v_pool = v_pool;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.err = ctx->err;
+  VFY_CUDA(vfy::launch_append_packed(p, s));
+  ++ctx->launches;
+  return VFY_OK;
+}
+
+vfy_status vfy_page_in_packed(vfy_ctx* ctx, const uint8_t* host_k, const uint8_t* host_v, int64_t num_host_chunks,
+                              uint8_t* k_pool, uint8_t* v_pool, int num_slots, const int32_t* pagein_list,
+                              const int32_t* pagein_count, int num_seqs, int k, vfy_stream_t stream) {
+  VFY_REQUIRE(ctx != nullptr && host_k != nullptr && host_v != nullptr && k_pool != nullptr && v_pool != nullptr);
+  VFY_REQUIRE(pagein_list != nullptr && pagein_count != nullptr);
+  VFY_REQUIRE(aligned16(host_k) && aligned16(host_v) && aligned16(k_pool) && aligned16(v_pool));
+  VFY_REQUIRE(num_host_chunks >= 1 && num_host_chunks <= INT_MAX && num_slots >= 1);
+  VFY_REQUIRE(num_seqs >= 1 && num_seqs <= ctx->cfg.max_seqs && k >= 1 && k <= vfy::kMaxSelectK);
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return VFY_ECUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  void* store[2] = {const_cast<uint8_t*>(host_k), const_cast<uint8_t*>(host_v)};
+  const vfy_status st = device_view(s, store, 2);
+  if (st != VFY_OK) return st;
+  // The same copy as vfy_page_in, of chunks of another size (a multiple of 16 bytes too).
+  vfy::PageInParams p;
+  p.host_k = static_cast<const uint16_t*>(store[0]);
+  p.host_v = static_cast<const uint16_t*>(store[1]);
+  p.num_host_chunks = num_host_chunks;
+  p.k_pool = reinterpret_cast<uint16_t*>(k_pool);
+  p.v_pool = reinterpret_cast<uint16_t*>(v_pool);
+  p.num_slots = num_slots;
+  p.list = pagein_list;
+  p.count = pagein_count;
+  p.num_seqs = num_seqs;
+  p.k = k;
+  p.chunk_elems = static_cast<long long>(ctx->cfg.num_kv_heads) * VFY_PACKED_BYTES(ctx->cfg.head_dim) / 2;
+  p.err = ctx->err;
+  p.parts = ctx->pagein_ctas > 0 ? ctx->pagein_ctas : 2;
+  VFY_CUDA(vfy::launch_page_in(p, s));
+  ++ctx->launches;
+  return VFY_OK;
+}
+
+vfy_status vfy_unpack_chunks(vfy_ctx* ctx, const uint8_t* k_pool, const uint8_t* v_pool, int num_slots,
+                             const int32_t* slots, int num_chunks, float k_scale, float v_scale, uint16_t* k_out,
+                             uint16_t* v_out, vfy_stream_t stream) {
+  VFY_REQUIRE(ctx != nullptr && k_pool != nullptr && v_pool != nullptr && num_slots >= 1 && num_chunks >= 0);
+  VFY_REQUIRE(tensor_scale_ok(k_scale) && tensor_scale_ok(v_scale));
+  if (num_chunks == 0) return VFY_OK;
+  VFY_REQUIRE(slots != nullptr && k_out != nullptr && v_out != nullptr);
+  VFY_REQUIRE(aligned16(k_pool) && aligned16(v_pool) && aligned16(k_out) && aligned16(v_out));
+  VFY_REQUIRE(static_cast<long long>(num_chunks) * ctx->cfg.num_kv_heads <= INT_MAX);
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return VFY_ECUDA;
+  vfy::UnpackParams p;
+  p.k_pool = k_pool;
+  p.v_pool = v_pool;
+  p.num_slots = num_slots;
+  p.slots = slots;
+  p.n = num_chunks;
+  p.hkv = ctx->cfg.num_kv_heads;
+  p.head_dim = ctx->cfg.head_dim;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.k_out = k_out;
+  p.v_out = v_out;
+  p.err = ctx->err;
+  VFY_CUDA(vfy::launch_unpack(p, reinterpret_cast<cudaStream_t>(stream)));
+  ++ctx->launches;
+  return VFY_OK;
+}
+
+vfy_status vfy_attend_full_packed(vfy_ctx* ctx, const uint16_t* q, const int32_t* cu_q, const uint8_t* k_pool,
+                                  const uint8_t* v_pool, int num_slots, const int32_t* resident_ids,
+                                  const int32_t* resident_slots, const int32_t* cu_resident, int max_resident_per_seq,
+                                  const int32_t* seq_len, float k_scale, float v_scale, uint16_t* out, float* lse,
+                                  int num_seqs, vfy_stream_t stream) {
+  VFY_REQUIRE(ctx != nullptr && q != nullptr && cu_q != nullptr && k_pool != nullptr && v_pool != nullptr);
+  VFY_REQUIRE(resident_ids != nullptr && resident_slots != nullptr && cu_resident != nullptr);
+  VFY_REQUIRE(seq_len != nullptr && out != nullptr);
+  VFY_REQUIRE(aligned16(q) && aligned16(k_pool) && aligned16(v_pool) && aligned16(out));
+  VFY_REQUIRE(lse == nullptr || (reinterpret_cast<uintptr_t>(lse) & 3u) == 0);
+  VFY_REQUIRE(num_seqs >= 1 && num_seqs <= ctx->cfg.max_seqs);
+  VFY_REQUIRE(num_slots >= 1 && max_resident_per_seq >= 0);
+  VFY_REQUIRE(tensor_scale_ok(k_scale) && tensor_scale_ok(v_scale));
+  const vfy_config& c = ctx->cfg;
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return VFY_ECUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  vfy::PackedAttnParams p;
+  p.q = q;
+  p.cu_q = cu_q;
+  p.seq_len = seq_len;
+  p.k_pool = k_pool;
+  p.v_pool = v_pool;
+  p.num_slots = num_slots;
+  p.res_ids = resident_ids;
+  p.res_slots = resident_slots;
+  p.cu_res = cu_resident;
+  p.hq = c.num_q_heads;
+  p.hkv = c.num_kv_heads;
+  p.group = p.hq / p.hkv;
+  p.head_dim = c.head_dim;
+  p.max_q = c.max_queries_per_seq;
+  p.row_tiles = ctx->row_tiles;
+  int splits = ctx->full_splits;
+  if (splits == 0) {
+    const long long items = static_cast<long long>(p.hkv) * num_seqs * p.row_tiles;
+    splits = clampi(ceil_div(ctx->num_sms * (num_seqs > 1 ? 4 : 1), items), 1, max_resident_per_seq > 0 ? max_resident_per_seq : 1);
+  }
+  p.num_splits = clampi(splits, 1, c.max_splits);
+  p.token_cap = num_seqs * c.max_queries_per_seq;
+  p.scale_log2 = ctx->scale * 1.4426950408889634f * k_scale;
+  p.v_scale = v_scale;
+  p.part_o = ctx->part_o;
+  p.part_ml = ctx->part_ml;
+  p.err = ctx->err;
+  VFY_CUDA(vfy::launch_attend_packed(p, num_seqs, s));
+  ++ctx->launches;
+  vfy::CombineParams cp;
+  cp.cu_q = cu_q;
+  cp.seq_len = seq_len;
+  cp.num_seqs = num_seqs;
+  cp.hq = p.hq;
+  cp.hkv = p.hkv;
+  cp.group = p.group;
+  cp.num_splits = p.num_splits;
+  cp.max_q = p.max_q;
+  cp.row_tiles = p.row_tiles;
+  cp.token_cap = p.token_cap;
+  cp.by_seq = false;
+  cp.stable_metadata = ctx->stable_metadata;
+  cp.part_o = ctx->part_o;
+  cp.part_ml = ctx->part_ml;
+  cp.out = out;
+  cp.lse = lse;
+  cp.err = ctx->err;
+  VFY_CUDA(vfy::launch_combine(c.head_dim, cp, s));
+  ++ctx->launches;
+  return VFY_OK;
+}
+
+vfy_status vfy_accept_sampled(vfy_ctx* ctx, const void* logits, int logits_type, int64_t row_stride, int vocab,
+                              const float* temperature, const int32_t* drafts, const float* draft_probs,
+                              const float* uniform, const float* noise, const int32_t* cu_rows, int max_rows,
+                              int32_t* accepted_len, int32_t* bonus, int32_t* committed, int num_seqs,
+                              vfy_stream_t stream) {
+  VFY_REQUIRE(ctx != nullptr && logits != nullptr && temperature != nullptr && noise != nullptr && cu_rows != nullptr);
+  VFY_REQUIRE(accepted_len != nullptr && bonus != nullptr && committed != nullptr);
+  VFY_REQUIRE(logits_type == VFY_LOGITS_F32 || logits_type == VFY_LOGITS_BF16);
+  const bool bf16 = logits_type == VFY_LOGITS_BF16;
+  VFY_REQUIRE(vocab >= 1 && vocab <= kMaxVocab && row_stride >= vocab);
+  VFY_REQUIRE((reinterpret_cast<uintptr_t>(logits) & (bf16 ? 1u : 3u)) == 0);
+  VFY_REQUIRE(((reinterpret_cast<uintptr_t>(draft_probs) | reinterpret_cast<uintptr_t>(noise)) & 3u) == 0);
+  VFY_REQUIRE(num_seqs >= 1 && num_seqs <= ctx->cfg.max_seqs);
+  VFY_REQUIRE(max_rows >= 1 && max_rows <= ctx->accept_rows_cap && max_rows <= 65535);
+  VFY_REQUIRE((drafts != nullptr && uniform != nullptr) || max_rows <= num_seqs);
+  VFY_REQUIRE(row_stride <= (INT64_MAX / 8) / max_rows);
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return VFY_ECUDA;
+  vfy::SampleParams p;
+  p.logits = logits;
+  p.stride = row_stride;
+  p.vocab = vocab;
+  p.temperature = temperature;
+  p.drafts = drafts;
+  p.probs = draft_probs;
+  p.uniform = uniform;
+  p.noise = noise;
+  p.cu_rows = cu_rows;
+  p.num_seqs = num_seqs;
+  p.max_rows = max_rows;
+  // As in vfy_accept: about two CTAs per SM over all rows, segments of at least 1024 entries (of whole 16-byte words).
+  p.parts = clampi(ceil_div(2LL * ctx->num_sms, max_rows), 1, ceil_div(vocab, 1024));
+  p.seg = (ceil_div(vocab, p.parts) + 7) & ~7;
+  p.parts = ceil_div(vocab, p.seg);
+  p.draw_parts = clampi(ceil_div(2LL * ctx->num_sms, num_seqs), 1, ceil_div(vocab, 1024));
+  p.draw_seg = ceil_div(vocab, p.draw_parts);
+  p.draw_parts = ceil_div(vocab, p.draw_seg);
+  p.accepted_len = accepted_len;
+  p.bonus = bonus;
+  p.committed = committed;
+  p.stats = ctx->sample_stats;
+  p.keys = ctx->sample_keys;
+  p.counters = ctx->sample_counters;
+  p.err = ctx->err;
+  VFY_CUDA(vfy::launch_accept_sampled(p, bf16, reinterpret_cast<cudaStream_t>(stream)));
+  ctx->launches += 2;
   return VFY_OK;
 }
 

@@ -1,0 +1,72 @@
+// 4-bit groups: 16 values in 8 bytes of e2m1 codes (the even value in a byte's low 4 bits) and one e4m3 scale.
+#pragma once
+
+#include <cstdint>
+
+namespace vfy {
+
+// Bytes of one (chunk, KV head) record of K or V.
+template <int HD>
+constexpr int kPackedBytes = 36 * HD;
+
+// A byte's two codes as fp16 values.
+__device__ __forceinline__ uint32_t e2m1_pair_f16(uint32_t byte) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 c, x0, x1, x2;\n\tmov.b32 {c, x0, x1, x2}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, c;\n\t}" : "=r"(r) : "r"(byte));
+  return r;
+}
+__device__ __forceinline__ float f16_value(uint32_t bits) {
+  float f;
+  asm("{\n\t.reg .f16 h;\n\tmov.b16 h, %1;\n\tcvt.f32.f16 %0, h;\n\t}" : "=f"(f) : "h"(static_cast<uint16_t>(bits)));
+  return f;
+}
+__device__ __forceinline__ float2 e2m1_pair(uint32_t byte) {
+  const uint32_t h = e2m1_pair_f16(byte);
+  return make_float2(f16_value(h & 0xffffu), f16_value(h >> 16));
+}
+// Two e4m3 bytes as fp16 values (the low byte in the low half).
+__device__ __forceinline__ uint32_t e4m3_pair_f16(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
+  return r;
+}
+__device__ __forceinline__ float e4m3_value(uint32_t byte) { return f16_value(e4m3_pair_f16(byte) & 0xffffu); }
+
+// The e4m3 byte nearest to x >= 0 (ties to even, at most 448; NaN gives 448).
+__device__ __forceinline__ uint32_t e4m3_of(float x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(fminf(x, 448.f)));
+  return r & 0xffu;
+}
+// Codes nearest to lo (low 4 bits) and hi: ties to the even code, at most 6 in size.
+__device__ __forceinline__ uint32_t e2m1_of(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 c;\n\tcvt.rn.satfinite.e2m1x2.f32 c, %2, %1;\n\tmov.b32 %0, {c, c, c, c};\n\t}"
+      : "=r"(r)
+      : "f"(lo), "f"(hi));
+  return r & 0xffu;
+}
+
+// 16 values to codes and their scale. Quotients are rounded as IEEE divisions: the scale's quotient can lie on a tie of
+// e4m3 only if it is exact, and so can a value's on a tie of e2m1.
+__device__ __forceinline__ uint2 pack_group(const float (&x)[16], uint32_t* scale) {
+  float top = 0.f;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(x[e]));
+  *scale = e4m3_of(__fdiv_rn(top, 6.f));
+  const float s = e4m3_value(*scale);
+  uint2 codes = make_uint2(0u, 0u);
+  if (s > 0.f) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t two = e2m1_of(__fdiv_rn(x[2 * e], s), __fdiv_rn(x[2 * e + 1], s));
+      if (e < 4)
+        codes.x |= two << (8 * e);
+      else
+        codes.y |= two << (8 * (e - 4));
+    }
+  }
+  return codes;
+}
+
+}  // namespace vfy

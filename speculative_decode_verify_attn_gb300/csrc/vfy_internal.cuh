@@ -285,6 +285,128 @@ struct AppendParams {
 };
 cudaError_t launch_append(bool ring, const AppendParams& p, cudaStream_t stream);
 
+// ------------------------------ rotation and append -------------------------------------------
+struct RopeParams {
+  const uint16_t* q;          // [T] rows of Hq * d, q_stride apart (null: no queries)
+  const uint16_t* k;          // [T] rows of Hkv * d
+  const uint16_t* v;
+  long long q_stride, k_stride, v_stride;
+  const float* inv_freq;      // [rot / 2]
+  int rot;                    // 0: no rotation
+  int interleaved;
+  float factor;               // of cos and sin
+  const uint16_t* q_norm;     // [d] or null
+  const uint16_t* k_norm;
+  float eps;
+  const int32_t* cu_q;        // [B+1]
+  const int32_t* seq_len;     // [B]
+  const int32_t* depth;       // [T] or null
+  int num_seqs;
+  int max_q;
+  int token_cap;              // host bound on cu_q[B]: the grid
+  int hq, hkv, head_dim;
+  uint16_t* q_out;            // [T][Hq][d]
+  uint16_t* k_dst;            // rows [T][Hkv][d], pool or ring
+  uint16_t* v_dst;            // pool or ring
+  // full layers (cu_chunks not null)
+  const int32_t* cu_chunks;
+  const int32_t* slot_of_chunk;
+  uint16_t* host_k;
+  uint16_t* host_v;
+  long long num_host_chunks;
+  int num_slots;
+  // window layers (ring_off not null)
+  const int32_t* ring_off;
+  int ring_len;
+  int* err;
+};
+cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream);
+
+// ------------------------------ 4-bit chunks --------------------------------------------------
+struct PackedAppendParams {
+  const uint16_t* k_new;      // [T][Hkv][d]
+  const uint16_t* v_new;
+  const int32_t* cu_q;        // [B+1]
+  const int32_t* seq_len;     // [B]
+  int num_seqs;
+  int max_q;
+  int token_cap;
+  int hkv, head_dim;
+  const int32_t* cu_chunks;
+  const int32_t* slot_of_chunk;
+  uint8_t* host_k;            // [chunks][Hkv] records
+  uint8_t* host_v;
+  long long num_host_chunks;
+  int num_slots;
+  uint8_t* k_pool;            // [slots][Hkv] records
+  uint8_t* v_pool;
+  float k_scale, v_scale;
+  int* err;
+};
+cudaError_t launch_append_packed(const PackedAppendParams& p, cudaStream_t stream);
+
+struct UnpackParams {
+  const uint8_t* k_pool;
+  const uint8_t* v_pool;
+  int num_slots;
+  const int32_t* slots;       // [n]
+  int n;
+  int hkv, head_dim;
+  float k_scale, v_scale;
+  uint16_t* k_out;            // [n][Hkv][64][d]
+  uint16_t* v_out;
+  int* err;
+};
+cudaError_t launch_unpack(const UnpackParams& p, cudaStream_t stream);
+
+struct PackedAttnParams {
+  const uint16_t* q;          // [T][Hq][d]
+  const int32_t* cu_q;        // [B+1]
+  const int32_t* seq_len;     // [B]
+  const uint8_t* k_pool;      // [slots][Hkv] records
+  const uint8_t* v_pool;
+  int num_slots;
+  const int32_t* res_ids;
+  const int32_t* res_slots;
+  const int32_t* cu_res;
+  int hq, hkv, group, head_dim;
+  int num_splits;
+  int max_q;
+  int row_tiles;              // of 128 rows, as the combine counts them
+  int token_cap;
+  float scale_log2;           // softmax scale * log2(e) * g of K
+  float v_scale;              // g of V
+  float* part_o;              // [B][row tiles][Hkv][splits][128][d]
+  float* part_ml;             // [B][row tiles][Hkv][splits][128][2] (m in log2 units, l)
+  int* err;
+};
+cudaError_t launch_attend_packed(const PackedAttnParams& p, int num_seqs, cudaStream_t stream);
+
+// ------------------------------ sampled acceptance --------------------------------------------
+struct SampleParams {
+  const void* logits;
+  long long stride;           // row stride, in entries
+  int vocab;
+  const float* temperature;   // [B]
+  const int32_t* drafts;      // [rows - B]
+  const float* probs;         // [rows - B][vocab] or null
+  const float* uniform;       // [rows - B]
+  const float* noise;         // [B][vocab]
+  const int32_t* cu_rows;     // [B+1]
+  int num_seqs;
+  int max_rows;
+  int parts, seg;             // CTAs per row of the first kernel, entries per CTA
+  int draw_parts, draw_seg;   // CTAs per sequence of the second, entries per CTA
+  int32_t* accepted_len;
+  int32_t* bonus;
+  int32_t* committed;
+  float4* stats;              // [max_rows * parts] workspace
+  unsigned long long* keys;   // [3 * max_seqs] workspace, zero between calls
+  unsigned int* counters;     // [max_seqs] workspace, zero between calls
+  int* err;
+};
+cudaError_t launch_accept_sampled(const SampleParams& p, bool bf16, cudaStream_t stream);
+
 // Launch with the programmatic-stream-serialization attribute so that a kernel's prologue can
 // overlap the tail of the kernel before it; every kernel calls griddepcontrol.wait before it
 // touches global memory.
@@ -336,6 +458,22 @@ cudaError_t ensure_smem_limit(K kernel, size_t bytes, size_t* done_per_device) {
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
   if (e == cudaSuccess && dev >= 0 && dev < 64) done_per_device[dev] = bytes;
   return e;
+}
+
+// The sequence that holds row t of a batch: the last b with cu[b] <= t (cu ascending, cu[0] taken as <= t), by all 32
+// lanes of a converged warp: one round trip to memory for up to 32 sequences.
+__device__ __forceinline__ int sequence_of(const int32_t* cu, int num_seqs, int t, int lane) {
+  int lo = 0, n = num_seqs;
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int at = lo + lane * step;
+    const bool before = lane == 0 || (at < lo + n && cu[at] <= t);
+    const int j = 31 - __clz(__ballot_sync(0xffffffffu, before));
+    const int next = lo + j * step;
+    n = min(step, lo + n - next);
+    lo = next;
+  }
+  return lo;
 }
 
 }  // namespace vfy

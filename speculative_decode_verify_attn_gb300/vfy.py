@@ -20,7 +20,9 @@ EXPORTS = ("vfy_create", "vfy_destroy", "vfy_get_status", "vfy_strerror", "vfy_s
            "vfy_accept_static", "vfy_launch_count", "vfy_append_full", "vfy_append_swa",
            "vfy_gate_depths", "vfy_test_wait_timeout", "vfy_set_stable_metadata", "vfy_set_pagein_ctas",
            "vfy_tree_plan", "vfy_attend_full_tree", "vfy_attend_swa_tree", "vfy_process_logits",
-           "vfy_count_tokens", "vfy_accept_tree", "vfy_compact_full", "vfy_compact_swa")
+           "vfy_count_tokens", "vfy_accept_tree", "vfy_compact_full", "vfy_compact_swa",
+           "vfy_rope", "vfy_rope_append_full", "vfy_rope_append_swa", "vfy_append_full_packed", "vfy_page_in_packed",
+           "vfy_unpack_chunks", "vfy_attend_full_packed", "vfy_accept_sampled")
 
 MAX_TREE_NODES = 256      # VFY_MAX_TREE_NODES
 TREE_WORDS = 8            # VFY_TREE_WORDS
@@ -85,6 +87,16 @@ def lib() -> ctypes.CDLL:
         L.vfy_accept_tree.argtypes = [_P, _P, _I, _P, _P, _P, _I, _P, _P, _P, _P, _I, _P]
         L.vfy_compact_full.argtypes = [_P, _P, _P, _P, _P, _P, _P, _I, _P, _P, ctypes.c_int64, _P, _P, _I, _I, _P]
         L.vfy_compact_swa.argtypes = [_P, _P, _P, _P, _P, _P, _I, _P, _P, _I, _P]
+        i64, f32 = ctypes.c_int64, ctypes.c_float
+        L.vfy_rope.argtypes = [_P, _P, _P, i64, _P, i64, _P, _P, _P, _P, _P, _I, _P]
+        L.vfy_rope_append_full.argtypes = [_P, _P, _P, i64, _P, i64, _P, i64, _P, _P, _P, _P, _P, _P, _P, i64, _P, _P, _I, _P,
+                                           _I, _P]
+        L.vfy_rope_append_swa.argtypes = [_P, _P, _P, i64, _P, i64, _P, i64, _P, _P, _P, _P, _P, _P, _P, _I, _P]
+        L.vfy_append_full_packed.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _P, i64, _P, _P, _I, f32, f32, _I, _P]
+        L.vfy_page_in_packed.argtypes = [_P, _P, _P, i64, _P, _P, _I, _P, _P, _I, _I, _P]
+        L.vfy_unpack_chunks.argtypes = [_P, _P, _P, _I, _P, _I, f32, f32, _P, _P, _P]
+        L.vfy_attend_full_packed.argtypes = [_P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _P, f32, f32, _P, _P, _I, _P]
+        L.vfy_accept_sampled.argtypes = [_P, _P, _I, i64, _I, _P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _P]
         L.vfy_launch_count.argtypes = [_P]
         L.vfy_launch_count.restype = ctypes.c_ulonglong
         for name in EXPORTS:
@@ -457,3 +469,161 @@ def vfy_compact_swa(ctx: Context, path, accepted_len, cu_q, seq_len, ring_offset
         ctx.handle, _ptr(ctx, path, I32, "path"), _ptr(ctx, accepted_len, I32, "accepted_len"),
         _ptr(ctx, cu_q, I32, "cu_q"), _ptr(ctx, seq_len, I32, "seq_len"), _ptr(ctx, ring_offset, I32, "ring_offset"),
         len(k_ring), kr, vr, num_seqs, _raw_stream(ctx, stream)), "vfy_compact_swa")
+
+
+# ---------------------------------------------------------------------------------------------
+# Position rotation and append
+# ---------------------------------------------------------------------------------------------
+
+class Rope:
+    """How a layer normalises and rotates its queries and keys (vfy_rotary). Keeps the tensors alive: build it once
+    per layer. `inv_freq`: float32 [rot_dim / 2] on the device (None: no rotation); `q_norm`, `k_norm`: bf16 [d]."""
+
+    class _Struct(ctypes.Structure):
+        _fields_ = [("inv_freq", _P), ("rot_dim", _I), ("interleaved", _I), ("attention_factor", ctypes.c_float),
+                    ("q_norm", _P), ("k_norm", _P), ("eps", ctypes.c_float)]
+
+    def __init__(self, inv_freq=None, rot_dim: int | None = None, interleaved: bool = False, attention_factor: float = 1.0,
+                 q_norm=None, k_norm=None, eps: float = 1e-6):
+        rot_dim = 2 * (0 if inv_freq is None else inv_freq.numel()) if rot_dim is None else int(rot_dim)
+        if inv_freq is not None and inv_freq.numel() != rot_dim // 2:
+            raise ValueError(f"inv_freq must have rot_dim / 2 = {rot_dim // 2} entries, got {inv_freq.numel()}")
+        self.tensors = (inv_freq, q_norm, k_norm)
+        self.norm_dims = {t.numel() for t in (q_norm, k_norm) if t is not None}
+        self.struct = Rope._Struct(_dev(inv_freq, F32, "inv_freq"), rot_dim, 1 if interleaved else 0, attention_factor,
+                                   _dev(q_norm, BF16, "q_norm"), _dev(k_norm, BF16, "k_norm"), eps)
+        self.at = ctypes.addressof(self.struct)
+        self.devices = {t.get_device() for t in self.tensors if t is not None}
+
+
+def _rows(ctx, t, heads: int, name: str):
+    """Address and row stride of bf16 rows [T][heads][d] (or [T][heads * d]), whose rows may lie further apart."""
+    if t is None:
+        return None, 0
+    d = ctx.cfg.head_dim
+    shape, step = t.shape, t.stride()
+    if t.dtype not in BF16 or _DEVICE_OF(t) != ctx.device:
+        raise TypeError(f"{name} must be a bf16 tensor on cuda:{ctx.device}, got {t.dtype} on {t.device}")
+    if not (shape[1:] == (heads, d) and step[2] == 1 and (step[1] == d or heads == 1)
+            or shape[1:] == (heads * d,) and step[1] == 1):
+        raise ValueError(f"{name} must be [rows][{heads}][{d}] with packed rows, got {tuple(shape)} with strides {step}")
+    return _DATA_PTR(t), step[0] if shape[0] > 1 else max(step[0], heads * d)
+
+
+def _rope_args(ctx, rope: Rope, q, k):
+    if not rope.devices <= {ctx.device}:
+        raise ValueError(f"the rotation is on cuda:{sorted(rope.devices)}, the context on cuda:{ctx.device}")
+    if not rope.norm_dims <= {ctx.cfg.head_dim}:
+        raise ValueError(f"q_norm and k_norm must have {ctx.cfg.head_dim} entries")
+    return (rope.at, *_rows(ctx, q, ctx.cfg.num_q_heads, "q"), *_rows(ctx, k, ctx.cfg.num_kv_heads, "k"))
+
+
+def vfy_rope(ctx: Context, rope: Rope, q, k, cu_q, seq_len, depth, q_out, k_out, num_seqs: int, stream=None):
+    """q, k: bf16 rows [T][heads][d], which may be views of a wider matrix; q_out, k_out: contiguous, or q, k themselves."""
+    _check(lib().vfy_rope(
+        ctx.handle, *_rope_args(ctx, rope, q, k), _ptr(ctx, cu_q, I32, "cu_q"), _ptr(ctx, seq_len, I32, "seq_len"),
+        _ptr(ctx, depth, I32, "depth"), _ptr(ctx, q_out, BF16, "q_out"), _ptr(ctx, k_out, BF16, "k_out"), num_seqs,
+        _raw_stream(ctx, stream)), "vfy_rope")
+
+
+def _store(ctx, t, dtypes, name: str):
+    """Address of a chunk store: on the context's device, or in (pinned) host memory."""
+    return _ptr(ctx, t, dtypes, name) if t.is_cuda else _host(t, dtypes, name)
+
+
+def vfy_rope_append_full(ctx: Context, rope: Rope, q, k, v, cu_q, seq_len, depth, cu_chunks, slot_of_chunk, host_k, host_v,
+                         num_host_chunks: int, k_pool, v_pool, num_slots: int, q_out, num_seqs: int, stream=None):
+    _check(lib().vfy_rope_append_full(
+        ctx.handle, *_rope_args(ctx, rope, q, k), *_rows(ctx, v, ctx.cfg.num_kv_heads, "v"),
+        _ptr(ctx, cu_q, I32, "cu_q"), _ptr(ctx, seq_len, I32, "seq_len"), _ptr(ctx, depth, I32, "depth"),
+        _ptr(ctx, cu_chunks, I32, "cu_chunks"), _ptr(ctx, slot_of_chunk, I32, "slot_of_chunk"),
+        _store(ctx, host_k, BF16, "host_k"), _store(ctx, host_v, BF16, "host_v"), num_host_chunks,
+        _ptr(ctx, k_pool, BF16, "k_pool"), _ptr(ctx, v_pool, BF16, "v_pool"), num_slots,
+        _ptr(ctx, q_out, BF16, "q_out"), num_seqs, _raw_stream(ctx, stream)), "vfy_rope_append_full")
+
+
+def vfy_rope_append_swa(ctx: Context, rope: Rope, q, k, v, cu_q, seq_len, depth, ring_offset, k_ring, v_ring, q_out,
+                        num_seqs: int, stream=None):
+    _check(lib().vfy_rope_append_swa(
+        ctx.handle, *_rope_args(ctx, rope, q, k), *_rows(ctx, v, ctx.cfg.num_kv_heads, "v"),
+        _ptr(ctx, cu_q, I32, "cu_q"), _ptr(ctx, seq_len, I32, "seq_len"), _ptr(ctx, depth, I32, "depth"),
+        _ptr(ctx, ring_offset, I32, "ring_offset"), _ptr(ctx, k_ring, BF16, "k_ring"), _ptr(ctx, v_ring, BF16, "v_ring"),
+        _ptr(ctx, q_out, BF16, "q_out"), num_seqs, _raw_stream(ctx, stream)), "vfy_rope_append_swa")
+
+
+# ---------------------------------------------------------------------------------------------
+# The 4-bit pool
+# ---------------------------------------------------------------------------------------------
+
+U8 = (torch.uint8,)
+
+
+def packed_bytes(head_dim: int) -> int:
+    """Bytes of one (chunk, KV head) record of K or V (VFY_PACKED_BYTES): pools are uint8 [slots][Hkv][this]."""
+    return 36 * head_dim
+
+
+def vfy_append_full_packed(ctx: Context, k_new, v_new, cu_q, seq_len, cu_chunks, slot_of_chunk, host_k, host_v,
+                           num_host_chunks: int, k_pool, v_pool, num_slots: int, k_scale: float, v_scale: float,
+                           num_seqs: int, stream=None):
+    _check(lib().vfy_append_full_packed(
+        ctx.handle, _ptr(ctx, k_new, BF16, "k_new"), _ptr(ctx, v_new, BF16, "v_new"), _ptr(ctx, cu_q, I32, "cu_q"),
+        _ptr(ctx, seq_len, I32, "seq_len"), _ptr(ctx, cu_chunks, I32, "cu_chunks"),
+        _ptr(ctx, slot_of_chunk, I32, "slot_of_chunk"), _store(ctx, host_k, U8, "host_k"), _store(ctx, host_v, U8, "host_v"),
+        num_host_chunks, _ptr(ctx, k_pool, U8, "k_pool"), _ptr(ctx, v_pool, U8, "v_pool"), num_slots, k_scale, v_scale,
+        num_seqs, _raw_stream(ctx, stream)), "vfy_append_full_packed")
+
+
+def vfy_page_in_packed(ctx: Context, host_k, host_v, num_host_chunks: int, k_pool, v_pool, num_slots: int, pagein_list,
+                       pagein_count, num_seqs: int, k: int, stream=None):
+    _check(lib().vfy_page_in_packed(
+        ctx.handle, _store(ctx, host_k, U8, "host_k"), _store(ctx, host_v, U8, "host_v"), num_host_chunks,
+        _ptr(ctx, k_pool, U8, "k_pool"), _ptr(ctx, v_pool, U8, "v_pool"), num_slots,
+        _ptr(ctx, pagein_list, I32, "pagein_list"), _ptr(ctx, pagein_count, I32, "pagein_count"), num_seqs, k,
+        _raw_stream(ctx, stream)), "vfy_page_in_packed")
+
+
+def vfy_unpack_chunks(ctx: Context, k_pool, v_pool, num_slots: int, slots, num_chunks: int, k_scale: float, v_scale: float,
+                      k_out, v_out, stream=None):
+    _check(lib().vfy_unpack_chunks(
+        ctx.handle, _ptr(ctx, k_pool, U8, "k_pool"), _ptr(ctx, v_pool, U8, "v_pool"), num_slots,
+        _ptr(ctx, slots, I32, "slots"), num_chunks, k_scale, v_scale, _ptr(ctx, k_out, BF16, "k_out"),
+        _ptr(ctx, v_out, BF16, "v_out"), _raw_stream(ctx, stream)), "vfy_unpack_chunks")
+
+
+def vfy_attend_full_packed(ctx: Context, q, cu_q, k_pool, v_pool, num_slots: int, resident_ids, resident_slots, cu_resident,
+                           max_resident_per_seq: int, seq_len, k_scale: float, v_scale: float, out, lse, num_seqs: int,
+                           stream=None):
+    _check(lib().vfy_attend_full_packed(
+        ctx.handle, _ptr(ctx, q, BF16, "q"), _ptr(ctx, cu_q, I32, "cu_q"), _ptr(ctx, k_pool, U8, "k_pool"),
+        _ptr(ctx, v_pool, U8, "v_pool"), num_slots, _ptr(ctx, resident_ids, I32, "resident_ids"),
+        _ptr(ctx, resident_slots, I32, "resident_slots"), _ptr(ctx, cu_resident, I32, "cu_resident"), max_resident_per_seq,
+        _ptr(ctx, seq_len, I32, "seq_len"), k_scale, v_scale, _ptr(ctx, out, BF16, "out"), _ptr(ctx, lse, F32, "lse"),
+        num_seqs, _raw_stream(ctx, stream)), "vfy_attend_full_packed")
+
+
+# ---------------------------------------------------------------------------------------------
+# Sampled acceptance
+# ---------------------------------------------------------------------------------------------
+
+def vfy_accept_sampled(ctx: Context, logits, vocab: int, temperature, drafts, draft_probs, uniform, noise, cu_rows,
+                       max_rows: int, accepted_len, bonus, committed, num_seqs: int, stream=None):
+    """`logits`: fp32 or bf16 [rows][vocab]; its rows may be further apart than `vocab` entries. `draft_probs` (fp32
+    [drafts][vocab], None: certain drafts), `uniform` (fp32, one a draft) and `noise` (fp32 [B][vocab], exponentially
+    distributed) are the caller's."""
+    if _DEVICE_OF(logits) != ctx.device or logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"logits must be a float32 or bfloat16 tensor on the context's device, got {logits.dtype} on "
+                        f"{logits.device}")
+    shape, step = logits.shape, logits.stride()
+    if len(shape) != 2 or step[1] != 1 or shape[1] < vocab:
+        raise ValueError("logits must be [rows][vocab] with contiguous rows")
+    for t, name in ((noise, "noise"), (draft_probs, "draft_probs")):
+        if t is not None and t.shape[-1] != vocab:
+            raise ValueError(f"{name} must have {vocab} entries a row, got {tuple(t.shape)}")
+    _check(lib().vfy_accept_sampled(
+        ctx.handle, _DATA_PTR(logits), 1 if logits.dtype == torch.bfloat16 else 0, step[0] if shape[0] > 1 else shape[1],
+        vocab, _ptr(ctx, temperature, F32, "temperature"), _ptr(ctx, drafts, I32, "drafts"),
+        _ptr(ctx, draft_probs, F32, "draft_probs"), _ptr(ctx, uniform, F32, "uniform"), _ptr(ctx, noise, F32, "noise"),
+        _ptr(ctx, cu_rows, I32, "cu_rows"), max_rows, _ptr(ctx, accepted_len, I32, "accepted_len"),
+        _ptr(ctx, bonus, I32, "bonus"), _ptr(ctx, committed, I32, "committed"), num_seqs, _raw_stream(ctx, stream)),
+        "vfy_accept_sampled")
