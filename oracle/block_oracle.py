@@ -78,11 +78,11 @@ def record_values(records, d):
 
 
 def attend_packed_seq(q, k_pool, v_pool, ids, slots, L, gk=1.0, gv=1.0, scale=None):
-    """One sequence: q [n][Hq][d] (fp64), pools uint8 [slots][Hkv][36 d]. Returns out, lse and sum_j p_j |v_j|."""
+    """One sequence: q [n][Hq][d] (fp64), pools uint8 [slots][Hkv][36 d]. Returns out, lse, sum_j p_j |v_j| and sum_j |v_j|."""
     n, hq, d = q.shape
     hkv = k_pool.shape[1]
     scale = 1 / np.sqrt(d) if scale is None else scale
-    out, mag = np.zeros((n, hq, d)), np.zeros((n, hq, d))
+    out, mag, all_v = np.zeros((n, hq, d)), np.zeros((n, hq, d)), np.zeros((n, hq, d))
     lse = np.full((n, hq), -np.inf)
     ids, slots = np.asarray(ids, dtype=np.int64), np.asarray(slots, dtype=np.int64)
     ok = (slots >= 0) & (slots < k_pool.shape[0]) & (ids >= 0)
@@ -101,8 +101,8 @@ def attend_packed_seq(q, k_pool, v_pool, ids, slots, L, gk=1.0, gv=1.0, scale=No
                 at = (i, h * (hq // hkv) + g)
                 lse[at] = m + np.log(p.sum())
                 p /= p.sum()
-                out[at], mag[at] = p @ v[see], p @ np.abs(v[see])
-    return out, lse, mag
+                out[at], mag[at], all_v[at] = p @ v[see], p @ np.abs(v[see]), np.abs(v[see]).sum(0)
+    return out, lse, mag, all_v
 
 
 def accept_sampled(logits, temperature, drafts, probs, uniform, noise, cu_rows):

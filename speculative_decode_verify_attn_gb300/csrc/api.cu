@@ -1198,10 +1198,17 @@ vfy_status vfy_attend_full_packed(vfy_ctx* ctx, const uint16_t* q, const int32_t
   p.head_dim = c.head_dim;
   p.max_q = c.max_queries_per_seq;
   p.row_tiles = ctx->row_tiles;
+  // Row tiles of equal size (in whole groups of eight rows).
+  const int block_rows = c.max_queries_per_seq * p.group;
+  p.n_tiles = ceil_div(block_rows, vfy::packed_tile_rows());
+  p.tile_rows = (ceil_div(block_rows, p.n_tiles) + 7) & ~7;
+  p.n_tiles = ceil_div(block_rows, p.tile_rows);
+  VFY_REQUIRE(static_cast<long long>(num_seqs) * p.n_tiles <= 65535);
   int splits = ctx->full_splits;
   if (splits == 0) {
-    const long long items = static_cast<long long>(p.hkv) * num_seqs * p.row_tiles;
-    splits = clampi(ceil_div(ctx->num_sms * (num_seqs > 1 ? 4 : 1), items), 1, max_resident_per_seq > 0 ? max_resident_per_seq : 1);
+    const long long items = static_cast<long long>(p.hkv) * num_seqs * p.n_tiles;
+    const int tiles = ceil_div(max_resident_per_seq, 2);
+    splits = clampi(num_seqs > 1 ? ceil_div(4 * ctx->num_sms, items) : static_cast<int>(ctx->num_sms / items), 1, tiles > 0 ? tiles : 1);
   }
   p.num_splits = clampi(splits, 1, c.max_splits);
   p.token_cap = num_seqs * c.max_queries_per_seq;
@@ -1209,6 +1216,8 @@ vfy_status vfy_attend_full_packed(vfy_ctx* ctx, const uint16_t* q, const int32_t
   p.v_scale = v_scale;
   p.part_o = ctx->part_o;
   p.part_ml = ctx->part_ml;
+  p.timeout_test_ns = ctx->timeout_test_ns;
+  p.stable_metadata = ctx->stable_metadata;
   p.err = ctx->err;
   VFY_CUDA(vfy::launch_attend_packed(p, num_seqs, s));
   ++ctx->launches;

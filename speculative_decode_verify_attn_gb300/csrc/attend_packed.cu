@@ -1,4 +1,21 @@
-// Attention of a block over a pool of 4-bit chunks.
+// Attention of a block over a pool of 4-bit chunks, on the tensor cores with the operands exchanged: a tile's 128 keys are
+// the M = 128 side of both products and the block's rows (queries x q-heads of one KV head, at most 80) the N side,
+//     S^T [128 keys][rows] = K Q^T,    O^T [d][rows] += V^T P^T,
+// so that the work follows the rows a block has: one token of G = 4 is N = 16, a block of 17 is N = 80. With the rows as M (as
+// in the bf16 layers) a 4-bit tile would be bound by the 128 rows' tensor time.
+//
+// A value is g s e; s e has 6 significant bits, so the operands in fp16 are exact. Queries are bf16: the tile's are scaled by
+// one power of two that puts the largest at 2^14, and fp16 holds all 8 bits of what is above 2^-28 of it. Weights P are
+// fp16 too (half a step, 2^-11): a row's reference is put 7 below its maximum (log2), weights grow to 2^15 before the
+// reference moves, and what fp16 drops (below 2^-25) is 2^-32 of the largest weight.
+//
+// One CTA per (split, KV head, sequence and row tile), a contiguous run of tiles of two chunks. Roles:
+//   warps 0-3, 4-7   softmax of even / odd tiles: a lane is a key, its 32-bit columns are the rows. Two groups with a
+//                    reference, row sums and O of their own, merged at the end; a group has two tiles' time for one.
+//   warps 8-11       K: a lane reads its key's codes and scales, writes fp16 into tensor memory (the A operand of S)
+//   warps 12-15      V: fp16 into shared memory, channels contiguous (the A operand of O^T, M-major)
+//   warp 16          bulk copies of the records (contiguous: no tensor map), and the tiles' geometry
+//   warp 17          tensor memory, and the MMA issuer (one lane)
 #include <cuda_bf16.h>
 
 #include "packed.cuh"
@@ -8,121 +25,664 @@
 namespace vfy {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kGroups = 5;                // warpgroups: softmax 0 and 1, K, V, the rest
+constexpr int kThreads = kGroups * 128;
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 152, kRegsUnpack = 64, kRegsRest = 40;
+static_assert(2 * kRegsSoftmax + 2 * kRegsUnpack + kRegsRest <= kGroups * kRegsLaunch, "registers the CTA was launched with");
+constexpr int kProducerWarp = 16, kMmaWarp = 17;
+constexpr int kKeys = 2 * kChunk;         // keys of a tile
+constexpr int kMaxN = 80;                 // rows of a tile: the softmax threads hold a partial sum of each
+constexpr int kStages = 4;
+constexpr int kGeo = 16;                  // tile-geometry ring: more than the tiles between producer and softmax
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColK = 0;             // two K tiles of up to 64 columns (two fp16 channels each)
+constexpr uint32_t kColS = 128;           // S^T of the two groups, 96 columns apart
+constexpr uint32_t kColO = 320;           // O^T of the two groups
+constexpr float kTop = 7.f;               // a row's maximum when its reference is set (log2)
+constexpr float kLimit = 15.f;            // the reference moves when a weight would pass 2^15
 
 template <int HD>
-struct Shape {
-  static constexpr int kKStride = HD + 1;
-  static constexpr int kSmemFloats = kChunk * kKStride + kChunk * HD + kMaxRows * HD + 2 * kMaxRows;
+struct Cfg {
+  static constexpr int kRecord = kPackedBytes<HD>;
+  static constexpr int kStageBytes = 4 * kRecord;                // K and V of two chunks
+  static constexpr int kBoxBytes = kKeys * 128;                  // 64 columns of 128 keys
+  static constexpr int kVBytes = 2 * kBoxBytes;                  // M = 128: d = 64 leaves the second box zero
+  static constexpr int kPBytes = 2 * kBoxBytes;
+  static constexpr int kQBoxBytes = kMaxN * 128;
+  static constexpr int kQBytes = (HD / 64) * kQBoxBytes;
+  static constexpr int kVOffset = 0;
+  static constexpr int kPOffset = 2 * kVBytes;
+  static constexpr int kQOffset = kPOffset + 2 * kPBytes;
+  static constexpr int kStageOffset = kQOffset + kQBytes;
+  static constexpr int kBarOffset = kStageOffset + kStages * kStageBytes;
+  static constexpr int kBarBytes = 6144;
+  static constexpr int kSmemBytes = kBarOffset + kBarBytes + 1024;
+  static_assert(kRecord % 16 == 0 && kStageBytes % 128 == 0, "bulk copies");
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
-// One CTA per (split, KV head, sequence and row tile): its chunks one by one, read as fp32 into shared memory; a warp per
-// row, a lane per key, then a lane per channel.
+struct Shared {
+  uint64_t full[kStages], empty[kStages];
+  uint64_t geo_full[kGeo];
+  uint64_t k_ready[2], v_ready[2];
+  uint64_t s_done[2];                     // S of a tile: its S^T is there, its K is free
+  uint64_t p_ready[2];                    // a tile's P is written, its S^T read
+  uint64_t pv_done[2];                    // O^T holds the tile, its P and V are free
+  uint64_t q_ready, drain, never;
+  uint32_t tmem_base;
+  int abort;
+  unsigned q_top;                         // largest |q| of the tile, as bf16 bits
+  int base[kGeo][2], valid[kGeo][2];      // per chunk of a tile
+  alignas(16) float neg_ref[2][kMaxN];    // [group] minus the rows' reference, log2 units
+  alignas(16) float limit[2][kMaxN];      // S value above which the reference moves
+  alignas(16) float alpha[2][kMaxN];
+  alignas(16) float part[2][4][kMaxN];    // [group][warp]: maxima, at the end sums
+};
+static_assert(sizeof(Shared) <= Cfg<128>::kBarBytes, "barrier block");
+
+struct Work {
+  int b, h, s;
+  int q0, nq, L;
+  int row0, rows;          // block rows of this CTA
+  int r0, nres;            // resident list
+  int tb, nt;              // tiles
+  bool bad;
+};
+
+__device__ __forceinline__ Work make_work(const PackedAttnParams& p) {
+  Work w;
+  w.s = blockIdx.x;
+  w.h = blockIdx.y;
+  w.b = static_cast<int>(blockIdx.z / static_cast<unsigned>(p.n_tiles));
+  const int rt = static_cast<int>(blockIdx.z) - w.b * p.n_tiles;
+  const int c0 = p.cu_q[w.b], c1 = p.cu_q[w.b + 1], cr0 = p.cu_res[w.b], cr1 = p.cu_res[w.b + 1];
+  w.L = p.seq_len[w.b];
+  w.q0 = c0;
+  w.nq = c1 - c0;
+  w.row0 = rt * p.tile_rows;
+  w.r0 = cr0;
+  w.nres = max(0, cr1 - cr0);
+  w.rows = w.tb = w.nt = 0;
+  w.bad = w.nq < 0 || w.nq > p.max_q || w.L < w.nq || static_cast<unsigned>(c0) > static_cast<unsigned>(p.token_cap - w.nq);
+  if (w.bad) return w;
+  w.rows = min(p.tile_rows, max(0, w.nq * p.group - w.row0));
+  if (w.rows == 0) return w;
+  const unsigned tiles = (static_cast<unsigned>(w.nres) + 1) / 2, ns = static_cast<unsigned>(p.num_splits);
+  // (splits <= 64 and tiles < 2^26: 32-bit products)
+  w.tb = static_cast<int>(static_cast<unsigned>(w.s) * tiles / ns);
+  w.nt = static_cast<int>(static_cast<unsigned>(w.s + 1) * tiles / ns) - w.tb;
+  return w;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Eight codes (a 32-bit word) times a scale (in both halves): eight fp16 values, two a register.
+__device__ __forceinline__ void unpack_word(uint32_t codes, uint32_t scale2, uint32_t* out) {
+  uint32_t a, b, c, d;
+  asm("{\n\t.reg .b8 x0, x1, x2, x3;\n\tmov.b32 {x0, x1, x2, x3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, x0;\n\tcvt.rn.f16x2.e2m1x2 %1, x1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, x2;\n\tcvt.rn.f16x2.e2m1x2 %3, x3;\n\t}"
+      : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+      : "r"(codes));
+  out[0] = mul_f16x2(a, scale2);
+  out[1] = mul_f16x2(b, scale2);
+  out[2] = mul_f16x2(c, scale2);
+  out[3] = mul_f16x2(d, scale2);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// One value per row of eight from 32 lanes: lane r (r < 8, and every lane alike modulo 8) gets row r's sum.
+__device__ __forceinline__ float sum_rows8(const float* l, int lane) {
+  float a[4], b[2], c;
+  const bool h4 = lane & 4, h2 = lane & 2, h1 = lane & 1;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float other = __shfl_xor_sync(0xffffffffu, h4 ? l[i] : l[i + 4], 4);
+    a[i] = (h4 ? l[i + 4] : l[i]) + other;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float other = __shfl_xor_sync(0xffffffffu, h2 ? a[i] : a[i + 2], 2);
+    b[i] = (h2 ? a[i + 2] : a[i]) + other;
+  }
+  const float other = __shfl_xor_sync(0xffffffffu, h1 ? b[0] : b[1], 1);
+  c = (h1 ? b[1] : b[0]) + other;
+  c += __shfl_xor_sync(0xffffffffu, c, 8);
+  c += __shfl_xor_sync(0xffffffffu, c, 16);
+  return c;
+}
+
 template <int HD>
-__global__ void __launch_bounds__(kThreads) attend_packed_kernel(const PackedAttnParams p) {
-  constexpr int kStride = Shape<HD>::kKStride;
-  constexpr int PER = HD / 32;
-  extern __shared__ float smem[];
-  float* sk = smem;
-  float* sv = sk + kChunk * kStride;
-  float* so = sv + kChunk * HD;
-  float* sm = so + kMaxRows * HD;
-  float* sl = sm + kMaxRows;
-  pdl_launch_dependents();
-  pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int s = blockIdx.x, h = blockIdx.y;
-  const int b = blockIdx.z / p.row_tiles, rt = blockIdx.z - b * p.row_tiles;
-  const int q0 = p.cu_q[b], nq = p.cu_q[b + 1] - q0, L = p.seq_len[b];
-  if (nq < 0 || nq > p.max_q || L < nq || q0 < 0 || q0 > p.token_cap - nq) {
-    if (threadIdx.x == 0 && s == 0 && h == 0) atomicOr(p.err, kErrDeviceInput);
-    return;
+__global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const PackedAttnParams p) {
+  using C = Cfg<HD>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sV = smem + C::kVOffset;
+  uint8_t* sP = smem + C::kPOffset;
+  uint8_t* sQ = smem + C::kQOffset;
+  uint8_t* sStage = smem + C::kStageOffset;
+  Shared* sh = reinterpret_cast<Shared*>(smem + C::kBarOffset);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == kProducerWarp * 32) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sh->full[i], 1);
+      mbar_init(&sh->empty[i], 8);
+    }
+    for (int i = 0; i < kGeo; ++i) mbar_init(&sh->geo_full[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->k_ready[i], 4);
+      mbar_init(&sh->v_ready[i], 4);
+      mbar_init(&sh->s_done[i], 1);
+      mbar_init(&sh->p_ready[i], 4);
+      mbar_init(&sh->pv_done[i], 1);
+    }
+    mbar_init(&sh->q_ready, 8);
+    mbar_init(&sh->drain, 1);
+    mbar_init(&sh->never, 1);
+    sh->abort = 0;
+    sh->q_top = 0u;
+    fence_mbar_init();
   }
-  const int row0 = rt * kMaxRows;
-  const int rows = min(kMaxRows, nq * p.group - row0);
-  if (rows <= 0) return;
-  const int r0 = p.cu_res[b], nres = max(0, p.cu_res[b + 1] - r0);
-  const int c0 = static_cast<int>(static_cast<long long>(s) * nres / p.num_splits);
-  const int c1 = static_cast<int>(static_cast<long long>(s + 1) * nres / p.num_splits);
-  for (int x = threadIdx.x; x < rows * HD; x += kThreads) so[x] = 0.f;
-  for (int x = threadIdx.x; x < rows; x += kThreads) sm[x] = -INFINITY, sl[x] = 0.f;
-  for (int e = c0; e < c1; ++e) {
-    const int cid = p.res_ids[r0 + e], slot = p.res_slots[r0 + e];
-    if (cid < 0 || cid >= (1 << 25) || slot < 0 || slot >= p.num_slots) {
-      if (threadIdx.x == 0) atomicOr(p.err, kErrDeviceInput);
-      continue;
-    }
-    const int base = cid * kChunk;
-    __syncthreads();
-    const size_t at = (static_cast<size_t>(slot) * p.hkv + h) * kPackedBytes<HD>;
-    for (int x = threadIdx.x; x < 2 * kChunk * (HD / 2); x += kThreads) {
-      const bool is_v = x >= kChunk * (HD / 2);
-      const int y = is_v ? x - kChunk * (HD / 2) : x;
-      const int row = y / (HD / 2), cb = y % (HD / 2);       // token, code byte of its row
-      const uint8_t* rec = (is_v ? p.v_pool : p.k_pool) + at;
-      float2 v = make_float2(0.f, 0.f);
-      if (base + row < L) {
-        const float sc = e4m3_value(rec[kChunk * (HD / 2) + row * (HD / 16) + cb / 8]);
-        v = e2m1_pair(rec[((cb / 16) * kChunk + row) * 16 + cb % 16]);
-        v.x *= sc;
-        v.y *= sc;
-      }
-      float* dst = is_v ? sv + row * HD + 2 * cb : sk + row * kStride + 2 * cb;
-      dst[0] = v.x;
-      dst[1] = v.y;
-    }
-    __syncthreads();
-    for (int r = warp; r < rows; r += kWarps) {
-      const int i = (row0 + r) / p.group, g = (row0 + r) % p.group;
-      const int pos = L - nq + i;
-      const uint16_t* qr = p.q + (static_cast<size_t>(q0 + i) * p.hq + static_cast<size_t>(h) * p.group + g) * HD;
-      float s0 = 0.f, s1 = 0.f;
-      for (int c = 0; c < HD; ++c) {
-        const float qv = __uint_as_float(static_cast<uint32_t>(__ldg(qr + c)) << 16);
-        s0 = fmaf(qv, sk[lane * kStride + c], s0);
-        s1 = fmaf(qv, sk[(lane + 32) * kStride + c], s1);
-      }
-      s0 = base + lane <= pos ? s0 * p.scale_log2 : -INFINITY;
-      s1 = base + lane + 32 <= pos ? s1 * p.scale_log2 : -INFINITY;
-      float m = fmaxf(s0, s1);
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const float m_old = sm[r], m_new = fmaxf(m_old, m);
-      if (m_new == -INFINITY) continue;
-      const float alpha = ex2_approx(m_old - m_new);
-      const float p0 = ex2_approx(s0 - m_new), p1 = ex2_approx(s1 - m_new);
-      float l = p0 + p1;
-      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-      float acc[PER];
-      for (int x = 0; x < PER; ++x) acc[x] = so[r * HD + lane + 32 * x] * alpha;
-      for (int k = 0; k < kChunk; ++k) {
-        const float pk = __shfl_sync(0xffffffffu, k < 32 ? p0 : p1, k & 31);
-        for (int x = 0; x < PER; ++x) acc[x] = fmaf(pk, sv[k * HD + lane + 32 * x], acc[x]);
-      }
-      for (int x = 0; x < PER; ++x) so[r * HD + lane + 32 * x] = acc[x];
-      __syncwarp();
-      if (lane == 0) sm[r] = m_new, sl[r] = sl[r] * alpha + l;
-      __syncwarp();
-    }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&sh->tmem_base, kTmemCols);
+    tmem_relinquish();
   }
+  if (HD == 64) {
+    // M = 128 with 64 channels: the second box of V stays zero
+    for (int x = threadIdx.x; x < 2 * C::kBoxBytes / 16; x += kThreads) {
+      const int buf = x / (C::kBoxBytes / 16), at = x % (C::kBoxBytes / 16);
+      *reinterpret_cast<uint4*>(sV + buf * C::kVBytes + C::kBoxBytes + at * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
   __syncthreads();
-  const size_t pidx = ((static_cast<size_t>(b) * p.row_tiles + rt) * p.hkv + h) * p.num_splits + s;
-  for (int x = threadIdx.x; x < rows * HD; x += kThreads) p.part_o[pidx * kMaxRows * HD + x] = so[x] * p.v_scale;
-  for (int x = threadIdx.x; x < rows; x += kThreads)
-    reinterpret_cast<float2*>(p.part_ml)[pidx * kMaxRows + x] = make_float2(sm[x], sl[x]);
+  tc_fence_after();
+  const uint32_t tbase = sh->tmem_base;
+  volatile int* abort = &sh->abort;
+
+  pdl_launch_dependents();
+  if (!p.stable_metadata) pdl_wait();
+  const Work w = make_work(p);
+  if (p.stable_metadata) pdl_wait();
+  if (w.bad && threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(p.err, kErrDeviceInput);
+
+  if (warp >= kProducerWarp) {
+    regs_dec<kRegsRest>();
+    if (warp == kProducerWarp) {
+      // ------------------------------ records and geometry --------------------------------
+      const uint64_t pol = l2_policy_evict_first();
+      int issued = 0;
+      bool reported = false;
+      int id = -1, slot = -1;             // of list entry 32 (j / 16) + lane
+      for (int j = 0; j < w.nt; ++j) {
+        if (j % 16 == 0) {
+          const int e = (w.tb + j) * 2 + lane;
+          const bool in = e < w.nres && e < (w.tb + w.nt) * 2;
+          id = in ? __ldg(p.res_ids + w.r0 + e) : -1;
+          slot = in ? __ldg(p.res_slots + w.r0 + e) : -1;
+        }
+        const int at = (j % 16) * 2;
+        int cid[2], sl[2];
+        bool ok[2];
+        int n = 0;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          cid[c] = __shfl_sync(0xffffffffu, id, at + c);
+          sl[c] = __shfl_sync(0xffffffffu, slot, at + c);
+          const bool present = (w.tb + j) * 2 + c < w.nres;
+          ok[c] = present && cid[c] >= 0 && cid[c] < (1 << 25) && sl[c] >= 0 && sl[c] < p.num_slots;
+          n += ok[c] ? 1 : 0;
+          if (present && !ok[c] && !reported) {
+            if (lane == 0) atomicOr(p.err, kErrDeviceInput);
+            reported = true;
+          }
+        }
+        const int st = j % kStages;
+        bool go = true;
+        if (lane == 0) {
+          if (j >= kStages) go = mbar_wait(&sh->empty[st], ((j / kStages) - 1) & 1, abort, p.err);
+          if (go) {
+            const int g = j % kGeo;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              sh->base[g][c] = ok[c] ? cid[c] * kChunk : 0;
+              sh->valid[g][c] = ok[c] ? 1 : 0;
+            }
+            mbar_arrive(&sh->geo_full[g]);
+            mbar_arrive_expect_tx(&sh->full[st], n * 2 * C::kRecord);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              if (!ok[c]) continue;
+              const size_t from = (static_cast<size_t>(sl[c]) * p.hkv + w.h) * C::kRecord;
+              uint8_t* to = sStage + st * C::kStageBytes;
+              bulk_load(to + c * C::kRecord, p.k_pool + from, C::kRecord, &sh->full[st], pol);
+              bulk_load(to + (2 + c) * C::kRecord, p.v_pool + from, C::kRecord, &sh->full[st], pol);
+            }
+          }
+        }
+        if (!__shfl_sync(0xffffffffu, go ? 1 : 0, 0)) break;
+        issued = j + 1;
+      }
+      // Every copy lands before the CTA can exit.
+      if (lane == 0)
+        for (int j = max(0, issued - kStages); j < issued; ++j)
+          mbar_drain(&sh->full[j % kStages], (j / kStages) & 1, p.err);
+      __syncwarp();
+    } else if (warp == kMmaWarp) {
+      // ------------------------------ MMA issuer ------------------------------------------
+      if (lane == 0 && w.nt > 0) {
+        if (p.timeout_test_ns != 0) mbar_wait_limit(&sh->never, 0, p.timeout_test_ns, abort, p.err);
+        bool ok = !*abort && mbar_wait(&sh->q_ready, 0, abort, p.err);
+        tc_fence_after();
+        const int n = (w.rows + 15) & ~15;
+        const uint32_t idesc_s = idesc_f16_f32(128, n, 0, 0);
+        const uint32_t idesc_o = idesc_f16_f32(128, n, 1, 1);
+        const uint64_t qdesc = sw128_desc(smem_u32(sQ), 16, 1024);
+        const uint64_t vdesc = sw128_desc(smem_u32(sV), C::kBoxBytes, 1024);
+        const uint64_t pdesc = sw128_desc(smem_u32(sP), C::kBoxBytes, 1024);
+        // S^T of tile j over its group's buffer: free once the group's P of tile j - 2 is written.
+        auto issue_s = [&](int j) {
+          tc_fence_after();
+          const int g = j & 1;
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk)
+            mma_ts(tbase + kColS + g * 96, tbase + kColK + g * 64 + kk * 8,
+                   qdesc + static_cast<uint64_t>(((kk >> 2) * C::kQBoxBytes + (kk & 3) * 32) >> 4), idesc_s, kk > 0 ? 1u : 0u);
+          mma_commit(&sh->s_done[g]);
+        };
+        for (int j = 0; ok && j < 2 && j < w.nt; ++j) {
+          ok = mbar_wait(&sh->k_ready[j & 1], 0, abort, p.err);
+          if (ok) issue_s(j);
+        }
+        for (int j = 0; ok && j < w.nt; ++j) {
+          const int g = j & 1, ph = (j >> 1) & 1;
+          ok = mbar_wait(&sh->p_ready[g], ph, abort, p.err);
+          if (!ok) break;
+          bool next = j + 2 < w.nt;
+          if (next && mbar_test_wait(&sh->k_ready[g], ph ^ 1)) {
+            issue_s(j + 2);
+            next = false;
+          }
+          ok = mbar_wait(&sh->v_ready[g], ph, abort, p.err);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            mma_ss(tbase + kColO + g * 96, vdesc + static_cast<uint64_t>((g * C::kVBytes + kk * 2048) >> 4),
+                   pdesc + static_cast<uint64_t>((g * C::kPBytes + kk * 2048) >> 4), idesc_o, (j > 1 || kk > 0) ? 1u : 0u);
+          mma_commit(&sh->pv_done[g]);
+          if (next) {
+            ok = mbar_wait(&sh->k_ready[g], ph ^ 1, abort, p.err);
+            if (ok) issue_s(j + 2);
+          }
+        }
+        mma_commit(&sh->drain);
+        mbar_drain(&sh->drain, 0, p.err);
+      }
+      __syncwarp();
+    }
+  } else if (warp >= 8) {
+    // ------------------------------ K and V to fp16 -----------------------------------------
+    regs_dec<kRegsUnpack>();
+    const bool is_v = warp >= 12;
+    const int key = (warp & 3) * 32 + lane;              // of the tile; a TMEM lane
+    const int c = key / kChunk, tok = key % kChunk;
+    uint64_t* done = is_v ? sh->pv_done : sh->s_done;
+    uint64_t* ready = is_v ? sh->v_ready : sh->k_ready;
+    const uint32_t lane_base = tbase + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    for (int j = 0; j < w.nt; ++j) {
+      const int st = j % kStages, g = j & 1, u = j >> 1;
+      bool ok = mbar_wait(&sh->full[st], (j / kStages) & 1, abort, p.err);
+      if (ok && u > 0) ok = mbar_wait(&done[g], (u - 1) & 1, abort, p.err);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const uint8_t* rec = sStage + st * C::kStageBytes + ((is_v ? 2 : 0) + c) * C::kRecord;
+      uint32_t scales[HD / 64];                          // four scale bytes a word
+#pragma unroll
+      for (int i = 0; i < HD / 64; ++i)
+        scales[i] = *reinterpret_cast<const uint32_t*>(rec + kChunk * (HD / 2) + tok * (HD / 16) + 4 * i);
+      if (is_v) {
+        // Keys that no row attends may hold anything: P is 0 there, but 0 * NaN is NaN.
+        const int geo = j % kGeo;
+        if (!sh->valid[geo][c] || sh->base[geo][c] + tok >= w.L) {
+#pragma unroll
+          for (int i = 0; i < HD / 64; ++i) scales[i] = 0u;
+        }
+      } else {
+        tc_fence_after();
+      }
+#pragma unroll
+      for (int x = 0; x < HD / 32; ++x) {                // 32 channels: 16 bytes of codes, two scales
+        const uint4 codes = *reinterpret_cast<const uint4*>(rec + (x * kChunk + tok) * 16);
+        const uint32_t two = e4m3_pair_f16((scales[x / 2] >> (16 * (x & 1))) & 0xffffu);
+        const uint32_t s0 = __byte_perm(two, two, 0x1010), s1 = __byte_perm(two, two, 0x3232);
+        uint32_t out[16];
+        unpack_word(codes.x, s0, out);
+        unpack_word(codes.y, s0, out + 4);
+        unpack_word(codes.z, s1, out + 8);
+        unpack_word(codes.w, s1, out + 12);
+        if (!is_v) {
+          tmem_st16_async(lane_base + kColK + g * 64 + x * 16, out);
+        } else {
+          uint8_t* row = sV + g * C::kVBytes + (x / 2) * C::kBoxBytes + key * 128;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int word = (x & 1) * 4 + i;            // 16-byte word of the 128-byte row
+            *reinterpret_cast<uint4*>(row + ((word ^ (key & 7)) << 4)) =
+                make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
+          }
+        }
+      }
+      if (is_v) {
+        fence_proxy_async_smem();
+      } else {
+        tmem_wait_st();
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sh->empty[st]);
+        mbar_arrive(&ready[g]);
+      }
+    }
+  } else {
+    // ------------------------------ softmax ---------------------------------------------------
+    regs_inc<kRegsSoftmax>();
+    const int grp = warp >> 2, wq = warp & 3, tg = threadIdx.x & 127;
+    const int key = tg;
+    const int bar = 1 + grp;                             // named barrier of the group; 3: both groups
+    // Q: words of 8 channels, all of a thread's in registers while the tile's largest value is found
+    constexpr int kWords = kMaxN * HD / 8 / 256 + ((kMaxN * HD / 8) % 256 != 0 ? 1 : 0);
+    float q_scale;                                       // of a score: softmax scale, g of K, the queries' power of two
+    {
+      uint4 qv[kWords];
+      unsigned top = 0u;
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const int x = threadIdx.x + i * 256;
+        const int r = x / (HD / 8), cw = x % (HD / 8);
+        qv[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < w.rows) {
+          const unsigned rg = static_cast<unsigned>(w.row0 + r), ug = static_cast<unsigned>(p.group);
+          const unsigned qi = rg / ug, hg = rg - qi * ug;
+          qv[i] = __ldg(reinterpret_cast<const uint4*>(
+                            p.q + (static_cast<size_t>(w.q0 + qi) * p.hq + static_cast<size_t>(w.h) * p.group + hg) * HD) + cw);
+        }
+        const uint32_t ws[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = max(top, max(ws[e] & 0x7fffu, (ws[e] >> 16) & 0x7fffu));
+      }
+      top = __reduce_max_sync(0xffffffffu, top);
+      if (lane == 0) atomicMax(&sh->q_top, top);
+      named_sync(3, 256);
+      const int qe = max(static_cast<int>(sh->q_top >> 7) - 127 - 14, -100);
+      const float down = __int_as_float((127 - qe) << 23);
+      q_scale = p.scale_log2 * __int_as_float((127 + qe) << 23);
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const int x = threadIdx.x + i * 256;
+        const int r = x / (HD / 8), cw = x % (HD / 8);
+        const uint32_t ws[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          o[e] = pack_f16(__uint_as_float(ws[e] << 16) * down, __uint_as_float(ws[e] & 0xffff0000u) * down);
+        if (r < kMaxN)
+          *reinterpret_cast<uint4*>(sQ + (cw >> 3) * C::kQBoxBytes + r * 128 + (((cw & 7) ^ (r & 7)) << 4)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->q_ready);
+    }
+    if (tg < kMaxN) {
+      // (rows past the block, Q = 0, keep weight 1: their columns are never read)
+      sh->neg_ref[grp][tg] = tg < w.rows ? INFINITY : 0.f;
+      sh->limit[grp][tg] = tg < w.rows ? -INFINITY : INFINITY;
+    }
+    named_sync(bar, 128);
+
+    const uint32_t lane_base = tbase + (static_cast<uint32_t>(wq * 32) << 16);
+    const uint32_t s_at = lane_base + kColS + grp * 96, o_at = lane_base + kColO + grp * 96;
+    uint8_t* prow = sP + grp * C::kPBytes + key * 128;
+    const int p0 = w.L - w.nq;
+    float l[kMaxN];
+#pragma unroll
+    for (int r = 0; r < kMaxN; ++r) l[r] = 0.f;
+    bool dead = false;                                   // a wait of this warp gave up
+    int u = 0;                                           // tiles of this group so far
+    for (int j = grp; j < w.nt; j += 2, ++u) {
+      const int geo = j % kGeo;
+      if (!mbar_wait(&sh->geo_full[geo], (j / kGeo) & 1, abort, p.err)) dead = true;
+      // Rows from n_min on attend this lane's key: row n is of block query (row0 + n) / G, at position p0 + that.
+      const int pos = sh->base[geo][key / kChunk] + key % kChunk;
+      int n_min = 0;
+      if (!sh->valid[geo][key / kChunk] || pos >= w.L)
+        n_min = kMaxN;
+      else if (pos > p0)
+        n_min = min(static_cast<long long>(kMaxN), max(0ll, static_cast<long long>(pos - p0) * p.group - w.row0));
+      const bool whole = __all_sync(0xffffffffu, n_min == 0);
+      if (!mbar_wait(&sh->s_done[grp], u & 1, abort, p.err)) dead = true;
+      dead = __any_sync(0xffffffffu, dead);
+      tc_fence_after();
+      bool moves = dead;
+      if (!dead) {
+#pragma unroll
+        for (int cb = 0; cb < kMaxN / 16; ++cb) {
+          if (cb * 16 < w.rows) {
+            uint32_t sr[16];
+            tmem_ld16(s_at + cb * 16, sr);
+            const float4* lim = reinterpret_cast<const float4*>(&sh->limit[grp][cb * 16]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float4 f = lim[e];
+              const int n = cb * 16 + 4 * e;
+              moves = moves || (__uint_as_float(sr[4 * e]) > f.x && n >= n_min) ||
+                      (__uint_as_float(sr[4 * e + 1]) > f.y && n + 1 >= n_min) ||
+                      (__uint_as_float(sr[4 * e + 2]) > f.z && n + 2 >= n_min) ||
+                      (__uint_as_float(sr[4 * e + 3]) > f.w && n + 3 >= n_min);
+            }
+          }
+        }
+      }
+      if (named_any(bar, 128, moves)) {
+        // A row's weights would pass the limit (or it has no reference yet): the rows' maxima over the tile, new
+        // references for those rows, their sums and O scaled. Every warp of the group comes here or none.
+        if (named_any(bar, 128, dead)) break;
+#pragma unroll
+        for (int cb = 0; cb < kMaxN / 8; ++cb) {
+          if (cb * 8 < w.rows) {
+            uint32_t sr[8];
+            tmem_ld8(s_at + cb * 8, sr);
+            float mine = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float m = warp_max(cb * 8 + e >= n_min ? __uint_as_float(sr[e]) : -INFINITY);
+              mine = lane == e ? m : mine;
+            }
+            if (lane < 8) sh->part[grp][wq][cb * 8 + lane] = mine;
+          }
+        }
+        named_sync(bar, 128);
+        if (tg < w.rows) {
+          const float m = fmaxf(fmaxf(sh->part[grp][0][tg], sh->part[grp][1][tg]),
+                                fmaxf(sh->part[grp][2][tg], sh->part[grp][3][tg]));
+          float a = 1.f;
+          if (m > sh->limit[grp][tg]) {
+            const float ref = m * q_scale - kTop;
+            const float old = -sh->neg_ref[grp][tg];
+            a = ex2_approx(old - ref);                   // 0 for the first
+            sh->neg_ref[grp][tg] = -ref;
+            sh->limit[grp][tg] = (ref + kLimit) / q_scale;
+          }
+          sh->alpha[grp][tg] = a;
+        }
+        named_sync(bar, 128);
+        if (u > 0) {
+          dead = !__all_sync(0xffffffffu, mbar_wait(&sh->pv_done[grp], (u - 1) & 1, abort, p.err));
+          tc_fence_after();
+        }
+#pragma unroll
+        for (int cb = 0; cb < kMaxN / 8; ++cb) {
+          if (cb * 8 < w.rows) {
+            uint32_t o[8];
+            if (u > 0 && !dead) tmem_ld8(o_at + cb * 8, o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float a = sh->alpha[grp][cb * 8 + e];
+              l[cb * 8 + e] *= a;
+              if (u > 0) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+            }
+            if (u > 0 && !dead) tmem_st8_async(o_at + cb * 8, o);
+          }
+        }
+        tmem_wait_st();
+        if (named_any(bar, 128, dead)) break;
+      }
+      // P = 2^(s scale - ref), and its sums
+      if (u > 0) {
+        dead = !__all_sync(0xffffffffu, mbar_wait(&sh->pv_done[grp], (u - 1) & 1, abort, p.err));
+      }
+      const float2 sc2 = make_float2(q_scale, q_scale);
+#pragma unroll
+      for (int cb = 0; cb < kMaxN / 16; ++cb) {
+        if (cb * 16 < w.rows) {
+          uint32_t sr[16];
+          tmem_ld16(s_at + cb * 16, sr);
+          const float4* nr = reinterpret_cast<const float4*>(&sh->neg_ref[grp][cb * 16]);
+          uint32_t pk[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 f = nr[e];
+            float2 a = fma_f32x2(make_float2(__uint_as_float(sr[4 * e]), __uint_as_float(sr[4 * e + 1])), sc2, make_float2(f.x, f.y));
+            float2 b = fma_f32x2(make_float2(__uint_as_float(sr[4 * e + 2]), __uint_as_float(sr[4 * e + 3])), sc2, make_float2(f.z, f.w));
+            a.x = ex2_approx(a.x);
+            a.y = ex2_approx(a.y);
+            b.x = ex2_approx(b.x);
+            b.y = ex2_approx(b.y);
+            if (!whole) {
+              const int n = cb * 16 + 4 * e;
+              a.x = n >= n_min ? a.x : 0.f;
+              a.y = n + 1 >= n_min ? a.y : 0.f;
+              b.x = n + 2 >= n_min ? b.x : 0.f;
+              b.y = n + 3 >= n_min ? b.y : 0.f;
+            }
+            const float2 l0 = add_f32x2(make_float2(l[cb * 16 + 4 * e], l[cb * 16 + 4 * e + 1]), a);
+            const float2 l1 = add_f32x2(make_float2(l[cb * 16 + 4 * e + 2], l[cb * 16 + 4 * e + 3]), b);
+            l[cb * 16 + 4 * e] = l0.x;
+            l[cb * 16 + 4 * e + 1] = l0.y;
+            l[cb * 16 + 4 * e + 2] = l1.x;
+            l[cb * 16 + 4 * e + 3] = l1.y;
+            pk[2 * e] = pack_f16(a.x, a.y);
+            pk[2 * e + 1] = pack_f16(b.x, b.y);
+          }
+          uint8_t* box = prow + (cb >> 2) * C::kBoxBytes;
+          const int w0 = (cb & 3) * 2;
+          *reinterpret_cast<uint4*>(box + ((w0 ^ (key & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          *reinterpret_cast<uint4*>(box + (((w0 + 1) ^ (key & 7)) << 4)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+        }
+      }
+      tc_fence_before();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && !dead) mbar_arrive(&sh->p_ready[grp]);
+    }
+    // ---- epilogue: the groups' sums and O merged into the split's partial (m, l, O not normalised) ----
+    if (u > 0 && !dead) dead = !__all_sync(0xffffffffu, mbar_wait(&sh->pv_done[grp], (u - 1) & 1, abort, p.err));
+    tc_fence_after();
+#pragma unroll
+    for (int cb = 0; cb < kMaxN / 8; ++cb) {
+      if (cb * 8 < w.rows) {
+        const float sum = sum_rows8(l + cb * 8, lane);
+        if (lane < 8) sh->part[grp][wq][cb * 8 + lane] = sum;
+      }
+    }
+    tc_fence_before();
+    named_sync(3, 256);
+    tc_fence_after();
+    if (static_cast<int>(threadIdx.x) < w.rows) {
+      const int r = threadIdx.x;
+      float lg[2], ref[2];
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        lg[g] = (sh->part[g][0][r] + sh->part[g][1][r]) + (sh->part[g][2][r] + sh->part[g][3][r]);
+        ref[g] = lg[g] > 0.f ? -sh->neg_ref[g][r] : -INFINITY;
+      }
+      const float m = fmaxf(ref[0], ref[1]);
+      float sum = 0.f;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const float wt = lg[g] > 0.f ? ex2_approx(ref[g] - m) : 0.f;
+        sum += wt * lg[g];
+        sh->alpha[g][r] = wt * p.v_scale;
+      }
+      const int rg = w.row0 + r;
+      const size_t pidx = ((static_cast<size_t>(w.b) * p.row_tiles + rg / kMaxRows) * p.hkv + w.h) * p.num_splits + w.s;
+      reinterpret_cast<float2*>(p.part_ml)[pidx * kMaxRows + rg % kMaxRows] = make_float2(m, sum);
+    }
+    named_sync(3, 256);
+    if (w.nt > 0 && wq * 32 < HD) {
+      // lane = channel: 32 neighbouring channels of a row are one 128-byte store. The groups take rows of eight in turn.
+#pragma unroll
+      for (int cb = 0; cb < kMaxN / 8; ++cb) {
+        if ((cb & 1) == grp && cb * 8 < w.rows) {
+          uint32_t o0[8], o1[8];
+          tmem_ld8(lane_base + kColO + cb * 8, o0);
+          tmem_ld8(lane_base + kColO + 96 + cb * 8, o1);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int r = cb * 8 + e;
+            if (r < w.rows) {
+              const float w0 = sh->alpha[0][r], w1 = sh->alpha[1][r];
+              const float v = (w0 > 0.f ? w0 * __uint_as_float(o0[e]) : 0.f) + (w1 > 0.f ? w1 * __uint_as_float(o1[e]) : 0.f);
+              const int rg = w.row0 + r;
+              const size_t pidx =
+                  ((static_cast<size_t>(w.b) * p.row_tiles + rg / kMaxRows) * p.hkv + w.h) * p.num_splits + w.s;
+              p.part_o[(pidx * kMaxRows + rg % kMaxRows) * HD + wq * 32 + lane] = v;
+            }
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tbase, kTmemCols);
+  }
 }
 
 template <int HD>
 cudaError_t launch_hd(const PackedAttnParams& p, int num_seqs, cudaStream_t stream) {
   static size_t done[64] = {};
-  constexpr size_t kSmem = Shape<HD>::kSmemFloats * 4;
-  const cudaError_t e = ensure_smem_limit(attend_packed_kernel<HD>, kSmem, done);
+  static bool registers = false;
+  auto kern = attend_packed_kernel<HD>;
+  if (!registers) {
+    // The warpgroups trade registers; a kernel launched with fewer than they take up would wait for ever.
+    cudaFuncAttributes a;
+    const cudaError_t e = cudaFuncGetAttributes(&a, kern);
+    if (e != cudaSuccess) return e;
+    if (a.numRegs < kRegsLaunch) return cudaErrorNotSupported;
+    registers = true;
+  }
+  const cudaError_t e = ensure_smem_limit(kern, Cfg<HD>::kSmemBytes, done);
   if (e != cudaSuccess) return e;
-  const dim3 grid(p.num_splits, p.hkv, num_seqs * p.row_tiles);
-  return launch_pdl(attend_packed_kernel<HD>, grid, dim3(kThreads), kSmem, stream, p);
+  const dim3 grid(p.num_splits, p.hkv, num_seqs * p.n_tiles);
+  return launch_pdl(kern, grid, dim3(kThreads), Cfg<HD>::kSmemBytes, stream, p);
 }
 
 }  // namespace
+
+int packed_tile_rows() { return kMaxN; }
 
 cudaError_t launch_attend_packed(const PackedAttnParams& p, int num_seqs, cudaStream_t stream) {
   return p.head_dim == 128 ? launch_hd<128>(p, num_seqs, stream) : launch_hd<64>(p, num_seqs, stream);

@@ -373,13 +373,18 @@ struct PackedAttnParams {
   int num_splits;
   int max_q;
   int row_tiles;              // of 128 rows, as the combine counts them
+  int n_tiles, tile_rows;     // this kernel's row tiles
   int token_cap;
   float scale_log2;           // softmax scale * log2(e) * g of K
   float v_scale;              // g of V
   float* part_o;              // [B][row tiles][Hkv][splits][128][d]
   float* part_ml;             // [B][row tiles][Hkv][splits][128][2] (m in log2 units, l)
+  unsigned long long timeout_test_ns;  // as in AttnParams
+  int stable_metadata;
   int* err;
 };
+// The most block rows that one CTA takes.
+int packed_tile_rows();
 cudaError_t launch_attend_packed(const PackedAttnParams& p, int num_seqs, cudaStream_t stream);
 
 // ------------------------------ sampled acceptance --------------------------------------------

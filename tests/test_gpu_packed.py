@@ -2,7 +2,9 @@
 
 Attention is compared within 2^-8 |o| (O's rounding to bf16) + (2^-10 + 7e-4) A, A = sum_j p_j |v_j|: weights are rounded to
 fp16 at most (half a step, 2^-11, and the next power of two's), scores are fp32 sums of d products of exact values. Codes and
-scales are read exactly. LSE: 3.1e-4 + 2^-22 |lse|, the scores' part alone."""
+scales are read exactly. fp16's smallest step is 2^-24: a weight is off by at most half of that, 2^-25, where the largest is at
+least 2^7 (the reference lies 7 below a maximum, in log2), so that O may be off by 2^-32 sum_j |v_j| more; it shows only in
+channels where the heavy keys' values are 0. LSE: 3.1e-4 + 2^-22 |lse|, the scores' part alone."""
 import numpy as np
 import pytest
 import torch
@@ -164,9 +166,10 @@ def test_page_in(env, hkv, d, ctas):
 # Attention
 # ---------------------------------------------------------------------------------------------
 
-def close(got, lse, ref, rlse, mag):
+def close(got, lse, ref, rlse, mag, all_v):
     g = O.bf16_to_f64(got)
-    assert np.all(np.abs(g - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -10 + 7e-4) * mag + 1e-30), np.abs(g - ref).max()
+    off = np.abs(g - ref) - (2.0 ** -8 * np.abs(ref) + (2.0 ** -10 + 7e-4) * mag + 2.0 ** -32 * all_v + 1e-30)
+    assert off.max(initial=-1) <= 0, (off.max(), np.abs(g - ref).max())
     fin = np.isfinite(rlse)
     assert np.array_equal(np.isneginf(lse), np.isneginf(rlse))
     assert np.all(np.abs(lse[fin] - rlse[fin]) <= 3.1e-4 + np.abs(rlse[fin]) * 2.0 ** -22)
@@ -277,7 +280,7 @@ def test_growing_scores(env, splits):
         ref = B.attend_packed_seq(O.bf16_to_f64(bits), *pools, np.arange(24), np.arange(24), L)
         # scores of up to 2000: 2^-22 of one is the fp32 sum's error, and that of a weight's exponent
         g = O.bf16_to_f64(got)
-        assert np.all(np.abs(g - ref[0]) <= 2.0 ** -8 * np.abs(ref[0]) + (2.0 ** -10 + 4e-3) * ref[2])
+        assert np.all(np.abs(g - ref[0]) <= 2.0 ** -8 * np.abs(ref[0]) + (2.0 ** -10 + 4e-3) * ref[2] + 2.0 ** -32 * ref[3])
         assert np.all(np.abs(lse - ref[1]) <= 3.1e-4 + 2.0 ** -20 * np.abs(ref[1]))
 
 

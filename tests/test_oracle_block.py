@@ -82,7 +82,7 @@ def test_attention_over_packed_chunks_is_that_over_their_values():
     for p in pool:
         p[..., 32 * d:] = rng.integers(0x28, 0x38, (3, 1, 4 * d))
     q = O.bf16_to_f64(B.to_bf16(rng.standard_normal((n, 2, d))))
-    out, lse, _ = B.attend_packed_seq(q, *pool, [0, 1, 2], [2, 0, 1], L)
+    out, lse, *_ = B.attend_packed_seq(q, *pool, [0, 1, 2], [2, 0, 1], L)
     kv = [B.to_bf16(B.record_values(p, d)) for p in pool]
     ref, rlse = O.attend_full_seq(B.to_bf16(q), *kv, np.arange(3, dtype=np.int32), np.array([2, 0, 1], np.int32), L)
     assert np.allclose(out, ref, atol=1e-12) and np.allclose(lse, rlse, atol=1e-12)
