@@ -25,14 +25,13 @@
 namespace vfy {
 namespace {
 
-constexpr int kGroups = 5;                // warpgroups: softmax 0 and 1, K, V, the rest
+constexpr int kGroups = 7;                // warpgroups: softmax 0 and 1, K twice, V twice, the rest
 constexpr int kThreads = kGroups * 128;
-constexpr int kRegsLaunch = 96, kRegsSoftmax = 152, kRegsUnpack = 64, kRegsRest = 40;
-static_assert(2 * kRegsSoftmax + 2 * kRegsUnpack + kRegsRest <= kGroups * kRegsLaunch, "registers the CTA was launched with");
-constexpr int kProducerWarp = 16, kMmaWarp = 17;
+constexpr int kRegsLaunch = 72, kRegsSoftmax = 152, kRegsUnpack = 40, kRegsRest = 40;
+static_assert(2 * kRegsSoftmax + 4 * kRegsUnpack + kRegsRest <= kGroups * kRegsLaunch, "registers the CTA was launched with");
+constexpr int kKWarp = 8, kVWarp = 16, kProducerWarp = 24, kMmaWarp = 25;
 constexpr int kKeys = 2 * kChunk;         // keys of a tile
-constexpr int kMaxN = 80;                 // rows of a tile: the softmax threads hold a partial sum of each
-constexpr int kStages = 4;
+constexpr int kFewN = 16, kMaxN = 80;     // rows of a tile (two kernels): the softmax threads hold a partial sum of each
 constexpr int kGeo = 16;                  // tile-geometry ring: more than the tiles between producer and softmax
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColK = 0;             // two K tiles of up to 64 columns (two fp16 channels each)
@@ -41,28 +40,29 @@ constexpr uint32_t kColO = 320;           // O^T of the two groups
 constexpr float kTop = 7.f;               // a row's maximum when its reference is set (log2)
 constexpr float kLimit = 15.f;            // the reference moves when a weight would pass 2^15
 
-template <int HD>
+template <int HD, int NT>
 struct Cfg {
+  static constexpr int kStages = NT > kFewN ? 4 : 6;
   static constexpr int kRecord = kPackedBytes<HD>;
   static constexpr int kStageBytes = 4 * kRecord;                // K and V of two chunks
   static constexpr int kBoxBytes = kKeys * 128;                  // 64 columns of 128 keys
   static constexpr int kVBytes = 2 * kBoxBytes;                  // M = 128: d = 64 leaves the second box zero
-  static constexpr int kPBytes = 2 * kBoxBytes;
-  static constexpr int kQBoxBytes = kMaxN * 128;
+  static constexpr int kPBytes = (NT + 63) / 64 * kBoxBytes;
+  static constexpr int kQBoxBytes = NT * 128;
   static constexpr int kQBytes = (HD / 64) * kQBoxBytes;
   static constexpr int kVOffset = 0;
   static constexpr int kPOffset = 2 * kVBytes;
   static constexpr int kQOffset = kPOffset + 2 * kPBytes;
   static constexpr int kStageOffset = kQOffset + kQBytes;
   static constexpr int kBarOffset = kStageOffset + kStages * kStageBytes;
-  static constexpr int kBarBytes = 6144;
+  static constexpr int kBarBytes = 5120;
   static constexpr int kSmemBytes = kBarOffset + kBarBytes + 1024;
   static_assert(kRecord % 16 == 0 && kStageBytes % 128 == 0, "bulk copies");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
 struct Shared {
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[6], empty[6];
   uint64_t geo_full[kGeo];
   uint64_t k_ready[2], v_ready[2];
   uint64_t s_done[2];                     // S of a tile: its S^T is there, its K is free
@@ -74,11 +74,11 @@ struct Shared {
   unsigned q_top;                         // largest |q| of the tile, as bf16 bits
   int base[kGeo][2], valid[kGeo][2];      // per chunk of a tile
   alignas(16) float neg_ref[2][kMaxN];    // [group] minus the rows' reference, log2 units
-  alignas(16) float limit[2][kMaxN];      // S value above which the reference moves
+  alignas(16) float neg_limit[2][kMaxN];  // minus the S value above which the reference moves
   alignas(16) float alpha[2][kMaxN];
   alignas(16) float part[2][4][kMaxN];    // [group][warp]: maxima, at the end sums
 };
-static_assert(sizeof(Shared) <= Cfg<128>::kBarBytes, "barrier block");
+static_assert(sizeof(Shared) <= Cfg<128, kMaxN>::kBarBytes, "barrier block");
 
 struct Work {
   int b, h, s;
@@ -138,6 +138,28 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return r;
 }
 
+__device__ __forceinline__ uint4 lds_u4(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+// 2 N bytes
+template <int N>
+__device__ __forceinline__ uint32_t lds_u16(uint32_t at) {
+  uint32_t v;
+  if constexpr (N == 2) {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+  } else {
+    uint16_t h;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(at));
+    v = h;
+  }
+  return v;
+}
+__device__ __forceinline__ void sts_u4(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 // One value per row of eight from 32 lanes: lane r (r < 8, and every lane alike modulo 8) gets row r's sum.
 __device__ __forceinline__ float sum_rows8(const float* l, int lane) {
   float a[4], b[2], c;
@@ -159,11 +181,14 @@ __device__ __forceinline__ float sum_rows8(const float* l, int lane) {
   return c;
 }
 
-template <int HD>
+template <int HD, int NT>
 __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const PackedAttnParams p) {
-  using C = Cfg<HD>;
+  using C = Cfg<HD, NT>;
+  constexpr int kStages = C::kStages;
+  constexpr bool kTrade = NT > kFewN;     // the softmax groups take up registers that the others give up
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sbase - smem_u32(smem_raw));
   uint8_t* sV = smem + C::kVOffset;
   uint8_t* sP = smem + C::kPOffset;
   uint8_t* sQ = smem + C::kQOffset;
@@ -174,12 +199,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
   if (threadIdx.x == kProducerWarp * 32) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&sh->full[i], 1);
-      mbar_init(&sh->empty[i], 8);
+      mbar_init(&sh->empty[i], 16);
     }
     for (int i = 0; i < kGeo; ++i) mbar_init(&sh->geo_full[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh->k_ready[i], 4);
-      mbar_init(&sh->v_ready[i], 4);
+      mbar_init(&sh->k_ready[i], 8);
+      mbar_init(&sh->v_ready[i], 8);
       mbar_init(&sh->s_done[i], 1);
       mbar_init(&sh->p_ready[i], 4);
       mbar_init(&sh->pv_done[i], 1);
@@ -216,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
   if (w.bad && threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(p.err, kErrDeviceInput);
 
   if (warp >= kProducerWarp) {
-    regs_dec<kRegsRest>();
+    if constexpr (kTrade) regs_dec<kRegsRest>();
     if (warp == kProducerWarp) {
       // ------------------------------ records and geometry --------------------------------
       const uint64_t pol = l2_policy_evict_first();
@@ -247,29 +272,28 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
           }
         }
         const int st = j % kStages;
-        bool go = true;
+        if (j >= kStages &&
+            !__all_sync(0xffffffffu, mbar_wait_tested(&sh->empty[st], ((j / kStages) - 1) & 1, abort, p.err)))
+          break;
         if (lane == 0) {
-          if (j >= kStages) go = mbar_wait(&sh->empty[st], ((j / kStages) - 1) & 1, abort, p.err);
-          if (go) {
-            const int g = j % kGeo;
+          const int g = j % kGeo;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              sh->base[g][c] = ok[c] ? cid[c] * kChunk : 0;
-              sh->valid[g][c] = ok[c] ? 1 : 0;
-            }
-            mbar_arrive(&sh->geo_full[g]);
-            mbar_arrive_expect_tx(&sh->full[st], n * 2 * C::kRecord);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              if (!ok[c]) continue;
-              const size_t from = (static_cast<size_t>(sl[c]) * p.hkv + w.h) * C::kRecord;
-              uint8_t* to = sStage + st * C::kStageBytes;
-              bulk_load(to + c * C::kRecord, p.k_pool + from, C::kRecord, &sh->full[st], pol);
-              bulk_load(to + (2 + c) * C::kRecord, p.v_pool + from, C::kRecord, &sh->full[st], pol);
-            }
+          for (int c = 0; c < 2; ++c) {
+            sh->base[g][c] = ok[c] ? cid[c] * kChunk : 0;
+            sh->valid[g][c] = ok[c] ? 1 : 0;
           }
+          mbar_arrive(&sh->geo_full[g]);
+          mbar_arrive_expect_tx(&sh->full[st], n * 2 * C::kRecord);
         }
-        if (!__shfl_sync(0xffffffffu, go ? 1 : 0, 0)) break;
+        __syncwarp();
+        // lanes 0, 1: K of the two chunks, 2, 3: V
+        const bool mine_ok = lane & 1 ? ok[1] : ok[0];
+        if (lane < 4 && mine_ok) {
+          const int mine = lane & 1 ? sl[1] : sl[0];
+          const size_t from = (static_cast<size_t>(mine) * p.hkv + w.h) * C::kRecord;
+          bulk_load(sStage + st * C::kStageBytes + lane * C::kRecord, (lane < 2 ? p.k_pool : p.v_pool) + from, C::kRecord,
+                    &sh->full[st], pol);
+        }
         issued = j + 1;
       }
       // Every copy lands before the CTA can exit.
@@ -279,105 +303,116 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
       __syncwarp();
     } else if (warp == kMmaWarp) {
       // ------------------------------ MMA issuer ------------------------------------------
-      if (lane == 0 && w.nt > 0) {
+      // The whole warp runs the loop (see elect_one). Tensor memory is allocated whole: it starts at column 0.
+      const int nt = uniform(w.nt), n = (uniform(w.rows) + 15) & ~15;
+      if (nt > 0) {
         if (p.timeout_test_ns != 0) mbar_wait_limit(&sh->never, 0, p.timeout_test_ns, abort, p.err);
-        bool ok = !*abort && mbar_wait(&sh->q_ready, 0, abort, p.err);
+        bool ok = __all_sync(0xffffffffu, !*abort && mbar_wait(&sh->q_ready, 0, abort, p.err));
         tc_fence_after();
-        const int n = (w.rows + 15) & ~15;
         const uint32_t idesc_s = idesc_f16_f32(128, n, 0, 0);
         const uint32_t idesc_o = idesc_f16_f32(128, n, 1, 1);
-        const uint64_t qdesc = sw128_desc(smem_u32(sQ), 16, 1024);
-        const uint64_t vdesc = sw128_desc(smem_u32(sV), C::kBoxBytes, 1024);
-        const uint64_t pdesc = sw128_desc(smem_u32(sP), C::kBoxBytes, 1024);
+        const uint64_t qdesc = sw128_desc(sbase + C::kQOffset, 16, 1024);
+        const uint64_t vdesc = sw128_desc(sbase + C::kVOffset, C::kBoxBytes, 1024);
+        const uint64_t pdesc = sw128_desc(sbase + C::kPOffset, C::kBoxBytes, 1024);
         // S^T of tile j over its group's buffer: free once the group's P of tile j - 2 is written.
         auto issue_s = [&](int j) {
           tc_fence_after();
           const int g = j & 1;
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < HD / 16; ++kk)
-            mma_ts(tbase + kColS + g * 96, tbase + kColK + g * 64 + kk * 8,
-                   qdesc + static_cast<uint64_t>(((kk >> 2) * C::kQBoxBytes + (kk & 3) * 32) >> 4), idesc_s, kk > 0 ? 1u : 0u);
-          mma_commit(&sh->s_done[g]);
+            for (int kk = 0; kk < HD / 16; ++kk)
+              mma_ts(kColS + g * 96, kColK + g * 64 + kk * 8,
+                     qdesc + static_cast<uint64_t>(((kk >> 2) * C::kQBoxBytes + (kk & 3) * 32) >> 4), idesc_s, kk > 0 ? 1u : 0u);
+            mma_commit(&sh->s_done[g]);
+          }
+          __syncwarp();
         };
-        for (int j = 0; ok && j < 2 && j < w.nt; ++j) {
-          ok = mbar_wait(&sh->k_ready[j & 1], 0, abort, p.err);
+        auto wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, mbar_wait_tested(bar, parity, abort, p.err)); };
+        for (int j = 0; ok && j < 2 && j < nt; ++j) {
+          ok = wait(&sh->k_ready[j & 1], 0);
           if (ok) issue_s(j);
         }
-        for (int j = 0; ok && j < w.nt; ++j) {
+        for (int j = 0; ok && j < nt; ++j) {
           const int g = j & 1, ph = (j >> 1) & 1;
-          ok = mbar_wait(&sh->p_ready[g], ph, abort, p.err);
+          ok = wait(&sh->p_ready[g], ph);
           if (!ok) break;
-          bool next = j + 2 < w.nt;
-          if (next && mbar_test_wait(&sh->k_ready[g], ph ^ 1)) {
+          bool next = j + 2 < nt;
+          if (next && __all_sync(0xffffffffu, mbar_test_wait(&sh->k_ready[g], ph ^ 1))) {
             issue_s(j + 2);
             next = false;
           }
-          ok = mbar_wait(&sh->v_ready[g], ph, abort, p.err);
+          ok = wait(&sh->v_ready[g], ph);
           if (!ok) break;
           tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk)
-            mma_ss(tbase + kColO + g * 96, vdesc + static_cast<uint64_t>((g * C::kVBytes + kk * 2048) >> 4),
-                   pdesc + static_cast<uint64_t>((g * C::kPBytes + kk * 2048) >> 4), idesc_o, (j > 1 || kk > 0) ? 1u : 0u);
-          mma_commit(&sh->pv_done[g]);
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              mma_ss(kColO + g * 96, vdesc + static_cast<uint64_t>((g * C::kVBytes + kk * 2048) >> 4),
+                     pdesc + static_cast<uint64_t>((g * C::kPBytes + kk * 2048) >> 4), idesc_o, (j > 1 || kk > 0) ? 1u : 0u);
+            mma_commit(&sh->pv_done[g]);
+          }
+          __syncwarp();
           if (next) {
-            ok = mbar_wait(&sh->k_ready[g], ph ^ 1, abort, p.err);
+            ok = wait(&sh->k_ready[g], ph ^ 1);
             if (ok) issue_s(j + 2);
           }
         }
-        mma_commit(&sh->drain);
+        if (elect_one()) mma_commit(&sh->drain);
+        __syncwarp();
         mbar_drain(&sh->drain, 0, p.err);
       }
       __syncwarp();
     }
-  } else if (warp >= 8) {
+  } else if (warp >= kKWarp) {
     // ------------------------------ K and V to fp16 -----------------------------------------
-    regs_dec<kRegsUnpack>();
-    const bool is_v = warp >= 12;
+    if constexpr (kTrade) regs_dec<kRegsUnpack>();
+    constexpr int kPieces = HD / 64;                     // of 32 channels: half of a key's
+    const bool is_v = warp >= kVWarp;
+    const int x0 = (warp & 4) ? kPieces : 0;
     const int key = (warp & 3) * 32 + lane;              // of the tile; a TMEM lane
     const int c = key / kChunk, tok = key % kChunk;
     uint64_t* done = is_v ? sh->pv_done : sh->s_done;
     uint64_t* ready = is_v ? sh->v_ready : sh->k_ready;
-    const uint32_t lane_base = tbase + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t rec = sbase + C::kStageOffset + ((is_v ? 2 : 0) + c) * C::kRecord;
+    const uint32_t scales_at = rec + kChunk * (HD / 2) + tok * (HD / 16) + 2 * x0;
+    const uint32_t codes_at = rec + (x0 * kChunk + tok) * 16;
+    const uint32_t kto = (static_cast<uint32_t>((warp & 3) * 32) << 16) + kColK + x0 * 16;
+    const uint32_t vto = sbase + C::kVOffset + (x0 / 2) * C::kBoxBytes + key * 128;
+    int st = 0, stage_phase = 0;
     for (int j = 0; j < w.nt; ++j) {
-      const int st = j % kStages, g = j & 1, u = j >> 1;
-      bool ok = mbar_wait(&sh->full[st], (j / kStages) & 1, abort, p.err);
-      if (ok && u > 0) ok = mbar_wait(&done[g], (u - 1) & 1, abort, p.err);
+      const int g = j & 1, u = j >> 1;
+      bool ok = mbar_wait_tested(&sh->full[st], stage_phase, abort, p.err);
+      if (ok && u > 0) ok = mbar_wait_tested(&done[g], (u - 1) & 1, abort, p.err);
       if (!__all_sync(0xffffffffu, ok)) break;
-      const uint8_t* rec = sStage + st * C::kStageBytes + ((is_v ? 2 : 0) + c) * C::kRecord;
-      uint32_t scales[HD / 64];                          // four scale bytes a word
+      // Everything that the key has is loaded before the first store (the compiler keeps loads behind stores).
+      uint32_t scales = lds_u16<kPieces>(scales_at + st * C::kStageBytes);
+      uint4 codes[kPieces];
 #pragma unroll
-      for (int i = 0; i < HD / 64; ++i)
-        scales[i] = *reinterpret_cast<const uint32_t*>(rec + kChunk * (HD / 2) + tok * (HD / 16) + 4 * i);
+      for (int x = 0; x < kPieces; ++x) codes[x] = lds_u4(codes_at + st * C::kStageBytes + x * kChunk * 16);
       if (is_v) {
         // Keys that no row attends may hold anything: P is 0 there, but 0 * NaN is NaN.
         const int geo = j % kGeo;
-        if (!sh->valid[geo][c] || sh->base[geo][c] + tok >= w.L) {
-#pragma unroll
-          for (int i = 0; i < HD / 64; ++i) scales[i] = 0u;
-        }
+        if (!sh->valid[geo][c] || sh->base[geo][c] + tok >= w.L) scales = 0u;
       } else {
         tc_fence_after();
       }
 #pragma unroll
-      for (int x = 0; x < HD / 32; ++x) {                // 32 channels: 16 bytes of codes, two scales
-        const uint4 codes = *reinterpret_cast<const uint4*>(rec + (x * kChunk + tok) * 16);
-        const uint32_t two = e4m3_pair_f16((scales[x / 2] >> (16 * (x & 1))) & 0xffffu);
+      for (int x = 0; x < kPieces; ++x) {
+        const uint32_t two = e4m3_pair_f16((scales >> (16 * x)) & 0xffffu);
         const uint32_t s0 = __byte_perm(two, two, 0x1010), s1 = __byte_perm(two, two, 0x3232);
         uint32_t out[16];
-        unpack_word(codes.x, s0, out);
-        unpack_word(codes.y, s0, out + 4);
-        unpack_word(codes.z, s1, out + 8);
-        unpack_word(codes.w, s1, out + 12);
+        unpack_word(codes[x].x, s0, out);
+        unpack_word(codes[x].y, s0, out + 4);
+        unpack_word(codes[x].z, s1, out + 8);
+        unpack_word(codes[x].w, s1, out + 12);
         if (!is_v) {
-          tmem_st16_async(lane_base + kColK + g * 64 + x * 16, out);
+          tmem_st16_async(kto + g * 64 + x * 16, out);
         } else {
-          uint8_t* row = sV + g * C::kVBytes + (x / 2) * C::kBoxBytes + key * 128;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int word = (x & 1) * 4 + i;            // 16-byte word of the 128-byte row
-            *reinterpret_cast<uint4*>(row + ((word ^ (key & 7)) << 4)) =
-                make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
+            const int word = ((x0 + x) & 1) * 4 + i;     // 16-byte word of the 128-byte row
+            sts_u4(vto + g * C::kVBytes + ((word ^ (key & 7)) << 4),
+                   make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]));
           }
         }
       }
@@ -392,15 +427,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
         mbar_arrive(&sh->empty[st]);
         mbar_arrive(&ready[g]);
       }
+      if (++st == kStages) st = 0, stage_phase ^= 1;
     }
   } else {
     // ------------------------------ softmax ---------------------------------------------------
-    regs_inc<kRegsSoftmax>();
+    if constexpr (kTrade) regs_inc<kRegsSoftmax>();
     const int grp = warp >> 2, wq = warp & 3, tg = threadIdx.x & 127;
     const int key = tg;
     const int bar = 1 + grp;                             // named barrier of the group; 3: both groups
     // Q: words of 8 channels, all of a thread's in registers while the tile's largest value is found
-    constexpr int kWords = kMaxN * HD / 8 / 256 + ((kMaxN * HD / 8) % 256 != 0 ? 1 : 0);
+    constexpr int kWords = (NT * HD / 8 + 255) / 256;
     float q_scale;                                       // of a score: softmax scale, g of K, the queries' power of two
     {
       uint4 qv[kWords];
@@ -435,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           o[e] = pack_f16(__uint_as_float(ws[e] << 16) * down, __uint_as_float(ws[e] & 0xffff0000u) * down);
-        if (r < kMaxN)
+        if (r < NT)
           *reinterpret_cast<uint4*>(sQ + (cw >> 3) * C::kQBoxBytes + r * 128 + (((cw & 7) ^ (r & 7)) << 4)) =
               make_uint4(o[0], o[1], o[2], o[3]);
       }
@@ -443,10 +479,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->q_ready);
     }
-    if (tg < kMaxN) {
+    if (tg < NT) {
       // (rows past the block, Q = 0, keep weight 1: their columns are never read)
       sh->neg_ref[grp][tg] = tg < w.rows ? INFINITY : 0.f;
-      sh->limit[grp][tg] = tg < w.rows ? -INFINITY : INFINITY;
+      sh->neg_limit[grp][tg] = tg < w.rows ? INFINITY : -INFINITY;
     }
     named_sync(bar, 128);
 
@@ -454,51 +490,58 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
     const uint32_t s_at = lane_base + kColS + grp * 96, o_at = lane_base + kColO + grp * 96;
     uint8_t* prow = sP + grp * C::kPBytes + key * 128;
     const int p0 = w.L - w.nq;
-    float l[kMaxN];
+    float l[NT];
 #pragma unroll
-    for (int r = 0; r < kMaxN; ++r) l[r] = 0.f;
+    for (int r = 0; r < NT; ++r) l[r] = 0.f;
     bool dead = false;                                   // a wait of this warp gave up
     int u = 0;                                           // tiles of this group so far
     for (int j = grp; j < w.nt; j += 2, ++u) {
       const int geo = j % kGeo;
-      if (!mbar_wait(&sh->geo_full[geo], (j / kGeo) & 1, abort, p.err)) dead = true;
+      if (!mbar_wait_tested(&sh->geo_full[geo], (j / kGeo) & 1, abort, p.err)) dead = true;
       // Rows from n_min on attend this lane's key: row n is of block query (row0 + n) / G, at position p0 + that.
       const int pos = sh->base[geo][key / kChunk] + key % kChunk;
       int n_min = 0;
       if (!sh->valid[geo][key / kChunk] || pos >= w.L)
-        n_min = kMaxN;
+        n_min = NT;
       else if (pos > p0)
-        n_min = min(static_cast<long long>(kMaxN), max(0ll, static_cast<long long>(pos - p0) * p.group - w.row0));
+        n_min = min(static_cast<long long>(NT), max(0ll, static_cast<long long>(pos - p0) * p.group - w.row0));
       const bool whole = __all_sync(0xffffffffu, n_min == 0);
       if (!mbar_wait(&sh->s_done[grp], u & 1, abort, p.err)) dead = true;
       dead = __any_sync(0xffffffffu, dead);
       tc_fence_after();
       bool moves = dead;
       if (!dead) {
+        float over[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // largest s - limit
+        uint32_t buf[2][16];                             // columns of 16 rows, the next 16 on their way
+        tmem_ld16_async(s_at, buf[0]);
 #pragma unroll
-        for (int cb = 0; cb < kMaxN / 16; ++cb) {
+        for (int cb = 0; cb < NT / 16; ++cb) {
           if (cb * 16 < w.rows) {
-            uint32_t sr[16];
-            tmem_ld16(s_at + cb * 16, sr);
-            const float4* lim = reinterpret_cast<const float4*>(&sh->limit[grp][cb * 16]);
+            uint32_t(&sr)[16] = buf[cb & 1];
+            tmem_wait_ld16(sr);
+            if (cb + 1 < NT / 16 && (cb + 1) * 16 < w.rows) tmem_ld16_async(s_at + (cb + 1) * 16, buf[(cb + 1) & 1]);
+            if (!whole) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) sr[e] = cb * 16 + e >= n_min ? sr[e] : 0xff800000u;
+            }
+            const float4* lim = reinterpret_cast<const float4*>(&sh->neg_limit[grp][cb * 16]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float4 f = lim[e];
-              const int n = cb * 16 + 4 * e;
-              moves = moves || (__uint_as_float(sr[4 * e]) > f.x && n >= n_min) ||
-                      (__uint_as_float(sr[4 * e + 1]) > f.y && n + 1 >= n_min) ||
-                      (__uint_as_float(sr[4 * e + 2]) > f.z && n + 2 >= n_min) ||
-                      (__uint_as_float(sr[4 * e + 3]) > f.w && n + 3 >= n_min);
+              const float2 a = add_f32x2(make_float2(__uint_as_float(sr[4 * e]), __uint_as_float(sr[4 * e + 1])), make_float2(f.x, f.y));
+              const float2 b = add_f32x2(make_float2(__uint_as_float(sr[4 * e + 2]), __uint_as_float(sr[4 * e + 3])), make_float2(f.z, f.w));
+              over[e] = fmaxf(fmaxf(fmaxf(over[e], a.x), fmaxf(a.y, b.x)), b.y);
             }
           }
         }
+        moves = fmaxf(fmaxf(over[0], over[1]), fmaxf(over[2], over[3])) > 0.f;
       }
       if (named_any(bar, 128, moves)) {
         // A row's weights would pass the limit (or it has no reference yet): the rows' maxima over the tile, new
         // references for those rows, their sums and O scaled. Every warp of the group comes here or none.
         if (named_any(bar, 128, dead)) break;
 #pragma unroll
-        for (int cb = 0; cb < kMaxN / 8; ++cb) {
+        for (int cb = 0; cb < NT / 8; ++cb) {
           if (cb * 8 < w.rows) {
             uint32_t sr[8];
             tmem_ld8(s_at + cb * 8, sr);
@@ -516,12 +559,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
           const float m = fmaxf(fmaxf(sh->part[grp][0][tg], sh->part[grp][1][tg]),
                                 fmaxf(sh->part[grp][2][tg], sh->part[grp][3][tg]));
           float a = 1.f;
-          if (m > sh->limit[grp][tg]) {
+          if (m > -sh->neg_limit[grp][tg]) {
             const float ref = m * q_scale - kTop;
             const float old = -sh->neg_ref[grp][tg];
             a = ex2_approx(old - ref);                   // 0 for the first
             sh->neg_ref[grp][tg] = -ref;
-            sh->limit[grp][tg] = (ref + kLimit) / q_scale;
+            sh->neg_limit[grp][tg] = (ref + kLimit) / -q_scale;
           }
           sh->alpha[grp][tg] = a;
         }
@@ -531,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
           tc_fence_after();
         }
 #pragma unroll
-        for (int cb = 0; cb < kMaxN / 8; ++cb) {
+        for (int cb = 0; cb < NT / 8; ++cb) {
           if (cb * 8 < w.rows) {
             uint32_t o[8];
             if (u > 0 && !dead) tmem_ld8(o_at + cb * 8, o);
@@ -549,14 +592,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
       }
       // P = 2^(s scale - ref), and its sums
       if (u > 0) {
-        dead = !__all_sync(0xffffffffu, mbar_wait(&sh->pv_done[grp], (u - 1) & 1, abort, p.err));
+        dead = !__all_sync(0xffffffffu, mbar_wait_tested(&sh->pv_done[grp], (u - 1) & 1, abort, p.err));
       }
       const float2 sc2 = make_float2(q_scale, q_scale);
+      uint32_t buf[2][16];
+      tmem_ld16_async(s_at, buf[0]);
 #pragma unroll
-      for (int cb = 0; cb < kMaxN / 16; ++cb) {
+      for (int cb = 0; cb < NT / 16; ++cb) {
         if (cb * 16 < w.rows) {
-          uint32_t sr[16];
-          tmem_ld16(s_at + cb * 16, sr);
+          uint32_t(&sr)[16] = buf[cb & 1];
+          tmem_wait_ld16(sr);
+          if (cb + 1 < NT / 16 && (cb + 1) * 16 < w.rows) tmem_ld16_async(s_at + (cb + 1) * 16, buf[(cb + 1) & 1]);
           const float4* nr = reinterpret_cast<const float4*>(&sh->neg_ref[grp][cb * 16]);
           uint32_t pk[8];
 #pragma unroll
@@ -599,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
     if (u > 0 && !dead) dead = !__all_sync(0xffffffffu, mbar_wait(&sh->pv_done[grp], (u - 1) & 1, abort, p.err));
     tc_fence_after();
 #pragma unroll
-    for (int cb = 0; cb < kMaxN / 8; ++cb) {
+    for (int cb = 0; cb < NT / 8; ++cb) {
       if (cb * 8 < w.rows) {
         const float sum = sum_rows8(l + cb * 8, lane);
         if (lane < 8) sh->part[grp][wq][cb * 8 + lane] = sum;
@@ -632,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
     if (w.nt > 0 && wq * 32 < HD) {
       // lane = channel: 32 neighbouring channels of a row are one 128-byte store. The groups take rows of eight in turn.
 #pragma unroll
-      for (int cb = 0; cb < kMaxN / 8; ++cb) {
+      for (int cb = 0; cb < NT / 8; ++cb) {
         if ((cb & 1) == grp && cb * 8 < w.rows) {
           uint32_t o0[8], o1[8];
           tmem_ld8(lane_base + kColO + cb * 8, o0);
@@ -661,23 +707,23 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
   }
 }
 
-template <int HD>
-cudaError_t launch_hd(const PackedAttnParams& p, int num_seqs, cudaStream_t stream) {
+template <int HD, int NT>
+cudaError_t launch_t(const PackedAttnParams& p, int num_seqs, cudaStream_t stream) {
   static size_t done[64] = {};
   static bool registers = false;
-  auto kern = attend_packed_kernel<HD>;
+  auto kern = attend_packed_kernel<HD, NT>;
   if (!registers) {
     // The warpgroups trade registers; a kernel launched with fewer than they take up would wait for ever.
     cudaFuncAttributes a;
     const cudaError_t e = cudaFuncGetAttributes(&a, kern);
     if (e != cudaSuccess) return e;
-    if (a.numRegs < kRegsLaunch) return cudaErrorNotSupported;
+    if (NT > kFewN && a.numRegs < kRegsLaunch) return cudaErrorNotSupported;
     registers = true;
   }
-  const cudaError_t e = ensure_smem_limit(kern, Cfg<HD>::kSmemBytes, done);
+  const cudaError_t e = ensure_smem_limit(kern, Cfg<HD, NT>::kSmemBytes, done);
   if (e != cudaSuccess) return e;
   const dim3 grid(p.num_splits, p.hkv, num_seqs * p.n_tiles);
-  return launch_pdl(kern, grid, dim3(kThreads), Cfg<HD>::kSmemBytes, stream, p);
+  return launch_pdl(kern, grid, dim3(kThreads), Cfg<HD, NT>::kSmemBytes, stream, p);
 }
 
 }  // namespace
@@ -685,7 +731,9 @@ cudaError_t launch_hd(const PackedAttnParams& p, int num_seqs, cudaStream_t stre
 int packed_tile_rows() { return kMaxN; }
 
 cudaError_t launch_attend_packed(const PackedAttnParams& p, int num_seqs, cudaStream_t stream) {
-  return p.head_dim == 128 ? launch_hd<128>(p, num_seqs, stream) : launch_hd<64>(p, num_seqs, stream);
+  if (p.tile_rows <= kFewN)
+    return p.head_dim == 128 ? launch_t<128, kFewN>(p, num_seqs, stream) : launch_t<64, kFewN>(p, num_seqs, stream);
+  return p.head_dim == 128 ? launch_t<128, kMaxN>(p, num_seqs, stream) : launch_t<64, kMaxN>(p, num_seqs, stream);
 }
 
 }  // namespace vfy
