@@ -12,10 +12,11 @@
 // One CTA per (split, KV head, sequence and row tile), a contiguous run of tiles of two chunks. Roles:
 //   warps 0-3, 4-7   softmax of even / odd tiles: a lane is a key, its 32-bit columns are the rows. Two groups with a
 //                    reference, row sums and O of their own, merged at the end; a group has two tiles' time for one.
-//   warps 8-11       K: a lane reads its key's codes and scales, writes fp16 into tensor memory (the A operand of S)
-//   warps 12-15      V: fp16 into shared memory, channels contiguous (the A operand of O^T, M-major)
-//   warp 16          bulk copies of the records (contiguous: no tensor map), and the tiles' geometry
-//   warp 17          tensor memory, and the MMA issuer (one lane)
+//   warps 8-11, 12-15   K of even / odd tiles: a lane reads its key's codes and scales, writes fp16 into tensor memory
+//                    (the A operand of S)
+//   warps 16-19, 20-23  V of even / odd tiles: fp16 into shared memory, channels contiguous (the A operand of O^T, M-major)
+//   warp 24          bulk copies of the records (contiguous: no tensor map), and the tiles' geometry
+//   warp 25          tensor memory, and the MMA issuer
 #include <cuda_bf16.h>
 
 #include "packed.cuh"
@@ -39,6 +40,8 @@ constexpr uint32_t kColS = 128;           // S^T of the two groups, 96 columns a
 constexpr uint32_t kColO = 320;           // O^T of the two groups
 constexpr float kTop = 7.f;               // a row's maximum when its reference is set (log2)
 constexpr float kLimit = 15.f;            // the reference moves when a weight would pass 2^15
+constexpr float kClamp = 24.f;            // weights past the limit are held at 2^24 until they are worked out again
+constexpr float kNone = 1e30f;            // minus the reference of a row that has none: every score passes the limit
 
 template <int HD, int NT>
 struct Cfg {
@@ -74,7 +77,7 @@ struct Shared {
   unsigned q_top;                         // largest |q| of the tile, as bf16 bits
   int base[kGeo][2], valid[kGeo][2];      // per chunk of a tile
   alignas(16) float neg_ref[2][kMaxN];    // [group] minus the rows' reference, log2 units
-  alignas(16) float neg_limit[2][kMaxN];  // minus the S value above which the reference moves
+  alignas(16) float old_ref[2][kMaxN];    // minus the reference before it moved
   alignas(16) float alpha[2][kMaxN];
   alignas(16) float part[2][4][kMaxN];    // [group][warp]: maxima, at the end sums
 };
@@ -138,22 +141,17 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return r;
 }
 
+__device__ __forceinline__ float2 pair(const uint32_t* r, int i) {
+  return make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+}
 __device__ __forceinline__ uint4 lds_u4(uint32_t at) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
   return v;
 }
-// 2 N bytes
-template <int N>
-__device__ __forceinline__ uint32_t lds_u16(uint32_t at) {
+__device__ __forceinline__ uint32_t lds_u32(uint32_t at) {
   uint32_t v;
-  if constexpr (N == 2) {
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
-  } else {
-    uint16_t h;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(at));
-    v = h;
-  }
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
   return v;
 }
 __device__ __forceinline__ void sts_u4(uint32_t at, uint4 v) {
@@ -161,7 +159,8 @@ __device__ __forceinline__ void sts_u4(uint32_t at, uint4 v) {
 }
 
 // One value per row of eight from 32 lanes: lane r (r < 8, and every lane alike modulo 8) gets row r's sum.
-__device__ __forceinline__ float sum_rows8(const float* l, int lane) {
+__device__ __forceinline__ float sum_rows8(const float2* l2, int lane) {
+  const float l[8] = {l2[0].x, l2[0].y, l2[1].x, l2[1].y, l2[2].x, l2[2].y, l2[3].x, l2[3].y};
   float a[4], b[2], c;
   const bool h4 = lane & 4, h2 = lane & 2, h1 = lane & 1;
 #pragma unroll
@@ -199,12 +198,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
   if (threadIdx.x == kProducerWarp * 32) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&sh->full[i], 1);
-      mbar_init(&sh->empty[i], 16);
+      mbar_init(&sh->empty[i], 8);
     }
     for (int i = 0; i < kGeo; ++i) mbar_init(&sh->geo_full[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh->k_ready[i], 8);
-      mbar_init(&sh->v_ready[i], 8);
+      mbar_init(&sh->k_ready[i], 4);
+      mbar_init(&sh->v_ready[i], 4);
       mbar_init(&sh->s_done[i], 1);
       mbar_init(&sh->p_ready[i], 4);
       mbar_init(&sh->pv_done[i], 1);
@@ -314,6 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
         const uint64_t qdesc = sw128_desc(sbase + C::kQOffset, 16, 1024);
         const uint64_t vdesc = sw128_desc(sbase + C::kVOffset, C::kBoxBytes, 1024);
         const uint64_t pdesc = sw128_desc(sbase + C::kPOffset, C::kBoxBytes, 1024);
+        auto wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, mbar_wait_tested(bar, parity, abort, p.err)); };
         // S^T of tile j over its group's buffer: free once the group's P of tile j - 2 is written.
         auto issue_s = [&](int j) {
           tc_fence_after();
@@ -327,9 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
           }
           __syncwarp();
         };
-        auto wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, mbar_wait_tested(bar, parity, abort, p.err)); };
         for (int j = 0; ok && j < 2 && j < nt; ++j) {
-          ok = wait(&sh->k_ready[j & 1], 0);
+          ok = wait(&sh->k_ready[j], 0);
           if (ok) issue_s(j);
         }
         for (int j = 0; ok && j < nt; ++j) {
@@ -366,53 +365,50 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
   } else if (warp >= kKWarp) {
     // ------------------------------ K and V to fp16 -----------------------------------------
     if constexpr (kTrade) regs_dec<kRegsUnpack>();
-    constexpr int kPieces = HD / 64;                     // of 32 channels: half of a key's
     const bool is_v = warp >= kVWarp;
-    const int x0 = (warp & 4) ? kPieces : 0;
+    const int g = (warp >> 2) & 1;                       // even or odd tiles; their buffer
     const int key = (warp & 3) * 32 + lane;              // of the tile; a TMEM lane
     const int c = key / kChunk, tok = key % kChunk;
-    uint64_t* done = is_v ? sh->pv_done : sh->s_done;
-    uint64_t* ready = is_v ? sh->v_ready : sh->k_ready;
+    uint64_t* done = is_v ? &sh->pv_done[g] : &sh->s_done[g];
+    uint64_t* ready = is_v ? &sh->v_ready[g] : &sh->k_ready[g];
     const uint32_t rec = sbase + C::kStageOffset + ((is_v ? 2 : 0) + c) * C::kRecord;
-    const uint32_t scales_at = rec + kChunk * (HD / 2) + tok * (HD / 16) + 2 * x0;
-    const uint32_t codes_at = rec + (x0 * kChunk + tok) * 16;
-    const uint32_t kto = (static_cast<uint32_t>((warp & 3) * 32) << 16) + kColK + x0 * 16;
-    const uint32_t vto = sbase + C::kVOffset + (x0 / 2) * C::kBoxBytes + key * 128;
-    int st = 0, stage_phase = 0;
-    for (int j = 0; j < w.nt; ++j) {
-      const int g = j & 1, u = j >> 1;
+    const uint32_t scales_at = rec + kChunk * (HD / 2) + tok * (HD / 16);
+    const uint32_t codes_at = rec + tok * 16;
+    const uint32_t kto = (static_cast<uint32_t>((warp & 3) * 32) << 16) + kColK + g * 64;
+    const uint32_t vto = sbase + C::kVOffset + g * C::kVBytes + key * 128;
+    int st = g % kStages, stage_phase = 0;               // (kStages is even)
+    for (int j = g; j < w.nt; j += 2) {
+      const int u = j >> 1;
       bool ok = mbar_wait_tested(&sh->full[st], stage_phase, abort, p.err);
-      if (ok && u > 0) ok = mbar_wait_tested(&done[g], (u - 1) & 1, abort, p.err);
+      if (ok && u > 0) ok = mbar_wait_tested(done, (u - 1) & 1, abort, p.err);
       if (!__all_sync(0xffffffffu, ok)) break;
-      // Everything that the key has is loaded before the first store (the compiler keeps loads behind stores).
-      uint32_t scales = lds_u16<kPieces>(scales_at + st * C::kStageBytes);
-      uint4 codes[kPieces];
+      const uint32_t at = st * C::kStageBytes;
+      // Keys that no row attends may hold anything: P is 0 there, but 0 * NaN is NaN.
+      bool keep = true;
+      if (is_v) keep = sh->valid[j % kGeo][c] && sh->base[j % kGeo][c] + tok < w.L;
+      if (!is_v) tc_fence_after();
 #pragma unroll
-      for (int x = 0; x < kPieces; ++x) codes[x] = lds_u4(codes_at + st * C::kStageBytes + x * kChunk * 16);
-      if (is_v) {
-        // Keys that no row attends may hold anything: P is 0 there, but 0 * NaN is NaN.
-        const int geo = j % kGeo;
-        if (!sh->valid[geo][c] || sh->base[geo][c] + tok >= w.L) scales = 0u;
-      } else {
-        tc_fence_after();
-      }
+      for (int y = 0; y < HD / 64; ++y) {                // 64 channels: two words of codes, four scales
+        // (both words loaded before the first store: the compiler keeps loads behind stores)
+        const uint4 codes[2] = {lds_u4(codes_at + at + 2 * y * kChunk * 16), lds_u4(codes_at + at + (2 * y + 1) * kChunk * 16)};
+        const uint32_t scales = keep ? lds_u32(scales_at + at + 4 * y) : 0u;
 #pragma unroll
-      for (int x = 0; x < kPieces; ++x) {
-        const uint32_t two = e4m3_pair_f16((scales >> (16 * x)) & 0xffffu);
-        const uint32_t s0 = __byte_perm(two, two, 0x1010), s1 = __byte_perm(two, two, 0x3232);
-        uint32_t out[16];
-        unpack_word(codes[x].x, s0, out);
-        unpack_word(codes[x].y, s0, out + 4);
-        unpack_word(codes[x].z, s1, out + 8);
-        unpack_word(codes[x].w, s1, out + 12);
-        if (!is_v) {
-          tmem_st16_async(kto + g * 64 + x * 16, out);
-        } else {
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t two = e4m3_pair_f16(x == 0 ? scales & 0xffffu : scales >> 16);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int word = ((x0 + x) & 1) * 4 + i;     // 16-byte word of the 128-byte row
-            sts_u4(vto + g * C::kVBytes + ((word ^ (key & 7)) << 4),
-                   make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]));
+          for (int i = 0; i < 2; ++i) {                  // 16 channels: one scale
+            const uint32_t sc = __byte_perm(two, two, i == 0 ? 0x1010 : 0x3232);
+            uint32_t out[8];
+            unpack_word(i == 0 ? codes[x].x : codes[x].z, sc, out);
+            unpack_word(i == 0 ? codes[x].y : codes[x].w, sc, out + 4);
+            if (!is_v) {
+              tmem_st8_async(kto + (4 * y + 2 * x + i) * 8, out);
+            } else {
+#pragma unroll
+              for (int z = 0; z < 2; ++z)                // 16-byte words of the 128-byte row
+                sts_u4(vto + y * C::kBoxBytes + (((x * 4 + 2 * i + z) ^ (key & 7)) << 4),
+                       make_uint4(out[4 * z], out[4 * z + 1], out[4 * z + 2], out[4 * z + 3]));
+            }
           }
         }
       }
@@ -425,16 +421,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&sh->empty[st]);
-        mbar_arrive(&ready[g]);
+        mbar_arrive(ready);
       }
-      if (++st == kStages) st = 0, stage_phase ^= 1;
+      st += 2;
+      if (st >= kStages) st -= kStages, stage_phase ^= 1;
     }
   } else {
     // ------------------------------ softmax ---------------------------------------------------
     if constexpr (kTrade) regs_inc<kRegsSoftmax>();
     const int grp = warp >> 2, wq = warp & 3, tg = threadIdx.x & 127;
     const int key = tg;
-    const int bar = 1 + grp;                             // named barrier of the group; 3: both groups
+    const int bar = 2 + grp;                             // named barrier of the group; 1: both groups
     // Q: words of 8 channels, all of a thread's in registers while the tile's largest value is found
     constexpr int kWords = (NT * HD / 8 + 255) / 256;
     float q_scale;                                       // of a score: softmax scale, g of K, the queries' power of two
@@ -458,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
       }
       top = __reduce_max_sync(0xffffffffu, top);
       if (lane == 0) atomicMax(&sh->q_top, top);
-      named_sync(3, 256);
+      named_sync(1, 256);
       const int qe = max(static_cast<int>(sh->q_top >> 7) - 127 - 14, -100);
       const float down = __int_as_float((127 - qe) << 23);
       q_scale = p.scale_log2 * __int_as_float((127 + qe) << 23);
@@ -479,20 +476,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->q_ready);
     }
-    if (tg < NT) {
-      // (rows past the block, Q = 0, keep weight 1: their columns are never read)
-      sh->neg_ref[grp][tg] = tg < w.rows ? INFINITY : 0.f;
-      sh->neg_limit[grp][tg] = tg < w.rows ? INFINITY : -INFINITY;
-    }
+    // (rows past the block, Q = 0, keep weight 1: never read)
+    if (tg < NT) sh->neg_ref[grp][tg] = tg < w.rows ? kNone : 0.f;
     named_sync(bar, 128);
 
-    const uint32_t lane_base = tbase + (static_cast<uint32_t>(wq * 32) << 16);
+    const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t s_at = lane_base + kColS + grp * 96, o_at = lane_base + kColO + grp * 96;
-    uint8_t* prow = sP + grp * C::kPBytes + key * 128;
+    const uint32_t prow = sbase + C::kPOffset + grp * C::kPBytes + key * 128;
     const int p0 = w.L - w.nq;
-    float l[NT];
+    const float2 sc2 = make_float2(q_scale, q_scale);
+    float2 l[NT / 2];
 #pragma unroll
-    for (int r = 0; r < NT; ++r) l[r] = 0.f;
+    for (int r = 0; r < NT / 2; ++r) l[r] = make_float2(0.f, 0.f);
     bool dead = false;                                   // a wait of this warp gave up
     int u = 0;                                           // tiles of this group so far
     for (int j = grp; j < w.nt; j += 2, ++u) {
@@ -506,153 +501,126 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
       else if (pos > p0)
         n_min = min(static_cast<long long>(NT), max(0ll, static_cast<long long>(pos - p0) * p.group - w.row0));
       const bool whole = __all_sync(0xffffffffu, n_min == 0);
-      if (!mbar_wait(&sh->s_done[grp], u & 1, abort, p.err)) dead = true;
+      if (u > 0 && !mbar_wait_tested(&sh->pv_done[grp], (u - 1) & 1, abort, p.err)) dead = true;   // P is free, O complete
+      if (!mbar_wait_tested(&sh->s_done[grp], u & 1, abort, p.err)) dead = true;
       dead = __any_sync(0xffffffffu, dead);
       tc_fence_after();
-      bool moves = dead;
-      if (!dead) {
-        float over[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // largest s - limit
-        uint32_t buf[2][16];                             // columns of 16 rows, the next 16 on their way
-        tmem_ld16_async(s_at, buf[0]);
+      // Weights P = 2^(s scale - ref), their sums, and the largest exponent: sixteen rows at a time, the next sixteen's
+      // scores on their way. `undo` takes the weights against the old references off the sums first.
+      auto weigh = [&](bool undo) -> float {
+        float top[2] = {-INFINITY, -INFINITY};
+        uint32_t buf[2][16];
+        tmem_ld_async(s_at, buf[0]);
 #pragma unroll
         for (int cb = 0; cb < NT / 16; ++cb) {
           if (cb * 16 < w.rows) {
-            uint32_t(&sr)[16] = buf[cb & 1];
-            tmem_wait_ld16(sr);
-            if (cb + 1 < NT / 16 && (cb + 1) * 16 < w.rows) tmem_ld16_async(s_at + (cb + 1) * 16, buf[(cb + 1) & 1]);
-            if (!whole) {
+            uint32_t(&s)[16] = buf[cb & 1];
+            tmem_wait_ld(s);
+            if (cb + 1 < NT / 16 && (cb + 1) * 16 < w.rows) tmem_ld_async(s_at + (cb + 1) * 16, buf[(cb + 1) & 1]);
+            if (!whole) {                                // 2^-inf = 0
 #pragma unroll
-              for (int e = 0; e < 16; ++e) sr[e] = cb * 16 + e >= n_min ? sr[e] : 0xff800000u;
+              for (int e = 0; e < 16; ++e) s[e] = cb * 16 + e >= n_min ? s[e] : 0xff800000u;
             }
-            const float4* lim = reinterpret_cast<const float4*>(&sh->neg_limit[grp][cb * 16]);
+            if (undo) {
+              const float2* old = reinterpret_cast<const float2*>(&sh->old_ref[grp][cb * 16]);
+              const float2* al = reinterpret_cast<const float2*>(&sh->alpha[grp][cb * 16]);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float2 x = fma_f32x2(pair(s, 2 * e), sc2, old[e]);
+                float2& sum = l[cb * 8 + e];
+                sum.x = (sum.x - ex2_approx(fminf(x.x, kClamp))) * al[e].x;
+                sum.y = (sum.y - ex2_approx(fminf(x.y, kClamp))) * al[e].y;
+              }
+            }
+            const float4* nr = reinterpret_cast<const float4*>(&sh->neg_ref[grp][cb * 16]);
+            uint32_t pk[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float4 f = lim[e];
-              const float2 a = add_f32x2(make_float2(__uint_as_float(sr[4 * e]), __uint_as_float(sr[4 * e + 1])), make_float2(f.x, f.y));
-              const float2 b = add_f32x2(make_float2(__uint_as_float(sr[4 * e + 2]), __uint_as_float(sr[4 * e + 3])), make_float2(f.z, f.w));
-              over[e] = fmaxf(fmaxf(fmaxf(over[e], a.x), fmaxf(a.y, b.x)), b.y);
+              const float4 f = nr[e];
+              float2 a = fma_f32x2(pair(s, 4 * e), sc2, make_float2(f.x, f.y));
+              float2 b = fma_f32x2(pair(s, 4 * e + 2), sc2, make_float2(f.z, f.w));
+              top[0] = fmaxf(fmaxf(top[0], a.x), a.y);
+              top[1] = fmaxf(fmaxf(top[1], b.x), b.y);
+              a.x = ex2_approx(fminf(a.x, kClamp));
+              a.y = ex2_approx(fminf(a.y, kClamp));
+              b.x = ex2_approx(fminf(b.x, kClamp));
+              b.y = ex2_approx(fminf(b.y, kClamp));
+              l[cb * 8 + 2 * e] = add_f32x2(l[cb * 8 + 2 * e], a);
+              l[cb * 8 + 2 * e + 1] = add_f32x2(l[cb * 8 + 2 * e + 1], b);
+              pk[2 * e] = pack_f16(a.x, a.y);
+              pk[2 * e + 1] = pack_f16(b.x, b.y);
             }
+            const uint32_t box = prow + (cb >> 2) * C::kBoxBytes;
+            const int word = (cb & 3) * 2;               // 16-byte word of the key's rows: 8 words a box
+            sts_u4(box + ((word ^ (key & 7)) << 4), make_uint4(pk[0], pk[1], pk[2], pk[3]));
+            sts_u4(box + (((word + 1) ^ (key & 7)) << 4), make_uint4(pk[4], pk[5], pk[6], pk[7]));
           }
         }
-        moves = fmaxf(fmaxf(over[0], over[1]), fmaxf(over[2], over[3])) > 0.f;
-      }
-      if (named_any(bar, 128, moves)) {
-        // A row's weights would pass the limit (or it has no reference yet): the rows' maxima over the tile, new
-        // references for those rows, their sums and O scaled. Every warp of the group comes here or none.
+        return fmaxf(top[0], top[1]);
+      };
+      // (the first tile sets the references: its weights are worked out once they are)
+      const bool moves = u == 0 || (!dead && weigh(false) > kLimit);
+      if (named_any(bar, 128, moves || dead)) {
+        // A row's weights passed the limit (or it has no reference yet): the rows' maxima over the tile, new
+        // references for those rows, O scaled, the tile weighed again. All warps of the group come here or none.
         if (named_any(bar, 128, dead)) break;
+#pragma unroll 1
+        for (int r = 0; r < w.rows; r += 8) {
+          uint32_t sr[8];
+          tmem_ld8(s_at + r, sr);
+          float mine = -INFINITY;
 #pragma unroll
-        for (int cb = 0; cb < NT / 8; ++cb) {
-          if (cb * 8 < w.rows) {
-            uint32_t sr[8];
-            tmem_ld8(s_at + cb * 8, sr);
-            float mine = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float m = warp_max(cb * 8 + e >= n_min ? __uint_as_float(sr[e]) : -INFINITY);
-              mine = lane == e ? m : mine;
-            }
-            if (lane < 8) sh->part[grp][wq][cb * 8 + lane] = mine;
+          for (int e = 0; e < 8; ++e) {
+            const float m = warp_max(r + e >= n_min ? __uint_as_float(sr[e]) : -INFINITY);
+            mine = lane == e ? m : mine;
           }
+          if (lane < 8) sh->part[grp][wq][r + lane] = mine;
         }
         named_sync(bar, 128);
-        if (tg < w.rows) {
-          const float m = fmaxf(fmaxf(sh->part[grp][0][tg], sh->part[grp][1][tg]),
-                                fmaxf(sh->part[grp][2][tg], sh->part[grp][3][tg]));
+        if (tg < NT) {
+          const float old = sh->neg_ref[grp][tg];
           float a = 1.f;
-          if (m > -sh->neg_limit[grp][tg]) {
-            const float ref = m * q_scale - kTop;
-            const float old = -sh->neg_ref[grp][tg];
-            a = ex2_approx(old - ref);                   // 0 for the first
-            sh->neg_ref[grp][tg] = -ref;
-            sh->neg_limit[grp][tg] = (ref + kLimit) / -q_scale;
+          if (tg < w.rows) {
+            const float m = fmaxf(fmaxf(sh->part[grp][0][tg], sh->part[grp][1][tg]),
+                                  fmaxf(sh->part[grp][2][tg], sh->part[grp][3][tg])) * q_scale;
+            if (m + old > kLimit) {
+              a = old == kNone ? 0.f : ex2_approx(kTop - m - old);
+              sh->neg_ref[grp][tg] = kTop - m;
+            }
           }
+          sh->old_ref[grp][tg] = old;
           sh->alpha[grp][tg] = a;
         }
         named_sync(bar, 128);
         if (u > 0) {
-          dead = !__all_sync(0xffffffffu, mbar_wait(&sh->pv_done[grp], (u - 1) & 1, abort, p.err));
-          tc_fence_after();
-        }
-#pragma unroll
-        for (int cb = 0; cb < NT / 8; ++cb) {
-          if (cb * 8 < w.rows) {
+#pragma unroll 1
+          for (int r = 0; r < w.rows; r += 8) {
             uint32_t o[8];
-            if (u > 0 && !dead) tmem_ld8(o_at + cb * 8, o);
+            tmem_ld8(o_at + r, o);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float a = sh->alpha[grp][cb * 8 + e];
-              l[cb * 8 + e] *= a;
-              if (u > 0) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-            }
-            if (u > 0 && !dead) tmem_st8_async(o_at + cb * 8, o);
+            for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * sh->alpha[grp][r + e]);
+            tmem_st8_async(o_at + r, o);
           }
+          tmem_wait_st();
         }
-        tmem_wait_st();
-        if (named_any(bar, 128, dead)) break;
-      }
-      // P = 2^(s scale - ref), and its sums
-      if (u > 0) {
-        dead = !__all_sync(0xffffffffu, mbar_wait_tested(&sh->pv_done[grp], (u - 1) & 1, abort, p.err));
-      }
-      const float2 sc2 = make_float2(q_scale, q_scale);
-      uint32_t buf[2][16];
-      tmem_ld16_async(s_at, buf[0]);
-#pragma unroll
-      for (int cb = 0; cb < NT / 16; ++cb) {
-        if (cb * 16 < w.rows) {
-          uint32_t(&sr)[16] = buf[cb & 1];
-          tmem_wait_ld16(sr);
-          if (cb + 1 < NT / 16 && (cb + 1) * 16 < w.rows) tmem_ld16_async(s_at + (cb + 1) * 16, buf[(cb + 1) & 1]);
-          const float4* nr = reinterpret_cast<const float4*>(&sh->neg_ref[grp][cb * 16]);
-          uint32_t pk[8];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float4 f = nr[e];
-            float2 a = fma_f32x2(make_float2(__uint_as_float(sr[4 * e]), __uint_as_float(sr[4 * e + 1])), sc2, make_float2(f.x, f.y));
-            float2 b = fma_f32x2(make_float2(__uint_as_float(sr[4 * e + 2]), __uint_as_float(sr[4 * e + 3])), sc2, make_float2(f.z, f.w));
-            a.x = ex2_approx(a.x);
-            a.y = ex2_approx(a.y);
-            b.x = ex2_approx(b.x);
-            b.y = ex2_approx(b.y);
-            if (!whole) {
-              const int n = cb * 16 + 4 * e;
-              a.x = n >= n_min ? a.x : 0.f;
-              a.y = n + 1 >= n_min ? a.y : 0.f;
-              b.x = n + 2 >= n_min ? b.x : 0.f;
-              b.y = n + 3 >= n_min ? b.y : 0.f;
-            }
-            const float2 l0 = add_f32x2(make_float2(l[cb * 16 + 4 * e], l[cb * 16 + 4 * e + 1]), a);
-            const float2 l1 = add_f32x2(make_float2(l[cb * 16 + 4 * e + 2], l[cb * 16 + 4 * e + 3]), b);
-            l[cb * 16 + 4 * e] = l0.x;
-            l[cb * 16 + 4 * e + 1] = l0.y;
-            l[cb * 16 + 4 * e + 2] = l1.x;
-            l[cb * 16 + 4 * e + 3] = l1.y;
-            pk[2 * e] = pack_f16(a.x, a.y);
-            pk[2 * e + 1] = pack_f16(b.x, b.y);
-          }
-          uint8_t* box = prow + (cb >> 2) * C::kBoxBytes;
-          const int w0 = (cb & 3) * 2;
-          *reinterpret_cast<uint4*>(box + ((w0 ^ (key & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-          *reinterpret_cast<uint4*>(box + (((w0 + 1) ^ (key & 7)) << 4)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-        }
+        weigh(u > 0);
       }
       tc_fence_before();
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0 && !dead) mbar_arrive(&sh->p_ready[grp]);
+      if (lane == 0) mbar_arrive(&sh->p_ready[grp]);
     }
     // ---- epilogue: the groups' sums and O merged into the split's partial (m, l, O not normalised) ----
     if (u > 0 && !dead) dead = !__all_sync(0xffffffffu, mbar_wait(&sh->pv_done[grp], (u - 1) & 1, abort, p.err));
-    tc_fence_after();
 #pragma unroll
     for (int cb = 0; cb < NT / 8; ++cb) {
       if (cb * 8 < w.rows) {
-        const float sum = sum_rows8(l + cb * 8, lane);
+        const float sum = sum_rows8(&l[cb * 4], lane);
         if (lane < 8) sh->part[grp][wq][cb * 8 + lane] = sum;
       }
     }
     tc_fence_before();
-    named_sync(3, 256);
+    named_sync(1, 256);
     tc_fence_after();
     if (static_cast<int>(threadIdx.x) < w.rows) {
       const int r = threadIdx.x;
@@ -674,26 +642,23 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
       const size_t pidx = ((static_cast<size_t>(w.b) * p.row_tiles + rg / kMaxRows) * p.hkv + w.h) * p.num_splits + w.s;
       reinterpret_cast<float2*>(p.part_ml)[pidx * kMaxRows + rg % kMaxRows] = make_float2(m, sum);
     }
-    named_sync(3, 256);
+    named_sync(1, 256);
     if (w.nt > 0 && wq * 32 < HD) {
       // lane = channel: 32 neighbouring channels of a row are one 128-byte store. The groups take rows of eight in turn.
+#pragma unroll 1
+      for (int r0 = grp * 8; r0 < w.rows; r0 += 16) {
+        uint32_t o0[8], o1[8];
+        tmem_ld8(lane_base + kColO + r0, o0);
+        tmem_ld8(lane_base + kColO + 96 + r0, o1);
+        const int rg = w.row0 + r0;                      // (a multiple of 8: the eight lie in one of the combine's tiles)
+        float* dst = p.part_o +
+                     ((((static_cast<size_t>(w.b) * p.row_tiles + rg / kMaxRows) * p.hkv + w.h) * p.num_splits + w.s) * kMaxRows +
+                      rg % kMaxRows) * HD + wq * 32 + lane;
 #pragma unroll
-      for (int cb = 0; cb < NT / 8; ++cb) {
-        if ((cb & 1) == grp && cb * 8 < w.rows) {
-          uint32_t o0[8], o1[8];
-          tmem_ld8(lane_base + kColO + cb * 8, o0);
-          tmem_ld8(lane_base + kColO + 96 + cb * 8, o1);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int r = cb * 8 + e;
-            if (r < w.rows) {
-              const float w0 = sh->alpha[0][r], w1 = sh->alpha[1][r];
-              const float v = (w0 > 0.f ? w0 * __uint_as_float(o0[e]) : 0.f) + (w1 > 0.f ? w1 * __uint_as_float(o1[e]) : 0.f);
-              const int rg = w.row0 + r;
-              const size_t pidx =
-                  ((static_cast<size_t>(w.b) * p.row_tiles + rg / kMaxRows) * p.hkv + w.h) * p.num_splits + w.s;
-              p.part_o[(pidx * kMaxRows + rg % kMaxRows) * HD + wq * 32 + lane] = v;
-            }
+        for (int e = 0; e < 8; ++e) {
+          if (r0 + e < w.rows) {
+            const float w0 = sh->alpha[0][r0 + e], w1 = sh->alpha[1][r0 + e];
+            dst[e * HD] = (w0 > 0.f ? w0 * __uint_as_float(o0[e]) : 0.f) + (w1 > 0.f ? w1 * __uint_as_float(o1[e]) : 0.f);
           }
         }
       }
