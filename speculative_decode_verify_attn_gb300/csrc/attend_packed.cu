@@ -16,7 +16,7 @@
 //                    (the A operand of S)
 //   warps 16-19, 20-23  V of even / odd tiles: fp16 into shared memory, channels contiguous (the A operand of O^T, M-major)
 //   warp 24          bulk copies of the records (contiguous: no tensor map), and the tiles' geometry
-//   warp 25          tensor memory, and the MMA issuer
+//   warp 25, 26      the MMA issuers of S and of O (25 also holds tensor memory)
 #include <cuda_bf16.h>
 
 #include "packed.cuh"
@@ -33,7 +33,7 @@ static_assert(2 * kRegsSoftmax + 4 * kRegsUnpack + kRegsRest <= kGroups * kRegsL
 constexpr int kKWarp = 8, kVWarp = 16, kProducerWarp = 24, kMmaWarp = 25;
 constexpr int kKeys = 2 * kChunk;         // keys of a tile
 constexpr int kFewN = 16, kMaxN = 80;     // rows of a tile (two kernels): the softmax threads hold a partial sum of each
-constexpr int kGeo = 16;                  // tile-geometry ring: more than the tiles between producer and softmax
+constexpr int kBatch = 16;                // tiles whose chunks a warp's lanes hold; their geometry lies in two such batches
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColK = 0;             // two K tiles of up to 64 columns (two fp16 channels each)
 constexpr uint32_t kColS = 128;           // S^T of the two groups, 96 columns apart
@@ -66,16 +66,17 @@ struct Cfg {
 
 struct Shared {
   uint64_t full[6], empty[6];
-  uint64_t geo_full[kGeo];
+  uint64_t geo_full[2];
   uint64_t k_ready[2], v_ready[2];
   uint64_t s_done[2];                     // S of a tile: its S^T is there, its K is free
   uint64_t p_ready[2];                    // a tile's P is written, its S^T read
   uint64_t pv_done[2];                    // O^T holds the tile, its P and V are free
-  uint64_t q_ready, drain, never;
+  uint64_t q_ready, drain[2], never;
   uint32_t tmem_base;
   int abort;
   unsigned q_top;                         // largest |q| of the tile, as bf16 bits
-  int base[kGeo][2], valid[kGeo][2];      // per chunk of a tile
+  int base[2 * kBatch][2];                // position of a chunk's first token, -1: no chunk
+  int plain[2 * kBatch];                  // every row attends every key of the tile
   alignas(16) float neg_ref[2][kMaxN];    // [group] minus the rows' reference, log2 units
   alignas(16) float old_ref[2][kMaxN];    // minus the reference before it moved
   alignas(16) float alpha[2][kMaxN];
@@ -154,8 +155,9 @@ __device__ __forceinline__ uint32_t lds_u32(uint32_t at) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
   return v;
 }
+// (no memory clobber: what is written is read by MMAs alone, behind a proxy fence, and loads may move ahead of it)
 __device__ __forceinline__ void sts_u4(uint32_t at, uint4 v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w));
 }
 
 // One value per row of eight from 32 lanes: lane r (r < 8, and every lane alike modulo 8) gets row r's sum.
@@ -197,11 +199,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
 
   if (threadIdx.x == kProducerWarp * 32) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&sh->full[i], 1);
+      mbar_init(&sh->full[i], 2);
       mbar_init(&sh->empty[i], 8);
     }
-    for (int i = 0; i < kGeo; ++i) mbar_init(&sh->geo_full[i], 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->geo_full[i], 1);
       mbar_init(&sh->k_ready[i], 4);
       mbar_init(&sh->v_ready[i], 4);
       mbar_init(&sh->s_done[i], 1);
@@ -209,7 +211,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
       mbar_init(&sh->pv_done[i], 1);
     }
     mbar_init(&sh->q_ready, 8);
-    mbar_init(&sh->drain, 1);
+    mbar_init(&sh->drain[0], 1);
+    mbar_init(&sh->drain[1], 1);
     mbar_init(&sh->never, 1);
     sh->abort = 0;
     sh->q_top = 0u;
@@ -243,122 +246,104 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
     if constexpr (kTrade) regs_dec<kRegsRest>();
     if (warp == kProducerWarp) {
       // ------------------------------ records and geometry --------------------------------
+      // A lane holds one chunk of sixteen tiles; a tile's two lanes issue its copies, with no word between them.
       const uint64_t pol = l2_policy_evict_first();
-      int issued = 0;
-      bool reported = false;
-      int id = -1, slot = -1;             // of list entry 32 (j / 16) + lane
+      int issued = 0, st = 0, empty_phase = 1;
+      bool ok = false;
+      const uint8_t *from_k = nullptr, *from_v = nullptr;
       for (int j = 0; j < w.nt; ++j) {
-        if (j % 16 == 0) {
+        if (j % kBatch == 0) {
           const int e = (w.tb + j) * 2 + lane;
           const bool in = e < w.nres && e < (w.tb + w.nt) * 2;
-          id = in ? __ldg(p.res_ids + w.r0 + e) : -1;
-          slot = in ? __ldg(p.res_slots + w.r0 + e) : -1;
+          const int cid = in ? __ldg(p.res_ids + w.r0 + e) : -1;
+          const int slot = in ? __ldg(p.res_slots + w.r0 + e) : -1;
+          ok = cid >= 0 && cid < (1 << 25) && slot >= 0 && slot < p.num_slots;
+          if (in && !ok) atomicOr(p.err, kErrDeviceInput);
+          const size_t from = (static_cast<size_t>(ok ? slot : 0) * p.hkv + w.h) * C::kRecord;
+          from_k = p.k_pool + from;
+          from_v = p.v_pool + from;
+          // The geometry of the sixteen tiles (the consumers of the sixteen that held these entries have long passed
+          // them: at most kStages + 4 tiles lie between this warp and the softmax).
+          const bool plain = ok && cid * kChunk + kChunk - 1 <= w.L - w.nq;
+          const bool both = __shfl_xor_sync(0xffffffffu, plain ? 1 : 0, 1) != 0 && plain;
+          const int at = (j / kBatch & 1) * kBatch + lane / 2;
+          sh->base[at][lane & 1] = ok ? cid * kChunk : -1;
+          if ((lane & 1) == 0) sh->plain[at] = both ? 1 : 0;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->geo_full[j / kBatch & 1]);
         }
-        const int at = (j % 16) * 2;
-        int cid[2], sl[2];
-        bool ok[2];
-        int n = 0;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          cid[c] = __shfl_sync(0xffffffffu, id, at + c);
-          sl[c] = __shfl_sync(0xffffffffu, slot, at + c);
-          const bool present = (w.tb + j) * 2 + c < w.nres;
-          ok[c] = present && cid[c] >= 0 && cid[c] < (1 << 25) && sl[c] >= 0 && sl[c] < p.num_slots;
-          n += ok[c] ? 1 : 0;
-          if (present && !ok[c] && !reported) {
-            if (lane == 0) atomicOr(p.err, kErrDeviceInput);
-            reported = true;
+        if (j >= kStages && !__all_sync(0xffffffffu, mbar_wait_tested(&sh->empty[st], empty_phase, abort, p.err))) break;
+        if (lane / 2 == j % kBatch) {
+          mbar_arrive_expect_tx(&sh->full[st], ok ? 2 * C::kRecord : 0);
+          if (ok) {
+            uint8_t* to = sStage + st * C::kStageBytes + (lane & 1) * C::kRecord;
+            bulk_load(to, from_k, C::kRecord, &sh->full[st], pol);
+            bulk_load(to + 2 * C::kRecord, from_v, C::kRecord, &sh->full[st], pol);
           }
-        }
-        const int st = j % kStages;
-        if (j >= kStages &&
-            !__all_sync(0xffffffffu, mbar_wait_tested(&sh->empty[st], ((j / kStages) - 1) & 1, abort, p.err)))
-          break;
-        if (lane == 0) {
-          const int g = j % kGeo;
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            sh->base[g][c] = ok[c] ? cid[c] * kChunk : 0;
-            sh->valid[g][c] = ok[c] ? 1 : 0;
-          }
-          mbar_arrive(&sh->geo_full[g]);
-          mbar_arrive_expect_tx(&sh->full[st], n * 2 * C::kRecord);
         }
         __syncwarp();
-        // lanes 0, 1: K of the two chunks, 2, 3: V
-        const bool mine_ok = lane & 1 ? ok[1] : ok[0];
-        if (lane < 4 && mine_ok) {
-          const int mine = lane & 1 ? sl[1] : sl[0];
-          const size_t from = (static_cast<size_t>(mine) * p.hkv + w.h) * C::kRecord;
-          bulk_load(sStage + st * C::kStageBytes + lane * C::kRecord, (lane < 2 ? p.k_pool : p.v_pool) + from, C::kRecord,
-                    &sh->full[st], pol);
-        }
         issued = j + 1;
+        if (++st == kStages) st = 0, empty_phase ^= 1;
       }
       // Every copy lands before the CTA can exit.
       if (lane == 0)
         for (int j = max(0, issued - kStages); j < issued; ++j)
           mbar_drain(&sh->full[j % kStages], (j / kStages) & 1, p.err);
       __syncwarp();
-    } else if (warp == kMmaWarp) {
-      // ------------------------------ MMA issuer ------------------------------------------
-      // The whole warp runs the loop (see elect_one). Tensor memory is allocated whole: it starts at column 0.
+    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+      // ------------------------------ MMA issuers -----------------------------------------
+      // One warp for S, one for O: issuing a tile's eight MMAs of one kind with its waits takes 500 to 600 cycles, more
+      // than the tensor core does (N = 16: 160 and 320). The whole warp runs the loop (see elect_one). Tensor memory is
+      // allocated whole: it starts at column 0.
+      const bool is_o = warp != kMmaWarp;
       const int nt = uniform(w.nt), n = (uniform(w.rows) + 15) & ~15;
       if (nt > 0) {
         if (p.timeout_test_ns != 0) mbar_wait_limit(&sh->never, 0, p.timeout_test_ns, abort, p.err);
         bool ok = __all_sync(0xffffffffu, !*abort && mbar_wait(&sh->q_ready, 0, abort, p.err));
         tc_fence_after();
-        const uint32_t idesc_s = idesc_f16_f32(128, n, 0, 0);
-        const uint32_t idesc_o = idesc_f16_f32(128, n, 1, 1);
-        const uint64_t qdesc = sw128_desc(sbase + C::kQOffset, 16, 1024);
-        const uint64_t vdesc = sw128_desc(sbase + C::kVOffset, C::kBoxBytes, 1024);
-        const uint64_t pdesc = sw128_desc(sbase + C::kPOffset, C::kBoxBytes, 1024);
         auto wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, mbar_wait_tested(bar, parity, abort, p.err)); };
-        // S^T of tile j over its group's buffer: free once the group's P of tile j - 2 is written.
-        auto issue_s = [&](int j) {
-          tc_fence_after();
-          const int g = j & 1;
-          if (elect_one()) {
+        if (!is_o) {
+          const uint32_t idesc = idesc_f16_f32(128, n, 0, 0);
+          const uint64_t qdesc = sw128_desc(sbase + C::kQOffset, 16, 1024);
+          for (int j = 0; j < nt; ++j) {
+            // S^T of tile j over its group's buffer: free once the group's P of tile j - 2 is written.
+            const int g = j & 1, ph = (j >> 1) & 1;
+            if (j > 1) ok = ok && wait(&sh->p_ready[g], ph ^ 1);
+            ok = ok && wait(&sh->k_ready[g], ph);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < HD / 16; ++kk)
-              mma_ts(kColS + g * 96, kColK + g * 64 + kk * 8,
-                     qdesc + static_cast<uint64_t>(((kk >> 2) * C::kQBoxBytes + (kk & 3) * 32) >> 4), idesc_s, kk > 0 ? 1u : 0u);
-            mma_commit(&sh->s_done[g]);
+              for (int kk = 0; kk < HD / 16; ++kk)
+                mma_ts(kColS + g * 96, kColK + g * 64 + kk * 8,
+                       qdesc + static_cast<uint64_t>(((kk >> 2) * C::kQBoxBytes + (kk & 3) * 32) >> 4), idesc, kk > 0 ? 1u : 0u);
+              mma_commit(&sh->s_done[g]);
+            }
+            __syncwarp();
           }
-          __syncwarp();
-        };
-        for (int j = 0; ok && j < 2 && j < nt; ++j) {
-          ok = wait(&sh->k_ready[j], 0);
-          if (ok) issue_s(j);
-        }
-        for (int j = 0; ok && j < nt; ++j) {
-          const int g = j & 1, ph = (j >> 1) & 1;
-          ok = wait(&sh->p_ready[g], ph);
-          if (!ok) break;
-          bool next = j + 2 < nt;
-          if (next && __all_sync(0xffffffffu, mbar_test_wait(&sh->k_ready[g], ph ^ 1))) {
-            issue_s(j + 2);
-            next = false;
-          }
-          ok = wait(&sh->v_ready[g], ph);
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) {
+        } else {
+          const uint32_t idesc = idesc_f16_f32(128, n, 1, 1);
+          const uint64_t vdesc = sw128_desc(sbase + C::kVOffset, C::kBoxBytes, 1024);
+          const uint64_t pdesc = sw128_desc(sbase + C::kPOffset, C::kBoxBytes, 1024);
+          for (int j = 0; j < nt; ++j) {
+            const int g = j & 1, ph = (j >> 1) & 1;
+            ok = ok && wait(&sh->v_ready[g], ph) && wait(&sh->p_ready[g], ph);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk)
-              mma_ss(kColO + g * 96, vdesc + static_cast<uint64_t>((g * C::kVBytes + kk * 2048) >> 4),
-                     pdesc + static_cast<uint64_t>((g * C::kPBytes + kk * 2048) >> 4), idesc_o, (j > 1 || kk > 0) ? 1u : 0u);
-            mma_commit(&sh->pv_done[g]);
-          }
-          __syncwarp();
-          if (next) {
-            ok = wait(&sh->k_ready[g], ph ^ 1);
-            if (ok) issue_s(j + 2);
+              for (int kk = 0; kk < kKeys / 16; ++kk)
+                mma_ss(kColO + g * 96, vdesc + static_cast<uint64_t>((g * C::kVBytes + kk * 2048) >> 4),
+                       pdesc + static_cast<uint64_t>((g * C::kPBytes + kk * 2048) >> 4), idesc, (j > 1 || kk > 0) ? 1u : 0u);
+              mma_commit(&sh->pv_done[g]);
+            }
+            __syncwarp();
           }
         }
-        if (elect_one()) mma_commit(&sh->drain);
+        // Every MMA issued above completes before tensor memory is freed.
+        if (elect_one()) mma_commit(&sh->drain[is_o]);
         __syncwarp();
-        mbar_drain(&sh->drain, 0, p.err);
+        mbar_drain(&sh->drain[is_o], 0, p.err);
       }
       __syncwarp();
     }
@@ -380,12 +365,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
     for (int j = g; j < w.nt; j += 2) {
       const int u = j >> 1;
       bool ok = mbar_wait_tested(&sh->full[st], stage_phase, abort, p.err);
+      if (is_v && j % kBatch == g && ok) ok = mbar_wait_tested(&sh->geo_full[j / kBatch & 1], j / kBatch >> 1 & 1, abort, p.err);
       if (ok && u > 0) ok = mbar_wait_tested(done, (u - 1) & 1, abort, p.err);
       if (!__all_sync(0xffffffffu, ok)) break;
       const uint32_t at = st * C::kStageBytes;
       // Keys that no row attends may hold anything: P is 0 there, but 0 * NaN is NaN.
       bool keep = true;
-      if (is_v) keep = sh->valid[j % kGeo][c] && sh->base[j % kGeo][c] + tok < w.L;
+      if (is_v && !sh->plain[j % (2 * kBatch)]) {
+        const int base = sh->base[j % (2 * kBatch)][c];
+        keep = base >= 0 && base + tok < w.L;
+      }
       if (!is_v) tc_fence_after();
 #pragma unroll
       for (int y = 0; y < HD / 64; ++y) {                // 64 channels: two words of codes, four scales
@@ -491,16 +480,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
     bool dead = false;                                   // a wait of this warp gave up
     int u = 0;                                           // tiles of this group so far
     for (int j = grp; j < w.nt; j += 2, ++u) {
-      const int geo = j % kGeo;
-      if (!mbar_wait_tested(&sh->geo_full[geo], (j / kGeo) & 1, abort, p.err)) dead = true;
-      // Rows from n_min on attend this lane's key: row n is of block query (row0 + n) / G, at position p0 + that.
-      const int pos = sh->base[geo][key / kChunk] + key % kChunk;
+      if (j % kBatch == grp && !mbar_wait_tested(&sh->geo_full[j / kBatch & 1], j / kBatch >> 1 & 1, abort, p.err)) dead = true;
+      const int geo = j % (2 * kBatch);
+      const bool whole = sh->plain[geo] != 0;
       int n_min = 0;
-      if (!sh->valid[geo][key / kChunk] || pos >= w.L)
-        n_min = NT;
-      else if (pos > p0)
-        n_min = min(static_cast<long long>(NT), max(0ll, static_cast<long long>(pos - p0) * p.group - w.row0));
-      const bool whole = __all_sync(0xffffffffu, n_min == 0);
+      if (!whole) {
+        // Rows from n_min on attend this lane's key: row n is of block query (row0 + n) / G, at position p0 + that.
+        const int base = sh->base[geo][key / kChunk], pos = base + key % kChunk;
+        if (base < 0 || pos >= w.L)
+          n_min = NT;
+        else if (pos > p0)
+          n_min = min(static_cast<long long>(NT), max(0ll, static_cast<long long>(pos - p0) * p.group - w.row0));
+      }
       if (u > 0 && !mbar_wait_tested(&sh->pv_done[grp], (u - 1) & 1, abort, p.err)) dead = true;   // P is free, O complete
       if (!mbar_wait_tested(&sh->s_done[grp], u & 1, abort, p.err)) dead = true;
       dead = __any_sync(0xffffffffu, dead);

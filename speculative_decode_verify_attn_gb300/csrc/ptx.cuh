@@ -337,7 +337,7 @@ __device__ __forceinline__ void tmem_ld_async(uint32_t taddr, uint32_t (&r)[16])
 }
 template <int N>
 __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[N]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;");
 #pragma unroll
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));   // (no use of a register moves before the wait)
 }
