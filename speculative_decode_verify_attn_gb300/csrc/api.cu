@@ -1198,8 +1198,9 @@ vfy_status vfy_attend_full_packed(vfy_ctx* ctx, const uint16_t* q, const int32_t
   p.head_dim = c.head_dim;
   p.max_q = c.max_queries_per_seq;
   p.row_tiles = ctx->row_tiles;
-  // Row tiles of equal size (in whole groups of eight rows).
   const int block_rows = c.max_queries_per_seq * p.group;
+  const bool few = block_rows <= vfy::kPackedFewRows;
+  // Row tiles of equal size (in whole groups of eight rows).
   p.n_tiles = ceil_div(block_rows, vfy::packed_tile_rows());
   p.tile_rows = (ceil_div(block_rows, p.n_tiles) + 7) & ~7;
   p.n_tiles = ceil_div(block_rows, p.tile_rows);
@@ -1207,8 +1208,14 @@ vfy_status vfy_attend_full_packed(vfy_ctx* ctx, const uint16_t* q, const int32_t
   int splits = ctx->full_splits;
   if (splits == 0) {
     const long long items = static_cast<long long>(p.hkv) * num_seqs * p.n_tiles;
-    const int tiles = ceil_div(max_resident_per_seq, 2);
-    splits = clampi(num_seqs > 1 ? ceil_div(4 * ctx->num_sms, items) : static_cast<int>(ctx->num_sms / items), 1, tiles > 0 ? tiles : 1);
+    if (few) {
+      // one CTA an SM (for a batch twice as many, which even out), each with a chunk for every warp
+      splits = static_cast<int>(ctx->num_sms * (num_seqs > 1 ? 2 : 1) / items);
+      splits = clampi(splits, 1, std::max(1, ceil_div(max_resident_per_seq, 16)));
+    } else {
+      const int tiles = ceil_div(max_resident_per_seq, 2);
+      splits = clampi(num_seqs > 1 ? ceil_div(4 * ctx->num_sms, items) : static_cast<int>(ctx->num_sms / items), 1, tiles > 0 ? tiles : 1);
+    }
   }
   p.num_splits = clampi(splits, 1, c.max_splits);
   p.token_cap = num_seqs * c.max_queries_per_seq;
@@ -1219,8 +1226,11 @@ vfy_status vfy_attend_full_packed(vfy_ctx* ctx, const uint16_t* q, const int32_t
   p.timeout_test_ns = ctx->timeout_test_ns;
   p.stable_metadata = ctx->stable_metadata;
   p.err = ctx->err;
-  VFY_CUDA(vfy::launch_attend_packed(p, num_seqs, s));
+  p.out = out;
+  p.lse = lse;
+  VFY_CUDA(few ? vfy::launch_attend_packed_few(p, num_seqs, s) : vfy::launch_attend_packed(p, num_seqs, s));
   ++ctx->launches;
+  if (few && p.num_splits == 1) return VFY_OK;
   vfy::CombineParams cp;
   cp.cu_q = cu_q;
   cp.seq_len = seq_len;

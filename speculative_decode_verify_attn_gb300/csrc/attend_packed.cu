@@ -1,5 +1,5 @@
 // Attention of a block over a pool of 4-bit chunks, on the tensor cores with the operands exchanged: a tile's 128 keys are
-// the M = 128 side of both products and the block's rows (queries x q-heads of one KV head, at most 80) the N side,
+// the M = 128 side of both products and the block's rows (queries x q-heads of one KV head, at most 72) the N side,
 //     S^T [128 keys][rows] = K Q^T,    O^T [d][rows] += V^T P^T,
 // so that the work follows the rows a block has: one token of G = 4 is N = 16, a block of 17 is N = 80. With the rows as M (as
 // in the bf16 layers) a 4-bit tile would be bound by the 128 rows' tensor time.
@@ -10,13 +10,14 @@
 // reference moves, and what fp16 drops (below 2^-25) is 2^-32 of the largest weight.
 //
 // One CTA per (split, KV head, sequence and row tile), a contiguous run of tiles of two chunks. Roles:
-//   warps 0-3, 4-7   softmax of even / odd tiles: a lane is a key, its 32-bit columns are the rows. Two groups with a
-//                    reference, row sums and O of their own, merged at the end; a group has two tiles' time for one.
-//   warps 8-11, 12-15   K of even / odd tiles: a lane reads its key's codes and scales, writes fp16 into tensor memory
-//                    (the A operand of S)
-//   warps 16-19, 20-23  V of even / odd tiles: fp16 into shared memory, channels contiguous (the A operand of O^T, M-major)
-//   warp 24          bulk copies of the records (contiguous: no tensor map), and the tiles' geometry
-//   warp 25, 26      the MMA issuers of S and of O (25 also holds tensor memory)
+//   softmax          a lane is a key, its 32-bit columns are the rows. Each warpgroup has up to 24 (8) of the rows, with their
+//                    reference, sums and columns of O: the groups meet only in the MMAs. While a tile's weights are
+//                    worked out, the next tile's scores are on their way and the vote whether one of them passes the limit.
+//   K, V             two warpgroups each, which take tiles in turn: a lane reads its key's codes and scales, writes fp16
+//                    into tensor memory (K, the A operand of S) or shared memory (V, channels contiguous: the A operand
+//                    of O^T, M-major)
+//   one warp         bulk copies of the records (contiguous: no tensor map), and the tiles' geometry
+//   two warps        the MMA issuers of S and of O
 #include <cuda_bf16.h>
 
 #include "packed.cuh"
@@ -26,61 +27,72 @@
 namespace vfy {
 namespace {
 
-constexpr int kGroups = 7;                // warpgroups: softmax 0 and 1, K twice, V twice, the rest
-constexpr int kThreads = kGroups * 128;
-constexpr int kRegsLaunch = 72, kRegsSoftmax = 152, kRegsUnpack = 40, kRegsRest = 40;
-static_assert(2 * kRegsSoftmax + 4 * kRegsUnpack + kRegsRest <= kGroups * kRegsLaunch, "registers the CTA was launched with");
-constexpr int kKWarp = 8, kVWarp = 16, kProducerWarp = 24, kMmaWarp = 25;
 constexpr int kKeys = 2 * kChunk;         // keys of a tile
-constexpr int kFewN = 16, kMaxN = 80;     // rows of a tile (two kernels): the softmax threads hold a partial sum of each
+constexpr int kFewN = 16, kMaxN = 72;     // rows of a tile (two kernels)
 constexpr int kBatch = 16;                // tiles whose chunks a warp's lanes hold; their geometry lies in two such batches
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColK = 0;             // two K tiles of up to 64 columns (two fp16 channels each)
-constexpr uint32_t kColS = 128;           // S^T of the two groups, 96 columns apart
-constexpr uint32_t kColO = 320;           // O^T of the two groups
 constexpr float kTop = 7.f;               // a row's maximum when its reference is set (log2)
 constexpr float kLimit = 15.f;            // the reference moves when a weight would pass 2^15
-constexpr float kClamp = 24.f;            // weights past the limit are held at 2^24 until they are worked out again
 constexpr float kNone = 1e30f;            // minus the reference of a row that has none: every score passes the limit
 
 template <int HD, int NT>
 struct Cfg {
-  static constexpr int kStages = NT > kFewN ? 4 : 6;
+  static constexpr bool kFew = NT <= kFewN;
+  static constexpr int kSoftmax = kFew ? 2 : 3;                  // warpgroups of softmax
+  static constexpr int kRowsT = NT / kSoftmax;                   // rows of a softmax thread
+  static constexpr int kUnpack = 2;                              // warpgroups of K, and of V
+  static constexpr int kGroups = kSoftmax + 2 * kUnpack + 1;
+  static constexpr int kThreads = kGroups * 128;
+  static constexpr int kKWarp = 4 * kSoftmax, kVWarp = kKWarp + 4 * kUnpack;
+  static constexpr int kProducerWarp = kVWarp + 4 * kUnpack, kMmaWarp = kProducerWarp + 1;
+  // Registers: with 72 rows the softmax groups take up what the others give up.
+  static constexpr bool kTrade = !kFew;
+  static constexpr int kRegsLaunch = 64, kRegsSoftmax = 104, kRegsUnpack = 40, kRegsRest = 40;
+  static_assert(!kTrade || kSoftmax * kRegsSoftmax + 2 * kUnpack * kRegsUnpack + kRegsRest <= kGroups * kRegsLaunch,
+                "registers the CTA was launched with");
+  static constexpr int kN = (NT + 15) / 16 * 16;                 // N of the MMAs: multiples of 16
+  static constexpr int kStages = 4;
+  static constexpr int kKBufs = kFew ? 4 : 2, kSBufs = kFew ? 4 : 3;   // in tensor memory
+  static constexpr int kVBufs = kFew ? 3 : 2;
+  // columns: K tiles of up to 64 (two fp16 channels each), S^T, O^T
+  static constexpr uint32_t kColS = kKBufs * 64, kColO = kColS + kSBufs * kN;
+  static_assert(kColO + kN <= kTmemCols && kStages % kUnpack == 0, "tensor memory, stages");
   static constexpr int kRecord = kPackedBytes<HD>;
   static constexpr int kStageBytes = 4 * kRecord;                // K and V of two chunks
   static constexpr int kBoxBytes = kKeys * 128;                  // 64 columns of 128 keys
   static constexpr int kVBytes = 2 * kBoxBytes;                  // M = 128: d = 64 leaves the second box zero
-  static constexpr int kPBytes = (NT + 63) / 64 * kBoxBytes;
-  static constexpr int kQBoxBytes = NT * 128;
+  static constexpr int kPBytes = (kN + 63) / 64 * kBoxBytes;
+  static constexpr int kQBoxBytes = kN * 128;
   static constexpr int kQBytes = (HD / 64) * kQBoxBytes;
   static constexpr int kVOffset = 0;
-  static constexpr int kPOffset = 2 * kVBytes;
+  static constexpr int kPOffset = kVBufs * kVBytes;
   static constexpr int kQOffset = kPOffset + 2 * kPBytes;
   static constexpr int kStageOffset = kQOffset + kQBytes;
   static constexpr int kBarOffset = kStageOffset + kStages * kStageBytes;
-  static constexpr int kBarBytes = 5120;
+  static constexpr int kBarBytes = 6144;
   static constexpr int kSmemBytes = kBarOffset + kBarBytes + 1024;
   static_assert(kRecord % 16 == 0 && kStageBytes % 128 == 0, "bulk copies");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
 struct Shared {
-  uint64_t full[6], empty[6];
+  uint64_t full[4], empty[4];
   uint64_t geo_full[2];
-  uint64_t k_ready[2], v_ready[2];
-  uint64_t s_done[2];                     // S of a tile: its S^T is there, its K is free
-  uint64_t p_ready[2];                    // a tile's P is written, its S^T read
-  uint64_t pv_done[2];                    // O^T holds the tile, its P and V are free
+  uint64_t k_ready[4], k_free[4];
+  uint64_t s_done[4], s_free[4];          // S^T written; read
+  uint64_t v_ready[3], v_free[3];
+  uint64_t p_ready[2], pv_done[2];        // P written; O^T holds the tile, its P is free
+  uint64_t vote[3], meet[3];              // [softmax group]: of one tile; where a reference moves
   uint64_t q_ready, drain[2], never;
   uint32_t tmem_base;
   int abort;
   unsigned q_top;                         // largest |q| of the tile, as bf16 bits
+  int moves[3][2];                        // [softmax group][tile parity]: a weight would pass the limit
   int base[2 * kBatch][2];                // position of a chunk's first token, -1: no chunk
   int plain[2 * kBatch];                  // every row attends every key of the tile
-  alignas(16) float neg_ref[2][kMaxN];    // [group] minus the rows' reference, log2 units
-  alignas(16) float old_ref[2][kMaxN];    // minus the reference before it moved
-  alignas(16) float alpha[2][kMaxN];
-  alignas(16) float part[2][4][kMaxN];    // [group][warp]: maxima, at the end sums
+  alignas(16) float neg_ref[kMaxN];       // minus the rows' reference, log2 units
+  alignas(16) float alpha[kMaxN];
+  alignas(16) float part[4][kMaxN];       // [lane quarter]: maxima, at the end sums
 };
 static_assert(sizeof(Shared) <= Cfg<128, kMaxN>::kBarBytes, "barrier block");
 
@@ -116,30 +128,6 @@ __device__ __forceinline__ Work make_work(const PackedAttnParams& p) {
   w.tb = static_cast<int>(static_cast<unsigned>(w.s) * tiles / ns);
   w.nt = static_cast<int>(static_cast<unsigned>(w.s + 1) * tiles / ns) - w.tb;
   return w;
-}
-
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-// Eight codes (a 32-bit word) times a scale (in both halves): eight fp16 values, two a register.
-__device__ __forceinline__ void unpack_word(uint32_t codes, uint32_t scale2, uint32_t* out) {
-  uint32_t a, b, c, d;
-  asm("{\n\t.reg .b8 x0, x1, x2, x3;\n\tmov.b32 {x0, x1, x2, x3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, x0;\n\tcvt.rn.f16x2.e2m1x2 %1, x1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, x2;\n\tcvt.rn.f16x2.e2m1x2 %3, x3;\n\t}"
-      : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
-      : "r"(codes));
-  out[0] = mul_f16x2(a, scale2);
-  out[1] = mul_f16x2(b, scale2);
-  out[2] = mul_f16x2(c, scale2);
-  out[3] = mul_f16x2(d, scale2);
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 
 __device__ __forceinline__ float2 pair(const uint32_t* r, int i) {
@@ -183,10 +171,10 @@ __device__ __forceinline__ float sum_rows8(const float2* l2, int lane) {
 }
 
 template <int HD, int NT>
-__global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const PackedAttnParams p) {
+__global__ void __launch_bounds__(Cfg<HD, NT>::kThreads, 1) attend_packed_kernel(const PackedAttnParams p) {
   using C = Cfg<HD, NT>;
-  constexpr int kStages = C::kStages;
-  constexpr bool kTrade = NT > kFewN;     // the softmax groups take up registers that the others give up
+  constexpr int kStages = C::kStages, kThreads = C::kThreads;
+  constexpr int kKWarp = C::kKWarp, kVWarp = C::kVWarp, kProducerWarp = C::kProducerWarp, kMmaWarp = C::kMmaWarp;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (sbase - smem_u32(smem_raw));
@@ -202,15 +190,29 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
       mbar_init(&sh->full[i], 2);
       mbar_init(&sh->empty[i], 8);
     }
+    for (int i = 0; i < C::kKBufs; ++i) {
+      mbar_init(&sh->k_ready[i], 4);
+      mbar_init(&sh->k_free[i], 1);
+    }
+    for (int i = 0; i < C::kSBufs; ++i) {
+      mbar_init(&sh->s_done[i], 1);
+      mbar_init(&sh->s_free[i], 4 * C::kSoftmax);
+    }
+    for (int i = 0; i < C::kVBufs; ++i) {
+      mbar_init(&sh->v_ready[i], 4);
+      mbar_init(&sh->v_free[i], 1);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh->geo_full[i], 1);
-      mbar_init(&sh->k_ready[i], 4);
-      mbar_init(&sh->v_ready[i], 4);
-      mbar_init(&sh->s_done[i], 1);
-      mbar_init(&sh->p_ready[i], 4);
+      mbar_init(&sh->p_ready[i], 4 * C::kSoftmax);
       mbar_init(&sh->pv_done[i], 1);
     }
-    mbar_init(&sh->q_ready, 8);
+    for (int i = 0; i < C::kSoftmax; ++i) {
+      mbar_init(&sh->vote[i], 4);
+      mbar_init(&sh->meet[i], 4);
+      sh->moves[i][0] = sh->moves[i][1] = 0;
+    }
+    mbar_init(&sh->q_ready, 4 * C::kSoftmax);
     mbar_init(&sh->drain[0], 1);
     mbar_init(&sh->drain[1], 1);
     mbar_init(&sh->never, 1);
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
   }
   if (HD == 64) {
     // M = 128 with 64 channels: the second box of V stays zero
-    for (int x = threadIdx.x; x < 2 * C::kBoxBytes / 16; x += kThreads) {
+    for (int x = threadIdx.x; x < C::kVBufs * C::kBoxBytes / 16; x += kThreads) {
       const int buf = x / (C::kBoxBytes / 16), at = x % (C::kBoxBytes / 16);
       *reinterpret_cast<uint4*>(sV + buf * C::kVBytes + C::kBoxBytes + at * 16) = make_uint4(0u, 0u, 0u, 0u);
     }
@@ -243,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
   if (w.bad && threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(p.err, kErrDeviceInput);
 
   if (warp >= kProducerWarp) {
-    if constexpr (kTrade) regs_dec<kRegsRest>();
+    if constexpr (C::kTrade) regs_dec<C::kRegsRest>();
     if (warp == kProducerWarp) {
       // ------------------------------ records and geometry --------------------------------
       // A lane holds one chunk of sixteen tiles; a tile's two lanes issue its copies, with no word between them.
@@ -305,39 +307,43 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
         if (!is_o) {
           const uint32_t idesc = idesc_f16_f32(128, n, 0, 0);
           const uint64_t qdesc = sw128_desc(sbase + C::kQOffset, 16, 1024);
+          int sb = 0, s_phase = 1;                       // S buffer; the parity of its earlier use
           for (int j = 0; j < nt; ++j) {
-            // S^T of tile j over its group's buffer: free once the group's P of tile j - 2 is written.
-            const int g = j & 1, ph = (j >> 1) & 1;
-            if (j > 1) ok = ok && wait(&sh->p_ready[g], ph ^ 1);
-            ok = ok && wait(&sh->k_ready[g], ph);
+            const int kb = j % C::kKBufs;
+            ok = wait(&sh->k_ready[kb], j / C::kKBufs & 1) && (j < C::kSBufs || wait(&sh->s_free[sb], s_phase));
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < HD / 16; ++kk)
-                mma_ts(kColS + g * 96, kColK + g * 64 + kk * 8,
+                mma_ts(C::kColS + sb * C::kN, kb * 64 + kk * 8,
                        qdesc + static_cast<uint64_t>(((kk >> 2) * C::kQBoxBytes + (kk & 3) * 32) >> 4), idesc, kk > 0 ? 1u : 0u);
-              mma_commit(&sh->s_done[g]);
+              mma_commit(&sh->s_done[sb]);
+              mma_commit(&sh->k_free[kb]);
             }
             __syncwarp();
+            if (++sb == C::kSBufs) sb = 0, s_phase ^= 1;
           }
         } else {
           const uint32_t idesc = idesc_f16_f32(128, n, 1, 1);
           const uint64_t vdesc = sw128_desc(sbase + C::kVOffset, C::kBoxBytes, 1024);
           const uint64_t pdesc = sw128_desc(sbase + C::kPOffset, C::kBoxBytes, 1024);
+          int vb = 0, v_phase = 0;
           for (int j = 0; j < nt; ++j) {
             const int g = j & 1, ph = (j >> 1) & 1;
-            ok = ok && wait(&sh->v_ready[g], ph) && wait(&sh->p_ready[g], ph);
+            ok = wait(&sh->v_ready[vb], v_phase) && wait(&sh->p_ready[g], ph);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < kKeys / 16; ++kk)
-                mma_ss(kColO + g * 96, vdesc + static_cast<uint64_t>((g * C::kVBytes + kk * 2048) >> 4),
-                       pdesc + static_cast<uint64_t>((g * C::kPBytes + kk * 2048) >> 4), idesc, (j > 1 || kk > 0) ? 1u : 0u);
+                mma_ss(C::kColO, vdesc + static_cast<uint64_t>((vb * C::kVBytes + kk * 2048) >> 4),
+                       pdesc + static_cast<uint64_t>((g * C::kPBytes + kk * 2048) >> 4), idesc, (j > 0 || kk > 0) ? 1u : 0u);
               mma_commit(&sh->pv_done[g]);
+              mma_commit(&sh->v_free[vb]);
             }
             __syncwarp();
+            if (++vb == C::kVBufs) vb = 0, v_phase ^= 1;
           }
         }
         // Every MMA issued above completes before tensor memory is freed.
@@ -349,25 +355,27 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
     }
   } else if (warp >= kKWarp) {
     // ------------------------------ K and V to fp16 -----------------------------------------
-    if constexpr (kTrade) regs_dec<kRegsUnpack>();
+    if constexpr (C::kTrade) regs_dec<C::kRegsUnpack>();
     const bool is_v = warp >= kVWarp;
-    const int g = (warp >> 2) & 1;                       // even or odd tiles; their buffer
+    const int wg = (warp >> 2) - (is_v ? kVWarp : kKWarp) / 4;   // takes tiles wg, wg + kUnpack, ...
     const int key = (warp & 3) * 32 + lane;              // of the tile; a TMEM lane
     const int c = key / kChunk, tok = key % kChunk;
-    uint64_t* done = is_v ? &sh->pv_done[g] : &sh->s_done[g];
-    uint64_t* ready = is_v ? &sh->v_ready[g] : &sh->k_ready[g];
+    const int bufs = is_v ? C::kVBufs : C::kKBufs;
+    uint64_t* free_bar = is_v ? sh->v_free : sh->k_free;
+    uint64_t* ready_bar = is_v ? sh->v_ready : sh->k_ready;
     const uint32_t rec = sbase + C::kStageOffset + ((is_v ? 2 : 0) + c) * C::kRecord;
     const uint32_t scales_at = rec + kChunk * (HD / 2) + tok * (HD / 16);
     const uint32_t codes_at = rec + tok * 16;
-    const uint32_t kto = (static_cast<uint32_t>((warp & 3) * 32) << 16) + kColK + g * 64;
-    const uint32_t vto = sbase + C::kVOffset + g * C::kVBytes + key * 128;
-    int st = g % kStages, stage_phase = 0;               // (kStages is even)
-    for (int j = g; j < w.nt; j += 2) {
-      const int u = j >> 1;
+    int st = wg, stage_phase = 0;
+    int buf = wg, free_phase = 1;                        // of this WG's next tile; its buffer's earlier use
+    for (int j = wg; j < w.nt; j += C::kUnpack) {
       bool ok = mbar_wait_tested(&sh->full[st], stage_phase, abort, p.err);
-      if (is_v && j % kBatch == g && ok) ok = mbar_wait_tested(&sh->geo_full[j / kBatch & 1], j / kBatch >> 1 & 1, abort, p.err);
-      if (ok && u > 0) ok = mbar_wait_tested(done, (u - 1) & 1, abort, p.err);
+      if (is_v && j % kBatch < C::kUnpack && ok)
+        ok = mbar_wait_tested(&sh->geo_full[j / kBatch & 1], j / kBatch >> 1 & 1, abort, p.err);
+      if (ok && j >= bufs) ok = mbar_wait_tested(&free_bar[buf], free_phase, abort, p.err);
       if (!__all_sync(0xffffffffu, ok)) break;
+      const uint32_t kto = (static_cast<uint32_t>((warp & 3) * 32) << 16) + buf * 64;
+      const uint32_t vto = sbase + C::kVOffset + buf * C::kVBytes + key * 128;
       const uint32_t at = st * C::kStageBytes;
       // Keys that no row attends may hold anything: P is 0 there, but 0 * NaN is NaN.
       bool keep = true;
@@ -410,26 +418,32 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&sh->empty[st]);
-        mbar_arrive(ready);
+        mbar_arrive(&ready_bar[buf]);
       }
-      st += 2;
-      if (st >= kStages) st -= kStages, stage_phase ^= 1;
+      st += C::kUnpack;
+      if (st >= C::kStages) st -= C::kStages, stage_phase ^= 1;
+      buf += C::kUnpack;
+      if (buf >= bufs) buf -= bufs, free_phase ^= 1;
     }
   } else {
     // ------------------------------ softmax ---------------------------------------------------
-    if constexpr (kTrade) regs_inc<kRegsSoftmax>();
-    const int grp = warp >> 2, wq = warp & 3, tg = threadIdx.x & 127;
+    if constexpr (C::kTrade) regs_inc<C::kRegsSoftmax>();
+    constexpr int kAll = 128 * C::kSoftmax;
+    const int grp = warp >> 2, wq = warp & 3;
+    const int rows_each = ((w.rows + C::kSoftmax - 1) / C::kSoftmax + 7) & ~7;
+    const int row_first = grp * rows_each;
+    const int my_rows = max(0, min(rows_each, w.rows - row_first));
+    const int tg = threadIdx.x & 127;                    // thread of the group; its key of a tile
     const int key = tg;
-    const int bar = 2 + grp;                             // named barrier of the group; 1: both groups
     // Q: words of 8 channels, all of a thread's in registers while the tile's largest value is found
-    constexpr int kWords = (NT * HD / 8 + 255) / 256;
+    constexpr int kWords = (C::kN * HD / 8 + kAll - 1) / kAll;
     float q_scale;                                       // of a score: softmax scale, g of K, the queries' power of two
     {
       uint4 qv[kWords];
       unsigned top = 0u;
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
-        const int x = threadIdx.x + i * 256;
+        const int x = threadIdx.x + i * kAll;
         const int r = x / (HD / 8), cw = x % (HD / 8);
         qv[i] = make_uint4(0u, 0u, 0u, 0u);
         if (r < w.rows) {
@@ -444,20 +458,20 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
       }
       top = __reduce_max_sync(0xffffffffu, top);
       if (lane == 0) atomicMax(&sh->q_top, top);
-      named_sync(1, 256);
+      named_sync(1, kAll);
       const int qe = max(static_cast<int>(sh->q_top >> 7) - 127 - 14, -100);
       const float down = __int_as_float((127 - qe) << 23);
       q_scale = p.scale_log2 * __int_as_float((127 + qe) << 23);
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
-        const int x = threadIdx.x + i * 256;
+        const int x = threadIdx.x + i * kAll;
         const int r = x / (HD / 8), cw = x % (HD / 8);
         const uint32_t ws[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
         uint32_t o[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           o[e] = pack_f16(__uint_as_float(ws[e] << 16) * down, __uint_as_float(ws[e] & 0xffff0000u) * down);
-        if (r < NT)
+        if (r < C::kN)
           *reinterpret_cast<uint4*>(sQ + (cw >> 3) * C::kQBoxBytes + r * 128 + (((cw & 7) ^ (r & 7)) << 4)) =
               make_uint4(o[0], o[1], o[2], o[3]);
       }
@@ -466,192 +480,221 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
       if (lane == 0) mbar_arrive(&sh->q_ready);
     }
     // (rows past the block, Q = 0, keep weight 1: never read)
-    if (tg < NT) sh->neg_ref[grp][tg] = tg < w.rows ? kNone : 0.f;
-    named_sync(bar, 128);
+    if (static_cast<int>(threadIdx.x) < NT) sh->neg_ref[threadIdx.x] = static_cast<int>(threadIdx.x) < w.rows ? kNone : 0.f;
+    named_sync(1, kAll);
 
     const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
-    const uint32_t s_at = lane_base + kColS + grp * 96, o_at = lane_base + kColO + grp * 96;
-    const uint32_t prow = sbase + C::kPOffset + grp * C::kPBytes + key * 128;
+    const uint32_t o_at = lane_base + C::kColO + row_first;
+    const uint32_t prow = sbase + C::kPOffset + key * 128;
     const int p0 = w.L - w.nq;
     const float2 sc2 = make_float2(q_scale, q_scale);
-    float2 l[NT / 2];
+    float2 l[C::kRowsT / 2];
 #pragma unroll
-    for (int r = 0; r < NT / 2; ++r) l[r] = make_float2(0.f, 0.f);
-    bool dead = false;                                   // a wait of this warp gave up
-    int u = 0;                                           // tiles of this group so far
-    for (int j = grp; j < w.nt; j += 2, ++u) {
-      if (j % kBatch == grp && !mbar_wait_tested(&sh->geo_full[j / kBatch & 1], j / kBatch >> 1 & 1, abort, p.err)) dead = true;
+    for (int r = 0; r < C::kRowsT / 2; ++r) l[r] = make_float2(0.f, 0.f);
+    auto wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, mbar_wait_tested(bar, parity, abort, p.err)); };
+    int met = 0;                                         // the group's meetings so far
+    auto meet = [&]() {                                  // all warps of the group, what they wrote to shared memory seen
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->meet[grp]);
+      return wait(&sh->meet[grp], met++ & 1);
+    };
+    // Rows from n_min on attend this lane's key of tile j: row n is of block query (row0 + n) / G, at position p0 + that.
+    auto first_row = [&](int j) -> int {
       const int geo = j % (2 * kBatch);
-      const bool whole = sh->plain[geo] != 0;
-      int n_min = 0;
-      if (!whole) {
-        // Rows from n_min on attend this lane's key: row n is of block query (row0 + n) / G, at position p0 + that.
-        const int base = sh->base[geo][key / kChunk], pos = base + key % kChunk;
-        if (base < 0 || pos >= w.L)
-          n_min = NT;
-        else if (pos > p0)
-          n_min = min(static_cast<long long>(NT), max(0ll, static_cast<long long>(pos - p0) * p.group - w.row0));
-      }
-      if (u > 0 && !mbar_wait_tested(&sh->pv_done[grp], (u - 1) & 1, abort, p.err)) dead = true;   // P is free, O complete
-      if (!mbar_wait_tested(&sh->s_done[grp], u & 1, abort, p.err)) dead = true;
-      dead = __any_sync(0xffffffffu, dead);
+      if (sh->plain[geo]) return 0;
+      const int base = sh->base[geo][key / kChunk], pos = base + key % kChunk;
+      if (base < 0 || pos >= w.L) return NT;
+      return pos > p0 ? min(static_cast<long long>(NT), max(0ll, static_cast<long long>(pos - p0) * p.group - w.row0)) : 0;
+    };
+    auto s_address = [&](int buf) { return lane_base + C::kColS + buf * C::kN + row_first; };
+    auto load_scores = [&](uint32_t(&x)[C::kRowsT], int buf) {
       tc_fence_after();
-      // Weights P = 2^(s scale - ref), their sums, and the largest exponent: sixteen rows at a time, the next sixteen's
-      // scores on their way. `undo` takes the weights against the old references off the sums first.
-      auto weigh = [&](bool undo) -> float {
-        float top[2] = {-INFINITY, -INFINITY};
-        uint32_t buf[2][16];
-        tmem_ld_async(s_at, buf[0]);
 #pragma unroll
-        for (int cb = 0; cb < NT / 16; ++cb) {
-          if (cb * 16 < w.rows) {
-            uint32_t(&s)[16] = buf[cb & 1];
-            tmem_wait_ld(s);
-            if (cb + 1 < NT / 16 && (cb + 1) * 16 < w.rows) tmem_ld_async(s_at + (cb + 1) * 16, buf[(cb + 1) & 1]);
-            if (!whole) {                                // 2^-inf = 0
+      for (int r = 0; r < C::kRowsT; r += 8) tmem_ld8_async(s_address(buf) + r, *reinterpret_cast<uint32_t(*)[8]>(x + r));
+    };
+    // Scores to exponents s scale - ref, masked keys to -inf; the largest.
+    auto exponents = [&](uint32_t(&x)[C::kRowsT], int n_min) -> float {
+      tmem_wait_ld(x);
+      if (!__all_sync(0xffffffffu, n_min == 0)) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e) s[e] = cb * 16 + e >= n_min ? s[e] : 0xff800000u;
-            }
-            if (undo) {
-              const float2* old = reinterpret_cast<const float2*>(&sh->old_ref[grp][cb * 16]);
-              const float2* al = reinterpret_cast<const float2*>(&sh->alpha[grp][cb * 16]);
+        for (int r = 0; r < C::kRowsT; ++r) x[r] = row_first + r >= n_min ? x[r] : 0xff800000u;
+      }
+      float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float2 x = fma_f32x2(pair(s, 2 * e), sc2, old[e]);
-                float2& sum = l[cb * 8 + e];
-                sum.x = (sum.x - ex2_approx(fminf(x.x, kClamp))) * al[e].x;
-                sum.y = (sum.y - ex2_approx(fminf(x.y, kClamp))) * al[e].y;
-              }
-            }
-            const float4* nr = reinterpret_cast<const float4*>(&sh->neg_ref[grp][cb * 16]);
-            uint32_t pk[8];
+      for (int r = 0; r < C::kRowsT; r += 8) {
+        if (r < my_rows) {
+          const float4* nr = reinterpret_cast<const float4*>(&sh->neg_ref[row_first + r]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float4 f = nr[e];
-              float2 a = fma_f32x2(pair(s, 4 * e), sc2, make_float2(f.x, f.y));
-              float2 b = fma_f32x2(pair(s, 4 * e + 2), sc2, make_float2(f.z, f.w));
-              top[0] = fmaxf(fmaxf(top[0], a.x), a.y);
-              top[1] = fmaxf(fmaxf(top[1], b.x), b.y);
-              a.x = ex2_approx(fminf(a.x, kClamp));
-              a.y = ex2_approx(fminf(a.y, kClamp));
-              b.x = ex2_approx(fminf(b.x, kClamp));
-              b.y = ex2_approx(fminf(b.y, kClamp));
-              l[cb * 8 + 2 * e] = add_f32x2(l[cb * 8 + 2 * e], a);
-              l[cb * 8 + 2 * e + 1] = add_f32x2(l[cb * 8 + 2 * e + 1], b);
-              pk[2 * e] = pack_f16(a.x, a.y);
-              pk[2 * e + 1] = pack_f16(b.x, b.y);
-            }
-            const uint32_t box = prow + (cb >> 2) * C::kBoxBytes;
-            const int word = (cb & 3) * 2;               // 16-byte word of the key's rows: 8 words a box
-            sts_u4(box + ((word ^ (key & 7)) << 4), make_uint4(pk[0], pk[1], pk[2], pk[3]));
-            sts_u4(box + (((word + 1) ^ (key & 7)) << 4), make_uint4(pk[4], pk[5], pk[6], pk[7]));
+          for (int e = 0; e < 2; ++e) {
+            const float4 f = nr[e];
+            const float2 a = fma_f32x2(pair(x, r + 4 * e), sc2, make_float2(f.x, f.y));
+            const float2 b = fma_f32x2(pair(x, r + 4 * e + 2), sc2, make_float2(f.z, f.w));
+            top[0] = fmaxf(fmaxf(top[0], a.x), a.y);
+            top[1] = fmaxf(fmaxf(top[1], b.x), b.y);
+            x[r + 4 * e] = __float_as_uint(a.x);
+            x[r + 4 * e + 1] = __float_as_uint(a.y);
+            x[r + 4 * e + 2] = __float_as_uint(b.x);
+            x[r + 4 * e + 3] = __float_as_uint(b.y);
           }
         }
-        return fmaxf(top[0], top[1]);
-      };
-      // (the first tile sets the references: its weights are worked out once they are)
-      const bool moves = u == 0 || (!dead && weigh(false) > kLimit);
-      if (named_any(bar, 128, moves || dead)) {
-        // A row's weights passed the limit (or it has no reference yet): the rows' maxima over the tile, new
-        // references for those rows, O scaled, the tile weighed again. All warps of the group come here or none.
-        if (named_any(bar, 128, dead)) break;
+      }
+      return fmaxf(top[0], top[1]);
+    };
+    auto vote = [&](float top, int j) {
+      if (top > kLimit) sh->moves[grp][j & 1] = 1;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->vote[grp]);
+    };
+    int sb = 0;                                          // S buffer of the current tile
+    int next_buf = 0, next_phase = 0;                    // and of the next
+    auto step_buf = [&]() { if (++next_buf == C::kSBufs) next_buf = 0, next_phase ^= 1; };
+    // One tile: its exponents are in `x` and their vote is under way; those of the next come into `next`.
+    auto tile = [&](uint32_t(&x)[C::kRowsT], uint32_t(&next)[C::kRowsT], int j) -> bool {
+      const int g = j & 1;
+      const bool more = j + 1 < w.nt;
+      bool loading = false;
+      if (more) {
+        loading = __all_sync(0xffffffffu, mbar_test_wait(&sh->s_done[next_buf], next_phase));
+        if (loading) load_scores(next, next_buf);
+      }
+      if (!wait(&sh->vote[grp], j & 1)) return false;
+      if (sh->moves[grp][g]) {
+        // A weight would pass the limit, or a row has no reference yet: the rows' maxima over the tile, new references for
+        // those rows, their sums and O scaled, the exponents again. All warps of the group come here or none.
+        const int n_min = first_row(j);
 #pragma unroll 1
-        for (int r = 0; r < w.rows; r += 8) {
+        for (int r = 0; r < my_rows; r += 8) {
           uint32_t sr[8];
-          tmem_ld8(s_at + r, sr);
+          tmem_ld8(s_address(sb) + r, sr);
           float mine = -INFINITY;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float m = warp_max(r + e >= n_min ? __uint_as_float(sr[e]) : -INFINITY);
+            const float m = warp_max(row_first + r + e >= n_min ? __uint_as_float(sr[e]) : -INFINITY);
             mine = lane == e ? m : mine;
           }
-          if (lane < 8) sh->part[grp][wq][r + lane] = mine;
+          if (lane < 8) sh->part[wq][row_first + r + lane] = mine;
         }
-        named_sync(bar, 128);
-        if (tg < NT) {
-          const float old = sh->neg_ref[grp][tg];
+        if (!meet()) return false;
+        if (tg == 0) sh->moves[grp][g] = 0;
+        if (tg < my_rows) {
+          const int r = row_first + tg;
+          const float m = fmaxf(fmaxf(sh->part[0][r], sh->part[1][r]), fmaxf(sh->part[2][r], sh->part[3][r])) * q_scale;
+          const float old = sh->neg_ref[r];
           float a = 1.f;
-          if (tg < w.rows) {
-            const float m = fmaxf(fmaxf(sh->part[grp][0][tg], sh->part[grp][1][tg]),
-                                  fmaxf(sh->part[grp][2][tg], sh->part[grp][3][tg])) * q_scale;
-            if (m + old > kLimit) {
-              a = old == kNone ? 0.f : ex2_approx(kTop - m - old);
-              sh->neg_ref[grp][tg] = kTop - m;
-            }
+          if (m + old > kLimit) {
+            a = old == kNone ? 0.f : ex2_approx(kTop - m - old);
+            sh->neg_ref[r] = kTop - m;
           }
-          sh->old_ref[grp][tg] = old;
-          sh->alpha[grp][tg] = a;
+          sh->alpha[r] = a;
         }
-        named_sync(bar, 128);
-        if (u > 0) {
+        if (!meet()) return false;
+        if (j > 0) {
+          if (!wait(&sh->pv_done[g ^ 1], ((j - 1) >> 1) & 1)) return false;
+          tc_fence_after();
 #pragma unroll 1
-          for (int r = 0; r < w.rows; r += 8) {
+          for (int r = 0; r < my_rows; r += 8) {
             uint32_t o[8];
             tmem_ld8(o_at + r, o);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * sh->alpha[grp][r + e]);
+            for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * sh->alpha[row_first + r + e]);
             tmem_st8_async(o_at + r, o);
           }
           tmem_wait_st();
+#pragma unroll
+          for (int r = 0; r < C::kRowsT; r += 2) {
+            if (r < my_rows) {
+              const float2 a = *reinterpret_cast<const float2*>(&sh->alpha[row_first + r]);
+              l[r / 2].x *= a.x;
+              l[r / 2].y *= a.y;
+            }
+          }
         }
-        weigh(u > 0);
+        load_scores(x, sb);
+        exponents(x, n_min);
+      }
+      tc_fence_before();
+      if (lane == 0) mbar_arrive(&sh->s_free[sb]);
+      if (more) {
+        if (j % kBatch == kBatch - 1 && !wait(&sh->geo_full[(j + 1) / kBatch & 1], (j + 1) / kBatch >> 1 & 1)) return false;
+        if (!loading) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&sh->s_done[next_buf], next_phase, abort, p.err))) return false;
+          load_scores(next, next_buf);
+        }
+        vote(exponents(next, first_row(j + 1)), j + 1);
+      }
+      sb = next_buf;
+      step_buf();
+      // Weights 2^x to shared memory, and their sums
+      if (j >= 2 && !wait(&sh->pv_done[g], ((j >> 1) - 1) & 1)) return false;
+#pragma unroll
+      for (int r = 0; r < C::kRowsT; r += 8) {
+        if (r < my_rows) {
+          uint32_t pk[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float2 a = pair(x, r + 2 * e);
+            a.x = ex2_approx(a.x);
+            a.y = ex2_approx(a.y);
+            l[r / 2 + e] = add_f32x2(l[r / 2 + e], a);
+            pk[e] = pack_f16(a.x, a.y);
+          }
+          const int word = (row_first + r) / 8;          // 16-byte word of the key's rows: 8 words a box
+          sts_u4(prow + g * C::kPBytes + (word >> 3) * C::kBoxBytes + (((word & 7) ^ (key & 7)) << 4),
+                 make_uint4(pk[0], pk[1], pk[2], pk[3]));
+        }
       }
       tc_fence_before();
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->p_ready[grp]);
-    }
-    // ---- epilogue: the groups' sums and O merged into the split's partial (m, l, O not normalised) ----
-    if (u > 0 && !dead) dead = !__all_sync(0xffffffffu, mbar_wait(&sh->pv_done[grp], (u - 1) & 1, abort, p.err));
-#pragma unroll
-    for (int cb = 0; cb < NT / 8; ++cb) {
-      if (cb * 8 < w.rows) {
-        const float sum = sum_rows8(&l[cb * 4], lane);
-        if (lane < 8) sh->part[grp][wq][cb * 8 + lane] = sum;
+      if (lane == 0) mbar_arrive(&sh->p_ready[g]);
+      return true;
+    };
+    bool ok = true;
+    if (w.nt > 0) {
+      uint32_t xa[C::kRowsT], xb[C::kRowsT];
+      ok = wait(&sh->geo_full[0], 0) && wait(&sh->s_done[0], 0);
+      if (ok) {
+        load_scores(xa, 0);
+        vote(exponents(xa, first_row(0)), 0);
+        step_buf();
+        for (int j = 0; ok && j < w.nt; j += 2) {
+          ok = tile(xa, xb, j);
+          if (ok && j + 1 < w.nt) ok = tile(xb, xa, j + 1);
+        }
       }
     }
-    tc_fence_before();
-    named_sync(1, 256);
+    // ---- epilogue: the split's partial (m, l, O not normalised) ----
+    if (ok && w.nt > 0) ok = wait(&sh->pv_done[(w.nt - 1) & 1], ((w.nt - 1) >> 1) & 1);
     tc_fence_after();
+#pragma unroll
+    for (int r = 0; r < C::kRowsT; r += 8) {
+      if (r < my_rows) {
+        const float sum = sum_rows8(&l[r / 2], lane);
+        if (lane < 8) sh->part[wq][row_first + r + lane] = sum;
+      }
+    }
+    named_sync(1, kAll);
     if (static_cast<int>(threadIdx.x) < w.rows) {
       const int r = threadIdx.x;
-      float lg[2], ref[2];
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        lg[g] = (sh->part[g][0][r] + sh->part[g][1][r]) + (sh->part[g][2][r] + sh->part[g][3][r]);
-        ref[g] = lg[g] > 0.f ? -sh->neg_ref[g][r] : -INFINITY;
-      }
-      const float m = fmaxf(ref[0], ref[1]);
-      float sum = 0.f;
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const float wt = lg[g] > 0.f ? ex2_approx(ref[g] - m) : 0.f;
-        sum += wt * lg[g];
-        sh->alpha[g][r] = wt * p.v_scale;
-      }
+      const float sum = (sh->part[0][r] + sh->part[1][r]) + (sh->part[2][r] + sh->part[3][r]);
       const int rg = w.row0 + r;
       const size_t pidx = ((static_cast<size_t>(w.b) * p.row_tiles + rg / kMaxRows) * p.hkv + w.h) * p.num_splits + w.s;
-      reinterpret_cast<float2*>(p.part_ml)[pidx * kMaxRows + rg % kMaxRows] = make_float2(m, sum);
+      reinterpret_cast<float2*>(p.part_ml)[pidx * kMaxRows + rg % kMaxRows] =
+          make_float2(sum > 0.f ? -sh->neg_ref[r] : -INFINITY, sum);
     }
-    named_sync(1, 256);
     if (w.nt > 0 && wq * 32 < HD) {
-      // lane = channel: 32 neighbouring channels of a row are one 128-byte store. The groups take rows of eight in turn.
+      // lane = channel: 32 neighbouring channels of a row are one 128-byte store
 #pragma unroll 1
-      for (int r0 = grp * 8; r0 < w.rows; r0 += 16) {
-        uint32_t o0[8], o1[8];
-        tmem_ld8(lane_base + kColO + r0, o0);
-        tmem_ld8(lane_base + kColO + 96 + r0, o1);
-        const int rg = w.row0 + r0;                      // (a multiple of 8: the eight lie in one of the combine's tiles)
+      for (int r = 0; r < my_rows; r += 8) {
+        uint32_t o[8];
+        tmem_ld8(o_at + r, o);
+        const int rg = w.row0 + row_first + r;           // (a multiple of 8: the eight lie in one of the combine's tiles)
         float* dst = p.part_o +
                      ((((static_cast<size_t>(w.b) * p.row_tiles + rg / kMaxRows) * p.hkv + w.h) * p.num_splits + w.s) * kMaxRows +
                       rg % kMaxRows) * HD + wq * 32 + lane;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (r0 + e < w.rows) {
-            const float w0 = sh->alpha[0][r0 + e], w1 = sh->alpha[1][r0 + e];
-            dst[e * HD] = (w0 > 0.f ? w0 * __uint_as_float(o0[e]) : 0.f) + (w1 > 0.f ? w1 * __uint_as_float(o1[e]) : 0.f);
-          }
-        }
+        for (int e = 0; e < 8; ++e)
+          if (r + e < my_rows) dst[e * HD] = __uint_as_float(o[e]) * p.v_scale;
       }
     }
   }
@@ -673,13 +716,13 @@ cudaError_t launch_t(const PackedAttnParams& p, int num_seqs, cudaStream_t strea
     cudaFuncAttributes a;
     const cudaError_t e = cudaFuncGetAttributes(&a, kern);
     if (e != cudaSuccess) return e;
-    if (NT > kFewN && a.numRegs < kRegsLaunch) return cudaErrorNotSupported;
+    if (Cfg<HD, NT>::kTrade && a.numRegs < Cfg<HD, NT>::kRegsLaunch) return cudaErrorNotSupported;
     registers = true;
   }
   const cudaError_t e = ensure_smem_limit(kern, Cfg<HD, NT>::kSmemBytes, done);
   if (e != cudaSuccess) return e;
   const dim3 grid(p.num_splits, p.hkv, num_seqs * p.n_tiles);
-  return launch_pdl(kern, grid, dim3(kThreads), Cfg<HD, NT>::kSmemBytes, stream, p);
+  return launch_pdl(kern, grid, dim3(Cfg<HD, NT>::kThreads), Cfg<HD, NT>::kSmemBytes, stream, p);
 }
 
 }  // namespace

@@ -32,6 +32,38 @@ __device__ __forceinline__ uint32_t e4m3_pair_f16(uint32_t two) {
 }
 __device__ __forceinline__ float e4m3_value(uint32_t byte) { return f16_value(e4m3_pair_f16(byte) & 0xffffu); }
 
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// The two codes of byte Y of a word times a scale (a pair of them, one for each half).
+template <int Y>
+__device__ __forceinline__ uint32_t unpack_byte(uint32_t codes, uint32_t scale2) {
+  uint32_t r;
+  if constexpr (Y == 0)
+    asm("{\n\t.reg .b8 x0, x1, x2, x3;\n\tmov.b32 {x0, x1, x2, x3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, x0;\n\t}" : "=r"(r) : "r"(codes));
+  else if constexpr (Y == 1)
+    asm("{\n\t.reg .b8 x0, x1, x2, x3;\n\tmov.b32 {x0, x1, x2, x3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, x1;\n\t}" : "=r"(r) : "r"(codes));
+  else if constexpr (Y == 2)
+    asm("{\n\t.reg .b8 x0, x1, x2, x3;\n\tmov.b32 {x0, x1, x2, x3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, x2;\n\t}" : "=r"(r) : "r"(codes));
+  else
+    asm("{\n\t.reg .b8 x0, x1, x2, x3;\n\tmov.b32 {x0, x1, x2, x3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, x3;\n\t}" : "=r"(r) : "r"(codes));
+  return mul_f16x2(r, scale2);
+}
+// Eight codes (a 32-bit word) times a scale: eight fp16 values, two a register.
+__device__ __forceinline__ void unpack_word(uint32_t codes, uint32_t scale2, uint32_t* out) {
+  out[0] = unpack_byte<0>(codes, scale2);
+  out[1] = unpack_byte<1>(codes, scale2);
+  out[2] = unpack_byte<2>(codes, scale2);
+  out[3] = unpack_byte<3>(codes, scale2);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // The e4m3 byte nearest to x >= 0 (ties to even, at most 448; NaN gives 448).
 __device__ __forceinline__ uint32_t e4m3_of(float x) {
   uint16_t r;

@@ -379,6 +379,8 @@ struct PackedAttnParams {
   float v_scale;              // g of V
   float* part_o;              // [B][row tiles][Hkv][splits][128][d]
   float* part_ml;             // [B][row tiles][Hkv][splits][128][2] (m in log2 units, l)
+  uint16_t* out;              // [T][Hq][d]
+  float* lse;                 // [T][Hq] or null
   unsigned long long timeout_test_ns;  // as in AttnParams
   int stable_metadata;
   int* err;
@@ -386,6 +388,9 @@ struct PackedAttnParams {
 // The most block rows that one CTA takes.
 int packed_tile_rows();
 cudaError_t launch_attend_packed(const PackedAttnParams& p, int num_seqs, cudaStream_t stream);
+// The same for contexts of at most kPackedFewRows block rows (max_q * G). A single split writes p.out / p.lse itself.
+constexpr int kPackedFewRows = 16;
+cudaError_t launch_attend_packed_few(const PackedAttnParams& p, int num_seqs, cudaStream_t stream);
 
 // ------------------------------ sampled acceptance --------------------------------------------
 struct SampleParams {
