@@ -1,8 +1,9 @@
-// Attention of a block over a pool of 4-bit chunks, on the tensor cores with the operands exchanged: a tile's 128 keys are
-// the M = 128 side of both products and the block's rows (queries x q-heads of one KV head, at most 72) the N side,
+// Attention of a block over a pool of 4-bit chunks, more than 16 rows a KV head, on the tensor cores with the operands
+// exchanged: a tile's 128 keys are the M = 128 side of both products and the block's rows (queries x q-heads of one KV head,
+// at most 72) the N side,
 //     S^T [128 keys][rows] = K Q^T,    O^T [d][rows] += V^T P^T,
-// so that the work follows the rows a block has: one token of G = 4 is N = 16, a block of 17 is N = 80. With the rows as M (as
-// in the bf16 layers) a 4-bit tile would be bound by the 128 rows' tensor time.
+// so that the work follows the rows a block has: a block of 17 with G = 4 is N = 80 (68 rows). With the rows as M (as in the
+// bf16 layers) a 4-bit tile would be bound by the 128 rows' tensor time.
 //
 // A value is g s e; s e has 6 significant bits, so the operands in fp16 are exact. Queries are bf16: the tile's are scaled by
 // one power of two that puts the largest at 2^14, and fp16 holds all 8 bits of what is above 2^-28 of it. Weights P are
@@ -10,14 +11,18 @@
 // reference moves, and what fp16 drops (below 2^-25) is 2^-32 of the largest weight.
 //
 // One CTA per (split, KV head, sequence and row tile), a contiguous run of tiles of two chunks. Roles:
-//   softmax          a lane is a key, its 32-bit columns are the rows. Each warpgroup has up to 24 (8) of the rows, with their
-//                    reference, sums and columns of O: the groups meet only in the MMAs. While a tile's weights are
-//                    worked out, the next tile's scores are on their way and the vote whether one of them passes the limit.
-//   K, V             two warpgroups each, which take tiles in turn: a lane reads its key's codes and scales, writes fp16
-//                    into tensor memory (K, the A operand of S) or shared memory (V, channels contiguous: the A operand
-//                    of O^T, M-major)
+//   softmax          of even / odd tiles: a lane is a key, its 32-bit columns are the rows. Two groups with a reference, row
+//                    sums and O of their own, merged at the end; a group has two tiles' time for one. A group is two
+//                    warpgroups, each with half of the rows, all of them in registers; a vote of the group says whether a
+//                    reference has to move, which is rare: then the tile is read again from tensor memory.
+//   K                a lane reads its key's codes and scales, writes fp16 into tensor memory (the A operand of S)
+//   V                the same into shared memory, channels contiguous (the A operand of O^T, M-major)
 //   one warp         bulk copies of the records (contiguous: no tensor map), and the tiles' geometry
 //   two warps        the MMA issuers of S and of O
+//
+// 17 rows, 16 q-heads over 4 KV heads, d = 128: 256K tokens in 59.6 us, 8K in 15.4, eight ragged sequences of up to 32K in 82.
+// A tile takes 1.8 thousand cycles. Shared memory moves 1.35 of them (V written and read 512, P and Q 450, records 290),
+// the schedulers issue 1.1 (K and V to fp16 a third, weights a third); the records alone, from HBM, would be 0.8.
 #include <cuda_bf16.h>
 
 #include "packed.cuh"
@@ -27,45 +32,35 @@
 namespace vfy {
 namespace {
 
+constexpr int kGroups = 8;                // warpgroups: softmax (0-3), K, V (of even, of odd tiles), the rest
+constexpr int kThreads = kGroups * 128, kVGroups = 2;
+constexpr int kRegsLaunch = 64, kRegsSoftmax = 96, kRegsUnpack = 32, kRegsRest = 32;
+static_assert(4 * kRegsSoftmax + (1 + kVGroups) * kRegsUnpack + kRegsRest <= kGroups * kRegsLaunch, "registers the CTA was launched with");
+constexpr int kKWarp = 16, kVWarp = 20, kProducerWarp = 28, kMmaWarp = 29;
 constexpr int kKeys = 2 * kChunk;         // keys of a tile
-constexpr int kFewN = 16, kMaxN = 72;     // rows of a tile (two kernels)
+constexpr int kMaxN = 72, kN = 80;        // rows of a tile; N of the MMAs, a multiple of 16
+static_assert(kMaxN == 72, "rows of the two halves of a group");
+constexpr int kRowsT = kMaxN / 2;         // rows of a softmax thread, which holds their scores and sums
+constexpr int kStages = 4;
 constexpr int kBatch = 16;                // tiles whose chunks a warp's lanes hold; their geometry lies in two such batches
 constexpr uint32_t kTmemCols = 512;
 constexpr float kTop = 7.f;               // a row's maximum when its reference is set (log2)
 constexpr float kLimit = 15.f;            // the reference moves when a weight would pass 2^15
-constexpr float kNone = 1e30f;            // minus the reference of a row that has none: every score passes the limit
+// columns of tensor memory: two K tiles of up to 64 (two fp16 channels each), S^T and O^T of the two groups
+constexpr uint32_t kColS = 128, kColO = kColS + 2 * kN;
+static_assert(kColO + 2 * kN <= kTmemCols, "tensor memory");
 
-template <int HD, int NT>
+template <int HD>
 struct Cfg {
-  static constexpr bool kFew = NT <= kFewN;
-  static constexpr int kSoftmax = kFew ? 2 : 3;                  // warpgroups of softmax
-  static constexpr int kRowsT = NT / kSoftmax;                   // rows of a softmax thread
-  static constexpr int kUnpack = 2;                              // warpgroups of K, and of V
-  static constexpr int kGroups = kSoftmax + 2 * kUnpack + 1;
-  static constexpr int kThreads = kGroups * 128;
-  static constexpr int kKWarp = 4 * kSoftmax, kVWarp = kKWarp + 4 * kUnpack;
-  static constexpr int kProducerWarp = kVWarp + 4 * kUnpack, kMmaWarp = kProducerWarp + 1;
-  // Registers: with 72 rows the softmax groups take up what the others give up.
-  static constexpr bool kTrade = !kFew;
-  static constexpr int kRegsLaunch = 64, kRegsSoftmax = 104, kRegsUnpack = 40, kRegsRest = 40;
-  static_assert(!kTrade || kSoftmax * kRegsSoftmax + 2 * kUnpack * kRegsUnpack + kRegsRest <= kGroups * kRegsLaunch,
-                "registers the CTA was launched with");
-  static constexpr int kN = (NT + 15) / 16 * 16;                 // N of the MMAs: multiples of 16
-  static constexpr int kStages = 4;
-  static constexpr int kKBufs = kFew ? 4 : 2, kSBufs = kFew ? 4 : 3;   // in tensor memory
-  static constexpr int kVBufs = kFew ? 3 : 2;
-  // columns: K tiles of up to 64 (two fp16 channels each), S^T, O^T
-  static constexpr uint32_t kColS = kKBufs * 64, kColO = kColS + kSBufs * kN;
-  static_assert(kColO + kN <= kTmemCols && kStages % kUnpack == 0, "tensor memory, stages");
   static constexpr int kRecord = kPackedBytes<HD>;
   static constexpr int kStageBytes = 4 * kRecord;                // K and V of two chunks
   static constexpr int kBoxBytes = kKeys * 128;                  // 64 columns of 128 keys
   static constexpr int kVBytes = 2 * kBoxBytes;                  // M = 128: d = 64 leaves the second box zero
-  static constexpr int kPBytes = (kN + 63) / 64 * kBoxBytes;
+  static constexpr int kPBytes = 2 * kBoxBytes;
   static constexpr int kQBoxBytes = kN * 128;
   static constexpr int kQBytes = (HD / 64) * kQBoxBytes;
   static constexpr int kVOffset = 0;
-  static constexpr int kPOffset = kVBufs * kVBytes;
+  static constexpr int kPOffset = 2 * kVBytes;
   static constexpr int kQOffset = kPOffset + 2 * kPBytes;
   static constexpr int kStageOffset = kQOffset + kQBytes;
   static constexpr int kBarOffset = kStageOffset + kStages * kStageBytes;
@@ -76,25 +71,25 @@ struct Cfg {
 };
 
 struct Shared {
-  uint64_t full[4], empty[4];
+  uint64_t full[kStages], empty[kStages];
   uint64_t geo_full[2];
-  uint64_t k_ready[4], k_free[4];
-  uint64_t s_done[4], s_free[4];          // S^T written; read
-  uint64_t v_ready[3], v_free[3];
-  uint64_t p_ready[2], pv_done[2];        // P written; O^T holds the tile, its P is free
-  uint64_t vote[3], meet[3];              // [softmax group]: of one tile; where a reference moves
+  // of even / odd tiles
+  uint64_t k_ready[2], s_done[2], s_free[2];   // K written; S^T written and K free; S^T read
+  uint64_t v_ready[2], p_ready[2];
+  uint64_t pv_done[2];                    // O^T holds the tile, its P and V are free
   uint64_t q_ready, drain[2], never;
   uint32_t tmem_base;
   int abort;
   unsigned q_top;                         // largest |q| of the tile, as bf16 bits
-  int moves[3][2];                        // [softmax group][tile parity]: a weight would pass the limit
   int base[2 * kBatch][2];                // position of a chunk's first token, -1: no chunk
+  int4 geom[2];                           // [group] length, position of the block's first token, first row, rows: read
+                                          // where they are needed, registers are short
   int plain[2 * kBatch];                  // every row attends every key of the tile
-  alignas(16) float neg_ref[kMaxN];       // minus the rows' reference, log2 units
-  alignas(16) float alpha[kMaxN];
-  alignas(16) float part[4][kMaxN];       // [lane quarter]: maxima, at the end sums
+  alignas(16) float neg_ref[2][kMaxN];    // [group] minus the rows' reference, log2 units
+  alignas(16) float alpha[2][kMaxN];      // a factor of what was summed before the reference moved
+  alignas(16) float part[2][4][kMaxN];    // [group][lane quarter]: maxima, at the end sums
 };
-static_assert(sizeof(Shared) <= Cfg<128, kMaxN>::kBarBytes, "barrier block");
+static_assert(sizeof(Shared) <= Cfg<128>::kBarBytes, "barrier block");
 
 struct Work {
   int b, h, s;
@@ -143,38 +138,95 @@ __device__ __forceinline__ uint32_t lds_u32(uint32_t at) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
   return v;
 }
+__device__ __forceinline__ void sts_u2(uint32_t at, uint2 v) {
+  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(v.x), "r"(v.y));
+}
 // (no memory clobber: what is written is read by MMAs alone, behind a proxy fence, and loads may move ahead of it)
 __device__ __forceinline__ void sts_u4(uint32_t at, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w));
 }
 
-// One value per row of eight from 32 lanes: lane r (r < 8, and every lane alike modulo 8) gets row r's sum.
-__device__ __forceinline__ float sum_rows8(const float2* l2, int lane) {
-  const float l[8] = {l2[0].x, l2[0].y, l2[1].x, l2[1].y, l2[2].x, l2[2].y, l2[3].x, l2[3].y};
-  float a[4], b[2], c;
-  const bool h4 = lane & 4, h2 = lane & 2, h1 = lane & 1;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float other = __shfl_xor_sync(0xffffffffu, h4 ? l[i] : l[i + 4], 4);
-    a[i] = (h4 ? l[i + 4] : l[i]) + other;
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float other = __shfl_xor_sync(0xffffffffu, h2 ? a[i] : a[i + 2], 2);
-    b[i] = (h2 ? a[i + 2] : a[i]) + other;
-  }
-  const float other = __shfl_xor_sync(0xffffffffu, h1 ? b[0] : b[1], 1);
-  c = (h1 ? b[1] : b[0]) + other;
+// One value per row of four from 32 lanes: lane r (and every lane alike modulo 4) gets row r's sum.
+__device__ __forceinline__ float sum_rows4(const float2* l2, int lane) {
+  const bool h2 = lane & 2, h1 = lane & 1;
+  const float2 mine = h2 ? l2[1] : l2[0], theirs = h2 ? l2[0] : l2[1];
+  const float a = mine.x + __shfl_xor_sync(0xffffffffu, theirs.x, 2), b = mine.y + __shfl_xor_sync(0xffffffffu, theirs.y, 2);
+  float c = (h1 ? b : a) + __shfl_xor_sync(0xffffffffu, h1 ? a : b, 1);
+  c += __shfl_xor_sync(0xffffffffu, c, 4);
   c += __shfl_xor_sync(0xffffffffu, c, 8);
   c += __shfl_xor_sync(0xffffffffu, c, 16);
   return c;
 }
 
-template <int HD, int NT>
-__global__ void __launch_bounds__(Cfg<HD, NT>::kThreads, 1) attend_packed_kernel(const PackedAttnParams p) {
-  using C = Cfg<HD, NT>;
-  constexpr int kStages = C::kStages, kThreads = C::kThreads;
-  constexpr int kKWarp = C::kKWarp, kVWarp = C::kVWarp, kProducerWarp = C::kProducerWarp, kMmaWarp = C::kMmaWarp;
+// The K or V role of a warpgroup: tiles first, first + step, ... A lane has one key of the tile (a lane of tensor memory).
+template <int HD, bool V>
+__device__ __forceinline__ void unpack_tiles(const PackedAttnParams& p, const Work& w, Shared* sh, uint32_t sbase, int first,
+                                             int step) {
+  using C = Cfg<HD>;
+  volatile int* abort = &sh->abort;
+  const int lane = threadIdx.x & 31, key = threadIdx.x & 127;
+  const int c = key / kChunk, tok = key % kChunk;
+  const uint32_t rec = sbase + C::kStageOffset + ((V ? 2 : 0) + c) * C::kRecord;
+  const uint32_t scales_at = rec + kChunk * (HD / 2) + tok * (HD / 16), codes_at = rec + tok * 16;
+  // (a row of 128 bytes starts with zeros in the bits that the swizzle changes: one XOR a word)
+  const uint32_t to = V ? sbase + C::kVOffset + key * 128 + ((key & 7) << 4) : static_cast<uint32_t>((key & 96) << 16);
+  for (int j = first; j < w.nt; j += step) {
+    const int st = j % kStages, g = j & 1;
+    bool ok = mbar_wait_tested(&sh->full[st], j / kStages & 1, abort, p.err);
+    if (V && j % kBatch == first && ok) ok = mbar_wait_tested(&sh->geo_full[j / kBatch & 1], j / kBatch >> 1 & 1, abort, p.err);
+    if (ok && j >= 2) ok = mbar_wait_tested(V ? &sh->pv_done[g] : &sh->s_done[g], (j >> 1 & 1) ^ 1, abort, p.err);
+    if (!__all_sync(0xffffffffu, ok)) break;
+    const uint32_t at = st * C::kStageBytes;
+    // Keys that no row attends may hold anything: P is 0 there, but 0 * NaN is NaN.
+    bool keep = true;
+    if (V && !sh->plain[j % (2 * kBatch)]) {
+      const int base = sh->base[j % (2 * kBatch)][c];
+      keep = base >= 0 && base + tok < w.L;
+    }
+    if (!V) tc_fence_after();
+#pragma unroll
+    for (int y = 0; y < HD / 64; ++y) {                  // 64 channels: two words of codes, four scales
+      // (both words loaded before the first store: the compiler keeps loads behind stores)
+      const uint4 codes[2] = {lds_u4(codes_at + at + 2 * y * kChunk * 16), lds_u4(codes_at + at + (2 * y + 1) * kChunk * 16)};
+      uint32_t scales = lds_u32(scales_at + at + 4 * y);
+      if (V && !keep) scales = 0u;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint32_t two = e4m3_pair_f16(x == 0 ? scales & 0xffffu : scales >> 16);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {                    // 16 channels: one scale
+          const uint32_t sc = __byte_perm(two, two, i == 0 ? 0x1010 : 0x3232);
+          uint32_t out[8];
+          unpack_word(i == 0 ? codes[x].x : codes[x].z, sc, out);
+          unpack_word(i == 0 ? codes[x].y : codes[x].w, sc, out + 4);
+          if constexpr (V) {
+#pragma unroll
+            for (int z = 0; z < 2; ++z)                  // 16-byte words of the 128-byte row
+              sts_u4(((to + g * C::kVBytes) ^ ((x * 4 + 2 * i + z) << 4)) + y * C::kBoxBytes,
+                     make_uint4(out[4 * z], out[4 * z + 1], out[4 * z + 2], out[4 * z + 3]));
+          } else {
+            tmem_st8_async(to + g * 64 + (4 * y + 2 * x + i) * 8, out);
+          }
+        }
+      }
+    }
+    if constexpr (V) {
+      fence_proxy_async_smem();
+    } else {
+      tmem_wait_st();
+      tc_fence_before();
+    }
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&sh->empty[st]);
+      mbar_arrive(V ? &sh->v_ready[g] : &sh->k_ready[g]);
+    }
+  }
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const PackedAttnParams p) {
+  using C = Cfg<HD>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (sbase - smem_u32(smem_raw));
@@ -190,29 +242,16 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::kThreads, 1) attend_packed_kernel
       mbar_init(&sh->full[i], 2);
       mbar_init(&sh->empty[i], 8);
     }
-    for (int i = 0; i < C::kKBufs; ++i) {
-      mbar_init(&sh->k_ready[i], 4);
-      mbar_init(&sh->k_free[i], 1);
-    }
-    for (int i = 0; i < C::kSBufs; ++i) {
-      mbar_init(&sh->s_done[i], 1);
-      mbar_init(&sh->s_free[i], 4 * C::kSoftmax);
-    }
-    for (int i = 0; i < C::kVBufs; ++i) {
-      mbar_init(&sh->v_ready[i], 4);
-      mbar_init(&sh->v_free[i], 1);
-    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh->geo_full[i], 1);
-      mbar_init(&sh->p_ready[i], 4 * C::kSoftmax);
+      mbar_init(&sh->k_ready[i], 4);
+      mbar_init(&sh->s_done[i], 1);
+      mbar_init(&sh->s_free[i], 8);
+      mbar_init(&sh->v_ready[i], 4);
+      mbar_init(&sh->p_ready[i], 8);
       mbar_init(&sh->pv_done[i], 1);
     }
-    for (int i = 0; i < C::kSoftmax; ++i) {
-      mbar_init(&sh->vote[i], 4);
-      mbar_init(&sh->meet[i], 4);
-      sh->moves[i][0] = sh->moves[i][1] = 0;
-    }
-    mbar_init(&sh->q_ready, 4 * C::kSoftmax);
+    mbar_init(&sh->q_ready, 16);
     mbar_init(&sh->drain[0], 1);
     mbar_init(&sh->drain[1], 1);
     mbar_init(&sh->never, 1);
@@ -226,7 +265,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::kThreads, 1) attend_packed_kernel
   }
   if (HD == 64) {
     // M = 128 with 64 channels: the second box of V stays zero
-    for (int x = threadIdx.x; x < C::kVBufs * C::kBoxBytes / 16; x += kThreads) {
+    for (int x = threadIdx.x; x < 2 * C::kBoxBytes / 16; x += kThreads) {
       const int buf = x / (C::kBoxBytes / 16), at = x % (C::kBoxBytes / 16);
       *reinterpret_cast<uint4*>(sV + buf * C::kVBytes + C::kBoxBytes + at * 16) = make_uint4(0u, 0u, 0u, 0u);
     }
@@ -245,7 +284,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::kThreads, 1) attend_packed_kernel
   if (w.bad && threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(p.err, kErrDeviceInput);
 
   if (warp >= kProducerWarp) {
-    if constexpr (C::kTrade) regs_dec<C::kRegsRest>();
+    regs_dec<kRegsRest>();
     if (warp == kProducerWarp) {
       // ------------------------------ records and geometry --------------------------------
       // A lane holds one chunk of sixteen tiles; a tile's two lanes issue its copies, with no word between them.
@@ -294,8 +333,8 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::kThreads, 1) attend_packed_kernel
       __syncwarp();
     } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
       // ------------------------------ MMA issuers -----------------------------------------
-      // One warp for S, one for O: issuing a tile's eight MMAs of one kind with its waits takes 500 to 600 cycles, more
-      // than the tensor core does (N = 16: 160 and 320). The whole warp runs the loop (see elect_one). Tensor memory is
+      // One warp for S, one for O: issuing a tile's eight MMAs of one kind with its waits takes 500 to 600 cycles, as long as
+      // the tensor core does. The whole warp runs the loop (see elect_one). Tensor memory is
       // allocated whole: it starts at column 0.
       const bool is_o = warp != kMmaWarp;
       const int nt = uniform(w.nt), n = (uniform(w.rows) + 15) & ~15;
@@ -307,43 +346,37 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::kThreads, 1) attend_packed_kernel
         if (!is_o) {
           const uint32_t idesc = idesc_f16_f32(128, n, 0, 0);
           const uint64_t qdesc = sw128_desc(sbase + C::kQOffset, 16, 1024);
-          int sb = 0, s_phase = 1;                       // S buffer; the parity of its earlier use
           for (int j = 0; j < nt; ++j) {
-            const int kb = j % C::kKBufs;
-            ok = wait(&sh->k_ready[kb], j / C::kKBufs & 1) && (j < C::kSBufs || wait(&sh->s_free[sb], s_phase));
+            const int g = j & 1, ph = j >> 1 & 1;
+            ok = wait(&sh->k_ready[g], ph) && (j < 2 || wait(&sh->s_free[g], ph ^ 1));
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < HD / 16; ++kk)
-                mma_ts(C::kColS + sb * C::kN, kb * 64 + kk * 8,
+                mma_ts(kColS + g * kN, g * 64 + kk * 8,
                        qdesc + static_cast<uint64_t>(((kk >> 2) * C::kQBoxBytes + (kk & 3) * 32) >> 4), idesc, kk > 0 ? 1u : 0u);
-              mma_commit(&sh->s_done[sb]);
-              mma_commit(&sh->k_free[kb]);
+              mma_commit(&sh->s_done[g]);
             }
             __syncwarp();
-            if (++sb == C::kSBufs) sb = 0, s_phase ^= 1;
           }
         } else {
           const uint32_t idesc = idesc_f16_f32(128, n, 1, 1);
           const uint64_t vdesc = sw128_desc(sbase + C::kVOffset, C::kBoxBytes, 1024);
           const uint64_t pdesc = sw128_desc(sbase + C::kPOffset, C::kBoxBytes, 1024);
-          int vb = 0, v_phase = 0;
           for (int j = 0; j < nt; ++j) {
-            const int g = j & 1, ph = (j >> 1) & 1;
-            ok = wait(&sh->v_ready[vb], v_phase) && wait(&sh->p_ready[g], ph);
+            const int g = j & 1, ph = j >> 1 & 1;
+            ok = wait(&sh->v_ready[g], ph) && wait(&sh->p_ready[g], ph);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < kKeys / 16; ++kk)
-                mma_ss(C::kColO, vdesc + static_cast<uint64_t>((vb * C::kVBytes + kk * 2048) >> 4),
-                       pdesc + static_cast<uint64_t>((g * C::kPBytes + kk * 2048) >> 4), idesc, (j > 0 || kk > 0) ? 1u : 0u);
+                mma_ss(kColO + g * kN, vdesc + static_cast<uint64_t>((g * C::kVBytes + kk * 2048) >> 4),
+                       pdesc + static_cast<uint64_t>((g * C::kPBytes + kk * 2048) >> 4), idesc, (j > 1 || kk > 0) ? 1u : 0u);
               mma_commit(&sh->pv_done[g]);
-              mma_commit(&sh->v_free[vb]);
             }
             __syncwarp();
-            if (++vb == C::kVBufs) vb = 0, v_phase ^= 1;
           }
         }
         // Every MMA issued above completes before tensor memory is freed.
@@ -355,88 +388,25 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::kThreads, 1) attend_packed_kernel
     }
   } else if (warp >= kKWarp) {
     // ------------------------------ K and V to fp16 -----------------------------------------
-    if constexpr (C::kTrade) regs_dec<C::kRegsUnpack>();
-    const bool is_v = warp >= kVWarp;
-    const int wg = (warp >> 2) - (is_v ? kVWarp : kKWarp) / 4;   // takes tiles wg, wg + kUnpack, ...
-    const int key = (warp & 3) * 32 + lane;              // of the tile; a TMEM lane
-    const int c = key / kChunk, tok = key % kChunk;
-    const int bufs = is_v ? C::kVBufs : C::kKBufs;
-    uint64_t* free_bar = is_v ? sh->v_free : sh->k_free;
-    uint64_t* ready_bar = is_v ? sh->v_ready : sh->k_ready;
-    const uint32_t rec = sbase + C::kStageOffset + ((is_v ? 2 : 0) + c) * C::kRecord;
-    const uint32_t scales_at = rec + kChunk * (HD / 2) + tok * (HD / 16);
-    const uint32_t codes_at = rec + tok * 16;
-    int st = wg, stage_phase = 0;
-    int buf = wg, free_phase = 1;                        // of this WG's next tile; its buffer's earlier use
-    for (int j = wg; j < w.nt; j += C::kUnpack) {
-      bool ok = mbar_wait_tested(&sh->full[st], stage_phase, abort, p.err);
-      if (is_v && j % kBatch < C::kUnpack && ok)
-        ok = mbar_wait_tested(&sh->geo_full[j / kBatch & 1], j / kBatch >> 1 & 1, abort, p.err);
-      if (ok && j >= bufs) ok = mbar_wait_tested(&free_bar[buf], free_phase, abort, p.err);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      const uint32_t kto = (static_cast<uint32_t>((warp & 3) * 32) << 16) + buf * 64;
-      const uint32_t vto = sbase + C::kVOffset + buf * C::kVBytes + key * 128;
-      const uint32_t at = st * C::kStageBytes;
-      // Keys that no row attends may hold anything: P is 0 there, but 0 * NaN is NaN.
-      bool keep = true;
-      if (is_v && !sh->plain[j % (2 * kBatch)]) {
-        const int base = sh->base[j % (2 * kBatch)][c];
-        keep = base >= 0 && base + tok < w.L;
-      }
-      if (!is_v) tc_fence_after();
-#pragma unroll
-      for (int y = 0; y < HD / 64; ++y) {                // 64 channels: two words of codes, four scales
-        // (both words loaded before the first store: the compiler keeps loads behind stores)
-        const uint4 codes[2] = {lds_u4(codes_at + at + 2 * y * kChunk * 16), lds_u4(codes_at + at + (2 * y + 1) * kChunk * 16)};
-        const uint32_t scales = keep ? lds_u32(scales_at + at + 4 * y) : 0u;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t two = e4m3_pair_f16(x == 0 ? scales & 0xffffu : scales >> 16);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {                  // 16 channels: one scale
-            const uint32_t sc = __byte_perm(two, two, i == 0 ? 0x1010 : 0x3232);
-            uint32_t out[8];
-            unpack_word(i == 0 ? codes[x].x : codes[x].z, sc, out);
-            unpack_word(i == 0 ? codes[x].y : codes[x].w, sc, out + 4);
-            if (!is_v) {
-              tmem_st8_async(kto + (4 * y + 2 * x + i) * 8, out);
-            } else {
-#pragma unroll
-              for (int z = 0; z < 2; ++z)                // 16-byte words of the 128-byte row
-                sts_u4(vto + y * C::kBoxBytes + (((x * 4 + 2 * i + z) ^ (key & 7)) << 4),
-                       make_uint4(out[4 * z], out[4 * z + 1], out[4 * z + 2], out[4 * z + 3]));
-            }
-          }
-        }
-      }
-      if (is_v) {
-        fence_proxy_async_smem();
-      } else {
-        tmem_wait_st();
-        tc_fence_before();
-      }
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&sh->empty[st]);
-        mbar_arrive(&ready_bar[buf]);
-      }
-      st += C::kUnpack;
-      if (st >= C::kStages) st -= C::kStages, stage_phase ^= 1;
-      buf += C::kUnpack;
-      if (buf >= bufs) buf -= bufs, free_phase ^= 1;
-    }
+    regs_dec<kRegsUnpack>();
+    // (V waits for O of two tiles before: with one warpgroup for it a tile took 3% longer)
+    if (warp >= kVWarp)
+      unpack_tiles<HD, true>(p, w, sh, sbase, (warp - kVWarp) >> 2, kVGroups);
+    else
+      unpack_tiles<HD, false>(p, w, sh, sbase, 0, 1);
   } else {
     // ------------------------------ softmax ---------------------------------------------------
-    if constexpr (C::kTrade) regs_inc<C::kRegsSoftmax>();
-    constexpr int kAll = 128 * C::kSoftmax;
-    const int grp = warp >> 2, wq = warp & 3;
-    const int rows_each = ((w.rows + C::kSoftmax - 1) / C::kSoftmax + 7) & ~7;
-    const int row_first = grp * rows_each;
-    const int my_rows = max(0, min(rows_each, w.rows - row_first));
-    const int tg = threadIdx.x & 127;                    // thread of the group; its key of a tile
-    const int key = tg;
+    regs_inc<kRegsSoftmax>();
+    constexpr int kAll = 512, kGroup = 256;
+    const int grp = warp >> 3, half = warp >> 2 & 1, wq = warp & 3;
+    // Rows of this thread: every other eight of the first 64, four of the last eight.
+    const int row_lo = half * 8, row_hi = 64 + half * 4;
+    auto row_of = [&](int r) { return r < 32 ? (r >> 3) * 16 + row_lo + (r & 7) : row_hi + r - 32; };
+    const int tg = threadIdx.x & 255;                    // thread of the group
+    const int key = threadIdx.x & 127;
+    const int bar = 2 + grp;                             // named barrier of the group; 1: both groups
     // Q: words of 8 channels, all of a thread's in registers while the tile's largest value is found
-    constexpr int kWords = (C::kN * HD / 8 + kAll - 1) / kAll;
+    constexpr int kWords = (kN * HD / 8 + kAll - 1) / kAll;
     float q_scale;                                       // of a score: softmax scale, g of K, the queries' power of two
     {
       uint4 qv[kWords];
@@ -471,7 +441,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::kThreads, 1) attend_packed_kernel
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           o[e] = pack_f16(__uint_as_float(ws[e] << 16) * down, __uint_as_float(ws[e] & 0xffff0000u) * down);
-        if (r < C::kN)
+        if (r < kN)
           *reinterpret_cast<uint4*>(sQ + (cw >> 3) * C::kQBoxBytes + r * 128 + (((cw & 7) ^ (r & 7)) << 4)) =
               make_uint4(o[0], o[1], o[2], o[3]);
       }
@@ -479,222 +449,195 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::kThreads, 1) attend_packed_kernel
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->q_ready);
     }
-    // (rows past the block, Q = 0, keep weight 1: never read)
-    if (static_cast<int>(threadIdx.x) < NT) sh->neg_ref[threadIdx.x] = static_cast<int>(threadIdx.x) < w.rows ? kNone : 0.f;
-    named_sync(1, kAll);
+    // No reference yet. Rows past the block weigh 0, whatever their scores hold: all 36 rows of a thread are computed
+    // without a branch.
+    if (tg < kMaxN) sh->neg_ref[grp][tg] = tg < w.rows ? 0.f : -INFINITY;
+    if (tg == 0) sh->geom[grp] = make_int4(w.L, w.L - w.nq, w.row0, w.rows);
+    bool has_ref = tg >= w.rows;                         // of row tg
+    bool all_have = false;                               // of the group
+    named_sync(bar, kGroup);
 
     const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
-    const uint32_t o_at = lane_base + C::kColO + row_first;
-    const uint32_t prow = sbase + C::kPOffset + key * 128;
-    const int p0 = w.L - w.nq;
+    const uint32_t s_at = lane_base + kColS + grp * kN;
+    const uint32_t prow = sbase + C::kPOffset + grp * C::kPBytes + key * 128 + (((key & 7) ^ half) << 4);   // word `half` of the row
     const float2 sc2 = make_float2(q_scale, q_scale);
-    float2 l[C::kRowsT / 2];
+    float2 l[kRowsT / 2];
 #pragma unroll
-    for (int r = 0; r < C::kRowsT / 2; ++r) l[r] = make_float2(0.f, 0.f);
-    auto wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, mbar_wait_tested(bar, parity, abort, p.err)); };
-    int met = 0;                                         // the group's meetings so far
-    auto meet = [&]() {                                  // all warps of the group, what they wrote to shared memory seen
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->meet[grp]);
-      return wait(&sh->meet[grp], met++ & 1);
-    };
-    // Rows from n_min on attend this lane's key of tile j: row n is of block query (row0 + n) / G, at position p0 + that.
-    auto first_row = [&](int j) -> int {
-      const int geo = j % (2 * kBatch);
-      if (sh->plain[geo]) return 0;
-      const int base = sh->base[geo][key / kChunk], pos = base + key % kChunk;
-      if (base < 0 || pos >= w.L) return NT;
-      return pos > p0 ? min(static_cast<long long>(NT), max(0ll, static_cast<long long>(pos - p0) * p.group - w.row0)) : 0;
-    };
-    auto s_address = [&](int buf) { return lane_base + C::kColS + buf * C::kN + row_first; };
-    auto load_scores = [&](uint32_t(&x)[C::kRowsT], int buf) {
+    for (int r = 0; r < kRowsT / 2; ++r) l[r] = make_float2(0.f, 0.f);
+    bool dead = false;                                   // a wait of this warp gave up
+    int u = 0;                                           // tiles of this group so far
+    for (int j = grp; j < w.nt; j += 2, ++u) {
+      if (j % kBatch == grp && !mbar_wait_tested(&sh->geo_full[j / kBatch & 1], j / kBatch >> 1 & 1, abort, p.err)) dead = true;
+      if (!mbar_wait_tested(&sh->s_done[grp], u & 1, abort, p.err)) dead = true;
+      dead = __any_sync(0xffffffffu, dead);
       tc_fence_after();
+      uint32_t s[kRowsT];
+      const int geo = j % (2 * kBatch);
+      bool pv = u == 0 || mbar_test_wait(&sh->pv_done[grp], (u - 1) & 1);
+      pv = __all_sync(0xffffffffu, pv);
+      bool stop = false;                                 // a warp of the group gave up
+      for (bool again = false;; again = true) {
+        // s = score - reference (log2)
 #pragma unroll
-      for (int r = 0; r < C::kRowsT; r += 8) tmem_ld8_async(s_address(buf) + r, *reinterpret_cast<uint32_t(*)[8]>(x + r));
-    };
-    // Scores to exponents s scale - ref, masked keys to -inf; the largest.
-    auto exponents = [&](uint32_t(&x)[C::kRowsT], int n_min) -> float {
-      tmem_wait_ld(x);
-      if (!__all_sync(0xffffffffu, n_min == 0)) {
+        for (int r = 0; r < 32; r += 8) tmem_ld8_async(s_at + row_of(r), s + r);
+        tmem_ld4_async(s_at + row_hi, s + 32);
+        tmem_wait_ld(s);
+        if (!sh->plain[geo]) {
+          // Rows from n_min on attend this lane's key: row n is of block query (row0 + n) / G, at position p0 + that.
+          const int base = sh->base[geo][key / kChunk], pos = base + key % kChunk;
+          const int4 gm = sh->geom[grp];
+          int n_min = 0;
+          if (base < 0 || pos >= gm.x)
+            n_min = kMaxN;
+          else if (pos > gm.y)
+            n_min = min(static_cast<long long>(kMaxN), max(0ll, static_cast<long long>(pos - gm.y) * p.group - gm.z));
 #pragma unroll
-        for (int r = 0; r < C::kRowsT; ++r) x[r] = row_first + r >= n_min ? x[r] : 0xff800000u;
-      }
-      float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int r = 0; r < C::kRowsT; r += 8) {
-        if (r < my_rows) {
-          const float4* nr = reinterpret_cast<const float4*>(&sh->neg_ref[row_first + r]);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float4 f = nr[e];
-            const float2 a = fma_f32x2(pair(x, r + 4 * e), sc2, make_float2(f.x, f.y));
-            const float2 b = fma_f32x2(pair(x, r + 4 * e + 2), sc2, make_float2(f.z, f.w));
-            top[0] = fmaxf(fmaxf(top[0], a.x), a.y);
-            top[1] = fmaxf(fmaxf(top[1], b.x), b.y);
-            x[r + 4 * e] = __float_as_uint(a.x);
-            x[r + 4 * e + 1] = __float_as_uint(a.y);
-            x[r + 4 * e + 2] = __float_as_uint(b.x);
-            x[r + 4 * e + 3] = __float_as_uint(b.y);
-          }
+          for (int r = 0; r < kRowsT; ++r) s[r] = row_of(r) >= n_min ? s[r] : 0xff800000u;   // 2^-inf = 0
         }
-      }
-      return fmaxf(top[0], top[1]);
-    };
-    auto vote = [&](float top, int j) {
-      if (top > kLimit) sh->moves[grp][j & 1] = 1;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->vote[grp]);
-    };
-    int sb = 0;                                          // S buffer of the current tile
-    int next_buf = 0, next_phase = 0;                    // and of the next
-    auto step_buf = [&]() { if (++next_buf == C::kSBufs) next_buf = 0, next_phase ^= 1; };
-    // One tile: its exponents are in `x` and their vote is under way; those of the next come into `next`.
-    auto tile = [&](uint32_t(&x)[C::kRowsT], uint32_t(&next)[C::kRowsT], int j) -> bool {
-      const int g = j & 1;
-      const bool more = j + 1 < w.nt;
-      bool loading = false;
-      if (more) {
-        loading = __all_sync(0xffffffffu, mbar_test_wait(&sh->s_done[next_buf], next_phase));
-        if (loading) load_scores(next, next_buf);
-      }
-      if (!wait(&sh->vote[grp], j & 1)) return false;
-      if (sh->moves[grp][g]) {
-        // A weight would pass the limit, or a row has no reference yet: the rows' maxima over the tile, new references for
-        // those rows, their sums and O scaled, the exponents again. All warps of the group come here or none.
-        const int n_min = first_row(j);
-#pragma unroll 1
-        for (int r = 0; r < my_rows; r += 8) {
-          uint32_t sr[8];
-          tmem_ld8(s_address(sb) + r, sr);
-          float mine = -INFINITY;
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float m = warp_max(row_first + r + e >= n_min ? __uint_as_float(sr[e]) : -INFINITY);
-            mine = lane == e ? m : mine;
-          }
-          if (lane < 8) sh->part[wq][row_first + r + lane] = mine;
+        for (int r = 0; r < kRowsT; r += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&sh->neg_ref[grp][row_of(r)]);
+          const float2 a = fma_f32x2(pair(s, r), sc2, make_float2(f.x, f.y));
+          const float2 b = fma_f32x2(pair(s, r + 2), sc2, make_float2(f.z, f.w));
+          s[r] = __float_as_uint(a.x);
+          s[r + 1] = __float_as_uint(a.y);
+          s[r + 2] = __float_as_uint(b.x);
+          s[r + 3] = __float_as_uint(b.y);
+          top[r / 2 % 4] = fmaxf(fmaxf(top[r / 2 % 4], a.x), a.y);
+          top[r / 2 % 4 + 1] = fmaxf(fmaxf(top[r / 2 % 4 + 1], b.x), b.y);
         }
-        if (!meet()) return false;
-        if (tg == 0) sh->moves[grp][g] = 0;
-        if (tg < my_rows) {
-          const int r = row_first + tg;
-          const float m = fmaxf(fmaxf(sh->part[0][r], sh->part[1][r]), fmaxf(sh->part[2][r], sh->part[3][r])) * q_scale;
-          const float old = sh->neg_ref[r];
+        if (again) break;
+        const bool moves = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > kLimit;
+        if (all_have && !named_any(bar, kGroup, moves || dead)) break;
+        // A row's weights would pass the limit, or a row has no reference yet: the rows' maxima over the tile, new
+        // references for those rows, their sums and O scaled, and once more. All warps of the group come here or none.
+        stop = named_any(bar, kGroup, dead);
+        if (stop) break;
+#pragma unroll
+        for (int r = 0; r < kRowsT; ++r) {
+          const float m = warp_max(__uint_as_float(s[r]));
+          if (lane == 0) sh->part[grp][wq][row_of(r)] = m;
+        }
+        named_sync(bar, kGroup);
+        const int rows = sh->geom[grp].w;
+        if (tg < rows) {
+          const float m = fmaxf(fmaxf(sh->part[grp][0][tg], sh->part[grp][1][tg]),
+                                fmaxf(sh->part[grp][2][tg], sh->part[grp][3][tg]));
           float a = 1.f;
-          if (m + old > kLimit) {
-            a = old == kNone ? 0.f : ex2_approx(kTop - m - old);
-            sh->neg_ref[r] = kTop - m;
+          if (m > (has_ref ? kLimit : -INFINITY)) {
+            const float old = -sh->neg_ref[grp][tg], ref = old + (m - kTop);
+            a = has_ref ? ex2_approx(old - ref) : 0.f;
+            sh->neg_ref[grp][tg] = -ref;
+            has_ref = true;
           }
-          sh->alpha[r] = a;
+          sh->alpha[grp][tg] = a;
         }
-        if (!meet()) return false;
-        if (j > 0) {
-          if (!wait(&sh->pv_done[g ^ 1], ((j - 1) >> 1) & 1)) return false;
+        all_have = !named_any(bar, kGroup, !has_ref);
+        if (u > 0) {
+          dead = !__all_sync(0xffffffffu, mbar_wait_tested(&sh->pv_done[grp], (u - 1) & 1, abort, p.err));
+          pv = true;
           tc_fence_after();
+          if (!dead) {
 #pragma unroll 1
-          for (int r = 0; r < my_rows; r += 8) {
-            uint32_t o[8];
-            tmem_ld8(o_at + r, o);
+            for (int r = 0; r < kRowsT; r += 4) {
+              const int row = row_of(r);
+              if (row >= rows) break;
+              uint32_t o[4];
+              tmem_ld4_async(s_at + (kColO - kColS) + row, o);
+              tmem_wait_ld(o);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * sh->alpha[row_first + r + e]);
-            tmem_st8_async(o_at + r, o);
+              for (int e = 0; e < 4; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * sh->alpha[grp][row + e]);
+              tmem_st4_async(s_at + (kColO - kColS) + row, o);
+            }
+            tmem_wait_st();
           }
-          tmem_wait_st();
 #pragma unroll
-          for (int r = 0; r < C::kRowsT; r += 2) {
-            if (r < my_rows) {
-              const float2 a = *reinterpret_cast<const float2*>(&sh->alpha[row_first + r]);
+          for (int r = 0; r < kRowsT; r += 2) {
+            if (row_of(r) < rows) {
+              const float2 a = *reinterpret_cast<const float2*>(&sh->alpha[grp][row_of(r)]);
               l[r / 2].x *= a.x;
               l[r / 2].y *= a.y;
             }
           }
         }
-        load_scores(x, sb);
-        exponents(x, n_min);
       }
+      if (stop) break;
       tc_fence_before();
-      if (lane == 0) mbar_arrive(&sh->s_free[sb]);
-      if (more) {
-        if (j % kBatch == kBatch - 1 && !wait(&sh->geo_full[(j + 1) / kBatch & 1], (j + 1) / kBatch >> 1 & 1)) return false;
-        if (!loading) {
-          if (!__all_sync(0xffffffffu, mbar_wait(&sh->s_done[next_buf], next_phase, abort, p.err))) return false;
-          load_scores(next, next_buf);
-        }
-        vote(exponents(next, first_row(j + 1)), j + 1);
-      }
-      sb = next_buf;
-      step_buf();
-      // Weights 2^x to shared memory, and their sums
-      if (j >= 2 && !wait(&sh->pv_done[g], ((j >> 1) - 1) & 1)) return false;
+      if (lane == 0) mbar_arrive(&sh->s_free[grp]);
+      // P = 2^s, and its sums
+      if (!pv) dead = !__all_sync(0xffffffffu, mbar_wait_tested(&sh->pv_done[grp], (u - 1) & 1, abort, p.err));
+      auto weigh4 = [&](int r) {                         // four rows' weights, as fp16
+        const float2 a = make_float2(ex2_approx(__uint_as_float(s[r])), ex2_approx(__uint_as_float(s[r + 1])));
+        const float2 b = make_float2(ex2_approx(__uint_as_float(s[r + 2])), ex2_approx(__uint_as_float(s[r + 3])));
+        l[r / 2] = add_f32x2(l[r / 2], a);
+        l[r / 2 + 1] = add_f32x2(l[r / 2 + 1], b);
+        return make_uint2(pack_f16(a.x, a.y), pack_f16(b.x, b.y));
+      };
+      // (eight rows are a 16-byte word of the key's; 64 rows a box)
 #pragma unroll
-      for (int r = 0; r < C::kRowsT; r += 8) {
-        if (r < my_rows) {
-          uint32_t pk[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float2 a = pair(x, r + 2 * e);
-            a.x = ex2_approx(a.x);
-            a.y = ex2_approx(a.y);
-            l[r / 2 + e] = add_f32x2(l[r / 2 + e], a);
-            pk[e] = pack_f16(a.x, a.y);
-          }
-          const int word = (row_first + r) / 8;          // 16-byte word of the key's rows: 8 words a box
-          sts_u4(prow + g * C::kPBytes + (word >> 3) * C::kBoxBytes + (((word & 7) ^ (key & 7)) << 4),
-                 make_uint4(pk[0], pk[1], pk[2], pk[3]));
-        }
+      for (int r = 0; r < 32; r += 8) {
+        const uint2 a = weigh4(r), b = weigh4(r + 4);
+        sts_u4(prow ^ (r << 2), make_uint4(a.x, a.y, b.x, b.y));
       }
-      tc_fence_before();
+      sts_u2((prow ^ (half << 4)) + C::kBoxBytes + half * 8, weigh4(32));
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->p_ready[g]);
-      return true;
-    };
-    bool ok = true;
-    if (w.nt > 0) {
-      uint32_t xa[C::kRowsT], xb[C::kRowsT];
-      ok = wait(&sh->geo_full[0], 0) && wait(&sh->s_done[0], 0);
-      if (ok) {
-        load_scores(xa, 0);
-        vote(exponents(xa, first_row(0)), 0);
-        step_buf();
-        for (int j = 0; ok && j < w.nt; j += 2) {
-          ok = tile(xa, xb, j);
-          if (ok && j + 1 < w.nt) ok = tile(xb, xa, j + 1);
-        }
+      if (lane == 0 && !dead) mbar_arrive(&sh->p_ready[grp]);
+    }
+    // ---- epilogue: the groups' sums and O merged into the split's partial (m, l, O not normalised) ----
+    const int4 gm = sh->geom[grp];
+    const unsigned b = blockIdx.z / static_cast<unsigned>(p.n_tiles);
+    if (u > 0 && !dead) dead = !__all_sync(0xffffffffu, mbar_wait(&sh->pv_done[grp], (u - 1) & 1, abort, p.err));
+#pragma unroll
+    for (int r = 0; r < kRowsT; r += 4) {
+      if (row_of(r) < gm.w) {
+        const float sum = sum_rows4(&l[r / 2], lane);
+        if (lane < 4) sh->part[grp][wq][row_of(r) + lane] = sum;
       }
     }
-    // ---- epilogue: the split's partial (m, l, O not normalised) ----
-    if (ok && w.nt > 0) ok = wait(&sh->pv_done[(w.nt - 1) & 1], ((w.nt - 1) >> 1) & 1);
+    tc_fence_before();
+    named_sync(1, kAll);
     tc_fence_after();
+    if (static_cast<int>(threadIdx.x) < gm.w) {
+      const int r = threadIdx.x;
+      float lg[2], ref[2];
 #pragma unroll
-    for (int r = 0; r < C::kRowsT; r += 8) {
-      if (r < my_rows) {
-        const float sum = sum_rows8(&l[r / 2], lane);
-        if (lane < 8) sh->part[wq][row_first + r + lane] = sum;
+      for (int g = 0; g < 2; ++g) {
+        lg[g] = (sh->part[g][0][r] + sh->part[g][1][r]) + (sh->part[g][2][r] + sh->part[g][3][r]);
+        ref[g] = lg[g] > 0.f ? -sh->neg_ref[g][r] : -INFINITY;
       }
+      const float m = fmaxf(ref[0], ref[1]);
+      float sum = 0.f;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const float wt = lg[g] > 0.f ? ex2_approx(ref[g] - m) : 0.f;
+        sum += wt * lg[g];
+        sh->alpha[g][r] = wt * p.v_scale;
+      }
+      const int rg = gm.z + r;
+      const size_t pidx = ((static_cast<size_t>(b) * p.row_tiles + rg / kMaxRows) * p.hkv + blockIdx.y) * p.num_splits + blockIdx.x;
+      reinterpret_cast<float2*>(p.part_ml)[pidx * kMaxRows + rg % kMaxRows] = make_float2(m, sum);
     }
     named_sync(1, kAll);
-    if (static_cast<int>(threadIdx.x) < w.rows) {
-      const int r = threadIdx.x;
-      const float sum = (sh->part[0][r] + sh->part[1][r]) + (sh->part[2][r] + sh->part[3][r]);
-      const int rg = w.row0 + r;
-      const size_t pidx = ((static_cast<size_t>(w.b) * p.row_tiles + rg / kMaxRows) * p.hkv + w.h) * p.num_splits + w.s;
-      reinterpret_cast<float2*>(p.part_ml)[pidx * kMaxRows + rg % kMaxRows] =
-          make_float2(sum > 0.f ? -sh->neg_ref[r] : -INFINITY, sum);
-    }
     if (w.nt > 0 && wq * 32 < HD) {
-      // lane = channel: 32 neighbouring channels of a row are one 128-byte store
+      // lane = channel: 32 neighbouring channels of a row are one 128-byte store. The warpgroups take rows of eight in turn.
 #pragma unroll 1
-      for (int r = 0; r < my_rows; r += 8) {
-        uint32_t o[8];
-        tmem_ld8(o_at + r, o);
-        const int rg = w.row0 + row_first + r;           // (a multiple of 8: the eight lie in one of the combine's tiles)
+      for (int r0 = (warp >> 2) * 8; r0 < gm.w; r0 += 32) {
+        uint32_t o0[8], o1[8];
+        tmem_ld8(lane_base + kColO + r0, o0);
+        tmem_ld8(lane_base + kColO + kN + r0, o1);
+        const int rg = gm.z + r0;                      // (a multiple of 8: the eight lie in one of the combine's tiles)
         float* dst = p.part_o +
-                     ((((static_cast<size_t>(w.b) * p.row_tiles + rg / kMaxRows) * p.hkv + w.h) * p.num_splits + w.s) * kMaxRows +
+                     ((((static_cast<size_t>(b) * p.row_tiles + rg / kMaxRows) * p.hkv + blockIdx.y) * p.num_splits + blockIdx.x) * kMaxRows +
                       rg % kMaxRows) * HD + wq * 32 + lane;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (r + e < my_rows) dst[e * HD] = __uint_as_float(o[e]) * p.v_scale;
+        for (int e = 0; e < 8; ++e) {
+          if (r0 + e < gm.w) {
+            const float w0 = sh->alpha[0][r0 + e], w1 = sh->alpha[1][r0 + e];
+            dst[e * HD] = (w0 > 0.f ? w0 * __uint_as_float(o0[e]) : 0.f) + (w1 > 0.f ? w1 * __uint_as_float(o1[e]) : 0.f);
+          }
+        }
       }
     }
   }
@@ -706,23 +649,23 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::kThreads, 1) attend_packed_kernel
   }
 }
 
-template <int HD, int NT>
-cudaError_t launch_t(const PackedAttnParams& p, int num_seqs, cudaStream_t stream) {
+template <int HD>
+cudaError_t launch_hd(const PackedAttnParams& p, int num_seqs, cudaStream_t stream) {
   static size_t done[64] = {};
   static bool registers = false;
-  auto kern = attend_packed_kernel<HD, NT>;
+  auto kern = attend_packed_kernel<HD>;
   if (!registers) {
     // The warpgroups trade registers; a kernel launched with fewer than they take up would wait for ever.
     cudaFuncAttributes a;
     const cudaError_t e = cudaFuncGetAttributes(&a, kern);
     if (e != cudaSuccess) return e;
-    if (Cfg<HD, NT>::kTrade && a.numRegs < Cfg<HD, NT>::kRegsLaunch) return cudaErrorNotSupported;
+    if (a.numRegs < kRegsLaunch) return cudaErrorNotSupported;
     registers = true;
   }
-  const cudaError_t e = ensure_smem_limit(kern, Cfg<HD, NT>::kSmemBytes, done);
+  const cudaError_t e = ensure_smem_limit(kern, Cfg<HD>::kSmemBytes, done);
   if (e != cudaSuccess) return e;
   const dim3 grid(p.num_splits, p.hkv, num_seqs * p.n_tiles);
-  return launch_pdl(kern, grid, dim3(Cfg<HD, NT>::kThreads), Cfg<HD, NT>::kSmemBytes, stream, p);
+  return launch_pdl(kern, grid, dim3(kThreads), Cfg<HD>::kSmemBytes, stream, p);
 }
 
 }  // namespace
@@ -730,9 +673,7 @@ cudaError_t launch_t(const PackedAttnParams& p, int num_seqs, cudaStream_t strea
 int packed_tile_rows() { return kMaxN; }
 
 cudaError_t launch_attend_packed(const PackedAttnParams& p, int num_seqs, cudaStream_t stream) {
-  if (p.tile_rows <= kFewN)
-    return p.head_dim == 128 ? launch_t<128, kFewN>(p, num_seqs, stream) : launch_t<64, kFewN>(p, num_seqs, stream);
-  return p.head_dim == 128 ? launch_t<128, kMaxN>(p, num_seqs, stream) : launch_t<64, kMaxN>(p, num_seqs, stream);
+  return p.head_dim == 128 ? launch_hd<128>(p, num_seqs, stream) : launch_hd<64>(p, num_seqs, stream);
 }
 
 }  // namespace vfy
