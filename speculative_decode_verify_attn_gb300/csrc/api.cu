@@ -95,6 +95,7 @@ struct DeviceGuard {
 
 // Largest vocabulary of the calls that step over it in whole segments (32-bit indices do not wrap).
 constexpr int kMaxVocab = 1 << 30;
+constexpr long long kSampleCtas = 4;    // CTAs per SM of the sampled acceptance's row statistics
 
 int ceil_div(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
 
@@ -190,7 +191,7 @@ vfy_status vfy_create(const vfy_config* cfg_in, int device, vfy_ctx** out) {
             cudaMalloc(&ctx->accept_counter, sizeof(unsigned int)) == cudaSuccess &&
             cudaMalloc(&ctx->tree_counters, cfg.max_seqs * sizeof(unsigned int)) == cudaSuccess &&
             cudaMalloc(&ctx->tree_pieces, ctx->num_sms * sizeof(vfy::TreePiece)) == cudaSuccess &&
-            cudaMalloc(&ctx->sample_stats, (ctx->accept_rows_cap + 2 * ctx->num_sms) * sizeof(float4)) == cudaSuccess &&
+            cudaMalloc(&ctx->sample_stats, (ctx->accept_rows_cap + kSampleCtas * ctx->num_sms) * sizeof(float4)) == cudaSuccess &&
             cudaMalloc(&ctx->sample_keys, 3 * cfg.max_seqs * sizeof(unsigned long long)) == cudaSuccess &&
             cudaMalloc(&ctx->sample_counters, cfg.max_seqs * sizeof(unsigned int)) == cudaSuccess &&
             cudaMalloc(&ctx->err, sizeof(int)) == cudaSuccess;
@@ -973,6 +974,8 @@ static bool rope_params(const vfy_ctx* ctx, const vfy_rotary* r, const uint16_t*
   p->num_seqs = num_seqs;
   p->max_q = c.max_queries_per_seq;
   p->token_cap = num_seqs * c.max_queries_per_seq;
+  // One token a CTA while all of them run at once, else one a warp.
+  p->tokens_per_cta = p->token_cap <= 4 * ctx->num_sms ? 1 : vfy::rope_cta_tokens();
   p->hq = c.num_q_heads;
   p->hkv = c.num_kv_heads;
   p->head_dim = c.head_dim;
@@ -1284,11 +1287,13 @@ vfy_status vfy_accept_sampled(vfy_ctx* ctx, const void* logits, int logits_type,
   p.cu_rows = cu_rows;
   p.num_seqs = num_seqs;
   p.max_rows = max_rows;
-  // As in vfy_accept: about two CTAs per SM over all rows, segments of at least 1024 entries (of whole 16-byte words).
-  p.parts = clampi(ceil_div(2LL * ctx->num_sms, max_rows), 1, ceil_div(vocab, 1024));
+  // Segments of whole 16-byte words, at least 4096 entries (one round of loads of a CTA), at most 32 of a row (a warp merges
+  // them), and no more than run at once, four CTAs per SM, over all rows.
+  p.parts = clampi(ceil_div(kSampleCtas * ctx->num_sms, max_rows), 1, std::min(32, ceil_div(vocab, 4096)));
   p.seg = (ceil_div(vocab, p.parts) + 7) & ~7;
   p.parts = ceil_div(vocab, p.seg);
-  p.draw_parts = clampi(ceil_div(2LL * ctx->num_sms, num_seqs), 1, ceil_div(vocab, 1024));
+  // The draw: at least one round of loads of a CTA, and no more than run at once, two CTAs per SM over the sequences.
+  p.draw_parts = clampi(static_cast<int>(2LL * ctx->num_sms / num_seqs), 1, ceil_div(vocab, 2048));
   p.draw_seg = ceil_div(vocab, p.draw_parts);
   p.draw_parts = ceil_div(vocab, p.draw_seg);
   p.accepted_len = accepted_len;

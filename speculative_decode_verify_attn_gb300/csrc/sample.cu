@@ -18,11 +18,14 @@
 namespace vfy {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;             // of the first kernel
 constexpr int kWarps = kThreads / 32;
+constexpr int kDrawThreads = 512;         // of the second
+constexpr int kDrawWarps = kDrawThreads / 32;
 
-// log2(e) / T in two pieces. A tiny T is held at 2^-100: any two different logits are then further apart than fp32 can
-// weigh. T = 0 (or one that is no temperature, which is reported) is greedy: 0.
+// log2(e) / T in two pieces (the rest of a division is exact in one fma; fp64, 1/64 of fp32's rate here, cost 2 us a CTA).
+// A tiny T is held at 2^-100: any two different logits are then further apart than fp32 can weigh. T = 0 (or one that is no
+// temperature, which is reported) is greedy: 0.
 struct Heat {
   float hi, lo;
 };
@@ -30,9 +33,11 @@ __device__ __forceinline__ bool is_temperature(float t) { return t >= 0.f && t <
 __device__ __forceinline__ Heat heat_of(float t) {
   Heat h = {0.f, 0.f};
   if (is_temperature(t) && t > 0.f) {
-    const double c = 1.4426950408889634 / static_cast<double>(fmaxf(t, 7.9e-31f));
-    h.hi = static_cast<float>(c);
-    h.lo = static_cast<float>(c - static_cast<double>(h.hi));
+    constexpr double kLog2e = 1.4426950408889634;
+    constexpr float kHi = static_cast<float>(kLog2e), kLo = static_cast<float>(kLog2e - static_cast<double>(kHi));
+    t = fmaxf(t, 7.9e-31f);
+    h.hi = kHi / t;
+    h.lo = (fmaf(-h.hi, t, kHi) + kLo) / t;
   }
   return h;
 }
@@ -47,6 +52,21 @@ __device__ __forceinline__ const void* row_at(const SampleParams& p, int row) {
   return static_cast<const char*>(p.logits) + static_cast<long long>(row) * p.stride * (BF16 ? 2 : 4);
 }
 
+// f(x, index) of every entry of a 16-byte word.
+template <bool BF16, typename F>
+__device__ __forceinline__ void each(const uint4& w, F f) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (BF16) {
+      f(__uint_as_float(u[i] << 16), 2 * i);
+      f(__uint_as_float(u[i] & 0xffff0000u), 2 * i + 1);
+    } else {
+      f(__uint_as_float(u[i]), i);
+    }
+  }
+}
+
 // 2^((a - top) c) where a <= top: the weight of a part whose maximum is a.
 __device__ __forceinline__ float rescale(float a, float top, float c) {
   return a == top ? 1.f : ex2_approx((a - top) * c);
@@ -55,35 +75,42 @@ __device__ __forceinline__ float rescale(float a, float top, float c) {
 // Maximum and sum of exponentials of some entries of a row.
 struct Stat {
   float m, z;
-  __device__ __forceinline__ void merge(const Stat& o, float c) {
-    const float top = fmaxf(m, o.m);
-    z = z * rescale(m, top, c) + o.z * rescale(o.m, top, c);
+  // Over the lanes of a converged warp; all of them get it.
+  __device__ __forceinline__ void merge_lanes(float c) {
+    const float top = warp_max(m);
+    z *= rescale(m, top, c);
     m = top;
-  }
-  template <int N>
-  __device__ __forceinline__ void add(const float (&x)[N], float c) {
-    float top = x[0];
 #pragma unroll
-    for (int e = 1; e < N; ++e) top = fmaxf(top, x[e]);
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+  }
+  // Entries of at most `top`, the largest of them; any(f) calls f(x) for each.
+  template <typename Any>
+  __device__ __forceinline__ void add(float top, float c, Any any) {
     if (top > m) {
       z *= rescale(m, top, c);
       m = top;
     }
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    int e = 0;
     if (m == INFINITY) {                  // +inf entries share the row
-#pragma unroll
-      for (int e = 0; e < N; ++e) z += x[e] == INFINITY ? 1.f : 0.f;
+      any([&](float x) { s[e++ & 3] += x == INFINITY ? 1.f : 0.f; });
     } else if (m != -INFINITY) {
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int e = 0; e < N; ++e) s[e & 3] += ex2_approx((x[e] - m) * c);
-      z += (s[0] + s[1]) + (s[2] + s[3]);
+      any([&](float x) { s[e++ & 3] += ex2_approx((x - m) * c); });
     }
+    z += (s[0] + s[1]) + (s[2] + s[3]);
   }
 };
 
+// The largest of 32 keys, in all lanes.
+__device__ __forceinline__ unsigned long long warp_umax64(unsigned long long key) {
+  const uint32_t hi = static_cast<uint32_t>(key >> 32), top = __reduce_max_sync(0xffffffffu, hi);
+  const uint32_t lo = __reduce_max_sync(0xffffffffu, hi == top ? static_cast<uint32_t>(key) : 0u);
+  return static_cast<unsigned long long>(top) << 32 | lo;
+}
+
 // ------------------------------ row statistics ----------------------------------------------
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) sample_stats_kernel(const SampleParams p) {
+__global__ void __launch_bounds__(kThreads, 4) sample_stats_kernel(const SampleParams p) {
   constexpr int kVec = BF16 ? 8 : 4;      // entries of a 16-byte word
   constexpr int kUnroll = 4;
   __shared__ Stat s_stat[kWarps];
@@ -93,10 +120,21 @@ __global__ void __launch_bounds__(kThreads) sample_stats_kernel(const SamplePara
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row = blockIdx.y;
-  const int total = p.cu_rows[p.num_seqs];
-  if (row >= total) return;
-  const int b = sequence_of(p.cu_rows, p.num_seqs, row, lane);
-  const float c = heat_of(p.temperature[b]).hi;
+  int total;
+  float temperature;
+  if (p.num_seqs <= 32) {                 // the row's sequence and its temperature in one round trip
+    const int end = lane < p.num_seqs ? p.cu_rows[lane + 1] : INT_MAX;
+    const float mine = lane < p.num_seqs ? p.temperature[lane] : 0.f;
+    total = __shfl_sync(0xffffffffu, end, p.num_seqs - 1);
+    const int b = min(__popc(__ballot_sync(0xffffffffu, end <= row)), p.num_seqs - 1);
+    temperature = __shfl_sync(0xffffffffu, mine, b);
+    if (row >= total) return;
+  } else {
+    total = p.cu_rows[p.num_seqs];
+    if (row >= total) return;
+    temperature = p.temperature[sequence_of(p.cu_rows, p.num_seqs, row, lane)];
+  }
+  const float c = heat_of(temperature).hi;
   const int v0 = blockIdx.x * p.seg, v1 = min(p.vocab, v0 + p.seg);
   const void* src = row_at<BF16>(p, row);
   // entries before the first whole 16-byte word, whole words, entries behind the last
@@ -108,89 +146,79 @@ __global__ void __launch_bounds__(kThreads) sample_stats_kernel(const SamplePara
   const uint4* body = reinterpret_cast<const uint4*>(at + head * (BF16 ? 2 : 4));
   Stat st = {-INFINITY, 0.f};
   unsigned long long key = 0ull;
-  for (int i0 = threadIdx.x; i0 < words; i0 += kThreads * kUnroll) {
-    float x[kUnroll * kVec];
+  constexpr uint32_t kNone = BF16 ? 0xff80ff80u : 0xff800000u;   // -inf
+  auto load = [&](int i0, uint4 (&w)[kUnroll]) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int i = i0 + u * kThreads;
-      const uint32_t none = BF16 ? 0xff80ff80u : 0xff800000u;
-      const uint4 w = i < words ? __ldg(body + i) : make_uint4(none, none, none, none);
-      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if constexpr (BF16) {
-          x[u * 8 + 2 * e] = __uint_as_float(ws[e] << 16);
-          x[u * 8 + 2 * e + 1] = __uint_as_float(ws[e] & 0xffff0000u);
-        } else {
-          x[u * 4 + e] = __uint_as_float(ws[e]);
-        }
-      }
+      w[u] = i < words ? __ldg(body + i) : make_uint4(kNone, kNone, kNone, kNone);
     }
-    if (c > 0.f) {
+  };
+  uint4 next[kUnroll];
+  load(threadIdx.x, next);
+  for (int i0 = threadIdx.x; i0 < words; i0 += kThreads * kUnroll) {
+    uint4 w[kUnroll];
 #pragma unroll
-      for (int e = 0; e < kUnroll * kVec; ++e) x[e] = fmaxf(x[e], -INFINITY);   // NaN -> -inf
-      st.add(x, c);
+    for (int u = 0; u < kUnroll; ++u) w[u] = next[u];
+    load(i0 + kThreads * kUnroll, next);  // (the next round's, while this one is summed)
+    auto any = [&](auto f) {              // every entry; NaN -> -inf
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) each<BF16>(w[u], [&](float x, int) { f(fmaxf(x, -INFINITY)); });
+    };
+    if (c > 0.f) {
+      float top = -INFINITY;
+      any([&](float x) { top = fmaxf(top, x); });
+      st.add(top, c, any);
     } else {
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-        for (int e = 0; e < kVec; ++e)
-          if (i0 + u * kThreads < words)
-            key = umax64(key, pack(x[u * kVec + e], v0 + head + (i0 + u * kThreads) * kVec + e));
+      for (int u = 0; u < kUnroll; ++u) {
+        const int i = i0 + u * kThreads;
+        if (i < words) each<BF16>(w[u], [&](float x, int e) { key = umax64(key, pack(x, v0 + head + i * kVec + e)); });
+      }
     }
   }
   // (fewer than kVec entries on each side)
   if (threadIdx.x < 2 * kVec) {
     const int v = threadIdx.x < kVec ? v0 + static_cast<int>(threadIdx.x) : tail + static_cast<int>(threadIdx.x) - kVec;
     if (threadIdx.x < kVec ? v < v0 + head : v < v1) {
-      const float x[1] = {entry<BF16>(src, v)};
-      if (c > 0.f) {
-        const float y[1] = {fmaxf(x[0], -INFINITY)};
-        st.add(y, c);
-      } else {
-        key = umax64(key, pack(x[0], v));
-      }
+      const float x = entry<BF16>(src, v);
+      if (c > 0.f)
+        st.add(fmaxf(x, -INFINITY), c, [&](auto f) { f(fmaxf(x, -INFINITY)); });
+      else
+        key = umax64(key, pack(x, v));
     }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const Stat other = {__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.z, o)};
-    st.merge(other, c);
-    key = umax64(key, __shfl_xor_sync(0xffffffffu, key, o));
-  }
+  if (c > 0.f)
+    st.merge_lanes(c);
+  else
+    key = warp_umax64(key);
   if (lane == 0) {
     s_stat[warp] = st;
     s_key[warp] = key;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kWarps; ++w) {
-      st.merge(s_stat[w], c);
-      key = umax64(key, s_key[w]);
+  if (warp == 0) {
+    st.m = -INFINITY;
+    st.z = 0.f;
+    key = 0ull;
+    if (lane < kWarps) {
+      st = s_stat[lane];
+      key = s_key[lane];
     }
-    p.stats[static_cast<size_t>(row) * p.parts + blockIdx.x] =
-        make_float4(st.m, st.z, __uint_as_float(static_cast<uint32_t>(key >> 32)), __uint_as_float(static_cast<uint32_t>(key)));
+    st.merge_lanes(c);
+    key = warp_umax64(key);
+    if (lane == 0)
+      p.stats[static_cast<size_t>(row) * p.parts + blockIdx.x] =
+          make_float4(st.m, st.z, __uint_as_float(static_cast<uint32_t>(key >> 32)), __uint_as_float(static_cast<uint32_t>(key)));
   }
 }
 
 // ------------------------------ acceptance and draw ------------------------------------------
-// A whole row's statistics, merged by a converged warp (all lanes get them).
-__device__ __forceinline__ Stat row_stat(const SampleParams& p, int row, float c, int lane, unsigned long long* key) {
-  Stat st = {-INFINITY, 0.f};
-  unsigned long long k = 0ull;
-  for (int i = lane; i < p.parts; i += 32) {
-    const float4 f = p.stats[static_cast<size_t>(row) * p.parts + i];
-    const Stat part = {f.x, f.y};
-    st.merge(part, c);
-    k = umax64(k, (static_cast<unsigned long long>(__float_as_uint(f.z)) << 32) | __float_as_uint(f.w));
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const Stat other = {__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.z, o)};
-    st.merge(other, c);
-    k = umax64(k, __shfl_xor_sync(0xffffffffu, k, o));
-  }
-  *key = k;
+// A whole row's statistics from its parts, one a lane (all lanes get them).
+__device__ __forceinline__ Stat row_stat(const float4& f, float c, unsigned long long* key) {
+  Stat st = {f.x, f.y};
+  st.merge_lanes(c);
+  *key = warp_umax64((static_cast<unsigned long long>(__float_as_uint(f.z)) << 32) | __float_as_uint(f.w));
   return st;
 }
 
@@ -208,18 +236,38 @@ __device__ __forceinline__ float weight(float x, float m, const Heat& c) {
   return ex2_approx(f) * __int_as_float((static_cast<int>(j) + 127) << 23);
 }
 
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleParams p) {
+__global__ void __launch_bounds__(kDrawThreads) sample_draw_kernel(const SampleParams p) {
   constexpr int kUnroll = 4;
   __shared__ int s_first;
-  __shared__ unsigned long long s_keys[3][kWarps];
+  __shared__ Stat s_stat;
+  __shared__ unsigned long long s_greedy;
+  __shared__ unsigned long long s_keys[3][kDrawWarps];
   __shared__ bool s_last;
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = blockIdx.y;
-  // Inputs of the callers' (complete since the first kernel let this one start), of a warp's first row.
+  // Inputs of the callers' (complete since the first kernel let this one start): the first drafts of a warp, and the noise of
+  // a thread's first tokens.
   const int r0 = p.cu_rows[b], r1 = p.cu_rows[b + 1], total = p.cu_rows[p.num_seqs];
   const float temperature = p.temperature[b];
+  const float* noise = p.noise + static_cast<size_t>(b) * p.vocab;
+  const int v0 = blockIdx.x * p.draw_seg, v1 = min(p.vocab, v0 + p.draw_seg);
+  float es[kUnroll];
+  auto load_noise = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const int v = i0 + k * kDrawThreads;
+      es[k] = v < v1 ? noise[v] : 0.f;
+    }
+  };
+  load_noise(v0 + threadIdx.x);
   const int depth = r1 - r0 - 1;
   const int d0 = r0 - b;                  // drafts of the sequence (every sequence before it has a row)
   const bool bad = d0 < 0 || depth < 0 || r1 > min(total, p.max_rows);
@@ -233,6 +281,16 @@ __global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleParam
     x = known ? entry<BF16>(row_at<BF16>(p, r0 + j), token) : -INFINITY;
   };
   if (!bad && warp < depth) load_draft(warp);
+  float xs[kUnroll];
+  auto load_logits = [&](int n, int i0) {
+    const void* src = row_at<BF16>(p, r0 + n);
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const int v = i0 + k * kDrawThreads;
+      xs[k] = v < v1 ? fmaxf(entry<BF16>(src, v), -INFINITY) : -INFINITY;
+    }
+  };
+  if (!bad && depth == 0) load_logits(0, v0 + threadIdx.x);   // nothing to accept: this is the row to draw from
   if (threadIdx.x == 0) s_first = depth;
   pdl_wait();
   if (bad || (blockIdx.x == 0 && !is_temperature(temperature))) {
@@ -241,77 +299,106 @@ __global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleParam
   }
   __syncthreads();
   const Heat c = heat_of(temperature);
-  for (int j = warp; j < depth; j += kWarps) {
-    if (j != warp) load_draft(j);
-    unsigned long long key;
-    const Stat st = row_stat(p, r0 + j, c.hi, lane, &key);
+  // A warp takes every sixteenth row (the one behind the drafts among them) and stops at its first refusal: the statistics
+  // that it then holds are the row's to draw from, if no other warp stops before.
+  auto load_parts = [&](int j) {
+    return j <= depth && lane < p.parts ? p.stats[static_cast<size_t>(r0 + j) * p.parts + lane]
+                                        : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+  };
+  Stat st = {-INFINITY, 0.f};
+  unsigned long long greedy = 0ull;
+  int j = warp;
+  float4 part = load_parts(j);
+  for (; j <= depth; j += kDrawWarps) {
+    const float4 next = load_parts(j + kDrawWarps);
+    if (j != warp && j < depth) load_draft(j);
+    st = row_stat(part, c.hi, &greedy);
+    part = next;
+    if (j == depth) break;
     const bool known = token >= 0 && token < p.vocab;
     if (!known && lane == 0 && blockIdx.x == 0) atomicOr(p.err, kErrDeviceInput);
     float prob;
     if (c.hi > 0.f)
       prob = st.z > 0.f ? weight(fmaxf(x, -INFINITY), st.m, c) / st.z : 0.f;
     else
-      prob = token == unpack_index(key) ? 1.f : 0.f;
-    const bool stays = known && static_cast<double>(u) * static_cast<double>(q) < static_cast<double>(prob);
-    if (!stays && lane == 0) atomicMin(&s_first, j);
+      prob = token == unpack_index(greedy) ? 1.f : 0.f;
+    // u q < prob exactly: where the rounded product equals prob, fp64 holds the whole one.
+    const float uq = u * q;
+    const bool stays =
+        known && (uq < prob || (uq == prob && static_cast<double>(u) * static_cast<double>(q) < static_cast<double>(prob)));
+    if (!stays) {
+      if (lane == 0) atomicMin(&s_first, j);
+      break;
+    }
   }
   __syncthreads();
-  const int n = s_first, row = r0 + n;
-  unsigned long long greedy;
-  const Stat st = row_stat(p, row, c.hi, lane, &greedy);
+  const int n = s_first;
+  if (j == n && lane == 0) {
+    s_stat = st;
+    s_greedy = greedy;
+  }
+  __syncthreads();
+  st = s_stat;
+  greedy = s_greedy;
 
   int bonus = 0;
   if (c.hi > 0.f) {
-    const int refused = n < depth ? p.drafts[d0 + n] : -1;
-    const float* qs = n < depth && p.probs != nullptr && refused >= 0 && refused < p.vocab
-                          ? p.probs + static_cast<size_t>(d0 + n) * p.vocab
-                          : nullptr;
-    const void* src = row_at<BF16>(p, row);
-    const float* noise = p.noise + static_cast<size_t>(b) * p.vocab;
-    const int v0 = blockIdx.x * p.draw_seg, v1 = min(p.vocab, v0 + p.draw_seg);
+    const bool refused = n < depth;
+    const int draft = refused ? p.drafts[d0 + n] : -1;
+    const float* qs =
+        refused && p.probs != nullptr && draft >= 0 && draft < p.vocab ? p.probs + static_cast<size_t>(d0 + n) * p.vocab : nullptr;
     const float inv_z = st.z > 0.f ? 1.f / st.z : 0.f;
-    // The best of w, of p and of the logits, each with its first index.
+    // The best of w (where a draft was refused), of p and of the logits, each with its first index.
     float best[3] = {0.f, 0.f, -INFINITY};
     int index[3] = {-1, -1, -1};
-    for (int i0 = v0 + threadIdx.x; i0 < v1; i0 += kThreads * kUnroll) {
-      float xs[kUnroll], es[kUnroll], ps[kUnroll];
+    for (int i0 = v0 + threadIdx.x; i0 < v1; i0 += kDrawThreads * kUnroll) {
+      const bool first = i0 < v0 + kDrawThreads * kUnroll;
+      if (!first) load_noise(i0);
+      if (!first || depth != 0) load_logits(n, i0);
+      float ps[kUnroll];
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) {
-        const int v = i0 + k * kThreads;
+        const int v = i0 + k * kDrawThreads;
         const bool in = v < v1;
-        xs[k] = in ? fmaxf(entry<BF16>(src, v), -INFINITY) : -INFINITY;
-        es[k] = in ? noise[v] : 0.f;
-        ps[k] = in && qs != nullptr ? qs[v] : (v == refused ? 1.f : 0.f);
+        ps[k] = in && qs != nullptr ? qs[v] : (v == draft ? 1.f : 0.f);
       }
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) {
-        const int v = i0 + k * kThreads;
-        const float prob = weight(xs[k], st.m, c) * inv_z;
-        const bool drawn = es[k] > 0.f && es[k] < INFINITY;
-        const float race = drawn ? prob / es[k] : 0.f;
-        const float left = drawn ? fmaxf(prob - ps[k], 0.f) / es[k] : 0.f;
-        if (left > best[0]) best[0] = left, index[0] = v;
+        const int v = i0 + k * kDrawThreads;
+        const float prob = weight(xs[k], st.m, c) * inv_z, rest = fmaxf(prob - ps[k], 0.f);
+        // (a factor to 2^-23 in place of two divisions, where it is no denormal)
+        float race = 0.f, left = 0.f;
+        if (es[k] > 1e-36f && es[k] < 1e36f) {
+          const float r = rcp_approx(es[k]);
+          race = prob * r;
+          left = rest * r;
+        } else if (es[k] > 0.f && es[k] < INFINITY) {
+          race = prob / es[k];
+          left = rest / es[k];
+        }
+        if (refused && left > best[0]) best[0] = left, index[0] = v;
         if (race > best[1]) best[1] = race, index[1] = v;
         if (xs[k] > best[2]) best[2] = xs[k], index[2] = v;
       }
     }
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-      unsigned long long key = index[k] >= 0 ? pack(best[k], index[k]) : 0ull;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) key = umax64(key, __shfl_xor_sync(0xffffffffu, key, o));
+      const unsigned long long key = warp_umax64(index[k] >= 0 ? pack(best[k], index[k]) : 0ull);
       if (lane == 0) s_keys[k][warp] = key;
     }
     __syncthreads();
+    if (warp < 3) {
+      const unsigned long long key = warp_umax64(lane < kDrawWarps ? s_keys[warp][lane] : 0ull);
+      if (lane == 0 && key != 0ull) atomicMax(p.keys + 3 * b + warp, key);
+    }
+    __syncthreads();
     if (threadIdx.x == 0) {
-      for (int k = 0; k < 3; ++k) {
-        unsigned long long key = s_keys[k][0];
-        for (int w = 1; w < kWarps; ++w) key = umax64(key, s_keys[k][w]);
-        if (key != 0ull) atomicMax(p.keys + 3 * b + k, key);
-      }
-      // (the add releases this CTA's keys; the finishing CTA acquires)
+      // (the barrier orders the warps' keys before this add, which releases them; the finishing CTA acquires)
       unsigned int ticket;
-      asm volatile("atom.add.release.gpu.global.u32 %0, [%1], 1;" : "=r"(ticket) : "l"(p.counters + b) : "memory");
+      asm volatile("fence.acq_rel.gpu;\n\tatom.add.relaxed.gpu.global.u32 %0, [%1], 1;"
+                   : "=r"(ticket)
+                   : "l"(p.counters + b)
+                   : "memory");
       s_last = ticket == gridDim.x - 1;
     }
     __syncthreads();
@@ -330,7 +417,7 @@ __global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleParam
     if (blockIdx.x != 0) return;
     bonus = unpack_index(greedy);
   }
-  for (int j = threadIdx.x; j <= depth; j += kThreads)
+  for (int j = threadIdx.x; j <= depth; j += kDrawThreads)
     p.committed[r0 + j] = j < n ? p.drafts[d0 + j] : (j == n ? bonus : -1);
   if (threadIdx.x == 0) {
     p.accepted_len[b] = n;
@@ -342,7 +429,7 @@ template <bool BF16>
 cudaError_t launch_typed(const SampleParams& p, cudaStream_t stream) {
   const cudaError_t e = launch_pdl(sample_stats_kernel<BF16>, dim3(p.parts, p.max_rows), dim3(kThreads), 0, stream, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(sample_draw_kernel<BF16>, dim3(p.draw_parts, p.num_seqs), dim3(kThreads), 0, stream, p);
+  return launch_pdl(sample_draw_kernel<BF16>, dim3(p.draw_parts, p.num_seqs), dim3(kDrawThreads), 0, stream, p);
 }
 
 }  // namespace

@@ -304,6 +304,7 @@ struct RopeParams {
   int num_seqs;
   int max_q;
   int token_cap;              // host bound on cu_q[B]: the grid
+  int tokens_per_cta;         // 1 .. rope_cta_tokens()
   int hq, hkv, head_dim;
   uint16_t* q_out;            // [T][Hq][d]
   uint16_t* k_dst;            // rows [T][Hkv][d], pool or ring
@@ -321,6 +322,7 @@ struct RopeParams {
   int* err;
 };
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream);
+int rope_cta_tokens();
 
 // ------------------------------ 4-bit chunks --------------------------------------------------
 struct PackedAppendParams {
