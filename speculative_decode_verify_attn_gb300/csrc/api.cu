@@ -1097,6 +1097,7 @@ vfy_status vfy_append_full_packed(vfy_ctx* ctx, const uint16_t* k_new, const uin
   p.num_slots = num_slots;
   p.k_pool = k_pool;
   p.v_pool = v_pool;
+  p.num_sms = ctx->num_sms;
   p.k_scale = k_scale;
   p.v_scale = v_scale;
   p.err = ctx->err;

@@ -17,81 +17,134 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Group job of token t: K then V, KV heads, groups of a head. Threads of a token are neighbours, and d / 16 is even: the
-// two groups of a 16-byte code word are a lane and the next.
+// Jobs of a token: K then V, KV heads, groups of a head; a CTA takes as many whole tokens as it has threads for, and goes
+// from tokens to tokens, the next ones' values on their way while these are packed: three CTAs an SM (8 x 1024 tokens of 4 KV
+// heads of 128 take 13.4 us; a CTA for every few tokens 4 us more). Threads of a token are neighbours, and
+// d / 16 is a multiple of 4: the two groups of a 16-byte code word are a lane and the next, and four lanes have four
+// neighbouring scales.
+__host__ __device__ __forceinline__ int jobs_of(int hkv, int head_dim) { return 2 * hkv * (head_dim / 16); }
+__host__ __device__ __forceinline__ int cta_tokens(int jobs) { return jobs < kThreads ? kThreads / jobs : 1; }
+__host__ __device__ __forceinline__ int job_rounds(int jobs) { return (jobs + kThreads - 1) / kThreads; }
+
+// One thread's job: its values, and where their codes go.
+struct AppendJob {
+  bool live;
+  int job, row, slot;
+  long long chunk;
+  uint4 lo, hi;
+};
+
 template <int HD>
-__global__ void __launch_bounds__(kThreads) append_packed_kernel(const PackedAppendParams p) {
+__global__ void __launch_bounds__(kThreads, 3) append_packed_kernel(const PackedAppendParams p) {
   constexpr int kGroups = HD / 16;
   pdl_launch_dependents();
   pdl_wait();
-  const unsigned per_token = 2u * p.hkv * kGroups;
-  const unsigned long long at = static_cast<unsigned long long>(blockIdx.x) * kThreads + threadIdx.x;
-  const unsigned long long tok = at / per_token;
-  const unsigned job = static_cast<unsigned>(at - tok * per_token);
-  const int total = p.cu_q[p.num_seqs];
-  bool live = tok < static_cast<unsigned long long>(p.token_cap) && static_cast<int>(tok) < total;
-  const int t = live ? static_cast<int>(tok) : 0;
-  int lo = 0, hi = p.num_seqs - 1;                        // the last sequence that starts at or before t
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (p.cu_q[mid] <= t) lo = mid; else hi = mid - 1;
+  const int lane = threadIdx.x & 31;
+  const int jobs = jobs_of(p.hkv, HD), tokens = cta_tokens(jobs), rounds = job_rounds(jobs), per_side = p.hkv * kGroups;
+  const int sub = tokens > 1 ? static_cast<int>(threadIdx.x) / jobs : 0, job0 = static_cast<int>(threadIdx.x) - sub * jobs;
+  // Up to 32 sequences are looked up by a lane each, in one round trip.
+  const bool few = p.num_seqs <= 32;
+  int lo = 0, hi = INT_MAX, len = 0, from = 0;
+  if (few && lane < p.num_seqs) {
+    lo = p.cu_q[lane];
+    hi = p.cu_q[lane + 1];
+    len = p.seq_len[lane];
+    from = p.cu_chunks[lane];
   }
-  const int b = lo;
-  const int q0 = p.cu_q[b], nq = p.cu_q[b + 1] - q0, L = p.seq_len[b];
-  const int i = t - q0;
-  bool bad = q0 < 0 || nq < 1 || nq > p.max_q || L < nq || i < 0 || i >= nq || q0 > p.token_cap - nq;
-  const long long pos = static_cast<long long>(L) - nq + i;
-  long long chunk = 0;
-  if (live && !bad) {
-    chunk = static_cast<long long>(p.cu_chunks[b]) + pos / kChunk;
-    bad = chunk < 0 || chunk >= p.num_host_chunks;
-  }
-  if (live && bad && job == 0) atomicOr(p.err, kErrDeviceInput);
-  live = live && !bad;
+  const int total = min(few ? __shfl_sync(0xffffffffu, hi, p.num_seqs - 1) : p.cu_q[p.num_seqs], p.token_cap);
 
-  const unsigned per_head = kGroups, per_side = p.hkv * kGroups;
-  const bool is_v = job >= per_side;
-  const unsigned in_side = is_v ? job - per_side : job;
-  const int h = static_cast<int>(in_side / per_head), g = static_cast<int>(in_side % per_head);
-  uint2 codes = make_uint2(0u, 0u);
-  uint32_t scale = 0u;
-  if (live) {
-    const uint4* src = reinterpret_cast<const uint4*>((is_v ? p.v_new : p.k_new) +
-                                                      (static_cast<size_t>(t) * p.hkv + h) * HD + g * 16);
-    const uint4 lo4 = src[0], hi4 = src[1];
-    const uint32_t w[8] = {lo4.x, lo4.y, lo4.z, lo4.w, hi4.x, hi4.y, hi4.z, hi4.w};
-    float x[16];
-    const float gs = is_v ? p.v_scale : p.k_scale;
+  // Item `at`: `rounds` items for every `tokens` tokens.
+  auto load = [&](long long at) {
+    AppendJob a = {};
+    const long long group = rounds > 1 ? at / rounds : at;
+    a.job = job0 + static_cast<int>(at - group * rounds) * kThreads;
+    const int t = static_cast<int>(min(group * tokens + sub, static_cast<long long>(total)));
+    int q0, q1, L, first_chunk, b = 0;                      // its sequence, the last that starts at or before it
+    if (few) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x[2 * e] = __fdiv_rn(__uint_as_float(w[e] << 16), gs);
-      x[2 * e + 1] = __fdiv_rn(__uint_as_float(w[e] & 0xffff0000u), gs);
+      for (int step = 16; step > 0; step >>= 1) {
+        const int start = __shfl_sync(0xffffffffu, lo, (b + step) & 31);
+        if (b + step < p.num_seqs && start <= t) b += step;
+      }
+      q0 = __shfl_sync(0xffffffffu, lo, b);
+      q1 = __shfl_sync(0xffffffffu, hi, b);
+      L = __shfl_sync(0xffffffffu, len, b);
+      first_chunk = __shfl_sync(0xffffffffu, from, b);
+    } else {
+      int last = p.num_seqs - 1;
+      while (b < last) {
+        const int mid = (b + last + 1) >> 1;
+        if (p.cu_q[mid] <= t) b = mid; else last = mid - 1;
+      }
+      q0 = p.cu_q[b];
+      q1 = p.cu_q[b + 1];
+      L = p.seq_len[b];
+      first_chunk = p.cu_chunks[b];
     }
-    codes = pack_group(x, &scale);
-  }
-  // A pair of lanes holds a 16-byte word of codes; the even one writes it. (Lanes of one token: d / 16 is even.)
-  const uint32_t ox = __shfl_xor_sync(0xffffffffu, codes.x, 1), oy = __shfl_xor_sync(0xffffffffu, codes.y, 1);
-  // Four lanes hold four neighbouring scale bytes; the first writes them. (d / 16 is a multiple of 4.)
-  uint32_t scales = scale << (8 * (g & 3));
-  scales |= __shfl_xor_sync(0xffffffffu, scales, 1);
-  scales |= __shfl_xor_sync(0xffffffffu, scales, 2);
-  if (!live) return;
-  const int row = static_cast<int>(pos % kChunk);
-  const size_t word = (static_cast<size_t>(g / 2) * kChunk + row) * 16;
-  const size_t scale_at = static_cast<size_t>(kChunk) * (HD / 2) + static_cast<size_t>(row) * kGroups + (g & ~3);
-  const int slot = p.slot_of_chunk[chunk];
-  uint8_t* store = (is_v ? p.host_v : p.host_k) + (static_cast<size_t>(chunk) * p.hkv + h) * kPackedBytes<HD>;
-  uint8_t* pool = slot >= 0 && slot < p.num_slots
-                      ? (is_v ? p.v_pool : p.k_pool) + (static_cast<size_t>(slot) * p.hkv + h) * kPackedBytes<HD>
-                      : nullptr;
-  if ((g & 1) == 0) {
-    const uint4 v = make_uint4(codes.x, codes.y, ox, oy);
-    *reinterpret_cast<uint4*>(store + word) = v;
-    if (pool != nullptr) *reinterpret_cast<uint4*>(pool + word) = v;
-  }
-  if ((g & 3) == 0) {
-    *reinterpret_cast<uint32_t*>(store + scale_at) = scales;
-    if (pool != nullptr) *reinterpret_cast<uint32_t*>(pool + scale_at) = scales;
+    if (sub >= tokens || t >= total || a.job >= jobs) return a;
+    const int nq = q1 - q0, i = t - q0;
+    const long long pos = static_cast<long long>(L) - nq + i;
+    bool bad = q0 < 0 || nq < 1 || nq > p.max_q || L < nq || i < 0 || i >= nq || q0 > p.token_cap - nq;
+    if (!bad) {
+      a.chunk = static_cast<long long>(first_chunk) + pos / kChunk;
+      bad = a.chunk < 0 || a.chunk >= p.num_host_chunks;
+    }
+    if (bad) {
+      if (a.job == 0) atomicOr(p.err, kErrDeviceInput);
+      return a;
+    }
+    a.live = true;
+    a.row = static_cast<int>(pos % kChunk);
+    const bool is_v = a.job >= per_side;
+    const uint4* src = reinterpret_cast<const uint4*>((is_v ? p.v_new : p.k_new) + static_cast<size_t>(t) * p.hkv * HD +
+                                                      (is_v ? a.job - per_side : a.job) * 16);
+    a.lo = src[0];
+    a.hi = src[1];
+    a.slot = p.slot_of_chunk[a.chunk];
+    return a;
+  };
+  auto pack = [&](const AppendJob& a) {
+    const bool is_v = a.job >= per_side;
+    const int in_side = is_v ? a.job - per_side : a.job, h = in_side / kGroups, g = in_side % kGroups;
+    uint2 codes = make_uint2(0u, 0u);
+    uint32_t scale = 0u;
+    if (a.live) {
+      const uint32_t w[8] = {a.lo.x, a.lo.y, a.lo.z, a.lo.w, a.hi.x, a.hi.y, a.hi.z, a.hi.w};
+      float2 x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
+      codes = pack_group(x, is_v ? p.v_scale : p.k_scale, &scale);
+    }
+    // A pair of lanes holds a 16-byte word of codes; the even one writes it.
+    const uint32_t ox = __shfl_xor_sync(0xffffffffu, codes.x, 1), oy = __shfl_xor_sync(0xffffffffu, codes.y, 1);
+    // Four lanes hold four neighbouring scale bytes; the first writes them.
+    uint32_t scales = scale << (8 * (g & 3));
+    scales |= __shfl_xor_sync(0xffffffffu, scales, 1);
+    scales |= __shfl_xor_sync(0xffffffffu, scales, 2);
+    if (!a.live) return;
+    const size_t word = (static_cast<size_t>(g / 2) * kChunk + a.row) * 16;
+    const size_t scale_at = static_cast<size_t>(kChunk) * (HD / 2) + static_cast<size_t>(a.row) * kGroups + (g & ~3);
+    uint8_t* store = (is_v ? p.host_v : p.host_k) + (static_cast<size_t>(a.chunk) * p.hkv + h) * kPackedBytes<HD>;
+    uint8_t* pool = a.slot >= 0 && a.slot < p.num_slots
+                        ? (is_v ? p.v_pool : p.k_pool) + (static_cast<size_t>(a.slot) * p.hkv + h) * kPackedBytes<HD>
+                        : nullptr;
+    if ((g & 1) == 0) {
+      const uint4 v = make_uint4(codes.x, codes.y, ox, oy);
+      *reinterpret_cast<uint4*>(store + word) = v;
+      if (pool != nullptr) *reinterpret_cast<uint4*>(pool + word) = v;
+    }
+    if ((g & 3) == 0) {
+      *reinterpret_cast<uint32_t*>(store + scale_at) = scales;
+      if (pool != nullptr) *reinterpret_cast<uint32_t*>(pool + scale_at) = scales;
+    }
+  };
+  const long long items = (static_cast<long long>(total) + tokens - 1) / tokens * rounds;
+  if (static_cast<long long>(blockIdx.x) >= items) return;
+  AppendJob next = load(blockIdx.x);
+  for (long long at = blockIdx.x; at < items; at += gridDim.x) {
+    const AppendJob a = next;
+    next = load(at + gridDim.x);
+    pack(a);
   }
 }
 
@@ -112,12 +165,20 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(const UnpackParams p) 
   const uint8_t* rec = (is_v ? p.v_pool : p.k_pool) + (static_cast<size_t>(slot) * p.hkv + h) * kPackedBytes<HD>;
   uint16_t* out = (is_v ? p.v_out : p.k_out) + static_cast<size_t>(blockIdx.x) * kChunk * HD;
   const float gs = is_v ? p.v_scale : p.k_scale;
+  constexpr int kMine = kChunk * kGroups / kThreads;
+  uint2 codes_of[kMine];
+  uint32_t scale_of[kMine];
 #pragma unroll
-  for (int x = threadIdx.x; x < kChunk * kGroups; x += kThreads) {
-    const int row = x / kGroups, g = x % kGroups;
-    const uint2 codes =
-        *reinterpret_cast<const uint2*>(rec + (static_cast<size_t>(g / 2) * kChunk + row) * 16 + (g & 1) * 8);
-    const float s = e4m3_value(rec[kChunk * (HD / 2) + x]) * gs;
+  for (int y = 0; y < kMine; ++y) {        // (all loads before the first store)
+    const int x = threadIdx.x + y * kThreads, row = x / kGroups, g = x % kGroups;
+    codes_of[y] = *reinterpret_cast<const uint2*>(rec + (static_cast<size_t>(g / 2) * kChunk + row) * 16 + (g & 1) * 8);
+    scale_of[y] = rec[kChunk * (HD / 2) + x];
+  }
+#pragma unroll
+  for (int y = 0; y < kMine; ++y) {
+    const int x = threadIdx.x + y * kThreads;
+    const uint2 codes = codes_of[y];
+    const float s = e4m3_value(scale_of[y]) * gs;
     uint32_t o[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -135,8 +196,9 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(const UnpackParams p) 
 }  // namespace
 
 cudaError_t launch_append_packed(const PackedAppendParams& p, cudaStream_t stream) {
-  const unsigned long long jobs = static_cast<unsigned long long>(p.token_cap) * 2 * p.hkv * (p.head_dim / 16);
-  const dim3 grid(static_cast<unsigned>((jobs + kThreads - 1) / kThreads));
+  const int jobs = jobs_of(p.hkv, p.head_dim), tokens = cta_tokens(jobs);
+  const long long items = (static_cast<long long>(p.token_cap) + tokens - 1) / tokens * job_rounds(jobs);
+  const dim3 grid(static_cast<unsigned>(items < 3LL * p.num_sms ? items : 3LL * p.num_sms));   // as many as run at once
   if (p.head_dim == 128) return launch_pdl(append_packed_kernel<128>, grid, dim3(kThreads), 0, stream, p);
   return launch_pdl(append_packed_kernel<64>, grid, dim3(kThreads), 0, stream, p);
 }

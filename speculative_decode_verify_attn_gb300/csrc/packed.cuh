@@ -3,6 +3,8 @@
 
 #include <cstdint>
 
+#include "ptx.cuh"
+
 namespace vfy {
 
 // Bytes of one (chunk, KV head) record of K or V.
@@ -79,24 +81,42 @@ __device__ __forceinline__ uint32_t e2m1_of(float lo, float hi) {
   return r & 0xffu;
 }
 
-// 16 values to codes and their scale. Quotients are rounded as IEEE divisions: the scale's quotient can lie on a tie of
-// e4m3 only if it is exact, and so can a value's on a tie of e2m1.
-__device__ __forceinline__ uint2 pack_group(const float (&x)[16], uint32_t* scale) {
+// 16 values x to the codes of x / g and their scale. Quotients are rounded as IEEE divisions: the scale's quotient can lie on
+// a tie of e4m3 only if it is exact, and so can a value's on a tie of e2m1. `x`: pairs.
+//
+// A quotient comes from the rounded reciprocal, one remainder and one correction (Markstein's division), two at a time
+// (with divisions the append of 8 x 1024 tokens took 16.2 us instead of 13.4). That is exact where nothing overflows and no
+// remainder underflows: g within 2^-100 .. 2^100, s is 2^-9 .. 448 and below 448 |x / g| is at most a little over 6 s, and a
+// value whose remainder underflows is far below a code. Anything else, infinities among it, is divided.
+__device__ __forceinline__ float2 quotients(float2 v, float2 minus_by, float2 r) {
+  const float2 q = mul_f32x2(v, r);
+  return fma_f32x2(fma_f32x2(q, minus_by, v), r, q);
+}
+__device__ __forceinline__ uint2 pack_group(float2 (&x)[8], float g, uint32_t* scale) {
   float top = 0.f;
 #pragma unroll
-  for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(x[e]));
+  for (int e = 0; e < 8; ++e) top = fmaxf(fmaxf(top, fabsf(x[e].x)), fabsf(x[e].y));
+  top = __fdiv_rn(top, g);                 // (the quotients' largest: rounding keeps order)
   *scale = e4m3_of(__fdiv_rn(top, 6.f));
   const float s = e4m3_value(*scale);
   uint2 codes = make_uint2(0u, 0u);
-  if (s > 0.f) {
+  if (!(s > 0.f)) return codes;
+  if (top < INFINITY && g > 7.9e-31f && g < 1.2e30f) {
+    const float rg = __frcp_rn(g), rs = __frcp_rn(s);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      x[e] = quotients(quotients(x[e], make_float2(-g, -g), make_float2(rg, rg)), make_float2(-s, -s), make_float2(rs, rs));
+  } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const uint32_t two = e2m1_of(__fdiv_rn(x[2 * e], s), __fdiv_rn(x[2 * e + 1], s));
-      if (e < 4)
-        codes.x |= two << (8 * e);
-      else
-        codes.y |= two << (8 * (e - 4));
+      x[e].x = __fdiv_rn(__fdiv_rn(x[e].x, g), s);
+      x[e].y = __fdiv_rn(__fdiv_rn(x[e].y, g), s);
     }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    codes.x |= e2m1_of(x[e].x, x[e].y) << (8 * e);
+    codes.y |= e2m1_of(x[e + 4].x, x[e + 4].y) << (8 * e);
   }
   return codes;
 }

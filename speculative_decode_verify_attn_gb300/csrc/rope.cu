@@ -4,16 +4,15 @@
 // in fp32, rounded once to bf16.
 //
 // A CTA of eight warps takes one token (few tokens: latency; 264 of a batch of trees 4.1 us against 5.8), or a token a warp
-// (8 x 1024 tokens 25.5 us against 52). The warps of a token work out its cosines
-// and sines once, in shared memory. A row of d channels is d / 8 lanes of two groups of four channels: the two groups that
-// rotate with one another, so that a pair lies in one lane. Many tokens are bound by instructions before they are by memory:
-// queries, keys and values have a loop each, without choices by row, and what a token costs once is not shared among few
-// rows. The look-up of up to 32 sequences is one round trip to memory.
+// (8 x 1024 tokens 25.5 us against 52). The warps of a token work out its cosines and sines once, in shared memory. A row of
+// d channels is d / 8 lanes of two groups of four channels: the two groups that rotate with one another, so that a pair lies
+// in one lane. Many tokens are bound by instructions before they are by memory: queries, keys and values have a loop each,
+// without choices by row, and what a token costs once is paid by one warp. The look-up of up to 32 sequences is one round trip to memory.
 // 17 tokens of 16 + 2 x 4 heads of 128 take 3.0 us (latency), 8 x 1024 25.5 (115 MB, 4.5 TB/s).
 //
 // Angles: the turns position * inv_freq / 2 pi modulo 1 (at position 262144 an fp32 product is off by 1/64 radian), with
-// inv_freq / 2 pi as the sum of two fp32 values and the products exact in pairs (product and fma remainder): within
-// 2^-23 turns below 2^24 turns. (fp64 has 1/64 of the fp32 rate here.)
+// inv_freq / 2 pi as the sum of two fp32 values and the products exact in pairs (product and fma remainder): one rounding,
+// 2^-26 turns, and 2^-47 of the turns. (fp64 has 1/64 of the fp32 rate here.)
 #include <cuda_bf16.h>
 
 #include "ptx.cuh"
@@ -35,8 +34,11 @@ __device__ __forceinline__ float turns_of(long long position, float freq) {
   const float a0 = static_cast<float>(static_cast<int>(position & 0xffff));
   const float p1 = a1 * hi, p0 = a0 * hi;
   const float e1 = fmaf(a1, hi, -p1), e0 = fmaf(a0, hi, -p0);
-  const float sum = ((p1 - rintf(p1)) + (p0 - rintf(p0))) + (((e1 - rintf(e1)) + (e0 - rintf(e0))) + fmaf(a1, lo, a0 * lo));
-  return sum - rintf(sum);
+  // (the sum of the two fractions with its error: what is rounded is the last addition)
+  const float f1 = p1 - rintf(p1), f0 = p0 - rintf(p0);
+  const float sum = f1 + f0, of0 = sum - f1, error = (f1 - (sum - of0)) + (f0 - of0);
+  const float small = ((e1 - rintf(e1)) + (e0 - rintf(e0))) + fmaf(a1, lo, a0 * lo) + error;
+  return (sum - rintf(sum)) + small;
 }
 
 // Where a token's K and V go: the row of KV head 0, of up to two copies. (`origin` of its sequence: cu_chunks, or the ring's

@@ -343,6 +343,7 @@ struct PackedAppendParams {
   uint8_t* k_pool;            // [slots][Hkv] records
   uint8_t* v_pool;
   float k_scale, v_scale;
+  int num_sms;
   int* err;
 };
 cudaError_t launch_append_packed(const PackedAppendParams& p, cudaStream_t stream);
