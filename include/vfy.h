@@ -571,7 +571,7 @@ typedef struct vfy_rotary {
  * vfy_rope -- normalise and rotate the block's queries and keys.
  * Row i of sequence b is at position p = seq_len[b] - q_b + i, or, with depths (a tree), at
  * seq_len[b] - q_b + depth[cu_q[b] + i]. With t = p * inv_freq[j] every pair (x, y) becomes
- * (x cos t - y sin t, x sin t + y cos t). Angles are reduced in 64 bits: far positions keep their precision.
+ * (x cos t - y sin t, x sin t + y cos t). Angles are within 2^-22 of a turn at every position (2^-25 up to 2^22).
  *  q, q_stride    bf16 rows of Hq * d values, q_stride values apart (>= Hq * d, a multiple of 8): a view of a
  *                 wider matrix. NULL with q_out NULL: no queries
  *  k, k_stride    bf16 rows of Hkv * d values; NULL with k_out NULL: no keys

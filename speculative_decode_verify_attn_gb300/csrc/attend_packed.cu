@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
         if (!is_o) {
           const uint32_t idesc = idesc_f16_f32(128, n, 0, 0);
           const uint64_t qdesc = sw128_desc(sbase + C::kQOffset, 16, 1024);
-          for (int j = 0; j < nt; ++j) {
+          for (int j = 0; ok && j < nt; ++j) {
             const int g = j & 1, ph = j >> 1 & 1;
             ok = wait(&sh->k_ready[g], ph) && (j < 2 || wait(&sh->s_free[g], ph ^ 1));
             if (!ok) break;
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
           const uint32_t idesc = idesc_f16_f32(128, n, 1, 1);
           const uint64_t vdesc = sw128_desc(sbase + C::kVOffset, C::kBoxBytes, 1024);
           const uint64_t pdesc = sw128_desc(sbase + C::kPOffset, C::kBoxBytes, 1024);
-          for (int j = 0; j < nt; ++j) {
+          for (int j = 0; ok && j < nt; ++j) {
             const int g = j & 1, ph = j >> 1 & 1;
             ok = wait(&sh->v_ready[g], ph) && wait(&sh->p_ready[g], ph);
             if (!ok) break;

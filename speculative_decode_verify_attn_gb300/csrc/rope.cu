@@ -11,8 +11,8 @@
 // 17 tokens of 16 + 2 x 4 heads of 128 take 3.0 us (latency), 8 x 1024 25.5 (115 MB, 4.5 TB/s).
 //
 // Angles: the turns position * inv_freq / 2 pi modulo 1 (at position 262144 an fp32 product is off by 1/64 radian), with
-// inv_freq / 2 pi as the sum of two fp32 values and the products exact in pairs (product and fma remainder): one rounding,
-// 2^-26 turns, and 2^-47 of the turns. (fp64 has 1/64 of the fp32 rate here.)
+// inv_freq / 2 pi as the sum of three fp32 values (to 2^-53) and the products exact in pairs (product and fma remainder):
+// within 2^-25 turns up to position 2^22 (the last addition), 2^-22 up to 2^31. (fp64 has 1/64 of the fp32 rate here.)
 #include <cuda_bf16.h>
 
 #include "ptx.cuh"
@@ -28,16 +28,20 @@ enum { kRows = 0, kFull = 1, kRing = 2 };
 // position * freq / 2 pi, modulo 1
 __device__ __forceinline__ float turns_of(long long position, float freq) {
   constexpr double kInv2Pi = 0.15915494309189535;
-  constexpr float kHi = static_cast<float>(kInv2Pi), kLo = static_cast<float>(kInv2Pi - static_cast<double>(kHi));
-  const float hi = freq * kHi, lo = fmaf(freq, kHi, -hi) + freq * kLo;
+  constexpr float k0 = static_cast<float>(kInv2Pi), k1 = static_cast<float>(kInv2Pi - static_cast<double>(k0));
+  constexpr float k2 = static_cast<float>(kInv2Pi - static_cast<double>(k0) - static_cast<double>(k1));
+  // freq / 2 pi = c0 + c1 + c2: a product; its remainder and the next product; their sum's error and what is left
+  const float c0 = freq * k0, r = fmaf(freq, k0, -c0);
+  const float m = freq * k1, c1 = r + m, back = c1 - r;
+  const float c2 = ((r - (c1 - back)) + (m - back)) + fmaf(freq, k2, fmaf(freq, k1, -m));
   const float a1 = static_cast<float>(static_cast<int>(position >> 16)) * 65536.f;   // both exact
   const float a0 = static_cast<float>(static_cast<int>(position & 0xffff));
-  const float p1 = a1 * hi, p0 = a0 * hi;
-  const float e1 = fmaf(a1, hi, -p1), e0 = fmaf(a0, hi, -p0);
-  // (the sum of the two fractions with its error: what is rounded is the last addition)
+  const float p1 = a1 * c0, p0 = a0 * c0, p2 = a1 * c1;
+  const float e1 = fmaf(a1, c0, -p1), e0 = fmaf(a0, c0, -p0), e2 = fmaf(a1, c1, -p2);
+  // (the sum of the first two fractions with its error: what is rounded is the last addition)
   const float f1 = p1 - rintf(p1), f0 = p0 - rintf(p0);
   const float sum = f1 + f0, of0 = sum - f1, error = (f1 - (sum - of0)) + (f0 - of0);
-  const float small = ((e1 - rintf(e1)) + (e0 - rintf(e0))) + fmaf(a1, lo, a0 * lo) + error;
+  const float small = ((e1 - rintf(e1)) + (e0 - rintf(e0))) + ((p2 - rintf(p2)) + e2) + (fmaf(a1, c2, a0 * c1) + error);
   return (sum - rintf(sum)) + small;
 }
 

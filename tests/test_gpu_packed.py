@@ -498,3 +498,117 @@ def test_a_layer_from_projection_to_output_in_a_graph(env):
         assert vfy.vfy_get_status(ctx) == vfy.VFY_OK
     finally:
         ctx.close()
+
+
+def appended(env, counts, lens, hkv, d, g, seed, x=None):
+    """Appends the counts and compares every byte of store and pool."""
+    H, vfy = env
+    rng = np.random.default_rng(seed)
+    T, chunks = sum(counts), [-(-n // C) for n in lens]
+    k, v = [O.bf16_to_f64(B.to_bf16(rng.standard_normal((T, hkv, d)) * 8.0 * g if x is None else x)) for _ in range(2)]
+    m = sum(chunks)
+    slot_of = rng.permutation(m + 2)[:m] - 2
+    store, pool = [records(rng, m, hkv, d) for _ in range(2)], [records(rng, m, hkv, d) for _ in range(2)]
+    sd, pd = [u8(r) for r in store], [u8(r) for r in pool]
+    cu_chunks = H.cu_from_counts(chunks)
+    ctx = vfy.vfy_create(hkv, hkv, d, max_seqs=len(counts), max_queries_per_seq=max(counts), device=0)
+    try:
+        vfy.vfy_append_full_packed(ctx, H.dev_bf16(B.to_bf16(k)), H.dev_bf16(B.to_bf16(v)), H.dev_i32(H.cu_from_counts(counts)),
+                                   H.dev_i32(lens), H.dev_i32(cu_chunks), H.dev_i32(slot_of), *sd, m, *pd, m, g, g, len(counts))
+        assert vfy.vfy_get_status(ctx) == vfy.VFY_OK
+    finally:
+        ctx.close()
+    seq = np.repeat(np.arange(len(counts)), counts)
+    at = np.concatenate([L - n + np.arange(n) for n, L in zip(counts, lens)])
+    chunk, row = np.asarray(cu_chunks)[seq] + at // C, at % C
+    for side, y in enumerate((k, v)):
+        codes, scales = B.pack_rows(y, g)
+        pairs = (codes[..., ::2] | codes[..., 1::2] << 4).reshape(T, hkv, d // 32, 16)
+        for t in range(T):
+            for recs, c in ((store, chunk[t]), (pool, slot_of[chunk[t]])):
+                if c >= 0:
+                    rec = recs[side][c]
+                    rec[:, :32 * d].reshape(hkv, d // 32, C, 16)[:, :, row[t]] = pairs[t]
+                    rec[:, 32 * d:].reshape(hkv, C, d // 16)[:, row[t]] = scales[t]
+    for got, want in zip(sd + pd, store + pool):
+        assert np.array_equal(got.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("hkv,d,counts", [(4, 128, [1000, 1, 0, 700, 500]), (1, 64, [1000] * 15 + [1]), (3, 64, [1000, 0, 1000, 1000]),
+                                          (32, 128, [300, 200]), (20, 64, [700])])
+def test_append_of_many_tokens(env, hkv, d, counts):
+    """More tokens than one round of CTAs holds; tokens of more jobs than a CTA has threads."""
+    appended(env, counts, [n + 17 if n else 0 for n in counts], hkv, d, 0.037, hkv)
+
+
+@pytest.mark.parametrize("seqs", [32, 33, 100])
+def test_append_to_many_sequences(env, seqs):
+    rng = np.random.default_rng(seqs)
+    counts = rng.integers(0, 4, seqs)
+    counts[-1] = 2
+    appended(env, counts.tolist(), (counts + rng.integers(0, 200, seqs)).tolist(), 2, 64, 1.0, seqs)
+
+
+@pytest.mark.parametrize("g", [1e-37, 1e-33, 2.0 ** -100, 2.0 ** -126, 1e29, 1e33, 2.0 ** 100, 2.0 ** 127])
+def test_append_with_extreme_tensor_scales(env, g):
+    """Quotients that overflow, underflow, or whose remainders would: the codes of IEEE divisions."""
+    rng = np.random.default_rng(3)
+    x = rng.standard_normal((40, 2, 64)) * np.exp2(np.clip(np.log2(g) + rng.integers(-14, 14, (40, 2, 1)), -130, 125))
+    appended(env, [40], [50], 2, 64, float(np.float32(g)), 3, x)
+
+
+@pytest.mark.parametrize("n", range(1, 17))
+@pytest.mark.parametrize("heads", [(1, 1, 64), (2, 2, 128)])
+def test_every_number_of_few_rows(env, heads, n):
+    one(env, heads, n, 1000 + n, seed=n)
+    one(env, heads, n, 1000 + n, seed=n, splits=1)                # (written by the attention kernel itself)
+
+
+@pytest.mark.parametrize("n", [1, 4, 5, 17, 40])
+@pytest.mark.parametrize("splits", [0, 1])
+def test_wait_timeout_is_reported_and_recovered(env, n, splits):
+    H, vfy = env
+    rng = np.random.default_rng(n)
+    m, L = 30, 30 * C
+    pools = [records(rng, m, 4, 128) for _ in range(2)]
+    q = B.to_bf16(rng.standard_normal((n, 16, 128)))
+    ctx = vfy.vfy_create(16, 4, 128, max_queries_per_seq=n, device=0)
+    try:
+        vfy.vfy_set_splits(ctx, splits, 0)
+        vfy.vfy_test_wait_timeout(ctx, 2000)
+        attend(env, ctx, q, [0, n], pools, np.arange(m), np.arange(m), [0, m], [L])
+        assert vfy.vfy_get_status(ctx) == vfy.VFY_EDEVICE_TIMEOUT
+        vfy.vfy_test_wait_timeout(ctx, 0)
+        got, lse = attend(env, ctx, q, [0, n], pools, np.arange(m), np.arange(m), [0, m], [L])
+        assert vfy.vfy_get_status(ctx) == vfy.VFY_OK
+        close(got, lse, *B.attend_packed_seq(O.bf16_to_f64(q), *pools, np.arange(m), np.arange(m), L))
+    finally:
+        ctx.close()
+
+
+@pytest.mark.parametrize("n", [2, 17])
+def test_stable_metadata_and_two_streams(env, n):
+    """Two contexts on two streams at once, with metadata that stays: both give what one call alone gives, every time."""
+    H, vfy = env
+    rng = np.random.default_rng(n)
+    m, L = 60, 60 * C
+    pools = [u8(records(rng, m, 4, 128)) for _ in range(2)]
+    q = H.dev_bf16(B.to_bf16(rng.standard_normal((n, 16, 128))))
+    ids, cu, cr, ln = H.dev_i32(np.arange(m)), H.dev_i32([0, n]), H.dev_i32([0, m]), H.dev_i32([L])
+    ctxs = [vfy.vfy_create(16, 4, 128, max_queries_per_seq=n, device=0) for _ in range(2)]
+    outs, lses = [torch.zeros_like(q) for _ in range(9)], [torch.zeros((n, 16), device="cuda") for _ in range(9)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    try:
+        vfy.vfy_attend_full_packed(ctxs[0], q, cu, *pools, m, ids, ids, cr, m, ln, 1.0, 1.0, outs[8], lses[8], 1)
+        for c in ctxs:
+            vfy.vfy_set_stable_metadata(c, True)
+        torch.cuda.synchronize()
+        for i in range(8):
+            with torch.cuda.stream(streams[i % 2]):
+                vfy.vfy_attend_full_packed(ctxs[i % 2], q, cu, *pools, m, ids, ids, cr, m, ln, 1.0, 1.0, outs[i], lses[i], 1)
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, outs[8]) for o in outs) and all(torch.equal(x, lses[8]) for x in lses)
+        assert all(vfy.vfy_get_status(c) == vfy.VFY_OK for c in ctxs)
+    finally:
+        for c in ctxs:
+            c.close()

@@ -334,3 +334,45 @@ def test_layer_in_a_graph(env, window):
         assert vfy.vfy_get_status(ctx) == vfy.VFY_OK
     finally:
         ctx.close()
+
+
+@pytest.mark.parametrize("heads", [(16, 4, 128), (4, 1, 64), (6, 3, 64), (1, 1, 128)])
+@pytest.mark.parametrize("rot,interleaved", [(None, False), (None, True), (24, True), (8, False)])
+def test_a_token_a_warp(env, heads, rot, interleaved):
+    """A context with room for many tokens takes one token a warp instead of a CTA: the same bits in every destination,
+    with tokens that no multiple of eight divides, and the same rows left as they were."""
+    H, vfy = env
+    hq, hkv, d = heads
+    rot = d if rot is None else rot
+    rng = np.random.default_rng([hq, d, rot, interleaved])
+    counts, lens, R = [17, 1, 0, 5, 30], [262144, 1, 0, 130, 1000], 512
+    T = sum(counts)
+    (_, _, _), (qd, kd, vd) = block(rng, T, hq, hkv, d)
+    rope = vfy.Rope(H.dev_f32(freqs(rot)), rot, interleaved, 0.75, H.dev_bf16(synth.normal_bf16(rng, (d,))),
+                    H.dev_bf16(synth.normal_bf16(rng, (d,))))
+    chunks = [-(-x // C) for x in lens]
+    cu, ln, phi = H.dev_i32(H.cu_from_counts(counts)), H.dev_i32(lens), H.dev_i32([3, -5, 0, 700, 255])
+    dep = H.dev_i32(np.concatenate([np.arange(n) // 2 for n in counts]))
+    # (only the block's chunks: the first sequence's others lie before the store)
+    first = lens[0] // C - 1
+    cu_c = H.dev_i32(np.concatenate([[-first], np.cumsum(chunks)[:-1] - first]))
+    n_chunks = sum(chunks) - first
+    slot_of = H.dev_i32(rng.permutation(n_chunks + 3)[:n_chunks] - 3)
+    results = []
+    for cap in (33, 200):
+        full = lambda *s: torch.full(s, 9.0, dtype=torch.bfloat16, device="cuda")   # noqa: E731
+        ctx = vfy.vfy_create(hq, hkv, d, max_seqs=5, max_queries_per_seq=cap, window=64, ring_len=R, device=0)
+        outs = [full(T + 9, hq, d), full(T + 9, hkv, d), full(T + 9, hq, d), *[full(n_chunks, hkv, C, d) for _ in range(4)],
+                full(T + 9, hq, d), *[full(5, hkv, R, d) for _ in range(2)]]
+        try:
+            vfy.vfy_rope(ctx, rope, qd, kd, cu, ln, dep, *outs[:2], 5)
+            vfy.vfy_rope_append_full(ctx, rope, qd, kd, vd, cu, ln, dep, cu_c, slot_of, *outs[3:5], n_chunks, *outs[5:7], n_chunks, outs[2], 5)
+            vfy.vfy_rope_append_swa(ctx, rope, qd, kd, vd, cu, ln, dep, phi, *outs[8:], outs[7], 5)
+            assert vfy.vfy_get_status(ctx) == vfy.VFY_OK
+        finally:
+            ctx.close()
+        assert all((o[T:] == 9).all() for o in (outs[0], outs[1], outs[2], outs[7]))
+        results.append(outs)
+    for a, b in zip(*results):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    assert torch.equal(results[0][0], results[0][2]) and torch.equal(results[0][0], results[0][7])

@@ -314,3 +314,33 @@ def test_draws_follow_the_target(env):
         assert np.all(np.abs(share - p) < 5 * np.sqrt(p * (1 - p) / N))
     finally:
         ctx.close()
+
+
+@pytest.mark.parametrize("counts,V", [([3, 1], 150001), ([1] * 40, 5000), ([2, 1, 3] * 15, 1001), ([50], 2049), ([1], 1 << 20)])
+def test_many_sequences_and_long_vocabularies(env, counts, V):
+    """More than 32 sequences, segments of several rounds, more draft rows than a CTA has warps."""
+    rng = np.random.default_rng([len(counts), V])
+    ctx = env[1].vfy_create(4, 1, 64, max_seqs=len(counts), max_queries_per_seq=max(counts), device=0)
+    try:
+        for bf16 in (False, True):
+            check(env, ctx, make(rng, counts, V, bf16), bf16=bf16)
+    finally:
+        ctx.close()
+
+
+@pytest.mark.parametrize("small,large", [(1e-38, 1.0), (1e-37, 3e38), (1.0, 1e37), (1e-40, 1e-39)])
+def test_noise_of_every_size(env, small, large):
+    """Exponentials whose reciprocals leave fp32's normal range: the token with the smallest time is drawn."""
+    rng = np.random.default_rng(5)
+    ctx = env[1].vfy_create(4, 1, 64, max_seqs=2, max_queries_per_seq=4, device=0)
+    try:
+        while True:
+            c = make(rng, [4, 1], 500)
+            for b in range(2):
+                c["noise"][b] = np.float32(large) * np.float32(1 + rng.random(500) * 0.1)
+                c["noise"][b, rng.integers(0, 500, 3)] = np.float32(small)
+            if B.accept_sampled(**c)[3] > 2.0 ** -18:
+                break
+        check(env, ctx, c)
+    finally:
+        ctx.close()
