@@ -14,6 +14,11 @@ CASE:
   tree256k   one full layer of a 64-node tree with all 4096 chunks resident (CTA pairs and their merge)
   logits     the rules on 17 x 131072 fp32 logits: penalties with drafts, 32 biases, a grammar mask per row
   accept_tree  argmax + the walk over a 17-node tree, 17 x 131072 fp32 logits
+  packed256k one full-attention layer of 17 rows over 4096 chunks held in 4 bits (144 MiB of KV)
+  decode256k the same for one row
+  rope       rotation, norms and append of 8 blocks of 1024 tokens
+  append4    8 blocks of 1024 tokens into 4-bit chunks
+  sampled    sampled acceptance of 17 x 131072 fp32 logits
 Each repetition writes a 256 MiB buffer first, so the kernel reads HBM, not L2. The device
 holds under 1 GiB in every case; the largest are full256k and tree256k, with 512 MiB of K/V beside
 the 256 MiB flush buffer.
@@ -37,7 +42,7 @@ from speculative_decode_verify_attn_gb300 import build, synth, vfy  # noqa: E402
 def main(argv=None):
     ap = argparse.ArgumentParser()
     ap.add_argument("case", choices=["full8k", "full256k", "swa", "accept", "select", "prefill", "drafter", "tree256k",
-                                     "logits", "accept_tree"])
+                                     "logits", "accept_tree", "packed256k", "decode256k", "rope", "append4", "sampled"])
     ap.add_argument("--reps", type=int, default=3)
     a = ap.parse_args(argv)
     build.build()
@@ -47,10 +52,11 @@ def main(argv=None):
     g.manual_seed(0)
     rng = np.random.default_rng(0)
     s = synth.LAGUNA
-    q, L = {"prefill": 1024, "drafter": 16, "tree256k": 64}.get(a.case, 17), 262144
+    q, L = {"prefill": 1024, "drafter": 16, "tree256k": 64, "decode256k": 1, "rope": 1024, "append4": 1024}.get(a.case, 17), 262144
+    seqs = 8 if a.case in ("rope", "append4") else 1
     W, R = (synth.DRAFTER_WINDOW, synth.DRAFTER_RING) if a.case == "drafter" else (synth.WINDOW, synth.RING)
     ctx = vfy.vfy_create(s.num_q_heads, s.num_kv_heads, s.head_dim, window=W, ring_len=R, max_queries_per_seq=q,
-                         device=0)
+                         max_seqs=seqs, device=0)
     # as in the 40-layer pass: the per-step metadata is set before the kernels run
     vfy.vfy_set_stable_metadata(ctx, True)
     flush = torch.empty(64 << 20, dtype=torch.float32, device=dev)
@@ -108,6 +114,53 @@ def main(argv=None):
 
         def run():
             vfy.vfy_process_logits(ctx, x, V, cu_q, q, rules, done, 1)
+    elif a.case in ("packed256k", "decode256k"):
+        n = L // 64
+        kp, vp = [torch.randint(0, 256, (n, s.num_kv_heads, vfy.packed_bytes(s.head_dim)), generator=g, device=dev,
+                                dtype=torch.uint8) for _ in range(2)]
+        for p in (kp, vp):                                  # scales of 1/8 .. 1
+            p[..., 32 * s.head_dim:] = torch.randint(0x20, 0x39, p[..., 32 * s.head_dim:].shape, generator=g, device=dev,
+                                                     dtype=torch.uint8)
+        ids = torch.arange(n, dtype=torch.int32, device=dev)
+        sl = torch.from_numpy(rng.permutation(n).astype(np.int32)).to(dev)
+        cr = torch.tensor([0, n], dtype=torch.int32, device=dev)
+
+        def run():
+            vfy.vfy_attend_full_packed(ctx, qt, cu_q, kp, vp, n, ids, sl, cr, n, seq_len, 1.0, 1.0, out, lse, 1)
+    elif a.case in ("rope", "append4"):
+        T, hq, hkv, d, n = seqs * q, s.num_q_heads, s.num_kv_heads, s.head_dim, 4096 // 64
+        wide = torch.randn((T, (hq + 2 * hkv) * d), generator=g, device=dev).bfloat16()
+        qs, ks, vs = [wide[:, x * d:y * d].unflatten(1, (-1, d)) for x, y in ((0, hq), (hq, hq + hkv), (hq + hkv, hq + 2 * hkv))]
+        cu = torch.arange(0, T + 1, q, dtype=torch.int32, device=dev)
+        lens = torch.full((seqs,), 4096, dtype=torch.int32, device=dev)
+        cu_c = torch.arange(0, (seqs + 1) * n, n, dtype=torch.int32, device=dev)
+        som = torch.arange(seqs * n, dtype=torch.int32, device=dev)
+        shape = (seqs * n, hkv, 64, d) if a.case == "rope" else (seqs * n, hkv, vfy.packed_bytes(d))
+        sk, sv, kp, vp = [torch.zeros(shape, device=dev, dtype=torch.bfloat16 if a.case == "rope" else torch.uint8)
+                          for _ in range(4)]
+        ones = torch.ones(d, device=dev, dtype=torch.bfloat16)
+        rope = vfy.Rope(10000.0 ** (-torch.arange(0, d, 2, device=dev, dtype=torch.float32) / d), q_norm=ones, k_norm=ones)
+        qo, kc, vc = torch.empty((T, hq, d), device=dev, dtype=torch.bfloat16), ks.contiguous(), vs.contiguous()
+
+        def run():
+            if a.case == "rope":
+                vfy.vfy_rope_append_full(ctx, rope, qs, ks, vs, cu, lens, None, cu_c, som, sk, sv, seqs * n, kp, vp, seqs * n,
+                                         qo, seqs)
+            else:
+                vfy.vfy_append_full_packed(ctx, kc, vc, cu, lens, cu_c, som, sk, sv, seqs * n, kp, vp, seqs * n, 0.037, 0.037,
+                                           seqs)
+    elif a.case == "sampled":
+        V = synth.VOCAB
+        x = torch.randn((q, V), generator=g, device=dev) * 2
+        probs = torch.softmax(x[:-1] + torch.randn((q - 1, V), generator=g, device=dev) * 0.5, -1)
+        drafts = torch.multinomial(probs, 1, generator=g).int().flatten()
+        uniform = torch.rand(q - 1, generator=g, device=dev)
+        noise = torch.empty((1, V), device=dev).exponential_(generator=g)
+        heat = torch.ones(1, device=dev)
+        acc, bon, com = [torch.empty(k, dtype=torch.int32, device=dev) for k in (1, 1, q)]
+
+        def run():
+            vfy.vfy_accept_sampled(ctx, x, V, heat, drafts, probs, uniform, noise, cu_q, q, acc, bon, com, 1)
     elif a.case in ("accept", "accept_tree"):
         targets = rng.integers(0, synth.VOCAB, q)
         logits = torch.from_numpy(synth.planted_logits(rng, targets, synth.VOCAB)).to(dev)
