@@ -689,8 +689,8 @@ VFY_API vfy_status vfy_attend_full_packed(vfy_ctx* ctx, const uint16_t* q, const
  * drafts, draft_probs and uniform may be NULL where every sequence has one row. If w leaves nothing to draw, p_n is drawn
  * from; if that leaves nothing, the row's argmax is taken.
  * Device errors: a drafted token outside [0, vocab) (refused; nothing is taken off p), a temperature that is negative,
- * NaN or infinite (taken as 0), rows out of range or a sequence without rows (its outputs are not written):
- * VFY_EDEVICE_INPUT.
+ * NaN or infinite (taken as 0), rows out of range, a sequence without rows, or drafts that would lie behind the last of
+ * cu_rows[B] - B (its outputs are not written): VFY_EDEVICE_INPUT.
  */
 VFY_API vfy_status vfy_accept_sampled(vfy_ctx* ctx, const void* logits, int logits_type, int64_t row_stride, int vocab,
                                       const float* temperature, const int32_t* drafts, const float* draft_probs,

@@ -344,3 +344,19 @@ def test_noise_of_every_size(env, small, large):
         check(env, ctx, c)
     finally:
         ctx.close()
+
+
+@pytest.mark.parametrize("counts,cu", [([1, 1], [0, 2, 2]), ([1, 1], [0, 0, 2]), ([2, 1], [0, 3, 3]), ([2, 1, 1, 1], [0, 5, 5, 5, 5])])
+def test_drafts_that_are_not_there_are_not_read(env, counts, cu):
+    """Sequences without rows make others need drafts behind the last one (or any, where there are none): reported, and the
+    outputs of both stay."""
+    H, vfy = env
+    c = make(np.random.default_rng(9), counts, 300)
+    ctx = vfy.vfy_create(4, 1, 64, max_seqs=len(counts), max_queries_per_seq=8, device=0)
+    try:
+        acc, bonus, _ = call(env, ctx, dict(c, cu_rows=np.array(cu)))
+        assert vfy.vfy_get_status(ctx) == vfy.VFY_EDEVICE_INPUT
+        assert acc == bonus == [-7] * len(counts)
+        check(env, ctx, c)
+    finally:
+        ctx.close()
