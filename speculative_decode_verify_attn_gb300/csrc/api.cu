@@ -1218,8 +1218,8 @@ vfy_status vfy_attend_full_packed(vfy_ctx* ctx, const uint16_t* q, const int32_t
       splits = static_cast<int>(ctx->num_sms * (num_seqs > 1 ? 2 : 1) / items);
       splits = clampi(splits, 1, std::max(1, ceil_div(max_resident_per_seq, 5)));
     } else {
-      // One CTA an SM, for a batch twice as many, which even out sequences of different lengths (8 ragged ones: one wave
-      // 89 us, two 71, four 82; 16: 39.8 two, 54.7 four), and no fewer than three tiles each: what a CTA begins and ends with
+      // One CTA an SM, for a batch twice as many, which even out sequences of different lengths (8 ragged ones: 9 splits
+      // 67.5 us, 5 74, 12 73; 16: 4 splits 38.2, 5 43.6), and no fewer than three tiles each: what a CTA begins and ends with
       // is as long (64 tiles: 22 splits 13.4 us, 38 15.5).
       splits = static_cast<int>(ctx->num_sms * (num_seqs > 1 ? 2 : 1) / items);
       splits = clampi(splits, 1, std::max(1, ceil_div(max_resident_per_seq, 6)));
@@ -1231,6 +1231,7 @@ vfy_status vfy_attend_full_packed(vfy_ctx* ctx, const uint16_t* q, const int32_t
   p.v_scale = v_scale;
   p.part_o = ctx->part_o;
   p.part_ml = ctx->part_ml;
+  p.num_seqs = num_seqs;
   p.timeout_test_ns = ctx->timeout_test_ns;
   p.stable_metadata = ctx->stable_metadata;
   p.err = ctx->err;

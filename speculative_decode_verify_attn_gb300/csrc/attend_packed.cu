@@ -82,6 +82,7 @@ struct Shared {
   int abort;
   unsigned q_top;                         // largest |q| of the tile, as bf16 bits
   int base[2 * kBatch][2];                // position of a chunk's first token, -1: no chunk
+  int seq;                                // of the batch
   int4 geom[2];                           // [group] length, position of the block's first token, first row, rows: read
                                           // where they are needed, registers are short
   int plain[2 * kBatch];                  // every row attends every key of the tile
@@ -104,10 +105,12 @@ __device__ __forceinline__ Work make_work(const PackedAttnParams& p) {
   Work w;
   w.s = blockIdx.x;
   w.h = blockIdx.y;
-  w.b = static_cast<int>(blockIdx.z / static_cast<unsigned>(p.n_tiles));
-  const int rt = static_cast<int>(blockIdx.z) - w.b * p.n_tiles;
-  const int c0 = p.cu_q[w.b], c1 = p.cu_q[w.b + 1], cr0 = p.cu_res[w.b], cr1 = p.cu_res[w.b + 1];
-  w.L = p.seq_len[w.b];
+  const int z = static_cast<int>(blockIdx.z / static_cast<unsigned>(p.n_tiles));
+  const int rt = static_cast<int>(blockIdx.z) - z * p.n_tiles;
+  const SequenceMeta meta = longest_first(p.cu_q, p.cu_res, p.seq_len, p.num_seqs, z, threadIdx.x & 31);
+  const int c0 = meta.c0, c1 = meta.c1, cr0 = meta.r0, cr1 = meta.r1;
+  w.b = meta.b;
+  w.L = meta.len;
   w.q0 = c0;
   w.nq = c1 - c0;
   w.row0 = rt * p.tile_rows;
@@ -452,6 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
     // No reference yet. Rows past the block weigh 0, whatever their scores hold: all 36 rows of a thread are computed
     // without a branch.
     if (tg < kMaxN) sh->neg_ref[grp][tg] = tg < w.rows ? 0.f : -INFINITY;
+    if (threadIdx.x == 0) sh->seq = w.b;
     if (tg == 0) sh->geom[grp] = make_int4(w.L, w.L - w.nq, w.row0, w.rows);
     bool has_ref = tg >= w.rows;                         // of row tg
     bool all_have = false;                               // of the group
@@ -587,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
     }
     // ---- epilogue: the groups' sums and O merged into the split's partial (m, l, O not normalised) ----
     const int4 gm = sh->geom[grp];
-    const unsigned b = blockIdx.z / static_cast<unsigned>(p.n_tiles);
+    const int b = sh->seq;
     if (u > 0 && !dead) dead = !__all_sync(0xffffffffu, mbar_wait(&sh->pv_done[grp], (u - 1) & 1, abort, p.err));
 #pragma unroll
     for (int r = 0; r < kRowsT; r += 4) {

@@ -103,9 +103,9 @@ __global__ void __launch_bounds__(Few<HD, NT>::kThreads, 1) attend_packed_few_ke
   __syncthreads();
   pdl_launch_dependents();
   if (!p.stable_metadata) pdl_wait();
-  const int s = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
-  const int q0 = p.cu_q[b], nq = p.cu_q[b + 1] - q0, L = p.seq_len[b];
-  const int r0 = p.cu_res[b], nres = max(0, p.cu_res[b + 1] - r0);
+  const int s = blockIdx.x, h = blockIdx.y;
+  const SequenceMeta meta = longest_first(p.cu_q, p.cu_res, p.seq_len, p.num_seqs, blockIdx.z, lane);
+  const int b = meta.b, q0 = meta.c0, nq = meta.c1 - q0, L = meta.len, r0 = meta.r0, nres = max(0, meta.r1 - r0);
   if (p.stable_metadata) pdl_wait();
   if (nq < 0 || nq > p.max_q || L < nq || static_cast<unsigned>(q0) > static_cast<unsigned>(p.token_cap - nq)) {
     if (threadIdx.x == 0 && s == 0 && h == 0) atomicOr(p.err, kErrDeviceInput);

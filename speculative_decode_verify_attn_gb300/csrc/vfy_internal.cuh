@@ -386,6 +386,7 @@ struct PackedAttnParams {
   float* lse;                 // [T][Hq] or null
   unsigned long long timeout_test_ns;  // as in AttnParams
   int stable_metadata;
+  int num_seqs;
   int* err;
 };
 // The most block rows that one CTA takes.
@@ -489,6 +490,47 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int num_seqs, int 
     lo = next;
   }
   return lo;
+}
+
+// The sequences of a batch by the length of their resident lists, longest first, so that the CTAs of long ones start first
+// (batches of up to 32; larger ones keep their order). 8 ragged sequences of 12K to 48K: 70.5 -> 67.5 us. Returns place `z` and its metadata, one round trip to memory for a
+// batch of up to 32, by all 32 lanes of a converged warp.
+struct SequenceMeta {
+  int b, c0, c1, r0, r1, len;
+};
+__device__ __forceinline__ SequenceMeta longest_first(const int32_t* cu_q, const int32_t* cu_res, const int32_t* seq_len,
+                                                      int num_seqs, int z, int lane) {
+  SequenceMeta m;
+  m.b = z;
+  if (num_seqs == 1 || num_seqs > 32) {
+    m.c0 = cu_q[z];
+    m.c1 = cu_q[z + 1];
+    m.r0 = cu_res[z];
+    m.r1 = cu_res[z + 1];
+    m.len = seq_len[z];
+    return m;
+  }
+  int c0 = 0, c1 = 0, r0 = 0, r1 = 0, len = 0;
+  if (lane < num_seqs) {
+    c0 = cu_q[lane];
+    c1 = cu_q[lane + 1];
+    r0 = cu_res[lane];
+    r1 = cu_res[lane + 1];
+    len = seq_len[lane];
+  }
+  const int mine = r1 - r0;
+  int place = 0;
+  for (int i = 0; i < num_seqs; ++i) {
+    const int other = __shfl_sync(0xffffffffu, mine, i);
+    place += other > mine || (other == mine && i < lane) ? 1 : 0;
+  }
+  m.b = __ffs(__ballot_sync(0xffffffffu, lane < num_seqs && place == z)) - 1;
+  m.c0 = __shfl_sync(0xffffffffu, c0, m.b);
+  m.c1 = __shfl_sync(0xffffffffu, c1, m.b);
+  m.r0 = __shfl_sync(0xffffffffu, r0, m.b);
+  m.r1 = __shfl_sync(0xffffffffu, r1, m.b);
+  m.len = __shfl_sync(0xffffffffu, len, m.b);
+  return m;
 }
 
 }  // namespace vfy

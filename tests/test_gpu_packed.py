@@ -612,3 +612,29 @@ def test_stable_metadata_and_two_streams(env, n):
     finally:
         for c in ctxs:
             c.close()
+
+
+@pytest.mark.parametrize("seqs", [2, 32, 33, 70])
+@pytest.mark.parametrize("cap", [2, 9])
+def test_batches_of_many_sequences(env, seqs, cap):
+    """Sequences of every length in any order, equal ones and empty lists among them; batches up to 32 are started longest
+    first."""
+    H, vfy = env
+    rng = np.random.default_rng([seqs, cap])
+    hq, hkv, d = 4, 2, 64
+    counts = rng.integers(1, cap + 1, seqs)
+    res = rng.integers(0, 9, seqs)
+    lens = np.maximum(res * C - rng.integers(0, C, seqs), counts)
+    cu, cu_res, total = H.cu_from_counts(counts), H.cu_from_counts(res), int(res.sum())
+    pools = [records(rng, total + 1, hkv, d) for _ in range(2)]
+    slots, ids = rng.permutation(total + 1)[:total], np.concatenate([np.arange(r) for r in res])
+    q = B.to_bf16(rng.standard_normal((int(cu[-1]), hq, d)))
+    ctx = vfy.vfy_create(hq, hkv, d, max_seqs=seqs, max_queries_per_seq=cap, device=0)
+    try:
+        got, lse = attend(env, ctx, q, cu, pools, ids, slots, cu_res, lens)
+        assert vfy.vfy_get_status(ctx) == vfy.VFY_OK
+    finally:
+        ctx.close()
+    for b in range(seqs):
+        at, e = slice(cu[b], cu[b + 1]), slice(cu_res[b], cu_res[b + 1])
+        close(got[at], lse[at], *B.attend_packed_seq(O.bf16_to_f64(q[at]), *pools, ids[e], slots[e], int(lens[b])))
