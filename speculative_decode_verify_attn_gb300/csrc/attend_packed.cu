@@ -20,10 +20,12 @@
 //   one warp         bulk copies of the records (contiguous: no tensor map), and the tiles' geometry
 //   two warps        the MMA issuers of S and of O
 //
-// 17 rows, 16 q-heads over 4 KV heads, d = 128: 256K tokens in 59.6 us, 8K in 13.4, eight ragged sequences of 12K to 48K in 71.
-// A tile takes 1.8 thousand cycles. Shared memory moves 1.35 of them (V written and read 512, P and Q 450, records 290),
-// the schedulers issue 1.1 (K and V to fp16 a third, weights a third); the records alone, from HBM, would be 0.8.
+// 17 rows, 16 q-heads over 4 KV heads, d = 128: 256K tokens in 60.2 us, 8K in 13.4, eight ragged sequences of 12K to 48K in
+// 65.5. A tile takes 1.8 thousand cycles. Shared memory moves 1.35 of them (V written and read 512, P and Q 450, records
+// 290), the schedulers issue 1.2 (K and V to fp16 a third, weights a third); the records alone, from HBM, would be 0.8.
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "packed.cuh"
 #include "ptx.cuh"
@@ -189,19 +191,18 @@ __device__ __forceinline__ void unpack_tiles(const PackedAttnParams& p, const Wo
     if (!V) tc_fence_after();
 #pragma unroll
     for (int y = 0; y < HD / 64; ++y) {                  // 64 channels: two words of codes, four scales
-      // (both words loaded before the first store: the compiler keeps loads behind stores)
-      const uint4 codes[2] = {lds_u4(codes_at + at + 2 * y * kChunk * 16), lds_u4(codes_at + at + (2 * y + 1) * kChunk * 16)};
       uint32_t scales = lds_u32(scales_at + at + 4 * y);
       if (V && !keep) scales = 0u;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
+        const uint4 cw = lds_u4(codes_at + at + (2 * y + x) * kChunk * 16);
         const uint32_t two = e4m3_pair_f16(x == 0 ? scales & 0xffffu : scales >> 16);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {                    // 16 channels: one scale
           const uint32_t sc = __byte_perm(two, two, i == 0 ? 0x1010 : 0x3232);
           uint32_t out[8];
-          unpack_word(i == 0 ? codes[x].x : codes[x].z, sc, out);
-          unpack_word(i == 0 ? codes[x].y : codes[x].w, sc, out + 4);
+          unpack_word(i == 0 ? cw.x : cw.z, sc, out);
+          unpack_word(i == 0 ? cw.y : cw.w, sc, out + 4);
           if constexpr (V) {
 #pragma unroll
             for (int z = 0; z < 2; ++z)                  // 16-byte words of the 128-byte row
@@ -470,125 +471,134 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
     for (int r = 0; r < kRowsT / 2; ++r) l[r] = make_float2(0.f, 0.f);
     bool dead = false;                                   // a wait of this warp gave up
     int u = 0;                                           // tiles of this group so far
-    for (int j = grp; j < w.nt; j += 2, ++u) {
-      if (j % kBatch == grp && !mbar_wait_tested(&sh->geo_full[j / kBatch & 1], j / kBatch >> 1 & 1, abort, p.err)) dead = true;
-      if (!mbar_wait_tested(&sh->s_done[grp], u & 1, abort, p.err)) dead = true;
-      dead = __any_sync(0xffffffffu, dead);
-      tc_fence_after();
-      uint32_t s[kRowsT];
-      const int geo = j % (2 * kBatch);
-      bool pv = u == 0 || mbar_test_wait(&sh->pv_done[grp], (u - 1) & 1);
-      pv = __all_sync(0xffffffffu, pv);
-      bool stop = false;                                 // a warp of the group gave up
-      for (bool again = false;; again = true) {
-        // s = score - reference (log2)
+    // R: rows of a thread. Up to 32 rows in all need no more than 16 (4 rows over 256K 49 us, with 36 of a thread 54.7; the second
+    // loop costs the first half a microsecond: 17 rows 59.7 -> 60.2).
+    auto tiles = [&](auto rows_of_thread) {
+      constexpr int R = decltype(rows_of_thread)::value;
+      for (int j = grp; j < w.nt; j += 2, ++u) {
+        if (j % kBatch == grp && !mbar_wait_tested(&sh->geo_full[j / kBatch & 1], j / kBatch >> 1 & 1, abort, p.err)) dead = true;
+        if (!mbar_wait_tested(&sh->s_done[grp], u & 1, abort, p.err)) dead = true;
+        dead = __any_sync(0xffffffffu, dead);
+        tc_fence_after();
+        uint32_t s[R];
+        const int geo = j % (2 * kBatch);
+        bool pv = u == 0 || mbar_test_wait(&sh->pv_done[grp], (u - 1) & 1);
+        pv = __all_sync(0xffffffffu, pv);
+        bool stop = false;                                 // a warp of the group gave up
+        for (bool again = false;; again = true) {
+          // s = score - reference (log2)
 #pragma unroll
-        for (int r = 0; r < 32; r += 8) tmem_ld8_async(s_at + row_of(r), s + r);
-        tmem_ld4_async(s_at + row_hi, s + 32);
-        tmem_wait_ld(s);
-        if (!sh->plain[geo]) {
-          // Rows from n_min on attend this lane's key: row n is of block query (row0 + n) / G, at position p0 + that.
-          const int base = sh->base[geo][key / kChunk], pos = base + key % kChunk;
-          const int4 gm = sh->geom[grp];
-          int n_min = 0;
-          if (base < 0 || pos >= gm.x)
-            n_min = kMaxN;
-          else if (pos > gm.y)
-            n_min = min(static_cast<long long>(kMaxN), max(0ll, static_cast<long long>(pos - gm.y) * p.group - gm.z));
+          for (int r = 0; r < R / 8 * 8; r += 8) tmem_ld8_async(s_at + row_of(r), s + r);
+          if constexpr (R % 8 != 0) tmem_ld4_async(s_at + row_hi, s + 32);
+          tmem_wait_ld(s);
+          if (!sh->plain[geo]) {
+            // Rows from n_min on attend this lane's key: row n is of block query (row0 + n) / G, at position p0 + that.
+            const int base = sh->base[geo][key / kChunk], pos = base + key % kChunk;
+            const int4 gm = sh->geom[grp];
+            int n_min = 0;
+            if (base < 0 || pos >= gm.x)
+              n_min = kMaxN;
+            else if (pos > gm.y)
+              n_min = min(static_cast<long long>(kMaxN), max(0ll, static_cast<long long>(pos - gm.y) * p.group - gm.z));
 #pragma unroll
-          for (int r = 0; r < kRowsT; ++r) s[r] = row_of(r) >= n_min ? s[r] : 0xff800000u;   // 2^-inf = 0
-        }
-        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int r = 0; r < kRowsT; r += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(&sh->neg_ref[grp][row_of(r)]);
-          const float2 a = fma_f32x2(pair(s, r), sc2, make_float2(f.x, f.y));
-          const float2 b = fma_f32x2(pair(s, r + 2), sc2, make_float2(f.z, f.w));
-          s[r] = __float_as_uint(a.x);
-          s[r + 1] = __float_as_uint(a.y);
-          s[r + 2] = __float_as_uint(b.x);
-          s[r + 3] = __float_as_uint(b.y);
-          top[r / 2 % 4] = fmaxf(fmaxf(top[r / 2 % 4], a.x), a.y);
-          top[r / 2 % 4 + 1] = fmaxf(fmaxf(top[r / 2 % 4 + 1], b.x), b.y);
-        }
-        if (again) break;
-        const bool moves = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > kLimit;
-        if (all_have && !named_any(bar, kGroup, moves || dead)) break;
-        // A row's weights would pass the limit, or a row has no reference yet: the rows' maxima over the tile, new
-        // references for those rows, their sums and O scaled, and once more. All warps of the group come here or none.
-        stop = named_any(bar, kGroup, dead);
-        if (stop) break;
-#pragma unroll
-        for (int r = 0; r < kRowsT; ++r) {
-          const float m = warp_max(__uint_as_float(s[r]));
-          if (lane == 0) sh->part[grp][wq][row_of(r)] = m;
-        }
-        named_sync(bar, kGroup);
-        const int rows = sh->geom[grp].w;
-        if (tg < rows) {
-          const float m = fmaxf(fmaxf(sh->part[grp][0][tg], sh->part[grp][1][tg]),
-                                fmaxf(sh->part[grp][2][tg], sh->part[grp][3][tg]));
-          float a = 1.f;
-          if (m > (has_ref ? kLimit : -INFINITY)) {
-            const float old = -sh->neg_ref[grp][tg], ref = old + (m - kTop);
-            a = has_ref ? ex2_approx(old - ref) : 0.f;
-            sh->neg_ref[grp][tg] = -ref;
-            has_ref = true;
+            for (int r = 0; r < R; ++r) s[r] = row_of(r) >= n_min ? s[r] : 0xff800000u;   // 2^-inf = 0
           }
-          sh->alpha[grp][tg] = a;
-        }
-        all_have = !named_any(bar, kGroup, !has_ref);
-        if (u > 0) {
-          dead = !__all_sync(0xffffffffu, mbar_wait_tested(&sh->pv_done[grp], (u - 1) & 1, abort, p.err));
-          pv = true;
-          tc_fence_after();
-          if (!dead) {
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int r = 0; r < R; r += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(&sh->neg_ref[grp][row_of(r)]);
+            const float2 a = fma_f32x2(pair(s, r), sc2, make_float2(f.x, f.y));
+            const float2 b = fma_f32x2(pair(s, r + 2), sc2, make_float2(f.z, f.w));
+            s[r] = __float_as_uint(a.x);
+            s[r + 1] = __float_as_uint(a.y);
+            s[r + 2] = __float_as_uint(b.x);
+            s[r + 3] = __float_as_uint(b.y);
+            top[r / 2 % 4] = fmaxf(fmaxf(top[r / 2 % 4], a.x), a.y);
+            top[r / 2 % 4 + 1] = fmaxf(fmaxf(top[r / 2 % 4 + 1], b.x), b.y);
+          }
+          if (again) break;
+          const bool moves = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > kLimit;
+          if (all_have && !named_any(bar, kGroup, moves || dead)) break;
+          // A row's weights would pass the limit, or a row has no reference yet: the rows' maxima over the tile, new
+          // references for those rows, their sums and O scaled, and once more. All warps of the group come here or none.
+          stop = named_any(bar, kGroup, dead);
+          if (stop) break;
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const float m = warp_max(__uint_as_float(s[r]));
+            if (lane == 0) sh->part[grp][wq][row_of(r)] = m;
+          }
+          named_sync(bar, kGroup);
+          const int rows = sh->geom[grp].w;
+          if (tg < rows) {
+            const float m = fmaxf(fmaxf(sh->part[grp][0][tg], sh->part[grp][1][tg]),
+                                  fmaxf(sh->part[grp][2][tg], sh->part[grp][3][tg]));
+            float a = 1.f;
+            if (m > (has_ref ? kLimit : -INFINITY)) {
+              const float old = -sh->neg_ref[grp][tg], ref = old + (m - kTop);
+              a = has_ref ? ex2_approx(old - ref) : 0.f;
+              sh->neg_ref[grp][tg] = -ref;
+              has_ref = true;
+            }
+            sh->alpha[grp][tg] = a;
+          }
+          all_have = !named_any(bar, kGroup, !has_ref);
+          if (u > 0) {
+            dead = !__all_sync(0xffffffffu, mbar_wait_tested(&sh->pv_done[grp], (u - 1) & 1, abort, p.err));
+            pv = true;
+            tc_fence_after();
+            if (!dead) {
 #pragma unroll 1
-            for (int r = 0; r < kRowsT; r += 4) {
-              const int row = row_of(r);
-              if (row >= rows) break;
-              uint32_t o[4];
-              tmem_ld4_async(s_at + (kColO - kColS) + row, o);
-              tmem_wait_ld(o);
+              for (int r = 0; r < R; r += 4) {
+                const int row = row_of(r);
+                if (row >= rows) break;
+                uint32_t o[4];
+                tmem_ld4_async(s_at + (kColO - kColS) + row, o);
+                tmem_wait_ld(o);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * sh->alpha[grp][row + e]);
-              tmem_st4_async(s_at + (kColO - kColS) + row, o);
+                for (int e = 0; e < 4; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * sh->alpha[grp][row + e]);
+                tmem_st4_async(s_at + (kColO - kColS) + row, o);
+              }
+              tmem_wait_st();
             }
-            tmem_wait_st();
-          }
 #pragma unroll
-          for (int r = 0; r < kRowsT; r += 2) {
-            if (row_of(r) < rows) {
-              const float2 a = *reinterpret_cast<const float2*>(&sh->alpha[grp][row_of(r)]);
-              l[r / 2].x *= a.x;
-              l[r / 2].y *= a.y;
+            for (int r = 0; r < R; r += 2) {
+              if (row_of(r) < rows) {
+                const float2 a = *reinterpret_cast<const float2*>(&sh->alpha[grp][row_of(r)]);
+                l[r / 2].x *= a.x;
+                l[r / 2].y *= a.y;
+              }
             }
           }
         }
-      }
-      if (stop) break;
-      tc_fence_before();
-      if (lane == 0) mbar_arrive(&sh->s_free[grp]);
-      // P = 2^s, and its sums
-      if (!pv) dead = !__all_sync(0xffffffffu, mbar_wait_tested(&sh->pv_done[grp], (u - 1) & 1, abort, p.err));
-      auto weigh4 = [&](int r) {                         // four rows' weights, as fp16
-        const float2 a = make_float2(ex2_approx(__uint_as_float(s[r])), ex2_approx(__uint_as_float(s[r + 1])));
-        const float2 b = make_float2(ex2_approx(__uint_as_float(s[r + 2])), ex2_approx(__uint_as_float(s[r + 3])));
-        l[r / 2] = add_f32x2(l[r / 2], a);
-        l[r / 2 + 1] = add_f32x2(l[r / 2 + 1], b);
-        return make_uint2(pack_f16(a.x, a.y), pack_f16(b.x, b.y));
-      };
-      // (eight rows are a 16-byte word of the key's; 64 rows a box)
+        if (stop) break;
+        tc_fence_before();
+        if (lane == 0) mbar_arrive(&sh->s_free[grp]);
+        // P = 2^s, and its sums
+        if (!pv) dead = !__all_sync(0xffffffffu, mbar_wait_tested(&sh->pv_done[grp], (u - 1) & 1, abort, p.err));
+        auto weigh4 = [&](int r) {                         // four rows' weights, as fp16
+          const float2 a = make_float2(ex2_approx(__uint_as_float(s[r])), ex2_approx(__uint_as_float(s[r + 1])));
+          const float2 b = make_float2(ex2_approx(__uint_as_float(s[r + 2])), ex2_approx(__uint_as_float(s[r + 3])));
+          l[r / 2] = add_f32x2(l[r / 2], a);
+          l[r / 2 + 1] = add_f32x2(l[r / 2 + 1], b);
+          return make_uint2(pack_f16(a.x, a.y), pack_f16(b.x, b.y));
+        };
+        // (eight rows are a 16-byte word of the key's; 64 rows a box)
 #pragma unroll
-      for (int r = 0; r < 32; r += 8) {
-        const uint2 a = weigh4(r), b = weigh4(r + 4);
-        sts_u4(prow ^ (r << 2), make_uint4(a.x, a.y, b.x, b.y));
+        for (int r = 0; r < R / 8 * 8; r += 8) {
+          const uint2 a = weigh4(r), b = weigh4(r + 4);
+          sts_u4(prow ^ (r << 2), make_uint4(a.x, a.y, b.x, b.y));
+        }
+        if constexpr (R % 8 != 0) sts_u2((prow ^ (half << 4)) + C::kBoxBytes + half * 8, weigh4(32));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && !dead) mbar_arrive(&sh->p_ready[grp]);
       }
-      sts_u2((prow ^ (half << 4)) + C::kBoxBytes + half * 8, weigh4(32));
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0 && !dead) mbar_arrive(&sh->p_ready[grp]);
-    }
+    };
+    if (w.rows <= 32)
+      tiles(std::integral_constant<int, 16>());
+    else
+      tiles(std::integral_constant<int, kRowsT>());
     // ---- epilogue: the groups' sums and O merged into the split's partial (m, l, O not normalised) ----
     const int4 gm = sh->geom[grp];
     const int b = sh->seq;

@@ -394,7 +394,7 @@ int packed_tile_rows();
 cudaError_t launch_attend_packed(const PackedAttnParams& p, int num_seqs, cudaStream_t stream);
 // The same for contexts of at most kPackedFewRows block rows (max_q * G). A single split writes p.out / p.lse itself. us of
 // one layer of 4 KV heads over 8K, 64K and 256K tokens, this kernel against the other: 4 rows 8.3 / 17.3 / 36.5 against
-// 10.9 / 22.3 / 54.7, 16 rows 11.5 / 19.8 / 48.0 against 11.5 / 22.8 / 55.2. (Its registers end at 16 rows.)
+// 10.0 / 19.9 / 49.1, 16 rows 11.5 / 19.8 / 48.0 against 10.3 / 20.6 / 49.7. (Its registers end at 16 rows.)
 constexpr int kPackedFewRows = 16;
 cudaError_t launch_attend_packed_few(const PackedAttnParams& p, int num_seqs, cudaStream_t stream);
 
@@ -493,7 +493,7 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int num_seqs, int 
 }
 
 // The sequences of a batch by the length of their resident lists, longest first, so that the CTAs of long ones start first
-// (batches of up to 32; larger ones keep their order). 8 ragged sequences of 12K to 48K: 70.5 -> 67.5 us. Returns place `z` and its metadata, one round trip to memory for a
+// (batches of up to 32; larger ones keep their order). 8 ragged sequences of 12K to 48K: 70.5 us without, 67.5 with. Returns place `z` and its metadata, one round trip to memory for a
 // batch of up to 32, by all 32 lanes of a converged warp.
 struct SequenceMeta {
   int b, c0, c1, r0, r1, len;
