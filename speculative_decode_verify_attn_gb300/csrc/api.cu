@@ -192,14 +192,14 @@ vfy_status vfy_create(const vfy_config* cfg_in, int device, vfy_ctx** out) {
             cudaMalloc(&ctx->tree_counters, cfg.max_seqs * sizeof(unsigned int)) == cudaSuccess &&
             cudaMalloc(&ctx->tree_pieces, ctx->num_sms * sizeof(vfy::TreePiece)) == cudaSuccess &&
             cudaMalloc(&ctx->sample_stats, (ctx->accept_rows_cap + kSampleCtas * ctx->num_sms) * sizeof(float4)) == cudaSuccess &&
-            cudaMalloc(&ctx->sample_keys, 3 * cfg.max_seqs * sizeof(unsigned long long)) == cudaSuccess &&
+            cudaMalloc(&ctx->sample_keys, cfg.max_seqs * sizeof(unsigned long long)) == cudaSuccess &&
             cudaMalloc(&ctx->sample_counters, cfg.max_seqs * sizeof(unsigned int)) == cudaSuccess &&
             cudaMalloc(&ctx->err, sizeof(int)) == cudaSuccess;
   if (ok)
     ok = cudaMemset(ctx->accept_keys, 0, ctx->accept_rows_cap * sizeof(unsigned long long)) == cudaSuccess &&
          cudaMemset(ctx->accept_counter, 0, sizeof(unsigned int)) == cudaSuccess &&
          cudaMemset(ctx->tree_counters, 0, cfg.max_seqs * sizeof(unsigned int)) == cudaSuccess &&
-         cudaMemset(ctx->sample_keys, 0, 3 * cfg.max_seqs * sizeof(unsigned long long)) == cudaSuccess &&
+         cudaMemset(ctx->sample_keys, 0, cfg.max_seqs * sizeof(unsigned long long)) == cudaSuccess &&
          cudaMemset(ctx->sample_counters, 0, cfg.max_seqs * sizeof(unsigned int)) == cudaSuccess &&
          cudaMemset(ctx->err, 0, sizeof(int)) == cudaSuccess &&
          cudaMemset(ctx->part_ml, 0, parts * 2 * sizeof(float)) == cudaSuccess &&
@@ -1295,7 +1295,7 @@ vfy_status vfy_accept_sampled(vfy_ctx* ctx, const void* logits, int logits_type,
   p.max_rows = max_rows;
   // Segments of whole 16-byte words, at least 4096 entries (one round of loads of a CTA), at most 32 of a row (a warp merges
   // them), and no more than run at once, four CTAs per SM, over all rows.
-  p.parts = clampi(ceil_div(kSampleCtas * ctx->num_sms, max_rows), 1, std::min(32, ceil_div(vocab, 4096)));
+  p.parts = clampi(static_cast<int>(kSampleCtas * ctx->num_sms / max_rows), 1, std::min(32, ceil_div(vocab, 4096)));
   p.seg = (ceil_div(vocab, p.parts) + 7) & ~7;
   p.parts = ceil_div(vocab, p.seg);
   // The draw: at least one round of loads of a CTA, and no more than run at once, two CTAs per SM over the sequences.

@@ -11,9 +11,9 @@
 // part a lane), finds n, and races its segment of row n; the last one to finish (a ticket) writes the outputs. What does not
 // wait for the first kernel (drafts, their probabilities, the first noise) is read before it is over.
 //
-// One sequence of 17 rows of 131072 fp32 logits takes 9.2 us, of which 1.5 are bytes: two kernels' chains of look-ups.
-// 16 sequences of 164 rows of 100003 bf16 logits take 16.2 us (46 MB, 2.8 TB/s): the first kernel ends at 3 instructions an
-// entry, the second at 60 for one row a sequence.
+// One sequence of 17 rows of 131072 fp32 logits takes 9.1 us, of which 1.5 are bytes: two kernels' chains of look-ups.
+// 16 sequences of 164 rows of 100003 bf16 logits take 18.8 us (46 MB, 2.4 TB/s): the first kernel ends at 3 instructions an
+// entry, the second at 45 for one row a sequence; with the argmax and the race over p in its loop, and no loads ahead, 20.2 us.
 #include <cuda_bf16.h>
 
 #include "argmax.cuh"
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kDrawThreads) sample_draw_kernel(const SampleP
   __shared__ int s_first;
   __shared__ Stat s_stat;
   __shared__ unsigned long long s_greedy;
-  __shared__ unsigned long long s_keys[3][kDrawWarps];
+  __shared__ unsigned long long s_keys[kDrawWarps];
   __shared__ bool s_last;
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -430,57 +430,56 @@ __global__ void __launch_bounds__(kDrawThreads) sample_draw_kernel(const SampleP
 
   int bonus = 0;
   if (c.hi > 0.f) {
-    const bool refused = n < depth;
-    const int draft = refused ? p.drafts[d0 + n] : -1;
-    const float* qs =
-        refused && p.probs != nullptr && draft >= 0 && draft < p.vocab ? p.probs + static_cast<size_t>(d0 + n) * p.vocab : nullptr;
+    const int draft = n < depth ? p.drafts[d0 + n] : -1;
+    const float* qs = draft >= 0 && draft < p.vocab && p.probs != nullptr ? p.probs + static_cast<size_t>(d0 + n) * p.vocab : nullptr;
     const float inv_z = st.z > 0.f ? 1.f / st.z : 0.f;
-    // The best of w (where a draft was refused), of p and of the logits, each with its first index.
-    float best[3] = {0.f, 0.f, -INFINITY};
-    int index[3] = {-1, -1, -1};
+    // max(p - taken, 0) / E, 0 where E is no exponential
+    auto race = [&](float x, float e, float taken) {
+      const float w = fmaxf(weight(x, st.m, c) * inv_z - taken, 0.f);
+      // (a factor to 2^-23 in place of a division, where it is no denormal)
+      if (e > 1e-36f && e < 1e36f) return w * rcp_approx(e);
+      return e > 0.f && e < INFINITY ? w / e : 0.f;
+    };
+    // The largest, with its first index, of a thread, a warp, the CTA (thread 0).
+    auto cta_max = [&](unsigned long long key) {
+      key = warp_umax64(key);
+      if (lane == 0) s_keys[warp] = key;
+      __syncthreads();
+      return warp == 0 ? warp_umax64(lane < kDrawWarps ? s_keys[lane] : 0ull) : 0ull;
+    };
+    float best = 0.f;
+    int index = -1;
+    // (a round's entries are asked for before the one before is weighed)
+    float ps[kUnroll];
+    auto load_taken = [&](int i0) {
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        const int v = i0 + k * kDrawThreads;
+        ps[k] = qs != nullptr && v < v1 ? qs[v] : (v == draft ? 1.f : 0.f);
+      }
+    };
+    if (depth != 0) load_logits(n, v0 + threadIdx.x);
+    load_taken(v0 + threadIdx.x);
     for (int i0 = v0 + threadIdx.x; i0 < v1; i0 += kDrawThreads * kUnroll) {
-      const bool first = i0 < v0 + kDrawThreads * kUnroll;
-      if (!first) load_noise(i0);
-      if (!first || depth != 0) load_logits(n, i0);
-      float ps[kUnroll];
+      float x[kUnroll], e[kUnroll], taken[kUnroll];
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k) {
-        const int v = i0 + k * kDrawThreads;
-        const bool in = v < v1;
-        ps[k] = in && qs != nullptr ? qs[v] : (v == draft ? 1.f : 0.f);
+      for (int k = 0; k < kUnroll; ++k) x[k] = xs[k], e[k] = es[k], taken[k] = ps[k];
+      const int next = i0 + kDrawThreads * kUnroll;
+      if (next < v1) {
+        load_noise(next);
+        load_logits(n, next);
+        load_taken(next);
       }
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) {
-        const int v = i0 + k * kDrawThreads;
-        const float prob = weight(xs[k], st.m, c) * inv_z, rest = fmaxf(prob - ps[k], 0.f);
-        // (a factor to 2^-23 in place of two divisions, where it is no denormal)
-        float race = 0.f, left = 0.f;
-        if (es[k] > 1e-36f && es[k] < 1e36f) {
-          const float r = rcp_approx(es[k]);
-          race = prob * r;
-          left = rest * r;
-        } else if (es[k] > 0.f && es[k] < INFINITY) {
-          race = prob / es[k];
-          left = rest / es[k];
-        }
-        if (refused && left > best[0]) best[0] = left, index[0] = v;
-        if (race > best[1]) best[1] = race, index[1] = v;
-        if (xs[k] > best[2]) best[2] = xs[k], index[2] = v;
+        const float t = race(x[k], e[k], taken[k]);
+        if (t > best) best = t, index = i0 + k * kDrawThreads;
       }
     }
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      const unsigned long long key = warp_umax64(index[k] >= 0 ? pack(best[k], index[k]) : 0ull);
-      if (lane == 0) s_keys[k][warp] = key;
-    }
-    __syncthreads();
-    if (warp < 3) {
-      const unsigned long long key = warp_umax64(lane < kDrawWarps ? s_keys[warp][lane] : 0ull);
-      if (lane == 0 && key != 0ull) atomicMax(p.keys + 3 * b + warp, key);
-    }
-    __syncthreads();
+    unsigned long long key = cta_max(index >= 0 ? pack(best, index) : 0ull);
     if (threadIdx.x == 0) {
-      // (the barrier orders the warps' keys before this add, which releases them; the finishing CTA acquires)
+      if (key != 0ull) atomicMax(p.keys + b, key);
+      // (the add releases the key; the finishing CTA acquires)
       unsigned int ticket;
       asm volatile("fence.acq_rel.gpu;\n\tatom.add.relaxed.gpu.global.u32 %0, [%1], 1;"
                    : "=r"(ticket)
@@ -491,15 +490,28 @@ __global__ void __launch_bounds__(kDrawThreads) sample_draw_kernel(const SampleP
     __syncthreads();
     if (!s_last) return;
     asm volatile("fence.acq_rel.gpu;" ::: "memory");
-    bonus = 0;                            // nothing to draw and no logit above -inf: token 0
-    for (int k = 2; k >= 0; --k) {
-      const unsigned long long key = __ldcg(p.keys + 3 * b + k);
-      if (key != 0ull) bonus = unpack_index(key);
+    key = __ldcg(p.keys + b);
+    // Nothing left to draw, which is rare (the drafter's q nowhere below p, noise that is none): this CTA alone draws from p,
+    // and where that leaves nothing either takes the largest logit, or token 0.
+    for (int mode = n < depth ? 0 : 1; mode < 2 && key == 0ull; ++mode) {
+      for (int v = threadIdx.x; v < p.vocab; v += kDrawThreads) {
+        const float x = fmaxf(entry<BF16>(row_at<BF16>(p, r0 + n), v), -INFINITY);
+        const float t = mode == 0 ? race(x, noise[v], 0.f) : x;
+        if (t > (mode == 0 ? 0.f : -INFINITY)) key = umax64(key, pack(t, v));
+      }
+      __syncthreads();
+      key = cta_max(key);
+      if (threadIdx.x == 0) s_greedy = key;
+      __syncthreads();
+      key = s_greedy;
     }
+    bonus = key != 0ull ? unpack_index(key) : 0;
     __syncthreads();
     // Leave the workspace as this call found it.
-    if (threadIdx.x < 3) p.keys[3 * b + threadIdx.x] = 0ull;
-    if (threadIdx.x == 3) p.counters[b] = 0u;
+    if (threadIdx.x == 0) {
+      p.keys[b] = 0ull;
+      p.counters[b] = 0u;
+    }
   } else {
     if (blockIdx.x != 0) return;
     bonus = unpack_index(greedy);

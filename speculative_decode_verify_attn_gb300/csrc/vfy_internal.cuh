@@ -417,7 +417,7 @@ struct SampleParams {
   int32_t* bonus;
   int32_t* committed;
   float4* stats;              // [max_rows * parts] workspace
-  unsigned long long* keys;   // [3 * max_seqs] workspace, zero between calls
+  unsigned long long* keys;   // [max_seqs] workspace, zero between calls
   unsigned int* counters;     // [max_seqs] workspace, zero between calls
   int* err;
 };

@@ -360,3 +360,27 @@ def test_drafts_that_are_not_there_are_not_read(env, counts, cu):
         check(env, ctx, c)
     finally:
         ctx.close()
+
+
+@pytest.mark.parametrize("V", [300, 9000, 40001])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_nothing_left_in_any_segment(env, V, bf16):
+    """A drafter's q that is nowhere below p, and noise that is none: p is drawn from, or the largest logit taken, by whichever
+    CTA comes last."""
+    rng = np.random.default_rng([V, bf16])
+    ctx = env[1].vfy_create(4, 1, 64, max_seqs=3, max_queries_per_seq=4, device=0)
+    try:
+        c = make(rng, [4, 1, 2], V, bf16)
+        c["probs"][:] = 1.0
+        c["uniform"][:] = 0.999
+        for kind in range(3):
+            if kind == 1:
+                c["noise"][1:] = 0.0                            # nothing to draw at all
+            if kind == 2:
+                c["noise"][:] = np.nan
+                c["noise"][0, V // 2] = 1.0                     # one token alone
+            want = B.accept_sampled(**c)
+            if kind or want[3] > 2.0 ** -18:
+                check(env, ctx, c, bf16=bf16)
+    finally:
+        ctx.close()
