@@ -1100,6 +1100,9 @@ vfy_status vfy_append_full_packed(vfy_ctx* ctx, const uint16_t* k_new, const uin
   p.num_sms = ctx->num_sms;
   p.k_scale = k_scale;
   p.v_scale = v_scale;
+  auto reciprocal = [](float g) { return g > 7.9e-31f && g < 1.2e30f ? 1.f / g : 0.f; };   // 2^-100 .. 2^100
+  p.k_inv = reciprocal(k_scale);
+  p.v_inv = reciprocal(v_scale);
   p.err = ctx->err;
   VFY_CUDA(vfy::launch_append_packed(p, s));
   ++ctx->launches;

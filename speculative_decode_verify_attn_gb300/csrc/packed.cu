@@ -3,8 +3,8 @@
 // [64 tokens][d / 16]; a value is g * s * e, e a 4-bit float e2m1. Codes are laid out by 32 channels, so that neighbouring
 // tokens' 16-byte words are neighbours: a warp that reads one word for each of 32 tokens reads 512 bytes in a row.
 //
-// Both kernels give one thread one group of 16 channels: its scale and its 8 bytes of codes. s * e has 6 significant bits,
-// so that the read value is exact in bf16 where g is a power of two.
+// The append gives one thread one group of 16 channels: its scale and its 8 bytes of codes. s * e has 6 significant bits, so
+// that the read value is exact in bf16 where g is a power of two.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -19,7 +19,7 @@ constexpr int kThreads = 256;
 
 // Jobs of a token: K then V, KV heads, groups of a head; a CTA takes as many whole tokens as it has threads for, and goes
 // from tokens to tokens, the next ones' values on their way while these are packed: three CTAs an SM (8 x 1024 tokens of 4 KV
-// heads of 128 take 13.4 us; a CTA for every few tokens 4 us more). Threads of a token are neighbours, and
+// heads of 128 take 12.7 us; a CTA for every few tokens 4 us more). Threads of a token are neighbours, and
 // d / 16 is a multiple of 4: the two groups of a 16-byte code word are a lane and the next, and four lanes have four
 // neighbouring scales.
 __host__ __device__ __forceinline__ int jobs_of(int hkv, int head_dim) { return 2 * hkv * (head_dim / 16); }
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_packed_kernel(const Packed
       float2 x[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
-      codes = pack_group(x, is_v ? p.v_scale : p.k_scale, &scale);
+      codes = pack_group(x, is_v ? p.v_scale : p.k_scale, is_v ? p.v_inv : p.k_inv, &scale);
     }
     // A pair of lanes holds a 16-byte word of codes; the even one writes it.
     const uint32_t ox = __shfl_xor_sync(0xffffffffu, codes.x, 1), oy = __shfl_xor_sync(0xffffffffu, codes.y, 1);
@@ -150,7 +150,6 @@ __global__ void __launch_bounds__(kThreads, 3) append_packed_kernel(const Packed
 
 template <int HD>
 __global__ void __launch_bounds__(kThreads) unpack_kernel(const UnpackParams p) {
-  constexpr int kGroups = HD / 16;
   pdl_launch_dependents();
   pdl_wait();
   // One CTA row (blockIdx.x) per (entry, KV head); K and V by blockIdx.y.
@@ -165,31 +164,26 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(const UnpackParams p) 
   const uint8_t* rec = (is_v ? p.v_pool : p.k_pool) + (static_cast<size_t>(slot) * p.hkv + h) * kPackedBytes<HD>;
   uint16_t* out = (is_v ? p.v_out : p.k_out) + static_cast<size_t>(blockIdx.x) * kChunk * HD;
   const float gs = is_v ? p.v_scale : p.k_scale;
-  constexpr int kMine = kChunk * kGroups / kThreads;
-  uint2 codes_of[kMine];
-  uint32_t scale_of[kMine];
+  // Eight channels a thread and step: 4 bytes of codes in, 16 bytes out, side by side in a warp.
+  constexpr int kEights = HD / 8, kMine = kChunk * kEights / kThreads;
+  uint32_t codes[kMine], scale[kMine];
 #pragma unroll
   for (int y = 0; y < kMine; ++y) {        // (all loads before the first store)
-    const int x = threadIdx.x + y * kThreads, row = x / kGroups, g = x % kGroups;
-    codes_of[y] = *reinterpret_cast<const uint2*>(rec + (static_cast<size_t>(g / 2) * kChunk + row) * 16 + (g & 1) * 8);
-    scale_of[y] = rec[kChunk * (HD / 2) + x];
+    const int x = threadIdx.x + y * kThreads, row = x / kEights, u = x % kEights;
+    codes[y] = *reinterpret_cast<const uint32_t*>(rec + (u / 4 * kChunk + row) * 16 + u % 4 * 4);
+    scale[y] = rec[kChunk * (HD / 2) + x / 2];
   }
 #pragma unroll
   for (int y = 0; y < kMine; ++y) {
-    const int x = threadIdx.x + y * kThreads;
-    const uint2 codes = codes_of[y];
-    const float s = e4m3_value(scale_of[y]) * gs;
-    uint32_t o[8];
+    const float s = e4m3_value(scale[y]) * gs;
+    uint32_t o[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t byte = ((e < 4 ? codes.x : codes.y) >> (8 * (e & 3))) & 0xffu;
-      const float2 v = e2m1_pair(byte);
+    for (int e = 0; e < 4; ++e) {
+      const float2 v = e2m1_pair((codes[y] >> (8 * e)) & 0xffu);
       const __nv_bfloat162 h2 = __floats2bfloat162_rn(v.x * s, v.y * s);
       o[e] = *reinterpret_cast<const uint32_t*>(&h2);
     }
-    uint4* dst = reinterpret_cast<uint4*>(out + static_cast<size_t>(x) * 16);
-    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    *reinterpret_cast<uint4*>(out + static_cast<size_t>(threadIdx.x + y * kThreads) * 8) = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 

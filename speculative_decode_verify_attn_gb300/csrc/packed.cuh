@@ -72,53 +72,56 @@ __device__ __forceinline__ uint32_t e4m3_of(float x) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(fminf(x, 448.f)));
   return r & 0xffu;
 }
-// Codes nearest to lo (low 4 bits) and hi: ties to the even code, at most 6 in size.
-__device__ __forceinline__ uint32_t e2m1_of(float lo, float hi) {
+// The codes nearest to eight values (the first in the low 4 bits): ties to the even code, at most 6 in size.
+__device__ __forceinline__ uint32_t e2m1_of(const float2& a, const float2& b, const float2& c, const float2& d) {
   uint32_t r;
-  asm("{\n\t.reg .b8 c;\n\tcvt.rn.satfinite.e2m1x2.f32 c, %2, %1;\n\tmov.b32 %0, {c, c, c, c};\n\t}"
+  asm("{\n\t.reg .b8 x0, x1, x2, x3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 x0, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 x1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 x2, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 x3, %8, %7;\n\t"
+      "mov.b32 %0, {x0, x1, x2, x3};\n\t}"
       : "=r"(r)
-      : "f"(lo), "f"(hi));
-  return r & 0xffu;
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y), "f"(d.x), "f"(d.y));
+  return r;
 }
 
 // 16 values x to the codes of x / g and their scale. Quotients are rounded as IEEE divisions: the scale's quotient can lie on
 // a tie of e4m3 only if it is exact, and so can a value's on a tie of e2m1. `x`: pairs.
 //
 // A quotient comes from the rounded reciprocal, one remainder and one correction (Markstein's division), two at a time
-// (with divisions the append of 8 x 1024 tokens took 16.2 us instead of 13.4). That is exact where nothing overflows and no
+// (with divisions the append of 8 x 1024 tokens took 16.2 us instead of 12.7). That is exact where nothing overflows and no
 // remainder underflows: g within 2^-100 .. 2^100, s is 2^-9 .. 448 and below 448 |x / g| is at most a little over 6 s, and a
 // value whose remainder underflows is far below a code. Anything else, infinities among it, is divided.
 __device__ __forceinline__ float2 quotients(float2 v, float2 minus_by, float2 r) {
   const float2 q = mul_f32x2(v, r);
   return fma_f32x2(fma_f32x2(q, minus_by, v), r, q);
 }
-__device__ __forceinline__ uint2 pack_group(float2 (&x)[8], float g, uint32_t* scale) {
+// `inv`: 1 / g rounded, 0 where g is out of that range.
+__device__ __forceinline__ uint2 pack_group(float2 (&x)[8], float g, float inv, uint32_t* scale) {
   float top = 0.f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) top = fmaxf(fmaxf(top, fabsf(x[e].x)), fabsf(x[e].y));
-  top = __fdiv_rn(top, g);                 // (the quotients' largest: rounding keeps order)
-  *scale = e4m3_of(__fdiv_rn(top, 6.f));
-  const float s = e4m3_value(*scale);
-  uint2 codes = make_uint2(0u, 0u);
-  if (!(s > 0.f)) return codes;
-  if (top < INFINITY && g > 7.9e-31f && g < 1.2e30f) {
-    const float rg = __frcp_rn(g), rs = __frcp_rn(s);
+  if (inv != 0.f && top < 1e38f && top * inv < 1e38f) {
+    // (the quotients' largest is the largest's: rounding keeps order)
+    const float2 most = quotients(make_float2(top, 0.f), make_float2(-g, -g), make_float2(inv, inv));
+    constexpr float kSixth = 1.f / 6.f;
+    *scale = e4m3_of(quotients(most, make_float2(-6.f, -6.f), make_float2(kSixth, kSixth)).x);
+    const float s = e4m3_value(*scale);
+    if (!(s > 0.f)) return make_uint2(0u, 0u);
+    const float rs = __frcp_rn(s);
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      x[e] = quotients(quotients(x[e], make_float2(-g, -g), make_float2(rg, rg)), make_float2(-s, -s), make_float2(rs, rs));
+      x[e] = quotients(quotients(x[e], make_float2(-g, -g), make_float2(inv, inv)), make_float2(-s, -s), make_float2(rs, rs));
   } else {
+    *scale = e4m3_of(__fdiv_rn(__fdiv_rn(top, g), 6.f));
+    const float s = e4m3_value(*scale);
+    if (!(s > 0.f)) return make_uint2(0u, 0u);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       x[e].x = __fdiv_rn(__fdiv_rn(x[e].x, g), s);
       x[e].y = __fdiv_rn(__fdiv_rn(x[e].y, g), s);
     }
   }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    codes.x |= e2m1_of(x[e].x, x[e].y) << (8 * e);
-    codes.y |= e2m1_of(x[e + 4].x, x[e + 4].y) << (8 * e);
-  }
-  return codes;
+  return make_uint2(e2m1_of(x[0], x[1], x[2], x[3]), e2m1_of(x[4], x[5], x[6], x[7]));
 }
 
 }  // namespace vfy

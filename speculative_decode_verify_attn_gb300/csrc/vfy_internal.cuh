@@ -343,6 +343,7 @@ struct PackedAppendParams {
   uint8_t* k_pool;            // [slots][Hkv] records
   uint8_t* v_pool;
   float k_scale, v_scale;
+  float k_inv, v_inv;         // their rounded reciprocals, or 0 (packed.cuh)
   int num_sms;
   int* err;
 };
