@@ -974,8 +974,9 @@ static bool rope_params(const vfy_ctx* ctx, const vfy_rotary* r, const uint16_t*
   p->num_seqs = num_seqs;
   p->max_q = c.max_queries_per_seq;
   p->token_cap = num_seqs * c.max_queries_per_seq;
-  // One token a CTA while all of them run at once, else one a warp.
-  p->tokens_per_cta = p->token_cap <= 4 * ctx->num_sms ? 1 : vfy::rope_cta_tokens();
+  // One token a CTA while all of them run at once (eight CTAs per SM), else one a warp: 17 tokens 2.8 us against 4.5, 608 3.4
+  // against 4.8, 1216 4.5 against 5.1; 2432 8.1 against 6.2.
+  p->tokens_per_cta = p->token_cap <= 8 * ctx->num_sms ? 1 : vfy::rope_cta_tokens();
   p->hq = c.num_q_heads;
   p->hkv = c.num_kv_heads;
   p->head_dim = c.head_dim;

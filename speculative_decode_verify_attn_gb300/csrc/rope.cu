@@ -3,12 +3,13 @@
 //     x^ = x * w / sqrt(mean(x^2) + eps);   (a, b) -> (a cos t - b sin t, a sin t + b cos t),   t = position * inv_freq
 // in fp32, rounded once to bf16.
 //
-// A CTA of eight warps takes one token (few tokens: latency; 264 of a batch of trees 4.1 us against 5.8), or a token a warp
-// (8 x 1024 tokens 25.5 us against 52). The warps of a token work out its cosines and sines once, in shared memory. A row of
-// d channels is d / 8 lanes of two groups of four channels: the two groups that rotate with one another, so that a pair lies
-// in one lane. Many tokens are bound by instructions before they are by memory: queries, keys and values have a loop each,
-// without choices by row, and what a token costs once is paid by one warp. The look-up of up to 32 sequences is one round trip to memory.
-// 17 tokens of 16 + 2 x 4 heads of 128 take 3.0 us (latency), 8 x 1024 25.5 (115 MB, 4.5 TB/s).
+// A CTA of four warps takes one token (few tokens: latency), or a token a warp (8 x 1024 tokens 25 us against 52). The warps of
+// a token work out its cosines and sines once, in shared memory. A row of d channels is d / 8 lanes of two groups of four
+// channels: the two groups that rotate with one another, so that a pair lies in one lane. Queries, keys and values have a
+// loop each, without choices by row, and two rows a lane ahead of the one it works on. The look-up of up to 32 sequences is
+// one round trip to memory.
+// 17 tokens of 16 + 2 x 4 heads of 128 take 3.1 us (latency), 264 of a batch of trees 3.6, 8 x 1024 25 (117 MB, 4.7 TB/s:
+// leaving out the angles or the norms changes nothing; CTAs of eight warps 25.7, of two 24.6 but 17 tokens 4.2).
 //
 // Angles: the turns position * inv_freq / 2 pi modulo 1 (at position 262144 an fp32 product is off by 1/64 radian), with
 // inv_freq / 2 pi as the sum of three fp32 values (to 2^-53) and the products exact in pairs (product and fma remainder):
@@ -21,7 +22,7 @@
 namespace vfy {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 enum { kRows = 0, kFull = 1, kRing = 2 };
 
@@ -146,7 +147,7 @@ struct Loader {
 };
 
 template <int HD, int DST>
-__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, 8) rope_kernel(const RopeParams p) {
   constexpr int kLanes = HD / 8, kPer = 32 / kLanes;    // lanes of a row, rows of a warp at a time
   __shared__ float4 s_cos[kWarps][HD / 8], s_sin[kWarps][HD / 8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

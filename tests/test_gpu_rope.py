@@ -359,7 +359,7 @@ def test_a_token_a_warp(env, heads, rot, interleaved):
     n_chunks = sum(chunks) - first
     slot_of = H.dev_i32(rng.permutation(n_chunks + 3)[:n_chunks] - 3)
     results = []
-    for cap in (33, 200):
+    for cap in (33, 300):
         full = lambda *s: torch.full(s, 9.0, dtype=torch.bfloat16, device="cuda")   # noqa: E731
         ctx = vfy.vfy_create(hq, hkv, d, max_seqs=5, max_queries_per_seq=cap, window=64, ring_len=R, device=0)
         outs = [full(T + 9, hq, d), full(T + 9, hkv, d), full(T + 9, hq, d), *[full(n_chunks, hkv, C, d) for _ in range(4)],
