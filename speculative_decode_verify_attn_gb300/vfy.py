@@ -186,6 +186,7 @@ class Context:
         self.handle = handle
         self.cfg = cfg
         self.device = device
+        self.heads = cfg.num_q_heads, cfg.num_kv_heads, cfg.head_dim   # (a field of a Structure costs 0.1 us)
 
     def close(self):
         if self.handle:
@@ -494,34 +495,42 @@ class Rope:
                                    _dev(q_norm, BF16, "q_norm"), _dev(k_norm, BF16, "k_norm"), eps)
         self.at = ctypes.addressof(self.struct)
         self.devices = {t.get_device() for t in self.tensors if t is not None}
+        self.fits = set()                  # (device, head dim) of contexts that it was found to suit
 
 
-def _rows(ctx, t, heads: int, name: str):
-    """Address and row stride of bf16 rows [T][heads][d] (or [T][heads * d]), whose rows may lie further apart."""
+def _rows(ctx, t, side: int, name: str):
+    """Address and row stride of bf16 rows [T][heads][d] (or [T][heads * d]), whose rows may lie further apart. `side`: 0 for
+    query heads, 1 for KV heads."""
     if t is None:
         return None, 0
-    d = ctx.cfg.head_dim
+    heads, d = ctx.heads[side], ctx.heads[2]
     shape, step = t.shape, t.stride()
     if t.dtype not in BF16 or _DEVICE_OF(t) != ctx.device:
         raise TypeError(f"{name} must be a bf16 tensor on cuda:{ctx.device}, got {t.dtype} on {t.device}")
-    if not (shape[1:] == (heads, d) and step[2] == 1 and (step[1] == d or heads == 1)
-            or shape[1:] == (heads * d,) and step[1] == 1):
+    if len(shape) == 3:
+        ok = shape[2] == d and shape[1] == heads and step[2] == 1 and (step[1] == d or heads == 1)
+    else:
+        ok = len(shape) == 2 and shape[1] == heads * d and step[1] == 1
+    if not ok:
         raise ValueError(f"{name} must be [rows][{heads}][{d}] with packed rows, got {tuple(shape)} with strides {step}")
     return _DATA_PTR(t), step[0] if shape[0] > 1 else max(step[0], heads * d)
 
 
-def _rope_args(ctx, rope: Rope, q, k):
-    if not rope.devices <= {ctx.device}:
-        raise ValueError(f"the rotation is on cuda:{sorted(rope.devices)}, the context on cuda:{ctx.device}")
-    if not rope.norm_dims <= {ctx.cfg.head_dim}:
-        raise ValueError(f"q_norm and k_norm must have {ctx.cfg.head_dim} entries")
-    return (rope.at, *_rows(ctx, q, ctx.cfg.num_q_heads, "q"), *_rows(ctx, k, ctx.cfg.num_kv_heads, "k"))
+def _rope_at(ctx, rope: Rope):
+    fit = ctx.device, ctx.heads[2]
+    if fit not in rope.fits:
+        if not rope.devices <= {ctx.device}:
+            raise ValueError(f"the rotation is on cuda:{sorted(rope.devices)}, the context on cuda:{ctx.device}")
+        if not rope.norm_dims <= {ctx.heads[2]}:
+            raise ValueError(f"q_norm and k_norm must have {ctx.heads[2]} entries")
+        rope.fits.add(fit)
+    return rope.at
 
 
 def vfy_rope(ctx: Context, rope: Rope, q, k, cu_q, seq_len, depth, q_out, k_out, num_seqs: int, stream=None):
     """q, k: bf16 rows [T][heads][d], which may be views of a wider matrix; q_out, k_out: contiguous, or q, k themselves."""
     _check(lib().vfy_rope(
-        ctx.handle, *_rope_args(ctx, rope, q, k), _ptr(ctx, cu_q, I32, "cu_q"), _ptr(ctx, seq_len, I32, "seq_len"),
+        ctx.handle, _rope_at(ctx, rope), *_rows(ctx, q, 0, "q"), *_rows(ctx, k, 1, "k"), _ptr(ctx, cu_q, I32, "cu_q"), _ptr(ctx, seq_len, I32, "seq_len"),
         _ptr(ctx, depth, I32, "depth"), _ptr(ctx, q_out, BF16, "q_out"), _ptr(ctx, k_out, BF16, "k_out"), num_seqs,
         _raw_stream(ctx, stream)), "vfy_rope")
 
@@ -534,7 +543,7 @@ def _store(ctx, t, dtypes, name: str):
 def vfy_rope_append_full(ctx: Context, rope: Rope, q, k, v, cu_q, seq_len, depth, cu_chunks, slot_of_chunk, host_k, host_v,
                          num_host_chunks: int, k_pool, v_pool, num_slots: int, q_out, num_seqs: int, stream=None):
     _check(lib().vfy_rope_append_full(
-        ctx.handle, *_rope_args(ctx, rope, q, k), *_rows(ctx, v, ctx.cfg.num_kv_heads, "v"),
+        ctx.handle, _rope_at(ctx, rope), *_rows(ctx, q, 0, "q"), *_rows(ctx, k, 1, "k"), *_rows(ctx, v, 1, "v"),
         _ptr(ctx, cu_q, I32, "cu_q"), _ptr(ctx, seq_len, I32, "seq_len"), _ptr(ctx, depth, I32, "depth"),
         _ptr(ctx, cu_chunks, I32, "cu_chunks"), _ptr(ctx, slot_of_chunk, I32, "slot_of_chunk"),
         _store(ctx, host_k, BF16, "host_k"), _store(ctx, host_v, BF16, "host_v"), num_host_chunks,
@@ -545,7 +554,7 @@ def vfy_rope_append_full(ctx: Context, rope: Rope, q, k, v, cu_q, seq_len, depth
 def vfy_rope_append_swa(ctx: Context, rope: Rope, q, k, v, cu_q, seq_len, depth, ring_offset, k_ring, v_ring, q_out,
                         num_seqs: int, stream=None):
     _check(lib().vfy_rope_append_swa(
-        ctx.handle, *_rope_args(ctx, rope, q, k), *_rows(ctx, v, ctx.cfg.num_kv_heads, "v"),
+        ctx.handle, _rope_at(ctx, rope), *_rows(ctx, q, 0, "q"), *_rows(ctx, k, 1, "k"), *_rows(ctx, v, 1, "v"),
         _ptr(ctx, cu_q, I32, "cu_q"), _ptr(ctx, seq_len, I32, "seq_len"), _ptr(ctx, depth, I32, "depth"),
         _ptr(ctx, ring_offset, I32, "ring_offset"), _ptr(ctx, k_ring, BF16, "k_ring"), _ptr(ctx, v_ring, BF16, "v_ring"),
         _ptr(ctx, q_out, BF16, "q_out"), num_seqs, _raw_stream(ctx, stream)), "vfy_rope_append_swa")
