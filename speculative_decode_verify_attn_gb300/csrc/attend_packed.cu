@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
       named_sync(1, kAll);
       const int qe = max(static_cast<int>(sh->q_top >> 7) - 127 - 14, -100);
       const float down = __int_as_float((127 - qe) << 23);
-      q_scale = p.scale_log2 * __int_as_float((127 + qe) << 23);
+      q_scale = fmaxf(p.scale_log2 * __int_as_float((127 + qe) << 23), 1.2e-38f);   // (0 times a masked key's -inf is NaN)
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
         const int x = threadIdx.x + i * kAll;

@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(Few<HD, NT>::kThreads, 1) attend_packed_few_ke
     top = __reduce_max_sync(0xffffffffu, top);
     const int qe = max(static_cast<int>(top >> 7) - 127 - 14, -100);
     const float down = __int_as_float((127 - qe) << 23);
-    q_scale = p.scale_log2 * __int_as_float((127 + qe) << 23);
+    q_scale = fmaxf(p.scale_log2 * __int_as_float((127 + qe) << 23), 1.2e-38f);   // (0 times a masked key's -inf is NaN)
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll

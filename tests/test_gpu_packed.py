@@ -638,3 +638,12 @@ def test_batches_of_many_sequences(env, seqs, cap):
     for b in range(seqs):
         at, e = slice(cu[b], cu[b + 1]), slice(cu_res[b], cu_res[b + 1])
         close(got[at], lse[at], *B.attend_packed_seq(O.bf16_to_f64(q[at]), *pools, ids[e], slots[e], int(lens[b])))
+
+
+@pytest.mark.parametrize("heads", [(16, 4, 128), (4, 1, 64)])
+@pytest.mark.parametrize("n", [1, 3, 4, 17])
+def test_scores_below_every_fp32_value(env, heads, n):
+    """Queries and a tensor scale so small that their product is 0: all keys a row attends weigh the same, the others
+    nothing."""
+    one(env, heads, n, 500 + n, spread=1e-30, gk=1e-30)
+    one(env, heads, n, 64 * 9 + n, spread=1e-38, gk=1e-38, splits=1)
