@@ -84,8 +84,9 @@ struct Shared {
   int abort;
   unsigned q_top;                         // largest |q| of the tile, as bf16 bits
   int base[2 * kBatch][2];                // position of a chunk's first token, -1: no chunk
-  int seq;                                // of the batch
-  int4 geom[2];                           // [group] length, position of the block's first token, first row, rows: read
+  // [group]: each group writes and reads its own, with its own barrier between (a group without tiles meets no other wait)
+  int seq[2];                             // of the batch
+  int4 geom[2];                           // length, position of the block's first token, first row, rows: read
                                           // where they are needed, registers are short
   int plain[2 * kBatch];                  // every row attends every key of the tile
   alignas(16) float neg_ref[2][kMaxN];    // [group] minus the rows' reference, log2 units
@@ -456,8 +457,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
     // No reference yet. Rows past the block weigh 0, whatever their scores hold: all 36 rows of a thread are computed
     // without a branch.
     if (tg < kMaxN) sh->neg_ref[grp][tg] = tg < w.rows ? 0.f : -INFINITY;
-    if (threadIdx.x == 0) sh->seq = w.b;
-    if (tg == 0) sh->geom[grp] = make_int4(w.L, w.L - w.nq, w.row0, w.rows);
+    if (tg == 0) {
+      sh->seq[grp] = w.b;
+      sh->geom[grp] = make_int4(w.L, w.L - w.nq, w.row0, w.rows);
+    }
     bool has_ref = tg >= w.rows;                         // of row tg
     bool all_have = false;                               // of the group
     named_sync(bar, kGroup);
@@ -601,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
       tiles(std::integral_constant<int, kRowsT>());
     // ---- epilogue: the groups' sums and O merged into the split's partial (m, l, O not normalised) ----
     const int4 gm = sh->geom[grp];
-    const int b = sh->seq;
+    const int b = sh->seq[grp];
     if (u > 0 && !dead) dead = !__all_sync(0xffffffffu, mbar_wait(&sh->pv_done[grp], (u - 1) & 1, abort, p.err));
 #pragma unroll
     for (int r = 0; r < kRowsT; r += 4) {
