@@ -355,9 +355,10 @@ __global__ void __launch_bounds__(kDrawThreads) sample_draw_kernel(const SampleP
   load_noise(v0 + threadIdx.x);
   const int depth = r1 - r0 - 1;
   const int d0 = r0 - b;                  // drafts of the sequence (every sequence before it has a row)
-  // (a sequence without rows behind it shifts the places of its drafts: they may end behind the total - num_seqs there are)
-  const bool bad = d0 < 0 || depth < 0 || r1 > min(total, p.max_rows) || d0 + depth > total - p.num_seqs ||
-                   (depth > 0 && p.drafts == nullptr);
+  // (a sequence without rows behind it shifts the places of its drafts: they may end behind the total - num_seqs there are.
+  // The caller has as many as max_rows allow, whatever the total says: none, and no arrays for them, up to num_seqs rows.)
+  const int rows = min(total, p.max_rows);
+  const bool bad = d0 < 0 || depth < 0 || r1 > rows || (depth > 0 && d0 + depth > rows - p.num_seqs);
   int token = -1;
   float u = 0.f, q = 1.f, x = -INFINITY;
   auto load_draft = [&](int j) {
