@@ -175,15 +175,25 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(const UnpackParams p) 
   }
 #pragma unroll
   for (int y = 0; y < kMine; ++y) {
-    const float s = e4m3_value(scale[y]) * gs;
-    uint32_t o[4];
+    const float s = e4m3_value(scale[y]), sg = s * gs;
+    uint16_t* to = out + static_cast<size_t>(threadIdx.x + y * kThreads) * 8;
+    if (plain_product(s, sg)) {
+      uint32_t o[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 v = e2m1_pair((codes[y] >> (8 * e)) & 0xffu);
-      const __nv_bfloat162 h2 = __floats2bfloat162_rn(v.x * s, v.y * s);
-      o[e] = *reinterpret_cast<const uint32_t*>(&h2);
+      for (int e = 0; e < 4; ++e) {
+        const float2 v = e2m1_pair((codes[y] >> (8 * e)) & 0xffu);
+        const __nv_bfloat162 h2 = __floats2bfloat162_rn(v.x * sg, v.y * sg);
+        o[e] = *reinterpret_cast<const uint32_t*>(&h2);
+      }
+      *reinterpret_cast<uint4*>(to) = make_uint4(o[0], o[1], o[2], o[3]);
+    } else {
+#pragma unroll 1
+      for (int e = 0; e < 4; ++e) {
+        const float2 v = e2m1_pair((codes[y] >> (8 * e)) & 0xffu);
+        *reinterpret_cast<__nv_bfloat162*>(to + 2 * e) =
+            __floats2bfloat162_rn(product_to_odd(v.x * s, gs), product_to_odd(v.y * s, gs));
+      }
     }
-    *reinterpret_cast<uint4*>(out + static_cast<size_t>(threadIdx.x + y * kThreads) * 8) = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 

@@ -1,0 +1,53 @@
+"""4-bit chunks: values, scales and scores at the ends of fp32, and roundings next to a tie."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import block_oracle as B
+from oracle import vfy_oracle as O
+from test_gpu_packed import attend, close, env, one, records, u8  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+C = 64
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("g", [0.037, 1 / 3, 1.9999999, 0.6653645634651184, 0.6497395634651184, 3e38, 1e36, 2.0 ** 120, 1e-30, 2.0 ** -126, 1e-38, 3e-41, 2.0 ** -149])
+def test_unpack_rounds_once(env, d, g):  # noqa: F811
+    """Every code with every finite scale: g s e, 30 bits at most and so exact in fp64, rounded to bf16 directly. Nothing
+    overflows or is lost on the way: a zero code is 0 whatever s g would be, results next to 0 keep bf16's last bit. (With
+    0.665 and 0.6497 many products lie within 2^-25 of the middle between two bf16 values.)"""
+    H, vfy = env
+    g = np.float32(g)
+    rng = np.random.default_rng(d)
+    rec = records(rng, 40, 1, d, 0, 127)
+    flat_scales = rec[..., 32 * d:].reshape(40, C, d // 16)
+    groups = flat_scales.size
+    flat_scales.reshape(-1)[:] = np.arange(groups) % 127         # all scales, beside random codes
+    rec[..., 32 * d:] = flat_scales.reshape(40, 1, -1)
+    out = [torch.zeros((40, 1, C, d), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    ctx = vfy.vfy_create(1, 1, d, device=0)
+    try:
+        vfy.vfy_unpack_chunks(ctx, u8(rec), u8(rec[::-1]), 40, H.dev_i32(np.arange(40)), 40, float(g), 1.0, *out)
+        assert vfy.vfy_get_status(ctx) == vfy.VFY_OK
+    finally:
+        ctx.close()
+    values = B.record_values(rec, d)
+    scales = np.repeat(flat_scales.reshape(40, 1, C, d // 16), 16, -1)
+    codes = np.where(np.signbit(values), 8, 0) + np.searchsorted(B.E2M1, np.abs(values) / np.where(scales > 0, B.E4M3[np.minimum(scales, 126)], 1.0))
+    seen = set(zip(scales[scales > 0].tolist(), codes[scales > 0].tolist()))
+    assert len(seen) == 126 * 16
+    ref = values * np.float64(g)                                 # exact
+    with np.errstate(over="ignore"):
+        want = nearest_bf16(ref)
+    got = O.bf16_to_f64(H.bits_of(out[0]))
+    assert np.array_equal(got, want)
+
+
+def nearest_bf16(x):
+    """fp64 -> the nearest bf16 value, ties to even: 8 significant bits, steps of 2^-133 at least, infinity from 2^128 on."""
+    m, e = np.frexp(x)
+    step = np.maximum(e - 8, -133)
+    y = np.ldexp(np.rint(np.ldexp(x, -step)), step)
+    return np.where(np.abs(y) >= 2.0 ** 128, np.copysign(np.inf, x), y)
