@@ -1231,7 +1231,10 @@ vfy_status vfy_attend_full_packed(vfy_ctx* ctx, const uint16_t* q, const int32_t
   }
   p.num_splits = clampi(splits, 1, c.max_splits);
   p.token_cap = num_seqs * c.max_queries_per_seq;
-  p.scale_log2 = ctx->scale * 1.4426950408889634f * k_scale;
+  int scale_exp = 0, k_exp = 0;
+  const float scale = std::frexp(ctx->scale, &scale_exp), k_part = std::frexp(k_scale, &k_exp);
+  p.scale_log2 = scale * 1.4426950408889634f * k_part;
+  p.scale_exp = scale_exp + k_exp;
   p.v_scale = v_scale;
   p.part_o = ctx->part_o;
   p.part_ml = ctx->part_ml;

@@ -434,9 +434,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
       top = __reduce_max_sync(0xffffffffu, top);
       if (lane == 0) atomicMax(&sh->q_top, top);
       named_sync(1, kAll);
-      const int qe = max(static_cast<int>(sh->q_top >> 7) - 127 - 14, -100);
-      const float down = __int_as_float((127 - qe) << 23);
-      q_scale = fmaxf(p.scale_log2 * __int_as_float((127 + qe) << 23), 1.2e-38f);   // (0 times a masked key's -inf is NaN)
+      const int qe = query_exponent(sh->q_top);
+      const PowerOfTwo down(-qe);
+      q_scale = score_scale(p.scale_log2, p.scale_exp, qe);
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
         const int x = threadIdx.x + i * kAll;
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
         uint32_t o[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          o[e] = pack_f16(__uint_as_float(ws[e] << 16) * down, __uint_as_float(ws[e] & 0xffff0000u) * down);
+          o[e] = pack_f16(down.times(__uint_as_float(ws[e] << 16)), down.times(__uint_as_float(ws[e] & 0xffff0000u)));
         if (r < kN)
           *reinterpret_cast<uint4*>(sQ + (cw >> 3) * C::kQBoxBytes + r * 128 + (((cw & 7) ^ (r & 7)) << 4)) =
               make_uint4(o[0], o[1], o[2], o[3]);

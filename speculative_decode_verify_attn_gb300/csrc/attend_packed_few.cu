@@ -188,16 +188,16 @@ __global__ void __launch_bounds__(Few<HD, NT>::kThreads, 1) attend_packed_few_ke
       }
     }
     top = __reduce_max_sync(0xffffffffu, top);
-    const int qe = max(static_cast<int>(top >> 7) - 127 - 14, -100);
-    const float down = __int_as_float((127 - qe) << 23);
-    q_scale = fmaxf(p.scale_log2 * __int_as_float((127 + qe) << 23), 1.2e-38f);   // (0 times a masked key's -inf is NaN)
+    const int qe = query_exponent(top);
+    const PowerOfTwo down(-qe);
+    q_scale = score_scale(p.scale_log2, p.scale_exp, qe);
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int k = 0; k < kSteps; ++k)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          qf[t][k][i] = pack_f16(__uint_as_float(qf[t][k][i] << 16) * down, __uint_as_float(qf[t][k][i] & 0xffff0000u) * down);
+          qf[t][k][i] = pack_f16(down.times(__uint_as_float(qf[t][k][i] << 16)), down.times(__uint_as_float(qf[t][k][i] & 0xffff0000u)));
   }
 
   float o[NT][kSteps][4];

@@ -108,6 +108,25 @@ __device__ __forceinline__ uint32_t e2m1_of(const float2& a, const float2& b, co
   return r;
 }
 
+// A power of two by halves: x * a * b = x 2^e for |e| <= 252, and nothing that the product can hold is lost between.
+struct PowerOfTwo {
+  float a, b;
+  __device__ __forceinline__ explicit PowerOfTwo(int e) {
+    e = min(max(e, -252), 252);
+    const int h = e >> 1;
+    a = __int_as_float((127 + h) << 23);
+    b = __int_as_float((127 + e - h) << 23);
+  }
+  __device__ __forceinline__ float times(float x) const { return x * a * b; }
+};
+// The queries of a tile, the largest of them with bf16 bits `top` (its size), are scaled by 2^-exponent to at most 2^15.
+__device__ __forceinline__ int query_exponent(unsigned top) { return static_cast<int>(top >> 7) - 127 - 14; }
+// What a product of scaled queries and s e is multiplied with to be a score in log2 units: a normal number, because 0 times a
+// masked key's -inf is NaN, and so is infinity times 0.
+__device__ __forceinline__ float score_scale(float scale_log2, int scale_exp, int query_exp) {
+  return fminf(fmaxf(PowerOfTwo(scale_exp + query_exp).times(scale_log2), 1.2e-38f), 3e38f);
+}
+
 // 16 values x to the codes of x / g and their scale. Quotients are rounded as IEEE divisions: the scale's quotient can lie on
 // a tie of e4m3 only if it is exact, and so can a value's on a tie of e2m1. `x`: pairs.
 //

@@ -379,7 +379,9 @@ struct PackedAttnParams {
   int row_tiles;              // of 128 rows, as the combine counts them
   int n_tiles, tile_rows;     // this kernel's row tiles
   int token_cap;
-  float scale_log2;           // softmax scale * log2(e) * g of K
+  // softmax scale * log2(e) * g of K is scale_log2 * 2^scale_exp: fp32 need not hold it, the queries' exponent comes on top
+  float scale_log2;
+  int scale_exp;
   float v_scale;              // g of V
   float* part_o;              // [B][row tiles][Hkv][splits][128][d]
   float* part_ml;             // [B][row tiles][Hkv][splits][128][2] (m in log2 units, l)

@@ -51,3 +51,23 @@ def nearest_bf16(x):
     step = np.maximum(e - 8, -133)
     y = np.ldexp(np.rint(np.ldexp(x, -step)), step)
     return np.where(np.abs(y) >= 2.0 ** 128, np.copysign(np.inf, x), y)
+
+
+HEADS = [(16, 4, 128), (4, 1, 64)]
+
+
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("n", [1, 4, 17])
+@pytest.mark.parametrize("e", [60, 100, 118])
+def test_small_queries_with_a_large_scale(env, heads, n, e):  # noqa: F811
+    """Queries of 2^-e and a tensor scale of 2^e have the scores of 1 and 1."""
+    one(env, heads, n, 500 + n, spread=2.0 ** -e, gk=2.0 ** e)
+    one(env, heads, n, 500 + n, spread=2.0 ** e, gk=2.0 ** -e, splits=1)
+
+
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("n", [1, 17])
+@pytest.mark.parametrize("spread,gk,scale", [(1e-30, 1e30, 1.0), (1.0, 3e38, 1e-38), (1e-36, 3e38, 1e-2), (1e-39, 1e36, 1e3), (1e-30, 1e38, 1e-8), (1e30, 1e-38, 1e7)])
+def test_scales_whose_product_leaves_fp32(env, heads, n, spread, gk, scale):  # noqa: F811
+    """Softmax scale, tensor scale and queries that make ordinary scores together, whatever two of them make."""
+    one(env, heads, n, 300 + n, spread=spread, gk=gk, scale=float(np.float32(scale)))
