@@ -625,16 +625,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
         ref[g] = lg[g] > 0.f ? -sh->neg_ref[g][r] : -INFINITY;
       }
       const float m = fmaxf(ref[0], ref[1]);
-      float sum = 0.f;
+      float wt[2], sum = 0.f;
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        const float wt = lg[g] > 0.f ? ex2_approx(ref[g] - m) : 0.f;
-        sum += wt * lg[g];
-        sh->alpha[g][r] = wt * p.v_scale;
+        wt[g] = lg[g] > 0.f ? ex2_approx(ref[g] - m) : 0.f;
+        sum += wt[g] * lg[g];
       }
+      const int e = partial_exponent(sum, p.v_scale);
+      const float down = __int_as_float((127 - e) << 23);
+#pragma unroll
+      for (int g = 0; g < 2; ++g) sh->alpha[g][r] = wt[g] * down * p.v_scale;
       const int rg = gm.z + r;
       const size_t pidx = ((static_cast<size_t>(b) * p.row_tiles + rg / kMaxRows) * p.hkv + blockIdx.y) * p.num_splits + blockIdx.x;
-      reinterpret_cast<float2*>(p.part_ml)[pidx * kMaxRows + rg % kMaxRows] = make_float2(m, sum);
+      reinterpret_cast<float2*>(p.part_ml)[pidx * kMaxRows + rg % kMaxRows] = make_float2(m + static_cast<float>(e), sum * down);
     }
     named_sync(1, kAll);
     if (w.nt > 0 && wq * 32 < HD) {

@@ -416,17 +416,20 @@ __global__ void __launch_bounds__(Few<HD, NT>::kThreads, 1) attend_packed_few_ke
     if (direct) {
       const unsigned qi = static_cast<unsigned>(r) / static_cast<unsigned>(p.group), hg = r - qi * p.group;
       const size_t row = static_cast<size_t>(q0 + qi) * p.hq + static_cast<size_t>(h) * p.group + hg;
-      const float inv = sum > 0.f ? p.v_scale / sum : 0.f;
-      const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+      const float inv = sum > 0.f ? 1.f / sum : 0.f, g = p.v_scale;      // (g / sum could be a denormal)
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv * g, acc.y * inv * g),
+                           hi = __floats2bfloat162_rn(acc.z * inv * g, acc.w * inv * g);
       *reinterpret_cast<uint2*>(p.out + row * HD + ch) =
           make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
       if (ch == 0 && p.lse != nullptr)
         p.lse[row] = sum > 0.f ? (m + __log2f(sum)) * 0.6931471805599453f : -INFINITY;
     } else {
       const size_t pidx = (static_cast<size_t>(b) * p.hkv + h) * p.num_splits + s;
+      const int e = partial_exponent(sum, p.v_scale);
+      const float down = __int_as_float((127 - e) << 23), scale = down * p.v_scale;
       *reinterpret_cast<float4*>(p.part_o + (pidx * kMaxRows + r) * HD + ch) =
-          make_float4(acc.x * p.v_scale, acc.y * p.v_scale, acc.z * p.v_scale, acc.w * p.v_scale);
-      if (ch == 0) reinterpret_cast<float2*>(p.part_ml)[pidx * kMaxRows + r] = make_float2(m, sum);
+          make_float4(acc.x * scale, acc.y * scale, acc.z * scale, acc.w * scale);
+      if (ch == 0) reinterpret_cast<float2*>(p.part_ml)[pidx * kMaxRows + r] = make_float2(m + static_cast<float>(e), sum * down);
     }
   }
 }

@@ -127,6 +127,14 @@ __device__ __forceinline__ float score_scale(float scale_log2, int scale_exp, in
   return fminf(fmaxf(PowerOfTwo(scale_exp + query_exp).times(scale_log2), 1.2e-38f), 3e38f);
 }
 
+// Exponent e for which a partial's O, sum and reference are handed on as O 2^-e, sum 2^-e and reference + e. Sums of weights
+// times values stay below 2^57 times g (2^15 a weight, 2^31 keys, values of 2688), which fp32 holds up to g = 1e20: until
+// there e is 0. Past it the sum becomes 2^-7 .. 2^-6, so that O, and what the combine adds up of 64 partials, is no larger
+// than the largest value.
+__device__ __forceinline__ int partial_exponent(float sum, float g) {
+  return g > 1e20f && sum > 0.f ? (static_cast<int>(__float_as_uint(sum) >> 23) - 127) + 7 : 0;
+}
+
 // 16 values x to the codes of x / g and their scale. Quotients are rounded as IEEE divisions: the scale's quotient can lie on
 // a tie of e4m3 only if it is exact, and so can a value's on a tie of e2m1. `x`: pairs.
 //

@@ -71,3 +71,35 @@ def test_small_queries_with_a_large_scale(env, heads, n, e):  # noqa: F811
 def test_scales_whose_product_leaves_fp32(env, heads, n, spread, gk, scale):  # noqa: F811
     """Softmax scale, tensor scale and queries that make ordinary scores together, whatever two of them make."""
     one(env, heads, n, 300 + n, spread=spread, gk=gk, scale=float(np.float32(scale)))
+
+
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("n", [1, 4, 17])
+@pytest.mark.parametrize("splits", [0, 1])
+def test_values_near_both_ends_of_fp32(env, heads, n, splits):  # noqa: F811
+    """O itself is within bf16; sums of weights times it on the way need not be. A power of two of g is one of O; LSE stays."""
+    H, vfy = env
+    hq, hkv, d = heads
+    m = 50
+    rng = np.random.default_rng([hq, n])
+    pools = [records(rng, m, hkv, d) for _ in range(2)]
+    bits = B.to_bf16(rng.standard_normal((n, hq, d)))
+    ctx = vfy.vfy_create(hq, hkv, d, max_queries_per_seq=n, device=0)
+    try:
+        vfy.vfy_set_splits(ctx, splits, 0)
+        run = lambda g: attend(env, ctx, bits, [0, n], pools, np.arange(m), np.arange(m), [0, m], [m * C], gv=g)   # noqa: E731
+        one_, lse = run(1.0)
+        one_ = O.bf16_to_f64(one_)
+        close(B.to_bf16(one_), lse, *B.attend_packed_seq(O.bf16_to_f64(bits), *pools, np.arange(m), np.arange(m), m * C))
+        for e in (66, 67, 100, 120, 125, -60, -100, -115, -126):
+            got, l2 = run(2.0 ** e)
+            want = nearest_bf16(one_ * 2.0 ** e)
+            got = O.bf16_to_f64(got)
+            # up to 2^66 exactly; past it a partial's reference is rounded otherwise, and a value next to a tie takes the
+            # neighbour, one step; next to 0 both sides are rounded once more
+            off = 2.0 ** -7 * np.abs(want) if e > 66 else 2.0 ** -133 if e < -110 else 0.0
+            assert np.all(np.abs(got - want) <= off), e
+            assert np.all(np.abs(l2 - lse) <= 2.0 ** -21 * (1 + np.abs(lse))), e
+        assert vfy.vfy_get_status(ctx) == vfy.VFY_OK
+    finally:
+        ctx.close()
