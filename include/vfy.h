@@ -659,8 +659,10 @@ VFY_API vfy_status vfy_unpack_chunks(vfy_ctx* ctx, const uint8_t* k_pool, const 
  * vfy_attend_full_packed -- vfy_attend_full over a pool of 4-bit chunks (a chain block; one row per sequence is plain
  * decoding).
  *  k_pool, v_pool    [num_slots][Hkv] records;  k_scale, v_scale  g of K and of V, finite and > 0
- *  The other arguments, results and device errors are those of vfy_attend_full. Queries and their scores must be finite
- *  in fp32; scales of tokens that some block query attends must not be NaN (vfy_append_full_packed writes none).
+ *  The other arguments, results and device errors are those of vfy_attend_full. Queries must be finite; scales of tokens
+ *  that some block query attends must not be NaN (vfy_append_full_packed writes none).
+ *  Scores (scaled, as in the LSE) reach to 2^25 in size. A row whose largest score so far lies past 2^26 log2 units gets
+ *  unspecified results, VFY_EDEVICE_INPUT: fp32 scores of that size are further apart than weights can be.
  *  A context made for at most 16 rows a KV head (max_queries_per_seq * Hq / Hkv) has a kernel of its own, which decodes a
  *  token up to a third faster.
  */

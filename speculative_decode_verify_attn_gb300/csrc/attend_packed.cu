@@ -542,6 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_packed_kernel(const Packed
               a = has_ref ? ex2_approx(old - ref) : 0.f;
               sh->neg_ref[grp][tg] = -ref;
               has_ref = true;
+              if (!(fabsf(ref) < kMostScore)) atomicOr(p.err, kErrDeviceInput);
             }
             sh->alpha[grp][tg] = a;
           }

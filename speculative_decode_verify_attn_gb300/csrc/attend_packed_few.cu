@@ -30,7 +30,7 @@ namespace vfy {
 namespace {
 
 constexpr float kTop = 7.f, kLimit = 15.f;   // log2: where a row's maximum is placed, where its reference moves
-constexpr float kNone = 1e30f;               // minus the reference of a row that has none
+constexpr float kNone = 3.4028235e38f;       // minus the reference of a row that has none: any finite score is above that
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -292,6 +292,7 @@ __global__ void __launch_bounds__(Few<HD, NT>::kThreads, 1) attend_packed_few_ke
           if (m + neg_ref[t][i] > kLimit) {
             const float a = neg_ref[t][i] == kNone ? 0.f : ex2_approx(kTop - m - neg_ref[t][i]);
             neg_ref[t][i] = kTop - m;
+            if (!(fabsf(m) < kMostScore)) atomicOr(p.err, kErrDeviceInput);
             l[t][i] *= a;
 #pragma unroll
             for (int y = 0; y < kSteps; ++y) {

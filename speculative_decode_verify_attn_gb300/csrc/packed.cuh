@@ -127,6 +127,10 @@ __device__ __forceinline__ float score_scale(float scale_log2, int scale_exp, in
   return fminf(fmaxf(PowerOfTwo(scale_exp + query_exp).times(scale_log2), 1.2e-38f), 3e38f);
 }
 
+// A row's reference (log2) is at most this in size, or the call reports the row: neighbouring fp32 scores are 8 apart from here
+// on, and a weight could land 16 above the place that its reference gives it, past fp16.
+constexpr float kMostScore = 67108864.f;   // 2^26
+
 // Exponent e for which a partial's O, sum and reference are handed on as O 2^-e, sum 2^-e and reference + e. Sums of weights
 // times values stay below 2^57 times g (2^15 a weight, 2^31 keys, values of 2688), which fp32 holds up to g = 1e20: until
 // there e is 0. Past it the sum becomes 2^-7 .. 2^-6, so that O, and what the combine adds up of 64 partials, is no larger

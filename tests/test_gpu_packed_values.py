@@ -103,3 +103,60 @@ def test_values_near_both_ends_of_fp32(env, heads, n, splits):  # noqa: F811
         assert vfy.vfy_get_status(ctx) == vfy.VFY_OK
     finally:
         ctx.close()
+
+
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("n", [1, 4, 17])
+@pytest.mark.parametrize("size", [2.0 ** 28, 2.0 ** 40, 1e20, 1e31, -2.0 ** 28, -1e20, -1e31, -1e33])
+def test_scores_past_the_limit_are_reported(env, heads, n, size):  # noqa: F811
+    """A row whose largest score lies past 2^26 (log2 units), where fp32 scores are further apart than weights can be."""
+    H, vfy = env
+    hq, hkv, d = heads
+    pools = [np.zeros((4, hkv, 36 * d), np.uint8) for _ in range(2)]
+    for p in pools:
+        p[..., :32 * d] = 0x22                                  # all ones
+        p[..., 32 * d:] = 0x38
+    q = np.zeros((n, hq, d))
+    q[..., 0] = np.sign(size)
+    for rows in (slice(None), slice(n - 1, n)):                 # all rows, or the last alone
+        x = np.where(np.arange(n)[:, None, None] >= (rows.start or 0), q, 0.0)
+        ctx = vfy.vfy_create(hq, hkv, d, max_queries_per_seq=n, softmax_scale=1.0, device=0)
+        try:
+            for splits in (0, 1):
+                vfy.vfy_set_splits(ctx, splits, 0)
+                attend(env, ctx, B.to_bf16(x), [0, n], pools, np.arange(4), np.arange(4), [0, 4], [4 * C], gk=abs(size))
+                assert vfy.vfy_get_status(ctx) == vfy.VFY_EDEVICE_INPUT
+        finally:
+            ctx.close()
+
+
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("n", [1, 4, 17])
+@pytest.mark.parametrize("size", [1e6, 2e7, -1e6, -2e7])
+def test_scores_up_to_the_limit(env, heads, n, size):  # noqa: F811
+    """One key's score far above all others: its value is the output. All alike: the mean is."""
+    H, vfy = env
+    hq, hkv, d = heads
+    pools = [np.zeros((4, hkv, 36 * d), np.uint8) for _ in range(2)]
+    rng = np.random.default_rng(1)
+    for p in pools:
+        p[..., :32 * d] = 0x22
+        p[..., 32 * d:] = 0x38
+    pools[1][..., :32 * d] = rng.integers(0, 256, (4, hkv, 32 * d))
+    for alike in (True, False):
+        if not alike:
+            code = 0x24 if size > 0 else 0x21                   # channel 0: 2, or 1/2, for 1
+            pools[0][1, :, 5 * 16] = code
+        q = np.zeros((n, hq, d))
+        q[..., 0] = np.sign(size)
+        bits = B.to_bf16(q)
+        ctx = vfy.vfy_create(hq, hkv, d, max_queries_per_seq=n, softmax_scale=1.0, device=0)
+        try:
+            for splits in (0, 1):
+                vfy.vfy_set_splits(ctx, splits, 0)
+                got, lse = attend(env, ctx, bits, [0, n], pools, np.arange(4), np.arange(4), [0, 4], [4 * C], gk=abs(size))
+                assert vfy.vfy_get_status(ctx) == vfy.VFY_OK
+                ref = B.attend_packed_seq(O.bf16_to_f64(bits), *pools, np.arange(4), np.arange(4), 4 * C, np.float32(abs(size)), 1.0, 1.0)
+                close(got, lse, *ref)
+        finally:
+            ctx.close()
