@@ -513,7 +513,7 @@ def _rows(ctx, t, side: int, name: str):
         ok = len(shape) == 2 and shape[1] == heads * d and step[1] == 1
     if not ok:
         raise ValueError(f"{name} must be [rows][{heads}][{d}] with packed rows, got {tuple(shape)} with strides {step}")
-    return _DATA_PTR(t), step[0] if shape[0] > 1 else max(step[0], heads * d)
+    return _DATA_PTR(t), step[0] if shape[0] > 1 else heads * d    # (one row lies apart from no other, whatever the view says)
 
 
 def _rope_at(ctx, rope: Rope):
