@@ -156,6 +156,7 @@ def _stream(stream) -> ctypes.c_void_p:
 # launch: these helpers take 0.23 us a tensor and 0.1 us for the stream (torch.cuda.current_stream()
 # builds a Stream object: 3 us).
 _DEVICE_OF, _CONTIGUOUS, _DATA_PTR = torch.Tensor.get_device, torch.Tensor.is_contiguous, torch.Tensor.data_ptr
+_NUMEL = torch.Tensor.numel
 
 def _raw_stream(ctx, stream) -> int:
     """The handle of `stream`, or of the current stream of the context's device."""
@@ -187,6 +188,7 @@ class Context:
         self.cfg = cfg
         self.device = device
         self.heads = cfg.num_q_heads, cfg.num_kv_heads, cfg.head_dim   # (a field of a Structure costs 0.1 us)
+        self.chunk_bytes = cfg.num_kv_heads * packed_bytes(cfg.head_dim)   # of a chunk's 4-bit records
 
     def close(self):
         if self.handle:
@@ -537,7 +539,7 @@ def vfy_rope(ctx: Context, rope: Rope, q, k, cu_q, seq_len, depth, q_out, k_out,
 
 def _store(ctx, t, dtypes, name: str):
     """Address of a chunk store: on the context's device, or in (pinned) host memory."""
-    return _ptr(ctx, t, dtypes, name) if t.is_cuda else _host(t, dtypes, name)
+    return _host(t, dtypes, name) if isinstance(t, torch.Tensor) and not t.is_cuda else _ptr(ctx, t, dtypes, name)
 
 
 def vfy_rope_append_full(ctx: Context, rope: Rope, q, k, v, cu_q, seq_len, depth, cu_chunks, slot_of_chunk, host_k, host_v,
@@ -572,22 +574,37 @@ def packed_bytes(head_dim: int) -> int:
     return 36 * head_dim
 
 
+def _records(ctx, t, count: int, name: str, address=_ptr):
+    """Address of `count` chunks' records: uint8 [chunks][Hkv][packed_bytes(d)] (a chunk's records, or all, may be one row of
+    bytes), no fewer chunks than `count`: the library knows the address alone."""
+    at = address(ctx, t, U8, name)
+    if at is not None and _NUMEL(t) != count * ctx.chunk_bytes:        # (as many bytes as that are those records)
+        _, hkv, d = ctx.heads
+        size, shape = packed_bytes(d), t.shape
+        fits = shape[-1] == size or len(shape) == 1 or (len(shape) == 2 and shape[1] == hkv * size)
+        if not fits or t.numel() < count * hkv * size:
+            raise ValueError(f"{name} must hold {count} chunks of {hkv} records of {size} bytes, got {tuple(shape)}")
+    return at
+
+
 def vfy_append_full_packed(ctx: Context, k_new, v_new, cu_q, seq_len, cu_chunks, slot_of_chunk, host_k, host_v,
                            num_host_chunks: int, k_pool, v_pool, num_slots: int, k_scale: float, v_scale: float,
                            num_seqs: int, stream=None):
     _check(lib().vfy_append_full_packed(
         ctx.handle, _ptr(ctx, k_new, BF16, "k_new"), _ptr(ctx, v_new, BF16, "v_new"), _ptr(ctx, cu_q, I32, "cu_q"),
         _ptr(ctx, seq_len, I32, "seq_len"), _ptr(ctx, cu_chunks, I32, "cu_chunks"),
-        _ptr(ctx, slot_of_chunk, I32, "slot_of_chunk"), _store(ctx, host_k, U8, "host_k"), _store(ctx, host_v, U8, "host_v"),
-        num_host_chunks, _ptr(ctx, k_pool, U8, "k_pool"), _ptr(ctx, v_pool, U8, "v_pool"), num_slots, k_scale, v_scale,
-        num_seqs, _raw_stream(ctx, stream)), "vfy_append_full_packed")
+        _ptr(ctx, slot_of_chunk, I32, "slot_of_chunk"), _records(ctx, host_k, num_host_chunks, "host_k", _store),
+        _records(ctx, host_v, num_host_chunks, "host_v", _store), num_host_chunks, _records(ctx, k_pool, num_slots, "k_pool"),
+        _records(ctx, v_pool, num_slots, "v_pool"), num_slots, k_scale, v_scale, num_seqs, _raw_stream(ctx, stream)),
+        "vfy_append_full_packed")
 
 
 def vfy_page_in_packed(ctx: Context, host_k, host_v, num_host_chunks: int, k_pool, v_pool, num_slots: int, pagein_list,
                        pagein_count, num_seqs: int, k: int, stream=None):
     _check(lib().vfy_page_in_packed(
-        ctx.handle, _store(ctx, host_k, U8, "host_k"), _store(ctx, host_v, U8, "host_v"), num_host_chunks,
-        _ptr(ctx, k_pool, U8, "k_pool"), _ptr(ctx, v_pool, U8, "v_pool"), num_slots,
+        ctx.handle, _records(ctx, host_k, num_host_chunks, "host_k", _store),
+        _records(ctx, host_v, num_host_chunks, "host_v", _store), num_host_chunks,
+        _records(ctx, k_pool, num_slots, "k_pool"), _records(ctx, v_pool, num_slots, "v_pool"), num_slots,
         _ptr(ctx, pagein_list, I32, "pagein_list"), _ptr(ctx, pagein_count, I32, "pagein_count"), num_seqs, k,
         _raw_stream(ctx, stream)), "vfy_page_in_packed")
 
@@ -595,7 +612,7 @@ def vfy_page_in_packed(ctx: Context, host_k, host_v, num_host_chunks: int, k_poo
 def vfy_unpack_chunks(ctx: Context, k_pool, v_pool, num_slots: int, slots, num_chunks: int, k_scale: float, v_scale: float,
                       k_out, v_out, stream=None):
     _check(lib().vfy_unpack_chunks(
-        ctx.handle, _ptr(ctx, k_pool, U8, "k_pool"), _ptr(ctx, v_pool, U8, "v_pool"), num_slots,
+        ctx.handle, _records(ctx, k_pool, num_slots, "k_pool"), _records(ctx, v_pool, num_slots, "v_pool"), num_slots,
         _ptr(ctx, slots, I32, "slots"), num_chunks, k_scale, v_scale, _ptr(ctx, k_out, BF16, "k_out"),
         _ptr(ctx, v_out, BF16, "v_out"), _raw_stream(ctx, stream)), "vfy_unpack_chunks")
 
@@ -604,8 +621,8 @@ def vfy_attend_full_packed(ctx: Context, q, cu_q, k_pool, v_pool, num_slots: int
                            max_resident_per_seq: int, seq_len, k_scale: float, v_scale: float, out, lse, num_seqs: int,
                            stream=None):
     _check(lib().vfy_attend_full_packed(
-        ctx.handle, _ptr(ctx, q, BF16, "q"), _ptr(ctx, cu_q, I32, "cu_q"), _ptr(ctx, k_pool, U8, "k_pool"),
-        _ptr(ctx, v_pool, U8, "v_pool"), num_slots, _ptr(ctx, resident_ids, I32, "resident_ids"),
+        ctx.handle, _ptr(ctx, q, BF16, "q"), _ptr(ctx, cu_q, I32, "cu_q"), _records(ctx, k_pool, num_slots, "k_pool"),
+        _records(ctx, v_pool, num_slots, "v_pool"), num_slots, _ptr(ctx, resident_ids, I32, "resident_ids"),
         _ptr(ctx, resident_slots, I32, "resident_slots"), _ptr(ctx, cu_resident, I32, "cu_resident"), max_resident_per_seq,
         _ptr(ctx, seq_len, I32, "seq_len"), k_scale, v_scale, _ptr(ctx, out, BF16, "out"), _ptr(ctx, lse, F32, "lse"),
         num_seqs, _raw_stream(ctx, stream)), "vfy_attend_full_packed")
