@@ -117,3 +117,36 @@ def test_many_tiles_of_one_cta(env, heads, n, m):  # noqa: F811
             close(got, lse, *ref)
     finally:
         ctx.close()
+
+
+@pytest.mark.parametrize("heads", [(16, 4, 128), (4, 1, 64)])
+@pytest.mark.parametrize("n", [1, 4, 17, 40])
+def test_the_same_bits_from_call_to_call(env, heads, n):  # noqa: F811
+    """Whatever other calls left in the workspace, and in a graph."""
+    H, vfy = env
+    hq, hkv, d = heads
+    rng = np.random.default_rng([hq, n])
+    m = 90
+    pools = [torch.from_numpy(records(rng, m, hkv, d)).cuda() for _ in range(2)]
+    ids, cu, cr, ln, ln2 = H.dev_i32(np.arange(m)), H.dev_i32([0, n]), H.dev_i32([0, m]), H.dev_i32([m * C - 5]), H.dev_i32([m * C - 700])
+    q, other = [H.dev_bf16(B.to_bf16(rng.standard_normal((n, hq, d)))) for _ in range(2)]
+    new = lambda: (torch.empty_like(q), torch.empty((n, hq), device="cuda"))   # noqa: E731
+    ctx = vfy.vfy_create(hq, hkv, d, max_queries_per_seq=n, device=0)
+    call = lambda x, l, o: vfy.vfy_attend_full_packed(ctx, x, cu, *pools, m, ids, ids, cr, m, l, 1.0, 1.0, *o, 1)   # noqa: E731
+    try:
+        first, scratch, got = new(), new(), new()
+        call(q, ln, first)
+        torch.cuda.synchronize()
+        side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        with torch.cuda.stream(side):
+            with torch.cuda.graph(graph, stream=side):
+                call(other, ln2, scratch)
+                call(q, ln, got)
+        for i in range(20):
+            got[0].fill_(9.0)
+            call(other, ln2, scratch) if i % 2 else call(q, ln, scratch)
+            call(q, ln, got) if i % 3 else graph.replay()
+            assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+        assert vfy.vfy_get_status(ctx) == vfy.VFY_OK
+    finally:
+        ctx.close()

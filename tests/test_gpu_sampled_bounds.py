@@ -53,3 +53,15 @@ def test_rows_past_the_bound(env, cu, max_rows, arrays, kept):  # noqa: F811
         check(env, ctx, c)                                      # the workspace is as it was
     finally:
         ctx.close()
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("counts", [[5], [1, 4, 2]])
+def test_a_bound_above_the_rows(env, counts, bf16):  # noqa: F811
+    """max_rows is a bound: a graph made for the most rows serves steps of fewer."""
+    c = make(np.random.default_rng(counts), counts, 5000, bf16)
+    ctx = env[1].vfy_create(4, 1, 64, max_seqs=len(counts), max_queries_per_seq=40, device=0)
+    try:
+        check(env, ctx, c, bf16=bf16, max_rows=40 * len(counts))
+    finally:
+        ctx.close()
