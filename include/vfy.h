@@ -571,7 +571,9 @@ typedef struct vfy_rotary {
  * vfy_rope -- normalise and rotate the block's queries and keys.
  * Row i of sequence b is at position p = seq_len[b] - q_b + i, or, with depths (a tree), at
  * seq_len[b] - q_b + depth[cu_q[b] + i]. With t = p * inv_freq[j] every pair (x, y) becomes
- * (x cos t - y sin t, x sin t + y cos t). Angles are within 2^-22 of a turn at every position (2^-25 up to 2^22).
+ * (x cos t - y sin t, x sin t + y cos t). With frequencies up to 1 in size angles are within 2^-22 of a turn at every
+ * position (2^-25 up to 2^22). Mean and root are fp32: with a norm, squares of a head's values must add up to less than 2^127
+ * and, where eps is 0, to more than 2^-100 (or be 0: 0 / 0 is NaN).
  *  q, q_stride    bf16 rows of Hq * d values, q_stride values apart (>= Hq * d, a multiple of 8): a view of a
  *                 wider matrix. NULL with q_out NULL: no queries
  *  k, k_stride    bf16 rows of Hkv * d values; NULL with k_out NULL: no keys
@@ -663,6 +665,9 @@ VFY_API vfy_status vfy_unpack_chunks(vfy_ctx* ctx, const uint8_t* k_pool, const 
  *  that some block query attends must not be NaN (vfy_append_full_packed writes none).
  *  Scores (scaled, as in the LSE) reach to 2^25 in size. A row whose largest score so far lies past 2^26 log2 units gets
  *  unspecified results, VFY_EDEVICE_INPUT: fp32 scores of that size are further apart than weights can be.
+ *  All queries of a tile (up to 72 rows of a KV head: block rows times q-heads) are scaled by one power of two and held in
+ *  fp16. A query value far below the tile's largest, q, is off by up to 2^-39 q, so that a score is off by up to
+ *  2^-39 q softmax_scale sum_j |k_j| beyond fp32's own roundings. Weights are fp16 (half a step, 2^-11 of a weight).
  *  A context made for at most 16 rows a KV head (max_queries_per_seq * Hq / Hkv) has a kernel of its own, which decodes a
  *  token up to a third faster.
  */
@@ -681,8 +686,8 @@ VFY_API vfy_status vfy_attend_full_packed(vfy_ctx* ctx, const uint16_t* q, const
  * n_b is the first refused draft, or D_b. The next token is drawn from w = max(p_n - q_n, 0) (n < D_b) or w = p_n
  * (n = D_b): the token with the largest w_v / E_v, ties to the lowest index. With E_v exponentially distributed that
  * is a draw in proportion to w, and the committed tokens are distributed as the target's own.
- *  logits, logits_type, row_stride, vocab, cu_rows, max_rows   as in vfy_process_logits. -inf is a token that cannot
- *                follow; a NaN counts as -inf; +inf entries share the whole row. One row per sequence is plain sampling
+ *  logits, logits_type, row_stride, vocab, cu_rows, max_rows   as in vfy_process_logits, with at most 65535 rows. -inf is a
+ *                token that cannot follow; a NaN counts as -inf; +inf entries share the whole row. One row per sequence is plain sampling
  *  temperature   fp32 [B]   T_b >= 0. T_b = 0: the row's argmax has all of p (vfy_accept's rules: ties, NaN), and is the
  *                next token
  *  drafts        int32 [cu_rows[B] - B], packed as in vfy_accept

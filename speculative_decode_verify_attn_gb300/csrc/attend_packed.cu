@@ -20,8 +20,8 @@
 //   one warp         bulk copies of the records (contiguous: no tensor map), and the tiles' geometry
 //   two warps        the MMA issuers of S and of O
 //
-// 17 rows, 16 q-heads over 4 KV heads, d = 128: 256K tokens in 60.2 us, 8K in 13.4, eight ragged sequences of 12K to 48K in
-// 65.5. A tile takes 1.8 thousand cycles. Shared memory moves 1.35 of them (V written and read 512, P and Q 450, records
+// 17 rows, 16 q-heads over 4 KV heads, d = 128: 256K tokens in 58.9 us, 8K in 13.2, eight ragged sequences of 12K to 48K in
+// 64.5. A tile takes 1.8 thousand cycles. Shared memory moves 1.35 of them (V written and read 512, P and Q 450, records
 // 290), the schedulers issue 1.2 (K and V to fp16 a third, weights a third); the records alone, from HBM, would be 0.8.
 #include <cuda_bf16.h>
 

@@ -17,7 +17,7 @@
 // Each warp keeps a ring of three (six) stages of 32 keys in shared memory, which its lanes fill by asynchronous copies of 16
 // bytes: 16 warps an SM have up to 220 KB on their way.
 //
-// 16 q-heads over 4 KV heads of 128, one row: 8K tokens in 8.3 us, 64K in 17.3, 256K in 36.4 (151 MB: 22.6 at the copy rate).
+// 16 q-heads over 4 KV heads of 128, one row: 8K tokens in 8.5 us, 64K in 17.1, 256K in 36.5 (151 MB: 22.6 at the copy rate).
 // Between short and long contexts it streams 5.9 TB/s at 53% of the issue slots; look-up, first copies, the merge of the warps
 // and of the splits are 10 us. With up to eight rows a thread takes 125 registers: 16 warps; with 16 rows twice, 8 warps.
 #include <cuda_bf16.h>

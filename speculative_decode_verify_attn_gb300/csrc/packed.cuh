@@ -143,7 +143,7 @@ __device__ __forceinline__ int partial_exponent(float sum, float g) {
 // a tie of e4m3 only if it is exact, and so can a value's on a tie of e2m1. `x`: pairs.
 //
 // A quotient comes from the rounded reciprocal, one remainder and one correction (Markstein's division), two at a time
-// (with divisions the append of 8 x 1024 tokens took 16.2 us instead of 12.7). That is exact where nothing overflows and no
+// (with divisions the append of 8 x 1024 tokens took a quarter longer). That is exact where nothing overflows and no
 // remainder underflows: g within 2^-100 .. 2^100, s is 2^-9 .. 448 and below 448 |x / g| is at most a little over 6 s, and a
 // value whose remainder underflows is far below a code. Anything else, infinities among it, is divided.
 __device__ __forceinline__ float2 quotients(float2 v, float2 minus_by, float2 r) {

@@ -9,7 +9,8 @@
 // attention kernels that run beside it. Measured in the 40-layer pass on GB300 against 2 CTAs per
 // chunk: 3 or 4 cost the pass 2 and 12 us; 1 for the page-ins after the first was 0.1 us/layer
 // faster on one box and 0.02 slower on another; half the loads in flight per thread made the
-// later page-ins late for their layers.
+// later page-ins late for their layers. Alone, with 4 KV heads of 128, 16 chunks take 12.9 us and 128 82.6 (203 GB/s); chunks
+// in 4 bits 5.4 and 25.2 (187 GB/s), and with 1 or 4 CTAs each 5.5 and 5.0, 25.5 and 25.4.
 #include "ptx.cuh"
 #include "vfy_internal.cuh"
 

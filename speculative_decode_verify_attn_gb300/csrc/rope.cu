@@ -8,12 +8,13 @@
 // channels: the two groups that rotate with one another, so that a pair lies in one lane. Queries, keys and values have a
 // loop each, without choices by row, and two rows a lane ahead of the one it works on. The look-up of up to 32 sequences is
 // one round trip to memory.
-// 17 tokens of 16 + 2 x 4 heads of 128 take 3.1 us (latency), 264 of a batch of trees 3.6, 8 x 1024 25 (117 MB, 4.7 TB/s:
+// 17 tokens of 16 + 2 x 4 heads of 128 take 2.9 us (latency), 264 of a batch of trees 3.2, 8 x 1024 24.7 (117 MB, 4.7 TB/s:
 // leaving out the angles or the norms changes nothing; CTAs of eight warps 25.7, of two 24.6 but 17 tokens 4.2).
 //
 // Angles: the turns position * inv_freq / 2 pi modulo 1 (at position 262144 an fp32 product is off by 1/64 radian), with
 // inv_freq / 2 pi as the sum of three fp32 values (to 2^-53) and the products exact in pairs (product and fma remainder):
-// within 2^-25 turns up to position 2^22 (the last addition), 2^-22 up to 2^31. (fp64 has 1/64 of the fp32 rate here.)
+// within 2^-25 turns up to position 2^22 (the last addition), 2^-22 up to 2^31, for frequencies up to 1 in size: 1 / 2 pi has
+// 53 bits, so that larger ones add some |inv_freq| position 2^-55. (fp64 has 1/64 of the fp32 rate here.)
 #include <cuda_bf16.h>
 
 #include "ptx.cuh"

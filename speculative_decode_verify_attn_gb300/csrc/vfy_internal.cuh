@@ -396,8 +396,10 @@ struct PackedAttnParams {
 int packed_tile_rows();
 cudaError_t launch_attend_packed(const PackedAttnParams& p, int num_seqs, cudaStream_t stream);
 // The same for contexts of at most kPackedFewRows block rows (max_q * G). A single split writes p.out / p.lse itself. us of
-// one layer of 4 KV heads over 8K, 64K and 256K tokens, this kernel against the other: 4 rows 8.3 / 17.3 / 36.5 against
-// 10.0 / 19.9 / 49.1, 16 rows 11.5 / 19.8 / 48.0 against 10.3 / 20.6 / 49.7. (Its registers end at 16 rows.)
+// one layer of 4 KV heads over 8K, 64K and 256K tokens, this kernel against the other: 4 rows 8.5 / 17.1 / 36.2 against
+// 9.6 / 19.7 / 48.1, 8 rows 9.4 / 18.1 / 36.8 against 9.8 / 20.0 / 48.5, 12 rows 11.0 / 19.5 / 47.1 against 9.9 / 20.1 / 48.8,
+// 16 rows 11.4 / 19.6 / 47.0 against 10.0 / 20.3 / 49.0. (Its registers end at 16 rows.) The rule goes by rows alone and takes
+// the slower kernel, by 1.4 us at most, for 9 to 16 rows over short contexts.
 constexpr int kPackedFewRows = 16;
 cudaError_t launch_attend_packed_few(const PackedAttnParams& p, int num_seqs, cudaStream_t stream);
 
@@ -496,8 +498,8 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int num_seqs, int 
 }
 
 // The sequences of a batch by the length of their resident lists, longest first, so that the CTAs of long ones start first
-// (batches of up to 32; larger ones keep their order). 8 ragged sequences of 12K to 48K: 70.5 us without, 67.5 with. Returns place `z` and its metadata, one round trip to memory for a
-// batch of up to 32, by all 32 lanes of a converged warp.
+// (batches of up to 32; larger ones keep their order): 8 ragged sequences of 12K to 48K take 3 us less. Returns place `z` and its
+// metadata, one round trip to memory for a batch of up to 32, by all 32 lanes of a converged warp.
 struct SequenceMeta {
   int b, c0, c1, r0, r1, len;
 };
