@@ -687,7 +687,8 @@ VFY_API vfy_status vfy_attend_full_packed(vfy_ctx* ctx, const uint16_t* q, const
  * (n = D_b): the token with the largest w_v / E_v, ties to the lowest index. With E_v exponentially distributed that
  * is a draw in proportion to w, and the committed tokens are distributed as the target's own.
  *  logits, logits_type, row_stride, vocab, cu_rows, max_rows   as in vfy_process_logits, with at most 65535 rows. -inf is a
- *                token that cannot follow; a NaN counts as -inf; +inf entries share the whole row. One row per sequence is plain sampling
+ *                token that cannot follow; a NaN counts as -inf; +inf entries share the whole row. One row per sequence
+ *                is plain sampling
  *  temperature   fp32 [B]   T_b >= 0. T_b = 0: the row's argmax has all of p (vfy_accept's rules: ties, NaN), and is the
  *                next token
  *  drafts        int32 [cu_rows[B] - B], packed as in vfy_accept

@@ -19,9 +19,9 @@ constexpr int kThreads = 256;
 
 // Jobs of a token: K then V, KV heads, groups of a head; a CTA takes as many whole tokens as it has threads for, and goes
 // from tokens to tokens, the next ones' values on their way while these are packed: three CTAs an SM (8 x 1024 tokens of 4 KV
-// heads of 128 take 10.5 us in a loop, and 94 into a pinned store, which is the host link; a CTA for every few tokens 4 us more). Threads of a token are neighbours, and
-// d / 16 is a multiple of 4: the two groups of a 16-byte code word are a lane and the next, and four lanes have four
-// neighbouring scales.
+// heads of 128 take 10.5 us in a loop, and 94 into a pinned store, which is the host link; a CTA for every few tokens 4 us
+// more). Threads of a token are neighbours, and d / 16 is a multiple of 4: the two groups of a 16-byte code word are a lane and
+// the next, and four lanes have four neighbouring scales.
 __host__ __device__ __forceinline__ int jobs_of(int hkv, int head_dim) { return 2 * hkv * (head_dim / 16); }
 __host__ __device__ __forceinline__ int cta_tokens(int jobs) { return jobs < kThreads ? kThreads / jobs : 1; }
 __host__ __device__ __forceinline__ int job_rounds(int jobs) { return (jobs + kThreads - 1) / kThreads; }

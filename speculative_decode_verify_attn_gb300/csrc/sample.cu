@@ -12,8 +12,9 @@
 // wait for the first kernel (drafts, their probabilities, the first noise) is read before it is over.
 //
 // One sequence of 17 rows of 131072 fp32 logits takes 8.6 us, of which 1.5 are bytes: two kernels' chains of look-ups.
-// 16 sequences of 164 rows of 100003 bf16 logits take 18.5 us (46 MB, 2.5 TB/s; 15.5 from L2): the first kernel ends at 3 instructions an
-// entry, the second at 45 for one row a sequence; with the argmax and the race over p in its loop, and no loads ahead, 20.2 us.
+// 16 sequences of 164 rows of 100003 bf16 logits take 18.5 us (46 MB, 2.5 TB/s; 15.5 from L2): the first kernel
+// ends at 3 instructions an entry, the second at 45 for one row a sequence; with the argmax and the race over p in its loop, and
+// no loads ahead, 20.2 us.
 #include <cuda_bf16.h>
 
 #include "argmax.cuh"
